@@ -326,13 +326,14 @@ def _plain_rotate(x, cs, rot, neox):
 
 
 def _plain_q4(x):
-    """Values as Q4_0 holds them: blocks of 32, scale = the value of largest magnitude / -8."""
+    """Values as Q4_0 holds them: blocks of 32, scale = the value of largest magnitude / -8, held in fp16;
+    codes are the multiples of the held scale, rounded half away from zero."""
     b = x.reshape(*x.shape[:-1], -1, 32)
-    big = b.gather(-1, b.abs().argmax(-1, keepdim=True))
-    d = big * -0.125
-    code = (b * (1.0 / d) + 8.5).floor().clamp(0, 15)
-    held = d.to(torch.float16).float()
-    return torch.where(held == 0, torch.zeros_like(b), held * (code - 8)).reshape(x.shape)
+    d = (b.gather(-1, b.abs().argmax(-1, keepdim=True)) * -0.125).to(torch.float16).float()
+    c = torch.where(d == 0, torch.zeros_like(b), b / d)
+    whole = c.trunc()
+    c = (whole + ((c - whole).abs() >= 0.5) * c.sign()).clamp(-8, 7)
+    return (d * c).reshape(x.shape)
 
 
 def _plain_rope(s):
@@ -453,9 +454,9 @@ def exact(case, seed):
 
         def held(x):
             x = x.unflatten(-1, (-1, 32))
-            scale = torch.take_along_dim(x, x.abs().max(-1, keepdim=True).indices, -1) / -8
-            stored = scale.half().double()
-            return (stored * (torch.floor(x / scale + 8.5).clamp(max=15) - 8)).flatten(-2)
+            scale = (torch.take_along_dim(x, x.abs().max(-1, keepdim=True).indices, -1) / -8).half().double()
+            steps = x / scale
+            return (scale * (steps.sign() * torch.floor(steps.abs() + 0.5)).clamp(-8, 7)).flatten(-2)
 
         return {"q": turned(s["q"], s["qw"]), "k": held(turned(s["k"], s["kw"])), "v": held(s["v"].double())}
     g, page = case["heads"] // hk, case["page"]
