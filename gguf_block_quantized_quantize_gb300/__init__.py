@@ -18,6 +18,7 @@ import torch
 
 F32, F16, Q4_0, Q8_0, Q8_1, Q4_K, Q5_K, Q6_K, BF16, MXFP4 = 0, 1, 2, 8, 9, 12, 13, 14, 30, 39
 GATE_UP_SWIGLU, DOWN_WEIGHTED_SUM, PLAIN = 0, 1, 2
+ROPE_NORM, ROPE_NEOX = 0, 2   # rotated pairs (2i, 2i + 1) or (i, i + rot / 2)
 Q8_1_BYTES = 36   # one q8_1 block: fp16 d, fp16 s, 32 int8 quants (a q8_1 row is k / 32 blocks)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -74,6 +75,29 @@ class MoeFfnArgs(ctypes.Structure):
                 ("y", ctypes.c_void_p), ("yt", ctypes.c_int), ("dev_status", ctypes.c_void_p)]
 
 
+class QkRopeArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("xt", ctypes.c_int),
+                ("n_tokens", ctypes.c_int64), ("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64),
+                ("n_heads", ctypes.c_int64), ("n_kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("positions", ctypes.c_void_p), ("cos_sin", ctypes.c_void_p), ("n_positions", ctypes.c_int64),
+                ("rot", ctypes.c_int64), ("rope_type", ctypes.c_int), ("q_out", ctypes.c_void_p),
+                ("ldqo", ctypes.c_int64), ("k_out", ctypes.c_void_p), ("ldko", ctypes.c_int64),
+                ("cache", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("slots", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
+
+
+class AttnArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("qt", ctypes.c_int), ("n_tokens", ctypes.c_int64), ("ldq", ctypes.c_int64),
+                ("cache", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("block_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("n_requests", ctypes.c_int64),
+                ("max_q_len", ctypes.c_int64), ("n_heads", ctypes.c_int64), ("n_kv_heads", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("scale", ctypes.c_float), ("window", ctypes.c_int64),
+                ("sinks", ctypes.c_int64), ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64),
+                ("dev_status", ctypes.c_void_p)]
+
+
 # name -> (restype, argtypes); the exported C-ABI of include/gguf_gb300.h
 _i, _i64, _p, _sz = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
 SIGNATURES = {
@@ -96,6 +120,12 @@ SIGNATURES = {
     "gguf_mul_mat_id": (_i, [ctypes.POINTER(MoeArgs), _p, _sz, _p]),
     "gguf_moe_ffn_ws_size": (_sz, [ctypes.POINTER(MoeFfnArgs)]),
     "gguf_moe_ffn": (_i, [ctypes.POINTER(MoeFfnArgs), _p, _sz, _p]),
+    "gguf_kv_page_bytes": (_i64, [_i64, _i64, _i64]),
+    "gguf_kv_plan": (_i, [_p, _p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _p]),
+    "gguf_qk_norm_rope": (_i, [ctypes.POINTER(QkRopeArgs), _p]),
+    "gguf_kv_get_rows": (_i, [_p, _i64, _i64, _i64, _i64, _p, _i64, _p, _p, _i, _p]),
+    "gguf_paged_attention_ws_size": (_sz, [ctypes.POINTER(AttnArgs)]),
+    "gguf_paged_attention": (_i, [ctypes.POINTER(AttnArgs), _p, _sz, _p]),
     "gguf_debug_block_dots": (_i, [_p, _i, _i64, _i64, _p, _i64, _p, _p]),
     "gguf_set_option": (_i, [ctypes.c_char_p, _i64]),
     "gguf_get_option": (_i64, [ctypes.c_char_p]),
@@ -451,6 +481,157 @@ def gguf_moe_ffn(w_gate_up: torch.Tensor, gate_up_type: int, gate_up_stride: int
     if ws is None:
         ws = _workspace(need, x.device)
     _check(load_library().gguf_moe_ffn(ctypes.byref(args), _ptr(ws), 0 if ws is None else ws.numel(), _stream()))
+    return out
+
+
+def gguf_kv_page_bytes(head_dim: int, n_kv_heads: int, page_size: int) -> int:
+    """Bytes of one page of the paged Q4_0 cache; -1 for unsupported sizes."""
+    return int(_lib_fast().gguf_kv_page_bytes(head_dim, n_kv_heads, page_size))
+
+
+def _int(what: str, name: str, t: torch.Tensor, numel: int):
+    if t.dtype is not torch.int32 or t.numel() < numel or not t.is_contiguous():
+        raise ValueError(f"{what}: {name} must be a contiguous int32 tensor of at least {numel}")
+    return _ptr(t)
+
+
+def _long(what: str, name: str, t: torch.Tensor, numel: int):
+    if t.dtype is not torch.int64 or t.numel() < numel or not t.is_contiguous():
+        raise ValueError(f"{what}: {name} must be a contiguous int64 tensor of at least {numel}")
+    return _ptr(t)
+
+
+def _table(what: str, t: torch.Tensor, rows: int):
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] < rows or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: block_table must be int32 [requests, width] with contiguous rows")
+    return _ptr(t)
+
+
+def _heads(what: str, name: str, t: torch.Tensor, shape, dtype):
+    """[tokens, heads, head_dim] with the heads of a token side by side; the tokens may be strided."""
+    if t.dtype is not dtype or t.shape != shape or (shape[2] > 1 and t.stride(2) != 1) or \
+            (shape[1] > 1 and t.stride(1) != shape[2]):
+        raise ValueError(f"{what}: {name} must be {tuple(shape)} of {dtype} with the heads of a token side by side")
+    return _ptr(t), (t.stride(0) if shape[0] > 1 else shape[1] * shape[2])
+
+
+def _cache(what: str, cache: torch.Tensor, head_dim: int, n_kv_heads: int, page_size: int):
+    nbytes = gguf_kv_page_bytes(head_dim, n_kv_heads, page_size)
+    if nbytes > 0 and (cache.dtype is not torch.uint8 or cache.dim() != 2 or cache.shape[1] != nbytes or
+                       not cache.is_contiguous()):
+        raise ValueError(f"{what}: cache must be a contiguous uint8 tensor [pages, {nbytes}]")
+    return _ptr(cache)
+
+
+def gguf_kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
+                 page_size: int, n_tokens: int, out=None, dev_status: torch.Tensor | None = None):
+    """Block tables, slots and positions of a step from its requests' lengths (one launch, no host sync).
+
+    Returns (q_start [r + 1], kv_len [r], positions [n_tokens] int32, slots [n_tokens] int64, pages_used [1]);
+    ``out`` may give these five tensors.  ``block_table`` is extended in place."""
+    what = "gguf_kv_plan"
+    r, dev = new_len.numel(), new_len.device
+    if out is None:
+        out = (torch.empty(r + 1, dtype=torch.int32, device=dev), torch.empty(r, dtype=torch.int32, device=dev),
+               torch.empty(n_tokens, dtype=torch.int32, device=dev), torch.empty(n_tokens, dtype=torch.int64, device=dev),
+               torch.empty(1, dtype=torch.int32, device=dev))
+    q_start, kv_len, positions, slots, used = out
+    _check(_lib_fast().gguf_kv_plan(
+        _int(what, "ctx_len", ctx_len, r), _int(what, "new_len", new_len, r), r,
+        _int(what, "free_pages", free_pages, 0), free_pages.numel(), _table(what, block_table, r),
+        block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1], block_table.shape[1], page_size,
+        n_tokens, _int(what, "q_start", q_start, r + 1), _int(what, "kv_len", kv_len, r),
+        _int(what, "positions", positions, n_tokens), _long(what, "slots", slots, n_tokens), _int(what, "pages_used", used, 1),
+        None if dev_status is None else _int(what, "dev_status", dev_status, 1), _stream()))
+    return out
+
+
+def gguf_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor | None, q_norm: torch.Tensor | None,
+                      k_norm: torch.Tensor | None, eps: float, positions: torch.Tensor, cos_sin: torch.Tensor | None,
+                      rope_type: int = ROPE_NEOX, cache: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+                      page_size: int = 0, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                      dev_status: torch.Tensor | None = None) -> torch.Tensor:
+    """Norms of queries and keys per head and the rotation by position in one pass, and the store of keys and
+    values into the cache slots (where ``cache`` is given).  q [t, heads, d], k and v [t, kv_heads, d] may be
+    strided over the tokens (views of a fused product); ``cos_sin`` [positions, rot] fp32 holds rot / 2 cosines,
+    then sines.  Returns ``q_out`` (which may be ``q``); ``k_out`` takes the keys in floats where given."""
+    what = "gguf_qk_norm_rope"
+    t, h, d = q.shape
+    dtype = q.dtype
+    if q_out is None:
+        q_out = torch.empty((t, h, d), dtype=dtype, device=q.device)
+    pq, ldq = _heads(what, "q", q, q.shape, dtype)
+    pqo, ldqo = _heads(what, "q_out", q_out, q.shape, dtype)
+    hk = 0 if k is None else k.shape[1]
+    pk = pv = pko = pc = ps = None
+    ldk = ldv = ldko = pages = 0
+    if k is not None:
+        pk, ldk = _heads(what, "k", k, (t, hk, d), dtype)
+    if k_out is not None:
+        pko, ldko = _heads(what, "k_out", k_out, (t, hk, d), dtype)
+    if cache is not None:
+        if k is None or v is None or slots is None:
+            raise ValueError(f"{what}: storing needs k, v and slots")
+        pv, ldv = _heads(what, "v", v, (t, hk, d), dtype)
+        pc, ps, pages = _cache(what, cache, d, hk, page_size), _long(what, "slots", slots, t), cache.shape[0]
+    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if w is not None and (w.dtype is not torch.float32 or w.shape != (d,) or w.stride(0) != 1):
+            raise ValueError(f"{what}: {name} must be {d} contiguous fp32 values")
+    rot = npos = 0
+    if cos_sin is not None:
+        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError(f"{what}: cos_sin must be a contiguous fp32 tensor [positions, rot]")
+        npos, rot = cos_sin.shape
+    args = QkRopeArgs(pq, pk, pv, _TYPE_OF[dtype], t, ldq, ldk, ldv, h, hk, d, _ptr(q_norm), _ptr(k_norm), eps,
+                      _int(what, "positions", positions, t), _ptr(cos_sin), npos, rot, rope_type, pqo, ldqo, pko, ldko,
+                      pc, pages, page_size, ps,
+                      None if dev_status is None else _int(what, "dev_status", dev_status, 1))
+    _check(_lib_fast().gguf_qk_norm_rope(ctypes.byref(args), _stream()))
+    return q_out
+
+
+def gguf_kv_get_rows(cache: torch.Tensor, slots: torch.Tensor, n_kv_heads: int, head_dim: int, page_size: int,
+                     out_dtype=torch.float32, out=None):
+    """Keys and values of cache slots as floats: two tensors [n, kv_heads, d] (``out`` may give them)."""
+    what = "gguf_kv_get_rows"
+    n = slots.numel()
+    if out is None:
+        out = [torch.empty((n, n_kv_heads, head_dim), dtype=out_dtype, device=slots.device) for _ in range(2)]
+    k, v = out
+    if k.dtype is not v.dtype or not k.is_contiguous() or not v.is_contiguous() or \
+            k.numel() < n * n_kv_heads * head_dim or v.numel() < n * n_kv_heads * head_dim:
+        raise ValueError(f"{what}: out must be two contiguous tensors [n, kv_heads, d] of one dtype")
+    _check(_lib_fast().gguf_kv_get_rows(_cache(what, cache, head_dim, n_kv_heads, page_size), cache.shape[0], page_size,
+                                        n_kv_heads, head_dim, _long(what, "slots", slots, n), n, _ptr(k), _ptr(v),
+                                        _TYPE_OF[k.dtype], _stream()))
+    return out
+
+
+def gguf_paged_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, q_start: torch.Tensor,
+                         kv_len: torch.Tensor, n_kv_heads: int, page_size: int, max_q_len: int, scale: float,
+                         window: int = 0, sinks: int = 0, out: torch.Tensor | None = None,
+                         ws: torch.Tensor | None = None, dev_status: torch.Tensor | None = None) -> torch.Tensor:
+    """Causal attention of q [t, heads, d] over the paged Q4_0 cache (see include/gguf_gb300.h): request r's queries
+    are rows q_start[r] .. q_start[r + 1] - 1 and its newest tokens.  ``window`` > 0 hides what lies further back,
+    except the first ``sinks`` tokens."""
+    what = "gguf_paged_attention"
+    t, h, d = q.shape
+    dtype = q.dtype
+    r = kv_len.numel()
+    if out is None:
+        out = torch.empty((t, h, d), dtype=dtype, device=q.device)
+    pq, ldq = _heads(what, "q", q, q.shape, dtype)
+    po, ldo = _heads(what, "out", out, q.shape, dtype)
+    width = block_table.shape[1]
+    args = AttnArgs(pq, _TYPE_OF[dtype], t, ldq, _cache(what, cache, d, n_kv_heads, page_size), cache.shape[0], page_size,
+                    _table(what, block_table, r), block_table.stride(0) if block_table.shape[0] > 1 else width, width,
+                    _int(what, "q_start", q_start, r + 1), _int(what, "kv_len", kv_len, r), r, max_q_len, h, n_kv_heads,
+                    d, scale, window, sinks, po, ldo,
+                    None if dev_status is None else _int(what, "dev_status", dev_status, 1))
+    lib, ref = _lib_fast(), ctypes.byref(args)
+    if ws is None:   # a caller's workspace is checked against the need by the library
+        ws = _workspace(int(lib.gguf_paged_attention_ws_size(ref)), q.device)
+    _check(lib.gguf_paged_attention(ref, _ptr(ws), 0 if ws is None else ws.numel(), _stream()))
     return out
 
 

@@ -195,4 +195,66 @@ cudaError_t launch_moe_finalize(const float *z, const int32_t *pos, const int32_
                                 const float *route_w, int64_t T, int64_t top_k, int64_t n, void *y, int yt,
                                 cudaStream_t s);
 
+// ---- the paged Q4_0 key / value cache (layout: kv.cuh)
+struct KvPlan {   // gguf_kv_plan
+    const int32_t *ctx, *add;
+    int64_t R;
+    const int32_t *free_pages;
+    int64_t n_free;
+    int32_t *table;
+    int64_t ld, width, page, n_tokens;
+    int32_t *q_start, *kv_len, *pos;
+    int64_t *slots;
+    int32_t *used, *status;
+};
+cudaError_t launch_kv_plan(const KvPlan &p, cudaStream_t s);
+
+struct QkRope {   // gguf_qk_norm_rope
+    const void *q, *k, *v;
+    int64_t ldq, ldk, ldv, n_tokens, h, hk;
+    int64_t rows;   // rows of a token to treat: h queries, then keys (k_out or cache), then values (cache)
+    const float *qw, *kw;
+    float eps;
+    const int32_t *pos;
+    const float *cos_sin;
+    int64_t n_pos;
+    int rot, neox;
+    void *q_out, *k_out;
+    int64_t ldqo, ldko;
+    uint8_t *cache;
+    int64_t n_pages, page;
+    const int64_t *slots;
+    int32_t *status;
+};
+// vec: every row of q, k, v, q_out and k_out is 16-byte aligned
+cudaError_t launch_qk_norm_rope(const QkRope &p, int64_t d, int xt, bool vec, cudaStream_t s);
+
+struct KvRows {   // gguf_kv_get_rows
+    const uint8_t *cache;
+    int64_t n_pages, page, hk;
+    const int64_t *slots;
+    int64_t n;
+    void *k, *v;
+};
+cudaError_t launch_kv_get_rows(const KvRows &p, int64_t d, int ot, bool vec, cudaStream_t s);
+
+struct Attn {   // gguf_paged_attention
+    const void *q;
+    int qt;
+    int64_t n_tokens, ldq;
+    const uint8_t *cache;
+    int64_t n_pages, page;
+    const int32_t *table;
+    int64_t ld, width;
+    const int32_t *q_start, *kv_len;
+    int64_t R, max_q, h, hk;
+    float scale;
+    int64_t window, sinks;
+    void *out;
+    int64_t ldo;
+    int32_t *status;
+};
+size_t attn_ws_size(const Attn &p, int64_t d);
+cudaError_t launch_attn(const Attn &p, int64_t d, void *ws, cudaStream_t s);
+
 }  // namespace gg

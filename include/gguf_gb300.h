@@ -497,6 +497,161 @@ int64_t gguf_get_option(const char *key);
 gguf_status gguf_device_errors(int32_t *flags, int clear, gguf_stream_t stream);
 gguf_status gguf_device_errors_async(int32_t *dev_flags, int clear, gguf_stream_t stream);
 
+/*
+ * The paged Q4_0 key / value cache and the operators on it: what stands
+ * between the q / k / v products of a layer and its output product in a decode
+ * or prefill step.
+ *
+ * A cache is [n_pages][gguf_kv_page_bytes(...)] bytes in device memory, 16-byte
+ * aligned, one per layer.  A page holds page_size tokens (a multiple of 16) of
+ * every KV head: keys and values as Q4_0 blocks of 32 values (fp16 scale d,
+ * codes q: value d * (q - 8)), 18 bytes per 32 values as a Q4_0 row has, in
+ * tiles of 16 tokens ordered for the attention kernels.  The order inside a
+ * tile is the library's own: the cache is written by gguf_qk_norm_rope and read
+ * back by gguf_kv_get_rows.  Whole pages may be copied or moved.
+ * A slot is a token's place: page * page_size + place in the page (64 bits).
+ * A block table row lists the pages of one request in order.
+ * Head sizes: 64, 128 and 256 (GGUF_ERR_SHAPE otherwise).
+ *
+ * dev_status (optional, int32 device counter, never cleared by the library)
+ * counts what a call had to leave out, as for the MoE calls; no page or slot
+ * outside the cache is ever read or written.
+ */
+#define GGUF_ROPE_NORM 0 /* rotated pairs (2i, 2i + 1) */
+#define GGUF_ROPE_NEOX 2 /* rotated pairs (i, i + rot / 2) */
+
+/* Bytes of one page; -1 for a head size or page size that is not supported. */
+int64_t gguf_kv_page_bytes(int64_t head_dim, int64_t n_kv_heads, int64_t page_size);
+
+/*
+ * gguf_kv_plan -- block tables, slots and positions of a step on the device,
+ * from the lengths of its requests.
+ *   ctx_len, new_len : [n_requests] int32: tokens cached before, tokens of this
+ *                      step (0 allowed; negative lengths count as 0).
+ *   free_pages       : [n_free] int32 page numbers to take new pages from, in
+ *                      request order and in table order within a request.
+ *   block_table      : [n_requests][ld_table] int32, of which width columns are
+ *                      used.  The first ceil(ctx / page_size) entries of a row
+ *                      are read, the entries of its new pages are written (-1
+ *                      for a page that free_pages no longer had), the others
+ *                      are left alone.
+ *   q_start          : out [n_requests + 1]: first token of each request.
+ *   kv_len           : out [n_requests]: ctx_len + new_len.
+ *   positions, slots : out [n_tokens] int32 / int64 of the step's tokens, request
+ *                      by request; -1 for the tokens past the last request's (a
+ *                      fixed n_tokens serves a captured graph), and slot -1 for
+ *                      a token without a page.
+ *   pages_used       : out [1]: pages taken from free_pages.
+ *   dev_status       : + the tokens without a page and the tokens past n_tokens.
+ * n_requests <= 16384 (GGUF_ERR_SHAPE above).
+ */
+gguf_status gguf_kv_plan(const int32_t *ctx_len, const int32_t *new_len, int64_t n_requests,
+                         const int32_t *free_pages, int64_t n_free, int32_t *block_table, int64_t ld_table,
+                         int64_t width, int64_t page_size, int64_t n_tokens, int32_t *q_start, int32_t *kv_len,
+                         int32_t *positions, int64_t *slots, int32_t *pages_used, int32_t *dev_status,
+                         gguf_stream_t stream);
+
+/*
+ * gguf_qk_norm_rope -- norms of queries and keys per head, the rotation by
+ * position, and the store of keys and values, in one pass:
+ *   y = x / sqrt(mean(x^2) + eps) * w    (fp32; left out where the weight is NULL)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)  for the pairs of the first rot values
+ * Queries go to q_out.  Keys go to k_out (optional) and, with the values (which
+ * are neither normed nor rotated), to the cache slots (optional): per block of
+ * 32, d = fp16(the value of largest magnitude (the first of equals) / -8) and
+ * code = clamp(roundf(x / d) + 8, 0, 15) (Q4_0; a block whose d rounds to 0
+ * stands for zeros), with an IEEE fp32 division.  Values must stay below 65504 in magnitude;
+ * NaN / Inf inputs give unspecified blocks (no fault).
+ *   q, k, v    : [n_tokens][ld] of type xt (F32, BF16, F16), heads side by side
+ *                in a row.  Rows that start on 16 bytes are read 16 bytes at a
+ *                time.  k and v may be NULL where nothing takes them.
+ *   q_norm, k_norm : [head_dim] fp32 weights, 16-byte aligned, or NULL.
+ *   positions  : [n_tokens] int32.  A token with a negative position (padding)
+ *                is left out: nothing of it is written.  So is one at or past
+ *                n_positions, which dev_status counts.
+ *   cos_sin    : [n_positions][rot] fp32, cos of the rot / 2 angles, then sin;
+ *                16-byte aligned; not looked at with rot = 0.
+ *   rot        : rotated values per head, a multiple of 16, <= head_dim.
+ *   q_out, k_out : rows of type xt; they may be q and k themselves (same stride).
+ *   slots      : [n_tokens] int64; a negative slot is not stored (quietly), one
+ *                past the cache neither (dev_status counts it).  Two tokens of
+ *                a call must not share a slot.
+ */
+typedef struct gguf_qk_rope_args {
+    const void *q, *k, *v;
+    int xt;
+    int64_t n_tokens, ldq, ldk, ldv, n_heads, n_kv_heads, head_dim;
+    const float *q_norm, *k_norm;
+    float eps;
+    const int32_t *positions;
+    const float *cos_sin;
+    int64_t n_positions, rot;
+    int rope_type;
+    void *q_out;
+    int64_t ldqo;
+    void *k_out;
+    int64_t ldko;
+    void *cache;
+    int64_t n_pages, page_size;
+    const int64_t *slots;
+    int32_t *dev_status;
+} gguf_qk_rope_args;
+gguf_status gguf_qk_norm_rope(const gguf_qk_rope_args *args, gguf_stream_t stream);
+
+/*
+ * gguf_kv_get_rows -- keys and values of n cache slots as floats:
+ * k, v [n][n_kv_heads][head_dim] of type ot (F32, F16, BF16).  The values
+ * d * (q - 8) are computed in fp32 and rounded to ot.  A slot outside the cache
+ * (negative, or past it) yields zero rows.
+ */
+gguf_status gguf_kv_get_rows(const void *cache, int64_t n_pages, int64_t page_size, int64_t n_kv_heads,
+                             int64_t head_dim, const int64_t *slots, int64_t n, void *k, void *v, int ot,
+                             gguf_stream_t stream);
+
+/*
+ * gguf_paged_attention -- causal attention of each request's newest tokens over
+ * its cached tokens:
+ *   o_i = sum_j softmax_j(scale * q_i . k_j) v_j
+ * over the tokens j <= pos_i, and with window > 0 only those with
+ * j > pos_i - window or j < sinks (the first tokens that stay visible).  Token i
+ * of n new ones stands at pos = kv_len - n + i: keys and values of the new
+ * tokens are in the cache before the call.  A query that sees no token (kv_len
+ * 0, or fewer cached tokens than queries) gets zeros.
+ *   q, out     : [n_tokens][ldq / ldo] of type qt (F32, BF16, F16), heads side by
+ *                side; rows of tokens outside [q_start[0], q_start[n_requests])
+ *                are not written.
+ *   n_heads    : a multiple of n_kv_heads; query head h reads KV head
+ *                h / (n_heads / n_kv_heads).
+ *   block_table: [n_requests][ld_table] int32, width columns used.  A page number
+ *                outside the cache hides its tokens, and dev_status counts it.
+ *   q_start    : [n_requests + 1] int32, non-decreasing; kv_len: [n_requests].
+ *   max_q_len  : at least the longest request's queries (requests with more get
+ *                only their first max_q_len rows): with the other host arguments
+ *                it chooses the kernels.  0 < max_q_len.
+ *   ws         : gguf_paged_attention_ws_size(args) bytes, 16-byte aligned.
+ * Softmax statistics and sums are fp32.  16-bit queries take 16-bit probabilities
+ * and values into the matrix instructions (about 3e-4 of a row's norm), fp32
+ * queries split operands (about 1e-6).  Same bits on every run.
+ */
+typedef struct gguf_attn_args {
+    const void *q;
+    int qt;
+    int64_t n_tokens, ldq;
+    const void *cache;
+    int64_t n_pages, page_size;
+    const int32_t *block_table;
+    int64_t ld_table, width;
+    const int32_t *q_start, *kv_len;
+    int64_t n_requests, max_q_len, n_heads, n_kv_heads, head_dim;
+    float scale;
+    int64_t window, sinks;
+    void *out;
+    int64_t ldo;
+    int32_t *dev_status;
+} gguf_attn_args;
+size_t gguf_paged_attention_ws_size(const gguf_attn_args *args);
+gguf_status gguf_paged_attention(const gguf_attn_args *args, void *ws, size_t ws_bytes, gguf_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
