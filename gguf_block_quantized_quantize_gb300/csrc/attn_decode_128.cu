@@ -1,0 +1,13 @@
+// attention of few query rows, heads of 128 values
+#include "attn_decode.cuh"
+
+namespace gg {
+
+cudaError_t launch_attn_decode_128(const AdShape &a, int nt, int ctas, cudaStream_t s) {
+    if (a.p.qt == GGUF_F32) return attn_decode_run<128, GGUF_F32, 1>(a, ctas, s);
+    if (a.p.qt == GGUF_F16)
+        return nt == 2 ? attn_decode_run<128, GGUF_F16, 2>(a, ctas, s) : attn_decode_run<128, GGUF_F16, 1>(a, ctas, s);
+    return nt == 2 ? attn_decode_run<128, GGUF_BF16, 2>(a, ctas, s) : attn_decode_run<128, GGUF_BF16, 1>(a, ctas, s);
+}
+
+}  // namespace gg

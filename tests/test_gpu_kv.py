@@ -217,12 +217,12 @@ def attn_setup(q_lens, kv_lens, h, hk, d, page, typ, seed=0, spare_cols=0, peaky
 
 
 def attn_ref(q, k, v, q_lens, kv_lens, scale, window, sinks):
-    """fp64 outputs, and the sums that error bounds are made of: sum p |v| and max_j scale sum |q k|."""
+    """fp64 outputs, and the sums that error bounds are made of: sum p |v|, max_j scale sum |q k| and sum |v|."""
     q, k, v = q.double().cpu(), k.double().cpu(), v.double().cpu()
     t, h, d = q.shape
     hk = k.shape[1]
-    out, size, reach = torch.zeros(t, h, d, dtype=torch.float64), torch.zeros(t, h, d, dtype=torch.float64), \
-        torch.zeros(t, h, 1, dtype=torch.float64)
+    out, size, total = (torch.zeros(t, h, d, dtype=torch.float64) for _ in range(3))
+    reach = torch.zeros(t, h, 1, dtype=torch.float64)
     a = b = 0
     for n, m in zip(q_lens, kv_lens):
         for i in range(n):
@@ -236,23 +236,26 @@ def attn_ref(q, k, v, q_lens, kv_lens, scale, window, sinks):
                 kk, vv = k[b + j, head // (h // hk)], v[b + j, head // (h // hk)]
                 p = torch.softmax(kk @ q[a + i, head] * scale, 0)
                 out[a + i, head], size[a + i, head] = p @ vv, p @ vv.abs()
+                total[a + i, head] = vv.abs().sum(0)
                 reach[a + i, head] = (kk.abs() @ q[a + i, head].abs()).max() * scale
         a, b = a + n, b + max(m, 0)
-    return out, size, reach
+    return out, size, reach, total
 
 
 def check_attn(got, refs, typ):
     """fp32: about 2^-21 from split operands, fp32 sums and the exponential of scores as large as `reach`.
     16 bits: p and v rounded to 11 bits each (2^-11 + 2^-11 of the terms), keys rounded to 11 bits move a
     score by at most 2^-12 reach, hence a probability and the sum by twice that; one rounding to the type (fp16
-    below 2^-14: multiples of 2^-24)."""
-    ref, size, reach = refs
+    below 2^-14: multiples of 2^-24). Probabilities go into the products as fp16 numbers of up to 2^10 times
+    their value, which are multiples of 2^-24: 2^-35 of the row's largest at most is lost of each."""
+    ref, size, reach, total = refs
     got = got.double().cpu()
     assert bool(torch.isfinite(got).all())
     if typ == "f32":
         tol = 2.0 ** -20 * size * (1 + reach)
     else:
         tol = HALF_ULP[typ] * ref.abs() * 1.01 + size * (2.0 ** -10 + 2.0 ** -11 * reach + 2.0 ** -20 * (1 + reach))
+    tol = tol + 2.0 ** -34 * total
     if typ == "f16":
         tol = tol + 2.0 ** -25
     err = (got - ref).abs()
