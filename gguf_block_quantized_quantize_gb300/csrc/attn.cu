@@ -9,6 +9,10 @@ cudaError_t launch_attn_decode_64(const AdShape &a, int nt, int ctas, cudaStream
 cudaError_t launch_attn_decode_128(const AdShape &a, int nt, int ctas, cudaStream_t s);
 cudaError_t launch_attn_decode_256(const AdShape &a, int nt, int ctas, cudaStream_t s);
 
+cudaError_t launch_attn_prefill_64(const AdShape &a, int ctas, cudaStream_t s);
+cudaError_t launch_attn_prefill_128(const AdShape &a, int ctas, cudaStream_t s);
+cudaError_t launch_attn_prefill_256(const AdShape &a, int ctas, cudaStream_t s);
+
 // one CTA per SM (the rings take the shared memory of one)
 static int decode_ctas() { return device_info().sm_count < AC_MAX ? device_info().sm_count : AC_MAX; }
 
@@ -25,10 +29,22 @@ cudaError_t launch_attn(const Attn &p, int64_t d, void *ws, cudaStream_t s) {
     a.meta = (int32_t *)((uint8_t *)ws + (size_t)ctas * 2 * (d == 256 ? 8 : 16) * (d + 2) * 4);
     a.vec = (reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.out)) % 16 == 0 && p.ldq * es % 16 == 0 &&
             p.ldo * es % 16 == 0;
+    // requests with few query rows per KV head go to the decode kernel, the others to the prefill kernel (which
+    // takes 16-bit queries); host and device sizes decide, request by request
+    const int64_t G = p.h / p.hk, most = G * p.max_q;
+    const bool prefill = p.qt != GGUF_F32 && most > 16;
+    if (prefill) a.max_rows = G <= 8 ? 8 : 16;
     // 16 rows at once where a unit has more than 8, so that its cache bytes are read and unpacked once
-    const int nt = p.h / p.hk * p.max_q > 8 && p.qt != GGUF_F32 ? 2 : 1;
-    return d == 64 ? launch_attn_decode_64(a, nt, ctas, s)
-         : d == 128 ? launch_attn_decode_128(a, nt, ctas, s) : launch_attn_decode_256(a, nt, ctas, s);
+    const int nt = (prefill ? a.max_rows : most) > 8 && p.qt != GGUF_F32 ? 2 : 1;
+    cudaError_t e = cudaSuccess;
+    if (!prefill || G <= a.max_rows)
+        e = d == 64 ? launch_attn_decode_64(a, nt, ctas, s)
+          : d == 128 ? launch_attn_decode_128(a, nt, ctas, s) : launch_attn_decode_256(a, nt, ctas, s);
+    if (e != cudaSuccess || !prefill) return e;
+    a.min_rows = a.max_rows;
+    a.max_rows = 0x7fffffff;
+    return d == 64 ? launch_attn_prefill_64(a, ctas, s)
+         : d == 128 ? launch_attn_prefill_128(a, ctas, s) : launch_attn_prefill_256(a, ctas, s);
 }
 
 }  // namespace gg
