@@ -12,19 +12,22 @@
 // over several CTAs, by a second small launch, always in the same order.
 //
 // A warp's tile: its 18 * D contiguous bytes come by one bulk copy into the
-// warp's own ring of stages, several tiles ahead.  Scores and outputs are
-// warp-level 16x8x16 matrix products with the codes as operands:
-//   S = Q K^T  A = 16 query rows, B = 8 keys.  The 4-bit code c is put into the
-//              mantissa of 16 (one shift, one and-or for two values), which is
-//              the exact number 16 + c; the accumulator starts from -24 sum(q),
-//              so it ends as sum q (c - 8) of one 32-value block, and the
-//              block's scale is applied to it in fp32.
-//   O^T = V^T P^T  A = 16 values of a head, B = 8 query rows; the accumulator of
-//              S is the B operand of O^T as it stands.  v = d * (c - 8) is
-//              rounded to fp16 (2^-12 of it at most) and p = 2^(s - max + 10)
-//              likewise; sums and statistics are fp32.
-// fp32 queries use three bf16 parts of q, and high and low fp16 parts of p and
-// v, for fp32 accuracy.
+// warp's own ring of stages; two tiles are treated at a time.  Scores and
+// outputs are warp-level 16x8x16 matrix products with the codes as operands:
+//   S^T = K Q^T    A = 16 keys, B = 8 query rows.  One and-or puts two 4-bit codes
+//                  c into the mantissas of 1024: the numbers 1024 + c, or from the
+//                  odd nibbles 1024 + 16 c, whose query values are held / 16.  The
+//                  accumulator starts from what the offsets add up to, negated, so
+//                  it ends as sum q (c - 8) of one 32-value block, and the block's
+//                  scale is applied to it in fp32.
+//   O^T = V^T P^T  A = 16 values of a head over 16 tokens, B = 8 query rows: the
+//                  accumulators of S^T, transposed 8 x 8 in registers.  v = d (c - 8)
+//                  is rounded to fp16 (2^-12 of it at most) and p = 2^(s - max + 10)
+//                  likewise; sums and statistics are fp32.
+// 16-bit query rows are scaled by a power of two to a largest value in [2^8,
+// 2^9), which fp16 holds exactly (bf16 values below 2^-15 of the row's largest
+// lose bits).  fp32 queries use three bf16 parts of q, the exact c - 8, and
+// high and low fp16 parts of p and v, for fp32 accuracy.
 #pragma once
 
 #include "common.cuh"
@@ -39,9 +42,14 @@ constexpr float AD_PBITS = 10.0f;   // probabilities are held times 2^10 (at mos
 template <int D, int QT, int NT>
 struct AdCfg {
     static constexpr int RG = 8 * NT;                       // query rows of a unit
-    static constexpr int WARPS = (D == 256 || NT == 2 || QT == GGUF_F32) ? 8 : 16;
-    static constexpr int STAGES = NT == 2 ? 8 : 4;
-    static constexpr int RING = STAGES * KvTile<D>::BYTES;  // bytes per warp, a multiple of 128
+    // warps that compute; one more warpgroup holds the warp that asks for the copies, and gives registers to them
+    static constexpr int WARPS = (D == 256 || NT == 2 || QT == GGUF_F32) ? 8 : 12;
+    static constexpr int THREADS = WARPS * 32 + 128;
+    static constexpr int REGS = WARPS == 8 ? 224 : 152, REGS_COPY = 56;   // sums of a launch at 168 and 128
+    static constexpr int TP = D == 256 && QT == GGUF_F32 ? 1 : D == 64 && NT == 1 && QT != GGUF_F32 ? 4 : 2;   // tiles at a time
+    static constexpr int STEP = TP * KvTile<D>::BYTES;
+    static constexpr int STAGES = NT == 2 || TP == 1 ? 4 : D == 256 ? 2 : 3;   // as the shared memory allows
+    static constexpr int RING = STAGES * STEP;              // bytes per warp, a multiple of 128
     static constexpr int SLOT = RG * (D + 2) * 4;           // one partial result: O, then max and sum per row
     static_assert(SLOT <= RING, "a warp's last partial result reuses its ring");
     static constexpr int SMEM = WARPS * (RING + SLOT);
@@ -93,17 +101,24 @@ __device__ __forceinline__ int64_t ad_tiles(const AdShape &a, const AdReq &q, in
     return (int64_t)q.nt * ((q.q * G + rg - 1) / rg) * a.p.hk;
 }
 
-__device__ __forceinline__ void mma_bf16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// d = A B + c of the warp-level 16x8x16 product, fp16 or (BF) bf16 operands
+template <bool BF>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                          float c1, float c2, float c3) {
+    if constexpr (BF)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
-__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// the 8 x 8 matrix of 16-bit values whose row lane / 4 holds the lane's pair, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t o) {
     uint32_t r;
@@ -118,20 +133,32 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// 16 + code of nibble i of both halves of w, as two fp16 / bf16 numbers
+// codes of nibble I of both halves of w as two fp16 numbers: 1024 + c (even I) or 1024 + 16 c (odd I)
 template <int I>
 __device__ __forceinline__ uint32_t codes_f16(uint32_t w) {
-    constexpr int SH = 4 * I - 6;
-    return and_or(SH < 0 ? w << (SH < 0 ? -SH : 0) : w >> (SH > 0 ? SH : 0), 0x03C003C0u, 0x4C004C00u);
+    return and_or(I < 2 ? w : w >> 8, I & 1 ? 0x00F000F0u : 0x000F000Fu, 0x64006400u);
 }
+// c - 8 of nibble I of both halves, exact
 template <int I>
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
+__device__ __forceinline__ __half2 signed_f16(uint32_t w) {
+    const __half2 x = u2h(codes_f16<I>(w));
+    return I & 1 ? __hfma2(x, u2h(0x2C002C00u), u2h(0xD480D480u))   // x / 16 - 72
+                 : __hsub2(x, u2h(0x64086408u));                    // x - 1032
+}
+// the same as two bf16 numbers (from 16 + c)
+template <int I>
+__device__ __forceinline__ uint32_t signed_bf16(uint32_t w) {
     constexpr int SH = 4 * I - 3;
-    return and_or(SH < 0 ? w << (SH < 0 ? -SH : 0) : w >> (SH > 0 ? SH : 0), 0x00780078u, 0x41804180u);
+    const uint32_t x = and_or(SH < 0 ? w << (SH < 0 ? -SH : 0) : w >> (SH > 0 ? SH : 0), 0x00780078u, 0x41804180u);
+    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x), __float2bfloat162_rn(24.0f));
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
-// 1024 + code, one operation fewer for the lowest nibble
-template <int I>
-__device__ __forceinline__ __half2 codes_1024(uint32_t w) { return u2h(and_or(w >> (4 * I), 0x000F000Fu, 0x64006400u)); }
+
+// a power of two that takes the largest magnitude of a row of queries into [2^8, 2^9)
+__device__ __forceinline__ float q_scale_up(float mx) {
+    const uint32_t e = max(__float_as_uint(mx) >> 23, 16u);
+    return __uint_as_float(mx == 0.0f ? 127u << 23 : min(262u - e, 254u) << 23);
+}
 
 // N consecutive words of shared memory as vector loads
 template <int N>
@@ -177,43 +204,39 @@ struct AdCursor {
     int r, u, tile;   // request, unit within it, tile within the unit
     AdReq q;
 };
-__device__ __forceinline__ void ad_next_request(const AdShape &a, AdCursor &c) {
+// the next unit with tiles
+template <int RG>
+__device__ __forceinline__ void ad_next_unit(const AdShape &a, AdCursor &c) {
+    c.tile = 0;
+    if (++c.u < (c.q.q * (int)(a.p.h / a.p.hk) + RG - 1) / RG * (int)a.p.hk) return;
+    c.u = 0;
     do {
-        c.r++;
-        if (c.r >= a.p.R) return;
+        if (++c.r >= a.p.R) return;
         c.q = ad_request(a, c.r);
     } while (c.q.nt == 0);
 }
-template <int RG>
-__device__ __forceinline__ void ad_advance(const AdShape &a, AdCursor &c) {
-    if (++c.tile < c.q.nt) return;
-    c.tile = 0;
-    const int G = (int)(a.p.h / a.p.hk);
-    if (++c.u < (c.q.q * G + RG - 1) / RG * (int)a.p.hk) return;
-    c.u = 0;
-    ad_next_request(a, c);
-}
-// first token of a tile
-__device__ __forceinline__ int ad_token(const AdCursor &c) {
-    return (c.tile < c.q.n_sink ? c.tile : c.q.w_tile + c.tile - c.q.n_sink) * KV_TILE;
-}
-// page entry that a cursor's tile needs; -1 past the table
-__device__ __forceinline__ int32_t ad_page(const AdShape &a, const AdCursor &c) {
-    if (c.r >= a.p.R) return -1;
-    const uint32_t pi = (uint32_t)ad_token(c) / (uint32_t)a.p.page;
-    return pi < a.p.width ? a.p.table[c.r * a.p.ld + pi] : -1;
+
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
 }
 
 template <int D, int QT, int NT>
-__global__ void __launch_bounds__(AdCfg<D, QT, NT>::WARPS * 32) attn_decode_kernel(const AdShape a) {
+__global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kernel(const AdShape a) {
     using C = AdCfg<D, QT, NT>;
     using L = KvTile<D>;
-    constexpr int RG = C::RG, NB = L::NB, BW = L::BW, NC = L::NC, ST = C::STAGES;
+    constexpr int RG = C::RG, NB = L::NB, BW = L::BW, NC = L::NC, ST = C::STAGES, TP = C::TP;
     constexpr int QP = QT == GGUF_F32 ? 3 : 1;   // bf16 parts of a query value
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t bars[C::WARPS][ST];
-    __shared__ int64_t chunk_end[C::WARPS * 32];
-    __shared__ int64_t warp_sum[C::WARPS];
+    __shared__ uint64_t full[C::WARPS][ST], freed[C::WARPS][ST];
+    __shared__ uint32_t absent[C::WARPS][ST];   // tiles of a stage that have no page
+    __shared__ int64_t chunk_end[C::THREADS];
+    __shared__ int64_t warp_sum[C::THREADS / 32];
+    __shared__ int32_t abort_word;
+    volatile int32_t *abort_flag = &abort_word;
     // what each warp leaves at its end: 1 a piece of a unit that began before the warp, which 2 goes on past the
     // warp; 4 the first piece of a unit that goes on past the warp
     __shared__ int32_t left[C::WARPS], left_r[C::WARPS], left_u[C::WARPS];
@@ -221,15 +244,15 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::WARPS * 32) attn_decode_kern
     const Attn &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, q4 = lane & 3;
-    uint8_t *ring = smem + warp * C::RING;
-    if (lane == 0)
-        for (int i = 0; i < ST; i++) tc::mbar_init(&bars[warp][i], 1);
+    if (tid < C::WARPS)
+        for (int i = 0; i < ST; i++) { tc::mbar_init(&full[tid][i], 1); tc::mbar_init(&freed[tid][i], 1); }
+    if (tid == 0) abort_word = 0;
     tc::fence_barrier_init();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // tiles of all requests: thread t holds those of requests [t * per, (t + 1) * per)
-    constexpr int NTHR = C::WARPS * 32;
+    constexpr int NTHR = C::THREADS;
     const int R = (int)p.R, per = (R + NTHR - 1) / NTHR;
     int64_t mine = 0;
     for (int r = tid * per; r < min(R, (tid + 1) * per); r++) mine += ad_tiles(a, ad_request(a, r), RG);
@@ -248,370 +271,452 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::WARPS * 32) attn_decode_kern
     const int64_t per_cta = (total + gridDim.x - 1) / gridDim.x;
     const int64_t cta0 = min(total, (int64_t)blockIdx.x * per_cta), cta1 = min(total, cta0 + per_cta);
     const int64_t per_warp = (cta1 - cta0 + C::WARPS - 1) / C::WARPS;
-    const int64_t t0 = min(cta1, cta0 + warp * per_warp), t1 = min(cta1, t0 + per_warp);
+    // the request, unit and tile of tile t0 < total of the sequence
+    auto locate = [&](int64_t t0) {
+        AdCursor cur;
+        int lo = -1, hi = NTHR - 1;   // first chunk that ends past t0
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (chunk_end[mid] > t0) hi = mid;
+            else lo = mid;
+        }
+        int64_t before = hi > 0 ? chunk_end[hi - 1] : 0;
+        for (cur.r = hi * per;; cur.r++) {   // it is there
+            cur.q = ad_request(a, cur.r);
+            const int64_t n = ad_tiles(a, cur.q, RG);
+            if (before + n > t0) break;
+            before += n;
+        }
+        const int64_t off = t0 - before;
+        cur.u = (int)(off / cur.q.nt);
+        cur.tile = (int)(off - (int64_t)cur.u * cur.q.nt);
+        return cur;
+    };
 
+    if (warp >= C::WARPS) {
+        // ================= copies: 8 lanes ask for those of one computing warp, a step of TP tiles of a unit at a
+        // time, a tile each; they hold the 16 table entries from page `base` on, the later 8 on their way early
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_COPY));
+        const int who = (warp - C::WARPS) * 4 + (lane >> 3), l8 = lane & 7;
+        if ((warp - C::WARPS) * 4 >= C::WARPS) return;
+        const uint32_t group = 0xffu << (lane & 24);
+        const int64_t t0 = min(cta1, cta0 + who * per_warp), t1 = min(cta1, t0 + per_warp);
+        int tiles = who < C::WARPS ? (int)min(t1 - t0, (int64_t)0x7fffffff) : 0;   // to ask for
+        int unit = 0;                 // of them, those of the unit
+        int step = 0;                 // steps asked for
+        int base = 0, of = -1;        // the table entries: first page, and request
+        int32_t now8 = -1, next8 = -1;
+        const int tpp = (int)(p.page / KV_TILE);
+        AdCursor feed;
+        if (tiles > 0) feed = locate(t0);
+        uint64_t idle_since = 0;
+        for (;;) {
+            const int stage = step % ST;
+            const bool can = tiles > 0 && (step < ST || mbar_test(&freed[who][stage], (uint32_t)(step / ST - 1) & 1u));
+            if (__any_sync(group, can)) {   // (a lane that saw the stage free speaks for the others)
+                if (unit == 0) {
+                    if (feed.tile == feed.q.nt) ad_next_unit<RG>(a, feed);
+                    unit = min(tiles, feed.q.nt - feed.tile);
+                }
+                const int cnt = min(TP, unit), i = feed.tile + min(l8, cnt - 1);
+                const int at = i < feed.q.n_sink ? i : feed.q.w_tile + i - feed.q.n_sink;   // tile of the request
+                const int page_at = (int)((uint32_t)at / (uint32_t)tpp), in_page = at - page_at * tpp;
+                const int first = __shfl_sync(group, page_at, lane & 24);
+                const int32_t *row = p.table + feed.r * p.ld;
+                if (of == feed.r && first >= base + 8 && first < base + 16) {
+                    base += 8;
+                    now8 = next8;
+                    next8 = base + 8 + l8 < p.width ? row[base + 8 + l8] : -1;
+                } else if (of != feed.r || first < base || first >= base + 8) {
+                    of = feed.r;
+                    base = first & ~7;
+                    now8 = base + l8 < p.width ? row[base + l8] : -1;
+                    next8 = base + 8 + l8 < p.width ? row[base + 8 + l8] : -1;
+                }
+                const int d = page_at - base;
+                const int32_t e0 = __shfl_sync(group, now8, (lane & 24) | (d & 7)), e1 = __shfl_sync(group, next8, (lane & 24) | (d & 7));
+                // a step may reach from the first tokens into the window: then the entry is read on the spot
+                const int32_t pg = d < 8 ? e0 : d < 16 ? e1 : page_at < p.width ? row[page_at] : -1;
+                const bool ok = l8 < cnt && pg >= 0 && pg < p.n_pages;
+                const uint32_t have = (__ballot_sync(group, ok) >> (lane & 24)) & 0xffu;
+                if (l8 == 0) {
+                    const uint32_t none = ~have & ((1u << cnt) - 1);
+                    absent[who][stage] = none;
+                    tc::mbar_arrive_expect_tx(&full[who][stage], (uint32_t)__popc(have) * L::BYTES);
+                    if (none && p.status != nullptr) atomicAdd(p.status, __popc(none));
+                }
+                __syncwarp(group);
+                if (ok)
+                    bulk_load(smem + who * C::RING + stage * C::STEP + l8 * L::BYTES,
+                              p.cache + pg * kv_page_bytes(D, p.hk, p.page) +
+                                  ((int64_t)(feed.u % (int)p.hk) * tpp + in_page) * L::BYTES,
+                              L::BYTES, &full[who][stage]);
+                feed.tile += cnt;
+                tiles -= cnt;
+                unit -= cnt;
+                step++;
+                idle_since = 0;
+            } else if (tiles > 0) {
+                const uint64_t now = tc::globaltimer();
+                if (idle_since == 0) idle_since = now;
+                if (now - idle_since > tc::kWaitLimitNs) *abort_flag = 1;
+                __nanosleep(20);
+            }
+            if (!__any_sync(0xffffffffu, tiles > 0 && !*abort_flag)) break;
+        }
+        if (*abort_flag && who < C::WARPS)   // copies that are under way land before the CTA exits
+            for (int i = max(0, step - ST); i < step; i++) tc::mbar_wait(&full[who][i % ST], (uint32_t)(i / ST) & 1u);
+        return;
+    }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS));
+    constexpr int NCOMP = C::WARPS * 32;
+    auto join_warps = [] { asm volatile("bar.sync 1, %0;" ::"n"(NCOMP) : "memory"); };
+    uint8_t *ring = smem + warp * C::RING;
+    const int64_t t0 = min(cta1, cta0 + warp * per_warp), t1 = min(cta1, t0 + per_warp);
     int flags = 0, open_r = 0, open_u = 0;
     int64_t open_end = 0;
     if (t0 < t1) {
-        // the request, unit and tile of t0
-        AdCursor cur;
-        {
-            int lo = -1, hi = NTHR - 1;   // first chunk that ends past t0
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (chunk_end[mid] > t0) hi = mid;
-                else lo = mid;
-            }
-            int64_t before = hi > 0 ? chunk_end[hi - 1] : 0;
-            cur.r = hi * per;
-            for (;; cur.r++) {   // it is there: t0 < total
-                cur.q = ad_request(a, cur.r);
-                const int64_t n = ad_tiles(a, cur.q, RG);
-                if (before + n > t0) break;
-                before += n;
-            }
-            const int64_t off = t0 - before;
-            cur.u = (int)(off / cur.q.nt);
-            cur.tile = (int)(off - (int64_t)cur.u * cur.q.nt);
-        }
+        AdCursor cur = locate(t0);
         const int G = (int)(p.h / p.hk);
-        const float sl = p.scale * 1.44269504088896341f;
-        AdCursor ahead = cur;
-        int64_t n_ahead = t0;      // next tile to ask for
-        uint32_t bad = 0;          // stages whose tile has no page
-        int32_t pg = ad_page(a, ahead);
-        auto ask = [&](int stage) {
-            const int tok = ad_token(ahead);
-            const bool ok = pg >= 0 && pg < p.n_pages;
-            bad = ok ? bad & ~(1u << stage) : bad | (1u << stage);
-            if (lane == 0) {
-                if (ok) {
-                    const int head = ahead.u % (int)p.hk;
-                    const uint32_t off = (uint32_t)tok % (uint32_t)p.page;
-                    const uint8_t *src = p.cache + pg * kv_page_bytes(D, p.hk, p.page) +
-                                         (head * (p.page / KV_TILE) + off / KV_TILE) * (int64_t)L::BYTES;
-                    tc::mbar_arrive_expect_tx(&bars[warp][stage], L::BYTES);
-                    bulk_load(ring + stage * L::BYTES, src, L::BYTES, &bars[warp][stage]);
-                } else {
-                    tc::mbar_arrive(&bars[warp][stage]);
-                    if (p.status != nullptr) atomicAdd(p.status, 1);
-                }
-            }
-            n_ahead++;
-            if (n_ahead < t1) {
-                ad_advance<RG>(a, ahead);
-                pg = ad_page(a, ahead);
-            }
-        };
-        for (int i = 0; i < ST && n_ahead < t1; i++) ask(i);
-
-        uint32_t qa[QP][NB][2][NT][2];   // A fragments of the queries
-        float corr[NB][NT];              // -24 sum of the row's block
-        float o[NB][2][NT][4];
-        float m[NT], lsum[NT];
-        int pos[NT];                     // position of the rows g and g + 8; -1 for a row that is not there
-        int pos_lo = 0, pos_hi = 0;
-        bool fresh = true, dead = false;
-        int stage = 0;
+        const float log2_scale = p.scale * 1.44269504088896341f;
+        bool dead = false;
+        int left_tiles = (int)min(t1 - t0, (int64_t)0x7fffffff), stage = 0;
         uint32_t phase = 0;
-        for (int64_t t = t0; t < t1; t++) {
-            if (fresh) {   // a unit begins: its query rows
-                const int row0 = cur.u / (int)p.hk * RG, head0 = cur.u % (int)p.hk * G;
-                const int rows = cur.q.q * G;
-                pos_lo = cur.q.pos0 + row0 / G;
-                pos_hi = cur.q.pos0 + (min(rows, row0 + RG) - 1) / G;
+        while (left_tiles > 0) {
+            // ---- a unit, or the part of it that is the warp's: its query rows
+            const int row0 = cur.u / (int)p.hk * RG, head0 = cur.u % (int)p.hk * G, rows = cur.q.q * G;
+            const int pos_lo = cur.q.pos0 + row0 / G, pos_hi = cur.q.pos0 + (min(rows, row0 + RG) - 1) / G;
+            uint32_t qb[QP][NB][2][NT][2];   // B fragments of the queries: row g, values 8 q4 .. of each block
+            float corr[NB][NT][2];           // what the code offsets add to rows 2 q4, + 1, negated
+            float sl[NT][2];                 // scores to log2 units
+            float o[NB][2][NT][4];
+            float m[NT][2], lsum[NT][2];
+            int pos[NT][2];                  // positions of rows 2 q4, + 1; -1 for a row that is not there
 #pragma unroll
-                for (int n = 0; n < NT; n++) {
-                    const int row = row0 + g + 8 * n;
-                    const bool there = row < rows;
-                    pos[n] = there ? cur.q.pos0 + row / G : -1;
-                    m[n] = -INFINITY;
-                    lsum[n] = 0.0f;
-                    const int64_t at = there ? (cur.q.rows0 + row / G) * p.ldq + (int64_t)(head0 + row % G) * D : 0;
+            for (int n = 0; n < NT; n++) {
+                const int row = row0 + g + 8 * n;
+                const bool there = row < rows;
+                const int64_t at = there ? (cur.q.rows0 + row / G) * p.ldq + (int64_t)(head0 + row % G) * D : 0;
+                if constexpr (QT != GGUF_F32) {
+                    uint32_t w[NB][4];
+                    float mx = 0.0f;
+#pragma unroll
+                    for (int b = 0; b < NB; b++) {
+                        const uint16_t *from = reinterpret_cast<const uint16_t *>(p.q) + at + 32 * b + 8 * q4;
+                        if (!there) w[b][0] = w[b][1] = w[b][2] = w[b][3] = 0;
+                        else if (a.vec) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(from);
+                            w[b][0] = v.x; w[b][1] = v.y; w[b][2] = v.z; w[b][3] = v.w;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; i++) w[b][i] = from[2 * i] | (uint32_t)from[2 * i + 1] << 16;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; i++) mx = fmaxf(mx, fmaxf(fabsf(from16<QT>(w[b][i] & 0xffff)), fabsf(from16<QT>(w[b][i] >> 16))));
+                    }
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const float up = q_scale_up(mx), inv = 1.0f / up;
+#pragma unroll
+                    for (int j = 0; j < 2; j++) sl[n][j] = log2_scale * __shfl_sync(0xffffffffu, inv, 8 * q4 + 4 * j);
 #pragma unroll
                     for (int b = 0; b < NB; b++) {
                         float s = 0.0f;
-                        uint32_t w[QP][4];
-                        if constexpr (QT != GGUF_F32) {
-                            const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + at + 32 * b + 8 * q4;
-                            uint32_t *x = w[0];
-                            if (!there) x[0] = x[1] = x[2] = x[3] = 0;
-                            else if (a.vec) {
-                                const uint4 v = *reinterpret_cast<const uint4 *>(src);
-                                x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-                            } else {
 #pragma unroll
-                                for (int i = 0; i < 4; i++) x[i] = src[2 * i] | (uint32_t)src[2 * i + 1] << 16;
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; i++)
-                                s += QT == GGUF_BF16 ? bf2f(x[i] & 0xffff) + bf2f(x[i] >> 16) : h2f(x[i] & 0xffff) + h2f(x[i] >> 16);
-                        } else {
-                            const float *src = reinterpret_cast<const float *>(p.q) + at + 32 * b + 8 * q4;
-#pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                float x[2] = {there ? src[2 * i] : 0.0f, there ? src[2 * i + 1] : 0.0f};
-#pragma unroll
-                                for (int part = 0; part < QP; part++) {   // what the part before left over
-                                    const uint32_t lo = f2bf_rn(x[0]), hi = f2bf_rn(x[1]);
-                                    w[part][i] = lo | hi << 16;
-                                    x[0] -= bf2f((uint16_t)lo);
-                                    x[1] -= bf2f((uint16_t)hi);
-                                }
-                            }
+                        for (int i = 0; i < 4; i++) {   // pair i belongs to nibble i of the key's word
+                            const float x = up * from16<QT>(w[b][i] & 0xffff), y = up * from16<QT>(w[b][i] >> 16);
+                            const float f = i & 1 ? 0.0625f : 1.0f;
+                            qb[0][b][i >> 1][n][i & 1] = pack_h2(x * f, y * f);
+                            s = fmaf(i & 1 ? -72.0f : -1032.0f, x + y, s);
                         }
                         s += __shfl_xor_sync(0xffffffffu, s, 1);
                         s += __shfl_xor_sync(0xffffffffu, s, 2);
-                        corr[b][n] = -24.0f * s;
 #pragma unroll
-                        for (int part = 0; part < QP; part++)
-#pragma unroll
-                            for (int k = 0; k < 2; k++)
-#pragma unroll
-                                for (int i = 0; i < 2; i++) qa[part][b][k][n][i] = w[part][2 * k + i];
-#pragma unroll
-                        for (int j = 0; j < 2; j++)
-#pragma unroll
-                            for (int i = 0; i < 4; i++) o[b][j][n][i] = 0.0f;
+                        for (int j = 0; j < 2; j++) corr[b][n][j] = __shfl_sync(0xffffffffu, s, 8 * q4 + 4 * j);
                     }
-                }
-                fresh = false;
-            }
-            bool ok = false;
-            if (t < n_ahead) {
-                ok = tc::mbar_wait(&bars[warp][stage], phase);
-                if (!__all_sync(0xffffffffu, ok)) {   // given up: ask for no more, wait for what is under way
-                    if (lane == 0 && a.err != nullptr) atomicOr(a.err, 1);
-                    dead = true;
-                    ok = false;
-                }
-                ok = ok && !((bad >> stage) & 1);
-            }
-            const uint8_t *tile = ring + stage * L::BYTES;
-            if (ok) {
-                // ---- scores of 16 tokens: n-tile e holds tokens 8e + 2 q4, + 1
-                float s[2][NT == 2 ? 4 : 2];
+                } else {
 #pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    uint32_t ds[NB];
-                    lds_words<NB>(tile + L::KS + 4 * (4 * e + q4) * NB, ds);
+                    for (int j = 0; j < 2; j++) sl[n][j] = log2_scale;
 #pragma unroll
-                    for (int i = 0; i < (NT == 2 ? 4 : 2); i++) s[e][i] = 0.0f;
+                    for (int b = 0; b < NB; b++) {
+                        const float *from = reinterpret_cast<const float *>(p.q) + at + 32 * b + 8 * q4;
+                        corr[b][n][0] = corr[b][n][1] = 0.0f;
 #pragma unroll
-                    for (int c = 0; c < NC; c++) {
-                        uint32_t w[BW];
-                        lds_words<BW>(tile + 4 * ((e * NC + c) * 32 + lane) * BW, w);
+                        for (int i = 0; i < 4; i++) {
+                            float x = there ? from[2 * i] : 0.0f, y = there ? from[2 * i + 1] : 0.0f;
 #pragma unroll
-                        for (int x = 0; x < BW; x++) {
-                            const int b = c * BW + x;
-                            float acc[4];
-                            acc[0] = acc[1] = QT == GGUF_F32 ? 0.0f : corr[b][0];
-                            acc[2] = acc[3] = QT == GGUF_F32 || NT == 1 ? 0.0f : corr[b][NT - 1];
-                            uint32_t cb[4];
-                            if constexpr (QT == GGUF_F16) {
-                                cb[0] = codes_f16<0>(w[x]); cb[1] = codes_f16<1>(w[x]);
-                                cb[2] = codes_f16<2>(w[x]); cb[3] = codes_f16<3>(w[x]);
-                            } else {
-                                cb[0] = codes_bf16<0>(w[x]); cb[1] = codes_bf16<1>(w[x]);
-                                cb[2] = codes_bf16<2>(w[x]); cb[3] = codes_bf16<3>(w[x]);
+                            for (int part = 0; part < QP; part++) {   // what the part before left over
+                                const uint32_t lo = f2bf_rn(x), hi = f2bf_rn(y);
+                                qb[part][b][i >> 1][n][i & 1] = lo | hi << 16;
+                                x -= bf2f((uint16_t)lo);
+                                y -= bf2f((uint16_t)hi);
                             }
-                            if constexpr (QT == GGUF_F32) {   // the exact c - 8, so that nothing large cancels
-#pragma unroll
-                                for (int i = 0; i < 4; i++) {
-                                    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&cb[i]),
-                                                                     __float2bfloat162_rn(24.0f));
-                                    cb[i] = *reinterpret_cast<const uint32_t *>(&v);
-                                }
-                            }
-#pragma unroll
-                            for (int part = 0; part < QP; part++)
-#pragma unroll
-                                for (int k = 0; k < 2; k++) {
-                                    const uint32_t a1 = NT == 2 ? qa[part][b][k][NT - 1][0] : 0u;
-                                    const uint32_t a3 = NT == 2 ? qa[part][b][k][NT - 1][1] : 0u;
-                                    if constexpr (QT == GGUF_F16)
-                                        mma_f16_16816(acc, qa[part][b][k][0][0], a1, qa[part][b][k][0][1], a3, cb[2 * k], cb[2 * k + 1]);
-                                    else
-                                        mma_bf16_16816(acc, qa[part][b][k][0][0], a1, qa[part][b][k][0][1], a3, cb[2 * k], cb[2 * k + 1]);
-                                }
-                            const float2 d = __half22float2(u2h(ds[b]));
-#pragma unroll
-                            for (int i = 0; i < (NT == 2 ? 4 : 2); i++)
-                                s[e][i] = fmaf(acc[i], i & 1 ? d.y : d.x, s[e][i]);
                         }
                     }
                 }
-                // ---- what is not seen; scores in units of log2
-                const int tok = ad_token(cur);
-                const bool whole = tok + KV_TILE - 1 <= pos_lo &&
-                                   (p.window <= 0 || tok > pos_hi - p.window || tok + KV_TILE <= p.sinks);
-                uint32_t keep[2] = {0xffffffffu, 0xffffffffu};   // value scales of tokens that some row sees
 #pragma unroll
-                for (int e = 0; e < 2; e++)
+                for (int j = 0; j < 2; j++) {
+                    const int r2 = row0 + 8 * n + 2 * q4 + j;
+                    pos[n][j] = r2 < rows ? cur.q.pos0 + r2 / G : -1;
+                    m[n][j] = -INFINITY;
+                    lsum[n][j] = 0.0f;
+                }
 #pragma unroll
-                    for (int i = 0; i < (NT == 2 ? 4 : 2); i++) s[e][i] *= sl;
+                for (int b = 0; b < NB; b++)
+#pragma unroll
+                    for (int j = 0; j < 2; j++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) o[b][j][n][i] = 0.0f;
+            }
+            const bool began = cur.tile == 0;
+            const int seg_end = min(cur.q.nt, cur.tile + left_tiles);
+            left_tiles -= seg_end - cur.tile;
+            // tiles that every row sees whole: below full_sink, and from full_lo to full_hi
+            int full_sink = 0, full_lo = 0, full_hi = pos_lo < 0 ? 0 : (pos_lo + 1) / KV_TILE;
+            if (p.window > 0) {
+                full_sink = (int)min((int64_t)cur.q.n_sink, p.sinks / KV_TILE);
+                const int64_t lo = (int64_t)pos_hi - p.window + 1;   // first token that the last row sees
+                const int lo_tile = lo > 0 ? (int)((lo + KV_TILE - 1) / KV_TILE) : 0, shift = cur.q.n_sink - cur.q.w_tile;
+                full_lo = max(lo_tile + shift, cur.q.n_sink);
+                full_hi += shift;
+            }
+            while (cur.tile < seg_end) {
+                // ---- up to TP tiles
+                const uint8_t *tile0 = ring + stage * C::STEP;
+                uint32_t use = 0;
+                if (!dead) {
+                    if (__all_sync(0xffffffffu, tc::mbar_wait(&full[warp][stage], phase)))
+                        use = ~absent[warp][stage] & ((1u << min(TP, seg_end - cur.tile)) - 1);
+                    else {   // given up: no tile counts any more
+                        if (lane == 0 && a.err != nullptr) atomicOr(a.err, 1);
+                        *abort_flag = 1;
+                        dead = true;
+                    }
+                }
+                // ---- scores: tokens g and g + 8 of a tile, rows 2 q4 and 2 q4 + 1
+                float s[TP][NT][4];
+#pragma unroll
+                for (int x = 0; x < TP; x++) {
+#pragma unroll
+                    for (int n = 0; n < NT; n++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) s[x][n][i] = 0.0f;
+                    uint32_t ds[2][NB];
+#pragma unroll
+                    for (int e = 0; e < 2; e++) lds_words<NB>(tile0 + x * L::BYTES + L::KS + 4 * (4 * e + (g >> 1)) * NB, ds[e]);
+#pragma unroll
+                    for (int c = 0; c < NC; c++) {
+                        uint32_t w[2][BW];
+#pragma unroll
+                        for (int e = 0; e < 2; e++) lds_words<BW>(tile0 + x * L::BYTES + 4 * ((e * NC + c) * 32 + lane) * BW, w[e]);
+#pragma unroll
+                        for (int i = 0; i < BW; i++) {
+                            const int b = c * BW + i;
+                            uint32_t k0[4], k1[4];
+                            if constexpr (QT != GGUF_F32) {
+                                k0[0] = codes_f16<0>(w[0][i]); k0[1] = codes_f16<0>(w[1][i]);
+                                k0[2] = codes_f16<1>(w[0][i]); k0[3] = codes_f16<1>(w[1][i]);
+                                k1[0] = codes_f16<2>(w[0][i]); k1[1] = codes_f16<2>(w[1][i]);
+                                k1[2] = codes_f16<3>(w[0][i]); k1[3] = codes_f16<3>(w[1][i]);
+                            } else {
+                                k0[0] = signed_bf16<0>(w[0][i]); k0[1] = signed_bf16<0>(w[1][i]);
+                                k0[2] = signed_bf16<1>(w[0][i]); k0[3] = signed_bf16<1>(w[1][i]);
+                                k1[0] = signed_bf16<2>(w[0][i]); k1[1] = signed_bf16<2>(w[1][i]);
+                                k1[2] = signed_bf16<3>(w[0][i]); k1[3] = signed_bf16<3>(w[1][i]);
+                            }
+                            const float2 d = __half22float2(u2h(__byte_perm(ds[0][b], ds[1][b], (g & 1) ? 0x7632 : 0x5410)));
+#pragma unroll
+                            for (int n = 0; n < NT; n++) {
+                                float acc[4];
+                                mma_16816<QT == GGUF_F32>(acc, k0, qb[0][b][0][n][0], qb[0][b][0][n][1], corr[b][n][0],
+                                                          corr[b][n][1], corr[b][n][0], corr[b][n][1]);
+                                mma_16816<QT == GGUF_F32>(acc, k1, qb[0][b][1][n][0], qb[0][b][1][n][1], acc[0], acc[1], acc[2], acc[3]);
+#pragma unroll
+                                for (int part = 1; part < QP; part++) {
+                                    mma_16816<true>(acc, k0, qb[part][b][0][n][0], qb[part][b][0][n][1], acc[0], acc[1], acc[2], acc[3]);
+                                    mma_16816<true>(acc, k1, qb[part][b][1][n][0], qb[part][b][1][n][1], acc[0], acc[1], acc[2], acc[3]);
+                                }
+                                s[x][n][0] = fmaf(acc[0], d.x, s[x][n][0]);
+                                s[x][n][1] = fmaf(acc[1], d.x, s[x][n][1]);
+                                s[x][n][2] = fmaf(acc[2], d.y, s[x][n][2]);
+                                s[x][n][3] = fmaf(acc[3], d.y, s[x][n][3]);
+                            }
+                        }
+                    }
+                }
+                // ---- what is not seen
+                const int i1 = cur.tile + TP;
+                const bool whole = use == (1u << TP) - 1 && (i1 <= full_sink || (cur.tile >= full_lo && i1 <= full_hi));
+                uint32_t keep[TP][2];   // value scales of tokens that some row sees
                 if (!whole) {
 #pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        keep[e] = 0;
+                    for (int x = 0; x < TP; x++) {
+                        const bool there = (use >> x) & 1;
+                        const int i = cur.tile + x, tok = (i < cur.q.n_sink ? i : cur.q.w_tile + i - cur.q.n_sink) * KV_TILE;
 #pragma unroll
-                        for (int j = 0; j < 2; j++) {
-                            const int at = tok + 8 * e + 2 * q4 + j;
+                        for (int e = 0; e < 2; e++) {
+                            keep[x][e] = 0;
+#pragma unroll
+                            for (int j = 0; j < 2; j++) {
+                                const int at = tok + 8 * e + 2 * q4 + j;
+                                if (there && at <= pos_hi && (p.window <= 0 || at < p.sinks || at > pos_lo - p.window))
+                                    keep[x][e] |= 0xffffu << (16 * j);
+                            }
+                            const int at = tok + 8 * e + g;
                             const bool in = p.window <= 0 || at < p.sinks;
-                            if (at <= pos_hi && (in || at > pos_lo - p.window)) keep[e] |= 0xffffu << (16 * j);
 #pragma unroll
                             for (int n = 0; n < NT; n++)
-                                if (!(at <= pos[n] && (in || at > pos[n] - p.window))) s[e][2 * n + j] = -INFINITY;
+#pragma unroll
+                                for (int j = 0; j < 2; j++)
+                                    if (!(there && at <= pos[n][j] && (in || at > pos[n][j] - p.window))) s[x][n][2 * e + j] = -INFINITY;
                         }
                     }
                 }
                 // ---- online softmax
-                uint32_t pb[NT][2], pl[NT][2];
+                uint32_t pb[TP][NT][2], pl[TP][NT][2];
                 bool grew = false;
-                float alpha[NT];
+                float alpha[NT][2];
 #pragma unroll
-                for (int n = 0; n < NT; n++) {
-                    float mx = fmaxf(fmaxf(s[0][2 * n], s[0][2 * n + 1]), fmaxf(s[1][2 * n], s[1][2 * n + 1]));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    const float mn = fmaxf(m[n], mx);
-                    alpha[n] = 1.0f;
-                    if (mn > m[n]) {
-                        alpha[n] = ex2(m[n] - mn);   // 0 from -inf
-                        grew = true;
-                    }
-                    m[n] = mn;
-                    const float base = mn == -INFINITY ? 0.0f : AD_PBITS - mn;
-                    float pr[2][2];
+                for (int n = 0; n < NT; n++)
 #pragma unroll
-                    for (int e = 0; e < 2; e++)
+                    for (int j = 0; j < 2; j++) {
+                        float mx = -INFINITY;
 #pragma unroll
-                        for (int j = 0; j < 2; j++) pr[e][j] = ex2(s[e][2 * n + j] + base);
-                    lsum[n] = fmaf(lsum[n], alpha[n], (pr[0][0] + pr[0][1]) + (pr[1][0] + pr[1][1]));
+                        for (int x = 0; x < TP; x++) mx = fmaxf(mx, fmaxf(s[x][n][j], s[x][n][2 + j]));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        const float mn = fmaxf(m[n][j], mx * sl[n][j]);
+                        alpha[n][j] = 1.0f;
+                        if (mn > m[n][j]) {
+                            alpha[n][j] = ex2(m[n][j] - mn);   // 0 from -inf
+                            grew = true;
+                        }
+                        m[n][j] = mn;
+                        const float base = mn == -INFINITY ? 0.0f : AD_PBITS - mn;
+                        lsum[n][j] *= alpha[n][j];
 #pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        pb[n][e] = pack_h2(pr[e][0], pr[e][1]);
-                        if constexpr (QT == GGUF_F32) {
-                            const float2 hi = __half22float2(u2h(pb[n][e]));
-                            pl[n][e] = pack_h2(pr[e][0] - hi.x, pr[e][1] - hi.y);
+                        for (int x = 0; x < TP; x++) {
+                            s[x][n][j] = ex2(fmaf(s[x][n][j], sl[n][j], base));
+                            s[x][n][2 + j] = ex2(fmaf(s[x][n][2 + j], sl[n][j], base));
+                            lsum[n][j] += s[x][n][j] + s[x][n][2 + j];
                         }
                     }
-                }
+#pragma unroll
+                for (int x = 0; x < TP; x++)
+#pragma unroll
+                    for (int n = 0; n < NT; n++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            const uint32_t hi = pack_h2(s[x][n][2 * e], s[x][n][2 * e + 1]);
+                            pb[x][n][e] = transpose8(hi);
+                            if constexpr (QT == GGUF_F32) {
+                                const float2 f = __half22float2(u2h(hi));
+                                pl[x][n][e] = transpose8(pack_h2(s[x][n][2 * e] - f.x, s[x][n][2 * e + 1] - f.y));
+                            }
+                        }
                 if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-                    for (int n = 0; n < NT; n++) {   // the columns of O^T: rows 2 q4, 2 q4 + 1
-                        const float a0 = __shfl_sync(0xffffffffu, alpha[n], 8 * q4);
-                        const float a1 = __shfl_sync(0xffffffffu, alpha[n], 8 * q4 + 4);
+                    for (int n = 0; n < NT; n++)
 #pragma unroll
                         for (int b = 0; b < NB; b++)
 #pragma unroll
-                            for (int j = 0; j < 2; j++) {
-                                o[b][j][n][0] *= a0; o[b][j][n][1] *= a1;
-                                o[b][j][n][2] *= a0; o[b][j][n][3] *= a1;
-                            }
-                    }
+                            for (int j = 0; j < 2; j++)
+#pragma unroll
+                                for (int i = 0; i < 4; i++) o[b][j][n][i] *= alpha[n][i & 1];
                 }
                 // ---- outputs
-                uint32_t dv[2][NB];
 #pragma unroll
-                for (int e = 0; e < 2; e++) lds_words<NB>(tile + L::VS + 4 * (4 * e + q4) * NB, dv[e]);
-                if (!whole) {
+                for (int x = 0; x < TP; x++) {
+                    uint32_t dv[2][NB];
 #pragma unroll
-                    for (int b = 0; b < NB; b++) { dv[0][b] &= keep[0]; dv[1][b] &= keep[1]; }
-                }
+                    for (int e = 0; e < 2; e++) lds_words<NB>(tile0 + x * L::BYTES + L::VS + 4 * (4 * e + q4) * NB, dv[e]);
+                    if (!whole) {
 #pragma unroll
-                for (int c = 0; c < NC; c++) {
-                    uint32_t w[2][BW];
+                        for (int b = 0; b < NB; b++) { dv[0][b] &= keep[x][0]; dv[1][b] &= keep[x][1]; }
+                    }
 #pragma unroll
-                    for (int e = 0; e < 2; e++) lds_words<BW>(tile + L::VC + 4 * ((e * NC + c) * 32 + lane) * BW, w[e]);
+                    for (int c = 0; c < NC; c++) {
+                        uint32_t w[2][BW];
 #pragma unroll
-                    for (int x = 0; x < BW; x++) {
-                        const int b = c * BW + x;
-                        const __half2 off = u2h(0x64086408u);   // 1032
-                        __half2 v[2][4];
+                        for (int e = 0; e < 2; e++) lds_words<BW>(tile0 + x * L::BYTES + L::VC + 4 * ((e * NC + c) * 32 + lane) * BW, w[e]);
 #pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            v[e][0] = __hsub2(codes_1024<0>(w[e][x]), off);
-                            v[e][1] = __hsub2(codes_1024<1>(w[e][x]), off);
-                            v[e][2] = __hsub2(codes_1024<2>(w[e][x]), off);
-                            v[e][3] = __hsub2(codes_1024<3>(w[e][x]), off);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 2; j++) {
+                        for (int i = 0; i < BW; i++) {
+                            const int b = c * BW + i;
                             const __half2 d0 = u2h(dv[0][b]), d1 = u2h(dv[1][b]);
-                            const __half2 f0 = __hmul2(v[0][2 * j], d0), f1 = __hmul2(v[0][2 * j + 1], d0);
-                            const __half2 f2 = __hmul2(v[1][2 * j], d1), f3 = __hmul2(v[1][2 * j + 1], d1);
+                            const __half2 v[2][4] = {{signed_f16<0>(w[0][i]), signed_f16<1>(w[0][i]), signed_f16<2>(w[0][i]), signed_f16<3>(w[0][i])},
+                                                     {signed_f16<0>(w[1][i]), signed_f16<1>(w[1][i]), signed_f16<2>(w[1][i]), signed_f16<3>(w[1][i])}};
 #pragma unroll
-                            for (int n = 0; n < NT; n++)
-                                mma_f16_16816(o[b][j][n], h2u(f0), h2u(f1), h2u(f2), h2u(f3), pb[n][0], pb[n][1]);
-                            if constexpr (QT == GGUF_F32) {
-                                const __half2 l0 = __hfma2(v[0][2 * j], d0, __hneg2(f0));
-                                const __half2 l1 = __hfma2(v[0][2 * j + 1], d0, __hneg2(f1));
-                                const __half2 l2 = __hfma2(v[1][2 * j], d1, __hneg2(f2));
-                                const __half2 l3 = __hfma2(v[1][2 * j + 1], d1, __hneg2(f3));
+                            for (int j = 0; j < 2; j++) {
+                                const __half2 f[4] = {__hmul2(v[0][2 * j], d0), __hmul2(v[0][2 * j + 1], d0),
+                                                      __hmul2(v[1][2 * j], d1), __hmul2(v[1][2 * j + 1], d1)};
+                                const uint32_t fa[4] = {h2u(f[0]), h2u(f[1]), h2u(f[2]), h2u(f[3])};
 #pragma unroll
                                 for (int n = 0; n < NT; n++) {
-                                    mma_f16_16816(o[b][j][n], h2u(l0), h2u(l1), h2u(l2), h2u(l3), pb[n][0], pb[n][1]);
-                                    mma_f16_16816(o[b][j][n], h2u(f0), h2u(f1), h2u(f2), h2u(f3), pl[n][0], pl[n][1]);
+                                    float(&oo)[4] = o[b][j][n];
+                                    mma_16816<false>(oo, fa, pb[x][n][0], pb[x][n][1], oo[0], oo[1], oo[2], oo[3]);
+                                    if constexpr (QT == GGUF_F32) {
+                                        const uint32_t la[4] = {h2u(__hfma2(v[0][2 * j], d0, __hneg2(f[0]))), h2u(__hfma2(v[0][2 * j + 1], d0, __hneg2(f[1]))),
+                                                                h2u(__hfma2(v[1][2 * j], d1, __hneg2(f[2]))), h2u(__hfma2(v[1][2 * j + 1], d1, __hneg2(f[3])))};
+                                        mma_16816<false>(oo, la, pb[x][n][0], pb[x][n][1], oo[0], oo[1], oo[2], oo[3]);
+                                        mma_16816<false>(oo, fa, pl[x][n][0], pl[x][n][1], oo[0], oo[1], oo[2], oo[3]);
+                                    }
                                 }
                             }
                         }
                     }
                 }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&freed[warp][stage]);
+                cur.tile = min(cur.tile + TP, seg_end);
+                if (++stage == ST) { stage = 0; phase ^= 1; }
             }
-            __syncwarp();   // the stage is free
-            if (n_ahead < t1 && !dead) ask(stage);
-            if (++stage == ST) { stage = 0; phase ^= 1; }
 
             // ---- the unit's or the warp's end
-            const bool unit_end = cur.tile == cur.q.nt - 1;
-            if (unit_end || t == t1 - 1) {
-                const bool began = t - cur.tile >= t0;   // with this warp
 #pragma unroll
-                for (int n = 0; n < NT; n++) {
-                    lsum[n] += __shfl_xor_sync(0xffffffffu, lsum[n], 1);
-                    lsum[n] += __shfl_xor_sync(0xffffffffu, lsum[n], 2);
-                }
-                if (unit_end && began) {   // a whole unit
-                    const int row0 = cur.u / (int)p.hk * RG, head0 = cur.u % (int)p.hk * G, rows = cur.q.q * G;
+            for (int n = 0; n < NT; n++)
 #pragma unroll
-                    for (int n = 0; n < NT; n++)
+                for (int j = 0; j < 2; j++)
 #pragma unroll
-                        for (int j = 0; j < 2; j++) {
-                            const float l = __shfl_sync(0xffffffffu, lsum[n], 8 * q4 + 4 * j);
-                            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                            const int row = row0 + 8 * n + 2 * q4 + j;
-                            if (row < rows) {
-                                const int64_t at = (cur.q.rows0 + row / G) * p.ldo + (int64_t)(head0 + row % G) * D;
+                    for (int i = 4; i < 32; i <<= 1) lsum[n][j] += __shfl_xor_sync(0xffffffffu, lsum[n][j], i);
+            const bool unit_end = cur.tile == cur.q.nt;
+            if (unit_end && began) {   // a whole unit
 #pragma unroll
-                                for (int b = 0; b < NB; b++)
-                                    store4<QT>(p.out, at + 32 * b + 4 * g, a.vec, o[b][0][n][j] * inv, o[b][0][n][2 + j] * inv,
-                                               o[b][1][n][j] * inv, o[b][1][n][2 + j] * inv);
-                            }
-                        }
-                } else {
-                    // a unit from before the warp leaves its piece beside the ring; one that goes on past the warp
-                    // ends with the warp's last tile, and takes the ring, where no copy is under way any more
-                    flags |= began ? 4 : unit_end ? 1 : 3;
-                    if (began) { open_r = cur.r; open_u = cur.u; open_end = t - cur.tile + cur.q.nt; }
-                    float *dst = reinterpret_cast<float *>(began ? ring : smem + C::WARPS * C::RING + warp * C::SLOT);
+                for (int n = 0; n < NT; n++)
 #pragma unroll
-                    for (int n = 0; n < NT; n++) {
-#pragma unroll
-                        for (int j = 0; j < 2; j++)
+                    for (int j = 0; j < 2; j++) {
+                        const float inv = lsum[n][j] == 0.0f ? 0.0f : 1.0f / lsum[n][j];
+                        const int row = row0 + 8 * n + 2 * q4 + j;
+                        if (row < rows) {
+                            const int64_t at = (cur.q.rows0 + row / G) * p.ldo + (int64_t)(head0 + row % G) * D;
 #pragma unroll
                             for (int b = 0; b < NB; b++)
-                                *reinterpret_cast<float4 *>(dst + (8 * n + 2 * q4 + j) * D + 32 * b + 4 * g) =
-                                    make_float4(o[b][0][n][j], o[b][0][n][2 + j], o[b][1][n][j], o[b][1][n][2 + j]);
-                        if (q4 == 0) {
-                            dst[RG * D + 2 * (8 * n + g)] = m[n];
-                            dst[RG * D + 2 * (8 * n + g) + 1] = lsum[n];
+                                store4<QT>(p.out, at + 32 * b + 4 * g, a.vec, o[b][0][n][j] * inv, o[b][0][n][2 + j] * inv,
+                                           o[b][1][n][j] * inv, o[b][1][n][2 + j] * inv);
                         }
                     }
-                }
-                fresh = true;
+            } else {
+                // a unit from before the warp leaves its piece beside the ring; one that goes on past the warp ends
+                // with the warp's last tile, and takes the ring, where no copy is under way any more
+                flags |= began ? 4 : unit_end ? 1 : 3;
+                if (began) { open_r = cur.r; open_u = cur.u; open_end = t1 + cur.q.nt - cur.tile; }
+                __syncwarp();
+                float *dst = reinterpret_cast<float *>(began ? ring : smem + C::WARPS * C::RING + warp * C::SLOT);
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                    for (int j = 0; j < 2; j++) {
+#pragma unroll
+                        for (int b = 0; b < NB; b++)
+                            *reinterpret_cast<float4 *>(dst + (8 * n + 2 * q4 + j) * D + 32 * b + 4 * g) =
+                                make_float4(o[b][0][n][j], o[b][0][n][2 + j], o[b][1][n][j], o[b][1][n][2 + j]);
+                        if (g == 0) {
+                            dst[RG * D + 2 * (8 * n + 2 * q4 + j)] = m[n][j];
+                            dst[RG * D + 2 * (8 * n + 2 * q4 + j) + 1] = lsum[n][j];
+                        }
+                    }
             }
-            if (t + 1 < t1) ad_advance<RG>(a, cur);
+            if (left_tiles > 0) ad_next_unit<RG>(a, cur);
         }
     }
     if (lane == 0) {
@@ -620,7 +725,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::WARPS * 32) attn_decode_kern
         left_u[warp] = open_u;
         left_end[warp] = open_end;
     }
-    __syncthreads();
+    join_warps();
 
     // ---- the CTA's pieces: a chain is the piece that opens a unit (or the first warp's piece of a unit from the CTA
     // before) and the pieces of the warps after it
@@ -632,7 +737,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::WARPS * 32) attn_decode_kern
     };
     auto join = [&](int end, bool open) {   // pieces of warps chain .. end
         const bool ring1 = !orphan;          // the first piece lies in the ring
-        for (int it = tid; it < RG * D / 4; it += NTHR) {
+        for (int it = tid; it < RG * D / 4; it += NCOMP) {
             const int row = it / (D / 4), col = it % (D / 4) * 4;
             float mx = -INFINITY;
             for (int w = chain; w <= end; w++) mx = fmaxf(mx, piece(w, ring1 && w == chain)[RG * D + 2 * row]);
@@ -764,10 +869,10 @@ static cudaError_t attn_decode_run(const AdShape &a, int ctas, cudaStream_t s) {
     using C = AdCfg<D, QT, NT>;
     cudaError_t err = cudaSuccess;
     const void *kern = (const void *)attn_decode_kernel<D, QT, NT>;
-    if (kernel_occupancy(kern, C::WARPS * 32, C::SMEM, &err) == 0) return err;
+    if (kernel_occupancy(kern, C::THREADS, C::SMEM, &err) == 0) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(C::WARPS * 32);
+    cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

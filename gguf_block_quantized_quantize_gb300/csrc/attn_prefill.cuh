@@ -211,9 +211,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                     // a row's lanes lie in one warp and all of them are here (AP_THREADS and ROWS are multiples of 32 / LPR rows)
 #pragma unroll
                     for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    // a power of two that takes the largest value into [2^8, 2^9)
-                    const uint32_t e = max(__float_as_uint(mx) >> 23, 16u);
-                    const float up = __uint_as_float(mx == 0.0f ? 127u << 23 : min(262u - e, 254u) << 23);
+                    const float up = q_scale_up(mx);
 #pragma unroll
                     for (int i = 0; i < 4; i++) w[i] = pack_h2(v[2 * i] * up, v[2 * i + 1] * up);
                     if (l == 0) q_inv[row] = 1.0f / up;
@@ -422,12 +420,11 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                             for (int i = 0; i < BW; i++) {
                                 const int b = c * BW + (i ^ (g & 1));
                                 const __half2 d = u2h(__byte_perm(ds[i], 0, (g & 1) ? 0x3232 : 0x1010));
-                                const __half2 off = u2h(0x64086408u);
                                 uint4 o;
-                                o.x = h2u(__hmul2(__hsub2(codes_1024<0>(w[i]), off), d));
-                                o.y = h2u(__hmul2(__hsub2(codes_1024<1>(w[i]), off), d));
-                                o.z = h2u(__hmul2(__hsub2(codes_1024<2>(w[i]), off), d));
-                                o.w = h2u(__hmul2(__hsub2(codes_1024<3>(w[i]), off), d));
+                                o.x = h2u(__hmul2(signed_f16<0>(w[i]), d));
+                                o.y = h2u(__hmul2(signed_f16<1>(w[i]), d));
+                                o.z = h2u(__hmul2(signed_f16<2>(w[i]), d));
+                                o.w = h2u(__hmul2(signed_f16<3>(w[i]), d));
                                 const int chunk = 4 * b + q4;   // of 8 values
                                 *reinterpret_cast<uint4 *>(sk + (chunk >> 3) * (BT * 128) + row * 128 +
                                                            (((chunk & 7) ^ (row & 7)) * 16)) = o;
@@ -477,7 +474,6 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
 #pragma unroll
                     for (int i = 0; i < XS; i++) {
                         const int b = hb * XS + i;
-                        const __half2 off = u2h(0x64086408u);
                         auto put = [&](int nib, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
                             const int row = 32 * b + 4 * g + nib;
                             *reinterpret_cast<uint4 *>(sv + gi * (D * 128) + row * 128 + ((chunk ^ (row & 7)) * 16)) =
@@ -487,10 +483,10 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
 #pragma unroll
                         for (int q = 0; q < 4; q++) {
                             const __half2 d = u2h(dv[q][i]);
-                            x[0][q] = h2u(__hmul2(__hsub2(codes_1024<0>(w[q][i]), off), d));
-                            x[1][q] = h2u(__hmul2(__hsub2(codes_1024<1>(w[q][i]), off), d));
-                            x[2][q] = h2u(__hmul2(__hsub2(codes_1024<2>(w[q][i]), off), d));
-                            x[3][q] = h2u(__hmul2(__hsub2(codes_1024<3>(w[q][i]), off), d));
+                            x[0][q] = h2u(__hmul2(signed_f16<0>(w[q][i]), d));
+                            x[1][q] = h2u(__hmul2(signed_f16<1>(w[q][i]), d));
+                            x[2][q] = h2u(__hmul2(signed_f16<2>(w[q][i]), d));
+                            x[3][q] = h2u(__hmul2(signed_f16<3>(w[q][i]), d));
                         }
 #pragma unroll
                         for (int nib = 0; nib < 4; nib++) put(nib, x[nib][0], x[nib][1], x[nib][2], x[nib][3]);

@@ -48,4 +48,7 @@ struct KvTile {
     static __device__ __forceinline__ int scale(int t, int b) { return 2 * (((t >> 1) * NB + b) * 2 + (t & 1)); }
 };
 
+template <int T>
+__device__ __forceinline__ float from16(uint32_t h) { return T == GGUF_BF16 ? bf2f((uint16_t)h) : h2f((uint16_t)h); }
+
 }  // namespace gg

@@ -24,9 +24,6 @@ namespace gg {
 
 constexpr int QR_THREADS = 256;
 
-template <int T>
-__device__ __forceinline__ float from16(uint32_t h) { return T == GGUF_BF16 ? bf2f((uint16_t)h) : h2f((uint16_t)h); }
-
 // 8 values at element offset `off` of x, 16-byte aligned (VEC) or element-aligned
 template <int T, bool VEC>
 __device__ __forceinline__ void ld8(const void *x, int64_t off, float (&v)[8]) {
