@@ -299,71 +299,76 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_COPY));
         const int who = (warp - C::WARPS) * 4 + (lane >> 3), l8 = lane & 7;
         if ((warp - C::WARPS) * 4 >= C::WARPS) return;
-        const uint32_t group = 0xffu << (lane & 24);
         const int64_t t0 = min(cta1, cta0 + who * per_warp), t1 = min(cta1, t0 + per_warp);
         int tiles = who < C::WARPS ? (int)min(t1 - t0, (int64_t)0x7fffffff) : 0;   // to ask for
         int unit = 0;                 // of them, those of the unit
-        int step = 0;                 // steps asked for
+        int stage = 0, uses = 0;      // next stage, and how often the ring has gone round
         int base = 0, of = -1;        // the table entries: first page, and request
         int32_t now8 = -1, next8 = -1;
-        const int tpp = (int)(p.page / KV_TILE);
-        AdCursor feed;
+        const uint32_t tpp = (uint32_t)(p.page / KV_TILE);
+        const int shift = (tpp & (tpp - 1)) == 0 ? __ffs(tpp) - 1 : -1;
+        AdCursor feed{};
         if (tiles > 0) feed = locate(t0);
+        const uint8_t *head = nullptr;   // the unit's head in page 0
         uint64_t idle_since = 0;
+        // the lanes stay together: a step is taken by all groups whose stage is free
         for (;;) {
-            const int stage = step % ST;
-            const bool can = tiles > 0 && (step < ST || mbar_test(&freed[who][stage], (uint32_t)(step / ST - 1) & 1u));
-            if (__any_sync(group, can)) {   // (a lane that saw the stage free speaks for the others)
-                if (unit == 0) {
-                    if (feed.tile == feed.q.nt) ad_next_unit<RG>(a, feed);
-                    unit = min(tiles, feed.q.nt - feed.tile);
-                }
-                const int cnt = min(TP, unit), i = feed.tile + min(l8, cnt - 1);
-                const int at = i < feed.q.n_sink ? i : feed.q.w_tile + i - feed.q.n_sink;   // tile of the request
-                const int page_at = (int)((uint32_t)at / (uint32_t)tpp), in_page = at - page_at * tpp;
-                const int first = __shfl_sync(group, page_at, lane & 24);
-                const int32_t *row = p.table + feed.r * p.ld;
-                if (of == feed.r && first >= base + 8 && first < base + 16) {
-                    base += 8;
-                    now8 = next8;
-                    next8 = base + 8 + l8 < p.width ? row[base + 8 + l8] : -1;
-                } else if (of != feed.r || first < base || first >= base + 8) {
-                    of = feed.r;
-                    base = first & ~7;
-                    now8 = base + l8 < p.width ? row[base + l8] : -1;
-                    next8 = base + 8 + l8 < p.width ? row[base + 8 + l8] : -1;
-                }
-                const int d = page_at - base;
-                const int32_t e0 = __shfl_sync(group, now8, (lane & 24) | (d & 7)), e1 = __shfl_sync(group, next8, (lane & 24) | (d & 7));
-                // a step may reach from the first tokens into the window: then the entry is read on the spot
-                const int32_t pg = d < 8 ? e0 : d < 16 ? e1 : page_at < p.width ? row[page_at] : -1;
-                const bool ok = l8 < cnt && pg >= 0 && pg < p.n_pages;
-                const uint32_t have = (__ballot_sync(group, ok) >> (lane & 24)) & 0xffu;
-                if (l8 == 0) {
-                    const uint32_t none = ~have & ((1u << cnt) - 1);
-                    absent[who][stage] = none;
-                    tc::mbar_arrive_expect_tx(&full[who][stage], (uint32_t)__popc(have) * L::BYTES);
-                    if (none && p.status != nullptr) atomicAdd(p.status, __popc(none));
-                }
-                __syncwarp(group);
-                if (ok)
-                    bulk_load(smem + who * C::RING + stage * C::STEP + l8 * L::BYTES,
-                              p.cache + pg * kv_page_bytes(D, p.hk, p.page) +
-                                  ((int64_t)(feed.u % (int)p.hk) * tpp + in_page) * L::BYTES,
-                              L::BYTES, &full[who][stage]);
+            bool go = tiles > 0 && (uses == 0 || mbar_test(&freed[who][stage], (uint32_t)(uses - 1) & 1u));
+            go = __shfl_sync(0xffffffffu, go, lane & 24);
+            if (!__any_sync(0xffffffffu, go)) {
+                if (!__any_sync(0xffffffffu, tiles > 0 && !*abort_flag)) break;
+                const uint64_t now = tc::globaltimer();
+                if (idle_since == 0) idle_since = now;
+                if (__any_sync(0xffffffffu, now - idle_since > tc::kWaitLimitNs)) { *abort_flag = 1; break; }
+                __nanosleep(20);
+                continue;
+            }
+            idle_since = 0;
+            if (go && unit == 0) {
+                if (feed.tile == feed.q.nt) ad_next_unit<RG>(a, feed);
+                unit = min(tiles, feed.q.nt - feed.tile);
+                head = p.cache + (int64_t)(feed.u % (int)p.hk) * tpp * L::BYTES;
+            }
+            __syncwarp();
+            const int cnt = min(TP, unit), i = feed.tile + max(min(l8, cnt - 1), 0);
+            const int at = i < feed.q.n_sink ? i : feed.q.w_tile + i - feed.q.n_sink;   // tile of the request
+            const int page_at = shift >= 0 ? at >> shift : (int)((uint32_t)at / tpp), in_page = at - page_at * (int)tpp;
+            const int first = __shfl_sync(0xffffffffu, page_at, lane & 24);
+            const int32_t *row = p.table + feed.r * p.ld;
+            if (go && (of != feed.r || first < base || first >= base + 8)) {
+                const bool slide = of == feed.r && first >= base + 8 && first < base + 16;
+                base = slide ? base + 8 : first & ~7;
+                now8 = slide ? next8 : base + l8 < p.width ? row[base + l8] : -1;
+                next8 = base + 8 + l8 < p.width ? row[base + 8 + l8] : -1;
+                of = feed.r;
+            }
+            __syncwarp();
+            const int d = page_at - base;
+            const int32_t e0 = __shfl_sync(0xffffffffu, now8, (lane & 24) | (d & 7));
+            const int32_t e1 = __shfl_sync(0xffffffffu, next8, (lane & 24) | (d & 7));
+            int32_t pg = d < 8 ? e0 : e1;
+            // a step may reach from the first tokens into the window: then the entry is read on the spot
+            if (go && (d < 0 || d >= 16)) pg = page_at < p.width ? row[page_at] : -1;
+            const bool ok = go && l8 < cnt && pg >= 0 && pg < p.n_pages;
+            const uint32_t have = (__ballot_sync(0xffffffffu, ok) >> (lane & 24)) & 0xffu;
+            if (go && l8 == 0) {
+                const uint32_t none = ~have & ((1u << cnt) - 1);
+                absent[who][stage] = none;
+                tc::mbar_arrive_expect_tx(&full[who][stage], (uint32_t)__popc(have) * L::BYTES);
+                if (none && p.status != nullptr) atomicAdd(p.status, __popc(none));
+            }
+            __syncwarp();
+            if (ok)
+                bulk_load(smem + who * C::RING + stage * C::STEP + l8 * L::BYTES,
+                          head + pg * kv_page_bytes(D, p.hk, p.page) + in_page * L::BYTES, L::BYTES, &full[who][stage]);
+            if (go) {
                 feed.tile += cnt;
                 tiles -= cnt;
                 unit -= cnt;
-                step++;
-                idle_since = 0;
-            } else if (tiles > 0) {
-                const uint64_t now = tc::globaltimer();
-                if (idle_since == 0) idle_since = now;
-                if (now - idle_since > tc::kWaitLimitNs) *abort_flag = 1;
-                __nanosleep(20);
+                if (++stage == ST) { stage = 0; uses++; }
             }
-            if (!__any_sync(0xffffffffu, tiles > 0 && !*abort_flag)) break;
         }
+        const int step = uses * ST + stage;
         if (*abort_flag && who < C::WARPS)   // copies that are under way land before the CTA exits
             for (int i = max(0, step - ST); i < step; i++) tc::mbar_wait(&full[who][i % ST], (uint32_t)(i / ST) & 1u);
         return;
@@ -391,7 +396,6 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             float sl[NT][2];                 // scores to log2 units
             float o[NB][2][NT][4];
             float m[NT][2], lsum[NT][2];
-            int pos[NT][2];                  // positions of rows 2 q4, + 1; -1 for a row that is not there
 #pragma unroll
             for (int n = 0; n < NT; n++) {
                 const int row = row0 + g + 8 * n;
@@ -456,8 +460,6 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                 }
 #pragma unroll
                 for (int j = 0; j < 2; j++) {
-                    const int r2 = row0 + 8 * n + 2 * q4 + j;
-                    pos[n][j] = r2 < rows ? cur.q.pos0 + r2 / G : -1;
                     m[n][j] = -INFINITY;
                     lsum[n][j] = 0.0f;
                 }
@@ -549,6 +551,14 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                 const bool whole = use == (1u << TP) - 1 && (i1 <= full_sink || (cur.tile >= full_lo && i1 <= full_hi));
                 uint32_t keep[TP][2];   // value scales of tokens that some row sees
                 if (!whole) {
+                    int pos[NT][2];   // positions of rows 2 q4, + 1; -1 for a row that is not there
+#pragma unroll
+                    for (int n = 0; n < NT; n++)
+#pragma unroll
+                        for (int j = 0; j < 2; j++) {
+                            const int row = row0 + 8 * n + 2 * q4 + j;
+                            pos[n][j] = row < rows ? cur.q.pos0 + row / G : -1;
+                        }
 #pragma unroll
                     for (int x = 0; x < TP; x++) {
                         const bool there = (use >> x) & 1;
