@@ -14,19 +14,20 @@ cudaError_t launch_attn_prefill_128(const AdShape &a, int ctas, cudaStream_t s);
 cudaError_t launch_attn_prefill_256(const AdShape &a, int ctas, cudaStream_t s);
 
 // one CTA per SM (the rings take the shared memory of one)
-static int decode_ctas() { return device_info().sm_count < AC_MAX ? device_info().sm_count : AC_MAX; }
+constexpr int MAX_CTAS = 1024;
+static int decode_ctas() { return device_info().sm_count < MAX_CTAS ? device_info().sm_count : MAX_CTAS; }
 
-// two partial results of up to 16 rows (8 rows of 256 values) per CTA, and its four words of meta data
+// two partial results of up to 16 rows (8 rows of 256 values) per CTA, and its meta data
 size_t attn_ws_size(const Attn &p, int64_t d) {
     (void)p;
-    return (size_t)decode_ctas() * (2 * (d == 256 ? 8 : 16) * (d + 2) * 4 + 16);
+    return (size_t)decode_ctas() * (2 * (d == 256 ? 8 : 16) * (d + 2) * 4 + sizeof(AdMeta));
 }
 
 cudaError_t launch_attn(const Attn &p, int64_t d, void *ws, cudaStream_t s) {
     const int ctas = decode_ctas();
     const int64_t es = p.qt == GGUF_F32 ? 4 : 2;
-    AdShape a{p, 0, 0x7fffffff, 0, (float *)ws, nullptr, tg_error_word()};
-    a.meta = (int32_t *)((uint8_t *)ws + (size_t)ctas * 2 * (d == 256 ? 8 : 16) * (d + 2) * 4);
+    AdShape a{p, 0, 0x7fffffff, 0, 0, (float *)ws, nullptr, tg_error_word()};
+    a.meta = (AdMeta *)((uint8_t *)ws + (size_t)ctas * 2 * (d == 256 ? 8 : 16) * (d + 2) * 4);
     a.vec = (reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.out)) % 16 == 0 && p.ldq * es % 16 == 0 &&
             p.ldo * es % 16 == 0;
     // requests with few query rows per KV head go to the decode kernel, the others to the prefill kernel (which

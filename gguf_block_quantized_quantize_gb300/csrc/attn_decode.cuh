@@ -30,6 +30,8 @@
 // high and low fp16 parts of p and v, for fp32 accuracy.
 #pragma once
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 #include "kv.cuh"
@@ -55,13 +57,19 @@ struct AdCfg {
     static constexpr int SMEM = WARPS * (RING + SLOT);
 };
 
+// the unit that a CTA began and did not end: the CTAs after it that hold pieces of it (0: there is none), its
+// request's first query token, its first head, its first row; how many rows
+struct AdMeta {
+    int32_t follow, rows0, head0, row0, rows, pad[3];
+};
 // what the requests look like to the kernels of one call
 struct AdShape {
     Attn p;
     int32_t min_rows, max_rows;   // requests with more than min_rows and at most max_rows query rows per KV head are taken
     int32_t vec;                  // rows of q and out start on 16 bytes
+    int32_t whole;                // each CTA takes one whole unit (few short ones), and nothing is left to join
     float *part;                  // CTA-level partial results, two slots per CTA
-    int32_t *meta;                // per CTA: units that continue past it (see attn_combine_kernel)
+    AdMeta *meta;                 // per CTA: the unit that goes on past it
     int *err;                     // error word: a wait for a copy was given up
 };
 
@@ -96,9 +104,14 @@ __device__ __forceinline__ AdReq ad_request(const AdShape &a, int r) {
     }
     return o;
 }
-__device__ __forceinline__ int64_t ad_tiles(const AdShape &a, const AdReq &q, int rg) {
+// its units: groups of rg query rows x KV heads
+__device__ __forceinline__ int64_t ad_units(const AdShape &a, const AdReq &q, int rg) {
     const int G = (int)(a.p.h / a.p.hk);
-    return (int64_t)q.nt * ((q.q * G + rg - 1) / rg) * a.p.hk;
+    return (int64_t)((q.q * G + rg - 1) / rg) * a.p.hk;
+}
+// a / b of non-negative numbers, mostly small ones
+__device__ __forceinline__ int64_t ad_div(int64_t a, int64_t b) {
+    return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
 // d = A B + c of the warp-level 16x8x16 product, fp16 or (BF) bf16 operands
@@ -233,8 +246,9 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[C::WARPS][ST], freed[C::WARPS][ST];
     __shared__ uint32_t absent[C::WARPS][ST];   // tiles of a stage that have no page
-    __shared__ int64_t chunk_end[C::THREADS];
+    __shared__ AdCursor starts[C::WARPS];
     __shared__ int64_t warp_sum[C::THREADS / 32];
+    __shared__ int32_t cta_tiles;
     __shared__ int32_t abort_word;
     volatile int32_t *abort_flag = &abort_word;
     // what each warp leaves at its end: 1 a piece of a unit that began before the warp, which 2 goes on past the
@@ -251,47 +265,65 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // tiles of all requests: thread t holds those of requests [t * per, (t + 1) * per)
+    // The cut.  Thread t holds requests [t * per, (t + 1) * per) of the sequence of tiles (or of units, where a CTA
+    // takes one whole unit) and, once the sum of what comes before is known, writes down where the warps start whose
+    // first tile lies in them.
     constexpr int NTHR = C::THREADS;
-    const int R = (int)p.R, per = (R + NTHR - 1) / NTHR;
+    const int R = (int)p.R, per = (R + NTHR - 1) / NTHR, r0 = tid * per, r1 = min(R, r0 + per);
+    AdReq rq{};
     int64_t mine = 0;
-    for (int r = tid * per; r < min(R, (tid + 1) * per); r++) mine += ad_tiles(a, ad_request(a, r), RG);
-    int64_t incl = mine;
+    for (int r = r0; r < r1; r++) {
+        rq = ad_request(a, r);
+        mine += ad_units(a, rq, RG) * (a.whole ? 1 : rq.nt);
+    }
+    int64_t before = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        const int64_t v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
     }
-    if (lane == 31) warp_sum[warp] = incl;
+    if (lane == 31) warp_sum[warp] = before;
+    if (tid < C::WARPS) starts[tid].q.nt = 0;
+    if (tid == 0) cta_tiles = 0;
     __syncthreads();
-    for (int w = 0; w < warp; w++) incl += warp_sum[w];
-    chunk_end[tid] = incl;
+    before -= mine;
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < NTHR / 32; w++) {
+        if (w < warp) before += warp_sum[w];
+        total += warp_sum[w];
+    }
+    const int64_t share = a.whole ? 1 : ad_div(total + gridDim.x - 1, gridDim.x);
+    int64_t cta0 = min(total, (int64_t)blockIdx.x * share), cta1 = min(total, cta0 + share);
+    int64_t per_warp = ad_div(cta1 - cta0 + C::WARPS - 1, C::WARPS);
+    for (int r = r0; r < r1; r++) {
+        if (per > 1) rq = ad_request(a, r);
+        const int64_t units = ad_units(a, rq, RG), n = units * (a.whole ? 1 : rq.nt);
+        if (before < cta1 && before + n > cta0) {
+            if (a.whole) {   // the CTA's unit: its tiles over the warps
+                const int share_w = (rq.nt + C::WARPS - 1) / C::WARPS;
+                for (int w = 0; w < C::WARPS; w++)
+                    if (w * share_w < rq.nt) starts[w] = AdCursor{r, (int)(cta0 - before), w * share_w, rq};
+                cta_tiles = rq.nt;
+            } else {
+                for (int w = 0; w < C::WARPS; w++) {
+                    const int64_t t = cta0 + w * per_warp;
+                    if (t >= before && t < before + n && t < cta1) {
+                        const int u = (int)ad_div(t - before, rq.nt);
+                        starts[w] = AdCursor{r, u, (int)(t - before - (int64_t)u * rq.nt), rq};
+                    }
+                }
+            }
+        }
+        before += n;
+    }
     __syncthreads();
-    const int64_t total = chunk_end[NTHR - 1];
-    const int64_t per_cta = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t cta0 = min(total, (int64_t)blockIdx.x * per_cta), cta1 = min(total, cta0 + per_cta);
-    const int64_t per_warp = (cta1 - cta0 + C::WARPS - 1) / C::WARPS;
-    // the request, unit and tile of tile t0 < total of the sequence
-    auto locate = [&](int64_t t0) {
-        AdCursor cur;
-        int lo = -1, hi = NTHR - 1;   // first chunk that ends past t0
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (chunk_end[mid] > t0) hi = mid;
-            else lo = mid;
-        }
-        int64_t before = hi > 0 ? chunk_end[hi - 1] : 0;
-        for (cur.r = hi * per;; cur.r++) {   // it is there
-            cur.q = ad_request(a, cur.r);
-            const int64_t n = ad_tiles(a, cur.q, RG);
-            if (before + n > t0) break;
-            before += n;
-        }
-        const int64_t off = t0 - before;
-        cur.u = (int)(off / cur.q.nt);
-        cur.tile = (int)(off - (int64_t)cur.u * cur.q.nt);
-        return cur;
-    };
+    if (a.whole) {
+        cta0 = 0;
+        cta1 = cta_tiles;
+        per_warp = (cta1 + C::WARPS - 1) / C::WARPS;
+    }
+    const int64_t per_cta = share;
 
     if (warp >= C::WARPS) {
         // ================= copies: 8 lanes ask for those of one computing warp, a step of TP tiles of a unit at a
@@ -308,7 +340,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
         const uint32_t tpp = (uint32_t)(p.page / KV_TILE);
         const int shift = (tpp & (tpp - 1)) == 0 ? __ffs(tpp) - 1 : -1;
         AdCursor feed{};
-        if (tiles > 0) feed = locate(t0);
+        if (tiles > 0) feed = starts[who];
         const uint8_t *head = nullptr;   // the unit's head in page 0
         uint64_t idle_since = 0;
         // the lanes stay together: a step is taken by all groups whose stage is free
@@ -381,7 +413,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     int flags = 0, open_r = 0, open_u = 0;
     int64_t open_end = 0;
     if (t0 < t1) {
-        AdCursor cur = locate(t0);
+        AdCursor cur = starts[warp];
         const int G = (int)(p.h / p.hk);
         const float log2_scale = p.scale * 1.44269504088896341f;
         bool dead = false;
@@ -392,7 +424,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             const int row0 = cur.u / (int)p.hk * RG, head0 = cur.u % (int)p.hk * G, rows = cur.q.q * G;
             const int pos_lo = cur.q.pos0 + row0 / G, pos_hi = cur.q.pos0 + (min(rows, row0 + RG) - 1) / G;
             uint32_t qb[QP][NB][2][NT][2];   // B fragments of the queries: row g, values 8 q4 .. of each block
-            float corr[NB][NT][2];           // what the code offsets add to rows 2 q4, + 1, negated
+            float corr[NB][NT][4];           // what the code offsets add to rows 2 q4, + 1 (twice: an accumulator), negated
             float sl[NT][2];                 // scores to log2 units
             float o[NB][2][NT][4];
             float m[NT][2], lsum[NT][2];
@@ -436,7 +468,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                         s += __shfl_xor_sync(0xffffffffu, s, 1);
                         s += __shfl_xor_sync(0xffffffffu, s, 2);
 #pragma unroll
-                        for (int j = 0; j < 2; j++) corr[b][n][j] = __shfl_sync(0xffffffffu, s, 8 * q4 + 4 * j);
+                        for (int j = 0; j < 4; j++) corr[b][n][j] = __shfl_sync(0xffffffffu, s, 8 * q4 + 4 * (j & 1) + (j >> 1));
                     }
                 } else {
 #pragma unroll
@@ -444,7 +476,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
 #pragma unroll
                     for (int b = 0; b < NB; b++) {
                         const float *from = reinterpret_cast<const float *>(p.q) + at + 32 * b + 8 * q4;
-                        corr[b][n][0] = corr[b][n][1] = 0.0f;
+                        corr[b][n][0] = corr[b][n][1] = corr[b][n][2] = corr[b][n][3] = 0.0f;
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
                             float x = there ? from[2 * i] : 0.0f, y = there ? from[2 * i + 1] : 0.0f;
@@ -531,7 +563,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                             for (int n = 0; n < NT; n++) {
                                 float acc[4];
                                 mma_16816<QT == GGUF_F32>(acc, k0, qb[0][b][0][n][0], qb[0][b][0][n][1], corr[b][n][0],
-                                                          corr[b][n][1], corr[b][n][0], corr[b][n][1]);
+                                                          corr[b][n][1], corr[b][n][2], corr[b][n][3]);
                                 mma_16816<QT == GGUF_F32>(acc, k1, qb[0][b][1][n][0], qb[0][b][1][n][1], acc[0], acc[1], acc[2], acc[3]);
 #pragma unroll
                                 for (int part = 1; part < QP; part++) {
@@ -779,7 +811,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             }
         }
     };
-    int follow = 0, meta_r = 0, meta_u = 0;
+    int follow = 0, opener = 0;
     for (int w = 0; w < C::WARPS; w++) {
         const int f = left[w];
         if (f & 1) {
@@ -794,16 +826,19 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             join(w, true);
             if (!orphan) {
                 follow = (int)((left_end[chain] - cta1 + per_cta - 1) / per_cta);
-                meta_r = left_r[chain];
-                meta_u = left_u[chain];
+                opener = chain;
             }
             break;
         }
     }
-    if (tid == 0) {
-        a.meta[4 * blockIdx.x] = follow;
-        a.meta[4 * blockIdx.x + 1] = meta_r;
-        a.meta[4 * blockIdx.x + 2] = meta_u;
+    if (tid == 0 && !a.whole) {
+        AdMeta m{};
+        if (follow > 0) {
+            const AdReq q = ad_request(a, left_r[opener]);
+            const int u = left_u[opener], row0 = u / (int)p.hk * RG;
+            m = AdMeta{follow, q.rows0, u % (int)p.hk * G, row0, min(q.q * G - row0, RG), {}};
+        }
+        a.meta[blockIdx.x] = m;
     }
     // ---- queries that see no token
     for (int r = blockIdx.x * C::WARPS + warp; r < R; r += gridDim.x * C::WARPS) {
@@ -816,67 +851,70 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
 }
 
 // Units that run over several CTAs of attn_decode_kernel: CTA c (blockIdx.x)
-// joins the unit that CTA c opened and did not finish (meta[c] = {CTAs after c
-// that hold pieces, request, unit}) for one query row (blockIdx.y), pieces in
-// the order of the CTAs.
+// joins the unit that CTA c opened and did not finish for one query row
+// (blockIdx.y).  A thread takes four columns of every LANES-th piece, with a
+// maximum and sum of its own, so that all loads are under way at once; the
+// threads' results are joined in a fixed order.
 constexpr int AC_THREADS = 256;
-constexpr int AC_MAX = 1024;   // CTAs of attn_decode_kernel at most
 template <int D, int QT, int NT>
 __global__ void __launch_bounds__(AC_THREADS) attn_combine_kernel(const AdShape a) {
     using C = AdCfg<D, QT, NT>;
     constexpr int COLS = D / 4, LANES = AC_THREADS / COLS;
-    __shared__ float wt[AC_MAX], red[AC_THREADS / 32], red_l[AC_THREADS / 32];
-    __shared__ float4 sum[AC_THREADS];
+    __shared__ float4 sum[LANES][COLS];
+    __shared__ float2 stat[LANES];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Attn &p = a.p;
-    const int c = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
-    const int n = a.meta[4 * c] + 1;
-    if (n == 1) return;
-    const AdReq q = ad_request(a, a.meta[4 * c + 1]);
-    const int u = a.meta[4 * c + 2], G = (int)(p.h / p.hk), at_row = u / (int)p.hk * C::RG + row;
-    if (at_row >= q.q * G) return;
-    auto slot = [&](int k) { return a.part + (int64_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * (C::SLOT / 4); };
-    float mx = -INFINITY;
-    for (int k = tid; k < n; k += AC_THREADS) mx = fmaxf(mx, slot(k)[C::RG * D + 2 * row]);
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (tid % 32 == 0) red[tid / 32] = mx;
-    __syncthreads();
-    for (int i = 0; i < AC_THREADS / 32; i++) mx = fmaxf(mx, red[i]);
-    const float base = mx == -INFINITY ? 0.0f : mx;
-    float l = 0.0f;
-    for (int k = tid; k < n; k += AC_THREADS) {
-        const float f = ex2(slot(k)[C::RG * D + 2 * row] - base);
-        wt[k] = f;
-        l = fmaf(f, slot(k)[C::RG * D + 2 * row + 1], l);
-    }
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (tid % 32 == 0) red_l[tid / 32] = l;
-    __syncthreads();
-    const int col = tid % COLS;
+    const int c = blockIdx.x, row = blockIdx.y, col = threadIdx.x % COLS, k0 = threadIdx.x / COLS;
+    const AdMeta m = a.meta[c];
+    if (m.follow == 0 || row >= m.rows) return;
+    const int n = m.follow + 1;
+    float mx = -INFINITY, l = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int k = tid / COLS; k < n; k += LANES) {
-        const float f = wt[k];
-        const float4 x = *reinterpret_cast<const float4 *>(slot(k) + row * D + 4 * col);
-        v.x = fmaf(f, x.x, v.x); v.y = fmaf(f, x.y, v.y); v.z = fmaf(f, x.z, v.z); v.w = fmaf(f, x.w, v.w);
+#pragma unroll 4
+    for (int k = k0; k < n; k += LANES) {
+        const float *src = a.part + (int64_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * (C::SLOT / 4);
+        const float4 x = *reinterpret_cast<const float4 *>(src + row * D + 4 * col);
+        const float2 ml = *reinterpret_cast<const float2 *>(src + C::RG * D + 2 * row);
+        const float mn = fmaxf(mx, ml.x), base = mn == -INFINITY ? 0.0f : mn;
+        const float f = ex2(mx - base), h = ex2(ml.x - base);
+        mx = mn;
+        l = fmaf(l, f, ml.y * h);
+        v.x = fmaf(v.x, f, x.x * h); v.y = fmaf(v.y, f, x.y * h);
+        v.z = fmaf(v.z, f, x.z * h); v.w = fmaf(v.w, f, x.w * h);
     }
-    sum[tid] = v;
+    sum[k0][col] = v;
+    if (col == 0) stat[k0] = make_float2(mx, l);
     __syncthreads();
-    if (tid >= COLS) return;
+    if (threadIdx.x >= COLS) return;
+    for (int i = 0; i < LANES; i++) mx = fmaxf(mx, stat[i].x);
+    const float base = mx == -INFINITY ? 0.0f : mx;
     l = 0.0f;
-    for (int i = 0; i < AC_THREADS / 32; i++) l += red_l[i];
-    for (int i = 1; i < LANES; i++) {
-        const float4 x = sum[i * COLS + tid];
-        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = 0; i < LANES; i++) {
+        const float h = ex2(stat[i].x - base);
+        const float4 x = sum[i][col];
+        l = fmaf(stat[i].y, h, l);
+        v.x = fmaf(x.x, h, v.x); v.y = fmaf(x.y, h, v.y); v.z = fmaf(x.z, h, v.z); v.w = fmaf(x.w, h, v.w);
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    store4<QT>(p.out, (q.rows0 + at_row / G) * p.ldo + (int64_t)(u % (int)p.hk * G + at_row % G) * D + 4 * col, a.vec,
-               v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    const int G = (int)(p.h / p.hk), at = m.row0 + row;
+    store4<QT>(p.out, (m.rows0 + at / G) * p.ldo + (int64_t)(m.head0 + at % G) * D + 4 * col, a.vec, v.x * inv, v.y * inv,
+               v.z * inv, v.w * inv);
 }
 
 template <int D, int QT, int NT>
-static cudaError_t attn_decode_run(const AdShape &a, int ctas, cudaStream_t s) {
+static cudaError_t attn_decode_run(const AdShape &shape, int ctas, cudaStream_t s) {
     using C = AdCfg<D, QT, NT>;
+    AdShape a = shape;
+    // Few units of few tiles: a CTA each, and the second launch is saved (about 4 us).  The table's width bounds the
+    // tiles: 2048 tokens are 128 tiles, 11 to 16 per warp, about 4 us.
+    const int64_t most_rows = std::min<int64_t>(a.max_rows, a.p.h / a.p.hk * a.p.max_q);
+    const int64_t units = a.p.R * a.p.hk * ((most_rows + C::RG - 1) / C::RG);
+    const int64_t span = a.p.window > 0 ? std::min(a.p.width * a.p.page, a.p.window + a.p.sinks + a.p.max_q + 3 * KV_TILE)
+                                        : a.p.width * a.p.page;
+    a.whole = units <= ctas && span <= 2048;
+    if (a.whole) ctas = (int)units;
     cudaError_t err = cudaSuccess;
     const void *kern = (const void *)attn_decode_kernel<D, QT, NT>;
     if (kernel_occupancy(kern, C::THREADS, C::SMEM, &err) == 0) return err;
@@ -891,7 +929,7 @@ static cudaError_t attn_decode_run(const AdShape &a, int ctas, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, QT, NT>, a);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.whole) return e;
     cfg.gridDim = dim3((unsigned)ctas, C::RG);
     cfg.blockDim = dim3(AC_THREADS);
     cfg.dynamicSmemBytes = 0;
