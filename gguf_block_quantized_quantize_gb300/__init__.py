@@ -2,7 +2,8 @@
 
 Each function has the name of the C-ABI entry point it calls and only
 marshals arguments (torch CUDA tensors -> device pointers, the current CUDA
-stream, workspace allocation through torch's caching allocator).  Every step
+stream, workspace allocation through torch's caching allocator), the paged-cache
+calls through the native module ``_bind``, the others through ctypes.  Every step
 of the computation runs in the library's CUDA kernels; there is no fallback:
 if the library is missing or the device is not a CUDA GPU, the calls raise.
 
@@ -134,11 +135,12 @@ SIGNATURES = {
 }
 
 _lib = None
+_native = None   # the module _bind: marshalling of the paged-cache calls
 
 
 def load_library(path: str = LIB_PATH):
     """Load libgguf_gb300.so (built by ``build.build()``); raise if it is missing."""
-    global _lib
+    global _lib, _native
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -148,6 +150,12 @@ def load_library(path: str = LIB_PATH):
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+    from . import _bind as native
+
+    native.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        "gguf_kv_plan", "gguf_qk_norm_rope", "gguf_kv_get_rows", "gguf_paged_attention_ws_size", "gguf_paged_attention",
+        "gguf_kv_page_bytes")))
+    _native = native
     _lib = lib
     return lib
 
@@ -160,11 +168,12 @@ def _check(st: int):
 # the current stream's raw handle without building a Stream object (the
 # public call is the fallback)
 _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_DEVICE = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream():
     if _RAW_STREAM is not None:
-        return _RAW_STREAM(torch.cuda.current_device())
+        return _RAW_STREAM(_DEVICE())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -489,38 +498,10 @@ def gguf_kv_page_bytes(head_dim: int, n_kv_heads: int, page_size: int) -> int:
     return int(_lib_fast().gguf_kv_page_bytes(head_dim, n_kv_heads, page_size))
 
 
-def _int(what: str, name: str, t: torch.Tensor, numel: int):
-    if t.dtype is not torch.int32 or t.numel() < numel or not t.is_contiguous():
-        raise ValueError(f"{what}: {name} must be a contiguous int32 tensor of at least {numel}")
-    return _ptr(t)
-
-
-def _long(what: str, name: str, t: torch.Tensor, numel: int):
-    if t.dtype is not torch.int64 or t.numel() < numel or not t.is_contiguous():
-        raise ValueError(f"{what}: {name} must be a contiguous int64 tensor of at least {numel}")
-    return _ptr(t)
-
-
-def _table(what: str, t: torch.Tensor, rows: int):
-    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] < rows or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: block_table must be int32 [requests, width] with contiguous rows")
-    return _ptr(t)
-
-
-def _heads(what: str, name: str, t: torch.Tensor, shape, dtype):
-    """[tokens, heads, head_dim] with the heads of a token side by side; the tokens may be strided."""
-    if t.dtype is not dtype or t.shape != shape or (shape[2] > 1 and t.stride(2) != 1) or \
-            (shape[1] > 1 and t.stride(1) != shape[2]):
-        raise ValueError(f"{what}: {name} must be {tuple(shape)} of {dtype} with the heads of a token side by side")
-    return _ptr(t), (t.stride(0) if shape[0] > 1 else shape[1] * shape[2])
-
-
-def _cache(what: str, cache: torch.Tensor, head_dim: int, n_kv_heads: int, page_size: int):
-    nbytes = gguf_kv_page_bytes(head_dim, n_kv_heads, page_size)
-    if nbytes > 0 and (cache.dtype is not torch.uint8 or cache.dim() != 2 or cache.shape[1] != nbytes or
-                       not cache.is_contiguous()):
-        raise ValueError(f"{what}: cache must be a contiguous uint8 tensor [pages, {nbytes}]")
-    return _ptr(cache)
+def _bound():
+    if _native is None:
+        load_library()
+    return _native
 
 
 def gguf_kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
@@ -529,20 +510,16 @@ def gguf_kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch
 
     Returns (q_start [r + 1], kv_len [r], positions [n_tokens] int32, slots [n_tokens] int64, pages_used [1]);
     ``out`` may give these five tensors.  ``block_table`` is extended in place."""
-    what = "gguf_kv_plan"
-    r, dev = new_len.numel(), new_len.device
     if out is None:
+        r, dev = new_len.numel(), new_len.device
         out = (torch.empty(r + 1, dtype=torch.int32, device=dev), torch.empty(r, dtype=torch.int32, device=dev),
                torch.empty(n_tokens, dtype=torch.int32, device=dev), torch.empty(n_tokens, dtype=torch.int64, device=dev),
                torch.empty(1, dtype=torch.int32, device=dev))
     q_start, kv_len, positions, slots, used = out
-    _check(_lib_fast().gguf_kv_plan(
-        _int(what, "ctx_len", ctx_len, r), _int(what, "new_len", new_len, r), r,
-        _int(what, "free_pages", free_pages, 0), free_pages.numel(), _table(what, block_table, r),
-        block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1], block_table.shape[1], page_size,
-        n_tokens, _int(what, "q_start", q_start, r + 1), _int(what, "kv_len", kv_len, r),
-        _int(what, "positions", positions, n_tokens), _long(what, "slots", slots, n_tokens), _int(what, "pages_used", used, 1),
-        None if dev_status is None else _int(what, "dev_status", dev_status, 1), _stream()))
+    st = _bound().kv_plan(ctx_len, new_len, free_pages, block_table, page_size, n_tokens, q_start, kv_len, positions, slots,
+                          used, dev_status, _stream())
+    if st:
+        _check(st)
     return out
 
 
@@ -555,55 +532,23 @@ def gguf_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor |
     values into the cache slots (where ``cache`` is given).  q [t, heads, d], k and v [t, kv_heads, d] may be
     strided over the tokens (views of a fused product); ``cos_sin`` [positions, rot] fp32 holds rot / 2 cosines,
     then sines.  Returns ``q_out`` (which may be ``q``); ``k_out`` takes the keys in floats where given."""
-    what = "gguf_qk_norm_rope"
-    t, h, d = q.shape
-    dtype = q.dtype
     if q_out is None:
-        q_out = torch.empty((t, h, d), dtype=dtype, device=q.device)
-    pq, ldq = _heads(what, "q", q, q.shape, dtype)
-    pqo, ldqo = _heads(what, "q_out", q_out, q.shape, dtype)
-    hk = 0 if k is None else k.shape[1]
-    pk = pv = pko = pc = ps = None
-    ldk = ldv = ldko = pages = 0
-    if k is not None:
-        pk, ldk = _heads(what, "k", k, (t, hk, d), dtype)
-    if k_out is not None:
-        pko, ldko = _heads(what, "k_out", k_out, (t, hk, d), dtype)
-    if cache is not None:
-        if k is None or v is None or slots is None:
-            raise ValueError(f"{what}: storing needs k, v and slots")
-        pv, ldv = _heads(what, "v", v, (t, hk, d), dtype)
-        pc, ps, pages = _cache(what, cache, d, hk, page_size), _long(what, "slots", slots, t), cache.shape[0]
-    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-        if w is not None and (w.dtype is not torch.float32 or w.shape != (d,) or w.stride(0) != 1):
-            raise ValueError(f"{what}: {name} must be {d} contiguous fp32 values")
-    rot = npos = 0
-    if cos_sin is not None:
-        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-            raise ValueError(f"{what}: cos_sin must be a contiguous fp32 tensor [positions, rot]")
-        npos, rot = cos_sin.shape
-    args = QkRopeArgs(pq, pk, pv, _TYPE_OF[dtype], t, ldq, ldk, ldv, h, hk, d, _ptr(q_norm), _ptr(k_norm), eps,
-                      _int(what, "positions", positions, t), _ptr(cos_sin), npos, rot, rope_type, pqo, ldqo, pko, ldko,
-                      pc, pages, page_size, ps,
-                      None if dev_status is None else _int(what, "dev_status", dev_status, 1))
-    _check(_lib_fast().gguf_qk_norm_rope(ctypes.byref(args), _stream()))
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    st = _bound().qk_norm_rope(q, k, v, q_norm, k_norm, eps, positions, cos_sin, rope_type, cache, slots, page_size, q_out,
+                               k_out, dev_status, _stream())
+    if st:
+        _check(st)
     return q_out
 
 
 def gguf_kv_get_rows(cache: torch.Tensor, slots: torch.Tensor, n_kv_heads: int, head_dim: int, page_size: int,
                      out_dtype=torch.float32, out=None):
     """Keys and values of cache slots as floats: two tensors [n, kv_heads, d] (``out`` may give them)."""
-    what = "gguf_kv_get_rows"
-    n = slots.numel()
     if out is None:
-        out = [torch.empty((n, n_kv_heads, head_dim), dtype=out_dtype, device=slots.device) for _ in range(2)]
-    k, v = out
-    if k.dtype is not v.dtype or not k.is_contiguous() or not v.is_contiguous() or \
-            k.numel() < n * n_kv_heads * head_dim or v.numel() < n * n_kv_heads * head_dim:
-        raise ValueError(f"{what}: out must be two contiguous tensors [n, kv_heads, d] of one dtype")
-    _check(_lib_fast().gguf_kv_get_rows(_cache(what, cache, head_dim, n_kv_heads, page_size), cache.shape[0], page_size,
-                                        n_kv_heads, head_dim, _long(what, "slots", slots, n), n, _ptr(k), _ptr(v),
-                                        _TYPE_OF[k.dtype], _stream()))
+        out = [torch.empty((slots.numel(), n_kv_heads, head_dim), dtype=out_dtype, device=slots.device) for _ in range(2)]
+    st = _bound().kv_get_rows(cache, slots, n_kv_heads, head_dim, page_size, out[0], out[1], _stream())
+    if st:
+        _check(st)
     return out
 
 
@@ -614,24 +559,17 @@ def gguf_paged_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torc
     """Causal attention of q [t, heads, d] over the paged Q4_0 cache (see include/gguf_gb300.h): request r's queries
     are rows q_start[r] .. q_start[r + 1] - 1 and its newest tokens.  ``window`` > 0 hides what lies further back,
     except the first ``sinks`` tokens."""
-    what = "gguf_paged_attention"
-    t, h, d = q.shape
-    dtype = q.dtype
-    r = kv_len.numel()
     if out is None:
-        out = torch.empty((t, h, d), dtype=dtype, device=q.device)
-    pq, ldq = _heads(what, "q", q, q.shape, dtype)
-    po, ldo = _heads(what, "out", out, q.shape, dtype)
-    width = block_table.shape[1]
-    args = AttnArgs(pq, _TYPE_OF[dtype], t, ldq, _cache(what, cache, d, n_kv_heads, page_size), cache.shape[0], page_size,
-                    _table(what, block_table, r), block_table.stride(0) if block_table.shape[0] > 1 else width, width,
-                    _int(what, "q_start", q_start, r + 1), _int(what, "kv_len", kv_len, r), r, max_q_len, h, n_kv_heads,
-                    d, scale, window, sinks, po, ldo,
-                    None if dev_status is None else _int(what, "dev_status", dev_status, 1))
-    lib, ref = _lib_fast(), ctypes.byref(args)
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    call = _bound().paged_attention
     if ws is None:   # a caller's workspace is checked against the need by the library
-        ws = _workspace(int(lib.gguf_paged_attention_ws_size(ref)), q.device)
-    _check(lib.gguf_paged_attention(ref, _ptr(ws), 0 if ws is None else ws.numel(), _stream()))
+        need = call(q, cache, block_table, q_start, kv_len, n_kv_heads, page_size, max_q_len, scale, window, sinks, out, 0,
+                    dev_status, 0)
+        ws = _workspace(need, q.device)
+    st = call(q, cache, block_table, q_start, kv_len, n_kv_heads, page_size, max_q_len, scale, window, sinks, out, ws,
+              dev_status, _stream())
+    if st:
+        _check(st)
     return out
 
 

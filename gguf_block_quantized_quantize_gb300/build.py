@@ -3,7 +3,8 @@
 Compiles every ``csrc/*.cu`` to an object in ``csrc/_build/`` (in parallel,
 only when a source or header is newer than its object) and links
 ``libgguf_gb300.so`` next to this file.  cudart is linked statically, so the
-library needs only the CUDA driver at run time.
+library needs only the CUDA driver at run time.  ``csrc/bind.cpp`` becomes the
+package's ``_bind.so`` (g++, against torch and Python headers).
 """
 from __future__ import annotations
 
@@ -12,11 +13,13 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(CSRC, "_build")
 LIB = os.path.join(HERE, "libgguf_gb300.so")
+BIND = os.path.join(HERE, "_bind.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -50,12 +53,35 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _bind() -> str:
+    """The native marshalling module, when its source or the header is newer."""
+    import torch
+
+    src = os.path.join(CSRC, "bind.cpp")
+    if os.path.exists(BIND) and os.path.getmtime(BIND) >= max(os.path.getmtime(src), _headers_mtime()):
+        return BIND
+    troot = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-isystem", os.path.join(troot, "include"), "-isystem", os.path.join(troot, "include/torch/csrc/api/include"),
+           "-isystem", cuda, "-isystem", sysconfig.get_paths()["include"], "-I", INCLUDE, src, "-o", tmp,
+           "-L", os.path.join(troot, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + os.path.join(troot, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for bind.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     extra = list(extra or [])
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(12, len(srcs) + 1)) as ex:
+        bound = ex.submit(_bind)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
+        bound.result()
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
