@@ -18,8 +18,9 @@
 // 2^(s - reference + 10), at most 2^15.  Statistics are fp32.
 //
 // Warps: 0-3 and 4-7 the softmax of a row tile each (TMEM lanes 32 * (warp %
-// 4) on), 8-11 unpack, 12 issues the MMAs (and owns the TMEM allocation), 13
-// loads.  Every wait is bounded (1 s); a timeout sets the error word and the
+// 4) on; a thread holds its row's scores of a block, so these warps take
+// registers from the others), 8-11 unpack, 12 issues the MMAs (and owns the
+// TMEM allocation), 13 loads.  Every wait is bounded (1 s); a timeout sets the error word and the
 // CTA drains and exits.
 #pragma once
 
@@ -27,7 +28,10 @@
 
 namespace gg {
 
-constexpr int AP_THREADS = 14 * 32;
+constexpr int AP_UW = 4;                         // warps that unpack
+constexpr int AP_THREADS = (12 + AP_UW) * 32;
+constexpr int AP_MMA = 8 + AP_UW, AP_LOAD = 9 + AP_UW;
+constexpr int AP_REGS = 176, AP_REGS_FEW = 80;   // of the softmax warps and of the others: 128 at launch on average
 
 template <int D>
 struct ApCfg {
@@ -43,7 +47,7 @@ struct ApCfg {
     static constexpr int OFF_K = Q_BYTES, OFF_V = OFF_K + KST * K_BYTES, OFF_RAW = OFF_V + VST * V_BYTES;
     static constexpr int SMEM = OFF_RAW + RAWST * RAW_BYTES + 1024;   // 1024 for the base's alignment
     static constexpr int COL_S = BT, COL_O = 256;      // TMEM columns: S buffer x at x * BT, O of row tile t at 256 + t * D
-    static_assert(SMEM <= 232448 - 5120, "static shared memory fits beside");
+    static_assert(SMEM <= 232448 - 6144, "static shared memory fits beside");
 };
 
 // a CTA's piece of work
@@ -61,15 +65,40 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// pairs of fp32 values in 64-bit registers, and two operations at once on them
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ float2 unpair(uint64_t p) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint64_t fma_2(uint64_t x, uint64_t m, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(m), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+
+// true in one lane of the warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
 }
 
 // row blocks (of ROWS query rows) x KV heads of one request
@@ -87,27 +116,29 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t raw_full[C::RAWST], raw_empty[C::RAWST], k_full[C::KST], k_empty[C::KST], v_full[C::VST],
-        v_empty[C::VST], s_full[2], p_full[2], pv_done[2], drain;
+        v_empty[C::VST], s_full[2], p_full[2], pv_done[2], q_full, drain;
     __shared__ int32_t raw_mask[C::RAWST], blk_mask[8];
     __shared__ float q_inv[ROWS];
     __shared__ uint32_t tmem_slot;
     __shared__ int32_t abort_word;
     __shared__ ApItem item;
-    __shared__ int64_t part[AP_THREADS / 32], chunk_end[AP_THREADS];
+    __shared__ int64_t part[AP_THREADS / 32];
+    __shared__ int32_t chunk_end[AP_THREADS];   // at most (tokens x heads / 128) items: 31 bits
     volatile int32_t *abort_flag = &abort_word;
     const Attn &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = (int)(p.h / p.hk);
     if (tid == 0) {
-        for (int i = 0; i < C::RAWST; i++) { tc::mbar_init(&raw_full[i], 1); tc::mbar_init(&raw_empty[i], 128); }
-        for (int i = 0; i < C::KST; i++) { tc::mbar_init(&k_full[i], 128); tc::mbar_init(&k_empty[i], 1); }
-        for (int i = 0; i < C::VST; i++) { tc::mbar_init(&v_full[i], 128); tc::mbar_init(&v_empty[i], 1); }
-        for (int i = 0; i < 2; i++) { tc::mbar_init(&s_full[i], 1); tc::mbar_init(&p_full[i], 128); tc::mbar_init(&pv_done[i], 1); }
+        for (int i = 0; i < C::RAWST; i++) { tc::mbar_init(&raw_full[i], 1); tc::mbar_init(&raw_empty[i], AP_UW); }
+        for (int i = 0; i < C::KST; i++) { tc::mbar_init(&k_full[i], AP_UW); tc::mbar_init(&k_empty[i], 1); }
+        for (int i = 0; i < C::VST; i++) { tc::mbar_init(&v_full[i], AP_UW); tc::mbar_init(&v_empty[i], 1); }
+        for (int i = 0; i < 2; i++) { tc::mbar_init(&s_full[i], 1); tc::mbar_init(&p_full[i], 4); tc::mbar_init(&pv_done[i], 1); }
+        tc::mbar_init(&q_full, 8);
         tc::mbar_init(&drain, 1);
         tc::fence_barrier_init();
         abort_word = 0;
     }
-    if (warp == 12) {
+    if (warp == AP_MMA) {
         tc::tmem_alloc(&tmem_slot, 512);
         tc::tmem_relinquish();
     }
@@ -129,7 +160,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         __syncthreads();
         tc::tc_fence_after();
         for (int w = 0; w < warp; w++) incl += part[w];
-        chunk_end[tid] = incl;
+        chunk_end[tid] = (int32_t)min(incl, (int64_t)0x7fffffff);
         __syncthreads();
     }
     const int64_t total = chunk_end[AP_THREADS - 1];
@@ -138,14 +169,33 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         *abort_flag = 1;
         if (a.err != nullptr) atomicOr(a.err, code);
     };
+    // one arrival for the warp, once all its lanes have come here (256 single ones take as many turns at the barrier)
+    auto arrive = [&](uint64_t *bar) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar);
+    };
     auto token_of = [&](int i) { return (i < item.n_sink ? i : item.w_tile + i - item.n_sink) * KV_TILE; };
 
-    // running uses of the stages and of the S buffers before the current item
-    int blocks_before = 0, groups_before = 0, uses[2] = {0, 0};
+    constexpr int GPB = BT / 64;   // loads per block
     // items in stripes of one per CTA, every other stripe backwards: a request's row blocks come longest first
-    for (int64_t stripe = 0; stripe * gridDim.x < total; stripe++) {
-        const int64_t it = stripe * gridDim.x + ((stripe & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        if (it >= total) continue;
+    const int64_t stripes = (total + gridDim.x - 1) / gridDim.x;
+    auto item_of = [&](int64_t stripe) { return stripe * gridDim.x + ((stripe & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x); };
+    auto everyone = [] { asm volatile("bar.sync 0, %0;" ::"n"(AP_THREADS) : "memory"); };
+    // what a role knows of the current item, and the running uses of the stages and of the S buffers before it
+    struct Walk {
+        int blocks_before = 0, groups_before = 0, uses[2] = {0, 0}, nrt = 0, nblk = 0, nitems = 0, items = -1;
+    };
+    // the item before is done with (its shared and tensor memory are free), and the next one is known
+    auto begin = [&](Walk &wk, int64_t it) {
+        wk.blocks_before += wk.nblk;
+        wk.groups_before += wk.nblk * GPB;
+        wk.uses[0] += (wk.nitems + 1) / 2;
+        wk.uses[1] += wk.nitems / 2;
+        wk.items++;
+        tc::tc_fence_before();
+        everyone();
+        tc::tc_fence_after();
+        if (*abort_flag) return false;
         if (tid == 0) {
             int lo = -1, hi = AP_THREADS - 1;
             while (hi - lo > 1) {
@@ -183,55 +233,61 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             }
             item = w;
         }
-        __syncthreads();
-        // ---- queries: D / 8 lanes per row, 8 values each
-        {
-            constexpr int LPR = D / 8;
-            for (int row = tid / LPR; row < ROWS; row += AP_THREADS / LPR) {
-                const int l = tid % LPR, rr = item.row0 + row;
-                uint32_t w[4] = {0, 0, 0, 0};
-                if (row < item.rows) {
-                    const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + (item.q0 + rr / G) * p.ldq +
-                                          (int64_t)(item.head * G + rr % G) * D + 8 * l;
-                    if (a.vec) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(src);
-                        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-                    } else {
+        everyone();
+        wk.nrt = item.rows > 128 ? 2 : 1;
+        wk.nblk = (item.nt + BT / KV_TILE - 1) / (BT / KV_TILE);
+        wk.nitems = wk.nblk * wk.nrt;
+        return true;
+    };
+    Walk wk;
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(AP_REGS));
+        for (int64_t st = 0; st < stripes; st++) {
+            const int64_t it = item_of(st);
+            if (it >= total) continue;
+            if (!begin(wk, it)) break;
+            // ---- queries: D / 8 lanes per row, 8 values each
+            {
+                constexpr int LPR = D / 8;
+                for (int row = tid / LPR; row < ROWS; row += 256 / LPR) {
+                    const int l = tid % LPR, rr = item.row0 + row;
+                    uint32_t w[4] = {0, 0, 0, 0};
+                    if (row < item.rows) {
+                        const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + (item.q0 + rr / G) * p.ldq +
+                                              (int64_t)(item.head * G + rr % G) * D + 8 * l;
+                        if (a.vec) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(src);
+                            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < 4; i++) w[i] = src[2 * i] | (uint32_t)src[2 * i + 1] << 16;
+                            for (int i = 0; i < 4; i++) w[i] = src[2 * i] | (uint32_t)src[2 * i + 1] << 16;
+                        }
                     }
+                    if constexpr (QT == GGUF_BF16) {
+                        float v[8], mx = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 8; i++) {
+                            v[i] = bf2f((uint16_t)(w[i / 2] >> (16 * (i & 1))));
+                            mx = fmaxf(mx, fabsf(v[i]));
+                        }
+                        // a row's lanes lie in one warp and all of them are here (256 / LPR divides ROWS)
+#pragma unroll
+                        for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        const float up = q_scale_up(mx);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) w[i] = pack_h2(v[2 * i] * up, v[2 * i + 1] * up);
+                        if (l == 0) q_inv[row] = 1.0f / up;
+                    } else if (l == 0) q_inv[row] = 1.0f;
+                    const int tile = row / 128, r7 = row % 128;
+                    *reinterpret_cast<uint4 *>(smem + tile * (128 * D * 2) + (8 * l / 64) * 16384 + r7 * 128 +
+                                               (((l & 7) ^ (r7 & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                if constexpr (QT == GGUF_BF16) {
-                    float v[8], mx = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        v[i] = bf2f((uint16_t)(w[i / 2] >> (16 * (i & 1))));
-                        mx = fmaxf(mx, fabsf(v[i]));
-                    }
-                    // a row's lanes lie in one warp and all of them are here (AP_THREADS and ROWS are multiples of 32 / LPR rows)
-#pragma unroll
-                    for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    const float up = q_scale_up(mx);
-#pragma unroll
-                    for (int i = 0; i < 4; i++) w[i] = pack_h2(v[2 * i] * up, v[2 * i + 1] * up);
-                    if (l == 0) q_inv[row] = 1.0f / up;
-                } else if (l == 0) q_inv[row] = 1.0f;
-                const int tile = row / 128, r7 = row % 128;
-                *reinterpret_cast<uint4 *>(smem + tile * (128 * D * 2) + (8 * l / 64) * 16384 + r7 * 128 +
-                                           (((l & 7) ^ (r7 & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+                tc::fence_proxy_async_smem();
+                arrive(&q_full);
             }
-            tc::fence_proxy_async_smem();
-        }
-        __syncthreads();
-        const int nrt = item.rows > 128 ? 2 : 1;
-        const int nblk = (item.nt + BT / KV_TILE - 1) / (BT / KV_TILE);
-        const int nitems = nblk * nrt;
-        constexpr int GPB = BT / 64;   // loads per block
-
-        if (warp < 8) {
             // ================= softmax
             const int t = warp >> 2;
-            if (t < nrt && t < C::RT) {
+            if (t < wk.nrt && t < C::RT) {
                 const int quad = warp & 3;
                 const int row = t * 128 + quad * 32 + lane;
                 const uint32_t lanes = (uint32_t)(quad * 32) << 16;
@@ -242,49 +298,50 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                 const int first = item.pos0 + (item.row0 + t * 128 + quad * 32) / G - item.tok0;
                 const int lastr = min(item.rows - 1, t * 128 + quad * 32 + 31);
                 const int last = item.pos0 + (item.row0 + lastr) / G - item.tok0;
-                const float sl = p.scale * 1.44269504088896341f * q_inv[row];
                 float ref = -INFINITY, lsum = 0.0f;
-                bool ok = true;
-                for (int j = 0; j < nblk && ok; j++) {
-                    const int n = j * nrt + t, x = n & 1;
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&s_full[x], (uint32_t)(uses[x] + n / 2) & 1u)) && !*abort_flag;
+                bool ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_full, (uint32_t)wk.items & 1u));
+                if (!ok && lane == 0) fail(1);
+                const float sl = p.scale * 1.44269504088896341f * q_inv[row];
+                for (int j = 0; j < wk.nblk && ok; j++) {
+                    const int n = j * wk.nrt + t, x = n & 1;
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&s_full[x], (uint32_t)(wk.uses[x] + n / 2) & 1u)) && !*abort_flag;
                     if (!ok) { if (lane == 0) fail(2); break; }
                     tc::tc_fence_after();
                     const uint32_t s_col = tmem + lanes + x * C::COL_S;
                     // whether every row of the warp sees the whole block
                     const int i0 = j * (BT / KV_TILE), i1 = min(item.nt, i0 + BT / KV_TILE);
-                    const int mask = blk_mask[(blocks_before + j) & 7];
+                    const int mask = blk_mask[(wk.blocks_before + j) & 7];
                     const int t_first = i0 < item.n_sink ? 0 : token_of(i0), t_last = token_of(i1 - 1) + KV_TILE - 1;
                     const bool whole = mask == (1 << (BT / KV_TILE)) - 1 && t_last <= first &&
                                        (p.window <= 0 || t_first > last - p.window || t_last < p.sinks);
-                    auto hide = [&](float (&s)[32], int c) {   // columns 32 c .. + 31: two cache tiles
+                    uint32_t rr[BT / 32][32];   // the row's scores
 #pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            const int i = i0 + 2 * c + h;
-                            const int tok = token_of(i);
-                            const bool there2 = (mask >> (2 * c + h)) & 1;
+                    for (int c = 0; c < BT / 32; c++) tc::tmem_ld_32x32b_x32(s_col + 32 * c, rr[c]);
+                    tc::tmem_ld_wait();
+                    if (!whole) {
+#pragma unroll
+                        for (int i = 0; i < BT / KV_TILE; i++) {
+                            const int tok = token_of(i0 + i);
                             // seen: tok + e <= pos, and tok + e > pos - window or tok + e < sinks
-                            const int hi = there2 ? pos - tok : -1;
-                            const int lo = p.window > 0 ? (int)max((int64_t)pos - p.window - tok, (int64_t)-1) : -1;
+                            const int hi = (mask >> i) & 1 ? min(pos - tok, 15) : -1;
+                            const int lo = p.window > 0 ? (int)min(max((int64_t)pos - p.window - tok, (int64_t)-1), (int64_t)15) : -1;
                             const int sk = (int)min(max(p.sinks - tok, (int64_t)0), (int64_t)KV_TILE);
+                            const uint32_t back = lo < 0 ? 0u : (2u << lo) - 1;   // too far back
+                            const uint32_t seen = hi < 0 ? 0u : ((2u << hi) - 1) & (~back | ((1u << sk) - 1));
 #pragma unroll
-                            for (int e = 0; e < 16; e++)
-                                if (!(e <= hi && (e > lo || e < sk))) s[16 * h + e] = -INFINITY;
+                            for (int e = 0; e < KV_TILE; e++)
+                                if (!(seen & (1u << e))) rr[i / 2][16 * (i & 1) + e] = 0xff800000u;   // -inf
                         }
-                    };
-                    float mx = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < BT / 32; c++) {
-                        uint32_t rr[32];
-                        tc::tmem_ld_32x32b_x32(s_col + 32 * c, rr);
-                        tc::tmem_ld_wait();
-                        float s[32];
-#pragma unroll
-                        for (int i = 0; i < 32; i++) s[i] = __uint_as_float(rr[i]);
-                        if (!whole) hide(s, c);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(s[i], s[i + 1]));
                     }
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < BT / 32; c++)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+#pragma unroll
+                            for (int u = 0; u < 4; u++)
+                                m4[u] = fmaxf(m4[u], fmaxf(__uint_as_float(rr[c][i + 2 * u]), __uint_as_float(rr[c][i + 2 * u + 1])));
+                    float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     mx *= sl;
                     float alpha = 1.0f;
                     if (mx > ref + 5.0f) {
@@ -294,48 +351,47 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                     }
                     if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
                         // O of the blocks before is complete once their last product is
-                        const int np = n - nrt, xp = np & 1;
-                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[xp], (uint32_t)(uses[xp] + np / 2) & 1u));
+                        const int np = n - wk.nrt, xp = np & 1;
+                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[xp], (uint32_t)(wk.uses[xp] + np / 2) & 1u));
                         if (!ok) { if (lane == 0) fail(2); break; }
                         tc::tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; c++) {
-                            uint32_t rr[32];
-                            tc::tmem_ld_32x32b_x32(o_col + 32 * c, rr);
+                        for (int c = 0; c < D / 16; c++) {   // few at a time: the scores are in registers
+                            uint32_t v[16];
+                            tmem_ld_x16(o_col + 16 * c, v);
                             tc::tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 32; i++) rr[i] = __float_as_uint(__uint_as_float(rr[i]) * alpha);
-                            tmem_st_x32(o_col + 32 * c, rr);
+                            for (int i = 0; i < 16; i++) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+                            tmem_st_x16(o_col + 16 * c, v);
                         }
                         tc::tmem_st_wait();
                     }
                     const float base = ref == -INFINITY ? 0.0f : AD_PBITS - ref;
-#pragma unroll 1
-                    for (int c = 0; c < BT / 32; c++) {
-                        uint32_t rr[32];
-                        tc::tmem_ld_32x32b_x32(s_col + 32 * c, rr);
-                        tc::tmem_ld_wait();
-                        float s[32];
+                    const uint64_t sl2 = pair(sl, sl), base2 = pair(base, base);
+                    uint64_t l2[4] = {0, 0, 0, 0};
 #pragma unroll
-                        for (int i = 0; i < 32; i++) s[i] = __uint_as_float(rr[i]);
-                        if (!whole) hide(s, c);
+                    for (int c = 0; c < BT / 32; c++) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int i = 0; i < 16; i++) {
-                            const float p0 = ex2(fmaf(s[2 * i], sl, base)), p1 = ex2(fmaf(s[2 * i + 1], sl, base));
-                            lsum += p0 + p1;
-                            pk[i] = pack_h2(p0, p1);
+                            float2 v = unpair(fma_2(pair(__uint_as_float(rr[c][2 * i]), __uint_as_float(rr[c][2 * i + 1])), sl2, base2));
+                            v.x = ex2(v.x);
+                            v.y = ex2(v.y);
+                            l2[i & 3] = add_2(l2[i & 3], pair(v.x, v.y));
+                            pk[i] = pack_h2(v.x, v.y);
                         }
-                        tmem_st_x16(s_col + 16 * c, pk);   // columns that were read before
+                        tmem_st_x16(s_col + 16 * c, pk);   // over scores, which are in registers by now
                     }
+                    const float2 ls = unpair(add_2(add_2(l2[0], l2[1]), add_2(l2[2], l2[3])));
+                    lsum += ls.x + ls.y;
                     tc::tmem_st_wait();
                     tc::tc_fence_before();
-                    tc::mbar_arrive(&p_full[x]);
+                    arrive(&p_full[x]);
                 }
                 // ---- the output rows
-                if (ok && nblk > 0) {
-                    const int np = nitems - nrt + t, xp = np & 1;
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[xp], (uint32_t)(uses[xp] + np / 2) & 1u));
+                if (ok && wk.nblk > 0) {
+                    const int np = wk.nitems - wk.nrt + t, xp = np & 1;
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[xp], (uint32_t)(wk.uses[xp] + np / 2) & 1u));
                     if (!ok && lane == 0) fail(8);
                     tc::tc_fence_after();
                 }
@@ -346,7 +402,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
 #pragma unroll 1
                     for (int c = 0; c < D / 32; c++) {
                         uint32_t rr[32];
-                        if (nblk > 0) {
+                        if (wk.nblk > 0) {
                             tc::tmem_ld_32x32b_x32(o_col + 32 * c, rr);
                             tc::tmem_ld_wait();
                         } else {
@@ -376,225 +432,276 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                     tc::tc_fence_before();
                 }
             }
-        } else if (warp < 12) {
-            // ================= unpack: warp w8 of four
+        }
+    } else if (warp < AP_MMA) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(AP_REGS_FEW));
+        for (int64_t st = 0; st < stripes; st++) {
+            const int64_t it = item_of(st);
+            if (it >= total) continue;
+            if (!begin(wk, it)) break;
+            // ================= unpack: a load (GT tiles) at a time, keys of a block first, then values.  The packed words
+            // of the next step are read from shared memory before the current one is computed: the matrix unit's reads
+            // fill the shared memory's bandwidth for long stretches, and a read may take many hundred cycles.
+            // Keys: warp w8 takes tile w8; lane (g, q) holds values 8 q .. of the blocks of tokens g and g + 8; odd g
+            // takes the blocks in another order, so that the stores of a warp hit different banks.
+            // Values: lane (tile, p, gs) holds 8 tokens (one 16-byte chunk of a row of V^T) of 4 values of half of the
+            // blocks; the tiles' pitch and the other eighth at odd p keep loads and stores off each other's banks.
+            constexpr int XS = NB / 2;
             const int w8 = warp - 8;
+            const int kg = lane >> 2, kq = lane & 3, odd = kg & 1;
+            const int tl = lane & 3, pp = (lane >> 2) & 1, hb = w8 >> 1, vg = 2 * (lane >> 3) + (pp ^ (w8 & 1));
+            const uint32_t k_off = (w8 * 16 + kg) * 128 + (((4 * odd + kq) ^ kg) * 16);   // of even blocks; odd ones: ^ 64
+            const uint32_t v_cx = ((2 * tl + pp) ^ (4 * (vg & 1))) * 16, v_row = (32 * XS * hb + 4 * vg) * 128;
+            const uint8_t *raws = smem + C::OFF_RAW;
+            const int last = item.pos0 + (item.row0 + item.rows - 1) / G - item.tok0 - 8 * pp;
+            const int n_sink = item.n_sink, w_tile = item.w_tile;
             bool ok = true;
-            for (int j = 0; j < nblk && ok; j++) {
-                const int kb = blocks_before + j, ks = kb % C::KST, vs = kb % C::VST;
+            auto raw_wait = [&](int grp) {
+                const int gb = wk.groups_before + grp;
+                ok = tc::mbar_wait(&raw_full[gb % C::RAWST], (uint32_t)(gb / C::RAWST) & 1u);
+            };
+            struct Keys { uint32_t w[2][NB], d[2][NB]; };
+            struct Values { uint32_t w[4][XS], d[4][XS]; };
+            auto load_keys = [&](int grp, Keys &x) {
+                const int rs = (wk.groups_before + grp) % C::RAWST;
+                const uint8_t *raw = raws + rs * C::RAW_BYTES + w8 * C::PITCH;
+                const bool live = (raw_mask[rs] >> w8) & 1;
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+#pragma unroll
+                    for (int c = 0; c < NC; c++) {
+                        uint32_t w[BW];
+                        lds_words<BW>(raw + 4 * ((e * NC + c) * 32 + lane) * BW, w);
+#pragma unroll
+                        for (int i = 0; i < BW; i++) x.w[e][c * BW + i] = odd ? w[i ^ 1] : w[i];
+                        lds_words<BW>(raw + L::KS + 4 * ((4 * e + (kg >> 1)) * NB + c * BW), w);
+#pragma unroll
+                        for (int i = 0; i < BW; i++) x.d[e][c * BW + i] = live ? (odd ? w[i ^ 1] : w[i]) : 0u;
+                    }
+                }
+            };
+            auto put_keys = [&](uint8_t *sk, int gi, const Keys &x) {
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    uint8_t *to = sk + (gi * 64 + e * 8) * 128;
+#pragma unroll
+                    for (int i = 0; i < NB; i++) {   // block i ^ odd
+                        const __half2 d = u2h(__byte_perm(x.d[e][i], 0, odd ? 0x3232 : 0x1010));
+                        const uint32_t w = x.w[e][i];
+                        *reinterpret_cast<uint4 *>(to + (i >> 1) * (BT * 128) + (k_off ^ (i & 1 ? 64 : 0))) =
+                            make_uint4(h2u(__hmul2(signed_f16<0>(w), d)), h2u(__hmul2(signed_f16<1>(w), d)),
+                                       h2u(__hmul2(signed_f16<2>(w), d)), h2u(__hmul2(signed_f16<3>(w), d)));
+                    }
+                }
+            };
+            auto load_values = [&](int grp, Values &x) {
+                const int rs = (wk.groups_before + grp) % C::RAWST;
+                const uint8_t *raw = raws + rs * C::RAW_BYTES + tl * C::PITCH;
+                const bool live = (raw_mask[rs] >> tl) & 1;
+                // scales of tokens past the last query's position may be anything
+                const int i = grp * C::GT + tl, end = live ? last - (i < n_sink ? i : w_tile + i - n_sink) * KV_TILE : -1;
+                const int b0 = hb * XS;
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    const uint8_t *wp = raw + L::VC + 4 * (((pp * NC + b0 / BW) * 32 + vg * 4 + q) * BW + b0 % BW);
+                    const uint8_t *dp = raw + L::VS + 4 * ((4 * pp + q) * NB + b0);
+                    if constexpr (XS == 1) {
+                        x.w[q][0] = *reinterpret_cast<const uint32_t *>(wp);
+                        x.d[q][0] = *reinterpret_cast<const uint32_t *>(dp);
+                    } else {
+                        lds_words<XS>(wp, x.w[q]);
+                        lds_words<XS>(dp, x.d[q]);
+                    }
+                }
+                if (end < 7) {
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        const uint32_t keep = (2 * q <= end ? 0xffffu : 0u) | (2 * q + 1 <= end ? 0xffff0000u : 0u);
+#pragma unroll
+                        for (int i = 0; i < XS; i++) x.d[q][i] &= keep;
+                    }
+                }
+            };
+            auto put_values = [&](uint8_t *sv, int gi, const Values &x) {
+                uint8_t *to = sv + gi * (D * 128) + v_row;
+#pragma unroll
+                for (int i = 0; i < XS; i++) {
+                    uint32_t v[4][4];
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        const __half2 d = u2h(x.d[q][i]);
+                        v[0][q] = h2u(__hmul2(signed_f16<0>(x.w[q][i]), d));
+                        v[1][q] = h2u(__hmul2(signed_f16<1>(x.w[q][i]), d));
+                        v[2][q] = h2u(__hmul2(signed_f16<2>(x.w[q][i]), d));
+                        v[3][q] = h2u(__hmul2(signed_f16<3>(x.w[q][i]), d));
+                    }
+#pragma unroll
+                    for (int nib = 0; nib < 4; nib++)
+                        *reinterpret_cast<uint4 *>(to + (32 * i + nib) * 128 + (v_cx ^ (nib * 16))) =
+                            make_uint4(v[nib][0], v[nib][1], v[nib][2], v[nib][3]);
+                }
+            };
+            Keys ka, kc;
+            Values va, vc;
+            if (wk.nblk > 0) {
+                raw_wait(0);
+                if (ok) load_keys(0, ka);
+            }
+            for (int j = 0; j < wk.nblk && ok; j++) {
+                const int kb = wk.blocks_before + j, ks = kb % C::KST, vs = kb % C::VST, grp = j * GPB;
                 uint8_t *sk = smem + C::OFF_K + ks * C::K_BYTES, *sv = smem + C::OFF_V + vs * C::V_BYTES;
-                ok = tc::mbar_wait(&k_empty[ks], ((uint32_t)(kb / C::KST) & 1u) ^ 1u);
-                int mask_all = 0;
-                for (int gi = 0; gi < GPB && ok; gi++) {
-                    const int gb = groups_before + j * GPB + gi, rs = gb % C::RAWST;
-                    ok = tc::mbar_wait(&raw_full[rs], (uint32_t)(gb / C::RAWST) & 1u);
-                    if (!ok) break;
-                    const uint8_t *raw = smem + C::OFF_RAW + rs * C::RAW_BYTES + w8 * C::PITCH;
-                    const int mask = raw_mask[rs];
-                    mask_all |= mask << (4 * gi);
-                    const bool live = (mask >> w8) & 1;
-                    // keys: warp w8 takes tile w8, 8 tokens at a time; lane (g, q) holds values 8 q .. of its blocks
-                    const int g = lane >> 2, q4 = lane & 3;
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const int row = gi * 64 + w8 * 16 + e * 8 + g;   // token within the block
-#pragma unroll
-                        for (int c = 0; c < NC; c++) {
-                            uint32_t w[BW], ds[BW];
-                            if (live) {
-                                lds_words<BW>(raw + 4 * ((e * NC + c) * 32 + lane) * BW, w);
-                                lds_words<BW>(raw + L::KS + 4 * ((4 * e + (g >> 1)) * NB + c * BW), ds);
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < BW; i++) w[i] = ds[i] = 0;
-                            }
-                            if (g & 1) {   // odd rows take the blocks in another order: their stores hit other banks
-#pragma unroll
-                                for (int i = 0; i < BW; i += 2) {
-                                    const uint32_t u = w[i], d = ds[i];
-                                    w[i] = w[i + 1]; w[i + 1] = u;
-                                    ds[i] = ds[i + 1]; ds[i + 1] = d;
-                                }
-                            }
-#pragma unroll
-                            for (int i = 0; i < BW; i++) {
-                                const int b = c * BW + (i ^ (g & 1));
-                                const __half2 d = u2h(__byte_perm(ds[i], 0, (g & 1) ? 0x3232 : 0x1010));
-                                uint4 o;
-                                o.x = h2u(__hmul2(signed_f16<0>(w[i]), d));
-                                o.y = h2u(__hmul2(signed_f16<1>(w[i]), d));
-                                o.z = h2u(__hmul2(signed_f16<2>(w[i]), d));
-                                o.w = h2u(__hmul2(signed_f16<3>(w[i]), d));
-                                const int chunk = 4 * b + q4;   // of 8 values
-                                *reinterpret_cast<uint4 *>(sk + (chunk >> 3) * (BT * 128) + row * 128 +
-                                                           (((chunk & 7) ^ (row & 7)) * 16)) = o;
-                            }
-                        }
-                    }
+                if constexpr (GPB == 2) raw_wait(grp + 1);
+                ok = ok && tc::mbar_wait(&k_empty[ks], ((uint32_t)(kb / C::KST) & 1u) ^ 1u);
+                if (!ok) break;
+                int mask = raw_mask[(wk.groups_before + grp) % C::RAWST];
+                if constexpr (GPB == 2) {
+                    mask |= raw_mask[(wk.groups_before + grp + 1) % C::RAWST] << C::GT;
+                    load_keys(grp + 1, kc);
+                } else load_values(grp, va);
+                put_keys(sk, 0, ka);
+                if constexpr (GPB == 2) {
+                    load_values(grp, va);
+                    put_keys(sk, 1, kc);
                 }
-                if (ok) {
-                    if (w8 == 0 && lane == 0) blk_mask[kb & 7] = mask_all;
-                    tc::fence_proxy_async_smem();
-                    tc::mbar_arrive(&k_full[ks]);
-                    ok = tc::mbar_wait(&v_empty[vs], ((uint32_t)(kb / C::VST) & 1u) ^ 1u);
+                if (w8 == 0 && lane == 0) blk_mask[kb & 7] = mask;
+                tc::fence_proxy_async_smem();
+                arrive(&k_full[ks]);
+                if constexpr (GPB == 2) load_values(grp + 1, vc);
+                ok = tc::mbar_wait(&v_empty[vs], ((uint32_t)(kb / C::VST) & 1u) ^ 1u);
+                if (!ok) break;
+                put_values(sv, 0, va);
+                arrive(&raw_empty[(wk.groups_before + grp) % C::RAWST]);
+                if constexpr (GPB == 2) {
+                    put_values(sv, 1, vc);
+                    arrive(&raw_empty[(wk.groups_before + grp + 1) % C::RAWST]);
                 }
-                for (int gi = 0; gi < GPB && ok; gi++) {
-                    const int gb = groups_before + j * GPB + gi, rs = gb % C::RAWST;
-                    const uint8_t *raw0 = smem + C::OFF_RAW + rs * C::RAW_BYTES;
-                    const int mask = raw_mask[rs];
-                    // values: lane (tile, p, gs): 8 tokens (one 16-byte chunk of a row of V^T) of 4 values of half of
-                    // the blocks; the tiles' pitch and the other eighth at odd p keep loads and stores off each
-                    // other's banks
-                    constexpr int XS = NB / 2;
-                    const int tl = lane & 3, pp = (lane >> 2) & 1, gs = lane >> 3, hb = w8 >> 1;
-                    const int g = 2 * gs + (pp ^ (w8 & 1));
-                    const bool live = (mask >> tl) & 1;
-                    const uint8_t *raw = raw0 + tl * C::PITCH;
-                    uint32_t w[4][XS], dv[4][XS];
-#pragma unroll
-                    for (int q = 0; q < 4; q++)
-#pragma unroll
-                        for (int i = 0; i < XS; i++) {
-                            const int b = hb * XS + i;
-                            w[q][i] = live ? *reinterpret_cast<const uint32_t *>(raw + L::VC + 4 * (((pp * NC + b / BW) * 32 + g * 4 + q) * BW + b % BW)) : 0;
-                            dv[q][i] = live ? *reinterpret_cast<const uint32_t *>(raw + L::VS + 4 * ((4 * pp + q) * NB + b)) : 0;
-                        }
-                    const int i0 = j * (BT / KV_TILE) + 4 * gi + tl;
-                    // scales of tokens past the last query's position may be anything
-                    const int end = item.pos0 + (item.row0 + item.rows - 1) / G - item.tok0 - token_of(i0) - 8 * pp;
-                    if (end < 7) {
-#pragma unroll
-                        for (int q = 0; q < 4; q++) {
-                            const uint32_t keep = (2 * q <= end ? 0xffffu : 0u) | (2 * q + 1 <= end ? 0xffff0000u : 0u);
-#pragma unroll
-                            for (int i = 0; i < XS; i++) dv[q][i] &= keep;
-                        }
-                    }
-                    const int chunk = tl * 2 + pp;
-#pragma unroll
-                    for (int i = 0; i < XS; i++) {
-                        const int b = hb * XS + i;
-                        auto put = [&](int nib, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
-                            const int row = 32 * b + 4 * g + nib;
-                            *reinterpret_cast<uint4 *>(sv + gi * (D * 128) + row * 128 + ((chunk ^ (row & 7)) * 16)) =
-                                make_uint4(x0, x1, x2, x3);
-                        };
-                        uint32_t x[4][4];
-#pragma unroll
-                        for (int q = 0; q < 4; q++) {
-                            const __half2 d = u2h(dv[q][i]);
-                            x[0][q] = h2u(__hmul2(signed_f16<0>(w[q][i]), d));
-                            x[1][q] = h2u(__hmul2(signed_f16<1>(w[q][i]), d));
-                            x[2][q] = h2u(__hmul2(signed_f16<2>(w[q][i]), d));
-                            x[3][q] = h2u(__hmul2(signed_f16<3>(w[q][i]), d));
-                        }
-#pragma unroll
-                        for (int nib = 0; nib < 4; nib++) put(nib, x[nib][0], x[nib][1], x[nib][2], x[nib][3]);
-                    }
-                    tc::mbar_arrive(&raw_empty[rs]);
-                }
-                if (ok) {
-                    tc::fence_proxy_async_smem();
-                    tc::mbar_arrive(&v_full[vs]);
-                }
-                if (!ok) { if (lane == 0) fail(4); }
+                tc::fence_proxy_async_smem();
+                arrive(&v_full[vs]);
                 if (*abort_flag) break;
+                if (j + 1 < wk.nblk) {
+                    raw_wait(grp + GPB);
+                    if (ok) load_keys(grp + GPB, ka);
+                }
             }
-        } else if (warp == 12) {
-            // ================= MMA
-            if (lane == 0 && nblk > 0) {
-                constexpr uint32_t idesc_s = tc::idesc_f16_f32(128, BT), idesc_o = tc::idesc_f16_f32(128, D);
-                const uint32_t q_base = tc::smem_u32(smem), k_base = q_base + C::OFF_K, v_base = q_base + C::OFF_V;
-                bool ok = true;
-                auto scores = [&](int n) {
-                    const int j = n / nrt, t = n % nrt, x = n & 1, kb = blocks_before + j, ks = kb % C::KST;
-                    if (t == 0) ok = ok && tc::mbar_wait(&k_full[ks], (uint32_t)(kb / C::KST) & 1u);
-                    if (!ok) return;
+            if (!ok && lane == 0) fail(4);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(AP_REGS_FEW));
+        for (int64_t st = 0; st < stripes; st++) {
+            const int64_t it = item_of(st);
+            if (it >= total) continue;
+            if (!begin(wk, it)) break;
+            if (warp == AP_MMA) {
+                // ================= MMA: the warp stays together and every operand comes from values that are known to
+                // be the same in all lanes, so that they are computed in uniform registers, where the instruction
+                // wants them (moving them there took 100 cycles an MMA); one elected lane issues
+                auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+                const int nrt = same(wk.nrt), nitems = same(wk.nitems), before = same(wk.blocks_before);
+                const int uses0 = same(wk.uses[0]), uses1 = same(wk.uses[1]);
+                const uint32_t tm = (uint32_t)same((int)tmem);
+                if (nitems > 0) {
+                    constexpr uint32_t idesc_s = tc::idesc_f16_f32(128, BT), idesc_o = tc::idesc_f16_f32(128, D);
+                    const uint32_t q_base = (uint32_t)same((int)tc::smem_u32(smem)), k_base = q_base + C::OFF_K, v_base = q_base + C::OFF_V;
+                    auto wait = [](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity)); };
+                    bool ok = wait(&q_full, (uint32_t)wk.items & 1u);
                     tc::tc_fence_after();
+                    auto scores = [&](int j, int t, int x) {
+                        const int kb = before + j, ks = kb % C::KST;
+                        if (t == 0) ok = ok && wait(&k_full[ks], (uint32_t)(kb / C::KST) & 1u);
+                        if (!ok) return;
+                        tc::tc_fence_after();
+                        // a step within a tile only adds to the address field of its descriptor
+                        const uint64_t qd = tc::sw128_desc(q_base + t * (128 * D * 2)), kd = tc::sw128_desc(k_base + ks * C::K_BYTES);
+                        const uint32_t d = tm + x * C::COL_S;
+                        if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; k++)
-                        tc::mma_f16(tmem + x * C::COL_S,
-                                    tc::sw128_desc(q_base + t * (128 * D * 2) + (k / 4) * 16384 + (k % 4) * 32),
-                                    tc::sw128_desc(k_base + ks * C::K_BYTES + (k / 4) * (BT * 128) + (k % 4) * 32), idesc_s, k > 0);
-                    tc::mma_commit(&s_full[x]);
-                    if (t == nrt - 1) tc::mma_commit(&k_empty[ks]);
-                };
-                scores(0);
-                if (nitems > 1) scores(1);
-                for (int n = 0; n < nitems && ok; n++) {
-                    const int j = n / nrt, t = n % nrt, x = n & 1, kb = blocks_before + j, vs = kb % C::VST;
-                    ok = tc::mbar_wait(&p_full[x], (uint32_t)(uses[x] + n / 2) & 1u);
-                    if (ok && t == 0) ok = tc::mbar_wait(&v_full[vs], (uint32_t)(kb / C::VST) & 1u);
-                    if (!ok || *abort_flag) break;
-                    tc::tc_fence_after();
+                            for (int k = 0; k < D / 16; k++)
+                                tc::mma_f16(d, qd + ((k / 4) * 16384 + (k % 4) * 32) / 16,
+                                            kd + ((k / 4) * (BT * 128) + (k % 4) * 32) / 16, idesc_s, k > 0);
+                            tc::mma_commit(&s_full[x]);
+                            if (t == nrt - 1) tc::mma_commit(&k_empty[ks]);
+                        }
+                        __syncwarp();
+                    };
+                    if (ok) scores(0, 0, 0);
+                    if (ok && nitems > 1) scores(nrt == 1 ? 1 : 0, nrt == 1 ? 0 : 1, 1);
+                    // item n: row tile t of block j, S buffer x; item n + 2 two row tiles on
+                    for (int n = 0, j = 0, t = 0; n < nitems && ok; n++) {
+                        const int x = n & 1, kb = before + j, vs = kb % C::VST;
+                        const uint32_t parity = (uint32_t)((x ? uses1 : uses0) + n / 2) & 1u;
+                        ok = wait(&p_full[x], parity);
+                        if (ok && t == 0) ok = wait(&v_full[vs], (uint32_t)(kb / C::VST) & 1u);
+                        if (!ok || __any_sync(0xffffffffu, *abort_flag)) break;
+                        tc::tc_fence_after();
+                        const uint64_t vd = tc::sw128_desc(v_base + vs * C::V_BYTES);
+                        const uint32_t d = tm + C::COL_O + t * D, pa = tm + x * C::COL_S, more = j > 0;
+                        if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < BT / 16; k++)
-                        tc::mma_f16_ts(tmem + C::COL_O + t * D, tmem + x * C::COL_S + 8 * k,
-                                       tc::sw128_desc(v_base + vs * C::V_BYTES + (k / 4) * (D * 128) + (k % 4) * 32), idesc_o,
-                                       j > 0 || k > 0);
-                    tc::mma_commit(&pv_done[x]);
-                    if (t == nrt - 1) tc::mma_commit(&v_empty[vs]);
-                    if (n + 2 < nitems) {
-                        // the next scores overwrite this P
-                        ok = tc::mbar_wait(&pv_done[x], (uint32_t)(uses[x] + n / 2) & 1u);
-                        if (ok) scores(n + 2);
+                            for (int k = 0; k < BT / 16; k++)
+                                tc::mma_f16_ts(d, pa + 8 * k, vd + ((k / 4) * (D * 128) + (k % 4) * 32) / 16, idesc_o, k > 0 ? 1 : more);
+                            tc::mma_commit(&pv_done[x]);
+                            if (t == nrt - 1) tc::mma_commit(&v_empty[vs]);
+                        }
+                        __syncwarp();
+                        if (n + 2 < nitems) {
+                            // the next scores overwrite this P
+                            ok = wait(&pv_done[x], parity);
+                            if (ok) scores(nrt == 1 ? j + 2 : j + 1, t, x);
+                        }
+                        if (++t == nrt) { t = 0; j++; }
                     }
-                }
-                if (!ok || *abort_flag) {   // what was issued ends before the CTA does
-                    fail(2);
-                    tc::mma_commit(&drain);
-                    tc::mbar_wait(&drain, 0);
-                }
-            }
-        } else {
-            // ================= loads: GT tiles at a time, lane i tile i
-            bool ok = true;
-            const int ngroups = nblk * GPB;
-            int issued = 0;
-            for (int gi = 0; gi < ngroups && ok; gi++) {
-                const int gb = groups_before + gi, rs = gb % C::RAWST;
-                const int i = gi * C::GT + (lane & 3);
-                int32_t pg = -1;
-                int tok = 0;
-                if (i < item.nt) {
-                    tok = token_of(i);
-                    const uint32_t pi = (uint32_t)tok / (uint32_t)p.page;
-                    pg = pi < p.width ? p.table[item.r * p.ld + pi] : -1;
-                    if (lane < 4 && (pg < 0 || pg >= p.n_pages) && p.status != nullptr) atomicAdd(p.status, 1);
-                }
-                const bool live = lane < 4 && pg >= 0 && pg < p.n_pages;
-                const uint32_t mask = __ballot_sync(0xffffffffu, live);
-                ok = __all_sync(0xffffffffu, tc::mbar_wait(&raw_empty[rs], ((uint32_t)(gb / C::RAWST) & 1u) ^ 1u)) && !*abort_flag;
-                if (!ok) { if (lane == 0) fail(32); break; }
-                if (lane == 0) {
-                    raw_mask[rs] = (int32_t)mask;
-                    tc::mbar_arrive_expect_tx(&raw_full[rs], (uint32_t)__popc(mask) * L::BYTES);
+                    if (!ok || __any_sync(0xffffffffu, *abort_flag)) {   // what was issued ends before the CTA does
+                        if (lane == 0) fail(2);
+                        if (elect_one()) tc::mma_commit(&drain);
+                        __syncwarp();
+                        tc::mbar_wait(&drain, 0);
+                    }
                 }
                 __syncwarp();
-                if (live) {
-                    const uint32_t off = (uint32_t)tok % (uint32_t)p.page;
-                    bulk_load(smem + C::OFF_RAW + rs * C::RAW_BYTES + lane * C::PITCH,
-                              p.cache + pg * kv_page_bytes(D, p.hk, p.page) +
-                                  (item.head * (p.page / KV_TILE) + off / KV_TILE) * (int64_t)L::BYTES,
-                              L::BYTES, &raw_full[rs]);
+            } else if (warp == AP_LOAD) {
+                // ================= loads: GT tiles at a time, lane i tile i
+                bool ok = true;
+                const int ngroups = wk.nblk * GPB;
+                int issued = 0;
+                for (int gi = 0; gi < ngroups && ok; gi++) {
+                    const int gb = wk.groups_before + gi, rs = gb % C::RAWST;
+                    const int i = gi * C::GT + (lane & 3);
+                    int32_t pg = -1;
+                    int tok = 0;
+                    if (i < item.nt) {
+                        tok = token_of(i);
+                        const uint32_t pi = (uint32_t)tok / (uint32_t)p.page;
+                        pg = pi < p.width ? p.table[item.r * p.ld + pi] : -1;
+                        if (lane < 4 && (pg < 0 || pg >= p.n_pages) && p.status != nullptr) atomicAdd(p.status, 1);
+                    }
+                    const bool live = lane < 4 && pg >= 0 && pg < p.n_pages;
+                    const uint32_t mask = __ballot_sync(0xffffffffu, live);
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&raw_empty[rs], ((uint32_t)(gb / C::RAWST) & 1u) ^ 1u)) && !*abort_flag;
+                    if (!ok) { if (lane == 0) fail(32); break; }
+                    if (lane == 0) {
+                        raw_mask[rs] = (int32_t)mask;
+                        tc::mbar_arrive_expect_tx(&raw_full[rs], (uint32_t)__popc(mask) * L::BYTES);
+                    }
+                    __syncwarp();
+                    if (live) {
+                        const uint32_t off = (uint32_t)tok % (uint32_t)p.page;
+                        bulk_load(smem + C::OFF_RAW + rs * C::RAW_BYTES + lane * C::PITCH,
+                                  p.cache + pg * kv_page_bytes(D, p.hk, p.page) +
+                                      (item.head * (p.page / KV_TILE) + off / KV_TILE) * (int64_t)L::BYTES,
+                                  L::BYTES, &raw_full[rs]);
+                    }
+                    issued = gi + 1;
                 }
-                issued = gi + 1;
+                if (!ok)   // copies that are under way land before the CTA exits
+                    for (int gi = max(0, issued - C::RAWST); gi < issued; gi++)
+                        tc::mbar_wait(&raw_full[(wk.groups_before + gi) % C::RAWST], (uint32_t)((wk.groups_before + gi) / C::RAWST) & 1u);
             }
-            if (!ok)   // copies that are under way land before the CTA exits
-                for (int gi = max(0, issued - C::RAWST); gi < issued; gi++)
-                    tc::mbar_wait(&raw_full[(groups_before + gi) % C::RAWST], (uint32_t)((groups_before + gi) / C::RAWST) & 1u);
         }
-        blocks_before += nblk;
-        groups_before += nblk * GPB;
-        uses[0] += (nitems + 1) / 2;
-        uses[1] += nitems / 2;
-        tc::tc_fence_before();
-        __syncthreads();   // the item's shared and tensor memory are free
-        tc::tc_fence_after();
-        if (*abort_flag) break;
     }
-    __syncthreads();
-    if (warp == 12) tc::tmem_dealloc(tmem, 512);
+    tc::tc_fence_before();
+    everyone();
+    tc::tc_fence_after();
+    if (warp == AP_MMA) tc::tmem_dealloc(tmem, 512);
 }
 
 template <int D, int QT>
