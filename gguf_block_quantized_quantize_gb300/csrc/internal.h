@@ -212,7 +212,7 @@ cudaError_t launch_kv_plan(const KvPlan &p, cudaStream_t s);
 struct QkRope {   // gguf_qk_norm_rope
     const void *q, *k, *v;
     int64_t ldq, ldk, ldv, n_tokens, h, hk;
-    int64_t rows;   // rows of a token to treat: h queries, then keys (k_out or cache), then values (cache)
+    int64_t rows;   // rows of a token to norm and rotate: h queries, then the keys
     const float *qw, *kw;
     float eps;
     const int32_t *pos;

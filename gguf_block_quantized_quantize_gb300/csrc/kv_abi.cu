@@ -103,7 +103,7 @@ gguf_status gguf_qk_norm_rope(const gguf_qk_rope_args *a, gguf_stream_t stream) 
     if (!at(a->q_norm, 16) || !at(a->k_norm, 16) || !at(a->cos_sin, 16) || !at(a->cache, 16))
         return report(GGUF_ERR_ALIGNMENT, "qk_norm_rope: q_norm, k_norm, cos_sin and cache must be 16-byte aligned");
     const QkRope p{a->q, a->k, a->v, a->ldq, a->ldk, a->ldv, a->n_tokens, a->n_heads, hk,
-                   a->n_heads + (keys ? hk : 0) + (store ? hk : 0), a->q_norm, a->k_norm, a->eps, a->positions,
+                   a->n_heads + hk, a->q_norm, a->k_norm, a->eps, a->positions,
                    a->cos_sin, a->rot > 0 ? a->n_positions : INT64_MAX, (int)a->rot, a->rope_type == GGUF_ROPE_NEOX, a->q_out, a->k_out,
                    a->ldqo, a->ldko, (uint8_t *)a->cache, a->n_pages, a->page_size, a->slots, a->dev_status};
     const bool vec = rows16(a->q, a->ldq, es) && rows16(keys ? a->k : nullptr, a->ldk, es) &&
