@@ -26,7 +26,18 @@ size_t attn_ws_size(const Attn &p, int64_t d) {
 cudaError_t launch_attn(const Attn &p, int64_t d, void *ws, cudaStream_t s) {
     const int ctas = decode_ctas();
     const int64_t es = p.qt == GGUF_F32 ? 4 : 2;
-    AdShape a{p, 0, 0x7fffffff, 0, 0, (float *)ws, nullptr, tg_error_word()};
+    AdShape a{};
+    a.p = p;
+    a.max_rows = 0x7fffffff;
+    a.part = (float *)ws;
+    a.err = tg_error_word();
+    auto shift_of = [](int32_t x) { return (x & (x - 1)) == 0 ? __builtin_ctz(x) : -1; };
+    a.G = (int32_t)(p.h / p.hk);
+    a.hk = (int32_t)p.hk;
+    a.G_shift = shift_of(a.G);
+    a.tpp = (int32_t)(p.page / KV_TILE);
+    a.tpp_shift = shift_of(a.tpp);
+    a.page_bytes = kv_page_bytes(d, p.hk, p.page);
     a.meta = (AdMeta *)((uint8_t *)ws + (size_t)ctas * 2 * (d == 256 ? 8 : 16) * (d + 2) * 4);
     a.vec = (reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.out)) % 16 == 0 && p.ldq * es % 16 == 0 &&
             p.ldo * es % 16 == 0;

@@ -67,12 +67,17 @@ struct AdShape {
     Attn p;
     int32_t min_rows, max_rows;   // requests with more than min_rows and at most max_rows query rows per KV head are taken
     int32_t vec;                  // rows of q and out start on 16 bytes
+    int32_t G, hk;                // query heads per KV head, KV heads
+    int32_t G_shift;              // G = 1 << G_shift, or -1
+    int32_t tpp, tpp_shift;       // tiles per page, likewise
+    int64_t page_bytes;
     int32_t whole;                // each CTA takes one whole unit (few short ones), and nothing is left to join
     float *part;                  // CTA-level partial results, two slots per CTA
     AdMeta *meta;                 // per CTA: the unit that goes on past it
     int *err;                     // error word: a wait for a copy was given up
 };
 
+__host__ __device__ __forceinline__ int ad_token_of_row(const AdShape &a, int row) { return a.G_shift >= 0 ? row >> a.G_shift : row / a.G; }
 // one request: its queries and the tiles that they see together
 struct AdReq {
     int32_t rows0;        // first query token
@@ -83,7 +88,7 @@ struct AdReq {
 __device__ __forceinline__ AdReq ad_request(const AdShape &a, int r) {
     AdReq o;
     const Attn &p = a.p;
-    const int G = (int)(p.h / p.hk);
+    const int G = a.G;
     o.rows0 = p.q_start[r];
     const int64_t q = min((int64_t)p.q_start[r + 1] - o.rows0, p.max_q);
     const bool mine = o.rows0 >= 0 && q > 0 && q * G > a.min_rows && q * G <= a.max_rows && o.rows0 + q <= p.n_tokens;
@@ -106,8 +111,7 @@ __device__ __forceinline__ AdReq ad_request(const AdShape &a, int r) {
 }
 // its units: groups of rg query rows x KV heads
 __device__ __forceinline__ int64_t ad_units(const AdShape &a, const AdReq &q, int rg) {
-    const int G = (int)(a.p.h / a.p.hk);
-    return (int64_t)((q.q * G + rg - 1) / rg) * a.p.hk;
+    return (int64_t)((q.q * a.G + rg - 1) / rg) * a.hk;
 }
 // a / b of non-negative numbers, mostly small ones
 __device__ __forceinline__ int64_t ad_div(int64_t a, int64_t b) {
@@ -221,7 +225,7 @@ struct AdCursor {
 template <int RG>
 __device__ __forceinline__ void ad_next_unit(const AdShape &a, AdCursor &c) {
     c.tile = 0;
-    if (++c.u < (c.q.q * (int)(a.p.h / a.p.hk) + RG - 1) / RG * (int)a.p.hk) return;
+    if (++c.u < (c.q.q * a.G + RG - 1) / RG * a.hk) return;
     c.u = 0;
     do {
         if (++c.r >= a.p.R) return;
@@ -337,8 +341,8 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
         int stage = 0, uses = 0;      // next stage, and how often the ring has gone round
         int base = 0, of = -1;        // the table entries: first page, and request
         int32_t now8 = -1, next8 = -1;
-        const uint32_t tpp = (uint32_t)(p.page / KV_TILE);
-        const int shift = (tpp & (tpp - 1)) == 0 ? __ffs(tpp) - 1 : -1;
+        const uint32_t tpp = (uint32_t)a.tpp;
+        const int shift = a.tpp_shift;
         AdCursor feed{};
         if (tiles > 0) feed = starts[who];
         const uint8_t *head = nullptr;   // the unit's head in page 0
@@ -359,7 +363,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             if (go && unit == 0) {
                 if (feed.tile == feed.q.nt) ad_next_unit<RG>(a, feed);
                 unit = min(tiles, feed.q.nt - feed.tile);
-                head = p.cache + (int64_t)(feed.u % (int)p.hk) * tpp * L::BYTES;
+                head = p.cache + (int64_t)(feed.u % a.hk) * tpp * L::BYTES;
             }
             __syncwarp();
             const int cnt = min(TP, unit), i = feed.tile + max(min(l8, cnt - 1), 0);
@@ -392,7 +396,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             __syncwarp();
             if (ok)
                 bulk_load(smem + who * C::RING + stage * C::STEP + l8 * L::BYTES,
-                          head + pg * kv_page_bytes(D, p.hk, p.page) + in_page * L::BYTES, L::BYTES, &full[who][stage]);
+                          head + pg * a.page_bytes + in_page * L::BYTES, L::BYTES, &full[who][stage]);
             if (go) {
                 feed.tile += cnt;
                 tiles -= cnt;
@@ -414,15 +418,15 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     int64_t open_end = 0;
     if (t0 < t1) {
         AdCursor cur = starts[warp];
-        const int G = (int)(p.h / p.hk);
+        const int G = a.G;
         const float log2_scale = p.scale * 1.44269504088896341f;
         bool dead = false;
         int left_tiles = (int)min(t1 - t0, (int64_t)0x7fffffff), stage = 0;
         uint32_t phase = 0;
         while (left_tiles > 0) {
             // ---- a unit, or the part of it that is the warp's: its query rows
-            const int row0 = cur.u / (int)p.hk * RG, head0 = cur.u % (int)p.hk * G, rows = cur.q.q * G;
-            const int pos_lo = cur.q.pos0 + row0 / G, pos_hi = cur.q.pos0 + (min(rows, row0 + RG) - 1) / G;
+            const int group = cur.u / a.hk, row0 = group * RG, head0 = (cur.u - group * a.hk) * G, rows = cur.q.q * G;
+            const int pos_lo = cur.q.pos0 + ad_token_of_row(a, row0), pos_hi = cur.q.pos0 + ad_token_of_row(a, min(rows, row0 + RG) - 1);
             uint32_t qb[QP][NB][2][NT][2];   // B fragments of the queries: row g, values 8 q4 .. of each block
             float corr[NB][NT][4];           // what the code offsets add to rows 2 q4, + 1 (twice: an accumulator), negated
             float sl[NT][2];                 // scores to log2 units
@@ -432,7 +436,8 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             for (int n = 0; n < NT; n++) {
                 const int row = row0 + g + 8 * n;
                 const bool there = row < rows;
-                const int64_t at = there ? (cur.q.rows0 + row / G) * p.ldq + (int64_t)(head0 + row % G) * D : 0;
+                const int tk = ad_token_of_row(a, row);
+                const int64_t at = there ? (cur.q.rows0 + tk) * p.ldq + (int64_t)(head0 + row - tk * G) * D : 0;
                 if constexpr (QT != GGUF_F32) {
                     uint32_t w[NB][4];
                     float mx = 0.0f;
@@ -589,7 +594,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
 #pragma unroll
                         for (int j = 0; j < 2; j++) {
                             const int row = row0 + 8 * n + 2 * q4 + j;
-                            pos[n][j] = row < rows ? cur.q.pos0 + row / G : -1;
+                            pos[n][j] = row < rows ? cur.q.pos0 + ad_token_of_row(a, row) : -1;
                         }
 #pragma unroll
                     for (int x = 0; x < TP; x++) {
@@ -730,7 +735,8 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                         const float inv = lsum[n][j] == 0.0f ? 0.0f : 1.0f / lsum[n][j];
                         const int row = row0 + 8 * n + 2 * q4 + j;
                         if (row < rows) {
-                            const int64_t at = (cur.q.rows0 + row / G) * p.ldo + (int64_t)(head0 + row % G) * D;
+                            const int tk = ad_token_of_row(a, row);
+                            const int64_t at = (cur.q.rows0 + tk) * p.ldo + (int64_t)(head0 + row - tk * G) * D;
 #pragma unroll
                             for (int b = 0; b < NB; b++)
                                 store4<QT>(p.out, at + 32 * b + 4 * g, a.vec, o[b][0][n][j] * inv, o[b][0][n][2 + j] * inv,
@@ -771,7 +777,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
 
     // ---- the CTA's pieces: a chain is the piece that opens a unit (or the first warp's piece of a unit from the CTA
     // before) and the pieces of the warps after it
-    const int G = (int)(p.h / p.hk);
+    const int G = a.G;
     int chain = -1;          // the warp that opened the chain, -1 none; `orphan`: it came from the CTA before
     bool orphan = false;
     auto piece = [&](int w, bool first) {
@@ -795,10 +801,10 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             }
             if (!orphan && !open) {
                 const AdReq q = ad_request(a, left_r[chain]);
-                const int u = left_u[chain], at_row = u / (int)p.hk * RG + row;
+                const int u = left_u[chain], at_row = u / a.hk * RG + row;
                 if (at_row < q.q * G) {
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                    store4<QT>(p.out, (q.rows0 + at_row / G) * p.ldo + (int64_t)(u % (int)p.hk * G + at_row % G) * D + col,
+                    store4<QT>(p.out, (q.rows0 + at_row / G) * p.ldo + (int64_t)(u % a.hk * G + at_row % G) * D + col,
                                a.vec, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
                 }
             } else {
@@ -835,8 +841,8 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
         AdMeta m{};
         if (follow > 0) {
             const AdReq q = ad_request(a, left_r[opener]);
-            const int u = left_u[opener], row0 = u / (int)p.hk * RG;
-            m = AdMeta{follow, q.rows0, u % (int)p.hk * G, row0, min(q.q * G - row0, RG), {}};
+            const int u = left_u[opener], row0 = u / a.hk * RG;
+            m = AdMeta{follow, q.rows0, u % a.hk * G, row0, min(q.q * G - row0, RG), {}};
         }
         a.meta[blockIdx.x] = m;
     }
@@ -898,7 +904,7 @@ __global__ void __launch_bounds__(AC_THREADS) attn_combine_kernel(const AdShape 
         v.x = fmaf(x.x, h, v.x); v.y = fmaf(x.y, h, v.y); v.z = fmaf(x.z, h, v.z); v.w = fmaf(x.w, h, v.w);
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int G = (int)(p.h / p.hk), at = m.row0 + row;
+    const int G = a.G, at = m.row0 + row;
     store4<QT>(p.out, (m.rows0 + at / G) * p.ldo + (int64_t)(m.head0 + at % G) * D + 4 * col, a.vec, v.x * inv, v.y * inv,
                v.z * inv, v.w * inv);
 }
@@ -909,7 +915,7 @@ static cudaError_t attn_decode_run(const AdShape &shape, int ctas, cudaStream_t 
     AdShape a = shape;
     // Few units of few tiles: a CTA each, and the second launch is saved (about 4 us).  The table's width bounds the
     // tiles: 2048 tokens are 128 tiles, 11 to 16 per warp, about 4 us.
-    const int64_t most_rows = std::min<int64_t>(a.max_rows, a.p.h / a.p.hk * a.p.max_q);
+    const int64_t most_rows = std::min<int64_t>(a.max_rows, a.G * a.p.max_q);
     const int64_t units = a.p.R * a.p.hk * ((most_rows + C::RG - 1) / C::RG);
     const int64_t span = a.p.window > 0 ? std::min(a.p.width * a.p.page, a.p.window + a.p.sinks + a.p.max_q + 3 * KV_TILE)
                                         : a.p.width * a.p.page;

@@ -104,8 +104,7 @@ __device__ __forceinline__ bool elect_one() {
 // row blocks (of ROWS query rows) x KV heads of one request
 template <int ROWS>
 __device__ __forceinline__ int64_t ap_items(const AdShape &a, const AdReq &q) {
-    const int G = (int)(a.p.h / a.p.hk);
-    return ((int64_t)q.q * G + ROWS - 1) / ROWS * a.p.hk;
+    return ((int64_t)q.q * a.G + ROWS - 1) / ROWS * a.p.hk;
 }
 
 template <int D, int QT>
@@ -127,7 +126,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     volatile int32_t *abort_flag = &abort_word;
     const Attn &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int G = (int)(p.h / p.hk);
+    const int G = a.G;
     if (tid == 0) {
         for (int i = 0; i < C::RAWST; i++) { tc::mbar_init(&raw_full[i], 1); tc::mbar_init(&raw_empty[i], AP_UW); }
         for (int i = 0; i < C::KST; i++) { tc::mbar_init(&k_full[i], AP_UW); tc::mbar_init(&k_empty[i], 1); }
@@ -686,7 +685,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                     if (live) {
                         const uint32_t off = (uint32_t)tok % (uint32_t)p.page;
                         bulk_load(smem + C::OFF_RAW + rs * C::RAW_BYTES + lane * C::PITCH,
-                                  p.cache + pg * kv_page_bytes(D, p.hk, p.page) +
+                                  p.cache + pg * a.page_bytes +
                                       (item.head * (p.page / KV_TILE) + off / KV_TILE) * (int64_t)L::BYTES,
                                   L::BYTES, &raw_full[rs]);
                     }
