@@ -41,15 +41,23 @@ cudaError_t launch_attn(const Attn &p, int64_t d, void *ws, cudaStream_t s) {
     a.meta = (AdMeta *)((uint8_t *)ws + (size_t)ctas * 2 * (d == 256 ? 8 : 16) * (d + 2) * 4);
     a.vec = (reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.out)) % 16 == 0 && p.ldq * es % 16 == 0 &&
             p.ldo * es % 16 == 0;
-    // requests with few query rows per KV head go to the decode kernel, the others to the prefill kernel (which
-    // takes 16-bit queries); host and device sizes decide, request by request
-    const int64_t G = p.h / p.hk, most = G * p.max_q;
-    const bool prefill = p.qt != GGUF_F32 && most > 16;
-    if (prefill) a.max_rows = G <= 8 ? 8 : 16;
+    // Requests with few query rows per KV head go to the decode kernel, the others to the prefill kernel (which takes
+    // 16-bit queries); the device decides request by request.  An SM spends about 1500 cycles on 128 tokens for 8 rows
+    // in the decode kernel (2100 for 16), 2800 and 5000 for up to 128 and 256 rows in the prefill kernel, so 16 rows are
+    // the limit where there is work for every SM.  The prefill kernel does not cut a row block's tokens among CTAs:
+    // with fewer row blocks than SMs the limit grows by what stands idle (5 requests of 3 tokens after 600, 8 heads of
+    // 256 per KV head: 48 us there, 17 us here).
+    const int64_t G = p.h / p.hk, most = G * p.max_q, sms = device_info().sm_count;
+    const int64_t blocks = p.R * p.hk * ((most + 255) / 256);
+    const int64_t few = std::min<int64_t>(std::max<int64_t>(16, 16 * sms / std::max<int64_t>(blocks, 1)), 64);
+    const bool prefill = p.qt != GGUF_F32 && most > few;
+    if (prefill) a.max_rows = (int32_t)few;
     // 16 rows at once where a unit has more than 8, so that its cache bytes are read and unpacked once
-    const int nt = (prefill ? a.max_rows : most) > 8 && p.qt != GGUF_F32 ? 2 : 1;
+    const int nt = (prefill ? few : most) > 8 && (G > 8 || !prefill) && p.qt != GGUF_F32 ? 2 : 1;
+    // half the rows per CTA where that fills the GPU better
+    a.item_rows = d == 256 || blocks < sms ? 128 : 256;
     cudaError_t e = cudaSuccess;
-    if (!prefill || G <= a.max_rows)
+    if (!prefill || G <= few)   // some request may have as few rows
         e = d == 64 ? launch_attn_decode_64(a, nt, ctas, s)
           : d == 128 ? launch_attn_decode_128(a, nt, ctas, s) : launch_attn_decode_256(a, nt, ctas, s);
     if (e != cudaSuccess || !prefill) return e;

@@ -71,6 +71,7 @@ struct AdShape {
     int32_t G_shift;              // G = 1 << G_shift, or -1
     int32_t tpp, tpp_shift;       // tiles per page, likewise
     int64_t page_bytes;
+    int32_t item_rows;            // prefill: query rows of a CTA's piece of work
     int32_t whole;                // each CTA takes one whole unit (few short ones), and nothing is left to join
     float *part;                  // CTA-level partial results, two slots per CTA
     AdMeta *meta;                 // per CTA: the unit that goes on past it
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     __shared__ uint32_t absent[C::WARPS][ST];   // tiles of a stage that have no page
     __shared__ AdCursor starts[C::WARPS];
     __shared__ int64_t warp_sum[C::THREADS / 32];
-    __shared__ int32_t cta_tiles;
+    __shared__ int32_t cta_tiles, blind;   // blind: some queries see no token
     __shared__ int32_t abort_word;
     volatile int32_t *abort_flag = &abort_word;
     // what each warp leaves at its end: 1 a piece of a unit that began before the warp, which 2 goes on past the
@@ -264,8 +265,9 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     const int g = lane >> 2, q4 = lane & 3;
     if (tid < C::WARPS)
         for (int i = 0; i < ST; i++) { tc::mbar_init(&full[tid][i], 1); tc::mbar_init(&freed[tid][i], 1); }
-    if (tid == 0) abort_word = 0;
+    if (tid == 0) abort_word = blind = 0;
     tc::fence_barrier_init();
+    __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -279,6 +281,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     for (int r = r0; r < r1; r++) {
         rq = ad_request(a, r);
         mine += ad_units(a, rq, RG) * (a.whole ? 1 : rq.nt);
+        if (rq.q > 0 && rq.nt == 0) blind = 1;   // (every writer writes the same)
     }
     int64_t before = mine;
 #pragma unroll
@@ -847,7 +850,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
         a.meta[blockIdx.x] = m;
     }
     // ---- queries that see no token
-    for (int r = blockIdx.x * C::WARPS + warp; r < R; r += gridDim.x * C::WARPS) {
+    for (int r = blockIdx.x * C::WARPS + warp; blind && r < R; r += gridDim.x * C::WARPS) {
         const AdReq q = ad_request(a, r);
         if (q.nt > 0) continue;
         const int64_t n = (int64_t)q.q * p.h * (D / 4);

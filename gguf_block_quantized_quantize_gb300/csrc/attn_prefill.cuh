@@ -101,10 +101,9 @@ __device__ __forceinline__ bool elect_one() {
     return one != 0;
 }
 
-// row blocks (of ROWS query rows) x KV heads of one request
-template <int ROWS>
+// row blocks (of item_rows query rows) x KV heads of one request
 __device__ __forceinline__ int64_t ap_items(const AdShape &a, const AdReq &q) {
-    return ((int64_t)q.q * a.G + ROWS - 1) / ROWS * a.p.hk;
+    return (int64_t)((q.q * a.G + a.item_rows - 1) / a.item_rows) * a.p.hk;
 }
 
 template <int D, int QT>
@@ -147,7 +146,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     const int R = (int)p.R, per = (R + AP_THREADS - 1) / AP_THREADS;
     {
         int64_t mine = 0;
-        for (int r = tid * per; r < min(R, (tid + 1) * per); r++) mine += ap_items<ROWS>(a, ad_request(a, r));
+        for (int r = tid * per; r < min(R, (tid + 1) * per); r++) mine += ap_items(a, ad_request(a, r));
         int64_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -207,14 +206,14 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             AdReq q;
             for (w.r = hi * per;; w.r++) {   // it is there: it < total
                 q = ad_request(a, w.r);
-                const int64_t n = ap_items<ROWS>(a, q);
+                const int64_t n = ap_items(a, q);
                 if (before + n > it) break;
                 before += n;
             }
-            const int rows = q.q * G, nblk = (rows + ROWS - 1) / ROWS;
+            const int rows = q.q * G, nblk = (rows + a.item_rows - 1) / a.item_rows;
             w.head = (int)((it - before) % p.hk);
-            w.row0 = (nblk - 1 - (int)((it - before) / p.hk)) * ROWS;
-            w.rows = min(ROWS, rows - w.row0);
+            w.row0 = (nblk - 1 - (int)((it - before) / p.hk)) * a.item_rows;
+            w.rows = min(a.item_rows, rows - w.row0);
             w.q0 = q.rows0;
             w.tok0 = w.row0 / G;
             w.pos0 = q.pos0 + w.tok0;
@@ -459,23 +458,18 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                 const int gb = wk.groups_before + grp;
                 ok = tc::mbar_wait(&raw_full[gb % C::RAWST], (uint32_t)(gb / C::RAWST) & 1u);
             };
-            struct Keys { uint32_t w[2][NB], d[2][NB]; };
-            struct Values { uint32_t w[4][XS], d[4][XS]; };
+            struct Keys { uint32_t w[2][NB], d[2][NB]; bool live; };
+            struct Values { uint32_t w[4][XS], d[4][XS]; int end; };   // end: last token of the 8 that counts
             auto load_keys = [&](int grp, Keys &x) {
                 const int rs = (wk.groups_before + grp) % C::RAWST;
                 const uint8_t *raw = raws + rs * C::RAW_BYTES + w8 * C::PITCH;
-                const bool live = (raw_mask[rs] >> w8) & 1;
+                x.live = (raw_mask[rs] >> w8) & 1;
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
 #pragma unroll
                     for (int c = 0; c < NC; c++) {
-                        uint32_t w[BW];
-                        lds_words<BW>(raw + 4 * ((e * NC + c) * 32 + lane) * BW, w);
-#pragma unroll
-                        for (int i = 0; i < BW; i++) x.w[e][c * BW + i] = odd ? w[i ^ 1] : w[i];
-                        lds_words<BW>(raw + L::KS + 4 * ((4 * e + (kg >> 1)) * NB + c * BW), w);
-#pragma unroll
-                        for (int i = 0; i < BW; i++) x.d[e][c * BW + i] = live ? (odd ? w[i ^ 1] : w[i]) : 0u;
+                        lds_words<BW>(raw + 4 * ((e * NC + c) * 32 + lane) * BW, *reinterpret_cast<uint32_t(*)[BW]>(&x.w[e][c * BW]));
+                        lds_words<BW>(raw + L::KS + 4 * ((4 * e + (kg >> 1)) * NB + c * BW), *reinterpret_cast<uint32_t(*)[BW]>(&x.d[e][c * BW]));
                     }
                 }
             };
@@ -485,8 +479,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                     uint8_t *to = sk + (gi * 64 + e * 8) * 128;
 #pragma unroll
                     for (int i = 0; i < NB; i++) {   // block i ^ odd
-                        const __half2 d = u2h(__byte_perm(x.d[e][i], 0, odd ? 0x3232 : 0x1010));
-                        const uint32_t w = x.w[e][i];
+                        const uint32_t w = odd ? x.w[e][i ^ 1] : x.w[e][i], s = odd ? x.d[e][i ^ 1] : x.d[e][i];
+                        const __half2 d = u2h(x.live ? __byte_perm(s, 0, odd ? 0x3232 : 0x1010) : 0u);
                         *reinterpret_cast<uint4 *>(to + (i >> 1) * (BT * 128) + (k_off ^ (i & 1 ? 64 : 0))) =
                             make_uint4(h2u(__hmul2(signed_f16<0>(w), d)), h2u(__hmul2(signed_f16<1>(w), d)),
                                        h2u(__hmul2(signed_f16<2>(w), d)), h2u(__hmul2(signed_f16<3>(w), d)));
@@ -497,8 +491,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                 const int rs = (wk.groups_before + grp) % C::RAWST;
                 const uint8_t *raw = raws + rs * C::RAW_BYTES + tl * C::PITCH;
                 const bool live = (raw_mask[rs] >> tl) & 1;
-                // scales of tokens past the last query's position may be anything
-                const int i = grp * C::GT + tl, end = live ? last - (i < n_sink ? i : w_tile + i - n_sink) * KV_TILE : -1;
+                const int i = grp * C::GT + tl;
+                x.end = live ? last - (i < n_sink ? i : w_tile + i - n_sink) * KV_TILE : -1;
                 const int b0 = hb * XS;
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
@@ -512,7 +506,11 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                         lds_words<XS>(dp, x.d[q]);
                     }
                 }
-                if (end < 7) {
+            };
+            auto put_values = [&](uint8_t *sv, int gi, Values &x) {
+                uint8_t *to = sv + gi * (D * 128) + v_row;
+                if (x.end < 7) {   // scales of tokens past the last query's position may be anything
+                    const int end = x.end;
 #pragma unroll
                     for (int q = 0; q < 4; q++) {
                         const uint32_t keep = (2 * q <= end ? 0xffffu : 0u) | (2 * q + 1 <= end ? 0xffff0000u : 0u);
@@ -520,9 +518,6 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                         for (int i = 0; i < XS; i++) x.d[q][i] &= keep;
                     }
                 }
-            };
-            auto put_values = [&](uint8_t *sv, int gi, const Values &x) {
-                uint8_t *to = sv + gi * (D * 128) + v_row;
 #pragma unroll
                 for (int i = 0; i < XS; i++) {
                     uint32_t v[4][4];
