@@ -402,3 +402,71 @@ def test_step_end_to_end():
                 for r in range(n)]
         kk, vv = g.gguf_kv_get_rows(cache, torch.cat(rows), hk, d, page)
         check_attn(out, attn_ref(q, kk, vv, new, ctx, d ** -0.5, 0, 0), "bf16")
+
+
+# ------------------------------------------------------------------ the binding, and all of it together
+
+def test_binding_refuses_what_does_not_fit():
+    h, hk, d, page = 4, 2, 64, 16
+    q, cache, table, start, kv_len, k, v = attn_setup([1], [40], h, hk, d, page, "bf16")
+    run = lambda **kw: g.gguf_paged_attention(*[kw.get(n, x) for n, x in (   # noqa: E731
+        ("q", q), ("cache", cache), ("table", table), ("start", start), ("kv_len", kv_len))], kw.get("hk", hk), page, 1, 0.1,
+        out=kw.get("out"), ws=kw.get("ws"))
+    bad = [dict(q=q.cpu()), dict(q=q.to(torch.float64)), dict(q=q[0]), dict(q=q.transpose(1, 2).contiguous().transpose(1, 2)),
+           dict(cache=cache[:, 1:]), dict(cache=cache.float()), dict(table=table.long()), dict(start=start.long()),
+           dict(kv_len=kv_len.float()), dict(out=torch.empty_like(q, dtype=torch.float32)), dict(out=torch.empty_like(q)[:, :2]),
+           dict(start=start[:1]), dict(hk=4)]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            run(**kw)
+    with pytest.raises(g.GgufError) as e:
+        run(ws=torch.empty(64, dtype=torch.uint8, device=DEV))
+    assert e.value.status == 5
+    with pytest.raises(g.GgufError) as e:
+        run(hk=3, cache=torch.zeros(2, g.gguf_kv_page_bytes(d, 3, page), dtype=torch.uint8, device=DEV))
+    assert e.value.status == 3
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32, device=DEV)   # noqa: E731
+    with pytest.raises(ValueError):
+        g.gguf_kv_plan(i32(2), i32(3), i32(4), torch.zeros(3, 4, dtype=torch.int32, device=DEV), 16, 1)
+    with pytest.raises(ValueError):
+        g.gguf_qk_norm_rope(q, k, v, None, None, 0.0, i32(1), None)                     # k of another dtype
+    with pytest.raises(ValueError):
+        g.gguf_qk_norm_rope(q, None, None, None, None, 0.0, i32(1), None, cache=cache)  # nothing to store
+    with pytest.raises(ValueError):
+        g.gguf_kv_get_rows(cache, kv_len, hk, d, page)                                  # slots must be int64
+    assert torch.isfinite(run().float()).all()
+
+
+def test_many_requests_and_heads():
+    """More requests than a CTA has threads, of all lengths from none on; one query head per KV head."""
+    n, h, hk, d, page = 700, 2, 2, 64, 16
+    kv_lens = [int(x) for x in np.random.default_rng(0).integers(0, 40, n)]
+    kv_lens[5] = 900
+    q, cache, table, start, kv_len, k, v = attn_setup([1] * n, kv_lens, h, hk, d, page, "bf16")
+    out = g.gguf_paged_attention(q, cache, table, start, kv_len, hk, page, 1, 0.125)
+    check_attn(out, attn_ref(q, k, v, [1] * n, kv_lens, 0.125, 0, 0), "bf16")
+
+
+@pytest.mark.parametrize("typ, window", [("bf16", 0), ("f16", 700)])
+def test_pieces_of_a_long_context(typ, window):
+    """A context that many CTAs share, and one that ends inside their pieces."""
+    q_lens, kv_lens, h, hk, d, page = [1, 1], [9001, 2500], 4, 1, 128, 64
+    q, cache, table, start, kv_len, k, v = attn_setup(q_lens, kv_lens, h, hk, d, page, typ)
+    out = g.gguf_paged_attention(q, cache, table, start, kv_len, hk, page, 1, d ** -0.5, window=window, sinks=17 if window else 0)
+    check_attn(out, attn_ref(q, k, v, q_lens, kv_lens, d ** -0.5, window, 17 if window else 0), typ)
+
+
+def test_no_device_errors():
+    assert g.gguf_device_errors() == 0
+
+
+def test_example_attention_layer():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_layer.py")
+    spec = importlib.util.spec_from_file_location("attention_layer", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    out = mod.main(["--requests", "3", "--prompt", "150", "--steps", "5"])
+    # the prompt, one step before the capture, and five replays
+    assert out["context"] == [50 + 6, 100 + 6, 150 + 6] and out["lost"] == 0 and out["finite"]
