@@ -251,14 +251,14 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[C::WARPS][ST], freed[C::WARPS][ST];
     __shared__ uint32_t absent[C::WARPS][ST];   // tiles of a stage that have no page
-    __shared__ AdCursor starts[C::WARPS];
+    __shared__ int32_t start_r[C::WARPS], start_at[C::WARPS];   // where a warp starts: request, tile of the request's
     __shared__ int64_t warp_sum[C::THREADS / 32];
     __shared__ int32_t cta_tiles, blind;   // blind: some queries see no token
     __shared__ int32_t abort_word;
     volatile int32_t *abort_flag = &abort_word;
     // what each warp leaves at its end: 1 a piece of a unit that began before the warp, which 2 goes on past the
     // warp; 4 the first piece of a unit that goes on past the warp
-    __shared__ int32_t left[C::WARPS], left_r[C::WARPS], left_u[C::WARPS];
+    __shared__ int32_t left[C::WARPS], left_row[C::WARPS], left_u[C::WARPS], left_rows[C::WARPS];   // first query, unit, rows
     __shared__ int64_t left_end[C::WARPS];
     const Attn &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -290,7 +290,6 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
         if (lane >= o) before += v;
     }
     if (lane == 31) warp_sum[warp] = before;
-    if (tid < C::WARPS) starts[tid].q.nt = 0;
     if (tid == 0) cta_tiles = 0;
     __syncthreads();
     before -= mine;
@@ -308,16 +307,21 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
         const int64_t units = ad_units(a, rq, RG), n = units * (a.whole ? 1 : rq.nt);
         if (before < cta1 && before + n > cta0) {
             if (a.whole) {   // the CTA's unit: its tiles over the warps
-                const int share_w = (rq.nt + C::WARPS - 1) / C::WARPS;
-                for (int w = 0; w < C::WARPS; w++)
-                    if (w * share_w < rq.nt) starts[w] = AdCursor{r, (int)(cta0 - before), w * share_w, rq};
-                cta_tiles = rq.nt;
-            } else {
+                const int share_w = (rq.nt + C::WARPS - 1) / C::WARPS, first = (int)(cta0 - before) * rq.nt;
+#pragma unroll
                 for (int w = 0; w < C::WARPS; w++) {
-                    const int64_t t = cta0 + w * per_warp;
-                    if (t >= before && t < before + n && t < cta1) {
-                        const int u = (int)ad_div(t - before, rq.nt);
-                        starts[w] = AdCursor{r, u, (int)(t - before - (int64_t)u * rq.nt), rq};
+                    start_r[w] = r;
+                    start_at[w] = first + w * share_w;
+                }
+                cta_tiles = rq.nt;
+            } else {   // (a request has less than 2^31 tiles in all its units)
+                const int64_t skip = cta0 - before;
+#pragma unroll
+                for (int w = 0; w < C::WARPS; w++) {
+                    const int64_t at = skip + w * per_warp;
+                    if (at >= 0 && at < n) {
+                        start_r[w] = r;
+                        start_at[w] = (int32_t)at;
                     }
                 }
             }
@@ -330,6 +334,14 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
         cta1 = cta_tiles;
         per_warp = (cta1 + C::WARPS - 1) / C::WARPS;
     }
+    auto start_of = [&](int w) {
+        AdCursor c;
+        c.r = start_r[w];
+        c.q = ad_request(a, c.r);
+        c.u = (int)((uint32_t)start_at[w] / (uint32_t)c.q.nt);
+        c.tile = start_at[w] - c.u * c.q.nt;
+        return c;
+    };
     const int64_t per_cta = share;
 
     if (warp >= C::WARPS) {
@@ -347,7 +359,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
         const uint32_t tpp = (uint32_t)a.tpp;
         const int shift = a.tpp_shift;
         AdCursor feed{};
-        if (tiles > 0) feed = starts[who];
+        if (tiles > 0) feed = start_of(who);
         const uint8_t *head = nullptr;   // the unit's head in page 0
         uint64_t idle_since = 0;
         // the lanes stay together: a step is taken by all groups whose stage is free
@@ -417,10 +429,10 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     auto join_warps = [] { asm volatile("bar.sync 1, %0;" ::"n"(NCOMP) : "memory"); };
     uint8_t *ring = smem + warp * C::RING;
     const int64_t t0 = min(cta1, cta0 + warp * per_warp), t1 = min(cta1, t0 + per_warp);
-    int flags = 0, open_r = 0, open_u = 0;
+    int flags = 0, open_row = 0, open_rows = 0, open_u = 0;
     int64_t open_end = 0;
     if (t0 < t1) {
-        AdCursor cur = starts[warp];
+        AdCursor cur = start_of(warp);
         const int G = a.G;
         const float log2_scale = p.scale * 1.44269504088896341f;
         bool dead = false;
@@ -750,7 +762,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                 // a unit from before the warp leaves its piece beside the ring; one that goes on past the warp ends
                 // with the warp's last tile, and takes the ring, where no copy is under way any more
                 flags |= began ? 4 : unit_end ? 1 : 3;
-                if (began) { open_r = cur.r; open_u = cur.u; open_end = t1 + cur.q.nt - cur.tile; }
+                if (began) { open_row = cur.q.rows0; open_rows = rows; open_u = cur.u; open_end = t1 + cur.q.nt - cur.tile; }
                 __syncwarp();
                 float *dst = reinterpret_cast<float *>(began ? ring : smem + C::WARPS * C::RING + warp * C::SLOT);
 #pragma unroll
@@ -772,7 +784,8 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     }
     if (lane == 0) {
         left[warp] = flags;
-        left_r[warp] = open_r;
+        left_row[warp] = open_row;
+        left_rows[warp] = open_rows;
         left_u[warp] = open_u;
         left_end[warp] = open_end;
     }
@@ -791,23 +804,26 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
         for (int it = tid; it < RG * D / 4; it += NCOMP) {
             const int row = it / (D / 4), col = it % (D / 4) * 4;
             float mx = -INFINITY;
+#pragma unroll 4
             for (int w = chain; w <= end; w++) mx = fmaxf(mx, piece(w, ring1 && w == chain)[RG * D + 2 * row]);
             const float base = mx == -INFINITY ? 0.0f : mx;
             float l = 0.0f;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
             for (int w = chain; w <= end; w++) {
                 const float *src = piece(w, ring1 && w == chain);
-                const float f = ex2(src[RG * D + 2 * row] - base);
+                const float2 ml = *reinterpret_cast<const float2 *>(src + RG * D + 2 * row);
                 const float4 x = *reinterpret_cast<const float4 *>(src + row * D + col);
-                l = fmaf(f, src[RG * D + 2 * row + 1], l);
+                const float f = ex2(ml.x - base);
+                l = fmaf(f, ml.y, l);
                 v.x = fmaf(f, x.x, v.x); v.y = fmaf(f, x.y, v.y); v.z = fmaf(f, x.z, v.z); v.w = fmaf(f, x.w, v.w);
             }
             if (!orphan && !open) {
-                const AdReq q = ad_request(a, left_r[chain]);
-                const int u = left_u[chain], at_row = u / a.hk * RG + row;
-                if (at_row < q.q * G) {
+                const int u = left_u[chain], group = u / a.hk, at_row = group * RG + row;
+                if (at_row < left_rows[chain]) {
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                    store4<QT>(p.out, (q.rows0 + at_row / G) * p.ldo + (int64_t)(u % a.hk * G + at_row % G) * D + col,
+                    const int tk = ad_token_of_row(a, at_row);
+                    store4<QT>(p.out, (int64_t)(left_row[chain] + tk) * p.ldo + (int64_t)((u - group * a.hk) * G + at_row - tk * G) * D + col,
                                a.vec, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
                 }
             } else {
@@ -843,9 +859,8 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     if (tid == 0 && !a.whole) {
         AdMeta m{};
         if (follow > 0) {
-            const AdReq q = ad_request(a, left_r[opener]);
             const int u = left_u[opener], row0 = u / a.hk * RG;
-            m = AdMeta{follow, q.rows0, u % a.hk * G, row0, min(q.q * G - row0, RG), {}};
+            m = AdMeta{follow, left_row[opener], u % a.hk * G, row0, min(left_rows[opener] - row0, RG), {}};
         }
         a.meta[blockIdx.x] = m;
     }

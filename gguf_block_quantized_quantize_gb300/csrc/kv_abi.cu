@@ -3,6 +3,8 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 #include "kv.cuh"
@@ -167,6 +169,14 @@ gguf_status gguf_paged_attention(const gguf_attn_args *a, void *ws, size_t ws_by
         return report(GGUF_ERR_INVALID_ARG, "paged_attention: a row stride is shorter than the row");
     if (!(a->scale > 0.0f) || a->scale > 3e38f) return report(GGUF_ERR_INVALID_ARG, "paged_attention: scale must be positive and finite");
     if (a->n_tokens == 0 || a->n_requests == 0) return GGUF_OK;
+    // fp32 queries walk over the tokens in groups of 8 rows: a request's groups x heads x tiles of 16 tokens are counted
+    // in 32 bits
+    if (a->qt == GGUF_F32) {
+        const double tiles = (double)a->width * (double)a->page_size / KV_TILE;
+        const double groups = (double)std::min<int64_t>(a->max_q_len, a->n_tokens) * (double)(a->n_heads / a->n_kv_heads) / 8.0 + 1.0;
+        if (tiles * groups * (double)a->n_kv_heads > 4.0e9)
+            return report(GGUF_ERR_SHAPE, "paged_attention: too many fp32 queries over too wide a table for one call; split it");
+    }
     if (!a->q || !a->out || !a->q_start || !a->kv_len || (a->n_pages > 0 && !a->cache) || (a->width > 0 && !a->block_table))
         return report(GGUF_ERR_INVALID_ARG, "paged_attention: null pointer");
     if (!at(a->q, es) || !at(a->out, es) || !at(a->cache, 16) || !at(a->block_table, 4) || !at(a->q_start, 4) ||

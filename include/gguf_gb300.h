@@ -472,8 +472,8 @@ gguf_status gguf_set_option(const char *key, int64_t value);
 int64_t gguf_get_option(const char *key);
 
 /*
- * gguf_device_errors -- the error word of the tensor-core kernels (MMQ and the
- * grouped MoE GEMMs) on the current device.  Those kernels bound every wait
+ * gguf_device_errors -- the error word of the tensor-core kernels (MMQ, the
+ * grouped MoE GEMMs and the paged attention) on the current device.  Those kernels bound every wait
  * of their pipeline (one second); a CTA whose wait gives up sets the bit of
  * its role, stops its work and exits, so the call that launched it has
  * already returned GGUF_OK while its output is incomplete.  The prior art
@@ -625,13 +625,17 @@ gguf_status gguf_kv_get_rows(const void *cache, int64_t n_pages, int64_t page_si
  *   block_table: [n_requests][ld_table] int32, width columns used.  A page number
  *                outside the cache hides its tokens, and dev_status counts it.
  *   q_start    : [n_requests + 1] int32, non-decreasing; kv_len: [n_requests].
- *   max_q_len  : at least the longest request's queries (requests with more get
- *                only their first max_q_len rows): with the other host arguments
- *                it chooses the kernels.  0 < max_q_len.
+ *   max_q_len  : at least the longest request's queries (of a request with more, only
+ *                the first max_q_len are computed): with the other host arguments it
+ *                chooses the kernels.  0 < max_q_len.
  *   ws         : gguf_paged_attention_ws_size(args) bytes, 16-byte aligned.
- * Softmax statistics and sums are fp32.  16-bit queries take 16-bit probabilities
- * and values into the matrix instructions (about 3e-4 of a row's norm), fp32
- * queries split operands (about 1e-6).  Same bits on every run.
+ * Softmax statistics and sums are fp32.  16-bit queries take fp16 probabilities and
+ * values into the matrix instructions, and in long prompts fp16 keys (2e-4 and 4e-4
+ * of a row's norm, beside the rounding of the output); fp32 queries split operands
+ * (about 1e-6; GGUF_ERR_SHAPE where max_q_len x heads / 8 x table tokens / 16 passes
+ * 4e9).  Probabilities below 2^-34 of a row's largest count as zero.  Same bits on
+ * every run.  Timeouts of the kernels' waits reach the caller as described at
+ * gguf_device_errors.
  */
 typedef struct gguf_attn_args {
     const void *q;
