@@ -99,7 +99,7 @@ def attn(lib, ws=256, ws_bytes=1 << 40, **kw):
     (dict(out=None), INVALID), (dict(cache=None), INVALID), (dict(block_table=None), INVALID),
     (dict(q_start=None), INVALID), (dict(kv_len=None), INVALID), (dict(q=257), ALIGN), (dict(out=257), ALIGN),
     (dict(cache=264), ALIGN), (dict(kv_len=257), ALIGN), (dict(q_start=258), ALIGN), (dict(block_table=258), ALIGN),
-    (dict(qt=g.F32, n_tokens=200000, max_q_len=200000, width=12500, ld_table=12500), SHAPE)])
+    (dict(qt=g.F32, n_tokens=200000, max_q_len=200000, width=25000, ld_table=25000), SHAPE)])
 def test_attention_refusals(lib, kw, want):
     assert attn(lib, **kw) == want
     assert b"paged_attention" in lib.gguf_last_error()
