@@ -348,10 +348,11 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
         // ================= copies: 8 lanes ask for those of one computing warp, a step of TP tiles of a unit at a
         // time, a tile each; they hold the 16 table entries from page `base` on, the later 8 on their way early
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_COPY));
-        const int who = (warp - C::WARPS) * 4 + (lane >> 3), l8 = lane & 7;
-        if ((warp - C::WARPS) * 4 >= C::WARPS) return;
+        constexpr int GW = C::WARPS / 4;   // warps that one of the four asks for: every scheduler bears the same load
+        const bool mine8 = (lane >> 3) < GW;
+        const int who = mine8 ? (warp - C::WARPS) * GW + (lane >> 3) : 0, l8 = lane & 7;
         const int64_t t0 = min(cta1, cta0 + who * per_warp), t1 = min(cta1, t0 + per_warp);
-        int tiles = who < C::WARPS ? (int)min(t1 - t0, (int64_t)0x7fffffff) : 0;   // to ask for
+        int tiles = mine8 ? (int)min(t1 - t0, (int64_t)0x7fffffff) : 0;   // to ask for
         int unit = 0;                 // of them, those of the unit
         int stage = 0, uses = 0;      // next stage, and how often the ring has gone round
         int base = 0, of = -1;        // the table entries: first page, and request
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                 const uint64_t now = tc::globaltimer();
                 if (idle_since == 0) idle_since = now;
                 if (__any_sync(0xffffffffu, now - idle_since > tc::kWaitLimitNs)) { *abort_flag = 1; break; }
-                __nanosleep(20);
+                __nanosleep(100);
                 continue;
             }
             idle_since = 0;
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             }
         }
         const int step = uses * ST + stage;
-        if (*abort_flag && who < C::WARPS)   // copies that are under way land before the CTA exits
+        if (*abort_flag && mine8)   // copies that are under way land before the CTA exits
             for (int i = max(0, step - ST); i < step; i++) tc::mbar_wait(&full[who][i % ST], (uint32_t)(i / ST) & 1u);
         return;
     }
