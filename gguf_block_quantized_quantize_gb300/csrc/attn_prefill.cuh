@@ -31,7 +31,6 @@ namespace gg {
 constexpr int AP_UW = 4;                         // warps that unpack
 constexpr int AP_THREADS = (12 + AP_UW) * 32;
 constexpr int AP_MMA = 8 + AP_UW, AP_LOAD = 9 + AP_UW;
-constexpr int AP_REGS = 176, AP_REGS_FEW = 80;   // of the softmax warps and of the others: 128 at launch on average
 
 template <int D>
 struct ApCfg {
@@ -40,6 +39,9 @@ struct ApCfg {
     static constexpr int KST = 2, VST = D == 256 ? 1 : 2;
     static constexpr int GT = 4;                       // cache tiles (of 16 tokens) per load
     static constexpr int RAWST = D == 64 ? 4 : 3;
+    // registers of the softmax warps (a row's scores) and of the others (packed words read ahead): 256 for the two, as at
+    // launch
+    static constexpr int REGS = D == 256 ? 120 : 176, REGS_OTHER = 256 - REGS;
     static constexpr int PITCH = 18 * D + 16;          // raw tiles apart by an odd number of 16-byte banks
     static constexpr int Q_BYTES = RT * 128 * D * 2;
     static constexpr int K_BYTES = BT * D * 2, V_BYTES = BT * D * 2;
@@ -94,6 +96,11 @@ __device__ __forceinline__ uint64_t add_2(uint64_t x, uint64_t y) {
     return r;
 }
 
+template <int N>
+__device__ __forceinline__ void set_registers() {   // from 128 at launch
+    if constexpr (N > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 // true in one lane of the warp
 __device__ __forceinline__ bool elect_one() {
     uint32_t one;
@@ -239,7 +246,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     };
     Walk wk;
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(AP_REGS));
+        set_registers<C::REGS>();
         for (int64_t st = 0; st < stripes; st++) {
             const int64_t it = item_of(st);
             if (it >= total) continue;
@@ -432,7 +439,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             }
         }
     } else if (warp < AP_MMA) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(AP_REGS_FEW));
+        set_registers<C::REGS_OTHER>();
         for (int64_t st = 0; st < stripes; st++) {
             const int64_t it = item_of(st);
             if (it >= total) continue;
@@ -580,7 +587,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             if (!ok && lane == 0) fail(4);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(AP_REGS_FEW));
+        set_registers<C::REGS_OTHER>();
         for (int64_t st = 0; st < stripes; st++) {
             const int64_t it = item_of(st);
             if (it >= total) continue;
