@@ -17,54 +17,77 @@ cudaError_t launch_attn_prefill_256(const AdShape &a, int ctas, cudaStream_t s);
 constexpr int MAX_CTAS = 1024;
 static int decode_ctas() { return device_info().sm_count < MAX_CTAS ? device_info().sm_count : MAX_CTAS; }
 
-// two partial results of up to 16 rows (8 rows of 256 values) per CTA, and its meta data
-size_t attn_ws_size(const Attn &p, int64_t d) {
-    (void)p;
-    return (size_t)decode_ctas() * (2 * (d == 256 ? 8 : 16) * (d + 2) * 4 + sizeof(AdMeta));
+// What a call runs, from its host arguments alone.
+struct AttnPlan {
+    int ctas;          // of both kernels
+    bool decode, prefill;
+    int32_t few;       // requests with at most this many query rows per KV head go to the decode kernel
+    int nt;            // its row tiles
+    int32_t max_splits;
+    size_t meta, base, pieces, bytes;   // offsets in the workspace behind the decode kernel's partial results, and its size
+};
+
+static AttnPlan attn_plan(const Attn &p, int64_t d) {
+    AttnPlan x{};
+    x.ctas = decode_ctas();
+    const int64_t G = p.h / p.hk, most = G * std::min(p.max_q, p.n_tokens), sms = device_info().sm_count;
+    // Requests with few query rows per KV head go to the decode kernel, the others to the prefill kernel (which takes
+    // 16-bit queries); the device decides request by request.  An SM spends about 1500 cycles on 128 tokens for 8 rows
+    // in the decode kernel (2100 for 16), 2800 and 5000 for up to 128 and 256 rows in the prefill kernel, so 16 rows are
+    // the limit where there is work for every SM.  With fewer row blocks than SMs the limit grows by what would stand
+    // idle (5 requests of 3 tokens after 600, 8 heads of 256 per KV head: 48 us there, 17 us here).
+    const int64_t blocks = p.R * p.hk * ((most + 255) / 256);
+    x.few = (int32_t)std::min<int64_t>(std::max<int64_t>(16, 16 * sms / std::max<int64_t>(blocks, 1)), 64);
+    x.prefill = p.qt != GGUF_F32 && most > x.few;
+    x.decode = !x.prefill || G <= x.few;   // some request may have as few rows
+    // 16 rows at once where a unit has more than 8, so that its cache bytes are read and unpacked once
+    x.nt = (x.prefill ? x.few : most) > 8 && (G > 8 || !x.prefill) && p.qt != GGUF_F32 ? 2 : 1;
+    // The device cuts the tokens of its row blocks into pieces where they would leave SMs idle; not where the tokens
+    // alone make enough row blocks, and pieces of 4 blocks at least.
+    const int64_t span = p.window > 0 ? std::min(p.width * p.page, p.window + p.sinks + p.max_q) : p.width * p.page;
+    const bool idle = x.prefill && (p.n_tokens - std::min(p.R, p.n_tokens)) * p.h / 128 <= sms / 2;
+    x.max_splits = idle ? (int32_t)std::max<int64_t>(1, std::min<int64_t>(span / (d == 256 ? 256 : 512), 16)) : 1;
+    auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
+    // two partial results of up to 16 rows (8 rows of 256 values) per CTA, and its meta data
+    x.meta = up((size_t)x.ctas * 2 * (d == 256 ? 8 : 16) * (d + 2) * 4);
+    x.base = up(x.meta + (size_t)x.ctas * sizeof(AdMeta));
+    x.pieces = x.max_splits > 1 ? up(x.base + (size_t)(p.R + 2) * 4) : x.base;   // a piece per SM at most, of 128 rows
+    x.bytes = x.max_splits > 1 ? x.pieces + (size_t)x.ctas * 128 * (d + 2) * 4 : x.base;
+    return x;
 }
 
+size_t attn_ws_size(const Attn &p, int64_t d) { return attn_plan(p, d).bytes; }
+
 cudaError_t launch_attn(const Attn &p, int64_t d, void *ws, cudaStream_t s) {
-    const int ctas = decode_ctas();
+    const AttnPlan x = attn_plan(p, d);
     const int64_t es = p.qt == GGUF_F32 ? 4 : 2;
     AdShape a{};
     a.p = p;
-    a.max_rows = 0x7fffffff;
+    a.max_rows = x.prefill ? x.few : 0x7fffffff;
     a.part = (float *)ws;
+    a.meta = (AdMeta *)((uint8_t *)ws + x.meta);
     a.err = tg_error_word();
-    auto shift_of = [](int32_t x) { return (x & (x - 1)) == 0 ? __builtin_ctz(x) : -1; };
+    auto shift_of = [](int32_t v) { return (v & (v - 1)) == 0 ? __builtin_ctz(v) : -1; };
     a.G = (int32_t)(p.h / p.hk);
     a.hk = (int32_t)p.hk;
     a.G_shift = shift_of(a.G);
     a.tpp = (int32_t)(p.page / KV_TILE);
     a.tpp_shift = shift_of(a.tpp);
     a.page_bytes = kv_page_bytes(d, p.hk, p.page);
-    a.meta = (AdMeta *)((uint8_t *)ws + (size_t)ctas * 2 * (d == 256 ? 8 : 16) * (d + 2) * 4);
     a.vec = (reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.out)) % 16 == 0 && p.ldq * es % 16 == 0 &&
             p.ldo * es % 16 == 0;
-    // Requests with few query rows per KV head go to the decode kernel, the others to the prefill kernel (which takes
-    // 16-bit queries); the device decides request by request.  An SM spends about 1500 cycles on 128 tokens for 8 rows
-    // in the decode kernel (2100 for 16), 2800 and 5000 for up to 128 and 256 rows in the prefill kernel, so 16 rows are
-    // the limit where there is work for every SM.  The prefill kernel does not cut a row block's tokens among CTAs:
-    // with fewer row blocks than SMs the limit grows by what stands idle (5 requests of 3 tokens after 600, 8 heads of
-    // 256 per KV head: 48 us there, 17 us here).
-    const int64_t G = p.h / p.hk, most = G * p.max_q, sms = device_info().sm_count;
-    const int64_t blocks = p.R * p.hk * ((most + 255) / 256);
-    const int64_t few = std::min<int64_t>(std::max<int64_t>(16, 16 * sms / std::max<int64_t>(blocks, 1)), 64);
-    const bool prefill = p.qt != GGUF_F32 && most > few;
-    if (prefill) a.max_rows = (int32_t)few;
-    // 16 rows at once where a unit has more than 8, so that its cache bytes are read and unpacked once
-    const int nt = (prefill ? few : most) > 8 && (G > 8 || !prefill) && p.qt != GGUF_F32 ? 2 : 1;
-    // half the rows per CTA where that fills the GPU better
-    a.item_rows = d == 256 || blocks < sms ? 128 : 256;
+    a.max_splits = x.max_splits;
+    a.item_base = (int32_t *)((uint8_t *)ws + x.base);
+    a.pieces = (float *)((uint8_t *)ws + x.pieces);
     cudaError_t e = cudaSuccess;
-    if (!prefill || G <= few)   // some request may have as few rows
-        e = d == 64 ? launch_attn_decode_64(a, nt, ctas, s)
-          : d == 128 ? launch_attn_decode_128(a, nt, ctas, s) : launch_attn_decode_256(a, nt, ctas, s);
-    if (e != cudaSuccess || !prefill) return e;
+    if (x.decode)
+        e = d == 64 ? launch_attn_decode_64(a, x.nt, x.ctas, s)
+          : d == 128 ? launch_attn_decode_128(a, x.nt, x.ctas, s) : launch_attn_decode_256(a, x.nt, x.ctas, s);
+    if (e != cudaSuccess || !x.prefill) return e;
     a.min_rows = a.max_rows;
     a.max_rows = 0x7fffffff;
-    return d == 64 ? launch_attn_prefill_64(a, ctas, s)
-         : d == 128 ? launch_attn_prefill_128(a, ctas, s) : launch_attn_prefill_256(a, ctas, s);
+    return d == 64 ? launch_attn_prefill_64(a, x.ctas, s)
+         : d == 128 ? launch_attn_prefill_128(a, x.ctas, s) : launch_attn_prefill_256(a, x.ctas, s);
 }
 
 }  // namespace gg

@@ -71,7 +71,9 @@ struct AdShape {
     int32_t G_shift;              // G = 1 << G_shift, or -1
     int32_t tpp, tpp_shift;       // tiles per page, likewise
     int64_t page_bytes;
-    int32_t item_rows;            // prefill: query rows of a CTA's piece of work
+    int32_t max_splits;           // prefill: the pieces that a row block's tokens may be cut into at most (1: no join),
+    int32_t *item_base;           // with the row blocks before each request, their rows and the pieces,
+    float *pieces;                // and the partial results, [row block][piece][row][max, sum, D values]
     int32_t whole;                // each CTA takes one whole unit (few short ones), and nothing is left to join
     float *part;                  // CTA-level partial results, two slots per CTA
     AdMeta *meta;                 // per CTA: the unit that goes on past it

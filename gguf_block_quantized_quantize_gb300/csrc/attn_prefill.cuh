@@ -57,7 +57,9 @@ struct ApItem {
     int r, head, row0, rows;      // request, KV head, first query row and rows (of token * G + head)
     int q0, pos0;                 // the request's first query token, position of row row0's token
     int tok0;                     // row0 / G
-    int nt, n_sink, w_tile;       // the tiles that the rows see (see AdReq)
+    int nt, n_sink, w_tile;       // the tiles that the rows see (see AdReq): the piece takes those from base to nt
+    int base;
+    int64_t part;                 // its place among the partial results, where a row block's tiles are cut
 };
 
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -108,12 +110,12 @@ __device__ __forceinline__ bool elect_one() {
     return one != 0;
 }
 
-// row blocks (of item_rows query rows) x KV heads of one request
-__device__ __forceinline__ int64_t ap_items(const AdShape &a, const AdReq &q) {
-    return (int64_t)((q.q * a.G + a.item_rows - 1) / a.item_rows) * a.p.hk;
+// row blocks (of `rows` query rows) x KV heads of one request
+__device__ __forceinline__ int ap_items(const AdShape &a, const AdReq &q, int rows) {
+    return (int)((q.q * (int64_t)a.G + rows - 1) / rows) * a.hk;
 }
 
-template <int D, int QT>
+template <int D, int QT, bool CUT>
 __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdShape a) {
     using C = ApCfg<D>;
     using L = KvTile<D>;
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     __shared__ uint32_t tmem_slot;
     __shared__ int32_t abort_word;
     __shared__ ApItem item;
-    __shared__ int64_t part[AP_THREADS / 32];
+    __shared__ int32_t part[2][AP_THREADS / 32], cut_rows, cut_pieces;
     __shared__ int32_t chunk_end[AP_THREADS];   // at most (tokens x heads / 128) items: 31 bits
     volatile int32_t *abort_flag = &abort_word;
     const Attn &p = a.p;
@@ -149,26 +151,54 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // work of all requests: thread t counts requests [t * per, (t + 1) * per)
+    // Work of all requests: thread t counts requests [t * per, (t + 1) * per), in row blocks of ROWS rows, and of 128.
+    // The larger ones unpack a key for twice the rows; the smaller ones, and row blocks whose tokens are cut into pieces
+    // (CUT; of 4 blocks at least, joined by a second launch), are for calls that would leave SMs idle.
     const int R = (int)p.R, per = (R + AP_THREADS - 1) / AP_THREADS;
     {
-        int64_t mine = 0;
-        for (int r = tid * per; r < min(R, (tid + 1) * per); r++) mine += ap_items(a, ad_request(a, r));
-        int64_t incl = mine;
+        int item_rows = ROWS, splits = 1;
+        int mine = 0, mine128 = 0;   // (tokens x heads / 128 is below 2^31)
+        for (int r = tid * per; r < min(R, (tid + 1) * per); r++) {
+            const AdReq q = ad_request(a, r);
+            mine += ap_items(a, q, ROWS);
+            mine128 += ap_items(a, q, 128);
+        }
+        int incl = mine, incl128 = mine128;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
+            const int v = __shfl_up_sync(0xffffffffu, incl, o), w = __shfl_up_sync(0xffffffffu, incl128, o);
+            if (lane >= o) { incl += v; incl128 += w; }
         }
-        if (lane == 31) part[warp] = incl;
+        if (lane == 31) { part[0][warp] = incl; part[1][warp] = incl128; }
         tc::tc_fence_before();
         __syncthreads();
         tc::tc_fence_after();
-        for (int w = 0; w < warp; w++) incl += part[w];
-        chunk_end[tid] = (int32_t)min(incl, (int64_t)0x7fffffff);
+        int all = 0, all128 = 0;
+        for (int w = 0; w < AP_THREADS / 32; w++) {
+            if (w < warp) { incl += part[0][w]; incl128 += part[1][w]; }
+            all += part[0][w];
+            all128 += part[1][w];
+        }
+        if (all128 <= (int)gridDim.x) {   // (two rounds of the smaller ones would take longer than one of the larger)
+            item_rows = 128;
+            incl = incl128;
+            mine = mine128;
+            all = all128;
+            if (CUT) splits = max(1, min(a.max_splits, (int)gridDim.x / max(all, 1)));
+        }
+        chunk_end[tid] = incl;
+        if (tid == 0) { cut_rows = item_rows; if (CUT) cut_pieces = splits; }
+        if (CUT && blockIdx.x == 0) {   // for the join: the items before each request, and the cut
+            int before = incl - mine;
+            for (int r = tid * per; r < min(R, (tid + 1) * per); r++) {
+                a.item_base[r] = before;
+                before += ap_items(a, ad_request(a, r), item_rows);
+            }
+            if (tid == 0) { a.item_base[R] = item_rows; a.item_base[R + 1] = splits; }
+        }
         __syncthreads();
     }
-    const int64_t total = chunk_end[AP_THREADS - 1];
+    const int64_t total = (int64_t)chunk_end[AP_THREADS - 1] * (CUT ? cut_pieces : 1);
     const uint32_t tmem = tmem_slot;
     auto fail = [&](int code) {
         *abort_flag = 1;
@@ -191,7 +221,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         int blocks_before = 0, groups_before = 0, uses[2] = {0, 0}, nrt = 0, nblk = 0, nitems = 0, items = -1;
     };
     // the item before is done with (its shared and tensor memory are free), and the next one is known
-    auto begin = [&](Walk &wk, int64_t it) {
+    auto begin = [&](Walk &wk, int64_t piece) {
         wk.blocks_before += wk.nblk;
         wk.groups_before += wk.nblk * GPB;
         wk.uses[0] += (wk.nitems + 1) / 2;
@@ -202,25 +232,27 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         tc::tc_fence_after();
         if (*abort_flag) return false;
         if (tid == 0) {
+            const int item_rows = cut_rows, splits = CUT ? cut_pieces : 1;
+            const int it = CUT ? (int)piece / splits : (int)piece, cut = (int)piece - it * splits;
             int lo = -1, hi = AP_THREADS - 1;
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
                 if (chunk_end[mid] > it) hi = mid;
                 else lo = mid;
             }
-            int64_t before = hi > 0 ? chunk_end[hi - 1] : 0;
+            int before = hi > 0 ? chunk_end[hi - 1] : 0;
             ApItem w;
             AdReq q;
             for (w.r = hi * per;; w.r++) {   // it is there: it < total
                 q = ad_request(a, w.r);
-                const int64_t n = ap_items(a, q);
+                const int n = ap_items(a, q, item_rows);
                 if (before + n > it) break;
                 before += n;
             }
-            const int rows = q.q * G, nblk = (rows + a.item_rows - 1) / a.item_rows;
-            w.head = (int)((it - before) % p.hk);
-            w.row0 = (nblk - 1 - (int)((it - before) / p.hk)) * a.item_rows;
-            w.rows = min(a.item_rows, rows - w.row0);
+            const int rows = q.q * G, nblk = (rows + item_rows - 1) / item_rows;
+            w.head = (it - before) % a.hk;
+            w.row0 = (nblk - 1 - (it - before) / a.hk) * item_rows;
+            w.rows = min(item_rows, rows - w.row0);
             w.q0 = q.rows0;
             w.tok0 = w.row0 / G;
             w.pos0 = q.pos0 + w.tok0;
@@ -236,11 +268,18 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                     w.nt = w.n_sink + end - w.w_tile;
                 }
             }
+            // the blocks of the row block, shared out over the pieces
+            if (CUT) {
+                const int64_t blocks = (w.nt + BT / KV_TILE - 1) / (BT / KV_TILE);
+                w.base = (int)(blocks * cut / splits) * (BT / KV_TILE);
+                w.nt = min(w.nt, (int)(blocks * (cut + 1) / splits) * (BT / KV_TILE));
+                w.part = piece;
+            }
             item = w;
         }
         everyone();
         wk.nrt = item.rows > 128 ? 2 : 1;
-        wk.nblk = (item.nt + BT / KV_TILE - 1) / (BT / KV_TILE);
+        wk.nblk = (item.nt - (CUT ? item.base : 0) + BT / KV_TILE - 1) / (BT / KV_TILE);
         wk.nitems = wk.nblk * wk.nrt;
         return true;
     };
@@ -314,7 +353,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                     tc::tc_fence_after();
                     const uint32_t s_col = tmem + lanes + x * C::COL_S;
                     // whether every row of the warp sees the whole block
-                    const int i0 = j * (BT / KV_TILE), i1 = min(item.nt, i0 + BT / KV_TILE);
+                    const int i0 = (CUT ? item.base : 0) + j * (BT / KV_TILE), i1 = min(item.nt, i0 + BT / KV_TILE);
                     const int mask = blk_mask[(wk.blocks_before + j) & 7];
                     const int t_first = i0 < item.n_sink ? 0 : token_of(i0), t_last = token_of(i1 - 1) + KV_TILE - 1;
                     const bool whole = mask == (1 << (BT / KV_TILE)) - 1 && t_last <= first &&
@@ -414,7 +453,13 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
 #pragma unroll
                             for (int i = 0; i < 32; i++) rr[i] = 0;
                         }
-                        if (there) {
+                        if (CUT && there && cut_pieces > 1) {
+                            float *to = a.pieces + (item.part * cut_rows + row) * (D + 2);
+                            float2 *dst = reinterpret_cast<float2 *>(to + 2 + 32 * c);
+#pragma unroll
+                            for (int i = 0; i < 16; i++) dst[i] = make_float2(__uint_as_float(rr[2 * i]), __uint_as_float(rr[2 * i + 1]));
+                            if (c == 0) *reinterpret_cast<float2 *>(to) = make_float2(ref, lsum);
+                        } else if (there) {
                             uint16_t *out = reinterpret_cast<uint16_t *>(p.out) + at + 32 * c;
                             uint32_t w[16];
 #pragma unroll
@@ -459,7 +504,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             const uint32_t v_cx = ((2 * tl + pp) ^ (4 * (vg & 1))) * 16, v_row = (32 * XS * hb + 4 * vg) * 128;
             const uint8_t *raws = smem + C::OFF_RAW;
             const int last = item.pos0 + (item.row0 + item.rows - 1) / G - item.tok0 - 8 * pp;
-            const int n_sink = item.n_sink, w_tile = item.w_tile;
+            const int n_sink = item.n_sink, w_tile = item.w_tile, i_base = CUT ? item.base : 0;
             bool ok = true;
             auto raw_wait = [&](int grp) {
                 const int gb = wk.groups_before + grp;
@@ -498,7 +543,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                 const int rs = (wk.groups_before + grp) % C::RAWST;
                 const uint8_t *raw = raws + rs * C::RAW_BYTES + tl * C::PITCH;
                 const bool live = (raw_mask[rs] >> tl) & 1;
-                const int i = grp * C::GT + tl;
+                const int i = i_base + grp * C::GT + tl;
                 x.end = live ? last - (i < n_sink ? i : w_tile + i - n_sink) * KV_TILE : -1;
                 const int b0 = hb * XS;
 #pragma unroll
@@ -666,7 +711,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                 int issued = 0;
                 for (int gi = 0; gi < ngroups && ok; gi++) {
                     const int gb = wk.groups_before + gi, rs = gb % C::RAWST;
-                    const int i = gi * C::GT + (lane & 3);
+                    const int i = (CUT ? item.base : 0) + gi * C::GT + (lane & 3);
                     int32_t pg = -1;
                     int tok = 0;
                     if (i < item.nt) {
@@ -705,10 +750,62 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     if (warp == AP_MMA) tc::tmem_dealloc(tmem, 512);
 }
 
+// The pieces of row blocks whose tiles were cut: a warp per query row and head
+// joins them in order.
 template <int D, int QT>
-static cudaError_t attn_prefill_run(const AdShape &a, int ctas, cudaStream_t s) {
+__global__ void __launch_bounds__(256) attn_prefill_join_kernel(const AdShape a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Attn &p = a.p;
+    const int64_t w = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5, t = w / p.h;
+    const int head = (int)(w - t * p.h), lane = threadIdx.x & 31;
+    if (t >= p.n_tokens || t < p.q_start[0]) return;
+    int r = 0;   // the last request that starts at or before t
+    for (int lo = 0, hi = (int)p.R; hi - lo > 1;) {
+        const int mid = (lo + hi) >> 1;
+        if (p.q_start[mid] <= t) lo = mid;
+        else hi = mid;
+        r = lo;
+    }
+    const int item_rows = a.item_base[p.R], splits = a.item_base[p.R + 1];
+    const AdReq q = ad_request(a, r);
+    if (splits == 1 || t - q.rows0 >= q.q) return;   // nothing was cut; not of the prefill kernel's, or past the rows that are computed
+    const int kh = head / a.G, row = (int)(t - q.rows0) * a.G + head - kh * a.G;
+    const int rb = row / item_rows, nrb = (q.q * a.G + item_rows - 1) / item_rows;
+    const int64_t item = a.item_base[r] + (int64_t)(nrb - 1 - rb) * a.hk + kh;
+    const float *from = a.pieces + (item * splits * item_rows + row - rb * item_rows) * (D + 2);
+    const int64_t step = (int64_t)item_rows * (D + 2);
+    float mx = -INFINITY, l = 0.0f;
+    for (int i = 0; i < splits; i++) mx = fmaxf(mx, from[i * step]);
+    const float base = mx == -INFINITY ? 0.0f : mx;
+    constexpr int PL = D / 64;   // pairs per lane
+    float2 v[PL];
+#pragma unroll
+    for (int x = 0; x < PL; x++) v[x] = make_float2(0.0f, 0.0f);
+    for (int i = 0; i < splits; i++) {
+        const float f = ex2(from[i * step] - base);
+        l = fmaf(f, from[i * step + 1], l);
+#pragma unroll
+        for (int x = 0; x < PL; x++) {
+            const float2 o = *reinterpret_cast<const float2 *>(from + i * step + 2 + 2 * lane + 64 * x);
+            v[x].x = fmaf(f, o.x, v[x].x);
+            v[x].y = fmaf(f, o.y, v[x].y);
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t *out = reinterpret_cast<uint16_t *>(p.out) + t * p.ldo + (int64_t)head * D + 2 * lane;
+#pragma unroll
+    for (int x = 0; x < PL; x++) {
+        const float f0 = l == 0.0f ? 0.0f : v[x].x * inv, f1 = l == 0.0f ? 0.0f : v[x].y * inv;
+        out[64 * x] = QT == GGUF_BF16 ? f2bf_rn(f0) : f2h_rn(f0);
+        out[64 * x + 1] = QT == GGUF_BF16 ? f2bf_rn(f1) : f2h_rn(f1);
+    }
+}
+
+template <int D, int QT, bool CUT>
+static cudaError_t attn_prefill_launch(const AdShape &a, int ctas, cudaStream_t s) {
     cudaError_t err = cudaSuccess;
-    if (kernel_occupancy((const void *)attn_prefill_kernel<D, QT>, AP_THREADS, ApCfg<D>::SMEM, &err) == 0) return err;
+    if (kernel_occupancy((const void *)attn_prefill_kernel<D, QT, CUT>, AP_THREADS, ApCfg<D>::SMEM, &err) == 0) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(AP_THREADS);
@@ -719,7 +816,17 @@ static cudaError_t attn_prefill_run(const AdShape &a, int ctas, cudaStream_t s) 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D, QT>, a);
+    if (const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D, QT, CUT>, a); e != cudaSuccess || !CUT) return e;
+    cfg.gridDim = dim3((unsigned)((a.p.n_tokens * a.p.h + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, attn_prefill_join_kernel<D, QT>, a);
+}
+
+// Two builds of the kernel: what cutting adds costs its spare registers (8192 tokens: 664 us with it, 644 without).
+template <int D, int QT>
+static cudaError_t attn_prefill_run(const AdShape &a, int ctas, cudaStream_t s) {
+    return a.max_splits > 1 ? attn_prefill_launch<D, QT, true>(a, ctas, s) : attn_prefill_launch<D, QT, false>(a, ctas, s);
 }
 
 }  // namespace gg

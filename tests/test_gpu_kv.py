@@ -470,3 +470,18 @@ def test_example_attention_layer():
     out = mod.main(["--requests", "3", "--prompt", "150", "--steps", "5"])
     # the prompt, one step before the capture, and five replays
     assert out["context"] == [50 + 6, 100 + 6, 150 + 6] and out["lost"] == 0 and out["finite"]
+
+
+@pytest.mark.parametrize("q_lens, kv_lens, h, hk, d, typ, window, sinks", [
+    ([40], [3000], 4, 1, 128, "bf16", 0, 0),            # 40 rows x 4 heads, tokens cut into pieces
+    ([70, 1, 33], [2100, 900, 1500], 4, 2, 64, "f16", 0, 0),
+    ([90], [2500], 2, 1, 256, "bf16", 0, 0),
+    ([150], [1900], 2, 2, 128, "bf16", 1100, 20),
+    ([80, 200], [1400, 150], 2, 1, 64, "bf16", 0, 0),   # a request with fewer tokens than queries: blind rows, empty pieces
+])
+def test_pieces_of_a_long_chunk(q_lens, kv_lens, h, hk, d, typ, window, sinks):
+    q, cache, table, start, kv_len, k, v = attn_setup(q_lens, kv_lens, h, hk, d, 16, typ)
+    run = lambda: g.gguf_paged_attention(q, cache, table, start, kv_len, hk, 16, max(q_lens), d ** -0.5, window=window, sinks=sinks)   # noqa: E731
+    out = run()
+    check_attn(out, attn_ref(q, k, v, q_lens, kv_lens, d ** -0.5, window, sinks), typ)
+    assert torch.equal(out, run())
