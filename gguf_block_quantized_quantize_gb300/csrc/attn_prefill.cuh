@@ -11,8 +11,8 @@
 //   O += P V    A = P (fp16, in TMEM, over the columns of its S), B = V^T in
 //               shared memory, O in TMEM
 // The packed tiles of a block come by bulk copies; four warps turn them into
-// fp16 operands (k, v = d * (c - 8), rounded to 2^-12 of them at most) once for
-// all rows of the CTA.  bf16 queries are scaled per row by a power of two into
+// fp16 operands (k, v = d * (c - 8), rounded to 2^-12 of them at most; for fp16
+// queries k exactly, in two parts) once for all rows of the CTA.  bf16 queries are scaled per row by a power of two into
 // fp16's range.  The softmax keeps a reference maximum per row and rescales O
 // only when a score exceeds it by 2^5: probabilities are held as
 // 2^(s - reference + 10), at most 2^15.  Statistics are fp32.
@@ -32,11 +32,15 @@ constexpr int AP_UW = 4;                         // warps that unpack
 constexpr int AP_THREADS = (12 + AP_UW) * 32;
 constexpr int AP_MMA = 8 + AP_UW, AP_LOAD = 9 + AP_UW;
 
-template <int D>
+template <int D, int QT>
 struct ApCfg {
     static constexpr int RT = D == 256 ? 1 : 2;        // row tiles of 128 (the O accumulators fill the TMEM)
     static constexpr int BT = D == 256 ? 64 : 128;     // tokens per block
-    static constexpr int KST = 2, VST = D == 256 ? 1 : 2;
+    // fp16 results keep more bits than keys rounded to fp16 leave in the scores (error 4.8e-4 of the outputs' norm; an
+    // output rounded once has 2.1e-4): for them keys are held in two parts, exactly, and scores are two products (3.0e-4;
+    // 146 -> 153 us at 2048 tokens of heads of 64, 644 -> 766 us at 8192 of heads of 128).  In bf16 results it is lost.
+    static constexpr int KP = QT == GGUF_F16 ? 2 : 1;
+    static constexpr int KST = D > 64 && KP == 2 ? 1 : 2, VST = D == 256 ? 1 : 2;   // as the shared memory allows
     static constexpr int GT = 4;                       // cache tiles (of 16 tokens) per load
     static constexpr int RAWST = D == 64 ? 4 : 3;
     // registers of the softmax warps (a row's scores) and of the others (packed words read ahead): 256 for the two, as at
@@ -44,7 +48,7 @@ struct ApCfg {
     static constexpr int REGS = D == 256 ? 120 : 176, REGS_OTHER = 256 - REGS;
     static constexpr int PITCH = 18 * D + 16;          // raw tiles apart by an odd number of 16-byte banks
     static constexpr int Q_BYTES = RT * 128 * D * 2;
-    static constexpr int K_BYTES = BT * D * 2, V_BYTES = BT * D * 2;
+    static constexpr int K_PART = BT * D * 2, K_BYTES = KP * K_PART, V_BYTES = BT * D * 2;
     static constexpr int RAW_BYTES = GT * PITCH;
     static constexpr int OFF_K = Q_BYTES, OFF_V = OFF_K + KST * K_BYTES, OFF_RAW = OFF_V + VST * V_BYTES;
     static constexpr int SMEM = OFF_RAW + RAWST * RAW_BYTES + 1024;   // 1024 for the base's alignment
@@ -117,7 +121,7 @@ __device__ __forceinline__ int ap_items(const AdShape &a, const AdReq &q, int ro
 
 template <int D, int QT, bool CUT>
 __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdShape a) {
-    using C = ApCfg<D>;
+    using C = ApCfg<D, QT>;
     using L = KvTile<D>;
     constexpr int NB = L::NB, BW = L::BW, NC = L::NC, BT = C::BT, ROWS = C::RT * 128;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -533,9 +537,17 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                     for (int i = 0; i < NB; i++) {   // block i ^ odd
                         const uint32_t w = odd ? x.w[e][i ^ 1] : x.w[e][i], s = odd ? x.d[e][i ^ 1] : x.d[e][i];
                         const __half2 d = u2h(x.live ? __byte_perm(s, 0, odd ? 0x3232 : 0x1010) : 0u);
-                        *reinterpret_cast<uint4 *>(to + (i >> 1) * (BT * 128) + (k_off ^ (i & 1 ? 64 : 0))) =
-                            make_uint4(h2u(__hmul2(signed_f16<0>(w), d)), h2u(__hmul2(signed_f16<1>(w), d)),
-                                       h2u(__hmul2(signed_f16<2>(w), d)), h2u(__hmul2(signed_f16<3>(w), d)));
+                        const __half2 c[4] = {signed_f16<0>(w), signed_f16<1>(w), signed_f16<2>(w), signed_f16<3>(w)};
+                        uint4 *at = reinterpret_cast<uint4 *>(to + (i >> 1) * (BT * 128) + (k_off ^ (i & 1 ? 64 : 0)));
+                        __half2 k[4];
+#pragma unroll
+                        for (int x = 0; x < 4; x++) k[x] = __hmul2(c[x], d);
+                        at[0] = make_uint4(h2u(k[0]), h2u(k[1]), h2u(k[2]), h2u(k[3]));
+                        if constexpr (C::KP == 2) {   // what the rounding left, exactly
+#pragma unroll
+                            for (int x = 0; x < 4; x++) k[x] = __hfma2(c[x], d, __hneg2(k[x]));
+                            at[C::K_PART / 16] = make_uint4(h2u(k[0]), h2u(k[1]), h2u(k[2]), h2u(k[3]));
+                        }
                     }
                 }
             };
@@ -664,6 +676,11 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                             for (int k = 0; k < D / 16; k++)
                                 tc::mma_f16(d, qd + ((k / 4) * 16384 + (k % 4) * 32) / 16,
                                             kd + ((k / 4) * (BT * 128) + (k % 4) * 32) / 16, idesc_s, k > 0);
+                            if constexpr (C::KP == 2)
+#pragma unroll
+                                for (int k = 0; k < D / 16; k++)
+                                    tc::mma_f16(d, qd + ((k / 4) * 16384 + (k % 4) * 32) / 16,
+                                                kd + (C::K_PART + (k / 4) * (BT * 128) + (k % 4) * 32) / 16, idesc_s, 1);
                             tc::mma_commit(&s_full[x]);
                             if (t == nrt - 1) tc::mma_commit(&k_empty[ks]);
                         }
@@ -805,11 +822,11 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const AdShape a)
 template <int D, int QT, bool CUT>
 static cudaError_t attn_prefill_launch(const AdShape &a, int ctas, cudaStream_t s) {
     cudaError_t err = cudaSuccess;
-    if (kernel_occupancy((const void *)attn_prefill_kernel<D, QT, CUT>, AP_THREADS, ApCfg<D>::SMEM, &err) == 0) return err;
+    if (kernel_occupancy((const void *)attn_prefill_kernel<D, QT, CUT>, AP_THREADS, ApCfg<D, QT>::SMEM, &err) == 0) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(AP_THREADS);
-    cfg.dynamicSmemBytes = ApCfg<D>::SMEM;
+    cfg.dynamicSmemBytes = ApCfg<D, QT>::SMEM;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
