@@ -41,12 +41,16 @@ struct ApCfg {
     // 146 -> 153 us at 2048 tokens of heads of 64, 644 -> 766 us at 8192 of heads of 128).  In bf16 results it is lost.
     static constexpr int KP = QT == GGUF_F16 ? 2 : 1;
     static constexpr int KST = D > 64 && KP == 2 ? 1 : 2, VST = D == 256 ? 1 : 2;   // as the shared memory allows
-    static constexpr int GT = 4;                       // cache tiles (of 16 tokens) per load
-    static constexpr int RAWST = D == 64 ? 4 : 3;
+    static constexpr int GT = BT / KV_TILE;            // cache tiles of a block; a load is their keys, or their values
+    // blocks by which keys are unpacked before values: with one V stage the values of a block wait for the product of the
+    // one before, and the next scores need not (8192 tokens of heads of 256: 2155 -> 1712 us; of 128: 644 -> 655 us, and
+    // with one K stage 766 -> 1023 us)
+    static constexpr int AHEAD = VST == 1 ? 1 : 0;
+    static constexpr int RAWST = D == 64 ? 6 : 3;
     // registers of the softmax warps (a row's scores) and of the others (packed words read ahead): 256 for the two, as at
     // launch
     static constexpr int REGS = D == 256 ? 120 : 176, REGS_OTHER = 256 - REGS;
-    static constexpr int PITCH = 18 * D + 16;          // raw tiles apart by an odd number of 16-byte banks
+    static constexpr int PITCH = 9 * D + 16;           // half tiles apart by an odd number of 16-byte banks
     static constexpr int Q_BYTES = RT * 128 * D * 2;
     static constexpr int K_PART = BT * D * 2, K_BYTES = KP * K_PART, V_BYTES = BT * D * 2;
     static constexpr int RAW_BYTES = GT * PITCH;
@@ -215,19 +219,18 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     };
     auto token_of = [&](int i) { return (i < item.n_sink ? i : item.w_tile + i - item.n_sink) * KV_TILE; };
 
-    constexpr int GPB = BT / 64;   // loads per block
     // items in stripes of one per CTA, every other stripe backwards: a request's row blocks come longest first
     const int64_t stripes = (total + gridDim.x - 1) / gridDim.x;
     auto item_of = [&](int64_t stripe) { return stripe * gridDim.x + ((stripe & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x); };
     auto everyone = [] { asm volatile("bar.sync 0, %0;" ::"n"(AP_THREADS) : "memory"); };
     // what a role knows of the current item, and the running uses of the stages and of the S buffers before it
     struct Walk {
-        int blocks_before = 0, groups_before = 0, uses[2] = {0, 0}, nrt = 0, nblk = 0, nitems = 0, items = -1;
+        int blocks_before = 0, loads_before = 0, uses[2] = {0, 0}, nrt = 0, nblk = 0, nitems = 0, items = -1;
     };
     // the item before is done with (its shared and tensor memory are free), and the next one is known
     auto begin = [&](Walk &wk, int64_t piece) {
         wk.blocks_before += wk.nblk;
-        wk.groups_before += wk.nblk * GPB;
+        wk.loads_before += 2 * wk.nblk;
         wk.uses[0] += (wk.nitems + 1) / 2;
         wk.uses[1] += wk.nitems / 2;
         wk.items++;
@@ -493,10 +496,10 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             const int64_t it = item_of(st);
             if (it >= total) continue;
             if (!begin(wk, it)) break;
-            // ================= unpack: a load (GT tiles) at a time, keys of a block first, then values.  The packed words
-            // of the next step are read from shared memory before the current one is computed: the matrix unit's reads
-            // fill the shared memory's bandwidth for long stretches, and a read may take many hundred cycles.
-            // Keys: warp w8 takes tile w8; lane (g, q) holds values 8 q .. of the blocks of tokens g and g + 8; odd g
+            // ================= unpack: the keys of block j + AHEAD, then the values of block j.  The packed words of the next
+            // step are read from shared memory before the current one is computed: the matrix unit's reads fill the shared
+            // memory's bandwidth for long stretches, and a read may take many hundred cycles.  Steps are of 4 tiles.
+            // Keys: warp w8 takes tile w8 of a step; lane (g, q) holds values 8 q .. of the blocks of tokens g and g + 8; odd g
             // takes the blocks in another order, so that the stores of a warp hit different banks.
             // Values: lane (tile, p, gs) holds 8 tokens (one 16-byte chunk of a row of V^T) of 4 values of half of the
             // blocks; the tiles' pitch and the other eighth at odd p keep loads and stores off each other's banks.
@@ -510,16 +513,17 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             const int last = item.pos0 + (item.row0 + item.rows - 1) / G - item.tok0 - 8 * pp;
             const int n_sink = item.n_sink, w_tile = item.w_tile, i_base = CUT ? item.base : 0;
             bool ok = true;
-            auto raw_wait = [&](int grp) {
-                const int gb = wk.groups_before + grp;
-                ok = tc::mbar_wait(&raw_full[gb % C::RAWST], (uint32_t)(gb / C::RAWST) & 1u);
+            constexpr int STEPS = C::GT / 4;
+            auto raw_wait = [&](int load) {
+                const int gb = wk.loads_before + load;
+                ok = ok && tc::mbar_wait(&raw_full[gb % C::RAWST], (uint32_t)(gb / C::RAWST) & 1u);
+                return gb % C::RAWST;
             };
             struct Keys { uint32_t w[2][NB], d[2][NB]; bool live; };
             struct Values { uint32_t w[4][XS], d[4][XS]; int end; };   // end: last token of the 8 that counts
-            auto load_keys = [&](int grp, Keys &x) {
-                const int rs = (wk.groups_before + grp) % C::RAWST;
-                const uint8_t *raw = raws + rs * C::RAW_BYTES + w8 * C::PITCH;
-                x.live = (raw_mask[rs] >> w8) & 1;
+            auto load_keys = [&](int rs, int step, Keys &x) {
+                const uint8_t *raw = raws + rs * C::RAW_BYTES + (4 * step + w8) * C::PITCH;
+                x.live = (raw_mask[rs] >> (4 * step + w8)) & 1;
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
 #pragma unroll
@@ -529,10 +533,10 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                     }
                 }
             };
-            auto put_keys = [&](uint8_t *sk, int gi, const Keys &x) {
+            auto put_keys = [&](uint8_t *sk, int step, const Keys &x) {
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    uint8_t *to = sk + (gi * 64 + e * 8) * 128;
+                    uint8_t *to = sk + (step * 64 + e * 8) * 128;
 #pragma unroll
                     for (int i = 0; i < NB; i++) {   // block i ^ odd
                         const uint32_t w = odd ? x.w[e][i ^ 1] : x.w[e][i], s = odd ? x.d[e][i ^ 1] : x.d[e][i];
@@ -551,17 +555,16 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                     }
                 }
             };
-            auto load_values = [&](int grp, Values &x) {
-                const int rs = (wk.groups_before + grp) % C::RAWST;
-                const uint8_t *raw = raws + rs * C::RAW_BYTES + tl * C::PITCH;
-                const bool live = (raw_mask[rs] >> tl) & 1;
-                const int i = i_base + grp * C::GT + tl;
+            auto load_values = [&](int rs, int j, int step, Values &x) {
+                const uint8_t *raw = raws + rs * C::RAW_BYTES + (4 * step + tl) * C::PITCH;
+                const bool live = (raw_mask[rs] >> (4 * step + tl)) & 1;
+                const int i = i_base + j * C::GT + 4 * step + tl;
                 x.end = live ? last - (i < n_sink ? i : w_tile + i - n_sink) * KV_TILE : -1;
                 const int b0 = hb * XS;
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
-                    const uint8_t *wp = raw + L::VC + 4 * (((pp * NC + b0 / BW) * 32 + vg * 4 + q) * BW + b0 % BW);
-                    const uint8_t *dp = raw + L::VS + 4 * ((4 * pp + q) * NB + b0);
+                    const uint8_t *wp = raw + 4 * (((pp * NC + b0 / BW) * 32 + vg * 4 + q) * BW + b0 % BW);
+                    const uint8_t *dp = raw + (L::VS - L::VC) + 4 * ((4 * pp + q) * NB + b0);
                     if constexpr (XS == 1) {
                         x.w[q][0] = *reinterpret_cast<const uint32_t *>(wp);
                         x.d[q][0] = *reinterpret_cast<const uint32_t *>(dp);
@@ -571,8 +574,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                     }
                 }
             };
-            auto put_values = [&](uint8_t *sv, int gi, Values &x) {
-                uint8_t *to = sv + gi * (D * 128) + v_row;
+            auto put_values = [&](uint8_t *sv, int step, Values &x) {
+                uint8_t *to = sv + step * (D * 128) + v_row;
                 if (x.end < 7) {   // scales of tokens past the last query's position may be anything
                     const int end = x.end;
 #pragma unroll
@@ -601,44 +604,57 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             };
             Keys ka, kc;
             Values va, vc;
+            int load = 0, rk = 0;   // loads taken, the stage of ka's
             if (wk.nblk > 0) {
-                raw_wait(0);
-                if (ok) load_keys(0, ka);
+                rk = raw_wait(0);
+                if (ok) load_keys(rk, 0, ka);
             }
-            for (int j = 0; j < wk.nblk && ok; j++) {
-                const int kb = wk.blocks_before + j, ks = kb % C::KST, vs = kb % C::VST, grp = j * GPB;
-                uint8_t *sk = smem + C::OFF_K + ks * C::K_BYTES, *sv = smem + C::OFF_V + vs * C::V_BYTES;
-                if constexpr (GPB == 2) raw_wait(grp + 1);
-                ok = ok && tc::mbar_wait(&k_empty[ks], ((uint32_t)(kb / C::KST) & 1u) ^ 1u);
-                if (!ok) break;
-                int mask = raw_mask[(wk.groups_before + grp) % C::RAWST];
-                if constexpr (GPB == 2) {
-                    mask |= raw_mask[(wk.groups_before + grp + 1) % C::RAWST] << C::GT;
-                    load_keys(grp + 1, kc);
-                } else load_values(grp, va);
-                put_keys(sk, 0, ka);
-                if constexpr (GPB == 2) {
-                    load_values(grp, va);
-                    put_keys(sk, 1, kc);
+            for (int j = -C::AHEAD; j < wk.nblk && ok; j++) {
+                int rv = 0;
+                if (j + C::AHEAD < wk.nblk) {
+                    const int kb = wk.blocks_before + j + C::AHEAD, ks = kb % C::KST;
+                    uint8_t *sk = smem + C::OFF_K + ks * C::K_BYTES;
+                    ok = tc::mbar_wait(&k_empty[ks], ((uint32_t)(kb / C::KST) & 1u) ^ 1u);
+                    if (!ok) break;
+                    const int mask = raw_mask[rk];
+                    load++;
+                    if constexpr (STEPS == 2) {
+                        load_keys(rk, 1, kc);
+                        put_keys(sk, 0, ka);
+                    }
+                    if (j >= 0) {
+                        rv = raw_wait(load);
+                        if (!ok) break;
+                        load_values(rv, j, 0, va);
+                    }
+                    if constexpr (STEPS == 2) put_keys(sk, 1, kc);
+                    else put_keys(sk, 0, ka);
+                    arrive(&raw_empty[rk]);
+                    if (w8 == 0 && lane == 0) blk_mask[kb & 7] = mask;
+                    tc::fence_proxy_async_smem();
+                    arrive(&k_full[ks]);
+                } else {
+                    rv = raw_wait(load);
+                    if (!ok) break;
+                    load_values(rv, j, 0, va);
                 }
-                if (w8 == 0 && lane == 0) blk_mask[kb & 7] = mask;
-                tc::fence_proxy_async_smem();
-                arrive(&k_full[ks]);
-                if constexpr (GPB == 2) load_values(grp + 1, vc);
-                ok = tc::mbar_wait(&v_empty[vs], ((uint32_t)(kb / C::VST) & 1u) ^ 1u);
-                if (!ok) break;
-                put_values(sv, 0, va);
-                arrive(&raw_empty[(wk.groups_before + grp) % C::RAWST]);
-                if constexpr (GPB == 2) {
-                    put_values(sv, 1, vc);
-                    arrive(&raw_empty[(wk.groups_before + grp + 1) % C::RAWST]);
+                if (j >= 0) {
+                    const int kb = wk.blocks_before + j, vs = kb % C::VST;
+                    uint8_t *sv = smem + C::OFF_V + vs * C::V_BYTES;
+                    load++;
+                    if constexpr (STEPS == 2) load_values(rv, j, 1, vc);
+                    ok = tc::mbar_wait(&v_empty[vs], ((uint32_t)(kb / C::VST) & 1u) ^ 1u);
+                    if (!ok) break;
+                    put_values(sv, 0, va);
+                    if constexpr (STEPS == 2) put_values(sv, 1, vc);
+                    arrive(&raw_empty[rv]);
+                    tc::fence_proxy_async_smem();
+                    arrive(&v_full[vs]);
+                    if (*abort_flag) break;
                 }
-                tc::fence_proxy_async_smem();
-                arrive(&v_full[vs]);
-                if (*abort_flag) break;
-                if (j + 1 < wk.nblk) {
-                    raw_wait(grp + GPB);
-                    if (ok) load_keys(grp + GPB, ka);
+                if (j + 1 + C::AHEAD < wk.nblk) {
+                    rk = raw_wait(load);
+                    if (ok) load_keys(rk, 0, ka);
                 }
             }
             if (!ok && lane == 0) fail(4);
@@ -722,42 +738,45 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                 }
                 __syncwarp();
             } else if (warp == AP_LOAD) {
-                // ================= loads: GT tiles at a time, lane i tile i
+                // ================= loads, in the order of the unpacking: the keys or the values of a block, lane i tile i
                 bool ok = true;
-                const int ngroups = wk.nblk * GPB;
+                const int nloads = 2 * wk.nblk;
                 int issued = 0;
-                for (int gi = 0; gi < ngroups && ok; gi++) {
-                    const int gb = wk.groups_before + gi, rs = gb % C::RAWST;
-                    const int i = (CUT ? item.base : 0) + gi * C::GT + (lane & 3);
+                for (int e = 0; e < nloads && ok; e++) {
+                    const int gb = wk.loads_before + e, rs = gb % C::RAWST;
+                    // K0 V0 K1 V1 .. or, with keys a block ahead, K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1)
+                    const bool values = C::AHEAD == 0 ? (e & 1) != 0 : (e > 0 && !(e & 1)) || e == nloads - 1;
+                    const int j = C::AHEAD == 0 ? e / 2 : values ? (e - 1) / 2 : (e + 1) / 2;
+                    const int i = (CUT ? item.base : 0) + j * C::GT + (lane & (C::GT - 1));
                     int32_t pg = -1;
                     int tok = 0;
                     if (i < item.nt) {
                         tok = token_of(i);
                         const uint32_t pi = (uint32_t)tok / (uint32_t)p.page;
                         pg = pi < p.width ? p.table[item.r * p.ld + pi] : -1;
-                        if (lane < 4 && (pg < 0 || pg >= p.n_pages) && p.status != nullptr) atomicAdd(p.status, 1);
+                        if (lane < C::GT && !values && (pg < 0 || pg >= p.n_pages) && p.status != nullptr) atomicAdd(p.status, 1);
                     }
-                    const bool live = lane < 4 && pg >= 0 && pg < p.n_pages;
+                    const bool live = lane < C::GT && pg >= 0 && pg < p.n_pages;
                     const uint32_t mask = __ballot_sync(0xffffffffu, live);
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&raw_empty[rs], ((uint32_t)(gb / C::RAWST) & 1u) ^ 1u)) && !*abort_flag;
                     if (!ok) { if (lane == 0) fail(32); break; }
                     if (lane == 0) {
                         raw_mask[rs] = (int32_t)mask;
-                        tc::mbar_arrive_expect_tx(&raw_full[rs], (uint32_t)__popc(mask) * L::BYTES);
+                        tc::mbar_arrive_expect_tx(&raw_full[rs], (uint32_t)__popc(mask) * (L::BYTES / 2));
                     }
                     __syncwarp();
                     if (live) {
                         const uint32_t off = (uint32_t)tok % (uint32_t)p.page;
                         bulk_load(smem + C::OFF_RAW + rs * C::RAW_BYTES + lane * C::PITCH,
-                                  p.cache + pg * a.page_bytes +
+                                  p.cache + pg * a.page_bytes + (values ? L::VC : 0) +
                                       (item.head * (p.page / KV_TILE) + off / KV_TILE) * (int64_t)L::BYTES,
-                                  L::BYTES, &raw_full[rs]);
+                                  L::BYTES / 2, &raw_full[rs]);
                     }
-                    issued = gi + 1;
+                    issued = e + 1;
                 }
                 if (!ok)   // copies that are under way land before the CTA exits
-                    for (int gi = max(0, issued - C::RAWST); gi < issued; gi++)
-                        tc::mbar_wait(&raw_full[(wk.groups_before + gi) % C::RAWST], (uint32_t)((wk.groups_before + gi) / C::RAWST) & 1u);
+                    for (int e = max(0, issued - C::RAWST); e < issued; e++)
+                        tc::mbar_wait(&raw_full[(wk.loads_before + e) % C::RAWST], (uint32_t)((wk.loads_before + e) / C::RAWST) & 1u);
             }
         }
     }
