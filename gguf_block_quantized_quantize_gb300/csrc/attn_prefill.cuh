@@ -40,12 +40,8 @@ struct ApCfg {
     // output rounded once has 2.1e-4): for them keys are held in two parts, exactly, and scores are two products (3.0e-4;
     // 146 -> 153 us at 2048 tokens of heads of 64, 644 -> 766 us at 8192 of heads of 128).  In bf16 results it is lost.
     static constexpr int KP = QT == GGUF_F16 ? 2 : 1;
-    static constexpr int KST = D > 64 && KP == 2 ? 1 : 2, VST = D == 256 ? 1 : 2;   // as the shared memory allows
+    static constexpr int KST = D > 64 && KP == 2 ? 1 : 2, VST = 2;   // as the shared memory allows
     static constexpr int GT = BT / KV_TILE;            // cache tiles of a block; a load is their keys, or their values
-    // blocks by which keys are unpacked before values: with one V stage the values of a block wait for the product of the
-    // one before, and the next scores need not (8192 tokens of heads of 256: 2155 -> 1712 us; of 128: 644 -> 655 us, and
-    // with one K stage 766 -> 1023 us)
-    static constexpr int AHEAD = VST == 1 ? 1 : 0;
     static constexpr int RAWST = D == 64 ? 6 : 3;
     // registers of the softmax warps (a row's scores) and of the others (packed words read ahead): 256 for the two, as at
     // launch
@@ -496,9 +492,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             const int64_t it = item_of(st);
             if (it >= total) continue;
             if (!begin(wk, it)) break;
-            // ================= unpack: the keys of block j + AHEAD, then the values of block j.  The packed words of the next
-            // step are read from shared memory before the current one is computed: the matrix unit's reads fill the shared
-            // memory's bandwidth for long stretches, and a read may take many hundred cycles.  Steps are of 4 tiles.
+            // ================= unpack: the keys of a block, then its values, 4 tiles a step.  The packed words of the next step are
+            // read from shared memory before the current one is computed: the matrix unit's reads fill the shared memory's
+            // bandwidth for long stretches, and a read may take many hundred cycles.
             // Keys: warp w8 takes tile w8 of a step; lane (g, q) holds values 8 q .. of the blocks of tokens g and g + 8; odd g
             // takes the blocks in another order, so that the stores of a warp hit different banks.
             // Values: lane (tile, p, gs) holds 8 tokens (one 16-byte chunk of a row of V^T) of 4 values of half of the
@@ -604,56 +600,40 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             };
             Keys ka, kc;
             Values va, vc;
-            int load = 0, rk = 0;   // loads taken, the stage of ka's
+            int rk = 0;
             if (wk.nblk > 0) {
                 rk = raw_wait(0);
                 if (ok) load_keys(rk, 0, ka);
             }
-            for (int j = -C::AHEAD; j < wk.nblk && ok; j++) {
-                int rv = 0;
-                if (j + C::AHEAD < wk.nblk) {
-                    const int kb = wk.blocks_before + j + C::AHEAD, ks = kb % C::KST;
-                    uint8_t *sk = smem + C::OFF_K + ks * C::K_BYTES;
-                    ok = tc::mbar_wait(&k_empty[ks], ((uint32_t)(kb / C::KST) & 1u) ^ 1u);
-                    if (!ok) break;
-                    const int mask = raw_mask[rk];
-                    load++;
-                    if constexpr (STEPS == 2) {
-                        load_keys(rk, 1, kc);
-                        put_keys(sk, 0, ka);
-                    }
-                    if (j >= 0) {
-                        rv = raw_wait(load);
-                        if (!ok) break;
-                        load_values(rv, j, 0, va);
-                    }
-                    if constexpr (STEPS == 2) put_keys(sk, 1, kc);
-                    else put_keys(sk, 0, ka);
-                    arrive(&raw_empty[rk]);
-                    if (w8 == 0 && lane == 0) blk_mask[kb & 7] = mask;
-                    tc::fence_proxy_async_smem();
-                    arrive(&k_full[ks]);
-                } else {
-                    rv = raw_wait(load);
-                    if (!ok) break;
-                    load_values(rv, j, 0, va);
+            for (int j = 0; j < wk.nblk && ok; j++) {
+                const int kb = wk.blocks_before + j, ks = kb % C::KST, vs = kb % C::VST;
+                uint8_t *sk = smem + C::OFF_K + ks * C::K_BYTES, *sv = smem + C::OFF_V + vs * C::V_BYTES;
+                ok = tc::mbar_wait(&k_empty[ks], ((uint32_t)(kb / C::KST) & 1u) ^ 1u);
+                if (!ok) break;
+                const int mask = raw_mask[rk];
+                if constexpr (STEPS == 2) {
+                    load_keys(rk, 1, kc);
+                    put_keys(sk, 0, ka);
                 }
-                if (j >= 0) {
-                    const int kb = wk.blocks_before + j, vs = kb % C::VST;
-                    uint8_t *sv = smem + C::OFF_V + vs * C::V_BYTES;
-                    load++;
-                    if constexpr (STEPS == 2) load_values(rv, j, 1, vc);
-                    ok = tc::mbar_wait(&v_empty[vs], ((uint32_t)(kb / C::VST) & 1u) ^ 1u);
-                    if (!ok) break;
-                    put_values(sv, 0, va);
-                    if constexpr (STEPS == 2) put_values(sv, 1, vc);
-                    arrive(&raw_empty[rv]);
-                    tc::fence_proxy_async_smem();
-                    arrive(&v_full[vs]);
-                    if (*abort_flag) break;
-                }
-                if (j + 1 + C::AHEAD < wk.nblk) {
-                    rk = raw_wait(load);
+                const int rv = raw_wait(2 * j + 1);
+                if (!ok) break;
+                load_values(rv, j, 0, va);
+                put_keys(sk, STEPS - 1, STEPS == 2 ? kc : ka);
+                arrive(&raw_empty[rk]);
+                if (w8 == 0 && lane == 0) blk_mask[kb & 7] = mask;
+                tc::fence_proxy_async_smem();
+                arrive(&k_full[ks]);
+                if constexpr (STEPS == 2) load_values(rv, j, 1, vc);
+                ok = tc::mbar_wait(&v_empty[vs], ((uint32_t)(kb / C::VST) & 1u) ^ 1u);
+                if (!ok) break;
+                put_values(sv, 0, va);
+                if constexpr (STEPS == 2) put_values(sv, 1, vc);
+                arrive(&raw_empty[rv]);
+                tc::fence_proxy_async_smem();
+                arrive(&v_full[vs]);
+                if (*abort_flag) break;
+                if (j + 1 < wk.nblk) {
+                    rk = raw_wait(2 * j + 2);
                     if (ok) load_keys(rk, 0, ka);
                 }
             }
@@ -738,15 +718,14 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                 }
                 __syncwarp();
             } else if (warp == AP_LOAD) {
-                // ================= loads, in the order of the unpacking: the keys or the values of a block, lane i tile i
+                // ================= loads: the keys of a block, its values, the next one's keys, ..; lane i tile i
                 bool ok = true;
                 const int nloads = 2 * wk.nblk;
                 int issued = 0;
                 for (int e = 0; e < nloads && ok; e++) {
                     const int gb = wk.loads_before + e, rs = gb % C::RAWST;
-                    // K0 V0 K1 V1 .. or, with keys a block ahead, K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1)
-                    const bool values = C::AHEAD == 0 ? (e & 1) != 0 : (e > 0 && !(e & 1)) || e == nloads - 1;
-                    const int j = C::AHEAD == 0 ? e / 2 : values ? (e - 1) / 2 : (e + 1) / 2;
+                    const bool values = e & 1;
+                    const int j = e / 2;
                     const int i = (CUT ? item.base : 0) + j * C::GT + (lane & (C::GT - 1));
                     int32_t pg = -1;
                     int tok = 0;
