@@ -43,7 +43,9 @@ static AttnPlan attn_plan(const Attn &p, int64_t d) {
     // 16 rows at once where a unit has more than 8, so that its cache bytes are read and unpacked once
     x.nt = (x.prefill ? x.few : most) > 8 && (G > 8 || !x.prefill) && p.qt != GGUF_F32 ? 2 : 1;
     // The device cuts the tokens of its row blocks into pieces where they would leave SMs idle; not where the tokens
-    // alone make enough row blocks, and pieces of 4 blocks at least.
+    // alone make enough row blocks, and pieces of 4 blocks at least
+    // (5 requests of up to 66 tokens, 32 heads of 256 after 3032 tokens: 141 us uncut, 106 us so; 8192 tokens: 664 us with
+    // what cutting costs the kernel, 644 us without).
     const int64_t span = p.window > 0 ? std::min(p.width * p.page, p.window + p.sinks + p.max_q) : p.width * p.page;
     const bool idle = x.prefill && (p.n_tokens - std::min(p.R, p.n_tokens)) * p.h / 128 <= sms / 2;
     x.max_splits = idle ? (int32_t)std::max<int64_t>(1, std::min<int64_t>(span / (d == 256 ? 256 : 512), 16)) : 1;

@@ -28,6 +28,13 @@
 // 2^9), which fp16 holds exactly (bf16 values below 2^-15 of the row's largest
 // lose bits).  fp32 queries use three bf16 parts of q, the exact c - 8, and
 // high and low fp16 parts of p and v, for fp32 accuracy.
+//
+// Measured, with 8 rows a unit: 32 requests of 8192 tokens (32 query heads, 8 KV
+// heads of 128) 52.9 us, 3.6 TB/s; 4 of 131072 (16 heads, 2 of 256) 60.4 us, 3.6
+// TB/s; 64 with a window of 4096 (32, 8 of 64) 49.5 us, 3.1 TB/s; 1 of 333 (fp32)
+// 11.9 us.  What bounds it now: instructions (16 bytes unpacked, two products and
+// the softmax by twelve warps a SM), then a unit's start and join (3500 cycles)
+// and the second launch (about 4 us).
 #pragma once
 
 #include <algorithm>

@@ -12,7 +12,8 @@
 // another CTA may be writing.
 //
 // Bound: latency (launch, one scan, two dependent loads); the bytes are 12 per
-// token.
+// token.  Measured in a captured graph: 8 decoding requests 3.8 us, 2048
+// requests of 131072 new tokens 7.8 us (1.6 MB).
 #include <algorithm>
 
 #include "common.cuh"

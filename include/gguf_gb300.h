@@ -630,8 +630,8 @@ gguf_status gguf_kv_get_rows(const void *cache, int64_t n_pages, int64_t page_si
  *                chooses the kernels.  0 < max_q_len.
  *   ws         : gguf_paged_attention_ws_size(args) bytes, 16-byte aligned.
  * Softmax statistics and sums are fp32.  16-bit queries take fp16 probabilities and
- * values into the matrix instructions, and in long prompts fp16 keys (2e-4 and 4e-4
- * of a row's norm, beside the rounding of the output); fp32 queries split operands
+ * values into the matrix instructions (2e-4 of a row's norm, beside the rounding of the
+ * output), and in long prompts of bf16 queries fp16 keys (4e-4); fp32 queries split operands
  * (about 1e-6; GGUF_ERR_SHAPE where max_q_len x heads / 8 x table tokens / 16 passes
  * 4e9).  Probabilities below 2^-34 of a row's largest count as zero.  Same bits on
  * every run.  Timeouts of the kernels' waits reach the caller as described at
