@@ -42,19 +42,22 @@ static AttnPlan attn_plan(const Attn &p, int64_t d) {
     x.decode = !x.prefill || G <= x.few;   // some request may have as few rows
     // 16 rows at once where a unit has more than 8, so that its cache bytes are read and unpacked once
     x.nt = (x.prefill ? x.few : most) > 8 && (G > 8 || !x.prefill) && p.qt != GGUF_F32 ? 2 : 1;
-    // The device cuts the tokens of its row blocks into pieces where they would leave SMs idle; not where the tokens
-    // alone make enough row blocks, and pieces of 4 blocks at least
-    // (5 requests of up to 66 tokens, 32 heads of 256 after 3032 tokens: 141 us uncut, 106 us so; 8192 tokens: 664 us with
-    // what cutting costs the kernel, 644 us without).
+    // The device cuts the tokens of row blocks into pieces, of 4 blocks at least, where SMs would stand idle: of all of
+    // them where there are fewer than SMs (5 requests of up to 66 tokens, 32 heads of 256 after 3032 tokens: 141 us uncut,
+    // 106 us so), of those after the last full round where few rounds end in a short one and what was cached before
+    // makes them long (4 chunks of 512 tokens after 3500, 24 heads of 128: 190 us uncut, 169 us so).  Elsewhere it
+    // only costs (8192 tokens: 664 us with what cutting costs the kernel, 644 us without).
     const int64_t span = p.window > 0 ? std::min(p.width * p.page, p.window + p.sinks + p.max_q) : p.width * p.page;
-    const bool idle = x.prefill && (p.n_tokens - std::min(p.R, p.n_tokens)) * p.h / 128 <= sms / 2;
-    x.max_splits = idle ? (int32_t)std::max<int64_t>(1, std::min<int64_t>(span / (d == 256 ? 256 : 512), 16)) : 1;
+    const int64_t rows = d == 256 ? 128 : 256, heads_rows = (p.n_tokens - std::min(p.R, p.n_tokens)) * p.h;
+    const int64_t rounds = heads_rows / rows / sms, rest = heads_rows / rows % sms;
+    const bool idle = heads_rows / 128 <= sms / 2 || (rounds >= 1 && rounds < 4 && rest <= sms / 2 && span >= 4 * p.max_q);
+    x.max_splits = x.prefill && idle ? (int32_t)std::max<int64_t>(1, std::min<int64_t>(span / (d == 256 ? 256 : 512), 16)) : 1;
     auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
     // two partial results of up to 16 rows (8 rows of 256 values) per CTA, and its meta data
     x.meta = up((size_t)x.ctas * 2 * (d == 256 ? 8 : 16) * (d + 2) * 4);
     x.base = up(x.meta + (size_t)x.ctas * sizeof(AdMeta));
-    x.pieces = x.max_splits > 1 ? up(x.base + (size_t)(p.R + 2) * 4) : x.base;   // a piece per SM at most, of 128 rows
-    x.bytes = x.max_splits > 1 ? x.pieces + (size_t)x.ctas * 128 * (d + 2) * 4 : x.base;
+    x.pieces = x.max_splits > 1 ? up(x.base + (size_t)(p.R + 3) * 4) : x.base;   // a piece per SM at most
+    x.bytes = x.max_splits > 1 ? x.pieces + (size_t)x.ctas * rows * (d + 2) * 4 : x.base;
     return x;
 }
 

@@ -79,7 +79,7 @@ struct AdShape {
     int32_t tpp, tpp_shift;       // tiles per page, likewise
     int64_t page_bytes;
     int32_t max_splits;           // prefill: the pieces that a row block's tokens may be cut into at most (1: no join),
-    int32_t *item_base;           // with the row blocks before each request, their rows and the pieces,
+    int32_t *item_base;           // with the row blocks before each request, their rows, the pieces and the first that is cut,
     float *pieces;                // and the partial results, [row block][piece][row][max, sum, D values]
     int32_t whole;                // each CTA takes one whole unit (few short ones), and nothing is left to join
     float *part;                  // CTA-level partial results, two slots per CTA

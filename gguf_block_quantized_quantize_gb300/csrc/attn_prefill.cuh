@@ -72,7 +72,7 @@ struct ApItem {
     int tok0;                     // row0 / G
     int nt, n_sink, w_tile;       // the tiles that the rows see (see AdReq): the piece takes those from base to nt
     int base;
-    int64_t part;                 // its place among the partial results, where a row block's tiles are cut
+    int part;                     // its place among the partial results where the row block's tiles are cut, else -1
 };
 
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     __shared__ uint32_t tmem_slot;
     __shared__ int32_t abort_word;
     __shared__ ApItem item;
-    __shared__ int32_t part[2][AP_THREADS / 32], cut_rows, cut_pieces;
+    __shared__ int32_t part[2][AP_THREADS / 32], cut_rows, cut_pieces, cut_from;
     __shared__ int32_t chunk_end[AP_THREADS];   // at most (tokens x heads / 128) items: 31 bits
     volatile int32_t *abort_flag = &abort_word;
     const Attn &p = a.p;
@@ -165,8 +165,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // Work of all requests: thread t counts requests [t * per, (t + 1) * per), in row blocks of ROWS rows, and of 128.
-    // The larger ones unpack a key for twice the rows; the smaller ones, and row blocks whose tokens are cut into pieces
-    // (CUT; of 4 blocks at least, joined by a second launch), are for calls that would leave SMs idle.
+    // The larger ones unpack a key for twice the rows; the smaller ones are for calls that would leave SMs idle, as are
+    // row blocks whose tokens are cut into pieces (CUT; of 4 blocks at least, joined by a second launch).
     const int R = (int)p.R, per = (R + AP_THREADS - 1) / AP_THREADS;
     {
         int item_rows = ROWS, splits = 1;
@@ -197,21 +197,24 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             incl = incl128;
             mine = mine128;
             all = all128;
-            if (CUT) splits = max(1, min(a.max_splits, (int)gridDim.x / max(all, 1)));
         }
+        // the row blocks after the last full round are cut where that gives every CTA at most one piece
+        const int rest = all % (int)gridDim.x;
+        if (CUT && rest > 0) splits = max(1, min(a.max_splits, (int)gridDim.x / rest));
+        const int from = splits > 1 ? all - rest : all;
         chunk_end[tid] = incl;
-        if (tid == 0) { cut_rows = item_rows; if (CUT) cut_pieces = splits; }
+        if (tid == 0) { cut_rows = item_rows; if (CUT) { cut_pieces = splits; cut_from = from; } }
         if (CUT && blockIdx.x == 0) {   // for the join: the items before each request, and the cut
             int before = incl - mine;
             for (int r = tid * per; r < min(R, (tid + 1) * per); r++) {
                 a.item_base[r] = before;
                 before += ap_items(a, ad_request(a, r), item_rows);
             }
-            if (tid == 0) { a.item_base[R] = item_rows; a.item_base[R + 1] = splits; }
+            if (tid == 0) { a.item_base[R] = item_rows; a.item_base[R + 1] = splits; a.item_base[R + 2] = from; }
         }
         __syncthreads();
     }
-    const int64_t total = (int64_t)chunk_end[AP_THREADS - 1] * (CUT ? cut_pieces : 1);
+    const int64_t total = CUT ? cut_from + (int64_t)(chunk_end[AP_THREADS - 1] - cut_from) * cut_pieces : chunk_end[AP_THREADS - 1];
     const uint32_t tmem = tmem_slot;
     auto fail = [&](int code) {
         *abort_flag = 1;
@@ -245,7 +248,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         if (*abort_flag) return false;
         if (tid == 0) {
             const int item_rows = cut_rows, splits = CUT ? cut_pieces : 1;
-            const int it = CUT ? (int)piece / splits : (int)piece, cut = (int)piece - it * splits;
+            const int place = CUT ? (int)piece - cut_from : -1;   // among the pieces of the cut ones
+            const int it = place >= 0 ? cut_from + place / splits : (int)piece, cut = place % splits;
             int lo = -1, hi = AP_THREADS - 1;
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
@@ -282,10 +286,13 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             }
             // the blocks of the row block, shared out over the pieces
             if (CUT) {
-                const int64_t blocks = (w.nt + BT / KV_TILE - 1) / (BT / KV_TILE);
-                w.base = (int)(blocks * cut / splits) * (BT / KV_TILE);
-                w.nt = min(w.nt, (int)(blocks * (cut + 1) / splits) * (BT / KV_TILE));
-                w.part = piece;
+                w.base = 0;
+                w.part = place;
+                if (place >= 0) {
+                    const int64_t blocks = (w.nt + BT / KV_TILE - 1) / (BT / KV_TILE);
+                    w.base = (int)(blocks * cut / splits) * (BT / KV_TILE);
+                    w.nt = min(w.nt, (int)(blocks * (cut + 1) / splits) * (BT / KV_TILE));
+                }
             }
             item = w;
         }
@@ -465,8 +472,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
 #pragma unroll
                             for (int i = 0; i < 32; i++) rr[i] = 0;
                         }
-                        if (CUT && there && cut_pieces > 1) {
-                            float *to = a.pieces + (item.part * cut_rows + row) * (D + 2);
+                        if (CUT && there && item.part >= 0) {
+                            float *to = a.pieces + ((int64_t)item.part * cut_rows + row) * (D + 2);
                             float2 *dst = reinterpret_cast<float2 *>(to + 2 + 32 * c);
 #pragma unroll
                             for (int i = 0; i < 16; i++) dst[i] = make_float2(__uint_as_float(rr[2 * i]), __uint_as_float(rr[2 * i + 1]));
@@ -792,12 +799,13 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const AdShape a)
         else hi = mid;
         r = lo;
     }
-    const int item_rows = a.item_base[p.R], splits = a.item_base[p.R + 1];
+    const int item_rows = a.item_base[p.R], splits = a.item_base[p.R + 1], first_cut = a.item_base[p.R + 2];
     const AdReq q = ad_request(a, r);
     if (splits == 1 || t - q.rows0 >= q.q) return;   // nothing was cut; not of the prefill kernel's, or past the rows that are computed
     const int kh = head / a.G, row = (int)(t - q.rows0) * a.G + head - kh * a.G;
     const int rb = row / item_rows, nrb = (q.q * a.G + item_rows - 1) / item_rows;
-    const int64_t item = a.item_base[r] + (int64_t)(nrb - 1 - rb) * a.hk + kh;
+    const int64_t item = a.item_base[r] + (int64_t)(nrb - 1 - rb) * a.hk + kh - first_cut;
+    if (item < 0) return;   // not cut
     const float *from = a.pieces + (item * splits * item_rows + row - rb * item_rows) * (D + 2);
     const int64_t step = (int64_t)item_rows * (D + 2);
     float mx = -INFINITY, l = 0.0f;

@@ -485,3 +485,19 @@ def test_pieces_of_a_long_chunk(q_lens, kv_lens, h, hk, d, typ, window, sinks):
     out = run()
     check_attn(out, attn_ref(q, k, v, q_lens, kv_lens, d ** -0.5, window, sinks), typ)
     assert torch.equal(out, run())
+
+
+@pytest.mark.parametrize("q, n, most, h, hk, d, typ, window, sinks", [
+    (64, 20, 2100, 32, 8, 128, "bf16", 0, 0),
+    (32, 40, 1300, 16, 2, 256, "f16", 0, 0),
+    (61, 21, 2900, 32, 8, 64, "f16", 1500, 4),
+])
+def test_pieces_after_a_full_round(q, n, most, h, hk, d, typ, window, sinks):
+    """A few row blocks more than SMs: the last ones are cut, the others are not."""
+    q_lens = [q] * n
+    kv_lens = [q - 5 if i == n - 2 else max(q, most * (i + 1) // n) for i in range(n)]   # one with fewer than its queries
+    qs, cache, table, start, kv_len, k, v = attn_setup(q_lens, kv_lens, h, hk, d, 16, typ)
+    run = lambda: g.gguf_paged_attention(qs, cache, table, start, kv_len, hk, 16, q, d ** -0.5, window=window, sinks=sinks)   # noqa: E731
+    out = run()
+    check_attn(out, attn_ref(qs, k, v, q_lens, kv_lens, d ** -0.5, window, sinks), typ)
+    assert torch.equal(out, run())
