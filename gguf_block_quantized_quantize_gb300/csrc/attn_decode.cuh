@@ -32,9 +32,9 @@
 // Measured, with 8 rows a unit: 32 requests of 8192 tokens (32 query heads, 8 KV
 // heads of 128) 52.9 us, 3.6 TB/s; 4 of 131072 (16 heads, 2 of 256) 60.4 us, 3.6
 // TB/s; 64 with a window of 4096 (32, 8 of 64) 49.5 us, 3.1 TB/s; 1 of 333 (fp32)
-// 11.9 us.  What bounds it now: instructions (16 bytes unpacked, two products and
-// the softmax by twelve warps a SM), then a unit's start and join (3500 cycles)
-// and the second launch (about 4 us).
+// 11.9 us.  What bounds it now: instructions (59 % of the issue slots, by the three
+// computing warps a scheduler that the registers allow; DRAM at 48 %), then a
+// unit's start and join (3500 cycles) and the second launch (about 4 us).
 #pragma once
 
 #include <algorithm>

@@ -27,10 +27,10 @@
 // Measured: a prompt of 8192 tokens, 32 query heads, 8 KV heads of 128, bf16: 644
 // us, 0.85 PFLOP/s (0.45 of the matrix rate); with heads of 256 1690 us (0.34);
 // 2 x 4093 tokens with a window of 1000, heads of 64, fp16: 154 us (0.27 PFLOP/s).
-// What bounds it now: per block and two row tiles the matrix unit works for 2600
-// of 4800 cycles; the rest is the chain scores, softmax, P, product of the S
-// buffer that the next scores wait for.  A larger block or a third S buffer
-// finds no room in TMEM.  Heads of 64 take nearly as long a block (4300 cycles).
+// What bounds it now: no unit (tensor pipe 37 % active, issue slots 45 % used at
+// heads of 128) but the chain scores, softmax, P, product of an S buffer, which
+// the next scores into it wait for: 4800 cycles per block and two row tiles, and
+// 4300 with heads of 64.  A third S buffer finds no room in TMEM.
 #pragma once
 
 #include "attn_decode.cuh"
