@@ -258,9 +258,9 @@ __global__ void __launch_bounds__(QR_THREADS, 4) qk_norm_rope_kernel(const QkRop
     uint8_t *tile0 = p.cache != nullptr ? slot_tile<D>(p, slot, tok) : nullptr;
     if (p.cache != nullptr && slot >= 0 && tile0 == nullptr && p.status != nullptr && g0 == 0 && l == 0) atomicAdd(p.status, 1);
     const int64_t head_step = p.page / KV_TILE * kv_tile_bytes(D);
-    float wv[8];
-    bool w_of_q = p.qw != nullptr;
-    if (w_of_q) ld8<GGUF_F32, true>(p.qw, 8 * l, wv);
+    float wv[8];   // the lane's weights: the queries' (where they have some) until the first key row
+    bool w_of_k = false;
+    if (p.qw != nullptr) ld8<GGUF_F32, true>(p.qw, 8 * l, wv);
     for (int r0 = g0; r0 < rows; r0 += QR_ROWS * groups) {
 #pragma unroll
         for (int i = 0; i < QR_ROWS; i++) {
@@ -272,9 +272,9 @@ __global__ void __launch_bounds__(QR_THREADS, 4) qk_norm_rope_kernel(const QkRop
             raw[i].floats(v);
             const float *w = is_q ? p.qw : p.kw;
             if (w != nullptr) {
-                if (is_q != w_of_q) {   // the first key row: its weights
+                if (!is_q && !w_of_k) {   // (rows come queries first)
                     ld8<GGUF_F32, true>(w, 8 * l, wv);
-                    w_of_q = is_q;
+                    w_of_k = true;
                 }
                 float ss = 0.0f;
 #pragma unroll
