@@ -100,8 +100,10 @@ __device__ __forceinline__ AdReq ad_request(const AdShape &a, int r) {
     const Attn &p = a.p;
     const int G = a.G;
     o.rows0 = p.q_start[r];
-    const int64_t q = min((int64_t)p.q_start[r + 1] - o.rows0, p.max_q);
-    const bool mine = o.rows0 >= 0 && q > 0 && q * G > a.min_rows && q * G <= a.max_rows && o.rows0 + q <= p.n_tokens;
+    // of a request that is longer than max_q, or reaches past the rows of q, the first queries (their positions follow from
+    // its whole length)
+    const int64_t q = min(min((int64_t)p.q_start[r + 1] - o.rows0, p.max_q), p.n_tokens - o.rows0);
+    const bool mine = o.rows0 >= 0 && q > 0 && q * G > a.min_rows && q * G <= a.max_rows;
     o.q = mine ? (int32_t)q : 0;
     o.nt = o.n_sink = o.w_tile = 0;
     const int32_t kv = p.kv_len[r];

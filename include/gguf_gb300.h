@@ -624,7 +624,9 @@ gguf_status gguf_kv_get_rows(const void *cache, int64_t n_pages, int64_t page_si
  *                h / (n_heads / n_kv_heads).
  *   block_table: [n_requests][ld_table] int32, width columns used.  A page number
  *                outside the cache hides its tokens, and dev_status counts it.
- *   q_start    : [n_requests + 1] int32, non-decreasing; kv_len: [n_requests].
+ *   q_start    : [n_requests + 1] int32, non-decreasing; kv_len: [n_requests].  It may
+ *                reach past n_tokens (a plan of more tokens than its arrays hold): the
+ *                queries that q holds are computed, at their positions in the whole step.
  *   max_q_len  : at least the longest request's queries (of a request with more, only
  *                the first max_q_len are computed): with the other host arguments it
  *                chooses the kernels.  0 < max_q_len.

@@ -50,3 +50,55 @@ def test_norm_of_one_side(orc, typ, side, t, h, hk, d, neox):
         ref = rope_ref(k, kw, cs, d, neox, eps)
         step = (ref.unflatten(-1, (-1, 32)).abs().amax(-1, keepdim=True) / 8).expand(t, hk, d // 32, 32).flatten(-2)
         assert bool(((gk.double().cpu() - ref).abs() <= step * 1.01 + 1e-6).all())
+
+
+# ------------------------------------------------------------------ more tokens planned than the call holds
+
+@pytest.mark.parametrize("q_lens, kv_lens, held, h, hk, d, typ, window", [
+    ([3, 5, 4], [40, 9, 77], 10, 8, 2, 128, "bf16", 0),       # the last request is cut
+    ([3, 5, 4], [40, 9, 77], 6, 8, 2, 64, "f16", 20),         # the second is, the third is left out
+    ([3, 5, 4], [40, 9, 77], 10, 4, 2, 128, "f32", 0),
+    ([70, 130], [100, 400], 150, 4, 2, 64, "bf16", 0),        # on the prompt kernel
+    ([70, 130], [100, 400], 73, 8, 1, 128, "f16", 0),         # cut down to few rows
+    ([130], [150], 129, 4, 2, 256, "bf16", 50),
+    ([40], [3000], 33, 4, 1, 128, "bf16", 0),                 # tokens in pieces
+    ([1] * 9, [30] * 9, 4, 4, 2, 128, "bf16", 0)])
+def test_step_with_more_tokens_than_the_call(q_lens, kv_lens, held, h, hk, d, typ, window):
+    """q_start reaches past the rows of q: the rows that are there are computed as in the whole step."""
+    q, cache, table, start, kv_len, k, v = attn_setup(q_lens, kv_lens, h, hk, d, 16, typ)
+    wide = torch.full((held + 3, h, d), 9.0, dtype=q.dtype, device=DEV)
+    g.gguf_paged_attention(q[:held], cache, table, start, kv_len, hk, 16, max(q_lens), d ** -0.5, window=window, out=wide[:held])
+    refs = attn_ref(q, k, v, q_lens, kv_lens, d ** -0.5, window, 0)
+    check_attn(wide[:held], [x[:held] for x in refs], typ)
+    assert bool((wide[held:] == 9).all())
+
+
+@pytest.mark.parametrize("q_lens, kv_lens, most, h, typ", [
+    ([3, 5, 1], [40, 9, 77], 2, 4, "bf16"), ([3, 5, 1], [40, 9, 77], 2, 4, "f32"), ([70, 130], [100, 400], 60, 8, "bf16"),
+    ([70, 130], [100, 2400], 100, 2, "f16")])
+def test_requests_longer_than_max_q_len(q_lens, kv_lens, most, h, typ):
+    """Of a longer request the first max_q_len queries are computed, the others are not written."""
+    hk, d = 2, 64
+    q, cache, table, start, kv_len, k, v = attn_setup(q_lens, kv_lens, h, hk, d, 16, typ)
+    out = torch.full_like(q, 9.0)
+    g.gguf_paged_attention(q, cache, table, start, kv_len, hk, 16, most, d ** -0.5, out=out)
+    refs = attn_ref(q, k, v, q_lens, kv_lens, d ** -0.5, 0, 0)
+    done = torch.cat([torch.arange(n) < most for n in q_lens])
+    check_attn(out[done], [x[done] for x in refs], typ)
+    assert bool((out[~done] == 9).all())
+
+
+def test_attention_after_an_overfull_plan():
+    """A plan of more tokens than its arrays hold, the store and the attention over what is there."""
+    torch.manual_seed(5)
+    h, hk, d, page, lens, held = 4, 2, 64, 16, [30, 45], 50
+    cache = torch.full((8, g.gguf_kv_page_bytes(d, hk, page)), 0xFF, dtype=torch.uint8, device=DEV)
+    table = torch.full((2, 4), -1, dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    start, kv_len, pos, slots, _ = g.gguf_kv_plan(I32([0, 0]), I32(lens), I32(list(range(8))), table, page, held, dev_status=status)
+    assert status.item() == sum(lens) - held
+    q, k, v = (torch.randn(held, n, d, device=DEV).to(torch.bfloat16) for n in (h, hk, hk))
+    q = g.gguf_qk_norm_rope(q, k, v, None, None, 0.0, pos, None, cache=cache, slots=slots, page_size=page)
+    out = g.gguf_paged_attention(q, cache, table, start, kv_len, hk, page, max(lens), d ** -0.5, out=torch.full_like(q, 9.0))
+    kk, vv = g.gguf_kv_get_rows(cache, slots, hk, d, page)
+    check_attn(out, attn_ref(q, kk, vv, [30, 20], [30, 20], d ** -0.5, 0, 0), "bf16")
