@@ -131,10 +131,13 @@ gguf_status gguf_kv_get_rows(const void *cache, int64_t n_pages, int64_t page_si
     return launched(launch_kv_get_rows(p, head_dim, ot, at(k, 16) && at(v, 16), (cudaStream_t)stream), "kv_get_rows");
 }
 
+// Positions are below 2^31: a window as wide as that hides nothing, and first tokens past it are all tokens.  No request has
+// more queries than the call.  With these bounds set here, sums of the three fit in 64 bits.
 static Attn attn_of(const gguf_attn_args *a) {
+    constexpr int64_t FAR = (int64_t)1 << 31;
     return Attn{a->q, a->qt, a->n_tokens, a->ldq, (const uint8_t *)a->cache, a->n_pages, a->page_size, a->block_table,
-                a->ld_table, a->width, a->q_start, a->kv_len, a->n_requests, a->max_q_len, a->n_heads, a->n_kv_heads,
-                a->scale, a->window, a->sinks, a->out, a->ldo, a->dev_status};
+                a->ld_table, a->width, a->q_start, a->kv_len, a->n_requests, std::min(a->max_q_len, a->n_tokens), a->n_heads,
+                a->n_kv_heads, a->scale, a->window < FAR ? a->window : 0, std::min(a->sinks, FAR), a->out, a->ldo, a->dev_status};
 }
 
 // the checks that the workspace size depends on

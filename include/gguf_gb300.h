@@ -629,7 +629,8 @@ gguf_status gguf_kv_get_rows(const void *cache, int64_t n_pages, int64_t page_si
  *                queries that q holds are computed, at their positions in the whole step.
  *   max_q_len  : at least the longest request's queries (of a request with more, only
  *                the first max_q_len are computed): with the other host arguments it
- *                chooses the kernels.  0 < max_q_len.
+ *                chooses the kernels.  0 < max_q_len; n_tokens serves where it is not known.
+ *   window, sinks : any value >= 0; what passes every position hides nothing.
  *   ws         : gguf_paged_attention_ws_size(args) bytes, 16-byte aligned.
  * Softmax statistics and sums are fp32.  16-bit queries take fp16 probabilities and
  * values into the matrix instructions (2e-4 of a row's norm, beside the rounding of the

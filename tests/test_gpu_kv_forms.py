@@ -102,3 +102,22 @@ def test_attention_after_an_overfull_plan():
     out = g.gguf_paged_attention(q, cache, table, start, kv_len, hk, page, max(lens), d ** -0.5, out=torch.full_like(q, 9.0))
     kk, vv = g.gguf_kv_get_rows(cache, slots, hk, d, page)
     check_attn(out, attn_ref(q, kk, vv, [30, 20], [30, 20], d ** -0.5, 0, 0), "bf16")
+
+
+# ------------------------------------------------------------------ arguments without a bound
+
+FAR = 2 ** 63 - 1
+
+
+@pytest.mark.parametrize("q_lens, kv_lens, h, hk, d, typ", [
+    ([1, 1], [700, 33], 8, 2, 128, "bf16"), ([2, 3, 1], [4, 3000, 0], 4, 2, 64, "f32"), ([5], [2], 12, 1, 128, "f16"),
+    ([70, 1], [150, 90], 4, 2, 64, "bf16"), ([40], [3000], 4, 1, 128, "f16"), ([90], [40], 2, 1, 256, "bf16")])
+@pytest.mark.parametrize("window, sinks, most", [
+    (FAR, 0, 0), (FAR, FAR, 0), (2 ** 31, 3, 0), (2 ** 31 - 1, 3, 0), (20, FAR, 0), (20, FAR - 14, FAR), (20, 2 ** 31, 0),
+    (0, 0, FAR), (0, 5, 2 ** 31), (20, 4, FAR)])
+def test_arguments_without_a_bound(q_lens, kv_lens, h, hk, d, typ, window, sinks, most):
+    """A window or first tokens beyond any length hide nothing; max_q_len may be larger than any request."""
+    q, cache, table, start, kv_len, k, v = attn_setup(q_lens, kv_lens, h, hk, d, 16, typ, spare_cols=1)
+    out = g.gguf_paged_attention(q, cache, table, start, kv_len, hk, 16, most or max(q_lens), d ** -0.5, window=window, sinks=sinks)
+    limit = 10 ** 6   # past every length here
+    check_attn(out, attn_ref(q, k, v, q_lens, kv_lens, d ** -0.5, min(window, limit), min(sinks, limit)), typ)
