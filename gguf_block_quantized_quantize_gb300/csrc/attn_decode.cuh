@@ -121,6 +121,11 @@ __device__ __forceinline__ AdReq ad_request(const AdShape &a, int r) {
     }
     return o;
 }
+// the tile of the request's i-th one, and whether it is the first of its page among them (a page that is not there counts once)
+__device__ __forceinline__ int ad_tile(const AdReq &q, int i) { return i < q.n_sink ? i : q.w_tile + i - q.n_sink; }
+__device__ __forceinline__ bool ad_starts_page(const AdShape &a, const AdReq &q, int i) {
+    return i == 0 || ad_tile(q, i) / a.tpp != ad_tile(q, i - 1) / a.tpp;
+}
 // its units: groups of rg query rows x KV heads
 __device__ __forceinline__ int64_t ad_units(const AdShape &a, const AdReq &q, int rg) {
     return (int64_t)((q.q * a.G + rg - 1) / rg) * a.hk;
@@ -394,7 +399,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             }
             __syncwarp();
             const int cnt = min(TP, unit), i = feed.tile + max(min(l8, cnt - 1), 0);
-            const int at = i < feed.q.n_sink ? i : feed.q.w_tile + i - feed.q.n_sink;   // tile of the request
+            const int at = ad_tile(feed.q, i);
             const int page_at = shift >= 0 ? at >> shift : (int)((uint32_t)at / tpp), in_page = at - page_at * (int)tpp;
             const int first = __shfl_sync(0xffffffffu, page_at, lane & 24);
             const int32_t *row = p.table + feed.r * p.ld;
@@ -418,8 +423,9 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                 const uint32_t none = ~have & ((1u << cnt) - 1);
                 absent[who][stage] = none;
                 tc::mbar_arrive_expect_tx(&full[who][stage], (uint32_t)__popc(have) * L::BYTES);
-                if (none && p.status != nullptr) atomicAdd(p.status, __popc(none));
             }
+            // counted by the request's first unit
+            if (go && l8 < cnt && !ok && feed.u == 0 && p.status != nullptr && ad_starts_page(a, feed.q, i)) atomicAdd(p.status, 1);
             __syncwarp();
             if (ok)
                 bulk_load(smem + who * C::RING + stage * C::STEP + l8 * L::BYTES,

@@ -128,6 +128,16 @@ __device__ __forceinline__ int ap_items(const AdShape &a, const AdReq &q, int ro
     return (int)((q.q * (int64_t)a.G + rows - 1) / rows) * a.hk;
 }
 
+// whether `tile` is the first of its page that the request's queries see, and no row block before this one sees it
+__device__ __forceinline__ bool ap_first_sight(const AdShape &a, const ApItem &w, int tile) {
+    const AdReq q = ad_request(a, w.r);
+    if (w.row0 > 0) {
+        const int before = q.pos0 + (w.row0 - 1) / a.G;   // the position of the row before
+        if (before >= 0 && tile <= before / KV_TILE) return false;
+    }
+    return ad_starts_page(a, q, tile < q.n_sink ? tile : tile - q.w_tile + q.n_sink);
+}
+
 template <int D, int QT, bool CUT>
 __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdShape a) {
     using C = ApCfg<D, QT>;
@@ -749,7 +759,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                         tok = token_of(i);
                         const uint32_t pi = (uint32_t)tok / (uint32_t)p.page;
                         pg = pi < p.width ? p.table[item.r * p.ld + pi] : -1;
-                        if (lane < C::GT && !values && (pg < 0 || pg >= p.n_pages) && p.status != nullptr) atomicAdd(p.status, 1);
+                        if (lane < C::GT && !values && item.head == 0 && (pg < 0 || pg >= p.n_pages) && p.status != nullptr &&
+                            ap_first_sight(a, item, tok / KV_TILE))
+                            atomicAdd(p.status, 1);
                     }
                     const bool live = lane < C::GT && pg >= 0 && pg < p.n_pages;
                     const uint32_t mask = __ballot_sync(0xffffffffu, live);

@@ -623,7 +623,9 @@ gguf_status gguf_kv_get_rows(const void *cache, int64_t n_pages, int64_t page_si
  *   n_heads    : a multiple of n_kv_heads; query head h reads KV head
  *                h / (n_heads / n_kv_heads).
  *   block_table: [n_requests][ld_table] int32, width columns used.  A page number
- *                outside the cache hides its tokens, and dev_status counts it.
+ *                outside the cache, or one past the table, hides its tokens.
+ *   dev_status : + such pages, each once per request whose queries would see a
+ *                token of it.
  *   q_start    : [n_requests + 1] int32, non-decreasing; kv_len: [n_requests].  It may
  *                reach past n_tokens (a plan of more tokens than its arrays hold): the
  *                queries that q holds are computed, at their positions in the whole step.

@@ -121,3 +121,46 @@ def test_arguments_without_a_bound(q_lens, kv_lens, h, hk, d, typ, window, sinks
     out = g.gguf_paged_attention(q, cache, table, start, kv_len, hk, 16, most or max(q_lens), d ** -0.5, window=window, sinks=sinks)
     limit = 10 ** 6   # past every length here
     check_attn(out, attn_ref(q, k, v, q_lens, kv_lens, d ** -0.5, min(window, limit), min(sinks, limit)), typ)
+
+
+# ------------------------------------------------------------------ counts
+
+@pytest.mark.parametrize("q_lens, kv_lens, h, hk, d, page, typ, window, sinks", [
+    ([1], [200], 4, 2, 64, 32, "bf16", 0, 0),
+    ([1, 1], [200, 333], 24, 2, 128, 48, "f16", 0, 0),              # two groups of rows per KV head
+    ([3, 2], [100, 77], 12, 4, 128, 16, "f32", 0, 0),
+    ([1, 2], [900, 1500], 8, 2, 64, 64, "bf16", 300, 40),           # a page between the first tokens and the window
+    ([1], [9000], 4, 1, 128, 16, "bf16", 0, 0),                     # one unit over many CTAs
+    ([80], [200], 4, 2, 64, 32, "bf16", 0, 0),
+    ([300, 1, 150], [450, 100, 150], 8, 2, 128, 16, "bf16", 0, 0),  # several row blocks, and a single token beside them
+    ([300], [700], 6, 1, 128, 64, "f16", 100, 20),
+    ([200], [900], 2, 2, 256, 32, "bf16", 210, 0),
+    ([40], [3000], 4, 1, 128, 16, "bf16", 0, 0)])                   # tokens in pieces
+def test_pages_outside_the_cache_are_counted_once(q_lens, kv_lens, h, hk, d, page, typ, window, sinks):
+    """Each page of a request that is outside the cache and would hold a token that some query of it sees counts one."""
+    q, cache, table, start, kv_len, k, v = attn_setup(q_lens, kv_lens, h, hk, d, page, typ, spare_cols=2)
+    rng = np.random.default_rng(len(q_lens) + kv_lens[0])
+    rows = table.cpu().numpy()
+    want = 0
+    for r, (n, m) in enumerate(zip(q_lens, kv_lens)):
+        for at in range(rows.shape[1]):
+            if rng.random() < 0.3 or at * page >= m:
+                rows[r, at] = rng.choice((-1, -7, cache.shape[0], 2 ** 31 - 1))
+        j = np.arange(m)
+        if window:
+            j = j[(j > m - n - window) | (j < sinks)]
+        want += sum(not 0 <= rows[r, at] < cache.shape[0] for at in np.unique(j // page))
+    assert want > 0
+    status = torch.full((1,), 5, dtype=torch.int32, device=DEV)
+    out = g.gguf_paged_attention(q, cache, torch.from_numpy(rows).to(DEV), start, kv_len, hk, page, max(q_lens), d ** -0.5,
+                                 window=window, sinks=sinks, dev_status=status)
+    assert status.item() == 5 + want and bool(torch.isfinite(out.float()).all())
+
+
+@pytest.mark.parametrize("q_len", [1, 80])
+def test_pages_past_the_table_are_counted_once(q_len):
+    h, hk, d, page = 8, 2, 64, 32
+    q, cache, table, start, kv_len, k, v = attn_setup([q_len], [200], h, hk, d, page, "bf16")
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    g.gguf_paged_attention(q, cache, table[:, :4], start, kv_len, hk, page, q_len, 0.125, dev_status=status)
+    assert status.item() == -(-200 // page) - 4
