@@ -140,7 +140,7 @@ _native = None   # the module _bind: marshalling of the paged-cache calls
 
 def load_library(path: str = LIB_PATH):
     """Load libgguf_gb300.so (built by ``build.build()``); raise if it is missing."""
-    global _lib, _native
+    global _lib
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -150,12 +150,6 @@ def load_library(path: str = LIB_PATH):
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    from . import _bind as native
-
-    native.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
-        "gguf_kv_plan", "gguf_qk_norm_rope", "gguf_kv_get_rows", "gguf_paged_attention_ws_size", "gguf_paged_attention",
-        "gguf_kv_page_bytes")))
-    _native = native
     _lib = lib
     return lib
 
@@ -499,8 +493,16 @@ def gguf_kv_page_bytes(head_dim: int, n_kv_heads: int, page_size: int) -> int:
 
 
 def _bound():
+    """The native module, on the first paged-cache call (no other call needs it)."""
+    global _native
     if _native is None:
-        load_library()
+        lib = load_library()
+        from . import _bind
+
+        _bind.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "gguf_kv_plan", "gguf_qk_norm_rope", "gguf_kv_get_rows", "gguf_paged_attention_ws_size", "gguf_paged_attention",
+            "gguf_kv_page_bytes")))
+        _native = _bind
     return _native
 
 
