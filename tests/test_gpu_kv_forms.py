@@ -164,3 +164,42 @@ def test_pages_past_the_table_are_counted_once(q_len):
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
     g.gguf_paged_attention(q, cache, table[:, :4], start, kv_len, hk, page, q_len, 0.125, dev_status=status)
     assert status.item() == -(-200 // page) - 4
+
+
+# ------------------------------------------------------------------ queries whose values share a sign
+
+@pytest.mark.parametrize("times", [1.0, 8.0])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("typ, h, q_len", [("f16", 32, 1), ("bf16", 32, 1), ("f16", 64, 2), ("f16", 16, 40)])
+def test_queries_of_one_sign(typ, h, q_len, d, times):
+    """What the code offsets add to the scores of such queries leaves no larger error than others have."""
+    hk, n = 4, 700
+    q, cache, table, start, kv_len, k, v = attn_setup([q_len], [n], h, hk, d, 16, typ, seed=d)
+    q = ((2 + 0.3 * torch.randn(q_len, h, d, device=DEV)) * times).to(DTYPES[typ])
+    refs = attn_ref(q, k, v, [q_len], [n], d ** -0.5, 0, 0)
+    out = g.gguf_paged_attention(q, cache, table, start, kv_len, hk, 16, q_len, d ** -0.5)
+    check_attn(out, refs, typ)
+    err = float((out.double().cpu() - refs[0]).norm() / refs[0].norm())
+    print(f"{typ} h{h} q{q_len} d{d} x{times}: {err:.2e}")
+    # the output's rounding (2.1e-4 of the norm in fp16, 1.7e-3 in bf16) and 2e-4 of operands rounded to fp16
+    assert err <= {"f16": 2.1e-4, "bf16": 1.7e-3}[typ] + 2e-4
+
+
+# ------------------------------------------------------------------ other forms
+
+@pytest.mark.parametrize("q_lens, kv_lens, h, hk, d, window", [
+    ([1, 1], [300, 41], 12, 1, 128, 0), ([2], [900], 40, 2, 64, 100), ([1], [2500], 32, 1, 256, 0), ([30], [30], 10, 1, 64, 0)])
+def test_fp32_with_many_heads_per_kv_head(q_lens, kv_lens, h, hk, d, window):
+    q, cache, table, start, kv_len, k, v = attn_setup(q_lens, kv_lens, h, hk, d, 16, "f32")
+    out = g.gguf_paged_attention(q, cache, table, start, kv_len, hk, 16, max(q_lens), d ** -0.5, window=window)
+    check_attn(out, attn_ref(q, k, v, q_lens, kv_lens, d ** -0.5, window, 0), "f32")
+
+
+@pytest.mark.parametrize("q_lens, kv_lens, typ", [([1, 3], [333, 60], "f32"), ([1], [333], "bf16"), ([40, 1], [90, 333], "bf16"),
+                                                  ([300], [300], "f16")])
+def test_table_wider_than_any_request(q_lens, kv_lens, typ):
+    """A table kept for long contexts, which chooses other kernels than a tight one."""
+    h, hk, d = 8, 2, 128
+    q, cache, table, start, kv_len, k, v = attn_setup(q_lens, kv_lens, h, hk, d, 16, typ, spare_cols=2000)
+    out = g.gguf_paged_attention(q, cache, table, start, kv_len, hk, 16, max(q_lens), d ** -0.5)
+    check_attn(out, attn_ref(q, k, v, q_lens, kv_lens, d ** -0.5, 0, 0), typ)
