@@ -46,7 +46,10 @@ static AttnPlan attn_plan(const Attn &p, int64_t d) {
     // them where there are fewer than SMs (5 requests of up to 66 tokens, 32 heads of 256 after 3032 tokens: 141 us uncut,
     // 106 us so), of those after the last full round where few rounds end in a short one and what was cached before
     // makes them long (4 chunks of 512 tokens after 3500, 24 heads of 128: 190 us uncut, 169 us so).  Elsewhere it
-    // only costs (8192 tokens: 664 us with what cutting costs the kernel, 644 us without).
+    // only costs (8192 tokens: 664 us with what cutting costs the kernel, 644 us without).  The count of row blocks here is
+    // an estimate: the device rounds up per request and KV head, so many short requests make more of them, and `span`
+    // comes from the table's width, not from the lengths (a prompt of 77 tokens, 32 heads of 128: 17.9 us with a table of
+    // its own width, 30.6 us with one of 32768 tokens; of 2048 tokens 69.9 and 70.6 us).
     const int64_t span = p.window > 0 ? std::min(p.width * p.page, p.window + p.sinks + p.max_q) : p.width * p.page;
     const int64_t rows = d == 256 ? 128 : 256, heads_rows = (p.n_tokens - std::min(p.R, p.n_tokens)) * p.h;
     const int64_t rounds = heads_rows / rows / sms, rest = heads_rows / rows % sms;

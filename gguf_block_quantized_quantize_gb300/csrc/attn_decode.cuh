@@ -29,12 +29,20 @@
 // lose bits).  fp32 queries use three bf16 parts of q, the exact c - 8, and
 // high and low fp16 parts of p and v, for fp32 accuracy.
 //
-// Measured, with 8 rows a unit: 32 requests of 8192 tokens (32 query heads, 8 KV
-// heads of 128) 52.9 us, 3.6 TB/s; 4 of 131072 (16 heads, 2 of 256) 60.4 us, 3.6
-// TB/s; 64 with a window of 4096 (32, 8 of 64) 49.5 us, 3.1 TB/s; 1 of 333 (fp32)
-// 11.9 us.  What bounds it now: instructions (59 % of the issue slots, by the three
-// computing warps a scheduler that the registers allow; DRAM at 48 %), then a
-// unit's start and join (3500 cycles) and the second launch (about 4 us).
+// Measured, with 8 rows a unit: 32 requests of up to 8192 tokens (32 query heads, 8
+// KV heads of 128) 51.7 us, 3.7 TB/s; 4 of 131072 (16 heads, 2 of 256) 60.0 us, 3.6
+// TB/s; 64 with a window of 4096 (32, 8 of 64) 48.8 us, 3.1 TB/s; 1 of 333 (fp32)
+// 10.9 us.  What bounds it now: no unit is full (issue slots 59 %, DRAM 48 %, tensor
+// pipe 20 %).  Three computing warps a scheduler, as many as the registers allow,
+// wait in the chain of a step (scores, maxima by shuffles, probabilities, outputs),
+// beside a unit's start and join (3500 cycles) and the second launch (about 4 us).
+// With 4 heads per KV head a single token fills half of a unit's 8 rows.  Spills a
+// thread: 96 bytes of stores and 56 of loads with heads of 128 (144 / 104 with 16
+// rows), 32 / 16 of 64, 112 / 88 of 256, 248 / 204 of 256 in fp32.
+//
+// fp32 queries of any number come here, 8 rows a unit: 32 requests of 8192 tokens
+// 112 us, a prompt of 1024 tokens 282 us, of 2048 1050 us, of 8192 15.9 ms (bf16 in
+// the prompt kernel: 42, 71 and 662 us).
 #pragma once
 
 #include <algorithm>
@@ -950,7 +958,8 @@ static cudaError_t attn_decode_run(const AdShape &shape, int ctas, cudaStream_t 
     using C = AdCfg<D, QT, NT>;
     AdShape a = shape;
     // Few units of few tiles: a CTA each, and the second launch is saved (about 4 us).  The table's width bounds the
-    // tiles: 2048 tokens are 128 tiles, 11 to 16 per warp, about 4 us.
+    // tiles: 2048 tokens are 128 tiles, 11 to 16 per warp, about 4 us.  (8 requests of 333 tokens, 32 heads of 128: 9.6 us
+    // with a table of their width, 12.2 us with one of 32768 tokens.)
     const int64_t most_rows = std::min<int64_t>(a.max_rows, a.G * a.p.max_q);
     const int64_t units = a.p.R * a.p.hk * ((most_rows + C::RG - 1) / C::RG);
     const int64_t span = a.p.window > 0 ? std::min(a.p.width * a.p.page, a.p.window + a.p.sinks + a.p.max_q + 3 * KV_TILE)

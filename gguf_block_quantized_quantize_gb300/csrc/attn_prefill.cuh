@@ -24,13 +24,16 @@
 // TMEM allocation), 13 loads.  Every wait is bounded (1 s); a timeout sets the
 // error word and the CTA drains and exits.
 //
-// Measured: a prompt of 8192 tokens, 32 query heads, 8 KV heads of 128, bf16: 644
+// Measured: a prompt of 8192 tokens, 32 query heads, 8 KV heads of 128, bf16: 648
 // us, 0.85 PFLOP/s (0.45 of the matrix rate); with heads of 256 1690 us (0.34);
 // 2 x 4093 tokens with a window of 1000, heads of 64, fp16: 154 us (0.27 PFLOP/s).
 // What bounds it now: no unit (tensor pipe 37 % active, issue slots 45 % used at
 // heads of 128) but the chain scores, softmax, P, product of an S buffer, which
 // the next scores into it wait for: 4800 cycles per block and two row tiles, and
-// 4300 with heads of 64.  A third S buffer finds no room in TMEM.
+// 4300 with heads of 64.  TMEM is full with heads of 128 only (two S buffers and O);
+// with heads of 64 and of 256 128 of its columns are unused (384 on, and 128 to 255).
+// Spills a thread: at most 76 bytes of stores and 64 of loads without CUT; with it
+// 216 / 228 with heads of 128, 108 / 128 of 64, none of 256.
 #pragma once
 
 #include "attn_decode.cuh"

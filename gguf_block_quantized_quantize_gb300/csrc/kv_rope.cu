@@ -14,14 +14,19 @@
 // registers.  Values: a warp takes one 32-value block of 8 tokens, so that the
 // 16 bits that a tile keeps together of 4 values of one token lie next to those
 // of the other tokens.  Products and sums of the rotation are rounded one by one
-// (no fused multiply-add), so that the stored codes are those of the formula
-// evaluated step by step.
+// (no fused multiply-add).  Codes are exactly those of the fp32 keys that k_out
+// shows for fp32 inputs; the norm's sum of squares is taken lane by lane, so a key
+// value on the border of two codes may take the neighbour of the code that another
+// order of that sum gives.
 //
 // Bound: HBM for prompts (reads q, k, v; writes q and 4.5 bits per k and v
-// value), latency for single tokens.  Measured: 1 token, 24 + 8 + 8 fp32 heads of
-// 128, 5.7 us; 77 tokens, 16 + 2 + 2 fp16 heads of 256, 6.4 us; 2048 tokens, 32 +
-// 8 + 8 bf16 heads of 128, 28.2 us (2.0 TB/s: with four warps a scheduler the
-// chain load, sum, rotate, round, store shows, not the bytes).
+// value), latency for single tokens.  Measured in a captured graph: 1 token, 32 +
+// 8 + 8 heads of 128, 2.8 us (bf16), 2.9 us (fp32); 2048 tokens 21.0 us (bf16; the
+// bytes take 6.7), 29.1 us (fp32); 16 + 2 + 2 heads of 256, 18.0 and 26.5 us.  Far
+// from the bytes: eight warps a scheduler at 64 registers, where four rows in flight
+// spill (16-bit heads of 128: 104 bytes of stores and 284 of loads a thread; fp32 294
+// and 528), 64-bit divisions for the place of a value block, and the chain load, sum,
+// rotate, round, store.
 #include <algorithm>
 
 #include "common.cuh"
@@ -328,7 +333,8 @@ __global__ void __launch_bounds__(QR_THREADS, 4) qk_norm_rope_kernel(const QkRop
 }
 
 // gguf_kv_get_rows: values d * (c - 8) of slots.  16 slots side by side in the lanes, so that the lanes share the sectors
-// of a tile that holds them all (with a slot's head per group of lanes 18 us, so 6 us: 2048 slots, 8 bf16 heads of 128).
+// of a tile that holds them all (with a slot's head per group of lanes 18 us, so 5.4 us: 2048 slots, 8 bf16 heads of 128;
+// the bytes take 1.6).
 template <int D, int T, bool VEC>
 __global__ void __launch_bounds__(QR_THREADS) kv_get_rows_kernel(const KvRows p) {
     constexpr int LPR = D / 8;

@@ -561,7 +561,9 @@ gguf_status gguf_kv_plan(const int32_t *ctx_len, const int32_t *new_len, int64_t
  * 32, d = fp16(the value of largest magnitude (the first of equals) / -8) and
  * code = clamp(roundf(x / d) + 8, 0, 15) (Q4_0; a block whose d rounds to 0
  * stands for zeros), with an IEEE fp32 division.  Values must stay below 65504 in magnitude;
- * NaN / Inf inputs give unspecified blocks (no fault).
+ * NaN / Inf inputs give unspecified blocks (no fault).  x of a key is rounded to fp32
+ * after the norm and each step of the rotation; on the border of two codes, the order
+ * of the norm's sum decides.
  *   q, k, v    : [n_tokens][ld] of type xt (F32, BF16, F16), heads side by side
  *                in a row.  Rows that start on 16 bytes are read 16 bytes at a
  *                time.  k and v may be NULL where nothing takes them.
@@ -622,7 +624,10 @@ gguf_status gguf_kv_get_rows(const void *cache, int64_t n_pages, int64_t page_si
  *                are not written.
  *   n_heads    : a multiple of n_kv_heads; query head h reads KV head
  *                h / (n_heads / n_kv_heads).
- *   block_table: [n_requests][ld_table] int32, width columns used.  A page number
+ *   block_table: [n_requests][ld_table] int32, width columns used.  The width bounds
+ *                the lengths in the choice of kernels and of cuts: a table that is
+ *                wider than the requests need costs short calls a few us (up to 13 us
+ *                measured; pass fewer columns where that counts).  A page number
  *                outside the cache, or one past the table, hides its tokens.
  *   dev_status : + such pages, each once per request whose queries would see a
  *                token of it.
@@ -635,11 +640,14 @@ gguf_status gguf_kv_get_rows(const void *cache, int64_t n_pages, int64_t page_si
  *   window, sinks : any value >= 0; what passes every position hides nothing.
  *   ws         : gguf_paged_attention_ws_size(args) bytes, 16-byte aligned.
  * Softmax statistics and sums are fp32.  16-bit queries take fp16 probabilities and
- * values into the matrix instructions (2e-4 of a row's norm, beside the rounding of the
- * output), and in long prompts of bf16 queries fp16 keys (4e-4); fp32 queries split operands
- * (about 1e-6; GGUF_ERR_SHAPE where max_q_len x heads / 8 x table tokens / 16 passes
- * 4e9).  Probabilities below 2^-34 of a row's largest count as zero.  Same bits on
- * every run.  Timeouts of the kernels' waits reach the caller as described at
+ * values into the matrix instructions (2e-4 of the outputs' norm, 3e-4 in prompts, beside
+ * the rounding of the output), and in prompts of bf16 queries fp16 keys (4e-4); so the
+ * bits of a request's outputs depend on the kernel, which depends on the call.  fp32
+ * queries split operands (about 1e-6; GGUF_ERR_SHAPE where max_q_len x heads / 8 x table
+ * tokens / 16 passes 4e9) and run 8 rows at a time: a prompt of 8192 tokens takes 24
+ * times as long as in bf16.  Probabilities below 2^-34 of a row's largest count as zero.
+ * A block that is not finite may reach the outputs of every query of its request in the
+ * call, those that must not see its token among them.  Same bits on every run.  Timeouts of the kernels' waits reach the caller as described at
  * gguf_device_errors.
  */
 typedef struct gguf_attn_args {
