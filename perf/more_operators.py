@@ -27,41 +27,41 @@ _EPS = 1e-6
 def listed():
     return [
         # one new token between two products of a decode step: latency; the next product takes q8_1 rows
-        {"name": "norm, 1 token", "op": "norm", "tokens": 1, "width": 4096, "type": "bf16", "resid": "bf16",
+        {"name": "norm 1 token", "op": "norm", "tokens": 1, "width": 4096, "type": "bf16", "resid": "bf16",
          "post": "none", "pre": "rms", "gate": "none", "float": False, "q8": True},
         # a decoding batch, norms on both sides and a gate of its own per token, residual stream in fp32
-        {"name": "norm, 64 tokens gated f16", "op": "norm", "tokens": 64, "width": 2048, "type": "f16", "resid": "f32",
+        {"name": "norm 64 tokens gated f16", "op": "norm", "tokens": 64, "width": 2048, "type": "f16", "resid": "f32",
          "post": "rms", "pre": "rms", "gate": "rows", "float": True, "q8": True},
         # fp32 activations with centred norms, biases and one gate row for all tokens, an odd width
-        {"name": "norm, 777 tokens centred f32", "op": "norm", "tokens": 777, "width": 1111, "type": "f32",
+        {"name": "norm 777 tokens centred f32", "op": "norm", "tokens": 777, "width": 1111, "type": "f32",
          "resid": "f32", "post": "layer", "pre": "layer", "gate": "row", "float": True, "q8": False},
         # a long prompt, norms on both sides
-        {"name": "norm, 8192 tokens", "op": "norm", "tokens": 8192, "width": 4096, "type": "bf16", "resid": "bf16",
+        {"name": "norm 8192 tokens", "op": "norm", "tokens": 8192, "width": 4096, "type": "bf16", "resid": "bf16",
          "post": "rms", "pre": "rms", "gate": "none", "float": True, "q8": True},
         # one token of a decode step: latency
-        {"name": "rope, 1 token", "op": "rope", "tokens": 1, "heads": 24, "kv_heads": 8, "dim": 128,
+        {"name": "rope 1 token", "op": "rope", "tokens": 1, "heads": 24, "kv_heads": 8, "dim": 128,
          "sections": "16,24,24", "mixed": False, "neox": True, "norm": True, "type": "bf16", "page": 16},
         # a small image, wide heads of which a quarter is rotated, two axes
-        {"name": "rope, 333 tokens d256 f16", "op": "rope", "tokens": 333, "heads": 16, "kv_heads": 2, "dim": 256,
+        {"name": "rope 333 tokens d256 f16", "op": "rope", "tokens": 333, "heads": 16, "kv_heads": 2, "dim": 256,
          "sections": "16,16", "mixed": False, "neox": False, "norm": True, "type": "f16", "page": 32},
         # a prompt of images and text, axes in turn
-        {"name": "rope, 4096 tokens", "op": "rope", "tokens": 4096, "heads": 32, "kv_heads": 8, "dim": 128,
+        {"name": "rope 4096 tokens", "op": "rope", "tokens": 4096, "heads": 32, "kv_heads": 8, "dim": 128,
          "sections": "24,20,20", "mixed": True, "neox": True, "norm": True, "type": "bf16", "page": 64},
         # two short requests, fp32 activations: latency
-        {"name": "attn, 2 x (700 + 60) f32", "op": "attn", "groups": 1, "per": 2, "prefix": 700, "tail": 60, "q": 1,
+        {"name": "attn 2 x (700 + 60) f32", "op": "attn", "groups": 1, "per": 2, "prefix": 700, "tail": 60, "q": 1,
          "heads": 24, "kv_heads": 8, "dim": 128, "type": "f32", "page": 16, "window": 0, "sinks": 0},
         # a decoding batch on one system prompt
-        {"name": "attn, 32 x (8192 + 512)", "op": "attn", "groups": 1, "per": 32, "prefix": 8192, "tail": 512, "q": 1,
+        {"name": "attn 32 x (8192 + 512)", "op": "attn", "groups": 1, "per": 32, "prefix": 8192, "tail": 512, "q": 1,
          "heads": 32, "kv_heads": 8, "dim": 128, "type": "bf16", "page": 64, "window": 0, "sinks": 0},
         # several prompts, each with a few requests, wide heads shared by eight queries
-        {"name": "attn, 6 x 8 x (5000 + 300) d256", "op": "attn", "groups": 6, "per": 8, "prefix": 5000, "tail": 300,
+        {"name": "attn 6 x 8 x (5000 + 300) d256", "op": "attn", "groups": 6, "per": 8, "prefix": 5000, "tail": 300,
          "q": 1, "heads": 16, "kv_heads": 2, "dim": 256, "type": "bf16", "page": 32, "window": 0, "sinks": 0},
         # a few tokens of each request to check at once, fp16
-        {"name": "attn, 16 x 4 x (20000 + 400) d64", "op": "attn", "groups": 1, "per": 16, "prefix": 20000,
+        {"name": "attn 16 x 4 x (20000 + 400) d64", "op": "attn", "groups": 1, "per": 16, "prefix": 20000,
          "tail": 400, "q": 4, "heads": 32, "kv_heads": 8, "dim": 64, "type": "f16", "page": 16, "window": 0,
          "sinks": 0},
         # many samples from one long document
-        {"name": "attn, 256 x (32768 + 128)", "op": "attn", "groups": 1, "per": 256, "prefix": 32768, "tail": 128,
+        {"name": "attn 256 x (32768 + 128)", "op": "attn", "groups": 1, "per": 256, "prefix": 32768, "tail": 128,
          "q": 1, "heads": 32, "kv_heads": 8, "dim": 128, "type": "bf16", "page": 64, "window": 0, "sinks": 0},
     ]
 
