@@ -20,6 +20,8 @@ import torch
 F32, F16, Q4_0, Q8_0, Q8_1, Q4_K, Q5_K, Q6_K, BF16, MXFP4 = 0, 1, 2, 8, 9, 12, 13, 14, 30, 39
 GATE_UP_SWIGLU, DOWN_WEIGHTED_SUM, PLAIN = 0, 1, 2
 ROPE_NORM, ROPE_NEOX = 0, 2   # rotated pairs (2i, 2i + 1) or (i, i + rot / 2)
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
+GATE_NONE, GATE_SIGMOID, GATE_TANH, GATE_SILU = 0, 1, 2, 3
 Q8_1_BYTES = 36   # one q8_1 block: fp16 d, fp16 s, 32 int8 quants (a q8_1 row is k / 32 blocks)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -88,6 +90,22 @@ class QkRopeArgs(ctypes.Structure):
                 ("slots", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
 
 
+class RopeAxes(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int64), ("ld_positions", ctypes.c_int64), ("sections", ctypes.c_int32 * 4),
+                ("interleaved", ctypes.c_int)]
+
+
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("xt", ctypes.c_int), ("ldx", ctypes.c_int64), ("h", ctypes.c_void_p),
+                ("ht", ctypes.c_int), ("ldh", ctypes.c_int64), ("gate", ctypes.c_void_p), ("gt", ctypes.c_int),
+                ("ldg", ctypes.c_int64), ("gate_act", ctypes.c_int), ("n_tokens", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("post_kind", ctypes.c_int), ("post_w", ctypes.c_void_p), ("post_b", ctypes.c_void_p),
+                ("post_eps", ctypes.c_float), ("pre_kind", ctypes.c_int), ("pre_w", ctypes.c_void_p),
+                ("pre_b", ctypes.c_void_p), ("pre_eps", ctypes.c_float), ("branch_scale", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("h_out", ctypes.c_void_p), ("ldho", ctypes.c_int64),
+                ("z", ctypes.c_void_p), ("zt", ctypes.c_int), ("ldz", ctypes.c_int64), ("z_q8_1", ctypes.c_void_p)]
+
+
 class AttnArgs(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("qt", ctypes.c_int), ("n_tokens", ctypes.c_int64), ("ldq", ctypes.c_int64),
                 ("cache", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
@@ -124,6 +142,8 @@ SIGNATURES = {
     "gguf_kv_page_bytes": (_i64, [_i64, _i64, _i64]),
     "gguf_kv_plan": (_i, [_p, _p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _p]),
     "gguf_qk_norm_rope": (_i, [ctypes.POINTER(QkRopeArgs), _p]),
+    "gguf_qk_norm_mrope": (_i, [ctypes.POINTER(QkRopeArgs), ctypes.POINTER(RopeAxes), _p]),
+    "gguf_block_norm": (_i, [ctypes.POINTER(BlockNormArgs), _p]),
     "gguf_kv_get_rows": (_i, [_p, _i64, _i64, _i64, _i64, _p, _i64, _p, _p, _i, _p]),
     "gguf_paged_attention_ws_size": (_sz, [ctypes.POINTER(AttnArgs)]),
     "gguf_paged_attention": (_i, [ctypes.POINTER(AttnArgs), _p, _sz, _p]),
@@ -135,7 +155,7 @@ SIGNATURES = {
 }
 
 _lib = None
-_native = None   # the module _bind: marshalling of the paged-cache calls
+_native = None   # the module _bind: marshalling of the paged-cache and block-norm calls
 
 
 def load_library(path: str = LIB_PATH):
@@ -493,7 +513,7 @@ def gguf_kv_page_bytes(head_dim: int, n_kv_heads: int, page_size: int) -> int:
 
 
 def _bound():
-    """The native module, on the first paged-cache call (no other call needs it)."""
+    """The native module, on the first paged-cache or block-norm call (no other call needs it)."""
     global _native
     if _native is None:
         lib = load_library()
@@ -501,7 +521,7 @@ def _bound():
 
         _bind.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "gguf_kv_plan", "gguf_qk_norm_rope", "gguf_kv_get_rows", "gguf_paged_attention_ws_size", "gguf_paged_attention",
-            "gguf_kv_page_bytes")))
+            "gguf_kv_page_bytes", "gguf_qk_norm_mrope", "gguf_block_norm")))
         _native = _bind
     return _native
 
@@ -541,6 +561,54 @@ def gguf_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor |
     if st:
         _check(st)
     return q_out
+
+
+def gguf_qk_norm_mrope(q: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor | None, q_norm: torch.Tensor | None,
+                       k_norm: torch.Tensor | None, eps: float, positions: torch.Tensor, cos_sin: torch.Tensor | None,
+                       sections, interleaved: bool = False, rope_type: int = ROPE_NEOX, cache: torch.Tensor | None = None,
+                       slots: torch.Tensor | None = None, page_size: int = 0, q_out: torch.Tensor | None = None,
+                       k_out: torch.Tensor | None = None, dev_status: torch.Tensor | None = None) -> torch.Tensor:
+    """gguf_qk_norm_rope with ``positions`` [axes, t] on up to 4 axes (time, height, width): ``sections`` gives the
+    rotated pairs of each axis (rot / 2 together), one section after another or, ``interleaved``, in turn."""
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    st = _bound().qk_norm_mrope(q, k, v, q_norm, k_norm, eps, positions, cos_sin, rope_type, cache, slots, page_size, q_out,
+                                k_out, dev_status, _stream(), tuple(sections), 1 if interleaved else 0)
+    if st:
+        _check(st)
+    return q_out
+
+
+def gguf_block_norm(x: torch.Tensor | None, residual: torch.Tensor | None, *, gate: torch.Tensor | None = None,
+                    gate_act: int = GATE_NONE, branch_scale: float = 1.0, residual_scale: float = 1.0,
+                    post_kind: int = NORM_NONE, post_weight: torch.Tensor | None = None,
+                    post_bias: torch.Tensor | None = None, pre_kind: int = NORM_RMS,
+                    pre_weight: torch.Tensor | None = None, pre_bias: torch.Tensor | None = None, eps: float = 1e-6,
+                    residual_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                    out_q8_1: torch.Tensor | None = None, q8_1: bool = False):
+    """From a block's output ``x`` [t, k] to the next block's input (see include/gguf_gb300.h):
+
+        y  = gate_act(gate) * N_post(x)
+        h' = residual_scale * residual + branch_scale * y
+        z  = N_pre(h')
+
+    Returns (h', z, z as q8_1 rows).  Given tensors are filled; without ``out`` and ``out_q8_1``, z is made in x's
+    dtype, or with ``q8_1=True`` as q8_1 rows alone; h' is made where ``x`` is given.  What is not made is None.
+    ``gate`` is [t, k], or [k] for all tokens.  ``residual_out`` may be ``residual``, ``out`` may be ``x``."""
+    a = x if x is not None else residual
+    if a is None:
+        raise ValueError("gguf_block_norm: x or residual must be given")
+    if residual_out is None and x is not None:
+        residual_out = torch.empty(a.shape, dtype=a.dtype if residual is None else residual.dtype, device=a.device)
+    if out is None and out_q8_1 is None and not q8_1:
+        out = torch.empty(a.shape, dtype=a.dtype, device=a.device)
+    if out_q8_1 is None and q8_1:
+        out_q8_1 = torch.empty((a.shape[0], max(gguf_row_size(Q8_1, a.shape[1]), 0)), dtype=torch.uint8, device=a.device)
+    st = _bound().block_norm(x, residual, gate, gate_act, branch_scale, residual_scale, post_kind, post_weight, post_bias, eps,
+                             pre_kind, pre_weight, pre_bias, eps, residual_out, out, out_q8_1, _stream())
+    if st:
+        _check(st)
+    return residual_out, out, out_q8_1
 
 
 def gguf_kv_get_rows(cache: torch.Tensor, slots: torch.Tensor, n_kv_heads: int, head_dim: int, page_size: int,

@@ -25,6 +25,8 @@ typedef gguf_status (*rows_fn)(const void *, int64_t, int64_t, int64_t, int64_t,
 typedef size_t (*attn_ws_fn)(const gguf_attn_args *);
 typedef gguf_status (*attn_fn)(const gguf_attn_args *, void *, size_t, gguf_stream_t);
 typedef int64_t (*page_fn)(int64_t, int64_t, int64_t);
+typedef gguf_status (*mrope_fn)(const gguf_qk_rope_args *, const gguf_rope_axes *, gguf_stream_t);
+typedef gguf_status (*norm_fn)(const gguf_block_norm_args *, gguf_stream_t);
 
 struct {
     plan_fn plan;
@@ -33,6 +35,8 @@ struct {
     attn_ws_fn attn_ws;
     attn_fn attn;
     page_fn page_bytes;
+    mrope_fn mrope;
+    norm_fn norm;
 } api;
 
 struct Bad {};   // a Python exception is set
@@ -162,63 +166,172 @@ PyObject *kv_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 // q, k, v, q_norm, k_norm, eps, positions, cos_sin, rope_type, cache, slots, page, q_out, k_out, status, stream
+// (positions apart)
+gguf_qk_rope_args rope_args(PyObject *const *a, const char *what) {
+    const at::Tensor &q = tensor(a[0], what, "q");
+    if (q.dim() != 3) refuse(what, "q", "[tokens, heads, head_dim]");
+    const int64_t t = q.size(0), h = q.size(1), d = q.size(2);
+    const at::ScalarType type = q.scalar_type();
+    gguf_qk_rope_args x{};
+    x.xt = float_type(type, what);
+    x.n_tokens = t;
+    x.n_heads = h;
+    x.head_dim = d;
+    Rows r = rows(q, t, h, d, type, what, "q");
+    x.q = r.p;
+    x.ldq = r.ld;
+    r = rows(tensor(a[12], what, "q_out"), t, h, d, type, what, "q_out");
+    x.q_out = r.p;
+    x.ldqo = r.ld;
+    if (a[1] != Py_None) {
+        const at::Tensor &k = tensor(a[1], what, "k");
+        x.n_kv_heads = k.dim() == 3 ? k.size(1) : 0;
+        r = rows(k, t, x.n_kv_heads, d, type, what, "k");
+        x.k = r.p;
+        x.ldk = r.ld;
+    }
+    if (a[13] != Py_None) {
+        r = rows(tensor(a[13], what, "k_out"), t, x.n_kv_heads, d, type, what, "k_out");
+        x.k_out = r.p;
+        x.ldko = r.ld;
+    }
+    x.page_size = integer(a[11]);
+    if (a[9] != Py_None) {
+        if (a[1] == Py_None || a[2] == Py_None || a[10] == Py_None) refuse(what, "k, v and slots", "given to store");
+        r = rows(tensor(a[2], what, "v"), t, x.n_kv_heads, d, type, what, "v");
+        x.v = r.p;
+        x.ldv = r.ld;
+        const Pages c = pages(a[9], d, x.n_kv_heads, x.page_size, what);
+        x.cache = c.p;
+        x.n_pages = c.n;
+        x.slots = array<int64_t>(a[10], t, what, "slots");
+    }
+    x.q_norm = weights(a[3], d, what, "q_norm");
+    x.k_norm = weights(a[4], d, what, "k_norm");
+    x.eps = static_cast<float>(real(a[5]));
+    if (a[7] != Py_None) {
+        const at::Tensor &c = tensor(a[7], what, "cos_sin");
+        if (c.scalar_type() != at::kFloat || c.dim() != 2 || !c.is_contiguous())
+            refuse(what, "cos_sin", "a contiguous fp32 tensor [positions, rot]");
+        x.cos_sin = static_cast<const float *>(c.data_ptr());
+        x.n_positions = c.size(0);
+        x.rot = c.size(1);
+    }
+    x.rope_type = static_cast<int>(integer(a[8]));
+    x.dev_status = array_or_none<int32_t>(a[14], 1, what, "dev_status");
+    return x;
+}
+
 PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
         const char *what = "gguf_qk_norm_rope";
         count(n, 16, what);
-        const at::Tensor &q = tensor(a[0], what, "q");
-        if (q.dim() != 3) refuse(what, "q", "[tokens, heads, head_dim]");
-        const int64_t t = q.size(0), h = q.size(1), d = q.size(2);
-        const at::ScalarType type = q.scalar_type();
-        gguf_qk_rope_args x{};
-        x.xt = float_type(type, what);
-        x.n_tokens = t;
-        x.n_heads = h;
-        x.head_dim = d;
-        Rows r = rows(q, t, h, d, type, what, "q");
-        x.q = r.p;
-        x.ldq = r.ld;
-        r = rows(tensor(a[12], what, "q_out"), t, h, d, type, what, "q_out");
-        x.q_out = r.p;
-        x.ldqo = r.ld;
-        if (a[1] != Py_None) {
-            const at::Tensor &k = tensor(a[1], what, "k");
-            x.n_kv_heads = k.dim() == 3 ? k.size(1) : 0;
-            r = rows(k, t, x.n_kv_heads, d, type, what, "k");
-            x.k = r.p;
-            x.ldk = r.ld;
-        }
-        if (a[13] != Py_None) {
-            r = rows(tensor(a[13], what, "k_out"), t, x.n_kv_heads, d, type, what, "k_out");
-            x.k_out = r.p;
-            x.ldko = r.ld;
-        }
-        x.page_size = integer(a[11]);
-        if (a[9] != Py_None) {
-            if (a[1] == Py_None || a[2] == Py_None || a[10] == Py_None) refuse(what, "k, v and slots", "given to store");
-            r = rows(tensor(a[2], what, "v"), t, x.n_kv_heads, d, type, what, "v");
-            x.v = r.p;
-            x.ldv = r.ld;
-            const Pages c = pages(a[9], d, x.n_kv_heads, x.page_size, what);
-            x.cache = c.p;
-            x.n_pages = c.n;
-            x.slots = array<int64_t>(a[10], t, what, "slots");
-        }
-        x.q_norm = weights(a[3], d, what, "q_norm");
-        x.k_norm = weights(a[4], d, what, "k_norm");
-        x.eps = static_cast<float>(real(a[5]));
-        x.positions = array<int32_t>(a[6], t, what, "positions");
-        if (a[7] != Py_None) {
-            const at::Tensor &c = tensor(a[7], what, "cos_sin");
-            if (c.scalar_type() != at::kFloat || c.dim() != 2 || !c.is_contiguous())
-                refuse(what, "cos_sin", "a contiguous fp32 tensor [positions, rot]");
-            x.cos_sin = static_cast<const float *>(c.data_ptr());
-            x.n_positions = c.size(0);
-            x.rot = c.size(1);
-        }
-        x.rope_type = static_cast<int>(integer(a[8]));
-        x.dev_status = array_or_none<int32_t>(a[14], 1, what, "dev_status");
+        gguf_qk_rope_args x = rope_args(a, what);
+        x.positions = array<int32_t>(a[6], x.n_tokens, what, "positions");
         return PyLong_FromLong(api.rope(&x, stream(a[15])));
+    });
+}
+
+// the same, then sections (a tuple) and interleaved
+PyObject *qk_norm_mrope(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        const char *what = "gguf_qk_norm_mrope";
+        count(n, 18, what);
+        gguf_qk_rope_args x = rope_args(a, what);
+        gguf_rope_axes axes{};
+        if (!PyTuple_Check(a[16])) refuse(what, "sections", "a tuple of the pairs of each axis");
+        axes.n_axes = PyTuple_GET_SIZE(a[16]);
+        for (int64_t i = 0; i < axes.n_axes && i < GGUF_MAX_AXES; i++) {
+            const int64_t pairs = integer(PyTuple_GET_ITEM(a[16], i));
+            if (pairs < 0 || pairs > 65535) refuse(what, "sections", "the pairs of each axis");
+            axes.sections[i] = static_cast<int32_t>(pairs);
+        }
+        const at::Tensor &pos = tensor(a[6], what, "positions");
+        if (pos.scalar_type() != at::kInt || pos.dim() != 2 || pos.size(0) != axes.n_axes || pos.size(1) != x.n_tokens ||
+            (x.n_tokens > 1 && pos.stride(1) != 1))
+            refuse(what, "positions", "int32 [axes, tokens] with contiguous rows");
+        x.positions = static_cast<const int32_t *>(pos.data_ptr());
+        axes.ld_positions = axes.n_axes > 1 ? pos.stride(0) : x.n_tokens;
+        axes.interleaved = static_cast<int>(integer(a[17]));
+        return PyLong_FromLong(api.mrope(&x, &axes, stream(a[15])));
+    });
+}
+
+// [tokens, k] with contiguous rows, or none
+struct Flat {
+    void *p;
+    int type;
+    int64_t ld;
+};
+Flat flat(PyObject *o, int64_t t, int64_t k, const char *what, const char *name) {
+    if (o == Py_None) return {nullptr, GGUF_F32, k};
+    const at::Tensor &x = tensor(o, what, name);
+    if (x.dim() != 2 || x.size(0) != t || x.size(1) != k || (k > 1 && x.stride(1) != 1)) {
+        PyErr_Format(PyExc_ValueError, "%s: %s must be [%lld, %lld] with contiguous rows", what, name, (long long)t, (long long)k);
+        throw Bad();
+    }
+    return {x.data_ptr(), float_type(x.scalar_type(), what), t > 1 ? x.stride(0) : k};
+}
+
+// x, h, gate, gate_act, branch_scale, residual_scale, post kind, weight, bias, eps, pre kind, weight, bias, eps, h_out, z,
+// z_q8_1, stream
+PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        const char *what = "gguf_block_norm";
+        count(n, 18, what);
+        const at::Tensor &any = tensor(a[0] != Py_None ? a[0] : a[1], what, a[0] != Py_None ? "x" : "residual");
+        if (any.dim() != 2) refuse(what, "x and residual", "[tokens, k]");
+        const int64_t t = any.size(0), k = any.size(1);
+        gguf_block_norm_args x{};
+        x.n_tokens = t;
+        x.k = k;
+        const Flat fx = flat(a[0], t, k, what, "x"), fh = flat(a[1], t, k, what, "residual");
+        const Flat fo = flat(a[14], t, k, what, "residual_out"), fz = flat(a[15], t, k, what, "out");
+        x.ht = a[1] != Py_None ? fh.type : a[14] != Py_None ? fo.type : fx.type;
+        x.xt = a[0] != Py_None ? fx.type : x.ht;
+        if (a[14] != Py_None && fo.type != x.ht) refuse(what, "residual_out", "of the residual's dtype");
+        x.x = fx.p;
+        x.ldx = fx.ld;
+        x.h = fh.p;
+        x.ldh = fh.ld;
+        x.h_out = fo.p;
+        x.ldho = fo.ld;
+        x.z = fz.p;
+        x.zt = fz.type;
+        x.ldz = fz.ld;
+        x.gt = x.xt;
+        if (a[2] != Py_None) {
+            const at::Tensor &g = tensor(a[2], what, "gate");
+            if (g.dim() == 1 || (g.dim() == 2 && g.size(0) == 1 && t != 1)) {   // one row for all tokens
+                if (g.size(-1) != k || (k > 1 && g.stride(-1) != 1)) refuse(what, "gate", "[tokens, k] or [k] with contiguous rows");
+                x.gate = g.data_ptr();
+                x.gt = float_type(g.scalar_type(), what);
+                x.ldg = 0;
+            } else {
+                const Flat fg = flat(a[2], t, k, what, "gate");
+                x.gate = fg.p;
+                x.gt = fg.type;
+                x.ldg = fg.ld;
+            }
+        }
+        x.gate_act = static_cast<int>(integer(a[3]));
+        x.branch_scale = static_cast<float>(real(a[4]));
+        x.residual_scale = static_cast<float>(real(a[5]));
+        x.post_kind = static_cast<int>(integer(a[6]));
+        x.post_w = weights(a[7], k, what, "post_weight");
+        x.post_b = weights(a[8], k, what, "post_bias");
+        x.post_eps = static_cast<float>(real(a[9]));
+        x.pre_kind = static_cast<int>(integer(a[10]));
+        x.pre_w = weights(a[11], k, what, "pre_weight");
+        x.pre_b = weights(a[12], k, what, "pre_bias");
+        x.pre_eps = static_cast<float>(real(a[13]));
+        if (a[16] != Py_None) {
+            const at::Tensor &q = tensor(a[16], what, "out_q8_1");
+            if (q.scalar_type() != at::kByte || q.dim() != 2 || q.size(0) != t || !q.is_contiguous() || q.size(1) != k / 32 * 36)
+                refuse(what, "out_q8_1", "contiguous uint8 [tokens, k / 32 * 36]");
+            x.z_q8_1 = q.data_ptr();
+        }
+        return PyLong_FromLong(api.norm(&x, stream(a[17])));
     });
 }
 
@@ -289,21 +402,23 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// the addresses of gguf_kv_plan, gguf_qk_norm_rope, gguf_kv_get_rows, gguf_paged_attention_ws_size, gguf_paged_attention
-// and gguf_kv_page_bytes
+// the addresses of gguf_kv_plan, gguf_qk_norm_rope, gguf_kv_get_rows, gguf_paged_attention_ws_size, gguf_paged_attention,
+// gguf_kv_page_bytes, gguf_qk_norm_mrope and gguf_block_norm
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
-        count(n, 6, "bind");
-        void *p[6];
-        for (int i = 0; i < 6; i++) p[i] = reinterpret_cast<void *>(static_cast<intptr_t>(integer(a[i])));
+        count(n, 8, "bind");
+        void *p[8];
+        for (int i = 0; i < 8; i++) p[i] = reinterpret_cast<void *>(static_cast<intptr_t>(integer(a[i])));
         api = {reinterpret_cast<plan_fn>(p[0]), reinterpret_cast<rope_fn>(p[1]), reinterpret_cast<rows_fn>(p[2]),
-               reinterpret_cast<attn_ws_fn>(p[3]), reinterpret_cast<attn_fn>(p[4]), reinterpret_cast<page_fn>(p[5])};
+               reinterpret_cast<attn_ws_fn>(p[3]), reinterpret_cast<attn_fn>(p[4]), reinterpret_cast<page_fn>(p[5]),
+               reinterpret_cast<mrope_fn>(p[6]), reinterpret_cast<norm_fn>(p[7])};
         Py_RETURN_NONE;
     });
 }
 
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind), FAST(kv_plan), FAST(qk_norm_rope), FAST(kv_get_rows), FAST(paged_attention),
+                         FAST(qk_norm_mrope), FAST(block_norm),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

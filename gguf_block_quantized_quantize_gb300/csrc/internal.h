@@ -195,6 +195,25 @@ cudaError_t launch_moe_finalize(const float *z, const int32_t *pos, const int32_
                                 const float *route_w, int64_t T, int64_t top_k, int64_t n, void *y, int yt,
                                 cudaStream_t s);
 
+// ---- norms between the products (norm.cu)
+struct BlockNorm {   // gguf_block_norm; eps, scales and kinds as its arguments
+    const void *x, *h, *gate;
+    int64_t ldx, ldh, ldg;   // ldg 0: one row for all tokens
+    int gt, act;
+    int64_t n_tokens, k;
+    int post, pre;
+    const float *post_w, *post_b, *pre_w, *pre_b;
+    float post_eps, pre_eps, branch, resid;
+    void *h_out;
+    int64_t ldho;
+    void *z;
+    int zt;
+    int64_t ldz;
+    uint8_t *zq;
+};
+// vec: every row of x, h, gate, h_out and z, and the weights, are 16-byte aligned
+cudaError_t launch_block_norm(const BlockNorm &p, int xt, int ht, bool vec, cudaStream_t s);
+
 // ---- the paged Q4_0 key / value cache (layout: kv.cuh)
 struct KvPlan {   // gguf_kv_plan
     const int32_t *ctx, *add;
@@ -209,7 +228,7 @@ struct KvPlan {   // gguf_kv_plan
 };
 cudaError_t launch_kv_plan(const KvPlan &p, cudaStream_t s);
 
-struct QkRope {   // gguf_qk_norm_rope
+struct QkRope {   // gguf_qk_norm_rope and gguf_qk_norm_mrope
     const void *q, *k, *v;
     int64_t ldq, ldk, ldv, n_tokens, h, hk;
     int64_t rows;   // rows of a token to norm and rotate: h queries, then the keys
@@ -225,6 +244,9 @@ struct QkRope {   // gguf_qk_norm_rope
     int64_t n_pages, page;
     const int64_t *slots;
     int32_t *status;
+    int n_axes;              // positions of a token: pos[a * ldpos + t]
+    int64_t ldpos;
+    uint16_t axis_of[16];    // the axes of 8 pairs, 2 bits each
 };
 // vec: every row of q, k, v, q_out and k_out is 16-byte aligned
 cudaError_t launch_qk_norm_rope(const QkRope &p, int64_t d, int xt, bool vec, cudaStream_t s);

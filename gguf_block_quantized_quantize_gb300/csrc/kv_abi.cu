@@ -1,33 +1,13 @@
 // C ABI of the paged Q4_0 cache operators: argument checks, then one launcher
 // each.
-#include <stdarg.h>
-#include <stdio.h>
-
 #include <algorithm>
 
+#include "abi_checks.h"
 #include "common.cuh"
 #include "internal.h"
 #include "kv.cuh"
 
 namespace gg {
-
-static gguf_status refuse(gguf_status st, const char *fmt, ...) {
-    char buf[256];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
-    va_end(ap);
-    return report(st, buf);
-}
-static gguf_status launched(cudaError_t e, const char *what) {
-    if (e == cudaSuccess) return GGUF_OK;
-    return refuse(GGUF_ERR_CUDA, "%s: CUDA error %d (%s)", what, (int)e, cudaGetErrorString(e));
-}
-static bool float_type(int t) { return t == GGUF_F32 || t == GGUF_F16 || t == GGUF_BF16; }
-static int64_t float_size(int t) { return t == GGUF_F32 ? 4 : 2; }
-static bool at(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-// every row of an array of rows starts on 16 bytes (or there is none)
-static bool rows16(const void *p, int64_t ld, int64_t es) { return p == nullptr || (at(p, 16) && (ld * es) % 16 == 0); }
 
 // sizes that the cache operators share
 static gguf_status check_cache(const char *what, int64_t d, int64_t hk, int64_t page, int64_t n_pages) {
@@ -38,6 +18,70 @@ static gguf_status check_cache(const char *what, int64_t d, int64_t hk, int64_t 
         return refuse(GGUF_ERR_SHAPE, "%s: page_size=%lld is not a multiple of 16 up to 2^20", what, (long long)page);
     if (n_pages < 0 || n_pages > 0x7fffffff) return refuse(GGUF_ERR_INVALID_ARG, "%s: n_pages=%lld", what, (long long)n_pages);
     return GGUF_OK;
+}
+
+// one position a token (axes null), or a position on each axis
+static gguf_status qk_norm_rope(const gguf_qk_rope_args *a, const gguf_rope_axes *axes, const char *what, cudaStream_t stream) {
+    if (!a) return refuse(GGUF_ERR_INVALID_ARG, "%s: null args", what);
+    if (!float_type(a->xt)) return refuse(GGUF_ERR_UNSUPPORTED_TYPE, "%s: type %d is not F32/BF16/F16", what, a->xt);
+    const bool store = a->cache != nullptr, keys = store || a->k_out != nullptr;
+    const int64_t hk = keys ? a->n_kv_heads : 0, d = a->head_dim, es = float_size(a->xt);
+    if (a->n_tokens < 0 || a->n_heads < 0 || a->n_positions < 0 || a->rot < 0)
+        return refuse(GGUF_ERR_INVALID_ARG, "%s: negative size", what);
+    gguf_status st = check_cache(what, d, keys ? hk : 1, store ? a->page_size : KV_TILE, store ? a->n_pages : 0);
+    if (st != GGUF_OK) return st;
+    if (a->n_heads > 65535 || a->n_tokens > 0x7fffffff)
+        return refuse(GGUF_ERR_SHAPE, "%s: at most 65535 heads and 2^31 - 1 tokens", what);
+    if (a->rope_type != GGUF_ROPE_NORM && a->rope_type != GGUF_ROPE_NEOX)
+        return refuse(GGUF_ERR_INVALID_ARG, "%s: rope_type %d", what, a->rope_type);
+    if (a->rot % 16 || a->rot > d)
+        return refuse(GGUF_ERR_SHAPE, "%s: rot=%lld is not a multiple of 16 up to head_dim", what, (long long)a->rot);
+    if (axes) {
+        if (axes->n_axes < 1 || axes->n_axes > GGUF_MAX_AXES)
+            return refuse(GGUF_ERR_SHAPE, "%s: %lld axes (1..%d)", what, (long long)axes->n_axes, GGUF_MAX_AXES);
+        int64_t pairs = 0;
+        for (int i = 0; i < axes->n_axes; i++) {
+            if (axes->sections[i] < 0) return refuse(GGUF_ERR_INVALID_ARG, "%s: negative section", what);
+            pairs += axes->sections[i];
+        }
+        if (pairs != a->rot / 2)
+            return refuse(GGUF_ERR_SHAPE, "%s: the sections hold %lld pairs, rot=%lld has %lld", what, (long long)pairs, (long long)a->rot,
+                          (long long)(a->rot / 2));
+        if (axes->n_axes > 1 && axes->ld_positions < a->n_tokens)
+            return refuse(GGUF_ERR_INVALID_ARG, "%s: ld_positions=%lld < n_tokens", what, (long long)axes->ld_positions);
+    }
+    if (a->ldq < a->n_heads * d || a->ldqo < a->n_heads * d || (keys && a->ldk < hk * d) ||
+        (store && a->ldv < hk * d) || (a->k_out && a->ldko < hk * d))
+        return refuse(GGUF_ERR_INVALID_ARG, "%s: a row stride is shorter than the row", what);
+    if (a->n_tokens == 0 || a->n_heads + hk == 0) return GGUF_OK;
+    if (!a->positions || (a->n_heads > 0 && (!a->q || !a->q_out)) || (keys && !a->k) || (store && (!a->v || !a->slots)) ||
+        (a->rot > 0 && !a->cos_sin))
+        return refuse(GGUF_ERR_INVALID_ARG, "%s: null pointer", what);
+    if (!at(a->q, es) || !at(a->k, es) || !at(a->v, es) || !at(a->q_out, es) || !at(a->k_out, es) ||
+        !at(a->positions, 4) || !at(a->slots, 8) || !at(a->dev_status, 4))
+        return refuse(GGUF_ERR_ALIGNMENT, "%s: misaligned array", what);
+    if (!at(a->q_norm, 16) || !at(a->k_norm, 16) || !at(a->cos_sin, 16) || !at(a->cache, 16))
+        return refuse(GGUF_ERR_ALIGNMENT, "%s: q_norm, k_norm, cos_sin and cache must be 16-byte aligned", what);
+    QkRope p{a->q, a->k, a->v, a->ldq, a->ldk, a->ldv, a->n_tokens, a->n_heads, hk,
+                   a->n_heads + hk, a->q_norm, a->k_norm, a->eps, a->positions,
+                   a->cos_sin, a->rot > 0 ? a->n_positions : INT64_MAX, (int)a->rot, a->rope_type == GGUF_ROPE_NEOX, a->q_out, a->k_out,
+                   a->ldqo, a->ldko, (uint8_t *)a->cache, a->n_pages, a->page_size, a->slots, a->dev_status, 1, 0, {}};
+    if (axes) {
+        p.n_axes = (int)axes->n_axes;
+        p.ldpos = axes->ld_positions;
+        int left[GGUF_MAX_AXES] = {}, on = 0;   // pairs that an axis has left; the axis of the next pair
+        for (int i = 0; i < p.n_axes; i++) left[i] = axes->sections[i];
+        for (int i = 0; i < a->rot / 2; i++) {
+            while (left[on] == 0) on = (on + 1) % p.n_axes;
+            p.axis_of[i / 8] |= (uint16_t)(on << (2 * (i % 8)));
+            left[on]--;
+            if (axes->interleaved) on = (on + 1) % p.n_axes;
+        }
+    }
+    const bool vec = rows16(a->q, a->ldq, es) && rows16(keys ? a->k : nullptr, a->ldk, es) &&
+                     rows16(store ? a->v : nullptr, a->ldv, es) && rows16(a->q_out, a->ldqo, es) &&
+                     rows16(a->k_out, a->ldko, es);
+    return launched(launch_qk_norm_rope(p, d, a->xt, vec, stream), what);
 }
 
 }  // namespace gg
@@ -78,40 +122,12 @@ gguf_status gguf_kv_plan(const int32_t *ctx_len, const int32_t *new_len, int64_t
 }
 
 gguf_status gguf_qk_norm_rope(const gguf_qk_rope_args *a, gguf_stream_t stream) {
-    if (!a) return report(GGUF_ERR_INVALID_ARG, "qk_norm_rope: null args");
-    if (!float_type(a->xt)) return refuse(GGUF_ERR_UNSUPPORTED_TYPE, "qk_norm_rope: type %d is not F32/BF16/F16", a->xt);
-    const bool store = a->cache != nullptr, keys = store || a->k_out != nullptr;
-    const int64_t hk = keys ? a->n_kv_heads : 0, d = a->head_dim, es = float_size(a->xt);
-    if (a->n_tokens < 0 || a->n_heads < 0 || a->n_positions < 0 || a->rot < 0)
-        return report(GGUF_ERR_INVALID_ARG, "qk_norm_rope: negative size");
-    gguf_status st = check_cache("qk_norm_rope", d, keys ? hk : 1, store ? a->page_size : KV_TILE, store ? a->n_pages : 0);
-    if (st != GGUF_OK) return st;
-    if (a->n_heads > 65535 || a->n_tokens > 0x7fffffff)
-        return report(GGUF_ERR_SHAPE, "qk_norm_rope: at most 65535 heads and 2^31 - 1 tokens");
-    if (a->rope_type != GGUF_ROPE_NORM && a->rope_type != GGUF_ROPE_NEOX)
-        return refuse(GGUF_ERR_INVALID_ARG, "qk_norm_rope: rope_type %d", a->rope_type);
-    if (a->rot % 16 || a->rot > d)
-        return refuse(GGUF_ERR_SHAPE, "qk_norm_rope: rot=%lld is not a multiple of 16 up to head_dim", (long long)a->rot);
-    if (a->ldq < a->n_heads * d || a->ldqo < a->n_heads * d || (keys && a->ldk < hk * d) ||
-        (store && a->ldv < hk * d) || (a->k_out && a->ldko < hk * d))
-        return report(GGUF_ERR_INVALID_ARG, "qk_norm_rope: a row stride is shorter than the row");
-    if (a->n_tokens == 0 || a->n_heads + hk == 0) return GGUF_OK;
-    if (!a->positions || (a->n_heads > 0 && (!a->q || !a->q_out)) || (keys && !a->k) || (store && (!a->v || !a->slots)) ||
-        (a->rot > 0 && !a->cos_sin))
-        return report(GGUF_ERR_INVALID_ARG, "qk_norm_rope: null pointer");
-    if (!at(a->q, es) || !at(a->k, es) || !at(a->v, es) || !at(a->q_out, es) || !at(a->k_out, es) ||
-        !at(a->positions, 4) || !at(a->slots, 8) || !at(a->dev_status, 4))
-        return report(GGUF_ERR_ALIGNMENT, "qk_norm_rope: misaligned array");
-    if (!at(a->q_norm, 16) || !at(a->k_norm, 16) || !at(a->cos_sin, 16) || !at(a->cache, 16))
-        return report(GGUF_ERR_ALIGNMENT, "qk_norm_rope: q_norm, k_norm, cos_sin and cache must be 16-byte aligned");
-    const QkRope p{a->q, a->k, a->v, a->ldq, a->ldk, a->ldv, a->n_tokens, a->n_heads, hk,
-                   a->n_heads + hk, a->q_norm, a->k_norm, a->eps, a->positions,
-                   a->cos_sin, a->rot > 0 ? a->n_positions : INT64_MAX, (int)a->rot, a->rope_type == GGUF_ROPE_NEOX, a->q_out, a->k_out,
-                   a->ldqo, a->ldko, (uint8_t *)a->cache, a->n_pages, a->page_size, a->slots, a->dev_status};
-    const bool vec = rows16(a->q, a->ldq, es) && rows16(keys ? a->k : nullptr, a->ldk, es) &&
-                     rows16(store ? a->v : nullptr, a->ldv, es) && rows16(a->q_out, a->ldqo, es) &&
-                     rows16(a->k_out, a->ldko, es);
-    return launched(launch_qk_norm_rope(p, d, a->xt, vec, (cudaStream_t)stream), "qk_norm_rope");
+    return qk_norm_rope(a, nullptr, "qk_norm_rope", (cudaStream_t)stream);
+}
+
+gguf_status gguf_qk_norm_mrope(const gguf_qk_rope_args *a, const gguf_rope_axes *axes, gguf_stream_t stream) {
+    if (!axes) return report(GGUF_ERR_INVALID_ARG, "qk_norm_mrope: null axes");
+    return qk_norm_rope(a, axes, "qk_norm_mrope", (cudaStream_t)stream);
 }
 
 gguf_status gguf_kv_get_rows(const void *cache, int64_t n_pages, int64_t page_size, int64_t n_kv_heads,

@@ -1,8 +1,9 @@
-// gguf_qk_norm_rope and gguf_kv_get_rows: what happens to a token's query, key
+// gguf_qk_norm_rope, gguf_qk_norm_mrope and gguf_kv_get_rows: what happens to a token's query, key
 // and value rows between their products and the attention.
 //
 //   y = x / sqrt(mean(x^2) + eps) * w             (queries and keys, per head)
 //   (a, b) -> (a cos - b sin, b cos + a sin)      (pairs of the first rot values)
+//                                                 (at pos, or each pair at the position of its axis)
 //   queries to q_out; keys (and values, untouched) to Q4_0 in their cache slot:
 //   d = fp16(the value of largest magnitude / -8), code = clamp(roundf(x / d) + 8, 0, 15).
 //
@@ -166,6 +167,45 @@ struct Raw8 {
     }
 };
 
+// the positions of a token on its axes; -1: left out (padding: negative on some axis, or past the table: then `past` is set)
+template <int AXES>
+__device__ __forceinline__ bool token_positions(const QkRope &p, int64_t t, int64_t (&pos)[AXES], bool &past) {
+    bool there = true;
+    past = false;
+#pragma unroll
+    for (int a = 0; a < AXES; a++) {
+        pos[a] = a == 0 || a < p.n_axes ? p.pos[a * p.ldpos + t] : 0;
+        there &= pos[a] >= 0;
+        past |= pos[a] >= p.n_pos;
+    }
+    past &= there;
+    return there && !past;
+}
+// N cosines and sines of pairs i .. of a token, a pair's from the row of its axis
+template <int AXES, int N>
+__device__ __forceinline__ void angles(const QkRope &p, const int64_t (&pos)[AXES], int i, float (&cs)[8], float (&sn)[8]) {
+    const int half = p.rot / 2;
+    const uint32_t of = AXES == 1 ? 0 : (uint32_t)p.axis_of[i >> 3] >> (2 * (i & 7));   // 2 bits a pair
+#pragma unroll
+    for (int a = 0; a < AXES; a++) {
+        uint32_t mine = 0;   // the pairs on this axis
+#pragma unroll
+        for (int x = 0; x < N; x++) mine |= ((of >> (2 * x)) & 3) == a ? 1u << x : 0u;
+        if (AXES > 1 && mine == 0) continue;
+        const float *row = p.cos_sin + pos[a] * p.rot + i;
+        float c[N], s[N];
+#pragma unroll
+        for (int x = 0; x < N; x += 4) {
+            const float4 u = *reinterpret_cast<const float4 *>(row + x), v = *reinterpret_cast<const float4 *>(row + half + x);
+            c[x] = u.x; c[x + 1] = u.y; c[x + 2] = u.z; c[x + 3] = u.w;
+            s[x] = v.x; s[x + 1] = v.y; s[x + 2] = v.z; s[x + 3] = v.w;
+        }
+#pragma unroll
+        for (int x = 0; x < N; x++)
+            if (AXES == 1 || (mine >> x) & 1) { cs[x] = c[x]; sn[x] = s[x]; }
+    }
+}
+
 // the tile (of KV head 0) and the token in it of a slot; null: nothing to store
 template <int D>
 __device__ __forceinline__ uint8_t *slot_tile(const QkRope &p, int64_t slot, int &tok) {
@@ -182,7 +222,7 @@ constexpr int QR_ROWS = 4;   // rows that a group loads together (1, 2 and 8 wer
 
 // blocks [0, qk_blocks): groups of D / 8 lanes, `groups` per token, over the rows of q and k; the blocks after them: a
 // warp per 8 tokens and 32-value block of v
-template <int D, int T, bool VEC>
+template <int D, int T, bool VEC, int AXES>
 __global__ void __launch_bounds__(QR_THREADS, 4) qk_norm_rope_kernel(const QkRope p, int groups, int qk_blocks) {
     constexpr int LPR = D / 8, NB = D / 32;   // lanes per row, blocks per row
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -201,9 +241,10 @@ __global__ void __launch_bounds__(QR_THREADS, 4) qk_norm_rope_kernel(const QkRop
         if (in) {
             raw.template load<VEC>(p.v, t * p.ldv + (int64_t)head * D + 32 * b + 8 * l4);
             const int64_t slot = p.slots[t];
-            const int32_t pos = p.pos[t];
+            int64_t pos[AXES];
+            bool past;
             raw.floats(v);
-            if (pos >= 0 && pos < p.n_pos) tile = slot_tile<D>(p, slot, tok);
+            if (token_positions<AXES>(p, t, pos, past)) tile = slot_tile<D>(p, slot, tok);
         }
         uint32_t code[8];
         const uint16_t d = q4_block(v, lane, 0xffffffffu, 8, code);
@@ -222,7 +263,9 @@ __global__ void __launch_bounds__(QR_THREADS, 4) qk_norm_rope_kernel(const QkRop
     const int64_t t = (uint64_t)gid >> 32 ? gid / groups : (int64_t)((uint32_t)gid / (uint32_t)groups);
     const int g0 = (int)(gid - t * groups);
     if (t >= p.n_tokens) return;   // whole groups of lanes
-    const int64_t pos = p.pos[t];
+    int64_t pos[AXES];
+    bool past;
+    const bool there = token_positions<AXES>(p, t, pos, past);
     const int64_t slot = p.slots != nullptr ? p.slots[t] : -1;
     const int rot = p.rot, half = rot / 2, rows = (int)p.rows;
     constexpr int ES = T == GGUF_F32 ? 4 : 2;
@@ -236,8 +279,8 @@ __global__ void __launch_bounds__(QR_THREADS, 4) qk_norm_rope_kernel(const QkRop
         const int r = g0 + i * groups;
         if (r < rows) raw[i].template load<VEC>((r < h ? q0 : k0) + r * (D * ES), 0);
     }
-    if (pos < 0 || pos >= p.n_pos) {   // a padding token (-1), or one past the table
-        if (pos >= p.n_pos && p.status != nullptr && g0 == 0 && l == 0) atomicAdd(p.status, 1);
+    if (!there) {   // a padding token (-1), or one past the table
+        if (past && p.status != nullptr && g0 == 0 && l == 0) atomicAdd(p.status, 1);
         return;
     }
     const bool turns = 8 * l < rot, low = 8 * l < half;
@@ -245,18 +288,12 @@ __global__ void __launch_bounds__(QR_THREADS, 4) qk_norm_rope_kernel(const QkRop
     // values whose partners are half / 8 lanes away
     float cs[8], sn[8];
     if (turns) {
-        const float *row = p.cos_sin + pos * rot;
         if (p.neox) {
-            const int i = low ? 8 * l : 8 * l - half;
-            ld8<GGUF_F32, true>(row, i, cs);
-            ld8<GGUF_F32, true>(row, half + i, sn);
+            angles<AXES, 8>(p, pos, low ? 8 * l : 8 * l - half, cs, sn);
 #pragma unroll
             for (int x = 0; x < 8; x++) sn[x] = low ? -sn[x] : sn[x];
         } else {
-            const float4 c = *reinterpret_cast<const float4 *>(row + 4 * l);
-            const float4 s = *reinterpret_cast<const float4 *>(row + half + 4 * l);
-            cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
-            sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w;
+            angles<AXES, 4>(p, pos, 4 * l, cs, sn);
         }
     }
     int tok = 0;
@@ -386,12 +423,15 @@ static cudaError_t launch_pdl(const void *kern, int64_t grid, cudaStream_t s, vo
     return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
-template <int D>
+template <int D, int AXES>
 static const void *rope_kernel(int t, bool vec) {
-    if (t == GGUF_F32) return vec ? (const void *)qk_norm_rope_kernel<D, GGUF_F32, true> : (const void *)qk_norm_rope_kernel<D, GGUF_F32, false>;
-    if (t == GGUF_F16) return vec ? (const void *)qk_norm_rope_kernel<D, GGUF_F16, true> : (const void *)qk_norm_rope_kernel<D, GGUF_F16, false>;
-    return vec ? (const void *)qk_norm_rope_kernel<D, GGUF_BF16, true> : (const void *)qk_norm_rope_kernel<D, GGUF_BF16, false>;
+    if (t == GGUF_F32) return vec ? (const void *)qk_norm_rope_kernel<D, GGUF_F32, true, AXES> : (const void *)qk_norm_rope_kernel<D, GGUF_F32, false, AXES>;
+    if (t == GGUF_F16) return vec ? (const void *)qk_norm_rope_kernel<D, GGUF_F16, true, AXES> : (const void *)qk_norm_rope_kernel<D, GGUF_F16, false, AXES>;
+    return vec ? (const void *)qk_norm_rope_kernel<D, GGUF_BF16, true, AXES> : (const void *)qk_norm_rope_kernel<D, GGUF_BF16, false, AXES>;
 }
+// one position a token, or up to four
+template <int D>
+static const void *rope_kernel(int t, bool vec, int axes) { return axes == 1 ? rope_kernel<D, 1>(t, vec) : rope_kernel<D, 4>(t, vec); }
 
 cudaError_t launch_qk_norm_rope(const QkRope &p, int64_t d, int xt, bool vec, cudaStream_t s) {
     // a group per row for few tokens, four rows per group once that fills the GPU (2048 threads per SM)
@@ -403,7 +443,7 @@ cudaError_t launch_qk_norm_rope(const QkRope &p, int64_t d, int xt, bool vec, cu
     const int64_t v_warps = p.cache != nullptr ? (p.n_tokens + 7) / 8 * p.hk * (d / 32) : 0;
     const int64_t grid = qk_blocks + (v_warps * 32 + QR_THREADS - 1) / QR_THREADS;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    const void *kern = d == 64 ? rope_kernel<64>(xt, vec) : d == 128 ? rope_kernel<128>(xt, vec) : rope_kernel<256>(xt, vec);
+    const void *kern = d == 64 ? rope_kernel<64>(xt, vec, p.n_axes) : d == 128 ? rope_kernel<128>(xt, vec, p.n_axes) : rope_kernel<256>(xt, vec, p.n_axes);
     QkRope a = p;
     int g = (int)groups, qb = (int)qk_blocks;
     void *args[3] = {&a, &g, &qb};

@@ -1,0 +1,310 @@
+// gguf_block_norm: what stands between the product that ends a block and the
+// product that begins the next one.
+//
+//   y  = act(g) * N_post(x)          N: RMS   v / sqrt(mean v^2 + eps) * w + b
+//   h' = rs * h + bs * y                LAYER (v - mean) / sqrt(mean (v - mean)^2 + eps) * w + b
+//   z  = N_pre(h')                   as floats, and / or as q8_1 blocks
+//
+// One pass: a row lies in the registers of 32 to 512 threads from its loads to
+// its stores, so x, h and g are read once and h', z and the blocks written once;
+// nothing in between goes to memory, and every step of it is fp32 (h' is rounded
+// for its store, but the next norm takes the sum before that rounding, z's blocks
+// are quantized from fp32).  A sum over the row is a tree within each warp, then the
+// warps' sums in order: the same bits on every run and in every thread.  LAYER takes
+// the mean first and the squares of the differences from it after, from registers.
+//
+// Aligned rows: a thread holds 8 consecutive values of each of its C chunks,
+// four threads a q8_1 block.  Other rows: values a row width of threads apart,
+// single loads that lie side by side, a warp a q8_1 block.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace gg {
+
+constexpr int BN_THREADS = 512;
+
+__device__ __forceinline__ float bn_from16(int t, uint32_t h) { return t == GGUF_BF16 ? bf2f((uint16_t)h) : h2f((uint16_t)h); }
+__device__ __forceinline__ uint32_t bn_to16(int t, float f) { return t == GGUF_BF16 ? f2bf_rn(f) : f2h_rn(f); }
+
+// n values of a chunk (8, or fewer in the last one) from element `at`, which is 16-byte aligned
+__device__ __forceinline__ void bn_ld8(const void *x, int t, int64_t at, int n, float (&v)[8]) {
+    if (n == 8) {
+        if (t == GGUF_F32) {
+            const float4 *p = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(x) + at);
+            const float4 a = p[0], b = p[1];
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+            const uint4 a = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(x) + at);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                v[2 * i] = bn_from16(t, w[i] & 0xffff);
+                v[2 * i + 1] = bn_from16(t, w[i] >> 16);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            v[i] = i >= n ? 0.0f : t == GGUF_F32 ? reinterpret_cast<const float *>(x)[at + i] : bn_from16(t, reinterpret_cast<const uint16_t *>(x)[at + i]);
+    }
+}
+__device__ __forceinline__ void bn_st8(void *x, int t, int64_t at, int n, const float (&v)[8]) {
+    if (n == 8) {
+        if (t == GGUF_F32) {
+            float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(x) + at);
+            p[0] = make_float4(v[0], v[1], v[2], v[3]);
+            p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) w[i] = bn_to16(t, v[2 * i]) | bn_to16(t, v[2 * i + 1]) << 16;
+            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(x) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < n) store_out(x, t, at + i, v[i]);
+    }
+}
+
+// the thread's part of a row
+template <int C, bool VEC>
+struct RowPart {
+    int tid, threads, k;
+    __device__ __forceinline__ int chunk(int c) const { return (c * threads + tid) * 8; }              // VEC: first value
+    __device__ __forceinline__ int left(int c) const { return min(max(k - chunk(c), 0), 8); }          // VEC: its values
+    __device__ __forceinline__ int one(int c, int i) const { return (c * 8 + i) * threads + tid; }     // else: value i
+    __device__ __forceinline__ bool has(int c, int i) const { return (VEC ? chunk(c) + i : one(c, i)) < k; }
+    __device__ __forceinline__ void load(const void *x, int t, int64_t row, float (&v)[C][8]) const {
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+            if constexpr (VEC) bn_ld8(x, t, row + chunk(c), left(c), v[c]);
+            else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int e = one(c, i);
+                    v[c][i] = e >= k ? 0.0f : t == GGUF_F32 ? reinterpret_cast<const float *>(x)[row + e]
+                                                            : bn_from16(t, reinterpret_cast<const uint16_t *>(x)[row + e]);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(void *x, int t, int64_t row, const float (&v)[C][8]) const {
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+            if constexpr (VEC) bn_st8(x, t, row + chunk(c), left(c), v[c]);
+            else {
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    if (one(c, i) < k) store_out(x, t, row + one(c, i), v[c][i]);
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ float row_sum(float v, float *part, int warps) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (warps == 1) return v;   // a row per warp
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0f;
+    for (int w = 0; w < warps; w++) v += part[w];
+    return v;
+}
+
+// v <- N(v); part: two arrays of partial sums that nothing else uses
+template <int C, bool VEC>
+__device__ __forceinline__ void normed(const RowPart<C, VEC> &r, int kind, const float *w, const float *b, float eps, float inv_k,
+                                       float (&v)[C][8], float (*part)[BN_THREADS / 32], int warps) {
+    if (kind == GGUF_NORM_NONE) return;
+    if (kind == GGUF_NORM_LAYER) {
+        float s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) s += v[c][i];   // (zeros past the row)
+        const float mean = row_sum(s, part[0], warps) * inv_k;
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[c][i] = r.has(c, i) ? v[c][i] - mean : 0.0f;
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+        for (int i = 0; i < 8; i++) s = fmaf(v[c][i], v[c][i], s);
+    const float inv = __frsqrt_rn(fmaf(row_sum(s, part[1], warps), inv_k, eps));
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[c][i] *= inv;
+    float wv[C][8];
+    if (w != nullptr) {
+        r.load(w, GGUF_F32, 0, wv);
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[c][i] *= wv[c][i];
+    }
+    if (b != nullptr) {
+        r.load(b, GGUF_F32, 0, wv);
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[c][i] += wv[c][i];
+    }
+}
+
+// roundf(v / d) of N values (ties away from zero; 0 with d == 0).  v * (1 / d) is within 2^-21 of the quotient relatively
+// and the quotient below 128, so within 2^-14, which decides the rounding unless it lies that near to a half, or d is so
+// small that 1 / d or the products might not be ordinary numbers: then the division itself does.  Adding 1.5 * 2^23 leaves
+// the rounded quotient in the low bits.
+template <int N>
+__device__ __forceinline__ void q8_codes(const float (&v)[N], float d, int (&q)[N]) {
+    const float inv = __frcp_rn(d);
+    bool near = !(d > 0x1p-100f);
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const float t = __fmul_rn(v[i], inv), r = __fadd_rn(t, kI2fBias);
+        near |= !(fabsf(__fsub_rn(t, __fsub_rn(r, kI2fBias))) < 0.5f - 0x1p-13f);
+        q[i] = __float_as_int(r) - 0x4B400000;
+    }
+    if (near) {
+#pragma unroll
+        for (int i = 0; i < N; i++) q[i] = d != 0.0f ? min(max((int)roundf(__fdiv_rn(v[i], d)), -127), 127) : 0;
+    }
+}
+
+template <int XT, int HT, int C, bool VEC>
+__global__ void __launch_bounds__(BN_THREADS) block_norm_kernel(const BlockNorm p) {
+    __shared__ float part[4][BN_THREADS / 32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    if (t >= p.n_tokens) return;   // whole warps, and rows of several warps have no other in their CTA
+    const RowPart<C, VEC> r{(int)threadIdx.x, (int)blockDim.x, (int)p.k};
+    const int warps = blockDim.x >> 5;
+    const float inv_k = 1.0f / (float)(int)p.k;
+    float v[C][8], o[C][8];
+    constexpr bool EARLY = C < 8;   // h is asked for before the norm of x: what registers there are for it
+    if (EARLY && p.h != nullptr) r.load(p.h, HT, t * p.ldh, o);
+    if (p.x != nullptr) {
+        r.load(p.x, XT, t * p.ldx, v);
+        normed(r, p.post, p.post_w, p.post_b, p.post_eps, inv_k, v, part, warps);
+        if (p.gate != nullptr) {
+            float g[C][8];
+            r.load(p.gate, p.gt, t * p.ldg, g);
+#pragma unroll
+            for (int c = 0; c < C; c++)
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    float a = g[c][i];
+                    if (p.act == GGUF_GATE_TANH) a = tanhf(a);
+                    else if (p.act != GGUF_GATE_NONE) a = __fdiv_rn(p.act == GGUF_GATE_SILU ? a : 1.0f, 1.0f + expf(-a));
+                    v[c][i] *= a;
+                }
+        }
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[c][i] *= p.branch;
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[c][i] = 0.0f;
+    }
+    if (p.h != nullptr) {
+        if (!EARLY) r.load(p.h, HT, t * p.ldh, o);
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[c][i] = fmaf(o[c][i], p.resid, v[c][i]);
+    }
+    if (p.h_out != nullptr) r.store(p.h_out, HT, t * p.ldho, v);
+    if (p.z == nullptr && p.zq == nullptr) return;
+    normed(r, p.pre, p.pre_w, p.pre_b, p.pre_eps, inv_k, v, part + 2, warps);
+    if (p.z != nullptr) r.store(p.z, p.zt, t * p.ldz, v);
+    if (p.zq == nullptr) return;
+    uint8_t *row = p.zq + t * (p.k / QK8 * Q8_1_BYTES);
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+        if constexpr (VEC) {
+            const int at = r.chunk(c), j = threadIdx.x & 3;
+            float amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; i++) amax = fmaxf(amax, fabsf(v[c][i]));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            const float d = __fdiv_rn(amax, 127.0f);
+            int q[8], sum = 0;
+            q8_codes<8>(v[c], d, q);
+#pragma unroll
+            for (int i = 0; i < 8; i++) sum += q[i];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if (at < r.k) {   // (k is a multiple of 32: whole blocks)
+                uint32_t *to = reinterpret_cast<uint32_t *>(row + at / QK8 * Q8_1_BYTES);
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+                    to[1 + 2 * j + i] = (q[4 * i] & 0xff) | (q[4 * i + 1] & 0xff) << 8 | (q[4 * i + 2] & 0xff) << 16 | (uint32_t)q[4 * i + 3] << 24;
+                if (j == 0) to[0] = f2h_rn(d) | (uint32_t)f2h_rn(__fmul_rn(d, (float)sum)) << 16;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int at = r.one(c, i);
+                float amax = fabsf(v[c][i]);
+#pragma unroll
+                for (int s = 1; s < 32; s <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+                const float d = __fdiv_rn(amax, 127.0f), one[1] = {v[c][i]};
+                int q[1];
+                q8_codes<1>(one, d, q);
+                const int sum = __reduce_add_sync(0xffffffffu, q[0]);
+                if (at >= r.k) continue;
+                uint8_t *to = row + at / QK8 * Q8_1_BYTES;
+                to[4 + at % QK8] = (uint8_t)q[0];
+                if (at % QK8 == 0) *reinterpret_cast<uint32_t *>(to) = f2h_rn(d) | (uint32_t)f2h_rn(__fmul_rn(d, (float)sum)) << 16;
+            }
+        }
+    }
+}
+
+template <int XT, int HT, bool VEC>
+static const void *norm_kernel(int c) {
+    return c == 1 ? (const void *)block_norm_kernel<XT, HT, 1, VEC> : c == 2 ? (const void *)block_norm_kernel<XT, HT, 2, VEC>
+         : c == 4 ? (const void *)block_norm_kernel<XT, HT, 4, VEC> : (const void *)block_norm_kernel<XT, HT, 8, VEC>;
+}
+template <bool VEC>
+static const void *norm_kernel(int xt, int ht, int c) {
+    if (xt == GGUF_F32) return norm_kernel<GGUF_F32, GGUF_F32, VEC>(c);
+    if (xt == GGUF_BF16)
+        return ht == GGUF_F32 ? norm_kernel<GGUF_BF16, GGUF_F32, VEC>(c) : norm_kernel<GGUF_BF16, GGUF_BF16, VEC>(c);
+    return ht == GGUF_F32 ? norm_kernel<GGUF_F16, GGUF_F32, VEC>(c) : norm_kernel<GGUF_F16, GGUF_F16, VEC>(c);
+}
+
+cudaError_t launch_block_norm(const BlockNorm &p, int xt, int ht, bool vec, cudaStream_t s) {
+    const int64_t eighths = (p.k + 7) / 8;
+    int c = 1;
+    while (eighths > (int64_t)BN_THREADS * c) c *= 2;
+    const int threads = (int)std::max<int64_t>(32, ((eighths + c - 1) / c + 31) / 32 * 32);
+    const int rows = threads == 32 ? 4 : 1;   // a row per warp needs no others of its CTA
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.n_tokens + rows - 1) / rows));
+    cfg.blockDim = dim3(threads, rows);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    BlockNorm a = p;
+    void *args[1] = {&a};
+    return cudaLaunchKernelExC(&cfg, vec ? norm_kernel<true>(xt, ht, c) : norm_kernel<false>(xt, ht, c), args);
+}
+
+}  // namespace gg

@@ -498,6 +498,71 @@ gguf_status gguf_device_errors(int32_t *flags, int clear, gguf_stream_t stream);
 gguf_status gguf_device_errors_async(int32_t *dev_flags, int clear, gguf_stream_t stream);
 
 /*
+ * gguf_block_norm -- from the end of one block to the start of the next, in one
+ * pass over the rows:
+ *   y  = gate_act(gate) * N_post(x)
+ *   h' = residual_scale * h + branch_scale * y
+ *   z  = N_pre(h')
+ * x is a block's output (the product that ends it), h the residual stream, z the
+ * input of the next block's products, as floats, as q8_1 rows (which
+ * gguf_mul_mat and its kin take as GGUF_Q8_1), or both.
+ *   N          : GGUF_NORM_RMS    v / sqrt(mean(v^2) + eps) * w + b
+ *                GGUF_NORM_LAYER  (v - mean(v)) / sqrt(mean((v - mean)^2) + eps) * w + b
+ *                GGUF_NORM_NONE   v; w and b are not looked at
+ *                Weights w and biases b are [k] fp32, or NULL (1 and 0).
+ *   x, xt, ldx : [n_tokens][ldx] of type xt (F32, BF16, F16), or NULL: y = 0 (the
+ *                norm before the first block).  Then there is no gate and no post norm.
+ *   h, ht, ldh : [n_tokens][ldh] of type ht, which is xt or F32, or NULL: h' is
+ *                branch_scale * y.
+ *   gate       : [n_tokens][ldg] of type gt (xt or F32), or NULL: no gate.  ldg = 0:
+ *                one row for all tokens.  gate_act: NONE g, SIGMOID 1 / (1 + e^-g),
+ *                TANH, SILU g / (1 + e^-g); the gate's values are finite.
+ *   h_out      : h' rounded to type ht, [n_tokens][ldho], or NULL.
+ *   z, zt, ldz : [n_tokens][ldz] of type zt (F32, BF16, F16), or NULL.
+ *   z_q8_1     : [n_tokens][k / 32] q8_1 blocks as gguf_quantize_q8_1 makes them from
+ *                the fp32 values of z, or NULL.  Needs k % 32 == 0.
+ * 1 <= k <= 32768.  Everything between the loads and the stores is fp32: z comes
+ * from h' before its rounding.  h_out may be h, and z may be x, with the same type
+ * and stride; otherwise outputs do not overlap inputs.  Rows (and weights) that all
+ * start on 16 bytes are read 16 bytes at a time.  NaN and infinities of a row stay
+ * in its own outputs (unspecified q8_1 blocks).  Same bits on every run.
+ */
+#define GGUF_NORM_NONE 0
+#define GGUF_NORM_RMS 1
+#define GGUF_NORM_LAYER 2
+#define GGUF_GATE_NONE 0
+#define GGUF_GATE_SIGMOID 1
+#define GGUF_GATE_TANH 2
+#define GGUF_GATE_SILU 3
+typedef struct gguf_block_norm_args {
+    const void *x;
+    int xt;
+    int64_t ldx;
+    const void *h;
+    int ht;
+    int64_t ldh;
+    const void *gate;
+    int gt;
+    int64_t ldg;
+    int gate_act;
+    int64_t n_tokens, k;
+    int post_kind;
+    const float *post_w, *post_b;
+    float post_eps;
+    int pre_kind;
+    const float *pre_w, *pre_b;
+    float pre_eps;
+    float branch_scale, residual_scale;
+    void *h_out;
+    int64_t ldho;
+    void *z;
+    int zt;
+    int64_t ldz;
+    void *z_q8_1;
+} gguf_block_norm_args;
+gguf_status gguf_block_norm(const gguf_block_norm_args *args, gguf_stream_t stream);
+
+/*
  * The paged Q4_0 key / value cache and the operators on it: what stands
  * between the q / k / v products of a layer and its output product in a decode
  * or prefill step.
@@ -599,6 +664,30 @@ typedef struct gguf_qk_rope_args {
     int32_t *dev_status;
 } gguf_qk_rope_args;
 gguf_status gguf_qk_norm_rope(const gguf_qk_rope_args *args, gguf_stream_t stream);
+
+/*
+ * gguf_qk_norm_mrope -- gguf_qk_norm_rope for tokens with positions on several
+ * axes (text, images and video: time, height, width): each of the rot / 2 pairs
+ * turns by its angle at the token's position on one of the axes.
+ *   args->positions : [n_axes][ld_positions] int32.  A token that is negative on
+ *                     any axis is left out as padding; one that is at or past
+ *                     n_positions on any is left out and counted, once.
+ *   sections        : pairs of each axis; together rot / 2.
+ *   interleaved     : 0: the first sections[0] pairs are on axis 0, the next
+ *                     sections[1] on axis 1, ..; else: the axes take pairs in turn,
+ *                     each as long as it has some left (0 1 2 0 1 2 .. 0 0 for
+ *                     24, 20, 20).
+ * All axes read the one table cos_sin, pair i its columns i and rot / 2 + i.
+ * Everything else is as gguf_qk_norm_rope; with equal positions on all axes the
+ * results are its, bit for bit.
+ */
+#define GGUF_MAX_AXES 4
+typedef struct gguf_rope_axes {
+    int64_t n_axes, ld_positions;
+    int32_t sections[GGUF_MAX_AXES];
+    int interleaved;
+} gguf_rope_axes;
+gguf_status gguf_qk_norm_mrope(const gguf_qk_rope_args *args, const gguf_rope_axes *axes, gguf_stream_t stream);
 
 /*
  * gguf_kv_get_rows -- keys and values of n cache slots as floats:
