@@ -147,6 +147,10 @@ SIGNATURES = {
     "gguf_kv_get_rows": (_i, [_p, _i64, _i64, _i64, _i64, _p, _i64, _p, _p, _i, _p]),
     "gguf_paged_attention_ws_size": (_sz, [ctypes.POINTER(AttnArgs)]),
     "gguf_paged_attention": (_i, [ctypes.POINTER(AttnArgs), _p, _sz, _p]),
+    "gguf_prefix_plan_bytes": (_i64, [_i64, _i64, _i64]),
+    "gguf_prefix_plan": (_i, [_p, _p, _i64, _p, _p, _i64, _i64, _i64, _p, _sz, _p]),
+    "gguf_prefix_attention_ws_size": (_sz, [ctypes.POINTER(AttnArgs), _i64]),
+    "gguf_prefix_attention": (_i, [ctypes.POINTER(AttnArgs), _p, _i64, _p, _sz, _p]),
     "gguf_debug_block_dots": (_i, [_p, _i, _i64, _i64, _p, _i64, _p, _p]),
     "gguf_set_option": (_i, [ctypes.c_char_p, _i64]),
     "gguf_get_option": (_i64, [ctypes.c_char_p]),
@@ -521,7 +525,8 @@ def _bound():
 
         _bind.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "gguf_kv_plan", "gguf_qk_norm_rope", "gguf_kv_get_rows", "gguf_paged_attention_ws_size", "gguf_paged_attention",
-            "gguf_kv_page_bytes", "gguf_qk_norm_mrope", "gguf_block_norm")))
+            "gguf_kv_page_bytes", "gguf_qk_norm_mrope", "gguf_block_norm", "gguf_prefix_plan", "gguf_prefix_attention_ws_size",
+            "gguf_prefix_attention", "gguf_prefix_plan_bytes")))
         _native = _bind
     return _native
 
@@ -637,6 +642,45 @@ def gguf_paged_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torc
                     dev_status, 0)
         ws = _workspace(need, q.device)
     st = call(q, cache, block_table, q_start, kv_len, n_kv_heads, page_size, max_q_len, scale, window, sinks, out, ws,
+              dev_status, _stream())
+    if st:
+        _check(st)
+    return out
+
+
+def gguf_prefix_plan_bytes(n_requests: int, n_groups: int, n_tokens: int) -> int:
+    """Bytes of a plan of gguf_prefix_plan; -1 for unsupported sizes."""
+    return int(_lib_fast().gguf_prefix_plan_bytes(n_requests, n_groups, n_tokens))
+
+
+def gguf_prefix_plan(q_start: torch.Tensor, kv_len: torch.Tensor, group_start: torch.Tensor, prefix_len: torch.Tensor,
+                     page_size: int, n_tokens: int, out: torch.Tensor | None = None) -> torch.Tensor:
+    """What the requests of a step share, for gguf_prefix_attention (one launch, no host sync; once for all layers):
+    group g is requests group_start[g] .. group_start[g + 1] - 1, which have their first prefix_len[g] tokens in
+    common.  ``n_tokens``: the rows of q.  Returns the plan (``out``: uint8, at least gguf_prefix_plan_bytes)."""
+    if out is None:
+        out = torch.empty(max(gguf_prefix_plan_bytes(kv_len.numel(), prefix_len.numel(), n_tokens), 0), dtype=torch.uint8,
+                          device=kv_len.device)
+    st = _bound().prefix_plan(q_start, kv_len, group_start, prefix_len, page_size, n_tokens, out, _stream())
+    if st:
+        _check(st)
+    return out
+
+
+def gguf_prefix_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, plan: torch.Tensor,
+                          n_groups: int, n_kv_heads: int, page_size: int, max_q_len: int, scale: float,
+                          window: int = 0, sinks: int = 0, out: torch.Tensor | None = None,
+                          ws: torch.Tensor | None = None, dev_status: torch.Tensor | None = None) -> torch.Tensor:
+    """gguf_paged_attention with the pages that the requests of a group share read once for all of them (see
+    include/gguf_gb300.h).  ``block_table`` has a row per request of the plan."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    call = _bound().prefix_attention
+    if ws is None:   # a caller's workspace is checked against the need by the library
+        need = call(q, cache, block_table, plan, n_groups, n_kv_heads, page_size, max_q_len, scale, window, sinks, out, 0,
+                    dev_status, 0)
+        ws = _workspace(need, q.device)
+    st = call(q, cache, block_table, plan, n_groups, n_kv_heads, page_size, max_q_len, scale, window, sinks, out, ws,
               dev_status, _stream())
     if st:
         _check(st)

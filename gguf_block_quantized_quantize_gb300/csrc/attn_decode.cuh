@@ -46,6 +46,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -72,6 +73,29 @@ struct AdCfg {
     static constexpr int SMEM = WARPS * (RING + SLOT);
 };
 
+// An entry of the plan of gguf_prefix_attention (attn_prefix.cu): queries that see tiles of one row of the block table.
+// Entry r < R: the queries of request r and its own tiles; entry R + g: those of all requests of group g and the tiles
+// that the group shares.
+struct PfEntry {
+    int32_t rows0, q;          // first query token, query tokens
+    int32_t tile0, tile1;      // tiles, before the window
+    int32_t pos_min, pos_max;  // of the queries
+    int32_t row;               // row of the block table
+    int32_t group;             // of a request: its group's entry, -1 for none
+};
+// gguf_prefix_attention: what its kernels have beside AdShape's members.  A query row (token and head) has a record of
+// PfStride<D> floats, its output, maximum and sum, for its request's own tiles and, n_tokens x heads records later, one
+// for its group's: the first piece of its unit, whatever else of the unit's tiles other CTAs took.  Those leave a slot each.
+struct PfShape {
+    const int32_t *plan;       // header, entries, then position and request of each token
+    int32_t n_entries, chained;   // chained: the decode kernel follows the prefill kernel of the call
+    float *records;
+    int64_t *base;             // tiles (decode kernel) or blocks (prefill kernel) before each entry's, of the kernel that takes it
+    int64_t *share;            // a CTA's tiles, a CTA's blocks
+};
+constexpr int PF_HEADER = 8, PF_MAGIC = 0x50465831;   // {magic, requests, groups, tokens, page size, 0, 0, 0}
+template <int D> struct PfStride { static constexpr int64_t value = D + 4; };   // 16-byte steps
+
 // the unit that a CTA began and did not end: the CTAs after it that hold pieces of it (0: there is none), its
 // request's first query token, its first head, its first row; how many rows
 struct AdMeta {
@@ -92,6 +116,7 @@ struct AdShape {
     int32_t whole;                // each CTA takes one whole unit (few short ones), and nothing is left to join
     float *part;                  // CTA-level partial results, two slots per CTA
     AdMeta *meta;                 // per CTA: the unit that goes on past it
+    PfShape pf;                   // gguf_prefix_attention alone
     int *err;                     // error word: a wait for a copy was given up
 };
 
@@ -102,6 +127,7 @@ struct AdReq {
     int32_t q;            // query tokens
     int32_t pos0;         // position of the first
     int32_t nt, n_sink, w_tile;   // tiles: n_sink first ones, then from w_tile on
+    int32_t row, pos_max;         // (PRE) row of the block table, the last position of a query
 };
 __device__ __forceinline__ AdReq ad_request(const AdShape &a, int r) {
     AdReq o;
@@ -113,6 +139,8 @@ __device__ __forceinline__ AdReq ad_request(const AdShape &a, int r) {
     const int64_t q = min(min((int64_t)p.q_start[r + 1] - o.rows0, p.max_q), p.n_tokens - o.rows0);
     const bool mine = o.rows0 >= 0 && q > 0 && q * G > a.min_rows && q * G <= a.max_rows;
     o.q = mine ? (int32_t)q : 0;
+    o.row = r;
+    o.pos_max = 0;
     o.nt = o.n_sink = o.w_tile = 0;
     const int32_t kv = p.kv_len[r];
     o.pos0 = kv - (p.q_start[r + 1] - o.rows0);
@@ -129,6 +157,52 @@ __device__ __forceinline__ AdReq ad_request(const AdShape &a, int r) {
     }
     return o;
 }
+// the same of an entry of the plan; what is not a plan of this call has no queries
+__device__ __forceinline__ const PfEntry *pf_entries(const PfShape &f) { return reinterpret_cast<const PfEntry *>(f.plan + PF_HEADER); }
+__device__ __forceinline__ int2 pf_token(const PfShape &f, int64_t t) {   // position and request
+    return reinterpret_cast<const int2 *>(pf_entries(f) + f.n_entries)[t];
+}
+__device__ __forceinline__ bool pf_plan_fits(const AdShape &a) {
+    const int32_t *h = a.pf.plan;
+    return h[0] == PF_MAGIC && h[1] == (int32_t)a.p.R && h[2] == a.pf.n_entries - (int32_t)a.p.R && h[3] == (int32_t)a.p.n_tokens &&
+           h[4] == (int32_t)a.p.page;
+}
+__device__ __forceinline__ AdReq pf_request(const AdShape &a, int e) {
+    AdReq o;
+    const Attn &p = a.p;
+    const int4 u = reinterpret_cast<const int4 *>(pf_entries(a.pf) + e)[0], v = reinterpret_cast<const int4 *>(pf_entries(a.pf) + e)[1];
+    o.rows0 = u.x;
+    const int32_t tile0 = max(u.z, 0), tile1 = max(min(u.w, 1 << 27), tile0);
+    const int64_t rows = (int64_t)u.y * a.G;
+    const bool mine = u.x >= 0 && u.y > 0 && (int64_t)u.x + u.y <= p.n_tokens && rows > a.min_rows && rows <= a.max_rows &&
+                      v.z >= 0 && v.z < p.R;
+    o.q = mine ? u.y : 0;
+    o.pos0 = v.x;
+    o.pos_max = v.y;
+    o.row = v.z;
+    o.n_sink = 0;
+    o.w_tile = tile0;
+    if (p.window > 0) {
+        const int64_t lo = (int64_t)v.x - p.window + 1;   // what the first query sees from
+        const int32_t w = lo > 0 ? (int32_t)min(lo / KV_TILE, (int64_t)tile1) : 0;
+        if (e >= p.R) {
+            o.w_tile = w;
+            o.n_sink = (int32_t)min((p.sinks + KV_TILE - 1) / KV_TILE, (int64_t)w);
+        } else if (p.sinks <= (int64_t)tile0 * KV_TILE) {   // (else first tokens of the request's own: all its tiles)
+            o.w_tile = max(w, tile0);
+        }
+    }
+    o.nt = o.q > 0 ? o.n_sink + tile1 - o.w_tile : 0;
+    return o;
+}
+template <bool PRE>
+__device__ __forceinline__ AdReq ad_request_of(const AdShape &a, int r) {
+    if constexpr (PRE) return pf_request(a, r);
+    else return ad_request(a, r);
+}
+template <bool PRE>
+__device__ __forceinline__ int ad_requests(const AdShape &a) { return PRE ? a.pf.n_entries : (int)a.p.R; }
+
 // the tile of the request's i-th one, and whether it is the first of its page among them (a page that is not there counts once)
 __device__ __forceinline__ int ad_tile(const AdReq &q, int i) { return i < q.n_sink ? i : q.w_tile + i - q.n_sink; }
 __device__ __forceinline__ bool ad_starts_page(const AdShape &a, const AdReq &q, int i) {
@@ -247,14 +321,14 @@ struct AdCursor {
     AdReq q;
 };
 // the next unit with tiles
-template <int RG>
+template <int RG, bool PRE>
 __device__ __forceinline__ void ad_next_unit(const AdShape &a, AdCursor &c) {
     c.tile = 0;
     if (++c.u < (c.q.q * a.G + RG - 1) / RG * a.hk) return;
     c.u = 0;
     do {
-        if (++c.r >= a.p.R) return;
-        c.q = ad_request(a, c.r);
+        if (++c.r >= ad_requests<PRE>(a)) return;
+        c.q = ad_request_of<PRE>(a, c.r);
     } while (c.q.nt == 0);
 }
 
@@ -266,7 +340,8 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
-template <int D, int QT, int NT>
+// PRE: a launch of gguf_prefix_attention, whose units leave records and slots instead of outputs
+template <int D, int QT, int NT, bool PRE>
 __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kernel(const AdShape a) {
     using C = AdCfg<D, QT, NT>;
     using L = KvTile<D>;
@@ -275,7 +350,9 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[C::WARPS][ST], freed[C::WARPS][ST];
     __shared__ uint32_t absent[C::WARPS][ST];   // tiles of a stage that have no page
-    __shared__ int32_t start_r[C::WARPS], start_at[C::WARPS];   // where a warp starts: request, tile of the request's
+    using At = std::conditional_t<PRE, int64_t, int32_t>;
+    __shared__ int32_t start_r[C::WARPS];
+    __shared__ At start_at[C::WARPS];   // where a warp starts: request, tile of the request's
     __shared__ int64_t warp_sum[C::THREADS / 32];
     __shared__ int32_t cta_tiles, blind;   // blind: some queries see no token
     __shared__ int32_t abort_word;
@@ -293,19 +370,22 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     tc::fence_barrier_init();
     __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // (the prefill kernel before it let this one start when all that came before the call was complete; it takes other
+    // entries and writes other records, so there is nothing of it to wait for until the end)
+    if (!PRE || !a.pf.chained) asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // The cut.  Thread t holds requests [t * per, (t + 1) * per) of the sequence of tiles (or of units, where a CTA
     // takes one whole unit) and, once the sum of what comes before is known, writes down where the warps start whose
     // first tile lies in them.
     constexpr int NTHR = C::THREADS;
-    const int R = (int)p.R, per = (R + NTHR - 1) / NTHR, r0 = tid * per, r1 = min(R, r0 + per);
+    const int R = PRE && !pf_plan_fits(a) ? 0 : ad_requests<PRE>(a);
+    const int per = (R + NTHR - 1) / NTHR, r0 = tid * per, r1 = min(R, r0 + per);
     AdReq rq{};
     int64_t mine = 0;
     for (int r = r0; r < r1; r++) {
-        rq = ad_request(a, r);
-        mine += ad_units(a, rq, RG) * (a.whole ? 1 : rq.nt);
-        if (rq.q > 0 && rq.nt == 0) blind = 1;   // (every writer writes the same)
+        rq = ad_request_of<PRE>(a, r);
+        mine += ad_units(a, rq, RG) * (!PRE && a.whole ? 1 : rq.nt);
+        if (!PRE && rq.q > 0 && rq.nt == 0) blind = 1;   // (every writer writes the same)
     }
     int64_t before = mine;
 #pragma unroll
@@ -323,14 +403,16 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
         if (w < warp) before += warp_sum[w];
         total += warp_sum[w];
     }
-    const int64_t share = a.whole ? 1 : ad_div(total + gridDim.x - 1, gridDim.x);
+    const int64_t share = !PRE && a.whole ? 1 : ad_div(total + gridDim.x - 1, gridDim.x);
+    if (PRE && blockIdx.x == 0 && tid == 0) a.pf.share[0] = share;
     int64_t cta0 = min(total, (int64_t)blockIdx.x * share), cta1 = min(total, cta0 + share);
     int64_t per_warp = ad_div(cta1 - cta0 + C::WARPS - 1, C::WARPS);
     for (int r = r0; r < r1; r++) {
-        if (per > 1) rq = ad_request(a, r);
-        const int64_t units = ad_units(a, rq, RG), n = units * (a.whole ? 1 : rq.nt);
+        if (per > 1) rq = ad_request_of<PRE>(a, r);
+        const int64_t units = ad_units(a, rq, RG), n = units * (!PRE && a.whole ? 1 : rq.nt);
+        if (PRE && blockIdx.x == 0 && rq.q > 0) a.pf.base[r] = before;
         if (before < cta1 && before + n > cta0) {
-            if (a.whole) {   // the CTA's unit: its tiles over the warps
+            if (!PRE && a.whole) {   // the CTA's unit: its tiles over the warps
                 const int share_w = (rq.nt + C::WARPS - 1) / C::WARPS, first = (int)(cta0 - before) * rq.nt;
 #pragma unroll
                 for (int w = 0; w < C::WARPS; w++) {
@@ -345,7 +427,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                     const int64_t at = skip + w * per_warp;
                     if (at >= 0 && at < n) {
                         start_r[w] = r;
-                        start_at[w] = (int32_t)at;
+                        start_at[w] = (At)at;
                     }
                 }
             }
@@ -353,7 +435,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
         before += n;
     }
     __syncthreads();
-    if (a.whole) {
+    if (!PRE && a.whole) {
         cta0 = 0;
         cta1 = cta_tiles;
         per_warp = (cta1 + C::WARPS - 1) / C::WARPS;
@@ -361,9 +443,10 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     auto start_of = [&](int w) {
         AdCursor c;
         c.r = start_r[w];
-        c.q = ad_request(a, c.r);
-        c.u = (int)((uint32_t)start_at[w] / (uint32_t)c.q.nt);
-        c.tile = start_at[w] - c.u * c.q.nt;
+        c.q = ad_request_of<PRE>(a, c.r);
+        if constexpr (PRE) c.u = (int)ad_div(start_at[w], c.q.nt);
+        else c.u = (int)((uint32_t)start_at[w] / (uint32_t)c.q.nt);
+        c.tile = (int)(start_at[w] - (At)c.u * c.q.nt);
         return c;
     };
     const int64_t per_cta = share;
@@ -401,7 +484,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             }
             idle_since = 0;
             if (go && unit == 0) {
-                if (feed.tile == feed.q.nt) ad_next_unit<RG>(a, feed);
+                if (feed.tile == feed.q.nt) ad_next_unit<RG, PRE>(a, feed);
                 unit = min(tiles, feed.q.nt - feed.tile);
                 head = p.cache + (int64_t)(feed.u % a.hk) * tpp * L::BYTES;
             }
@@ -410,7 +493,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             const int at = ad_tile(feed.q, i);
             const int page_at = shift >= 0 ? at >> shift : (int)((uint32_t)at / tpp), in_page = at - page_at * (int)tpp;
             const int first = __shfl_sync(0xffffffffu, page_at, lane & 24);
-            const int32_t *row = p.table + feed.r * p.ld;
+            const int32_t *row = p.table + (PRE ? feed.q.row : feed.r) * p.ld;
             if (go && (of != feed.r || first < base || first >= base + 8)) {
                 const bool slide = of == feed.r && first >= base + 8 && first < base + 16;
                 base = slide ? base + 8 : first & ~7;
@@ -467,7 +550,12 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
         while (left_tiles > 0) {
             // ---- a unit, or the part of it that is the warp's: its query rows
             const int group = cur.u / a.hk, row0 = group * RG, head0 = (cur.u - group * a.hk) * G, rows = cur.q.q * G;
-            const int pos_lo = cur.q.pos0 + ad_token_of_row(a, row0), pos_hi = cur.q.pos0 + ad_token_of_row(a, min(rows, row0 + RG) - 1);
+            int pos_lo = cur.q.pos0 + ad_token_of_row(a, row0), pos_hi = cur.q.pos0 + ad_token_of_row(a, min(rows, row0 + RG) - 1);
+            if constexpr (PRE) {   // rows of several requests: the first and the last position among them
+                const int pos = pf_token(a.pf, cur.q.rows0 + ad_token_of_row(a, min(rows, row0 + RG) - 1 - lane % min(RG, rows - row0))).x;
+                pos_lo = __reduce_min_sync(0xffffffffu, pos);
+                pos_hi = __reduce_max_sync(0xffffffffu, pos);
+            }
             uint32_t qb[QP][NB][2][NT][2];   // B fragments of the queries: row g, values 8 q4 .. of each block
             float corr[NB][NT][4];           // what the code offsets add to rows 2 q4, + 1 (twice: an accumulator), negated
             float sl[NT][2];                 // scores to log2 units
@@ -553,6 +641,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             left_tiles -= seg_end - cur.tile;
             // tiles that every row sees whole: below full_sink, and from full_lo to full_hi
             int full_sink = 0, full_lo = 0, full_hi = pos_lo < 0 ? 0 : (pos_lo + 1) / KV_TILE;
+            if (PRE && p.window <= 0) full_hi -= cur.q.w_tile;
             if (p.window > 0) {
                 full_sink = (int)min((int64_t)cur.q.n_sink, p.sinks / KV_TILE);
                 const int64_t lo = (int64_t)pos_hi - p.window + 1;   // first token that the last row sees
@@ -635,7 +724,8 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
 #pragma unroll
                         for (int j = 0; j < 2; j++) {
                             const int row = row0 + 8 * n + 2 * q4 + j;
-                            pos[n][j] = row < rows ? cur.q.pos0 + ad_token_of_row(a, row) : -1;
+                            pos[n][j] = row >= rows ? -1 : PRE ? pf_token(a.pf, cur.q.rows0 + ad_token_of_row(a, row)).x
+                                                               : cur.q.pos0 + ad_token_of_row(a, row);
                         }
 #pragma unroll
                     for (int x = 0; x < TP; x++) {
@@ -768,7 +858,23 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
 #pragma unroll
                     for (int i = 4; i < 32; i <<= 1) lsum[n][j] += __shfl_xor_sync(0xffffffffu, lsum[n][j], i);
             const bool unit_end = cur.tile == cur.q.nt;
-            if (unit_end && began) {   // a whole unit
+            if (PRE && unit_end && began) {   // a whole unit: its records
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                    for (int j = 0; j < 2; j++) {
+                        const int row = row0 + 8 * n + 2 * q4 + j;
+                        if (row < rows) {
+                            const int tk = ad_token_of_row(a, row);
+                            float *to = a.pf.records + ((cur.q.rows0 + tk + (cur.r >= p.R ? p.n_tokens : 0)) * p.h + head0 + row - tk * G) * PfStride<D>::value;
+#pragma unroll
+                            for (int b = 0; b < NB; b++)
+                                *reinterpret_cast<float4 *>(to + 32 * b + 4 * g) =
+                                    make_float4(o[b][0][n][j], o[b][0][n][2 + j], o[b][1][n][j], o[b][1][n][2 + j]);
+                            if (g == 0) *reinterpret_cast<float2 *>(to + D) = make_float2(m[n][j], lsum[n][j]);
+                        }
+                    }
+            } else if (unit_end && began) {   // a whole unit
 #pragma unroll
                 for (int n = 0; n < NT; n++)
 #pragma unroll
@@ -788,7 +894,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                 // a unit from before the warp leaves its piece beside the ring; one that goes on past the warp ends
                 // with the warp's last tile, and takes the ring, where no copy is under way any more
                 flags |= began ? 4 : unit_end ? 1 : 3;
-                if (began) { open_row = cur.q.rows0; open_rows = rows; open_u = cur.u; open_end = t1 + cur.q.nt - cur.tile; }
+                if (began) { open_row = cur.q.rows0 + (PRE && cur.r >= p.R ? (int)p.n_tokens : 0); open_rows = rows; open_u = cur.u; open_end = t1 + cur.q.nt - cur.tile; }
                 __syncwarp();
                 float *dst = reinterpret_cast<float *>(began ? ring : smem + C::WARPS * C::RING + warp * C::SLOT);
 #pragma unroll
@@ -805,7 +911,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                         }
                     }
             }
-            if (left_tiles > 0) ad_next_unit<RG>(a, cur);
+            if (left_tiles > 0) ad_next_unit<RG, PRE>(a, cur);
         }
     }
     if (lane == 0) {
@@ -844,7 +950,15 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                 l = fmaf(f, ml.y, l);
                 v.x = fmaf(f, x.x, v.x); v.y = fmaf(f, x.y, v.y); v.z = fmaf(f, x.z, v.z); v.w = fmaf(f, x.w, v.w);
             }
-            if (!orphan && !open) {
+            if (PRE && !orphan) {
+                const int u = left_u[chain], group = u / a.hk, at_row = group * RG + row;
+                if (at_row < left_rows[chain]) {
+                    const int tk = ad_token_of_row(a, at_row);
+                    float *to = a.pf.records + (((int64_t)left_row[chain] + tk) * p.h + (u - group * a.hk) * G + at_row - tk * G) * PfStride<D>::value;
+                    *reinterpret_cast<float4 *>(to + col) = v;
+                    if (col == 0) *reinterpret_cast<float2 *>(to + D) = make_float2(mx, l);
+                }
+            } else if (!orphan && !open) {
                 const int u = left_u[chain], group = u / a.hk, at_row = group * RG + row;
                 if (at_row < left_rows[chain]) {
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -853,7 +967,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                                a.vec, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
                 }
             } else {
-                float *dst = a.part + (int64_t)(2 * blockIdx.x + (orphan ? 0 : 1)) * (C::SLOT / 4);
+                float *dst = a.part + (PRE ? (int64_t)blockIdx.x : (int64_t)(2 * blockIdx.x + (orphan ? 0 : 1))) * (C::SLOT / 4);
                 *reinterpret_cast<float4 *>(dst + row * D + col) = v;
                 if (col == 0) {
                     dst[RG * D + 2 * row] = mx;
@@ -881,6 +995,10 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             }
             break;
         }
+    }
+    if constexpr (PRE) {   // what follows this launch may count on the prefill kernel's records too
+        if (a.pf.chained) asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
     }
     if (tid == 0 && !a.whole) {
         AdMeta m{};
@@ -967,7 +1085,7 @@ static cudaError_t attn_decode_run(const AdShape &shape, int ctas, cudaStream_t 
     a.whole = units <= ctas && span <= 2048;
     if (a.whole) ctas = (int)units;
     cudaError_t err = cudaSuccess;
-    const void *kern = (const void *)attn_decode_kernel<D, QT, NT>;
+    const void *kern = (const void *)attn_decode_kernel<D, QT, NT, false>;
     if (kernel_occupancy(kern, C::THREADS, C::SMEM, &err) == 0) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
@@ -979,12 +1097,31 @@ static cudaError_t attn_decode_run(const AdShape &shape, int ctas, cudaStream_t 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, QT, NT>, a);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, QT, NT, false>, a);
     if (e != cudaSuccess || a.whole) return e;
     cfg.gridDim = dim3((unsigned)ctas, C::RG);
     cfg.blockDim = dim3(AC_THREADS);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, QT, NT>, a);
+}
+
+// the launch of gguf_prefix_attention
+template <int D, int QT, int NT>
+static cudaError_t attn_prefix_decode_run(const AdShape &a, int ctas, cudaStream_t s) {
+    using C = AdCfg<D, QT, NT>;
+    cudaError_t err = cudaSuccess;
+    if (kernel_occupancy((const void *)attn_decode_kernel<D, QT, NT, true>, C::THREADS, C::SMEM, &err) == 0) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, QT, NT, true>, a);
 }
 
 }  // namespace gg

@@ -76,7 +76,8 @@ struct ApItem {
     int nt, n_sink, w_tile;       // the tiles that the rows see (see AdReq): the piece takes those from base to nt
     int base;
     int part;                     // its place among the partial results where the row block's tiles are cut, else -1
-};
+    int first, pos_max;           // (PRE) 1: the piece with the row block's first tiles, of a request's own tiles; 2: of a
+};                                // group's; 0: another piece.  The entry's last position
 
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -131,6 +132,13 @@ __device__ __forceinline__ int ap_items(const AdShape &a, const AdReq &q, int ro
     return (int)((q.q * (int64_t)a.G + rows - 1) / rows) * a.hk;
 }
 
+// (PRE) whether the i-th tile is the first of its page that the entry's queries see; its first row block counts
+__device__ __forceinline__ bool pf_first_sight(const AdShape &a, const ApItem &w, int i) {
+    AdReq q{};
+    q.n_sink = w.n_sink;
+    q.w_tile = w.w_tile;
+    return w.row0 == 0 && ad_starts_page(a, q, i);
+}
 // whether `tile` is the first of its page that the request's queries see, and no row block before this one sees it
 __device__ __forceinline__ bool ap_first_sight(const AdShape &a, const ApItem &w, int tile) {
     const AdReq q = ad_request(a, w.r);
@@ -141,8 +149,13 @@ __device__ __forceinline__ bool ap_first_sight(const AdShape &a, const ApItem &w
     return ad_starts_page(a, q, tile < q.n_sink ? tile : tile - q.w_tile + q.n_sink);
 }
 
-template <int D, int QT, bool CUT>
+// PLAIN: whole row blocks.  CUT: some of them in pieces.  PRE: a launch of gguf_prefix_attention: the blocks of all row
+// blocks in one sequence, cut evenly over the CTAs; rows of several requests, each with its own position; records and
+// slots instead of outputs.
+enum { AP_PLAIN = 0, AP_CUT = 1, AP_PRE = 2 };
+template <int D, int QT, int MODE>
 __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdShape a) {
+    constexpr bool CUT = MODE == AP_CUT, PRE = MODE == AP_PRE, PARTS = MODE != AP_PLAIN;
     using C = ApCfg<D, QT>;
     using L = KvTile<D>;
     constexpr int NB = L::NB, BW = L::BW, NC = L::NC, BT = C::BT, ROWS = C::RT * 128;
@@ -156,7 +169,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     __shared__ int32_t abort_word;
     __shared__ ApItem item;
     __shared__ int32_t part[2][AP_THREADS / 32], cut_rows, cut_pieces, cut_from;
-    __shared__ int32_t chunk_end[AP_THREADS];   // at most (tokens x heads / 128) items: 31 bits
+    using Count = std::conditional_t<PRE, int64_t, int32_t>;
+    __shared__ Count chunk_end[AP_THREADS];   // at most (tokens x heads / 128) items: 31 bits; (PRE) blocks of all items
+    __shared__ Count pre_sum[PRE ? AP_THREADS / 32 : 1];
     volatile int32_t *abort_flag = &abort_word;
     const Attn &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -175,13 +190,44 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         tc::tmem_alloc(&tmem_slot, 512);
         tc::tmem_relinquish();
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // (PRE: the decode kernel that follows starts where SMs are free, without a wait of its own: not before all that came
+    // before this call is complete)
+    if (!PRE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (PRE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // Work of all requests: thread t counts requests [t * per, (t + 1) * per), in row blocks of ROWS rows, and of 128.
     // The larger ones unpack a key for twice the rows; the smaller ones are for calls that would leave SMs idle, as are
     // row blocks whose tokens are cut into pieces (CUT; of 4 blocks at least, joined by a second launch).
-    const int R = (int)p.R, per = (R + AP_THREADS - 1) / AP_THREADS;
-    {
+    const int R = PRE && !pf_plan_fits(a) ? 0 : ad_requests<PRE>(a), per = (R + AP_THREADS - 1) / AP_THREADS;
+    auto blocks_of = [](const AdReq &q) { return (q.nt + BT / KV_TILE - 1) / (BT / KV_TILE); };
+    if constexpr (PRE) {
+        int64_t mine = 0;
+        for (int r = tid * per; r < min(R, (tid + 1) * per); r++) {
+            const AdReq q = pf_request(a, r);
+            mine += (int64_t)ap_items(a, q, ROWS) * blocks_of(q);
+        }
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) pre_sum[warp] = incl;
+        tc::tc_fence_before();
+        __syncthreads();
+        tc::tc_fence_after();
+        for (int w = 0; w < warp; w++) incl += pre_sum[w];
+        chunk_end[tid] = incl;
+        if (blockIdx.x == 0) {   // for the join
+            int64_t before = incl - mine;
+            for (int r = tid * per; r < min(R, (tid + 1) * per); r++) {
+                const AdReq q = pf_request(a, r);
+                if (q.q > 0) a.pf.base[r] = before;
+                before += (int64_t)ap_items(a, q, ROWS) * blocks_of(q);
+            }
+        }
+        __syncthreads();
+    } else {
         int item_rows = ROWS, splits = 1;
         int mine = 0, mine128 = 0;   // (tokens x heads / 128 is below 2^31)
         for (int r = tid * per; r < min(R, (tid + 1) * per); r++) {
@@ -227,7 +273,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         }
         __syncthreads();
     }
-    const int64_t total = CUT ? cut_from + (int64_t)(chunk_end[AP_THREADS - 1] - cut_from) * cut_pieces : chunk_end[AP_THREADS - 1];
+    const int64_t total = PRE ? (int64_t)chunk_end[AP_THREADS - 1] : CUT ? cut_from + (int64_t)(chunk_end[AP_THREADS - 1] - cut_from) * cut_pieces : chunk_end[AP_THREADS - 1];
     const uint32_t tmem = tmem_slot;
     auto fail = [&](int code) {
         *abort_flag = 1;
@@ -238,6 +284,10 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar);
     };
+    // (PRE) the CTA's blocks of the sequence
+    const int64_t share = PRE ? ad_div(total + gridDim.x - 1, gridDim.x) : 0;
+    const int64_t own0 = PRE ? min(total, (int64_t)blockIdx.x * share) : 0, own1 = PRE ? min(total, own0 + share) : 0;
+    if (PRE && blockIdx.x == 0 && tid == 0) a.pf.share[1] = share;
     auto token_of = [&](int i) { return (i < item.n_sink ? i : item.w_tile + i - item.n_sink) * KV_TILE; };
 
     // items in stripes of one per CTA, every other stripe backwards: a request's row blocks come longest first
@@ -259,7 +309,42 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         everyone();
         tc::tc_fence_after();
         if (*abort_flag) return false;
-        if (tid == 0) {
+        if (PRE && tid == 0) {   // piece: the first block
+            int lo = -1, hi = AP_THREADS - 1;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (chunk_end[mid] > piece) hi = mid;
+                else lo = mid;
+            }
+            int64_t before = hi > 0 ? chunk_end[hi - 1] : 0;
+            ApItem w;
+            AdReq q;
+            int e = hi * per, nblk;
+            for (;; e++) {   // it is there: piece < total
+                q = pf_request(a, e);
+                nblk = blocks_of(q);
+                const int64_t n = (int64_t)ap_items(a, q, ROWS) * nblk;
+                if (before + n > piece) break;
+                before += n;
+            }
+            const int64_t u = ad_div(piece - before, nblk);
+            const int blk = (int)(piece - before - u * nblk), left = (int)min((int64_t)(nblk - blk), own1 - piece);
+            w.r = q.row;
+            w.head = (int)(u % a.hk);
+            w.row0 = (int)(u / a.hk) * ROWS;
+            w.rows = min(ROWS, q.q * G - w.row0);
+            w.q0 = q.rows0;
+            w.tok0 = w.row0 / G;
+            w.pos0 = 0;
+            w.n_sink = q.n_sink;
+            w.w_tile = q.w_tile;
+            w.base = blk * (BT / KV_TILE);
+            w.nt = min(q.nt, (blk + left) * (BT / KV_TILE));
+            w.first = blk > 0 ? 0 : e >= p.R ? 2 : 1;
+            w.pos_max = q.pos_max;
+            item = w;
+        }
+        if (!PRE && tid == 0) {
             const int item_rows = cut_rows, splits = CUT ? cut_pieces : 1;
             const int place = CUT ? (int)piece - cut_from : -1;   // among the pieces of the cut ones
             const int it = place >= 0 ? cut_from + place / splits : (int)piece, cut = place % splits;
@@ -311,16 +396,16 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         }
         everyone();
         wk.nrt = item.rows > 128 ? 2 : 1;
-        wk.nblk = (item.nt - (CUT ? item.base : 0) + BT / KV_TILE - 1) / (BT / KV_TILE);
+        wk.nblk = (item.nt - (PARTS ? item.base : 0) + BT / KV_TILE - 1) / (BT / KV_TILE);
         wk.nitems = wk.nblk * wk.nrt;
         return true;
     };
     Walk wk;
     if (warp < 8) {
         set_registers<C::REGS>();
-        for (int64_t st = 0; st < stripes; st++) {
-            const int64_t it = item_of(st);
-            if (it >= total) continue;
+        for (int64_t st = 0; PRE ? own0 + st < own1 : st < stripes; st += PRE ? wk.nblk : 1) {
+            const int64_t it = PRE ? own0 + st : item_of(st);
+            if (!PRE && it >= total) continue;
             if (!begin(wk, it)) break;
             // ---- queries: D / 8 lanes per row, 8 values each
             {
@@ -369,11 +454,11 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                 const uint32_t lanes = (uint32_t)(quad * 32) << 16;
                 const uint32_t o_col = tmem + lanes + C::COL_O + t * D;
                 const bool there = row < item.rows;
-                const int pos = there ? item.pos0 + (item.row0 + row) / G - item.tok0 : -1;
+                const int pos = !there ? -1 : PRE ? pf_token(a.pf, item.q0 + (item.row0 + row) / G).x : item.pos0 + (item.row0 + row) / G - item.tok0;
                 // positions of the warp's rows, from the first to the last that is there
-                const int first = item.pos0 + (item.row0 + t * 128 + quad * 32) / G - item.tok0;
                 const int lastr = min(item.rows - 1, t * 128 + quad * 32 + 31);
-                const int last = item.pos0 + (item.row0 + lastr) / G - item.tok0;
+                const int first = PRE ? __reduce_min_sync(0xffffffffu, there ? pos : 0x7fffffff) : item.pos0 + (item.row0 + t * 128 + quad * 32) / G - item.tok0;
+                const int last = PRE ? __reduce_max_sync(0xffffffffu, pos) : item.pos0 + (item.row0 + lastr) / G - item.tok0;
                 float ref = -INFINITY, lsum = 0.0f;
                 bool ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_full, (uint32_t)wk.items & 1u));
                 if (!ok && lane == 0) fail(1);
@@ -385,7 +470,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                     tc::tc_fence_after();
                     const uint32_t s_col = tmem + lanes + x * C::COL_S;
                     // whether every row of the warp sees the whole block
-                    const int i0 = (CUT ? item.base : 0) + j * (BT / KV_TILE), i1 = min(item.nt, i0 + BT / KV_TILE);
+                    const int i0 = (PARTS ? item.base : 0) + j * (BT / KV_TILE), i1 = min(item.nt, i0 + BT / KV_TILE);
                     const int mask = blk_mask[(wk.blocks_before + j) & 7];
                     const int t_first = i0 < item.n_sink ? 0 : token_of(i0), t_last = token_of(i1 - 1) + KV_TILE - 1;
                     const bool whole = mask == (1 << (BT / KV_TILE)) - 1 && t_last <= first &&
@@ -485,7 +570,19 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
 #pragma unroll
                             for (int i = 0; i < 32; i++) rr[i] = 0;
                         }
-                        if (CUT && there && item.part >= 0) {
+                        if (PRE) {   // the record of the row, or its part of the CTA's slot
+                            if (there) {
+                                float *to = item.first ? a.pf.records + ((item.q0 + rr0 / G + (item.first == 2 ? p.n_tokens : 0)) * p.h +
+                                                                         item.head * G + rr0 % G) * PfStride<D>::value
+                                                       : a.pieces + ((int64_t)blockIdx.x * ROWS + row) * PfStride<D>::value;
+                                float4 *dst = reinterpret_cast<float4 *>(to + 32 * c);
+#pragma unroll
+                                for (int i = 0; i < 8; i++)
+                                    dst[i] = make_float4(__uint_as_float(rr[4 * i]), __uint_as_float(rr[4 * i + 1]),
+                                                         __uint_as_float(rr[4 * i + 2]), __uint_as_float(rr[4 * i + 3]));
+                                if (c == 0) *reinterpret_cast<float2 *>(to + D) = make_float2(ref, lsum);
+                            }
+                        } else if (CUT && there && item.part >= 0) {
                             float *to = a.pieces + ((int64_t)item.part * cut_rows + row) * (D + 2);
                             float2 *dst = reinterpret_cast<float2 *>(to + 2 + 32 * c);
 #pragma unroll
@@ -517,9 +614,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         }
     } else if (warp < AP_MMA) {
         set_registers<C::REGS_OTHER>();
-        for (int64_t st = 0; st < stripes; st++) {
-            const int64_t it = item_of(st);
-            if (it >= total) continue;
+        for (int64_t st = 0; PRE ? own0 + st < own1 : st < stripes; st += PRE ? wk.nblk : 1) {
+            const int64_t it = PRE ? own0 + st : item_of(st);
+            if (!PRE && it >= total) continue;
             if (!begin(wk, it)) break;
             // ================= unpack: the keys of a block, then its values, 4 tiles a step.  The packed words of the next step are
             // read from shared memory before the current one is computed: the matrix unit's reads fill the shared memory's
@@ -535,8 +632,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             const uint32_t k_off = (w8 * 16 + kg) * 128 + (((4 * odd + kq) ^ kg) * 16);   // of even blocks; odd ones: ^ 64
             const uint32_t v_cx = ((2 * tl + pp) ^ (4 * (vg & 1))) * 16, v_row = (32 * XS * hb + 4 * vg) * 128;
             const uint8_t *raws = smem + C::OFF_RAW;
-            const int last = item.pos0 + (item.row0 + item.rows - 1) / G - item.tok0 - 8 * pp;
-            const int n_sink = item.n_sink, w_tile = item.w_tile, i_base = CUT ? item.base : 0;
+            const int last = (PRE ? item.pos_max : item.pos0 + (item.row0 + item.rows - 1) / G - item.tok0) - 8 * pp;
+            const int n_sink = item.n_sink, w_tile = item.w_tile, i_base = PARTS ? item.base : 0;
             bool ok = true;
             constexpr int STEPS = C::GT / 4;
             auto raw_wait = [&](int load) {
@@ -670,9 +767,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         }
     } else {
         set_registers<C::REGS_OTHER>();
-        for (int64_t st = 0; st < stripes; st++) {
-            const int64_t it = item_of(st);
-            if (it >= total) continue;
+        for (int64_t st = 0; PRE ? own0 + st < own1 : st < stripes; st += PRE ? wk.nblk : 1) {
+            const int64_t it = PRE ? own0 + st : item_of(st);
+            if (!PRE && it >= total) continue;
             if (!begin(wk, it)) break;
             if (warp == AP_MMA) {
                 // ================= MMA: the warp stays together and every operand comes from values that are known to
@@ -755,7 +852,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                     const int gb = wk.loads_before + e, rs = gb % C::RAWST;
                     const bool values = e & 1;
                     const int j = e / 2;
-                    const int i = (CUT ? item.base : 0) + j * C::GT + (lane & (C::GT - 1));
+                    const int i = (PARTS ? item.base : 0) + j * C::GT + (lane & (C::GT - 1));
                     int32_t pg = -1;
                     int tok = 0;
                     if (i < item.nt) {
@@ -763,7 +860,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                         const uint32_t pi = (uint32_t)tok / (uint32_t)p.page;
                         pg = pi < p.width ? p.table[item.r * p.ld + pi] : -1;
                         if (lane < C::GT && !values && item.head == 0 && (pg < 0 || pg >= p.n_pages) && p.status != nullptr &&
-                            ap_first_sight(a, item, tok / KV_TILE))
+                            (PRE ? pf_first_sight(a, item, i) : ap_first_sight(a, item, tok / KV_TILE)))
                             atomicAdd(p.status, 1);
                     }
                     const bool live = lane < C::GT && pg >= 0 && pg < p.n_pages;
@@ -850,10 +947,10 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const AdShape a)
     }
 }
 
-template <int D, int QT, bool CUT>
+template <int D, int QT, int MODE>
 static cudaError_t attn_prefill_launch(const AdShape &a, int ctas, cudaStream_t s) {
     cudaError_t err = cudaSuccess;
-    if (kernel_occupancy((const void *)attn_prefill_kernel<D, QT, CUT>, AP_THREADS, ApCfg<D, QT>::SMEM, &err) == 0) return err;
+    if (kernel_occupancy((const void *)attn_prefill_kernel<D, QT, MODE>, AP_THREADS, ApCfg<D, QT>::SMEM, &err) == 0) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(AP_THREADS);
@@ -864,17 +961,20 @@ static cudaError_t attn_prefill_launch(const AdShape &a, int ctas, cudaStream_t 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D, QT, CUT>, a); e != cudaSuccess || !CUT) return e;
-    cfg.gridDim = dim3((unsigned)((a.p.n_tokens * a.p.h + 7) / 8));
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, attn_prefill_join_kernel<D, QT>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D, QT, MODE>, a);
+    if constexpr (MODE == AP_CUT) {
+        if (e != cudaSuccess) return e;
+        cfg.gridDim = dim3((unsigned)((a.p.n_tokens * a.p.h + 7) / 8));
+        cfg.blockDim = dim3(256);
+        cfg.dynamicSmemBytes = 0;
+        return cudaLaunchKernelEx(&cfg, attn_prefill_join_kernel<D, QT>, a);
+    } else return e;
 }
 
 // Two builds of the kernel: what cutting adds costs its spare registers (8192 tokens: 664 us with it, 644 without).
 template <int D, int QT>
 static cudaError_t attn_prefill_run(const AdShape &a, int ctas, cudaStream_t s) {
-    return a.max_splits > 1 ? attn_prefill_launch<D, QT, true>(a, ctas, s) : attn_prefill_launch<D, QT, false>(a, ctas, s);
+    return a.max_splits > 1 ? attn_prefill_launch<D, QT, AP_CUT>(a, ctas, s) : attn_prefill_launch<D, QT, AP_PLAIN>(a, ctas, s);
 }
 
 }  // namespace gg

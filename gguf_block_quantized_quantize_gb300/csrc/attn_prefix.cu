@@ -1,0 +1,337 @@
+// gguf_prefix_plan and gguf_prefix_attention: attention of a batch whose requests
+// share long prefixes, group by group, over the paged Q4_0 cache.
+//
+//   o_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = 2^(s_ij - m),   j over [0, P) and [P, pos_i]
+//
+// The sums over the two ranges are taken apart, each with a maximum of its own,
+// and joined: (m, l, O) + (m', l', O') = (M, 2^(m-M) l + 2^(m'-M) l', 2^(m-M) O +
+// 2^(m'-M) O').  So the queries of all requests of a group stand together as the
+// rows of one matrix against the group's P shared tokens, which are read and
+// unpacked once for all of them; only what a request has of its own is walked over
+// per request.
+//
+// An entry of the plan is a set of consecutive queries and a range of tiles of one
+// row of the block table: one for each request (its own tiles) and one for each
+// group (the shared ones, through its first request's row).  Entries with more than
+// `few` query rows per KV head go to the tensor-core kernel of prompts
+// (attn_prefill.cuh), the others to the kernel of few rows (attn_decode.cuh), each in
+// a mode that cuts all its tiles evenly over the CTAs, takes every row's position
+// from the plan, and leaves (m, l, O) in fp32: a record per query row for the first
+// piece of its unit, a slot per CTA for a piece that goes on from the CTA before.  The
+// second kernel starts as the first one's CTAs end, without waiting for its results.
+// The join takes a warp per query row, which works out from the cut where its pieces
+// lie.
+#include <algorithm>
+
+#include "attn_decode.cuh"
+#include "attn_prefix.h"
+
+namespace gg {
+
+int *tg_error_word();   // the library's device error word (mmq.cu)
+
+// ---------------------------------------------------------------- plan
+
+struct PfPlanArgs {
+    const int32_t *q_start, *kv_len;
+    int64_t R;
+    const int32_t *group_start, *prefix_len;
+    int64_t NG, page, n_tokens;
+    int32_t *plan;
+};
+// the last i in [0, n) with a[i] <= x, or -1 (a does not decrease)
+__device__ __forceinline__ int64_t last_up_to(const int32_t *a, int64_t n, int64_t x) {
+    int64_t lo = -1, hi = n;
+    while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (a[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+struct PfGroup {
+    int64_t s, e;    // its requests
+    int32_t tiles;   // shared ones
+};
+__device__ __forceinline__ PfGroup pf_group(const PfPlanArgs &p, int64_t g) {
+    PfGroup o;
+    o.s = max((int64_t)p.group_start[g], (int64_t)0);
+    o.e = min((int64_t)p.group_start[g + 1], p.R);
+    // whole pages: the one that a prefix ends in holds tokens of a request's own, and is its own
+    o.tiles = o.e - o.s >= 2 ? (int32_t)(max(p.prefix_len[g], 0) / p.page * (p.page / KV_TILE)) : 0;
+    return o;
+}
+// the queries of requests s .. e - 1 that the call's arrays hold
+__device__ __forceinline__ void pf_queries(const PfPlanArgs &p, int64_t s, int64_t e, PfEntry &o) {
+    const int64_t a = p.q_start[s], b = min((int64_t)p.q_start[e], p.n_tokens);
+    o.rows0 = (int32_t)max(a, (int64_t)0);
+    o.q = a >= 0 && b > a ? (int32_t)(b - a) : 0;
+}
+
+// Three independent parts, over all CTAs: a thread per token, a thread per request, a warp per group.  Latency-bound: a
+// token's request is a binary search of q_start, a group's positions a loop of its requests by 32.
+constexpr int PF_THREADS = 256;
+__global__ void __launch_bounds__(PF_THREADS) prefix_plan_kernel(const PfPlanArgs p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t id = (int64_t)blockIdx.x * PF_THREADS + threadIdx.x;
+    PfEntry *entries = reinterpret_cast<PfEntry *>(p.plan + PF_HEADER);
+    if (id == 0) {
+        const int32_t h[PF_HEADER] = {PF_MAGIC, (int32_t)p.R, (int32_t)p.NG, (int32_t)p.n_tokens, (int32_t)p.page, 0, 0, 0};
+        for (int i = 0; i < PF_HEADER; i++) p.plan[i] = h[i];
+    }
+    if (id < p.n_tokens) {
+        const int64_t r = last_up_to(p.q_start, p.R + 1, id);
+        const bool in = r >= 0 && r < p.R;
+        reinterpret_cast<int2 *>(entries + p.R + p.NG)[id] =
+            make_int2(in ? (int)(p.kv_len[r] - ((int64_t)p.q_start[r + 1] - id)) : -1, in ? (int)r : -1);
+    }
+    if (id < p.R) {
+        PfEntry o{};
+        pf_queries(p, id, id + 1, o);
+        o.pos_min = (int32_t)max(p.kv_len[id] - ((int64_t)p.q_start[id + 1] - p.q_start[id]), (int64_t)INT32_MIN / 2);
+        o.pos_max = o.pos_min + o.q - 1;
+        const int64_t g = last_up_to(p.group_start, p.NG + 1, id);
+        o.group = -1;
+        if (g >= 0 && g < p.NG) {
+            const PfGroup in = pf_group(p, g);
+            if (id >= in.s && id < in.e && in.tiles > 0) {
+                o.tile0 = in.tiles;
+                o.group = (int32_t)(p.R + g);
+            }
+        }
+        o.tile1 = max(o.tile0, o.q > 0 && o.pos_max >= 0 ? o.pos_max / KV_TILE + 1 : 0);
+        o.row = (int32_t)id;
+        entries[id] = o;
+    }
+    const int64_t g = id >> 5;
+    if (g < p.NG) {   // whole warps
+        const PfGroup in = pf_group(p, g);
+        PfEntry o{};
+        if (in.tiles > 0) {
+            pf_queries(p, in.s, in.e, o);
+            int lo = INT32_MAX, hi = INT32_MIN;
+            for (int64_t r = in.s + (threadIdx.x & 31); r < in.e; r += 32) {
+                PfEntry one{};
+                pf_queries(p, r, r + 1, one);
+                if (one.q == 0) continue;
+                const int first = (int)max(p.kv_len[r] - ((int64_t)p.q_start[r + 1] - p.q_start[r]), (int64_t)INT32_MIN / 2);
+                lo = min(lo, first);
+                hi = max(hi, first + one.q - 1);
+            }
+            o.pos_min = __reduce_min_sync(0xffffffffu, lo);
+            o.pos_max = __reduce_max_sync(0xffffffffu, hi);
+            o.tile1 = o.q > 0 && o.pos_max >= 0 ? min(in.tiles, o.pos_max / KV_TILE + 1) : 0;
+            o.row = (int32_t)in.s;
+        }
+        o.group = -1;
+        if ((threadIdx.x & 31) == 0) entries[p.R + g] = o;
+    }
+}
+
+int64_t prefix_plan_bytes(int64_t R, int64_t NG, int64_t n_tokens) {
+    return PF_HEADER * 4 + (R + NG) * (int64_t)sizeof(PfEntry) + n_tokens * 8;
+}
+
+static cudaError_t launch_chained(const void *kern, int64_t grid, int threads, cudaStream_t s, void **args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, kern, args);
+}
+
+cudaError_t launch_prefix_plan(const int32_t *q_start, const int32_t *kv_len, int64_t R, const int32_t *group_start,
+                               const int32_t *prefix_len, int64_t NG, int64_t page, int64_t n_tokens, void *plan, cudaStream_t s) {
+    PfPlanArgs a{q_start, kv_len, R, group_start, prefix_len, NG, page, n_tokens, (int32_t *)plan};
+    const int64_t most = std::max<int64_t>(std::max(R, n_tokens), std::max<int64_t>(32 * NG, 1));
+    void *args[1] = {&a};
+    return launch_chained((const void *)prefix_plan_kernel, (most + PF_THREADS - 1) / PF_THREADS, PF_THREADS, s, args);
+}
+
+// ---------------------------------------------------------------- join
+
+// a query row's pieces of one entry: the record, then n - 1 slots
+struct PfPieces {
+    const float *o, *ml, *slot_o, *slot_ml;
+    int64_t step;
+    int n;
+    __device__ __forceinline__ float2 stat(int i) const { return *reinterpret_cast<const float2 *>(i == 0 ? ml : slot_ml + (i - 1) * step); }
+    __device__ __forceinline__ const float *out(int i) const { return i == 0 ? o : slot_o + (i - 1) * step; }
+};
+template <int D>
+__device__ __forceinline__ PfPieces pf_pieces(const AdShape &a, int e, int64_t t, int head, int few, int rg) {
+    constexpr int64_t RS = PfStride<D>::value;
+    constexpr int ROWS = D == 256 ? 128 : 256, BTILES = D == 256 ? 4 : 8;   // the prefill kernel's (ApCfg)
+    PfPieces x{};
+    const AdReq q = pf_request(a, e);
+    if (q.nt == 0 || t < q.rows0 || t >= (int64_t)q.rows0 + q.q) return x;
+    const int kh = head / a.G, row = (int)(t - q.rows0) * a.G + head - kh * a.G;
+    const bool tc = (int64_t)q.q * a.G > few;
+    const int rows = tc ? ROWS : rg, n = tc ? (q.nt + BTILES - 1) / BTILES : q.nt;
+    const int64_t share = a.pf.share[tc], from = a.pf.base[e] + ((int64_t)(row / rows) * a.hk + kh) * n;
+    const int64_t c0 = ad_div(from, share), c1 = ad_div(from + n - 1, share);
+    x.n = (int)(c1 - c0) + 1;
+    x.o = a.pf.records + ((t + (e >= a.p.R ? a.p.n_tokens : 0)) * a.p.h + head) * RS;
+    x.ml = x.o + D;
+    const int in = row % rows;
+    if (tc) {
+        x.step = ROWS * RS;
+        x.slot_o = a.pieces + (c0 + 1) * x.step + in * RS;
+        x.slot_ml = x.slot_o + D;
+    } else {
+        x.step = (int64_t)rg * (D + 2);
+        x.slot_o = a.part + (c0 + 1) * x.step + in * D;
+        x.slot_ml = a.part + (c0 + 1) * x.step + rg * D + 2 * in;
+    }
+    return x;
+}
+
+// Bound: the pieces' bytes, from the L2 mostly.  A warp per query row; its lanes take the statistics of 32 pieces at a time,
+// so that the outputs' loads wait for nothing.
+template <int D, int QT>
+__global__ void __launch_bounds__(PF_THREADS) prefix_join_kernel(const AdShape a, const int few, const int rg) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Attn &p = a.p;
+    if (!pf_plan_fits(a)) {
+        if (blockIdx.x == 0 && threadIdx.x == 0 && p.status != nullptr) atomicAdd(p.status, 1);
+        return;
+    }
+    const int64_t w = ((int64_t)blockIdx.x * PF_THREADS + threadIdx.x) >> 5, t = w / p.h;
+    const int head = (int)(w - t * p.h), lane = threadIdx.x & 31;
+    if (t >= p.n_tokens) return;
+    const int r = pf_token(a.pf, t).y;
+    if (r < 0 || r >= p.R) return;
+    const int g = pf_entries(a.pf)[r].group;
+    const PfPieces x[2] = {pf_pieces<D>(a, r, t, head, few, rg),
+                           g >= p.R && g < a.pf.n_entries ? pf_pieces<D>(a, g, t, head, few, rg) : PfPieces{}};
+    float mx = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 2; k++)
+        for (int i = lane; i < x[k].n; i += 32) mx = fmaxf(mx, x[k].stat(i).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float base = mx == -INFINITY ? 0.0f : mx;
+    constexpr int W = D == 64 ? 2 : 4, PL = D / 32 / W;   // values per load, loads per lane
+    float l = 0.0f, v[PL * W];
+#pragma unroll
+    for (int i = 0; i < PL * W; i++) v[i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+#pragma unroll 4
+        for (int i = 0; i < x[k].n; i++) {
+            const float2 ml = x[k].stat(i);
+            const float *src = x[k].out(i) + W * lane;
+            const float f = ex2(ml.x - base);
+            l = fmaf(f, ml.y, l);
+#pragma unroll
+            for (int c = 0; c < PL; c++) {
+                if constexpr (W == 4) {
+                    const float4 u = *reinterpret_cast<const float4 *>(src + 128 * c);
+                    v[4 * c] = fmaf(f, u.x, v[4 * c]);
+                    v[4 * c + 1] = fmaf(f, u.y, v[4 * c + 1]);
+                    v[4 * c + 2] = fmaf(f, u.z, v[4 * c + 2]);
+                    v[4 * c + 3] = fmaf(f, u.w, v[4 * c + 3]);
+                } else {
+                    const float2 u = *reinterpret_cast<const float2 *>(src);
+                    v[0] = fmaf(f, u.x, v[0]);
+                    v[1] = fmaf(f, u.y, v[1]);
+                }
+            }
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t at = t * p.ldo + (int64_t)head * D + W * lane;
+#pragma unroll
+    for (int c = 0; c < PL; c++) {
+        float u[W];
+#pragma unroll
+        for (int i = 0; i < W; i++) u[i] = l == 0.0f ? 0.0f : v[W * c + i] * inv;
+        if constexpr (W == 4) store4<QT>(p.out, at + 128 * c, a.vec, u[0], u[1], u[2], u[3]);
+        else
+#pragma unroll
+            for (int i = 0; i < W; i++) store_out(p.out, QT, at + i, u[i]);
+    }
+}
+
+template <int D>
+static const void *join_kernel(int qt) {
+    return qt == GGUF_F32 ? (const void *)prefix_join_kernel<D, GGUF_F32>
+         : qt == GGUF_F16 ? (const void *)prefix_join_kernel<D, GGUF_F16> : (const void *)prefix_join_kernel<D, GGUF_BF16>;
+}
+
+// ---------------------------------------------------------------- what a call runs
+
+struct PfRun {
+    int ctas;
+    bool tc;           // the tensor-core kernel runs
+    int few, rg;       // entries of at most `few` query rows per KV head, in units of rg rows, go to the other one
+    size_t base, share, records, part, pieces, bytes;   // offsets in the workspace
+};
+static PfRun prefix_run(const Attn &p, int64_t NG, int64_t d) {
+    PfRun x{};
+    x.ctas = std::min(device_info().sm_count, 1024);
+    const int64_t G = p.h / p.hk;
+    // Units of 16 rows where a request alone has more than 8 (heads of 256 and fp32 queries have no such units).  The
+    // tensor-core kernel takes what is more than a unit: 2800 cycles for 128 tokens and up to 128 rows, against 1500 for
+    // each 8 rows and 2100 for each 16.
+    x.rg = p.qt != GGUF_F32 && d != 256 && G * p.max_q > 8 ? 16 : 8;
+    x.tc = p.qt != GGUF_F32 && p.n_tokens * G > x.rg;
+    x.few = x.tc ? x.rg : 0x7fffffff;
+    auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
+    const size_t rs = (size_t)(d + 4) * 4;
+    x.share = up((size_t)(p.R + NG) * 8);
+    x.records = x.share + 256;
+    x.part = up(x.records + 2 * (size_t)p.n_tokens * p.h * rs);
+    x.pieces = up(x.part + (size_t)x.ctas * x.rg * (d + 2) * 4);
+    x.bytes = x.tc ? x.pieces + (size_t)x.ctas * (d == 256 ? 128 : 256) * rs : x.pieces;
+    return x;
+}
+
+size_t prefix_attn_ws_size(const Attn &p, int64_t NG, int64_t d) { return prefix_run(p, NG, d).bytes; }
+
+cudaError_t launch_prefix_attn(const Attn &p, const void *plan, int64_t NG, int64_t d, void *ws, cudaStream_t s) {
+    const PfRun x = prefix_run(p, NG, d);
+    const int64_t es = p.qt == GGUF_F32 ? 4 : 2;
+    uint8_t *w = (uint8_t *)ws;
+    AdShape a{};
+    a.p = p;
+    a.err = tg_error_word();
+    auto shift_of = [](int32_t v) { return (v & (v - 1)) == 0 ? __builtin_ctz(v) : -1; };
+    a.G = (int32_t)(p.h / p.hk);
+    a.hk = (int32_t)p.hk;
+    a.G_shift = shift_of(a.G);
+    a.tpp = (int32_t)(p.page / KV_TILE);
+    a.tpp_shift = shift_of(a.tpp);
+    a.page_bytes = kv_page_bytes(d, p.hk, p.page);
+    a.vec = (reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.out)) % 16 == 0 && p.ldq * es % 16 == 0 &&
+            p.ldo * es % 16 == 0;
+    a.part = (float *)(w + x.part);
+    a.pieces = (float *)(w + x.pieces);
+    a.pf = PfShape{(const int32_t *)plan, (int32_t)(p.R + NG), x.tc, (float *)(w + x.records), (int64_t *)w, (int64_t *)(w + x.share)};
+    a.min_rows = x.few;
+    a.max_rows = 0x7fffffff;
+    if (x.tc) {
+        const cudaError_t e = d == 64 ? launch_prefix_prefill_64(a, x.ctas, s)
+                            : d == 128 ? launch_prefix_prefill_128(a, x.ctas, s) : launch_prefix_prefill_256(a, x.ctas, s);
+        if (e != cudaSuccess) return e;
+    }
+    a.min_rows = 0;
+    a.max_rows = x.few;
+    const cudaError_t e = d == 64 ? launch_prefix_decode_64(a, x.rg / 8, x.ctas, s)
+                        : d == 128 ? launch_prefix_decode_128(a, x.rg / 8, x.ctas, s) : launch_prefix_decode_256(a, x.rg / 8, x.ctas, s);
+    if (e != cudaSuccess) return e;
+    a.max_rows = 0x7fffffff;   // the join looks at all entries
+    int few = x.few, rg = x.rg;
+    void *args[3] = {&a, &few, &rg};
+    return launch_chained(d == 64 ? join_kernel<64>(p.qt) : d == 128 ? join_kernel<128>(p.qt) : join_kernel<256>(p.qt),
+                          (p.n_tokens * p.h + PF_THREADS / 32 - 1) / (PF_THREADS / 32), PF_THREADS, s, args);
+}
+
+}  // namespace gg

@@ -26,6 +26,10 @@ typedef size_t (*attn_ws_fn)(const gguf_attn_args *);
 typedef gguf_status (*attn_fn)(const gguf_attn_args *, void *, size_t, gguf_stream_t);
 typedef int64_t (*page_fn)(int64_t, int64_t, int64_t);
 typedef gguf_status (*mrope_fn)(const gguf_qk_rope_args *, const gguf_rope_axes *, gguf_stream_t);
+typedef gguf_status (*pplan_fn)(const int32_t *, const int32_t *, int64_t, const int32_t *, const int32_t *, int64_t, int64_t,
+                                int64_t, void *, size_t, gguf_stream_t);
+typedef size_t (*pattn_ws_fn)(const gguf_attn_args *, int64_t);
+typedef gguf_status (*pattn_fn)(const gguf_attn_args *, const void *, int64_t, void *, size_t, gguf_stream_t);
 typedef gguf_status (*norm_fn)(const gguf_block_norm_args *, gguf_stream_t);
 
 struct {
@@ -37,6 +41,10 @@ struct {
     page_fn page_bytes;
     mrope_fn mrope;
     norm_fn norm;
+    pplan_fn pplan;
+    pattn_ws_fn pattn_ws;
+    pattn_fn pattn;
+    page_fn pplan_bytes;
 } api;
 
 struct Bad {};   // a Python exception is set
@@ -352,35 +360,52 @@ PyObject *kv_get_rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// of q, cache, n_kv_heads, page, max_q_len, scale, window, sinks, out, status
+gguf_attn_args attn_args(PyObject *q_, PyObject *cache, PyObject *const *a, const char *what) {
+    const at::Tensor &q = tensor(q_, what, "q");
+    if (q.dim() != 3) refuse(what, "q", "[tokens, heads, head_dim]");
+    gguf_attn_args x{};
+    const at::ScalarType type = q.scalar_type();
+    x.qt = float_type(type, what);
+    x.n_tokens = q.size(0);
+    x.n_heads = q.size(1);
+    x.head_dim = q.size(2);
+    x.n_kv_heads = integer(a[0]);
+    x.page_size = integer(a[1]);
+    x.max_q_len = integer(a[2]);
+    x.scale = static_cast<float>(real(a[3]));
+    x.window = integer(a[4]);
+    x.sinks = integer(a[5]);
+    Rows r = rows(q, x.n_tokens, x.n_heads, x.head_dim, type, what, "q");
+    x.q = r.p;
+    x.ldq = r.ld;
+    r = rows(tensor(a[6], what, "out"), x.n_tokens, x.n_heads, x.head_dim, type, what, "out");
+    x.out = r.p;
+    x.ldo = r.ld;
+    const Pages c = pages(cache, x.head_dim, x.n_kv_heads, x.page_size, what);
+    x.cache = c.p;
+    x.n_pages = c.n;
+    x.dev_status = array_or_none<int32_t>(a[8], 1, what, "dev_status");
+    return x;
+}
+struct Bytes {
+    void *p;
+    size_t n;
+};
+Bytes bytes_or_none(PyObject *o, const char *what, const char *name) {
+    if (o == Py_None) return {nullptr, 0};
+    const at::Tensor &w = tensor(o, what, name);
+    if (!w.is_contiguous()) refuse(what, name, "contiguous");
+    return {w.data_ptr(), static_cast<size_t>(w.numel() * w.element_size())};
+}
+
 // q, cache, table, q_start, kv_len, n_kv_heads, page, max_q_len, scale, window, sinks, out, ws, status, stream; with ws an
 // int instead of a tensor, the bytes of workspace are returned and nothing runs
 PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
         const char *what = "gguf_paged_attention";
         count(n, 15, what);
-        const at::Tensor &q = tensor(a[0], what, "q");
-        if (q.dim() != 3) refuse(what, "q", "[tokens, heads, head_dim]");
-        gguf_attn_args x{};
-        const at::ScalarType type = q.scalar_type();
-        x.qt = float_type(type, what);
-        x.n_tokens = q.size(0);
-        x.n_heads = q.size(1);
-        x.head_dim = q.size(2);
-        x.n_kv_heads = integer(a[5]);
-        x.page_size = integer(a[6]);
-        x.max_q_len = integer(a[7]);
-        x.scale = static_cast<float>(real(a[8]));
-        x.window = integer(a[9]);
-        x.sinks = integer(a[10]);
-        Rows r = rows(q, x.n_tokens, x.n_heads, x.head_dim, type, what, "q");
-        x.q = r.p;
-        x.ldq = r.ld;
-        r = rows(tensor(a[11], what, "out"), x.n_tokens, x.n_heads, x.head_dim, type, what, "out");
-        x.out = r.p;
-        x.ldo = r.ld;
-        const Pages c = pages(a[1], x.head_dim, x.n_kv_heads, x.page_size, what);
-        x.cache = c.p;
-        x.n_pages = c.n;
+        gguf_attn_args x = attn_args(a[0], a[1], a + 5, what);
         x.n_requests = tensor(a[4], what, "kv_len").numel();
         const Table t = table(a[2], x.n_requests, what);
         x.block_table = t.p;
@@ -388,37 +413,70 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
         x.width = t.width;
         x.q_start = array<int32_t>(a[3], x.n_requests + 1, what, "q_start");
         x.kv_len = array<int32_t>(a[4], x.n_requests, what, "kv_len");
-        x.dev_status = array_or_none<int32_t>(a[13], 1, what, "dev_status");
         if (PyLong_Check(a[12])) return PyLong_FromSize_t(api.attn_ws(&x));
-        void *ws = nullptr;
-        size_t bytes = 0;
-        if (a[12] != Py_None) {
-            const at::Tensor &w = tensor(a[12], what, "ws");
-            if (!w.is_contiguous()) refuse(what, "ws", "contiguous");
-            ws = w.data_ptr();
-            bytes = w.numel() * w.element_size();
+        const Bytes w = bytes_or_none(a[12], what, "ws");
+        return PyLong_FromLong(api.attn(&x, w.p, w.n, stream(a[14])));
+    });
+}
+
+// q_start, kv_len, group_start, prefix_len, page, n_tokens, plan, stream
+PyObject *prefix_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        const char *what = "gguf_prefix_plan";
+        count(n, 8, what);
+        const int64_t r = tensor(a[1], what, "kv_len").numel(), groups = tensor(a[3], what, "prefix_len").numel();
+        const Bytes plan = bytes_or_none(a[6], what, "plan");
+        return PyLong_FromLong(api.pplan(array<int32_t>(a[0], r + 1, what, "q_start"), array<int32_t>(a[1], r, what, "kv_len"), r,
+                                         array<int32_t>(a[2], groups + 1, what, "group_start"),
+                                         array<int32_t>(a[3], groups, what, "prefix_len"), groups, integer(a[4]), integer(a[5]), plan.p,
+                                         plan.n, stream(a[7])));
+    });
+}
+
+// q, cache, table, plan, n_groups, n_kv_heads, page, max_q_len, scale, window, sinks, out, ws, status, stream; ws as above
+PyObject *prefix_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        const char *what = "gguf_prefix_attention";
+        count(n, 15, what);
+        gguf_attn_args x = attn_args(a[0], a[1], a + 5, what);
+        const Table t = table(a[2], 0, what);
+        x.n_requests = tensor(a[2], what, "block_table").size(0);
+        x.block_table = t.p;
+        x.ld_table = t.ld;
+        x.width = t.width;
+        const int64_t groups = integer(a[4]);
+        if (PyLong_Check(a[12])) return PyLong_FromSize_t(api.pattn_ws(&x, groups));
+        const at::Tensor &plan = tensor(a[3], what, "plan");
+        const int64_t need = api.pplan_bytes(x.n_requests, groups, x.n_tokens);
+        if (need >= 0 && (!plan.is_contiguous() || plan.numel() * plan.element_size() < need)) {
+            PyErr_Format(PyExc_ValueError, "%s: plan must be contiguous and of at least %lld bytes (this many requests, groups and tokens)",
+                         what, (long long)need);
+            throw Bad();
         }
-        return PyLong_FromLong(api.attn(&x, ws, bytes, stream(a[14])));
+        const Bytes w = bytes_or_none(a[12], what, "ws");
+        return PyLong_FromLong(api.pattn(&x, plan.data_ptr(), groups, w.p, w.n, stream(a[14])));
     });
 }
 
 // the addresses of gguf_kv_plan, gguf_qk_norm_rope, gguf_kv_get_rows, gguf_paged_attention_ws_size, gguf_paged_attention,
-// gguf_kv_page_bytes, gguf_qk_norm_mrope and gguf_block_norm
+// gguf_kv_page_bytes, gguf_qk_norm_mrope, gguf_block_norm, gguf_prefix_plan, gguf_prefix_attention_ws_size,
+// gguf_prefix_attention and gguf_prefix_plan_bytes
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
-        count(n, 8, "bind");
-        void *p[8];
-        for (int i = 0; i < 8; i++) p[i] = reinterpret_cast<void *>(static_cast<intptr_t>(integer(a[i])));
+        count(n, 12, "bind");
+        void *p[12];
+        for (int i = 0; i < 12; i++) p[i] = reinterpret_cast<void *>(static_cast<intptr_t>(integer(a[i])));
         api = {reinterpret_cast<plan_fn>(p[0]), reinterpret_cast<rope_fn>(p[1]), reinterpret_cast<rows_fn>(p[2]),
                reinterpret_cast<attn_ws_fn>(p[3]), reinterpret_cast<attn_fn>(p[4]), reinterpret_cast<page_fn>(p[5]),
-               reinterpret_cast<mrope_fn>(p[6]), reinterpret_cast<norm_fn>(p[7])};
+               reinterpret_cast<mrope_fn>(p[6]), reinterpret_cast<norm_fn>(p[7]), reinterpret_cast<pplan_fn>(p[8]),
+               reinterpret_cast<pattn_ws_fn>(p[9]), reinterpret_cast<pattn_fn>(p[10]), reinterpret_cast<page_fn>(p[11])};
         Py_RETURN_NONE;
     });
 }
 
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind), FAST(kv_plan), FAST(qk_norm_rope), FAST(kv_get_rows), FAST(paged_attention),
-                         FAST(qk_norm_mrope), FAST(block_norm),
+                         FAST(qk_norm_mrope), FAST(block_norm), FAST(prefix_plan), FAST(prefix_attention),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

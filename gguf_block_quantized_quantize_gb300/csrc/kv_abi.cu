@@ -157,36 +157,52 @@ static Attn attn_of(const gguf_attn_args *a) {
 }
 
 // the checks that the workspace size depends on
-static gguf_status check_attn_sizes(const gguf_attn_args *a) {
-    if (!a) return report(GGUF_ERR_INVALID_ARG, "paged_attention: null args");
-    if (!float_type(a->qt)) return refuse(GGUF_ERR_UNSUPPORTED_TYPE, "paged_attention: type %d is not F32/BF16/F16", a->qt);
-    gguf_status st = check_cache("paged_attention", a->head_dim, a->n_kv_heads, a->page_size, a->n_pages);
+static gguf_status check_attn_sizes(const gguf_attn_args *a, const char *what) {
+    if (!a) return refuse(GGUF_ERR_INVALID_ARG, "%s: null args", what);
+    if (!float_type(a->qt)) return refuse(GGUF_ERR_UNSUPPORTED_TYPE, "%s: type %d is not F32/BF16/F16", what, a->qt);
+    gguf_status st = check_cache(what, a->head_dim, a->n_kv_heads, a->page_size, a->n_pages);
     if (st != GGUF_OK) return st;
     if (a->n_tokens < 0 || a->n_requests < 0 || a->width < 0 || a->window < 0 || a->sinks < 0)
-        return report(GGUF_ERR_INVALID_ARG, "paged_attention: negative size");
+        return refuse(GGUF_ERR_INVALID_ARG, "%s: negative size", what);
     if (a->n_heads < 1 || a->n_heads > 65535 || a->n_heads % a->n_kv_heads)
-        return refuse(GGUF_ERR_SHAPE, "paged_attention: n_heads=%lld is not a multiple of n_kv_heads=%lld (at most 65535)",
+        return refuse(GGUF_ERR_SHAPE, "%s: n_heads=%lld is not a multiple of n_kv_heads=%lld (at most 65535)", what,
                       (long long)a->n_heads, (long long)a->n_kv_heads);
     if (a->n_tokens > 0x7fffffff || a->width > 0x7fffffff)
-        return report(GGUF_ERR_SHAPE, "paged_attention: n_tokens and width must fit in 31 bits");
+        return refuse(GGUF_ERR_SHAPE, "%s: n_tokens and width must fit in 31 bits", what);
     if (a->n_requests > 16384)
-        return refuse(GGUF_ERR_SHAPE, "paged_attention: %lld requests (at most 16384)", (long long)a->n_requests);
-    if (a->max_q_len < 1) return report(GGUF_ERR_INVALID_ARG, "paged_attention: max_q_len must be positive");
+        return refuse(GGUF_ERR_SHAPE, "%s: %lld requests (at most 16384)", what, (long long)a->n_requests);
+    if (a->max_q_len < 1) return refuse(GGUF_ERR_INVALID_ARG, "%s: max_q_len must be positive", what);
+    return GGUF_OK;
+}
+
+static gguf_status check_attn_rows(const gguf_attn_args *a, const char *what) {
+    const int64_t row = a->n_heads * a->head_dim;
+    if (a->ldq < row || a->ldo < row || a->ld_table < a->width)
+        return refuse(GGUF_ERR_INVALID_ARG, "%s: a row stride is shorter than the row", what);
+    if (!(a->scale > 0.0f) || a->scale > 3e38f) return refuse(GGUF_ERR_INVALID_ARG, "%s: scale must be positive and finite", what);
+    return GGUF_OK;
+}
+static gguf_status check_attn_arrays(const gguf_attn_args *a, const void *ws, size_t ws_bytes, size_t need, const char *what) {
+    const int64_t es = float_size(a->qt);
+    if (!a->q || !a->out || (a->n_pages > 0 && !a->cache) || (a->width > 0 && !a->block_table))
+        return refuse(GGUF_ERR_INVALID_ARG, "%s: null pointer", what);
+    if (!at(a->q, es) || !at(a->out, es) || !at(a->cache, 16) || !at(a->block_table, 4) || !at(a->dev_status, 4))
+        return refuse(GGUF_ERR_ALIGNMENT, "%s: cache must be 16-byte aligned, the arrays by their elements", what);
+    if (ws_bytes < need || (need > 0 && !ws))
+        return refuse(GGUF_ERR_WORKSPACE, "%s: workspace of %zu bytes < required %zu", what, ws_bytes, need);
+    if (need > 0 && !at(ws, 16)) return refuse(GGUF_ERR_ALIGNMENT, "%s: workspace must be 16-byte aligned", what);
     return GGUF_OK;
 }
 
 size_t gguf_paged_attention_ws_size(const gguf_attn_args *a) {
-    if (check_attn_sizes(a) != GGUF_OK || a->n_tokens == 0 || a->n_requests == 0) return 0;
+    if (check_attn_sizes(a, "paged_attention") != GGUF_OK || a->n_tokens == 0 || a->n_requests == 0) return 0;
     return attn_ws_size(attn_of(a), a->head_dim);
 }
 
 gguf_status gguf_paged_attention(const gguf_attn_args *a, void *ws, size_t ws_bytes, gguf_stream_t stream) {
-    gguf_status st = check_attn_sizes(a);
+    gguf_status st = check_attn_sizes(a, "paged_attention");
+    if (st == GGUF_OK) st = check_attn_rows(a, "paged_attention");
     if (st != GGUF_OK) return st;
-    const int64_t row = a->n_heads * a->head_dim, es = float_size(a->qt);
-    if (a->ldq < row || a->ldo < row || a->ld_table < a->width)
-        return report(GGUF_ERR_INVALID_ARG, "paged_attention: a row stride is shorter than the row");
-    if (!(a->scale > 0.0f) || a->scale > 3e38f) return report(GGUF_ERR_INVALID_ARG, "paged_attention: scale must be positive and finite");
     if (a->n_tokens == 0 || a->n_requests == 0) return GGUF_OK;
     // fp32 queries walk over the tokens in groups of 8 rows: a request's groups x heads x tiles of 16 tokens are counted
     // in 32 bits
@@ -196,17 +212,72 @@ gguf_status gguf_paged_attention(const gguf_attn_args *a, void *ws, size_t ws_by
         if (tiles * groups * (double)a->n_kv_heads > 4.0e9)
             return report(GGUF_ERR_SHAPE, "paged_attention: too many fp32 queries over too wide a table for one call; split it");
     }
-    if (!a->q || !a->out || !a->q_start || !a->kv_len || (a->n_pages > 0 && !a->cache) || (a->width > 0 && !a->block_table))
-        return report(GGUF_ERR_INVALID_ARG, "paged_attention: null pointer");
-    if (!at(a->q, es) || !at(a->out, es) || !at(a->cache, 16) || !at(a->block_table, 4) || !at(a->q_start, 4) ||
-        !at(a->kv_len, 4) || !at(a->dev_status, 4))
-        return report(GGUF_ERR_ALIGNMENT, "paged_attention: cache must be 16-byte aligned, the arrays by their elements");
+    if (!a->q_start || !a->kv_len) return report(GGUF_ERR_INVALID_ARG, "paged_attention: null pointer");
+    if (!at(a->q_start, 4) || !at(a->kv_len, 4)) return report(GGUF_ERR_ALIGNMENT, "paged_attention: misaligned q_start or kv_len");
     const Attn p = attn_of(a);
-    const size_t need = attn_ws_size(p, a->head_dim);
-    if (ws_bytes < need || (need > 0 && !ws))
-        return refuse(GGUF_ERR_WORKSPACE, "paged_attention: workspace of %zu bytes < required %zu", ws_bytes, need);
-    if (need > 0 && !at(ws, 16)) return report(GGUF_ERR_ALIGNMENT, "paged_attention: workspace must be 16-byte aligned");
+    st = check_attn_arrays(a, ws, ws_bytes, attn_ws_size(p, a->head_dim), "paged_attention");
+    if (st != GGUF_OK) return st;
     return launched(launch_attn(p, a->head_dim, ws, (cudaStream_t)stream), "paged_attention");
+}
+
+// requests, groups and tokens of a plan, and the step that they belong to
+static gguf_status check_plan_sizes(int64_t n_requests, int64_t n_groups, int64_t n_tokens, const char *what) {
+    if (n_requests < 0 || n_groups < 0 || n_tokens < 0) return refuse(GGUF_ERR_INVALID_ARG, "%s: negative size", what);
+    if (n_requests > 16384 || n_groups > 16384)
+        return refuse(GGUF_ERR_SHAPE, "%s: %lld requests in %lld groups (at most 16384)", what, (long long)n_requests, (long long)n_groups);
+    if (n_tokens > 0x7fffffff) return refuse(GGUF_ERR_SHAPE, "%s: n_tokens must fit in 31 bits", what);
+    return GGUF_OK;
+}
+
+int64_t gguf_prefix_plan_bytes(int64_t n_requests, int64_t n_groups, int64_t n_tokens) {
+    if (check_plan_sizes(n_requests, n_groups, n_tokens, "prefix_plan_bytes") != GGUF_OK) return -1;
+    return prefix_plan_bytes(n_requests, n_groups, n_tokens);
+}
+
+gguf_status gguf_prefix_plan(const int32_t *q_start, const int32_t *kv_len, int64_t n_requests, const int32_t *group_start,
+                             const int32_t *prefix_len, int64_t n_groups, int64_t page_size, int64_t n_tokens, void *plan,
+                             size_t plan_bytes, gguf_stream_t stream) {
+    const gguf_status st = check_plan_sizes(n_requests, n_groups, n_tokens, "prefix_plan");
+    if (st != GGUF_OK) return st;
+    if (page_size < KV_TILE || page_size % KV_TILE || page_size > (1 << 20))
+        return refuse(GGUF_ERR_SHAPE, "prefix_plan: page_size=%lld is not a multiple of 16 up to 2^20", (long long)page_size);
+    if (!plan || !q_start || (n_requests > 0 && !kv_len) || (n_groups > 0 && (!group_start || !prefix_len)))
+        return report(GGUF_ERR_INVALID_ARG, "prefix_plan: null pointer");
+    if (!at(q_start, 4) || !at(kv_len, 4) || !at(group_start, 4) || !at(prefix_len, 4) || !at(plan, 16))
+        return report(GGUF_ERR_ALIGNMENT, "prefix_plan: the plan must be 16-byte aligned, the arrays by their elements");
+    const int64_t need = prefix_plan_bytes(n_requests, n_groups, n_tokens);
+    if (plan_bytes < (size_t)need)
+        return refuse(GGUF_ERR_WORKSPACE, "prefix_plan: plan of %zu bytes < required %lld", plan_bytes, (long long)need);
+    return launched(launch_prefix_plan(q_start, kv_len, n_requests, group_start, prefix_len, n_groups, page_size, n_tokens, plan,
+                                       (cudaStream_t)stream), "prefix_plan");
+}
+
+static gguf_status check_prefix_sizes(const gguf_attn_args *a, int64_t n_groups) {
+    gguf_status st = check_attn_sizes(a, "prefix_attention");
+    if (st == GGUF_OK) st = check_plan_sizes(a->n_requests, n_groups, a->n_tokens, "prefix_attention");
+    if (st != GGUF_OK) return st;
+    if (a->n_tokens * a->n_heads > (1 << 30))   // records are counted in 31 bits, two a query row
+        return refuse(GGUF_ERR_SHAPE, "prefix_attention: %lld tokens x %lld heads (at most 2^30)", (long long)a->n_tokens, (long long)a->n_heads);
+    return GGUF_OK;
+}
+
+size_t gguf_prefix_attention_ws_size(const gguf_attn_args *a, int64_t n_groups) {
+    if (check_prefix_sizes(a, n_groups) != GGUF_OK || a->n_tokens == 0 || a->n_requests == 0) return 0;
+    return prefix_attn_ws_size(attn_of(a), n_groups, a->head_dim);
+}
+
+gguf_status gguf_prefix_attention(const gguf_attn_args *a, const void *plan, int64_t n_groups, void *ws, size_t ws_bytes,
+                                  gguf_stream_t stream) {
+    gguf_status st = check_prefix_sizes(a, n_groups);
+    if (st == GGUF_OK) st = check_attn_rows(a, "prefix_attention");
+    if (st != GGUF_OK) return st;
+    if (a->n_tokens == 0 || a->n_requests == 0) return GGUF_OK;
+    if (!plan) return report(GGUF_ERR_INVALID_ARG, "prefix_attention: null pointer");
+    if (!at(plan, 16)) return report(GGUF_ERR_ALIGNMENT, "prefix_attention: the plan must be 16-byte aligned");
+    const Attn p = attn_of(a);
+    st = check_attn_arrays(a, ws, ws_bytes, prefix_attn_ws_size(p, n_groups, a->head_dim), "prefix_attention");
+    if (st != GGUF_OK) return st;
+    return launched(launch_prefix_attn(p, plan, n_groups, a->head_dim, ws, (cudaStream_t)stream), "prefix_attention");
 }
 
 }  // extern "C"

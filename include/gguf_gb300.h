@@ -758,6 +758,53 @@ typedef struct gguf_attn_args {
 size_t gguf_paged_attention_ws_size(const gguf_attn_args *args);
 gguf_status gguf_paged_attention(const gguf_attn_args *args, void *ws, size_t ws_bytes, gguf_stream_t stream);
 
+/*
+ * gguf_prefix_plan -- which tokens the requests of a step share, group by group, as
+ * gguf_prefix_attention takes it: made once a step on the device, for all layers.
+ *   q_start, kv_len : [n_requests + 1] and [n_requests], as gguf_paged_attention's.
+ *   group_start     : [n_groups + 1] int32, non-decreasing: group g is requests
+ *                     group_start[g] .. group_start[g + 1] - 1.  Requests outside every
+ *                     group share nothing, nor does a group of one.
+ *   prefix_len      : [n_groups] int32: tokens that the group's requests have in common
+ *                     (negative: 0).  The whole pages among them are shared: they are read
+ *                     through the block table row of the group's first request.  The page
+ *                     that a prefix ends in is each request's own.
+ *   n_tokens        : rows of q of the attention; the plan covers the queries that fit.
+ *   plan            : gguf_prefix_plan_bytes(...) bytes of device memory, 16-byte aligned
+ *                     (-1 for sizes that are not supported: up to 16384 requests and groups).
+ * A request may be shorter than its group's prefix: its queries see what stands at or before
+ * their positions, as everywhere.
+ */
+int64_t gguf_prefix_plan_bytes(int64_t n_requests, int64_t n_groups, int64_t n_tokens);
+gguf_status gguf_prefix_plan(const int32_t *q_start, const int32_t *kv_len, int64_t n_requests, const int32_t *group_start,
+                             const int32_t *prefix_len, int64_t n_groups, int64_t page_size, int64_t n_tokens, void *plan,
+                             size_t plan_bytes, gguf_stream_t stream);
+
+/*
+ * gguf_prefix_attention -- gguf_paged_attention for a batch whose requests share long
+ * prefixes: the shared tokens of a group are read and unpacked once for the queries of all
+ * its requests.  Where the rows of the block table list the same pages for the tokens that a
+ * group shares, the outputs are gguf_paged_attention's (in other bits).
+ *   args : as gguf_paged_attention; q_start and kv_len are not looked at (they are in the
+ *          plan).  max_q_len only chooses kernels: all queries are computed.
+ *   plan : made by gguf_prefix_plan, on this stream or complete, with these n_requests,
+ *          n_groups, n_tokens and page_size.  A plan of other sizes is not used: nothing
+ *          is written, and dev_status counts 1.
+ *   dev_status : + pages outside the cache or past the table, each once per request whose
+ *          own tokens, or once per group whose shared ones, would be seen in it.
+ *   ws   : gguf_prefix_attention_ws_size(args, n_groups) bytes, 16-byte aligned: about
+ *          8 (head_dim + 4) bytes per token and head, and up to 21 MB (40 MB with heads of 256).
+ * n_tokens x n_heads <= 2^30 (GGUF_ERR_SHAPE above).  Precision, windows, blocks that are not
+ * finite (which may reach the queries of their group) and timeouts are as described at
+ * gguf_paged_attention; the bits of a request's outputs depend on the batch.  Made for few
+ * queries per request (decoding, tokens to check): long chunks of prompts go through, but
+ * blocks that causality hides from all of a chunk's first rows are computed and dropped.
+ * Same bits on every run.
+ */
+size_t gguf_prefix_attention_ws_size(const gguf_attn_args *args, int64_t n_groups);
+gguf_status gguf_prefix_attention(const gguf_attn_args *args, const void *plan, int64_t n_groups, void *ws, size_t ws_bytes,
+                                  gguf_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

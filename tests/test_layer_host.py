@@ -69,3 +69,55 @@ def test_mrope_refusals(lib, kw, want):
 def test_mrope_nothing_to_do(lib):
     assert mrope(lib, n_tokens=0, q=None, positions=None) == 0
     assert lib.gguf_qk_norm_mrope(None, ctypes.byref(g.RopeAxes()), None) == INVALID
+
+
+def test_prefix_plan_bytes(lib):
+    assert g.gguf_prefix_plan_bytes(0, 0, 0) == 32
+    assert g.gguf_prefix_plan_bytes(5, 2, 11) == 32 + 7 * 32 + 11 * 8
+    for bad in ((-1, 0, 0), (0, -1, 0), (0, 0, -1), (16385, 0, 0), (0, 16385, 0), (0, 0, 1 << 31)):
+        assert g.gguf_prefix_plan_bytes(*bad) == -1
+
+
+def plan(lib, **kw):
+    a = dict(start=256, kv=256, r=4, group=256, prefix=256, ng=2, page=16, n=8, plan=256, bytes=1 << 20, stream=None)
+    a.update(kw)
+    return lib.gguf_prefix_plan(*a.values())
+
+
+@pytest.mark.parametrize("kw, want", [
+    (dict(r=-1), INVALID), (dict(ng=-1), INVALID), (dict(n=-1), INVALID), (dict(r=16385), SHAPE), (dict(ng=16385), SHAPE),
+    (dict(n=1 << 31), SHAPE), (dict(page=0), SHAPE), (dict(page=24), SHAPE), (dict(page=1 << 21), SHAPE), (dict(start=None), INVALID),
+    (dict(kv=None), INVALID), (dict(group=None), INVALID), (dict(prefix=None), INVALID), (dict(plan=None), INVALID),
+    (dict(start=258), ALIGN), (dict(kv=257), ALIGN), (dict(group=258), ALIGN), (dict(prefix=258), ALIGN), (dict(plan=264), ALIGN),
+    (dict(bytes=32 + 6 * 32 + 8 * 8 - 1), WS)])
+def test_prefix_plan_refusals(lib, kw, want):
+    assert plan(lib, **kw) == want
+    assert b"prefix_plan" in lib.gguf_last_error()
+
+
+def prefix(lib, plan=256, ng=2, ws=256, ws_bytes=1 << 40, **kw):
+    a = dict(q=256, qt=g.BF16, n_tokens=4, ldq=1024, cache=256, n_pages=4, page_size=16, block_table=256, ld_table=4,
+             width=4, q_start=0, kv_len=0, n_requests=4, max_q_len=1, n_heads=8, n_kv_heads=2, head_dim=128,
+             scale=0.1, window=0, sinks=0, out=256, ldo=1024, dev_status=0)
+    a.update(kw)
+    return lib.gguf_prefix_attention(ctypes.byref(g.AttnArgs(*a.values())), plan, ng, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw, want", [
+    (dict(qt=g.Q4_0), TYPE), (dict(n_tokens=-1), INVALID), (dict(n_requests=-1), INVALID), (dict(ng=-1), INVALID),
+    (dict(ng=16385), SHAPE), (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(head_dim=80), SHAPE),
+    (dict(page_size=20), SHAPE), (dict(n_kv_heads=3), SHAPE), (dict(n_requests=16385), SHAPE), (dict(max_q_len=0), INVALID),
+    (dict(n_tokens=(1 << 27) + 1), SHAPE), (dict(ldq=1000), INVALID), (dict(ldo=1000), INVALID), (dict(ld_table=3), INVALID),
+    (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID), (dict(q=None), INVALID), (dict(out=None), INVALID),
+    (dict(plan=None), INVALID), (dict(cache=None), INVALID), (dict(block_table=None), INVALID), (dict(plan=264), ALIGN),
+    (dict(q=257), ALIGN), (dict(out=257), ALIGN), (dict(cache=264), ALIGN), (dict(block_table=258), ALIGN), (dict(dev_status=258), ALIGN)])
+def test_prefix_attention_refusals(lib, kw, want):
+    assert prefix(lib, **kw) == want
+    assert b"prefix_attention" in lib.gguf_last_error()
+
+
+def test_prefix_attention_nothing_to_do(lib):
+    assert prefix(lib, n_tokens=0, q=None, out=None, plan=None) == 0
+    assert prefix(lib, n_requests=0, q=None, out=None, plan=None) == 0
+    assert lib.gguf_prefix_attention(None, 256, 2, None, 0, None) == INVALID
+    assert lib.gguf_prefix_attention_ws_size(None, 2) == 0
