@@ -150,7 +150,7 @@ SIGNATURES = {
     "gguf_prefix_plan_bytes": (_i64, [_i64, _i64, _i64]),
     "gguf_prefix_plan": (_i, [_p, _p, _i64, _p, _p, _i64, _i64, _i64, _p, _sz, _p]),
     "gguf_prefix_attention_ws_size": (_sz, [ctypes.POINTER(AttnArgs), _i64]),
-    "gguf_prefix_attention": (_i, [ctypes.POINTER(AttnArgs), _p, _i64, _p, _sz, _p]),
+    "gguf_prefix_attention": (_i, [ctypes.POINTER(AttnArgs), _p, _sz, _i64, _p, _sz, _p]),
     "gguf_debug_block_dots": (_i, [_p, _i, _i64, _i64, _p, _i64, _p, _p]),
     "gguf_set_option": (_i, [ctypes.c_char_p, _i64]),
     "gguf_get_option": (_i64, [ctypes.c_char_p]),
@@ -526,7 +526,7 @@ def _bound():
         _bind.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "gguf_kv_plan", "gguf_qk_norm_rope", "gguf_kv_get_rows", "gguf_paged_attention_ws_size", "gguf_paged_attention",
             "gguf_kv_page_bytes", "gguf_qk_norm_mrope", "gguf_block_norm", "gguf_prefix_plan", "gguf_prefix_attention_ws_size",
-            "gguf_prefix_attention", "gguf_prefix_plan_bytes")))
+            "gguf_prefix_attention")))
         _native = _bind
     return _native
 

@@ -57,11 +57,12 @@ namespace gg {
 
 constexpr float AD_PBITS = 10.0f;   // probabilities are held times 2^10 (at most 1024): small ones keep their bits in fp16
 
+constexpr int ad_warps(int d, bool f32, int nt) { return d == 256 || nt == 2 || f32 ? 8 : 12; }
 template <int D, int QT, int NT>
 struct AdCfg {
     static constexpr int RG = 8 * NT;                       // query rows of a unit
     // warps that compute; one more warpgroup holds the warp that asks for the copies, and gives registers to them
-    static constexpr int WARPS = (D == 256 || NT == 2 || QT == GGUF_F32) ? 8 : 12;
+    static constexpr int WARPS = ad_warps(D, QT == GGUF_F32, NT);
     static constexpr int THREADS = WARPS * 32 + 128;
     static constexpr int REGS = WARPS == 8 ? 224 : 152, REGS_COPY = 56;   // sums of a launch at 168 and 128
     static constexpr int TP = D == 256 && QT == GGUF_F32 ? 1 : D == 64 && NT == 1 && QT != GGUF_F32 ? 4 : 2;   // tiles at a time
@@ -85,14 +86,17 @@ struct PfEntry {
 };
 // gguf_prefix_attention: what its kernels have beside AdShape's members.  A query row (token and head) has a record of
 // PfStride<D> floats, its output, maximum and sum, for its request's own tiles and, n_tokens x heads records later, one
-// for its group's: the first piece of its unit, whatever else of the unit's tiles other CTAs took.  Those leave a slot each.
+// for its group's: of the first piece of its unit.  The rest of the unit's tiles went to the warps (decode kernel) or CTAs
+// (prefill kernel) that follow in the sequence; each has one slot, of rows like records, for a unit that began before it.
 struct PfShape {
-    const int32_t *plan;       // header, entries, then position and request of each token
+    const int32_t *plan;       // header, entries, then of each token its position, and its request and group (pf_pack)
     int32_t n_entries, chained;   // chained: the decode kernel follows the prefill kernel of the call
     float *records;
     int64_t *base;             // tiles (decode kernel) or blocks (prefill kernel) before each entry's, of the kernel that takes it
-    int64_t *share;            // a CTA's tiles, a CTA's blocks
+    int64_t *share;            // tiles of a CTA (decode kernel), blocks of a CTA (prefill kernel), tiles of a warp
 };
+// warps of a CTA that have tiles
+__device__ __forceinline__ int pf_warps(int64_t share, int64_t per_warp) { return (int)((share + per_warp - 1) / per_warp); }
 constexpr int PF_HEADER = 8, PF_MAGIC = 0x50465831;   // {magic, requests, groups, tokens, page size, 0, 0, 0}
 template <int D> struct PfStride { static constexpr int64_t value = D + 4; };   // 16-byte steps
 
@@ -159,13 +163,16 @@ __device__ __forceinline__ AdReq ad_request(const AdShape &a, int r) {
 }
 // the same of an entry of the plan; what is not a plan of this call has no queries
 __device__ __forceinline__ const PfEntry *pf_entries(const PfShape &f) { return reinterpret_cast<const PfEntry *>(f.plan + PF_HEADER); }
-__device__ __forceinline__ int2 pf_token(const PfShape &f, int64_t t) {   // position and request
+__device__ __forceinline__ int2 pf_token(const PfShape &f, int64_t t) {
     return reinterpret_cast<const int2 *>(pf_entries(f) + f.n_entries)[t];
 }
+// a request and its group (-1: none) in one word; -1: no request
+__device__ __forceinline__ int pf_pack(int r, int g) { return r < 0 ? -1 : r | (g + 1) << 16; }
+__device__ __forceinline__ int2 pf_unpack(int w) { return w < 0 ? make_int2(-1, -1) : make_int2(w & 0xffff, (w >> 16) - 1); }
 __device__ __forceinline__ bool pf_plan_fits(const AdShape &a) {
-    const int32_t *h = a.pf.plan;
-    return h[0] == PF_MAGIC && h[1] == (int32_t)a.p.R && h[2] == a.pf.n_entries - (int32_t)a.p.R && h[3] == (int32_t)a.p.n_tokens &&
-           h[4] == (int32_t)a.p.page;
+    const int4 h = *reinterpret_cast<const int4 *>(a.pf.plan);
+    return h.x == PF_MAGIC && h.y == (int32_t)a.p.R && h.z == a.pf.n_entries - (int32_t)a.p.R && h.w == (int32_t)a.p.n_tokens &&
+           a.pf.plan[4] == (int32_t)a.p.page;
 }
 __device__ __forceinline__ AdReq pf_request(const AdShape &a, int e) {
     AdReq o;
@@ -292,12 +299,7 @@ __device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t (&w)[N]) {
     }
 }
 
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     tc::smem_u32(dst)),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(tc::smem_u32(bar))
-                 : "memory");
-}
+using tc::bulk_load;
 
 // four consecutive outputs
 template <int QT>
@@ -378,12 +380,14 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     // takes one whole unit) and, once the sum of what comes before is known, writes down where the warps start whose
     // first tile lies in them.
     constexpr int NTHR = C::THREADS;
-    const int R = PRE && !pf_plan_fits(a) ? 0 : ad_requests<PRE>(a);
-    const int per = (R + NTHR - 1) / NTHR, r0 = tid * per, r1 = min(R, r0 + per);
+    const int R = ad_requests<PRE>(a), per = (R + NTHR - 1) / NTHR, r0 = tid * per, r1 = min(R, r0 + per);
     AdReq rq{};
     int64_t mine = 0;
+    bool fits = true;   // (the entries are there to be read in any case)
+    if constexpr (PRE) fits = pf_plan_fits(a);
     for (int r = r0; r < r1; r++) {
         rq = ad_request_of<PRE>(a, r);
+        if (PRE && !fits) rq.q = rq.nt = 0;
         mine += ad_units(a, rq, RG) * (!PRE && a.whole ? 1 : rq.nt);
         if (!PRE && rq.q > 0 && rq.nt == 0) blind = 1;   // (every writer writes the same)
     }
@@ -404,11 +408,17 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
         total += warp_sum[w];
     }
     const int64_t share = !PRE && a.whole ? 1 : ad_div(total + gridDim.x - 1, gridDim.x);
-    if (PRE && blockIdx.x == 0 && tid == 0) a.pf.share[0] = share;
     int64_t cta0 = min(total, (int64_t)blockIdx.x * share), cta1 = min(total, cta0 + share);
     int64_t per_warp = ad_div(cta1 - cta0 + C::WARPS - 1, C::WARPS);
+    if constexpr (PRE) {   // the same in all CTAs
+        per_warp = ad_div(share + C::WARPS - 1, C::WARPS);
+        if (blockIdx.x == 0 && tid == 0) { a.pf.share[0] = share; a.pf.share[2] = per_warp; }
+    }
     for (int r = r0; r < r1; r++) {
-        if (per > 1) rq = ad_request_of<PRE>(a, r);
+        if (per > 1) {
+            rq = ad_request_of<PRE>(a, r);
+            if (PRE && !fits) rq.q = rq.nt = 0;
+        }
         const int64_t units = ad_units(a, rq, RG), n = units * (!PRE && a.whole ? 1 : rq.nt);
         if (PRE && blockIdx.x == 0 && rq.q > 0) a.pf.base[r] = before;
         if (before < cta1 && before + n > cta0) {
@@ -858,7 +868,10 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
 #pragma unroll
                     for (int i = 4; i < 32; i <<= 1) lsum[n][j] += __shfl_xor_sync(0xffffffffu, lsum[n][j], i);
             const bool unit_end = cur.tile == cur.q.nt;
-            if (PRE && unit_end && began) {   // a whole unit: its records
+            if constexpr (PRE) {   // rows of a unit that began here: their records; of one from the warp before: the warp's slot
+                const int64_t at = (cur.q.rows0 + (cur.r >= p.R ? p.n_tokens : 0)) * p.h + head0;
+                const int used = pf_warps(share, per_warp);
+                float *slot = a.part + (int64_t)(blockIdx.x * used + warp) * (RG * PfStride<D>::value);
 #pragma unroll
                 for (int n = 0; n < NT; n++)
 #pragma unroll
@@ -866,7 +879,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                         const int row = row0 + 8 * n + 2 * q4 + j;
                         if (row < rows) {
                             const int tk = ad_token_of_row(a, row);
-                            float *to = a.pf.records + ((cur.q.rows0 + tk + (cur.r >= p.R ? p.n_tokens : 0)) * p.h + head0 + row - tk * G) * PfStride<D>::value;
+                            float *to = began ? a.pf.records + (at + tk * p.h + row - tk * G) * PfStride<D>::value : slot + (row - row0) * PfStride<D>::value;
 #pragma unroll
                             for (int b = 0; b < NB; b++)
                                 *reinterpret_cast<float4 *>(to + 32 * b + 4 * g) =
@@ -894,7 +907,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                 // a unit from before the warp leaves its piece beside the ring; one that goes on past the warp ends
                 // with the warp's last tile, and takes the ring, where no copy is under way any more
                 flags |= began ? 4 : unit_end ? 1 : 3;
-                if (began) { open_row = cur.q.rows0 + (PRE && cur.r >= p.R ? (int)p.n_tokens : 0); open_rows = rows; open_u = cur.u; open_end = t1 + cur.q.nt - cur.tile; }
+                if (began) { open_row = cur.q.rows0; open_rows = rows; open_u = cur.u; open_end = t1 + cur.q.nt - cur.tile; }
                 __syncwarp();
                 float *dst = reinterpret_cast<float *>(began ? ring : smem + C::WARPS * C::RING + warp * C::SLOT);
 #pragma unroll
@@ -913,6 +926,10 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             }
             if (left_tiles > 0) ad_next_unit<RG, PRE>(a, cur);
         }
+    }
+    if constexpr (PRE) {   // what follows this launch may count on the prefill kernel's records too
+        if (a.pf.chained) asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
     }
     if (lane == 0) {
         left[warp] = flags;
@@ -950,15 +967,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                 l = fmaf(f, ml.y, l);
                 v.x = fmaf(f, x.x, v.x); v.y = fmaf(f, x.y, v.y); v.z = fmaf(f, x.z, v.z); v.w = fmaf(f, x.w, v.w);
             }
-            if (PRE && !orphan) {
-                const int u = left_u[chain], group = u / a.hk, at_row = group * RG + row;
-                if (at_row < left_rows[chain]) {
-                    const int tk = ad_token_of_row(a, at_row);
-                    float *to = a.pf.records + (((int64_t)left_row[chain] + tk) * p.h + (u - group * a.hk) * G + at_row - tk * G) * PfStride<D>::value;
-                    *reinterpret_cast<float4 *>(to + col) = v;
-                    if (col == 0) *reinterpret_cast<float2 *>(to + D) = make_float2(mx, l);
-                }
-            } else if (!orphan && !open) {
+            if (!orphan && !open) {
                 const int u = left_u[chain], group = u / a.hk, at_row = group * RG + row;
                 if (at_row < left_rows[chain]) {
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -967,7 +976,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                                a.vec, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
                 }
             } else {
-                float *dst = a.part + (PRE ? (int64_t)blockIdx.x : (int64_t)(2 * blockIdx.x + (orphan ? 0 : 1))) * (C::SLOT / 4);
+                float *dst = a.part + (int64_t)(2 * blockIdx.x + (orphan ? 0 : 1)) * (C::SLOT / 4);
                 *reinterpret_cast<float4 *>(dst + row * D + col) = v;
                 if (col == 0) {
                     dst[RG * D + 2 * row] = mx;
@@ -995,10 +1004,6 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             }
             break;
         }
-    }
-    if constexpr (PRE) {   // what follows this launch may count on the prefill kernel's records too
-        if (a.pf.chained) asm volatile("griddepcontrol.wait;" ::: "memory");
-        return;
     }
     if (tid == 0 && !a.whole) {
         AdMeta m{};

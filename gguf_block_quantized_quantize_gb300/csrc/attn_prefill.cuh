@@ -79,6 +79,12 @@ struct ApItem {
     int first, pos_max;           // (PRE) 1: the piece with the row block's first tiles, of a request's own tiles; 2: of a
 };                                // group's; 0: another piece.  The entry's last position
 
+// (PRE) a place in the sequence of blocks: entry, row block x head, block
+struct ApPlace {
+    int entry, unit, blk;
+    AdReq q;
+};
+
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -114,6 +120,15 @@ __device__ __forceinline__ uint64_t add_2(uint64_t x, uint64_t y) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
     return r;
 }
+
+// a bulk copy from shared memory; the thread's copies have read their sources; they are complete
+__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
+                 "r"(tc::smem_u32(src)), "r"(bytes) : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 template <int N>
 __device__ __forceinline__ void set_registers() {   // from 128 at launch
@@ -153,6 +168,31 @@ __device__ __forceinline__ bool ap_first_sight(const AdShape &a, const ApItem &w
 // blocks in one sequence, cut evenly over the CTAs; rows of several requests, each with its own position; records and
 // slots instead of outputs.
 enum { AP_PLAIN = 0, AP_CUT = 1, AP_PRE = 2 };
+// where block `at` of the sequence lies (it is there: a thread holds `per` entries, and chunk_end the blocks up to its last)
+template <int D, int QT, class Count>
+__device__ __forceinline__ ApPlace ap_place(const AdShape &a, const Count *chunk_end, int64_t at, int per) {
+    using C = ApCfg<D, QT>;
+    int lo = -1, hi = AP_THREADS - 1;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (chunk_end[mid] > at) hi = mid;
+        else lo = mid;
+    }
+    if (hi > 0) at -= chunk_end[hi - 1];
+    ApPlace w;
+    int nblk;
+    for (w.entry = hi * per;; w.entry++) {
+        w.q = pf_request(a, w.entry);
+        nblk = (w.q.nt + C::GT - 1) / C::GT;
+        const int64_t n = (int64_t)ap_items(a, w.q, C::RT * 128) * nblk;
+        if (at < n) break;
+        at -= n;
+    }
+    w.unit = (int)ad_div(at, nblk);
+    w.blk = (int)(at - (int64_t)w.unit * nblk);
+    return w;
+}
+
 template <int D, int QT, int MODE>
 __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdShape a) {
     constexpr bool CUT = MODE == AP_CUT, PRE = MODE == AP_PRE, PARTS = MODE != AP_PLAIN;
@@ -172,6 +212,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     using Count = std::conditional_t<PRE, int64_t, int32_t>;
     __shared__ Count chunk_end[AP_THREADS];   // at most (tokens x heads / 128) items: 31 bits; (PRE) blocks of all items
     __shared__ Count pre_sum[PRE ? AP_THREADS / 32 : 1];
+    __shared__ ApPlace place[1];   // thread 0's
     volatile int32_t *abort_flag = &abort_word;
     const Attn &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -198,14 +239,16 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     // Work of all requests: thread t counts requests [t * per, (t + 1) * per), in row blocks of ROWS rows, and of 128.
     // The larger ones unpack a key for twice the rows; the smaller ones are for calls that would leave SMs idle, as are
     // row blocks whose tokens are cut into pieces (CUT; of 4 blocks at least, joined by a second launch).
-    const int R = PRE && !pf_plan_fits(a) ? 0 : ad_requests<PRE>(a), per = (R + AP_THREADS - 1) / AP_THREADS;
+    const int R = ad_requests<PRE>(a), per = (R + AP_THREADS - 1) / AP_THREADS;
     auto blocks_of = [](const AdReq &q) { return (q.nt + BT / KV_TILE - 1) / (BT / KV_TILE); };
     if constexpr (PRE) {
         int64_t mine = 0;
+        const bool fits = pf_plan_fits(a);   // (the entries are there to be read in any case)
         for (int r = tid * per; r < min(R, (tid + 1) * per); r++) {
             const AdReq q = pf_request(a, r);
             mine += (int64_t)ap_items(a, q, ROWS) * blocks_of(q);
         }
+        if (!fits) mine = 0;
         int64_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -218,7 +261,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         tc::tc_fence_after();
         for (int w = 0; w < warp; w++) incl += pre_sum[w];
         chunk_end[tid] = incl;
-        if (blockIdx.x == 0) {   // for the join
+        if (blockIdx.x == 0 && fits) {   // for the join
             int64_t before = incl - mine;
             for (int r = tid * per; r < min(R, (tid + 1) * per); r++) {
                 const AdReq q = pf_request(a, r);
@@ -285,12 +328,17 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         if (lane == 0) tc::mbar_arrive(bar);
     };
     // (PRE) the CTA's blocks of the sequence
-    const int64_t share = PRE ? ad_div(total + gridDim.x - 1, gridDim.x) : 0;
-    const int64_t own0 = PRE ? min(total, (int64_t)blockIdx.x * share) : 0, own1 = PRE ? min(total, own0 + share) : 0;
-    if (PRE && blockIdx.x == 0 && tid == 0) a.pf.share[1] = share;
+    int own = 0;
+    if constexpr (PRE) {
+        const int64_t share = ad_div(total + gridDim.x - 1, gridDim.x), own0 = min(total, (int64_t)blockIdx.x * share);
+        own = (int)(min(total, own0 + share) - own0);
+        if (blockIdx.x == 0 && tid == 0) a.pf.share[1] = share;
+        if (own > 0 && tid == 0) place[0] = ap_place<D, QT>(a, chunk_end, own0, per);
+    }
     auto token_of = [&](int i) { return (i < item.n_sink ? i : item.w_tile + i - item.n_sink) * KV_TILE; };
 
     // items in stripes of one per CTA, every other stripe backwards: a request's row blocks come longest first
+    using Stripe = std::conditional_t<PRE, int, int64_t>;   // (PRE) blocks of the CTA's own
     const int64_t stripes = (total + gridDim.x - 1) / gridDim.x;
     auto item_of = [&](int64_t stripe) { return stripe * gridDim.x + ((stripe & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x); };
     auto everyone = [] { asm volatile("bar.sync 0, %0;" ::"n"(AP_THREADS) : "memory"); };
@@ -299,7 +347,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         int blocks_before = 0, loads_before = 0, uses[2] = {0, 0}, nrt = 0, nblk = 0, nitems = 0, items = -1;
     };
     // the item before is done with (its shared and tensor memory are free), and the next one is known
-    auto begin = [&](Walk &wk, int64_t piece) {
+    auto begin = [&](Walk &wk, Stripe piece) {
         wk.blocks_before += wk.nblk;
         wk.loads_before += 2 * wk.nblk;
         wk.uses[0] += (wk.nitems + 1) / 2;
@@ -309,40 +357,33 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         everyone();
         tc::tc_fence_after();
         if (*abort_flag) return false;
-        if (PRE && tid == 0) {   // piece: the first block
-            int lo = -1, hi = AP_THREADS - 1;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (chunk_end[mid] > piece) hi = mid;
-                else lo = mid;
-            }
-            int64_t before = hi > 0 ? chunk_end[hi - 1] : 0;
+        if (PRE && tid == 0) {   // piece: its first block, of the CTA's own
+            ApPlace at = place[0];
+            const int nblk = blocks_of(at.q), left = min(nblk - at.blk, own - (int)piece), rb = at.unit / a.hk;
             ApItem w;
-            AdReq q;
-            int e = hi * per, nblk;
-            for (;; e++) {   // it is there: piece < total
-                q = pf_request(a, e);
-                nblk = blocks_of(q);
-                const int64_t n = (int64_t)ap_items(a, q, ROWS) * nblk;
-                if (before + n > piece) break;
-                before += n;
-            }
-            const int64_t u = ad_div(piece - before, nblk);
-            const int blk = (int)(piece - before - u * nblk), left = (int)min((int64_t)(nblk - blk), own1 - piece);
-            w.r = q.row;
-            w.head = (int)(u % a.hk);
-            w.row0 = (int)(u / a.hk) * ROWS;
-            w.rows = min(ROWS, q.q * G - w.row0);
-            w.q0 = q.rows0;
-            w.tok0 = w.row0 / G;
+            w.r = at.q.row;
+            w.head = at.unit - rb * a.hk;
+            w.row0 = rb * ROWS;
+            w.rows = min(ROWS, at.q.q * G - w.row0);
+            w.q0 = at.q.rows0;
+            w.tok0 = 0;
             w.pos0 = 0;
-            w.n_sink = q.n_sink;
-            w.w_tile = q.w_tile;
-            w.base = blk * (BT / KV_TILE);
-            w.nt = min(q.nt, (blk + left) * (BT / KV_TILE));
-            w.first = blk > 0 ? 0 : e >= p.R ? 2 : 1;
-            w.pos_max = q.pos_max;
+            w.n_sink = at.q.n_sink;
+            w.w_tile = at.q.w_tile;
+            w.base = at.blk * (BT / KV_TILE);
+            w.nt = min(at.q.nt, (at.blk + left) * (BT / KV_TILE));
+            w.part = -1;
+            w.first = at.blk > 0 ? 0 : at.entry >= p.R ? 2 : 1;
+            w.pos_max = at.q.pos_max;
             item = w;
+            // the next one
+            at.blk = 0;
+            if ((int)piece + left < own && ++at.unit == ap_items(a, at.q, ROWS)) {
+                at.unit = 0;
+                do at.q = pf_request(a, ++at.entry);
+                while (at.q.nt == 0);
+            }
+            place[0] = at;
         }
         if (!PRE && tid == 0) {
             const int item_rows = cut_rows, splits = CUT ? cut_pieces : 1;
@@ -403,45 +444,58 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     Walk wk;
     if (warp < 8) {
         set_registers<C::REGS>();
-        for (int64_t st = 0; PRE ? own0 + st < own1 : st < stripes; st += PRE ? wk.nblk : 1) {
-            const int64_t it = PRE ? own0 + st : item_of(st);
+        for (Stripe st = 0; PRE ? st < own : st < stripes; st += PRE ? wk.nblk : 1) {
+            const int64_t it = PRE ? st : item_of(st);
             if (!PRE && it >= total) continue;
             if (!begin(wk, it)) break;
             // ---- queries: D / 8 lanes per row, 8 values each
             {
-                constexpr int LPR = D / 8;
-                for (int row = tid / LPR; row < ROWS; row += 256 / LPR) {
-                    const int l = tid % LPR, rr = item.row0 + row;
-                    uint32_t w[4] = {0, 0, 0, 0};
-                    if (row < item.rows) {
-                        const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + (item.q0 + rr / G) * p.ldq +
-                                              (int64_t)(item.head * G + rr % G) * D + 8 * l;
-                        if (a.vec) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(src);
-                            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-                        } else {
+                // (PRE: few blocks follow, so the loads of many rows are under way at once: one at a time took 12000 cycles)
+                constexpr int LPR = D / 8, AT_ONCE = PRE ? 8 : 1;
+                const int rows_used = PRE ? wk.nrt * 128 : ROWS;
+                for (int row0 = tid / LPR; row0 < rows_used; row0 += AT_ONCE * (256 / LPR)) {
+                    uint32_t w[AT_ONCE][4];
+                    const int l = tid % LPR;
 #pragma unroll
-                            for (int i = 0; i < 4; i++) w[i] = src[2 * i] | (uint32_t)src[2 * i + 1] << 16;
+                    for (int i = 0; i < AT_ONCE; i++) {
+                        const int row = row0 + i * (256 / LPR), rr = item.row0 + row;
+                        w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0;
+                        if (row < item.rows) {
+                            const int tk = PRE ? ad_token_of_row(a, rr) : rr / G;
+                            const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + (item.q0 + tk) * p.ldq +
+                                                  (int64_t)(item.head * G + rr - tk * G) * D + 8 * l;
+                            if (a.vec) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(src);
+                                w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+                            } else {
+#pragma unroll
+                                for (int x = 0; x < 4; x++) w[i][x] = src[2 * x] | (uint32_t)src[2 * x + 1] << 16;
+                            }
                         }
                     }
-                    if constexpr (QT == GGUF_BF16) {
-                        float v[8], mx = 0.0f;
 #pragma unroll
-                        for (int i = 0; i < 8; i++) {
-                            v[i] = bf2f((uint16_t)(w[i / 2] >> (16 * (i & 1))));
-                            mx = fmaxf(mx, fabsf(v[i]));
-                        }
-                        // a row's lanes lie in one warp and all of them are here (256 / LPR divides ROWS)
+                    for (int i = 0; i < AT_ONCE; i++) {
+                        const int row = row0 + i * (256 / LPR);
+                        if constexpr (QT == GGUF_BF16) {
+                            float v[8], mx = 0.0f;
 #pragma unroll
-                        for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                        const float up = q_scale_up(mx);
+                            for (int x = 0; x < 8; x++) {
+                                v[x] = bf2f((uint16_t)(w[i][x / 2] >> (16 * (x & 1))));
+                                mx = fmaxf(mx, fabsf(v[x]));
+                            }
+                            // a row's lanes lie in one warp and all of them are here (256 / LPR divides the rows)
 #pragma unroll
-                        for (int i = 0; i < 4; i++) w[i] = pack_h2(v[2 * i] * up, v[2 * i + 1] * up);
-                        if (l == 0) q_inv[row] = 1.0f / up;
-                    } else if (l == 0) q_inv[row] = 1.0f;
-                    const int tile = row / 128, r7 = row % 128;
-                    *reinterpret_cast<uint4 *>(smem + tile * (128 * D * 2) + (8 * l / 64) * 16384 + r7 * 128 +
-                                               (((l & 7) ^ (r7 & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                            const float up = q_scale_up(mx);
+#pragma unroll
+                            for (int x = 0; x < 4; x++) w[i][x] = pack_h2(v[2 * x] * up, v[2 * x + 1] * up);
+                            if (l == 0 && row < rows_used) q_inv[row] = 1.0f / up;
+                        } else if (l == 0 && row < rows_used) q_inv[row] = 1.0f;
+                        const int tile = row / 128, r7 = row % 128;
+                        if (row < rows_used)
+                            *reinterpret_cast<uint4 *>(smem + tile * (128 * D * 2) + (8 * l / 64) * 16384 + r7 * 128 +
+                                                       (((l & 7) ^ (r7 & 7)) * 16)) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+                    }
                 }
                 tc::fence_proxy_async_smem();
                 arrive(&q_full);
@@ -454,7 +508,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                 const uint32_t lanes = (uint32_t)(quad * 32) << 16;
                 const uint32_t o_col = tmem + lanes + C::COL_O + t * D;
                 const bool there = row < item.rows;
-                const int pos = !there ? -1 : PRE ? pf_token(a.pf, item.q0 + (item.row0 + row) / G).x : item.pos0 + (item.row0 + row) / G - item.tok0;
+                const int pos = !there ? -1 : PRE ? pf_token(a.pf, item.q0 + ad_token_of_row(a, item.row0 + row)).x : item.pos0 + (item.row0 + row) / G - item.tok0;
                 // positions of the warp's rows, from the first to the last that is there
                 const int lastr = min(item.rows - 1, t * 128 + quad * 32 + 31);
                 const int first = PRE ? __reduce_min_sync(0xffffffffu, there ? pos : 0x7fffffff) : item.pos0 + (item.row0 + t * 128 + quad * 32) / G - item.tok0;
@@ -553,12 +607,21 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                 if (ok && wk.nblk > 0) {
                     const int np = wk.nitems - wk.nrt + t, xp = np & 1;
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[xp], (uint32_t)(wk.uses[xp] + np / 2) & 1u));
+                    if (PRE && ok && wk.nrt == 2 && t == 0) {   // the other row tile's last products read operands too
+                        const int nl = wk.nitems - 1, xl = nl & 1;
+                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[xl], (uint32_t)(wk.uses[xl] + nl / 2) & 1u));
+                    }
                     if (!ok && lane == 0) fail(8);
                     tc::tc_fence_after();
                 }
                 if (ok) {
                     const float inv = lsum == 0.0f ? 0.0f : 1.0f / lsum;
                     const int rr0 = item.row0 + row;
+                    // PRE: a row's record is put together where the operands lay (nothing reads them any more) and leaves
+                    // by one bulk copy; 16-byte stores of 32 rows side by side took twice as long (4400 cycles)
+                    constexpr int64_t RS = PfStride<D>::value;
+                    static_assert(ROWS * RS * 4 <= C::OFF_RAW, "the records fit in the operands' space");
+                    float *rec = reinterpret_cast<float *>(smem) + row * RS;
                     const int64_t at = (item.q0 + rr0 / G) * p.ldo + (int64_t)(item.head * G + rr0 % G) * D;
 #pragma unroll 1
                     for (int c = 0; c < D / 32; c++) {
@@ -570,18 +633,12 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
 #pragma unroll
                             for (int i = 0; i < 32; i++) rr[i] = 0;
                         }
-                        if (PRE) {   // the record of the row, or its part of the CTA's slot
-                            if (there) {
-                                float *to = item.first ? a.pf.records + ((item.q0 + rr0 / G + (item.first == 2 ? p.n_tokens : 0)) * p.h +
-                                                                         item.head * G + rr0 % G) * PfStride<D>::value
-                                                       : a.pieces + ((int64_t)blockIdx.x * ROWS + row) * PfStride<D>::value;
-                                float4 *dst = reinterpret_cast<float4 *>(to + 32 * c);
+                        if (PRE) {
+                            float4 *dst = reinterpret_cast<float4 *>(rec + 32 * c);
 #pragma unroll
-                                for (int i = 0; i < 8; i++)
-                                    dst[i] = make_float4(__uint_as_float(rr[4 * i]), __uint_as_float(rr[4 * i + 1]),
-                                                         __uint_as_float(rr[4 * i + 2]), __uint_as_float(rr[4 * i + 3]));
-                                if (c == 0) *reinterpret_cast<float2 *>(to + D) = make_float2(ref, lsum);
-                            }
+                            for (int i = 0; i < 8; i++)
+                                dst[i] = make_float4(__uint_as_float(rr[4 * i]), __uint_as_float(rr[4 * i + 1]),
+                                                     __uint_as_float(rr[4 * i + 2]), __uint_as_float(rr[4 * i + 3]));
                         } else if (CUT && there && item.part >= 0) {
                             float *to = a.pieces + ((int64_t)item.part * cut_rows + row) * (D + 2);
                             float2 *dst = reinterpret_cast<float2 *>(to + 2 + 32 * c);
@@ -608,14 +665,27 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                             }
                         }
                     }
+                    if constexpr (PRE) {
+                        if (there) {
+                            const int tk = ad_token_of_row(a, rr0);
+                            float *to = item.first ? a.pf.records + ((item.q0 + tk + (item.first == 2 ? p.n_tokens : 0)) * p.h +
+                                                                     item.head * G + rr0 - tk * G) * RS
+                                                   : a.pieces + ((int64_t)blockIdx.x * ROWS + row) * RS;
+                            *reinterpret_cast<float4 *>(rec + D) = make_float4(ref, lsum, 0.0f, 0.0f);
+                            tc::fence_proxy_async_smem();
+                            bulk_store(to, rec, RS * 4);
+                        }
+                        bulk_store_read();   // the space is free for the next piece's operands
+                    }
                     tc::tc_fence_before();
                 }
             }
         }
+        if constexpr (PRE) bulk_store_done();
     } else if (warp < AP_MMA) {
         set_registers<C::REGS_OTHER>();
-        for (int64_t st = 0; PRE ? own0 + st < own1 : st < stripes; st += PRE ? wk.nblk : 1) {
-            const int64_t it = PRE ? own0 + st : item_of(st);
+        for (Stripe st = 0; PRE ? st < own : st < stripes; st += PRE ? wk.nblk : 1) {
+            const int64_t it = PRE ? st : item_of(st);
             if (!PRE && it >= total) continue;
             if (!begin(wk, it)) break;
             // ================= unpack: the keys of a block, then its values, 4 tiles a step.  The packed words of the next step are
@@ -767,8 +837,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         }
     } else {
         set_registers<C::REGS_OTHER>();
-        for (int64_t st = 0; PRE ? own0 + st < own1 : st < stripes; st += PRE ? wk.nblk : 1) {
-            const int64_t it = PRE ? own0 + st : item_of(st);
+        for (Stripe st = 0; PRE ? st < own : st < stripes; st += PRE ? wk.nblk : 1) {
+            const int64_t it = PRE ? st : item_of(st);
             if (!PRE && it >= total) continue;
             if (!begin(wk, it)) break;
             if (warp == AP_MMA) {

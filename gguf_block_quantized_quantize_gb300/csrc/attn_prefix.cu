@@ -17,7 +17,7 @@
 // (attn_prefill.cuh), the others to the kernel of few rows (attn_decode.cuh), each in
 // a mode that cuts all its tiles evenly over the CTAs, takes every row's position
 // from the plan, and leaves (m, l, O) in fp32: a record per query row for the first
-// piece of its unit, a slot per CTA for a piece that goes on from the CTA before.  The
+// piece of its unit, a slot per warp or CTA for a unit that goes on from the one before.  The
 // second kernel starts as the first one's CTAs end, without waiting for its results.
 // The join takes a warp per query row, which works out from the cut where its pieces
 // lie.
@@ -49,6 +49,8 @@ __device__ __forceinline__ int64_t last_up_to(const int32_t *a, int64_t n, int64
     }
     return lo;
 }
+// the arrays that are searched, in shared memory where they fit: a search of 9 steps takes 300 cycles there, 5000 in the L2
+constexpr int PF_HELD = 2048;
 struct PfGroup {
     int64_t s, e;    // its requests
     int32_t tiles;   // shared ones
@@ -61,6 +63,13 @@ __device__ __forceinline__ PfGroup pf_group(const PfPlanArgs &p, int64_t g) {
     o.tiles = o.e - o.s >= 2 ? (int32_t)(max(p.prefix_len[g], 0) / p.page * (p.page / KV_TILE)) : 0;
     return o;
 }
+// the group with which a request shares tiles, or -1
+__device__ __forceinline__ int pf_group_of(const PfPlanArgs &p, int64_t r) {
+    const int64_t g = last_up_to(p.group_start, p.NG + 1, r);
+    if (g < 0 || g >= p.NG) return -1;
+    const PfGroup in = pf_group(p, g);
+    return r >= in.s && r < in.e && in.tiles > 0 ? (int)g : -1;
+}
 // the queries of requests s .. e - 1 that the call's arrays hold
 __device__ __forceinline__ void pf_queries(const PfPlanArgs &p, int64_t s, int64_t e, PfEntry &o) {
     const int64_t a = p.q_start[s], b = min((int64_t)p.q_start[e], p.n_tokens);
@@ -71,9 +80,20 @@ __device__ __forceinline__ void pf_queries(const PfPlanArgs &p, int64_t s, int64
 // Three independent parts, over all CTAs: a thread per token, a thread per request, a warp per group.  Latency-bound: a
 // token's request is a binary search of q_start, a group's positions a loop of its requests by 32.
 constexpr int PF_THREADS = 256;
-__global__ void __launch_bounds__(PF_THREADS) prefix_plan_kernel(const PfPlanArgs p) {
+__global__ void __launch_bounds__(PF_THREADS) prefix_plan_kernel(const PfPlanArgs args) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ int32_t held[2][PF_HELD];
+    PfPlanArgs p = args;
+    if (p.R < PF_HELD) {
+        for (int i = threadIdx.x; i <= p.R; i += PF_THREADS) held[0][i] = p.q_start[i];
+        p.q_start = held[0];
+    }
+    if (p.NG > 0 && p.NG < PF_HELD) {
+        for (int i = threadIdx.x; i <= p.NG; i += PF_THREADS) held[1][i] = p.group_start[i];
+        p.group_start = held[1];
+    }
+    __syncthreads();
     const int64_t id = (int64_t)blockIdx.x * PF_THREADS + threadIdx.x;
     PfEntry *entries = reinterpret_cast<PfEntry *>(p.plan + PF_HEADER);
     if (id == 0) {
@@ -82,23 +102,23 @@ __global__ void __launch_bounds__(PF_THREADS) prefix_plan_kernel(const PfPlanArg
     }
     if (id < p.n_tokens) {
         const int64_t r = last_up_to(p.q_start, p.R + 1, id);
-        const bool in = r >= 0 && r < p.R;
-        reinterpret_cast<int2 *>(entries + p.R + p.NG)[id] =
-            make_int2(in ? (int)(p.kv_len[r] - ((int64_t)p.q_start[r + 1] - id)) : -1, in ? (int)r : -1);
+        int2 o = make_int2(-1, -1);
+        if (r >= 0 && r < p.R) {
+            o.x = (int)(p.kv_len[r] - ((int64_t)p.q_start[r + 1] - id));
+            o.y = pf_pack((int)r, pf_group_of(p, r));
+        }
+        reinterpret_cast<int2 *>(entries + p.R + p.NG)[id] = o;
     }
     if (id < p.R) {
         PfEntry o{};
         pf_queries(p, id, id + 1, o);
         o.pos_min = (int32_t)max(p.kv_len[id] - ((int64_t)p.q_start[id + 1] - p.q_start[id]), (int64_t)INT32_MIN / 2);
         o.pos_max = o.pos_min + o.q - 1;
-        const int64_t g = last_up_to(p.group_start, p.NG + 1, id);
+        const int g = pf_group_of(p, id);
         o.group = -1;
-        if (g >= 0 && g < p.NG) {
-            const PfGroup in = pf_group(p, g);
-            if (id >= in.s && id < in.e && in.tiles > 0) {
-                o.tile0 = in.tiles;
-                o.group = (int32_t)(p.R + g);
-            }
+        if (g >= 0) {
+            o.tile0 = pf_group(p, g).tiles;
+            o.group = (int32_t)(p.R + g);
         }
         o.tile1 = max(o.tile0, o.q > 0 && o.pos_max >= 0 ? o.pos_max / KV_TILE + 1 : 0);
         o.row = (int32_t)id;
@@ -158,92 +178,98 @@ cudaError_t launch_prefix_plan(const int32_t *q_start, const int32_t *kv_len, in
 
 // a query row's pieces of one entry: the record, then n - 1 slots
 struct PfPieces {
-    const float *o, *ml, *slot_o, *slot_ml;
+    const float *first, *slot;
     int64_t step;
     int n;
-    __device__ __forceinline__ float2 stat(int i) const { return *reinterpret_cast<const float2 *>(i == 0 ? ml : slot_ml + (i - 1) * step); }
-    __device__ __forceinline__ const float *out(int i) const { return i == 0 ? o : slot_o + (i - 1) * step; }
+    __device__ __forceinline__ const float *at(int i) const { return i == 0 ? first : slot + i * step; }
 };
 template <int D>
-__device__ __forceinline__ PfPieces pf_pieces(const AdShape &a, int e, int64_t t, int head, int few, int rg) {
+__device__ __forceinline__ PfPieces pf_pieces(const AdShape &a, const AdReq &q, bool group, int64_t base, const int64_t (&shares)[3],
+                                              int64_t t, int head, int few, int rg) {
     constexpr int64_t RS = PfStride<D>::value;
     constexpr int ROWS = D == 256 ? 128 : 256, BTILES = D == 256 ? 4 : 8;   // the prefill kernel's (ApCfg)
     PfPieces x{};
-    const AdReq q = pf_request(a, e);
     if (q.nt == 0 || t < q.rows0 || t >= (int64_t)q.rows0 + q.q) return x;
     const int kh = head / a.G, row = (int)(t - q.rows0) * a.G + head - kh * a.G;
     const bool tc = (int64_t)q.q * a.G > few;
-    const int rows = tc ? ROWS : rg, n = tc ? (q.nt + BTILES - 1) / BTILES : q.nt;
-    const int64_t share = a.pf.share[tc], from = a.pf.base[e] + ((int64_t)(row / rows) * a.hk + kh) * n;
-    const int64_t c0 = ad_div(from, share), c1 = ad_div(from + n - 1, share);
-    x.n = (int)(c1 - c0) + 1;
-    x.o = a.pf.records + ((t + (e >= a.p.R ? a.p.n_tokens : 0)) * a.p.h + head) * RS;
-    x.ml = x.o + D;
-    const int in = row % rows;
-    if (tc) {
-        x.step = ROWS * RS;
-        x.slot_o = a.pieces + (c0 + 1) * x.step + in * RS;
-        x.slot_ml = x.slot_o + D;
-    } else {
-        x.step = (int64_t)rg * (D + 2);
-        x.slot_o = a.part + (c0 + 1) * x.step + in * D;
-        x.slot_ml = a.part + (c0 + 1) * x.step + rg * D + 2 * in;
-    }
+    const int rows = tc ? ROWS : rg, n = tc ? (q.nt + BTILES - 1) / BTILES : q.nt, block = row / rows;
+    const int64_t from = base + ((int64_t)block * a.hk + kh) * n;
+    // the CTA, or the warp of a CTA, that a tile or block of the sequence went to
+    auto taker = [&](int64_t i) {
+        const int64_t cta = ad_div(i, shares[tc]);
+        return tc ? cta : cta * pf_warps(shares[0], shares[2]) + ad_div(i - cta * shares[0], shares[2]);
+    };
+    const int64_t c0 = taker(from);
+    x.n = (int)(taker(from + n - 1) - c0) + 1;
+    x.first = a.pf.records + ((t + (group ? a.p.n_tokens : 0)) * a.p.h + head) * RS;
+    x.step = rows * RS;
+    x.slot = (tc ? a.pieces : a.part) + c0 * x.step + (row - block * rows) * RS;
     return x;
 }
 
-// Bound: the pieces' bytes, from the L2 mostly.  A warp per query row; its lanes take the statistics of 32 pieces at a time,
-// so that the outputs' loads wait for nothing.
+// Bound: the pieces' bytes, from the L2 mostly, and for few pieces the chain token, entry, pieces.  A warp per query row
+// takes AT_ONCE pieces at a time, so that their loads are under way together.
 template <int D, int QT>
 __global__ void __launch_bounds__(PF_THREADS) prefix_join_kernel(const AdShape a, const int few, const int rg) {
+    constexpr int AT_ONCE = 8, W = D == 64 ? 2 : 4, PL = D / 32 / W;   // values per load, loads per lane
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Attn &p = a.p;
+    const int64_t w = ((int64_t)blockIdx.x * PF_THREADS + threadIdx.x) >> 5, t = (uint64_t)w >> 31 ? w / p.h : (int64_t)((uint32_t)w / (uint32_t)p.h);
+    const int head = (int)(w - t * p.h), lane = threadIdx.x & 31;
+    const int2 at_rg = pf_unpack(t < p.n_tokens ? pf_token(a.pf, t).y : -1);
+    const int64_t shares[3] = {a.pf.share[0], a.pf.share[1], a.pf.share[2]};
     if (!pf_plan_fits(a)) {
-        if (blockIdx.x == 0 && threadIdx.x == 0 && p.status != nullptr) atomicAdd(p.status, 1);
+        if (w == 0 && lane == 0 && p.status != nullptr) atomicAdd(p.status, 1);
         return;
     }
-    const int64_t w = ((int64_t)blockIdx.x * PF_THREADS + threadIdx.x) >> 5, t = w / p.h;
-    const int head = (int)(w - t * p.h), lane = threadIdx.x & 31;
-    if (t >= p.n_tokens) return;
-    const int r = pf_token(a.pf, t).y;
+    const int r = at_rg.x, ge = (int)p.R + at_rg.y;
     if (r < 0 || r >= p.R) return;
-    const int g = pf_entries(a.pf)[r].group;
-    const PfPieces x[2] = {pf_pieces<D>(a, r, t, head, few, rg),
-                           g >= p.R && g < a.pf.n_entries ? pf_pieces<D>(a, g, t, head, few, rg) : PfPieces{}};
-    float mx = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < 2; k++)
-        for (int i = lane; i < x[k].n; i += 32) mx = fmaxf(mx, x[k].stat(i).x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float base = mx == -INFINITY ? 0.0f : mx;
-    constexpr int W = D == 64 ? 2 : 4, PL = D / 32 / W;   // values per load, loads per lane
-    float l = 0.0f, v[PL * W];
+    const bool grouped = ge >= p.R && ge < a.pf.n_entries;
+    const int e1 = grouped ? ge : r;
+    const int64_t base0 = a.pf.base[r], base1 = a.pf.base[e1];
+    const AdReq q0 = pf_request(a, r), q1 = pf_request(a, e1);
+    PfPieces x[2];
+    x[0] = pf_pieces<D>(a, q0, false, base0, shares, t, head, few, rg);
+    x[1] = PfPieces{};
+    if (grouped) x[1] = pf_pieces<D>(a, q1, true, base1, shares, t, head, few, rg);
+    const int n = x[0].n + x[1].n;
+    float mx = -INFINITY, l = 0.0f, v[PL * W];
 #pragma unroll
     for (int i = 0; i < PL * W; i++) v[i] = 0.0f;
+    for (int i0 = 0; i0 < n; i0 += AT_ONCE) {
+        float2 ml[AT_ONCE];
+        float u[AT_ONCE][PL * W];
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
-#pragma unroll 4
-        for (int i = 0; i < x[k].n; i++) {
-            const float2 ml = x[k].stat(i);
-            const float *src = x[k].out(i) + W * lane;
-            const float f = ex2(ml.x - base);
-            l = fmaf(f, ml.y, l);
+        for (int i = 0; i < AT_ONCE; i++) {
+            const int k = i0 + i;
+            ml[i] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
-            for (int c = 0; c < PL; c++) {
-                if constexpr (W == 4) {
-                    const float4 u = *reinterpret_cast<const float4 *>(src + 128 * c);
-                    v[4 * c] = fmaf(f, u.x, v[4 * c]);
-                    v[4 * c + 1] = fmaf(f, u.y, v[4 * c + 1]);
-                    v[4 * c + 2] = fmaf(f, u.z, v[4 * c + 2]);
-                    v[4 * c + 3] = fmaf(f, u.w, v[4 * c + 3]);
-                } else {
-                    const float2 u = *reinterpret_cast<const float2 *>(src);
-                    v[0] = fmaf(f, u.x, v[0]);
-                    v[1] = fmaf(f, u.y, v[1]);
+            for (int c = 0; c < PL * W; c++) u[i][c] = 0.0f;
+            if (k < n) {
+                const float *src = k < x[0].n ? x[0].at(k) : x[1].at(k - x[0].n);
+                ml[i] = *reinterpret_cast<const float2 *>(src + D);
+#pragma unroll
+                for (int c = 0; c < PL; c++) {
+                    if constexpr (W == 4) *reinterpret_cast<float4 *>(&u[i][4 * c]) = *reinterpret_cast<const float4 *>(src + 4 * lane + 128 * c);
+                    else *reinterpret_cast<float2 *>(&u[i][0]) = *reinterpret_cast<const float2 *>(src + 2 * lane);
                 }
             }
+        }
+        float mn = mx;
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; i++) mn = fmaxf(mn, ml[i].x);
+        const float base = mn == -INFINITY ? 0.0f : mn, f0 = ex2(mx - base);
+        mx = mn;
+        l *= f0;
+#pragma unroll
+        for (int c = 0; c < PL * W; c++) v[c] *= f0;
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; i++) {
+            const float f = ex2(ml[i].x - base);
+            l = fmaf(f, ml[i].y, l);
+#pragma unroll
+            for (int c = 0; c < PL * W; c++) v[c] = fmaf(f, u[i][c], v[c]);
         }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -289,7 +315,7 @@ static PfRun prefix_run(const Attn &p, int64_t NG, int64_t d) {
     x.share = up((size_t)(p.R + NG) * 8);
     x.records = x.share + 256;
     x.part = up(x.records + 2 * (size_t)p.n_tokens * p.h * rs);
-    x.pieces = up(x.part + (size_t)x.ctas * x.rg * (d + 2) * 4);
+    x.pieces = up(x.part + (size_t)x.ctas * ad_warps((int)d, p.qt == GGUF_F32, x.rg / 8) * x.rg * rs);
     x.bytes = x.tc ? x.pieces + (size_t)x.ctas * (d == 256 ? 128 : 256) * rs : x.pieces;
     return x;
 }

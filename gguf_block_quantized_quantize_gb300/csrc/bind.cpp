@@ -29,7 +29,7 @@ typedef gguf_status (*mrope_fn)(const gguf_qk_rope_args *, const gguf_rope_axes 
 typedef gguf_status (*pplan_fn)(const int32_t *, const int32_t *, int64_t, const int32_t *, const int32_t *, int64_t, int64_t,
                                 int64_t, void *, size_t, gguf_stream_t);
 typedef size_t (*pattn_ws_fn)(const gguf_attn_args *, int64_t);
-typedef gguf_status (*pattn_fn)(const gguf_attn_args *, const void *, int64_t, void *, size_t, gguf_stream_t);
+typedef gguf_status (*pattn_fn)(const gguf_attn_args *, const void *, size_t, int64_t, void *, size_t, gguf_stream_t);
 typedef gguf_status (*norm_fn)(const gguf_block_norm_args *, gguf_stream_t);
 
 struct {
@@ -44,7 +44,6 @@ struct {
     pplan_fn pplan;
     pattn_ws_fn pattn_ws;
     pattn_fn pattn;
-    page_fn pplan_bytes;
 } api;
 
 struct Bad {};   // a Python exception is set
@@ -446,30 +445,24 @@ PyObject *prefix_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
         x.width = t.width;
         const int64_t groups = integer(a[4]);
         if (PyLong_Check(a[12])) return PyLong_FromSize_t(api.pattn_ws(&x, groups));
-        const at::Tensor &plan = tensor(a[3], what, "plan");
-        const int64_t need = api.pplan_bytes(x.n_requests, groups, x.n_tokens);
-        if (need >= 0 && (!plan.is_contiguous() || plan.numel() * plan.element_size() < need)) {
-            PyErr_Format(PyExc_ValueError, "%s: plan must be contiguous and of at least %lld bytes (this many requests, groups and tokens)",
-                         what, (long long)need);
-            throw Bad();
-        }
+        const Bytes plan = bytes_or_none(a[3], what, "plan");
         const Bytes w = bytes_or_none(a[12], what, "ws");
-        return PyLong_FromLong(api.pattn(&x, plan.data_ptr(), groups, w.p, w.n, stream(a[14])));
+        return PyLong_FromLong(api.pattn(&x, plan.p, plan.n, groups, w.p, w.n, stream(a[14])));
     });
 }
 
 // the addresses of gguf_kv_plan, gguf_qk_norm_rope, gguf_kv_get_rows, gguf_paged_attention_ws_size, gguf_paged_attention,
-// gguf_kv_page_bytes, gguf_qk_norm_mrope, gguf_block_norm, gguf_prefix_plan, gguf_prefix_attention_ws_size,
-// gguf_prefix_attention and gguf_prefix_plan_bytes
+// gguf_kv_page_bytes, gguf_qk_norm_mrope, gguf_block_norm, gguf_prefix_plan, gguf_prefix_attention_ws_size and
+// gguf_prefix_attention
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
-        count(n, 12, "bind");
-        void *p[12];
-        for (int i = 0; i < 12; i++) p[i] = reinterpret_cast<void *>(static_cast<intptr_t>(integer(a[i])));
+        count(n, 11, "bind");
+        void *p[11];
+        for (int i = 0; i < 11; i++) p[i] = reinterpret_cast<void *>(static_cast<intptr_t>(integer(a[i])));
         api = {reinterpret_cast<plan_fn>(p[0]), reinterpret_cast<rope_fn>(p[1]), reinterpret_cast<rows_fn>(p[2]),
                reinterpret_cast<attn_ws_fn>(p[3]), reinterpret_cast<attn_fn>(p[4]), reinterpret_cast<page_fn>(p[5]),
                reinterpret_cast<mrope_fn>(p[6]), reinterpret_cast<norm_fn>(p[7]), reinterpret_cast<pplan_fn>(p[8]),
-               reinterpret_cast<pattn_ws_fn>(p[9]), reinterpret_cast<pattn_fn>(p[10]), reinterpret_cast<page_fn>(p[11])};
+               reinterpret_cast<pattn_ws_fn>(p[9]), reinterpret_cast<pattn_fn>(p[10])};
         Py_RETURN_NONE;
     });
 }

@@ -266,14 +266,17 @@ size_t gguf_prefix_attention_ws_size(const gguf_attn_args *a, int64_t n_groups) 
     return prefix_attn_ws_size(attn_of(a), n_groups, a->head_dim);
 }
 
-gguf_status gguf_prefix_attention(const gguf_attn_args *a, const void *plan, int64_t n_groups, void *ws, size_t ws_bytes,
-                                  gguf_stream_t stream) {
+gguf_status gguf_prefix_attention(const gguf_attn_args *a, const void *plan, size_t plan_bytes, int64_t n_groups, void *ws,
+                                  size_t ws_bytes, gguf_stream_t stream) {
     gguf_status st = check_prefix_sizes(a, n_groups);
     if (st == GGUF_OK) st = check_attn_rows(a, "prefix_attention");
     if (st != GGUF_OK) return st;
     if (a->n_tokens == 0 || a->n_requests == 0) return GGUF_OK;
     if (!plan) return report(GGUF_ERR_INVALID_ARG, "prefix_attention: null pointer");
     if (!at(plan, 16)) return report(GGUF_ERR_ALIGNMENT, "prefix_attention: the plan must be 16-byte aligned");
+    const int64_t planned = prefix_plan_bytes(a->n_requests, n_groups, a->n_tokens);
+    if (plan_bytes < (size_t)planned)
+        return refuse(GGUF_ERR_WORKSPACE, "prefix_attention: plan of %zu bytes < required %lld", plan_bytes, (long long)planned);
     const Attn p = attn_of(a);
     st = check_attn_arrays(a, ws, ws_bytes, prefix_attn_ws_size(p, n_groups, a->head_dim), "prefix_attention");
     if (st != GGUF_OK) return st;

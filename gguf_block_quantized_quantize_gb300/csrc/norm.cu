@@ -20,13 +20,22 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "tc.cuh"
 
 namespace gg {
+
+int *tg_error_word();   // the library's device error word (mmq.cu)
 
 constexpr int BN_THREADS = 512;
 
 __device__ __forceinline__ float bn_from16(int t, uint32_t h) { return t == GGUF_BF16 ? bf2f((uint16_t)h) : h2f((uint16_t)h); }
-__device__ __forceinline__ uint32_t bn_to16(int t, float f) { return t == GGUF_BF16 ? f2bf_rn(f) : f2h_rn(f); }
+// two values rounded to 16 bits, the first in the low half
+__device__ __forceinline__ uint32_t bn_pair16(int t, float a, float b) {
+    uint32_t w;
+    if (t == GGUF_BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    return w;
+}
 
 // n values of a chunk (8, or fewer in the last one) from element `at`, which is 16-byte aligned
 __device__ __forceinline__ void bn_ld8(const void *x, int t, int64_t at, int n, float (&v)[8]) {
@@ -59,7 +68,7 @@ __device__ __forceinline__ void bn_st8(void *x, int t, int64_t at, int n, const 
         } else {
             uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; i++) w[i] = bn_to16(t, v[2 * i]) | bn_to16(t, v[2 * i + 1]) << 16;
+            for (int i = 0; i < 4; i++) w[i] = bn_pair16(t, v[2 * i], v[2 * i + 1]);
             *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(x) + at) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     } else {
@@ -104,14 +113,22 @@ struct RowPart {
     }
 };
 
-__device__ __forceinline__ float row_sum(float v, float *part, int warps) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+// (every warp sums up the warps' parts in the same tree: the same bits everywhere)
+__device__ __forceinline__ float row_sum(float v, float *part, int warps) {
+    v = warp_sum(v);
     if (warps == 1) return v;   // a row per warp
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    constexpr int MOST = BN_THREADS / 32;   // 16: both halves of a warp sum them up
+    const int lane = threadIdx.x & 31, w = lane % MOST;
+    if (lane == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.0f;
-    for (int w = 0; w < warps; w++) v += part[w];
+    v = w < warps ? part[w] : 0.0f;
+#pragma unroll
+    for (int o = MOST / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
@@ -159,45 +176,40 @@ __device__ __forceinline__ void normed(const RowPart<C, VEC> &r, int kind, const
     }
 }
 
-// roundf(v / d) of N values (ties away from zero; 0 with d == 0).  v * (1 / d) is within 2^-21 of the quotient relatively
-// and the quotient below 128, so within 2^-14, which decides the rounding unless it lies that near to a half, or d is so
-// small that 1 / d or the products might not be ordinary numbers: then the division itself does.  Adding 1.5 * 2^23 leaves
-// the rounded quotient in the low bits.
+// roundf(v / d) of N values (ties away from zero; 0 with d == 0), as the low bytes of q.  v * (1 / d) is within 2^-21 of
+// the quotient relatively and the quotient below 128, so within 2^-14, which decides the rounding unless it lies that near to
+// a half, or d is so small that 1 / d or the products might not be ordinary numbers: then the division itself does.
+// Adding 1.5 * 2^23 leaves the rounded quotient in the low bits.
 template <int N>
-__device__ __forceinline__ void q8_codes(const float (&v)[N], float d, int (&q)[N]) {
+__device__ __forceinline__ void q8_codes(const float (&v)[N], float d, uint32_t (&q)[N]) {
     const float inv = __frcp_rn(d);
     bool near = !(d > 0x1p-100f);
 #pragma unroll
     for (int i = 0; i < N; i++) {
-        const float t = __fmul_rn(v[i], inv), r = __fadd_rn(t, kI2fBias);
-        near |= !(fabsf(__fsub_rn(t, __fsub_rn(r, kI2fBias))) < 0.5f - 0x1p-13f);
-        q[i] = __float_as_int(r) - 0x4B400000;
+        const float r = __fmaf_rn(v[i], inv, kI2fBias), off = __fmaf_rn(v[i], inv, -__fsub_rn(r, kI2fBias));
+        near |= !(fabsf(off) < 0.5f - 0x1p-13f);
+        q[i] = __float_as_uint(r);
     }
     if (near) {
 #pragma unroll
-        for (int i = 0; i < N; i++) q[i] = d != 0.0f ? min(max((int)roundf(__fdiv_rn(v[i], d)), -127), 127) : 0;
+        for (int i = 0; i < N; i++) q[i] = d != 0.0f ? (uint32_t)min(max((int)roundf(__fdiv_rn(v[i], d)), -127), 127) : 0u;
     }
 }
 
-template <int XT, int HT, int C, bool VEC>
-__global__ void __launch_bounds__(BN_THREADS) block_norm_kernel(const BlockNorm p) {
-    __shared__ float part[4][BN_THREADS / 32];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    if (t >= p.n_tokens) return;   // whole warps, and rows of several warps have no other in their CTA
-    const RowPart<C, VEC> r{(int)threadIdx.x, (int)blockDim.x, (int)p.k};
+// a row, from its x, h and gate to its outputs; release(): they are not read any more
+template <int XT, int HT, int C, bool VEC, bool EARLY, class F>
+__device__ __forceinline__ void norm_row(const BlockNorm &p, const RowPart<C, VEC> &r, int64_t t, const void *x, const void *h,
+                                         const void *gate, float (*part)[BN_THREADS / 32], F release) {
     const int warps = blockDim.x >> 5;
     const float inv_k = 1.0f / (float)(int)p.k;
     float v[C][8], o[C][8];
-    constexpr bool EARLY = C < 8;   // h is asked for before the norm of x: what registers there are for it
-    if (EARLY && p.h != nullptr) r.load(p.h, HT, t * p.ldh, o);
+    if (EARLY && p.h != nullptr) r.load(h, HT, 0, o);
     if (p.x != nullptr) {
-        r.load(p.x, XT, t * p.ldx, v);
+        r.load(x, XT, 0, v);
         normed(r, p.post, p.post_w, p.post_b, p.post_eps, inv_k, v, part, warps);
         if (p.gate != nullptr) {
             float g[C][8];
-            r.load(p.gate, p.gt, t * p.ldg, g);
+            r.load(gate, p.gt, 0, g);
 #pragma unroll
             for (int c = 0; c < C; c++)
 #pragma unroll
@@ -219,12 +231,13 @@ __global__ void __launch_bounds__(BN_THREADS) block_norm_kernel(const BlockNorm 
             for (int i = 0; i < 8; i++) v[c][i] = 0.0f;
     }
     if (p.h != nullptr) {
-        if (!EARLY) r.load(p.h, HT, t * p.ldh, o);
+        if (!EARLY) r.load(h, HT, 0, o);
 #pragma unroll
         for (int c = 0; c < C; c++)
 #pragma unroll
             for (int i = 0; i < 8; i++) v[c][i] = fmaf(o[c][i], p.resid, v[c][i]);
     }
+    release();
     if (p.h_out != nullptr) r.store(p.h_out, HT, t * p.ldho, v);
     if (p.z == nullptr && p.zq == nullptr) return;
     normed(r, p.pre, p.pre_w, p.pre_b, p.pre_eps, inv_k, v, part + 2, warps);
@@ -241,17 +254,18 @@ __global__ void __launch_bounds__(BN_THREADS) block_norm_kernel(const BlockNorm 
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             const float d = __fdiv_rn(amax, 127.0f);
-            int q[8], sum = 0;
+            uint32_t q[8], word[2];
             q8_codes<8>(v[c], d, q);
 #pragma unroll
-            for (int i = 0; i < 8; i++) sum += q[i];
+            for (int i = 0; i < 2; i++)
+                word[i] = __byte_perm(__byte_perm(q[4 * i], q[4 * i + 1], 0x0040), __byte_perm(q[4 * i + 2], q[4 * i + 3], 0x0040), 0x5410);
+            int sum = dp4a_ss((int)word[1], 0x01010101, dp4a_ss((int)word[0], 0x01010101, 0));
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             if (at < r.k) {   // (k is a multiple of 32: whole blocks)
                 uint32_t *to = reinterpret_cast<uint32_t *>(row + at / QK8 * Q8_1_BYTES);
-#pragma unroll
-                for (int i = 0; i < 2; i++)
-                    to[1 + 2 * j + i] = (q[4 * i] & 0xff) | (q[4 * i + 1] & 0xff) << 8 | (q[4 * i + 2] & 0xff) << 16 | (uint32_t)q[4 * i + 3] << 24;
+                to[1 + 2 * j] = word[0];
+                to[2 + 2 * j] = word[1];
                 if (j == 0) to[0] = f2h_rn(d) | (uint32_t)f2h_rn(__fmul_rn(d, (float)sum)) << 16;
             }
         } else {
@@ -262,15 +276,85 @@ __global__ void __launch_bounds__(BN_THREADS) block_norm_kernel(const BlockNorm 
 #pragma unroll
                 for (int s = 1; s < 32; s <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
                 const float d = __fdiv_rn(amax, 127.0f), one[1] = {v[c][i]};
-                int q[1];
+                uint32_t q[1];
                 q8_codes<1>(one, d, q);
-                const int sum = __reduce_add_sync(0xffffffffu, q[0]);
+                const int sum = __reduce_add_sync(0xffffffffu, (int)(int8_t)q[0]);
                 if (at >= r.k) continue;
                 uint8_t *to = row + at / QK8 * Q8_1_BYTES;
                 to[4 + at % QK8] = (uint8_t)q[0];
                 if (at % QK8 == 0) *reinterpret_cast<uint32_t *>(to) = f2h_rn(d) | (uint32_t)f2h_rn(__fmul_rn(d, (float)sum)) << 16;
             }
         }
+    }
+}
+
+__device__ __forceinline__ const uint8_t *row_at(const void *x, int t, int64_t i) { return reinterpret_cast<const uint8_t *>(x) + i * (t == GGUF_F32 ? 4 : 2); }
+
+template <int XT, int HT, int C, bool VEC>
+__global__ void __launch_bounds__(BN_THREADS) block_norm_kernel(const BlockNorm p) {
+    __shared__ float part[4][BN_THREADS / 32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    if (t >= p.n_tokens) return;   // whole warps, and rows of several warps have no other in their CTA
+    const RowPart<C, VEC> r{(int)threadIdx.x, (int)blockDim.x, (int)p.k};
+    // h is asked for before the norm of x, where there are registers for it
+    norm_row<XT, HT, C, VEC, (C < 8)>(p, r, t, row_at(p.x, XT, t * p.ldx), row_at(p.h, HT, t * p.ldh), row_at(p.gate, p.gt, t * p.ldg),
+                                      part, [] {});
+}
+
+// Many rows: a CTA takes every gridDim-th row, and bulk copies bring the rows ahead into a ring in shared memory while it
+// computes; without them the loads, sums and stores of the 2 to 4 rows that an SM holds wait for one another.
+// Rows of x, h and gate (that of one row for all tokens apart) start and end on 16 bytes.
+constexpr int BN_STAGES = 4;
+struct BnRing {
+    int stages;
+    uint32_t bytes_x, bytes_h, bytes_g;   // of a row; 0: not there
+    int *err;
+};
+template <int XT, int HT, int C>
+__global__ void __launch_bounds__(BN_THREADS, C <= 2 ? 2 : 1) block_norm_ring_kernel(const BlockNorm p, const BnRing ring) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float part[4][BN_THREADS / 32];
+    __shared__ uint64_t full[BN_STAGES];
+    const int tid = threadIdx.x;
+    if (tid == 0)
+        for (int i = 0; i < ring.stages; i++) tc::mbar_init(&full[i], 1);
+    tc::fence_barrier_init();
+    __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const RowPart<C, true> r{tid, (int)blockDim.x, (int)p.k};
+    const uint32_t bytes = ring.bytes_x + ring.bytes_h + ring.bytes_g;
+    auto ask = [&](int64_t t, int stage) {   // thread 0
+        if (t >= p.n_tokens) return;
+        uint8_t *to = smem + (size_t)stage * bytes;
+        tc::mbar_arrive_expect_tx(&full[stage], bytes);
+        if (ring.bytes_x) tc::bulk_load(to, row_at(p.x, XT, t * p.ldx), ring.bytes_x, &full[stage]);
+        if (ring.bytes_h) tc::bulk_load(to + ring.bytes_x, row_at(p.h, HT, t * p.ldh), ring.bytes_h, &full[stage]);
+        if (ring.bytes_g) tc::bulk_load(to + ring.bytes_x + ring.bytes_h, row_at(p.gate, p.gt, t * p.ldg), ring.bytes_g, &full[stage]);
+    };
+    if (tid == 0)
+        for (int i = 0; i < ring.stages; i++) ask(blockIdx.x + (int64_t)i * gridDim.x, i);
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int64_t t = blockIdx.x; t < p.n_tokens; t += gridDim.x) {
+        const bool ok = tc::mbar_wait(&full[stage], phase);
+        if (!__syncthreads_and(ok)) {   // given up: what is under way lands before the CTA exits
+            if (tid == 0) {
+                if (ring.err != nullptr) atomicOr(ring.err, 1);
+                for (int i = 0; i < ring.stages; i++)
+                    if (t + (int64_t)i * gridDim.x < p.n_tokens) tc::mbar_wait(&full[(stage + i) % ring.stages], stage + i < ring.stages ? phase : phase ^ 1);
+            }
+            return;
+        }
+        const uint8_t *x = smem + (size_t)stage * bytes, *h = x + ring.bytes_x;
+        const void *gate = ring.bytes_g ? h + ring.bytes_h : row_at(p.gate, p.gt, 0);
+        norm_row<XT, HT, C, true, false>(p, r, t, x, h, gate, part, [&] {
+            __syncthreads();
+            if (tid == 0) ask(t + (int64_t)ring.stages * gridDim.x, stage);
+        });
+        if (++stage == ring.stages) { stage = 0; phase ^= 1; }
     }
 }
 
@@ -285,6 +369,17 @@ static const void *norm_kernel(int xt, int ht, int c) {
     if (xt == GGUF_BF16)
         return ht == GGUF_F32 ? norm_kernel<GGUF_BF16, GGUF_F32, VEC>(c) : norm_kernel<GGUF_BF16, GGUF_BF16, VEC>(c);
     return ht == GGUF_F32 ? norm_kernel<GGUF_F16, GGUF_F32, VEC>(c) : norm_kernel<GGUF_F16, GGUF_F16, VEC>(c);
+}
+
+template <int XT, int HT>
+static const void *ring_kernel(int c) {
+    return c == 1 ? (const void *)block_norm_ring_kernel<XT, HT, 1> : c == 2 ? (const void *)block_norm_ring_kernel<XT, HT, 2>
+                                                                             : (const void *)block_norm_ring_kernel<XT, HT, 4>;
+}
+static const void *ring_kernel(int xt, int ht, int c) {
+    if (xt == GGUF_F32) return ring_kernel<GGUF_F32, GGUF_F32>(c);
+    if (xt == GGUF_BF16) return ht == GGUF_F32 ? ring_kernel<GGUF_BF16, GGUF_F32>(c) : ring_kernel<GGUF_BF16, GGUF_BF16>(c);
+    return ht == GGUF_F32 ? ring_kernel<GGUF_F16, GGUF_F32>(c) : ring_kernel<GGUF_F16, GGUF_F16>(c);
 }
 
 cudaError_t launch_block_norm(const BlockNorm &p, int xt, int ht, bool vec, cudaStream_t s) {
@@ -303,6 +398,29 @@ cudaError_t launch_block_norm(const BlockNorm &p, int xt, int ht, bool vec, cuda
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     BlockNorm a = p;
+    auto size = [](int t) { return t == GGUF_F32 ? 4u : 2u; };
+    BnRing ring{0, p.x ? (uint32_t)p.k * size(xt) : 0, p.h ? (uint32_t)p.k * size(ht) : 0,
+                p.gate && p.ldg ? (uint32_t)p.k * size(p.gt) : 0, nullptr};
+    const uint32_t bytes = ring.bytes_x + ring.bytes_h + ring.bytes_g;
+    const int64_t sms = device_info().sm_count;
+    if (vec && p.k > 256 && p.k <= 16384 && p.n_tokens > 8 * sms && ring.bytes_x % 16 == 0 && ring.bytes_h % 16 == 0 &&
+        ring.bytes_g % 16 == 0 && 2 * bytes <= 200 * 1024) {
+        // two chunks a thread where that leaves four warps: what a row costs beside its values is shared by more of them
+        while (c < (p.k >= 2048 ? 2 : 1)) c *= 2;
+        const int tpr = (int)(((eighths + c - 1) / c + 31) / 32 * 32);
+        const int ctas = c <= 2 ? std::max(2, std::min(1024 / tpr, 8)) : 1;   // what registers leave room for
+        ring.stages = std::max(2, std::min<int>(BN_STAGES, (int)(200 * 1024 / ctas / bytes)));
+        ring.err = tg_error_word();
+        const void *kern = ring_kernel(xt, ht, c);
+        cudaError_t err = cudaSuccess;
+        const int per_sm = kernel_occupancy(kern, tpr, (size_t)ring.stages * bytes, &err);
+        if (per_sm == 0) return err;
+        cfg.blockDim = dim3(tpr);
+        cfg.gridDim = dim3((unsigned)std::min<int64_t>(p.n_tokens, per_sm * sms));
+        cfg.dynamicSmemBytes = (size_t)ring.stages * bytes;
+        void *args[2] = {&a, &ring};
+        return cudaLaunchKernelExC(&cfg, kern, args);
+    }
     void *args[1] = {&a};
     return cudaLaunchKernelExC(&cfg, vec ? norm_kernel<true>(xt, ht, c) : norm_kernel<false>(xt, ht, c), args);
 }

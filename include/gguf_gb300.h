@@ -788,12 +788,13 @@ gguf_status gguf_prefix_plan(const int32_t *q_start, const int32_t *kv_len, int6
  *   args : as gguf_paged_attention; q_start and kv_len are not looked at (they are in the
  *          plan).  max_q_len only chooses kernels: all queries are computed.
  *   plan : made by gguf_prefix_plan, on this stream or complete, with these n_requests,
- *          n_groups, n_tokens and page_size.  A plan of other sizes is not used: nothing
- *          is written, and dev_status counts 1.
+ *          n_groups, n_tokens and page_size: plan_bytes, at least gguf_prefix_plan_bytes of
+ *          them.  A plan of other sizes is not used: nothing is written, and dev_status
+ *          counts 1.
  *   dev_status : + pages outside the cache or past the table, each once per request whose
  *          own tokens, or once per group whose shared ones, would be seen in it.
  *   ws   : gguf_prefix_attention_ws_size(args, n_groups) bytes, 16-byte aligned: about
- *          8 (head_dim + 4) bytes per token and head, and up to 21 MB (40 MB with heads of 256).
+ *          8 (head_dim + 4) bytes per token and head, and up to 32 MB.
  * n_tokens x n_heads <= 2^30 (GGUF_ERR_SHAPE above).  Precision, windows, blocks that are not
  * finite (which may reach the queries of their group) and timeouts are as described at
  * gguf_paged_attention; the bits of a request's outputs depend on the batch.  Made for few
@@ -802,8 +803,8 @@ gguf_status gguf_prefix_plan(const int32_t *q_start, const int32_t *kv_len, int6
  * Same bits on every run.
  */
 size_t gguf_prefix_attention_ws_size(const gguf_attn_args *args, int64_t n_groups);
-gguf_status gguf_prefix_attention(const gguf_attn_args *args, const void *plan, int64_t n_groups, void *ws, size_t ws_bytes,
-                                  gguf_stream_t stream);
+gguf_status gguf_prefix_attention(const gguf_attn_args *args, const void *plan, size_t plan_bytes, int64_t n_groups, void *ws,
+                                  size_t ws_bytes, gguf_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -267,3 +267,32 @@ def test_binding_refuses_what_does_not_fit():
     with pytest.raises(g.GgufError, match="block_norm"):
         f(x, h, pre_kind=9)
     assert np.isfinite(f(x, h)[1].float().cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("t, k, typ, resid, post, pre, gate, pad, lead", [
+    (1300, 288, "bf16", "bf16", "rms", "rms", "none", 0, 0), (1501, 512, "f16", "f32", "layer", "rms", "rows", 8, 0),
+    (1219, 2048, "bf16", "f32", "rms", "layer", "row", 0, 0), (2500, 1000, "f32", "f32", "rms", "rms", "rows32", 24, 4),
+    (1300, 4096, "f16", "f16", "layer", "layer", "rows", 0, 0), (1250, 8224, "bf16", "bf16", "none", "rms", "rows", 0, 0),
+    (1220, 16384, "bf16", "f32", "rms", "rms", "none", 0, 0), (1220, 4100, "f32", "f32", "none", "layer", "none", 0, 0),
+    (1300, 17000, "bf16", "bf16", "rms", "rms", "none", 0, 0), (1300, 700, "bf16", "bf16", "rms", "rms", "none", 1, 1)])
+def test_many_rows(t, k, typ, resid, post, pre, gate, pad, lead):
+    """More rows than the GPU holds at once: copies of rows ahead, strides, in place."""
+    x, h, gt, (pw, nw) = make(t, k, typ, resid, gate, 21, pad, lead)
+    kw = dict(gate=gt, gate_act=g.GATE_SIGMOID, branch_scale=0.75, post_kind=KINDS[post], post_weight=pw[0],
+              post_bias=pw[1] if post == "layer" else None, pre_kind=KINDS[pre], pre_weight=nw[0],
+              pre_bias=nw[1] if pre == "layer" else None)
+    want = ref(x, h, gt, "sigmoid", 0.75, 1.0, post, (pw[0], kw["post_bias"]), pre, (nw[0], kw["pre_bias"]))
+    out = torch.empty_like(x)
+    h2, z, q8 = g.gguf_block_norm(x, h, out=out, q8_1=k % 32 == 0, **kw)
+    check(h2, *want[:2], "h'")
+    check(z, *want[2:], "z")
+    if k % 32 == 0:
+        check_q8(q8, *want[2:])
+    for _ in range(3):   # the same bits, whatever the order of the rows
+        again = g.gguf_block_norm(x, h, **kw)
+        assert torch.equal(again[0], h2) and torch.equal(again[1], z)
+    a, b, _ = g.gguf_block_norm(x, h, residual_out=h, out=x, **kw)
+    assert torch.equal(a, h2) and torch.equal(b, z)
+    alone = g.gguf_block_norm(None, h, pre_weight=nw[0])[1]
+    check(alone, *ref(None, h, pre_wb=(nw[0], None))[2:], "z alone")
+    assert g.gguf_device_errors() == 0

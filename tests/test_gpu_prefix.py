@@ -179,7 +179,8 @@ def plan_ref(start, kv, gs, prefix, page, n_tokens):
         entries.append([start[s], n, 0, min(shared[j], hi // 16 + 1) if n and hi >= 0 else 0, lo, hi, s, -1])
     for t in range(n_tokens):
         r = next((r for r in range(R) if start[r] <= t < start[r + 1]), -1)
-        tokens.append([kv[r] - (start[r + 1] - t) if r >= 0 else -1, r])
+        j = group.get(r, -1) if r >= 0 else -1   # request in the low half, group + 1 above it
+        tokens.append([kv[r] - (start[r + 1] - t), r | ((j if j >= 0 and shared[j] else -1) + 1) << 16] if r >= 0 else [-1, -1])
     return np.array(entries, dtype=np.int64).reshape(-1, 8), np.array(tokens, dtype=np.int64).reshape(-1, 2)
 
 
@@ -261,7 +262,7 @@ def test_another_plan_is_not_used():
         assert bool((out == 7).all()) and int(status.item()) == i + 1
     call(make())
     check_attn(out, reference({**b, "scale": 0.125}), "bf16")
-    with pytest.raises(ValueError):
+    with pytest.raises(g.GgufError, match="plan of"):
         call(make()[:-8])
 
 

@@ -95,12 +95,12 @@ def test_prefix_plan_refusals(lib, kw, want):
     assert b"prefix_plan" in lib.gguf_last_error()
 
 
-def prefix(lib, plan=256, ng=2, ws=256, ws_bytes=1 << 40, **kw):
+def prefix(lib, plan=256, plan_bytes=1 << 20, ng=2, ws=256, ws_bytes=1 << 40, **kw):
     a = dict(q=256, qt=g.BF16, n_tokens=4, ldq=1024, cache=256, n_pages=4, page_size=16, block_table=256, ld_table=4,
              width=4, q_start=0, kv_len=0, n_requests=4, max_q_len=1, n_heads=8, n_kv_heads=2, head_dim=128,
              scale=0.1, window=0, sinks=0, out=256, ldo=1024, dev_status=0)
     a.update(kw)
-    return lib.gguf_prefix_attention(ctypes.byref(g.AttnArgs(*a.values())), plan, ng, ws, ws_bytes, None)
+    return lib.gguf_prefix_attention(ctypes.byref(g.AttnArgs(*a.values())), plan, plan_bytes, ng, ws, ws_bytes, None)
 
 
 @pytest.mark.parametrize("kw, want", [
@@ -109,7 +109,7 @@ def prefix(lib, plan=256, ng=2, ws=256, ws_bytes=1 << 40, **kw):
     (dict(page_size=20), SHAPE), (dict(n_kv_heads=3), SHAPE), (dict(n_requests=16385), SHAPE), (dict(max_q_len=0), INVALID),
     (dict(n_tokens=(1 << 27) + 1), SHAPE), (dict(ldq=1000), INVALID), (dict(ldo=1000), INVALID), (dict(ld_table=3), INVALID),
     (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID), (dict(q=None), INVALID), (dict(out=None), INVALID),
-    (dict(plan=None), INVALID), (dict(cache=None), INVALID), (dict(block_table=None), INVALID), (dict(plan=264), ALIGN),
+    (dict(plan=None), INVALID), (dict(plan_bytes=32 + 6 * 32 + 4 * 8 - 1), WS), (dict(cache=None), INVALID), (dict(block_table=None), INVALID), (dict(plan=264), ALIGN),
     (dict(q=257), ALIGN), (dict(out=257), ALIGN), (dict(cache=264), ALIGN), (dict(block_table=258), ALIGN), (dict(dev_status=258), ALIGN)])
 def test_prefix_attention_refusals(lib, kw, want):
     assert prefix(lib, **kw) == want
@@ -119,5 +119,5 @@ def test_prefix_attention_refusals(lib, kw, want):
 def test_prefix_attention_nothing_to_do(lib):
     assert prefix(lib, n_tokens=0, q=None, out=None, plan=None) == 0
     assert prefix(lib, n_requests=0, q=None, out=None, plan=None) == 0
-    assert lib.gguf_prefix_attention(None, 256, 2, None, 0, None) == INVALID
+    assert lib.gguf_prefix_attention(None, 256, 1 << 20, 2, None, 0, None) == INVALID
     assert lib.gguf_prefix_attention_ws_size(None, 2) == 0
