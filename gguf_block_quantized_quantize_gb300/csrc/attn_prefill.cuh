@@ -168,30 +168,119 @@ __device__ __forceinline__ bool ap_first_sight(const AdShape &a, const ApItem &w
 // blocks in one sequence, cut evenly over the CTAs; rows of several requests, each with its own position; records and
 // slots instead of outputs.
 enum { AP_PLAIN = 0, AP_CUT = 1, AP_PRE = 2 };
-// where block `at` of the sequence lies (it is there: a thread holds `per` entries, and chunk_end the blocks up to its last)
-template <int D, int QT, class Count>
-__device__ __forceinline__ ApPlace ap_place(const AdShape &a, const Count *chunk_end, int64_t at, int per) {
+// Unpacks a block of packed tiles, 4 tiles a step, by four warps: the keys, or the values.
+// Keys: warp w8 takes tile w8 of a step; lane (g, q) holds values 8 q .. of the blocks of tokens g and g + 8; odd g
+// takes the blocks in another order, so that the stores of a warp hit different banks.
+// Values: lane (tile, p, gs) holds 8 tokens (one 16-byte chunk of a row of V^T) of 4 values of half of the
+// blocks; the tiles' pitch and the other eighth at odd p keep loads and stores off each other's banks.
+template <int D, int QT>
+struct ApUnpack {
     using C = ApCfg<D, QT>;
-    int lo = -1, hi = AP_THREADS - 1;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (chunk_end[mid] > at) hi = mid;
-        else lo = mid;
+    using L = KvTile<D>;
+    static constexpr int NB = L::NB, BW = L::BW, NC = L::NC, BT = C::BT, XS = NB / 2, STEPS = C::GT / 4;
+    const uint8_t *raws;
+    const int32_t *raw_mask;
+    int lane, w8, last, n_sink, w_tile, i_base;
+    int kg, odd, tl, pp, hb, vg;
+    uint32_t k_off, v_cx, v_row;
+    __device__ __forceinline__ ApUnpack(const uint8_t *smem, const int32_t *masks, int lane_, int w8_, const ApItem &item, int base, int last_)
+        : raws(smem + C::OFF_RAW), raw_mask(masks), lane(lane_), w8(w8_), n_sink(item.n_sink), w_tile(item.w_tile), i_base(base) {
+        const int kq = lane & 3;
+        kg = lane >> 2;
+        odd = kg & 1;
+        tl = lane & 3;
+        pp = (lane >> 2) & 1;
+        hb = w8 >> 1;
+        vg = 2 * (lane >> 3) + (pp ^ (w8 & 1));
+        k_off = (w8 * 16 + kg) * 128 + (((4 * odd + kq) ^ kg) * 16);   // of even blocks; odd ones: ^ 64
+        v_cx = ((2 * tl + pp) ^ (4 * (vg & 1))) * 16;
+        v_row = (32 * XS * hb + 4 * vg) * 128;
+        last = last_ - 8 * pp;
     }
-    if (hi > 0) at -= chunk_end[hi - 1];
-    ApPlace w;
-    int nblk;
-    for (w.entry = hi * per;; w.entry++) {
-        w.q = pf_request(a, w.entry);
-        nblk = (w.q.nt + C::GT - 1) / C::GT;
-        const int64_t n = (int64_t)ap_items(a, w.q, C::RT * 128) * nblk;
-        if (at < n) break;
-        at -= n;
+    struct Keys { uint32_t w[2][NB], d[2][NB]; bool live; };
+    struct Values { uint32_t w[4][XS], d[4][XS]; int end; };   // end: last token of the 8 that counts
+    __device__ __forceinline__ void load_keys(int rs, int step, Keys &x) const {
+        const uint8_t *raw = raws + rs * C::RAW_BYTES + (4 * step + w8) * C::PITCH;
+        x.live = (raw_mask[rs] >> (4 * step + w8)) & 1;
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+#pragma unroll
+            for (int c = 0; c < NC; c++) {
+                lds_words<BW>(raw + 4 * ((e * NC + c) * 32 + lane) * BW, *reinterpret_cast<uint32_t(*)[BW]>(&x.w[e][c * BW]));
+                lds_words<BW>(raw + L::KS + 4 * ((4 * e + (kg >> 1)) * NB + c * BW), *reinterpret_cast<uint32_t(*)[BW]>(&x.d[e][c * BW]));
+            }
+        }
     }
-    w.unit = (int)ad_div(at, nblk);
-    w.blk = (int)(at - (int64_t)w.unit * nblk);
-    return w;
-}
+    __device__ __forceinline__ void put_keys(uint8_t *sk, int step, const Keys &x) const {
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            uint8_t *to = sk + (step * 64 + e * 8) * 128;
+#pragma unroll
+            for (int i = 0; i < NB; i++) {   // block i ^ odd
+                const uint32_t w = odd ? x.w[e][i ^ 1] : x.w[e][i], s = odd ? x.d[e][i ^ 1] : x.d[e][i];
+                const __half2 d = u2h(x.live ? __byte_perm(s, 0, odd ? 0x3232 : 0x1010) : 0u);
+                const __half2 c[4] = {signed_f16<0>(w), signed_f16<1>(w), signed_f16<2>(w), signed_f16<3>(w)};
+                uint4 *at = reinterpret_cast<uint4 *>(to + (i >> 1) * (BT * 128) + (k_off ^ (i & 1 ? 64 : 0)));
+                __half2 k[4];
+#pragma unroll
+                for (int x = 0; x < 4; x++) k[x] = __hmul2(c[x], d);
+                at[0] = make_uint4(h2u(k[0]), h2u(k[1]), h2u(k[2]), h2u(k[3]));
+                if constexpr (C::KP == 2) {   // what the rounding left, exactly
+#pragma unroll
+                    for (int x = 0; x < 4; x++) k[x] = __hfma2(c[x], d, __hneg2(k[x]));
+                    at[C::K_PART / 16] = make_uint4(h2u(k[0]), h2u(k[1]), h2u(k[2]), h2u(k[3]));
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void load_values(int rs, int j, int step, Values &x) const {
+        const uint8_t *raw = raws + rs * C::RAW_BYTES + (4 * step + tl) * C::PITCH;
+        const bool live = (raw_mask[rs] >> (4 * step + tl)) & 1;
+        const int i = i_base + j * C::GT + 4 * step + tl;
+        x.end = live ? last - (i < n_sink ? i : w_tile + i - n_sink) * KV_TILE : -1;
+        const int b0 = hb * XS;
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const uint8_t *wp = raw + 4 * (((pp * NC + b0 / BW) * 32 + vg * 4 + q) * BW + b0 % BW);
+            const uint8_t *dp = raw + (L::VS - L::VC) + 4 * ((4 * pp + q) * NB + b0);
+            if constexpr (XS == 1) {
+                x.w[q][0] = *reinterpret_cast<const uint32_t *>(wp);
+                x.d[q][0] = *reinterpret_cast<const uint32_t *>(dp);
+            } else {
+                lds_words<XS>(wp, x.w[q]);
+                lds_words<XS>(dp, x.d[q]);
+            }
+        }
+    }
+    __device__ __forceinline__ void put_values(uint8_t *sv, int step, Values &x) const {
+        uint8_t *to = sv + step * (D * 128) + v_row;
+        if (x.end < 7) {   // scales of tokens past the last query's position may be anything
+            const int end = x.end;
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const uint32_t keep = (2 * q <= end ? 0xffffu : 0u) | (2 * q + 1 <= end ? 0xffff0000u : 0u);
+#pragma unroll
+                for (int i = 0; i < XS; i++) x.d[q][i] &= keep;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < XS; i++) {
+            uint32_t v[4][4];
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const __half2 d = u2h(x.d[q][i]);
+                v[0][q] = h2u(__hmul2(signed_f16<0>(x.w[q][i]), d));
+                v[1][q] = h2u(__hmul2(signed_f16<1>(x.w[q][i]), d));
+                v[2][q] = h2u(__hmul2(signed_f16<2>(x.w[q][i]), d));
+                v[3][q] = h2u(__hmul2(signed_f16<3>(x.w[q][i]), d));
+            }
+#pragma unroll
+            for (int nib = 0; nib < 4; nib++)
+                *reinterpret_cast<uint4 *>(to + (32 * i + nib) * 128 + (v_cx ^ (nib * 16))) =
+                    make_uint4(v[nib][0], v[nib][1], v[nib][2], v[nib][3]);
+        }
+    }
+};
 
 template <int D, int QT, int MODE>
 __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdShape a) {
@@ -209,9 +298,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     __shared__ int32_t abort_word;
     __shared__ ApItem item;
     __shared__ int32_t part[2][AP_THREADS / 32], cut_rows, cut_pieces, cut_from;
-    using Count = std::conditional_t<PRE, int64_t, int32_t>;
-    __shared__ Count chunk_end[AP_THREADS];   // at most (tokens x heads / 128) items: 31 bits; (PRE) blocks of all items
-    __shared__ Count pre_sum[PRE ? AP_THREADS / 32 : 1];
+    __shared__ int32_t chunk_end[AP_THREADS];   // at most (tokens x heads / 128) items: 31 bits
+    __shared__ int64_t pre_sum[AP_THREADS / 32];   // (PRE) blocks
     __shared__ ApPlace place[1];   // thread 0's
     volatile int32_t *abort_flag = &abort_word;
     const Attn &p = a.p;
@@ -241,6 +329,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     // row blocks whose tokens are cut into pieces (CUT; of 4 blocks at least, joined by a second launch).
     const int R = ad_requests<PRE>(a), per = (R + AP_THREADS - 1) / AP_THREADS;
     auto blocks_of = [](const AdReq &q) { return (q.nt + BT / KV_TILE - 1) / (BT / KV_TILE); };
+    int own = 0;   // (PRE) blocks of the CTA
+    int64_t pre_total = 0;
     if constexpr (PRE) {
         int64_t mine = 0;
         const bool fits = pf_plan_fits(a);   // (the entries are there to be read in any case)
@@ -259,17 +349,32 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         tc::tc_fence_before();
         __syncthreads();
         tc::tc_fence_after();
-        for (int w = 0; w < warp; w++) incl += pre_sum[w];
-        chunk_end[tid] = incl;
-        if (blockIdx.x == 0 && fits) {   // for the join
-            int64_t before = incl - mine;
-            for (int r = tid * per; r < min(R, (tid + 1) * per); r++) {
-                const AdReq q = pf_request(a, r);
-                if (q.q > 0) a.pf.base[r] = before;
-                before += (int64_t)ap_items(a, q, ROWS) * blocks_of(q);
-            }
+        // (every warp adds up the warps' sums, a lane each)
+        const int64_t part_sum = pre_sum[lane % (AP_THREADS / 32)];
+        int64_t upto = part_sum;
+#pragma unroll
+        for (int o = 1; o < AP_THREADS / 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o, AP_THREADS / 32);
+            if (lane % (AP_THREADS / 32) >= o) upto += v;
         }
-        __syncthreads();
+        pre_total = __shfl_sync(0xffffffffu, upto, AP_THREADS / 32 - 1);
+        int64_t before = incl - mine + __shfl_sync(0xffffffffu, upto - part_sum, warp);
+        // the CTA's blocks of the sequence; the thread that holds the entry of the first one writes it down
+        const int64_t share = ad_div(pre_total + gridDim.x - 1, gridDim.x), own0 = min(pre_total, (int64_t)blockIdx.x * share);
+        own = (int)(min(pre_total, own0 + share) - own0);
+        if (blockIdx.x == 0 && tid == 0) a.pf.share[1] = share;
+        for (int r = tid * per; mine > 0 && r < min(R, (tid + 1) * per); r++) {
+            const AdReq q = pf_request(a, r);
+            const int nblk = blocks_of(q);
+            const int64_t n = (int64_t)ap_items(a, q, ROWS) * nblk;
+            if (blockIdx.x == 0 && q.q > 0) a.pf.base[r] = before;   // for the join
+            if (own > 0 && before <= own0 && own0 < before + n) {
+                const int unit = (int)ad_div(own0 - before, nblk);
+                place[0] = ApPlace{r, unit, (int)(own0 - before - (int64_t)unit * nblk), q};
+            }
+            before += n;
+        }
+        // (the first item begins behind a barrier)
     } else {
         int item_rows = ROWS, splits = 1;
         int mine = 0, mine128 = 0;   // (tokens x heads / 128 is below 2^31)
@@ -316,7 +421,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         }
         __syncthreads();
     }
-    const int64_t total = PRE ? (int64_t)chunk_end[AP_THREADS - 1] : CUT ? cut_from + (int64_t)(chunk_end[AP_THREADS - 1] - cut_from) * cut_pieces : chunk_end[AP_THREADS - 1];
+    const int64_t total = PRE ? pre_total : CUT ? cut_from + (int64_t)(chunk_end[AP_THREADS - 1] - cut_from) * cut_pieces : chunk_end[AP_THREADS - 1];
     const uint32_t tmem = tmem_slot;
     auto fail = [&](int code) {
         *abort_flag = 1;
@@ -327,14 +432,6 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar);
     };
-    // (PRE) the CTA's blocks of the sequence
-    int own = 0;
-    if constexpr (PRE) {
-        const int64_t share = ad_div(total + gridDim.x - 1, gridDim.x), own0 = min(total, (int64_t)blockIdx.x * share);
-        own = (int)(min(total, own0 + share) - own0);
-        if (blockIdx.x == 0 && tid == 0) a.pf.share[1] = share;
-        if (own > 0 && tid == 0) place[0] = ap_place<D, QT>(a, chunk_end, own0, per);
-    }
     auto token_of = [&](int i) { return (i < item.n_sink ? i : item.w_tile + i - item.n_sink) * KV_TILE; };
 
     // items in stripes of one per CTA, every other stripe backwards: a request's row blocks come longest first
@@ -442,6 +539,49 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         return true;
     };
     Walk wk;
+    // the keys of an item's blocks, or their values, by four warps that do nothing else
+    auto unpack_keys = [&](const ApUnpack<D, QT> &u) {
+        bool ok = true;
+        for (int j = 0; j < wk.nblk && ok; j++) {
+            const int gb = wk.loads_before + 2 * j, rk = gb % C::RAWST, kb = wk.blocks_before + j, ks = kb % C::KST;
+            uint8_t *sk = smem + C::OFF_K + ks * C::K_BYTES;
+            typename ApUnpack<D, QT>::Keys x[C::GT / 4];
+            ok = tc::mbar_wait(&raw_full[rk], (uint32_t)(gb / C::RAWST) & 1u);
+            if (!ok) break;
+            const int mask = raw_mask[rk];
+#pragma unroll
+            for (int i = 0; i < C::GT / 4; i++) u.load_keys(rk, i, x[i]);
+            ok = tc::mbar_wait(&k_empty[ks], ((uint32_t)(kb / C::KST) & 1u) ^ 1u) && !*abort_flag;
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < C::GT / 4; i++) u.put_keys(sk, i, x[i]);
+            arrive(&raw_empty[rk]);
+            if (u.w8 == 0 && lane == 0) blk_mask[kb & 7] = mask;
+            tc::fence_proxy_async_smem();
+            arrive(&k_full[ks]);
+        }
+        if (!ok && lane == 0) fail(4);
+    };
+    auto unpack_values = [&](const ApUnpack<D, QT> &u) {
+        bool ok = true;
+        for (int j = 0; j < wk.nblk && ok; j++) {
+            const int gb = wk.loads_before + 2 * j + 1, rv = gb % C::RAWST, kb = wk.blocks_before + j, vs = kb % C::VST;
+            uint8_t *sv = smem + C::OFF_V + vs * C::V_BYTES;
+            typename ApUnpack<D, QT>::Values x[C::GT / 4];
+            ok = tc::mbar_wait(&raw_full[rv], (uint32_t)(gb / C::RAWST) & 1u);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < C::GT / 4; i++) u.load_values(rv, j, i, x[i]);
+            ok = tc::mbar_wait(&v_empty[vs], ((uint32_t)(kb / C::VST) & 1u) ^ 1u) && !*abort_flag;
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < C::GT / 4; i++) u.put_values(sv, i, x[i]);
+            arrive(&raw_empty[rv]);
+            tc::fence_proxy_async_smem();
+            arrive(&v_full[vs]);
+        }
+        if (!ok && lane == 0) fail(4);
+    };
     if (warp < 8) {
         set_registers<C::REGS>();
         for (Stripe st = 0; PRE ? st < own : st < stripes; st += PRE ? wk.nblk : 1) {
@@ -452,7 +592,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             {
                 // (PRE: few blocks follow, so the loads of many rows are under way at once: one at a time took 12000 cycles)
                 constexpr int LPR = D / 8, AT_ONCE = PRE ? 8 : 1;
-                const int rows_used = PRE ? wk.nrt * 128 : ROWS;
+                // (rows that are not there keep what lies in their places: a row's results depend on its own operands alone)
+                const int rows_used = PRE ? (item.rows + 256 / LPR - 1) / (256 / LPR) * (256 / LPR) : ROWS;
                 for (int row0 = tid / LPR; row0 < rows_used; row0 += AT_ONCE * (256 / LPR)) {
                     uint32_t w[AT_ONCE][4];
                     const int l = tid % LPR;
@@ -476,29 +617,32 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
 #pragma unroll
                     for (int i = 0; i < AT_ONCE; i++) {
                         const int row = row0 + i * (256 / LPR);
+                        if (PRE && row >= rows_used) break;   // (for all threads)
                         if constexpr (QT == GGUF_BF16) {
-                            float v[8], mx = 0.0f;
+                            __nv_bfloat162 big = __float2bfloat162_rn(0.0f);   // the largest magnitudes of both halves
 #pragma unroll
-                            for (int x = 0; x < 8; x++) {
-                                v[x] = bf2f((uint16_t)(w[i][x / 2] >> (16 * (x & 1))));
-                                mx = fmaxf(mx, fabsf(v[x]));
-                            }
+                            for (int x = 0; x < 4; x++) big = __hmax2(big, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i][x])));
                             // a row's lanes lie in one warp and all of them are here (256 / LPR divides the rows)
 #pragma unroll
-                            for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                            const float up = q_scale_up(mx);
+                            for (int o = 1; o < LPR; o <<= 1) big = __hmax2(big, __shfl_xor_sync(0xffffffffu, big, o));
+                            const float up = q_scale_up(__bfloat162float(__hmax(__low2bfloat16(big), __high2bfloat16(big))));
 #pragma unroll
-                            for (int x = 0; x < 4; x++) w[i][x] = pack_h2(v[2 * x] * up, v[2 * x + 1] * up);
-                            if (l == 0 && row < rows_used) q_inv[row] = 1.0f / up;
-                        } else if (l == 0 && row < rows_used) q_inv[row] = 1.0f;
+                            for (int x = 0; x < 4; x++)
+                                w[i][x] = pack_h2(__uint_as_float(w[i][x] << 16) * up, __uint_as_float(w[i][x] & 0xffff0000u) * up);
+                            // 1 / up, of a power of two
+                            if (l == 0) q_inv[row] = __uint_as_float((254u << 23) - __float_as_uint(up));
+                        } else if (l == 0) q_inv[row] = 1.0f;
                         const int tile = row / 128, r7 = row % 128;
-                        if (row < rows_used)
-                            *reinterpret_cast<uint4 *>(smem + tile * (128 * D * 2) + (8 * l / 64) * 16384 + r7 * 128 +
-                                                       (((l & 7) ^ (r7 & 7)) * 16)) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+                        *reinterpret_cast<uint4 *>(smem + tile * (128 * D * 2) + (8 * l / 64) * 16384 + r7 * 128 +
+                                                   (((l & 7) ^ (r7 & 7)) * 16)) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
                     }
                 }
                 tc::fence_proxy_async_smem();
                 arrive(&q_full);
+            }
+            if (PRE && wk.nrt == 1 && warp >= 4) {   // no rows of its own: the values
+                unpack_values(ApUnpack<D, QT>(smem, raw_mask, lane, warp - 4, item, item.base, item.pos_max));
+                continue;
             }
             // ================= softmax
             const int t = warp >> 2;
@@ -521,6 +665,10 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                     const int n = j * wk.nrt + t, x = n & 1;
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&s_full[x], (uint32_t)(wk.uses[x] + n / 2) & 1u)) && !*abort_flag;
                     if (!ok) { if (lane == 0) fail(2); break; }
+                    if (PRE && lastr < t * 128 + quad * 32) {   // no row of the warp is there: its P may be anything
+                        arrive(&p_full[x]);
+                        continue;
+                    }
                     tc::tc_fence_after();
                     const uint32_t s_col = tmem + lanes + x * C::COL_S;
                     // whether every row of the warp sees the whole block
@@ -614,7 +762,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                     if (!ok && lane == 0) fail(8);
                     tc::tc_fence_after();
                 }
-                if (ok) {
+                if (ok && (!PRE || lastr >= t * 128 + quad * 32)) {
                     const float inv = lsum == 0.0f ? 0.0f : 1.0f / lsum;
                     const int rr0 = item.row0 + row;
                     // PRE: a row's record is put together where the operands lay (nothing reads them any more) and leaves
@@ -666,14 +814,17 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                         }
                     }
                     if constexpr (PRE) {
-                        if (there) {
-                            const int tk = ad_token_of_row(a, rr0);
+                        if (there) *reinterpret_cast<float4 *>(rec + D) = make_float4(ref, lsum, 0.0f, 0.0f);
+                        tc::fence_proxy_async_smem();
+                        __syncwarp();
+                        // the rows of a token lie side by side among the records, all rows among the slots: a copy for each run
+                        // (one for each row took 2600 cycles)
+                        const int tk = ad_token_of_row(a, rr0), in_token = rr0 - tk * G, left = lastr - row + 1;
+                        if (there && (lane == 0 || (item.first && in_token == 0))) {
                             float *to = item.first ? a.pf.records + ((item.q0 + tk + (item.first == 2 ? p.n_tokens : 0)) * p.h +
-                                                                     item.head * G + rr0 - tk * G) * RS
+                                                                     item.head * G + in_token) * RS
                                                    : a.pieces + ((int64_t)blockIdx.x * ROWS + row) * RS;
-                            *reinterpret_cast<float4 *>(rec + D) = make_float4(ref, lsum, 0.0f, 0.0f);
-                            tc::fence_proxy_async_smem();
-                            bulk_store(to, rec, RS * 4);
+                            bulk_store(to, rec, (uint32_t)((item.first ? min(left, G - in_token) : left) * RS * 4));
                         }
                         bulk_store_read();   // the space is free for the next piece's operands
                     }
@@ -688,118 +839,29 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             const int64_t it = PRE ? st : item_of(st);
             if (!PRE && it >= total) continue;
             if (!begin(wk, it)) break;
-            // ================= unpack: the keys of a block, then its values, 4 tiles a step.  The packed words of the next step are
+            // ================= unpack: the keys of a block, then its values.  The packed words of the next step are
             // read from shared memory before the current one is computed: the matrix unit's reads fill the shared memory's
             // bandwidth for long stretches, and a read may take many hundred cycles.
-            // Keys: warp w8 takes tile w8 of a step; lane (g, q) holds values 8 q .. of the blocks of tokens g and g + 8; odd g
-            // takes the blocks in another order, so that the stores of a warp hit different banks.
-            // Values: lane (tile, p, gs) holds 8 tokens (one 16-byte chunk of a row of V^T) of 4 values of half of the
-            // blocks; the tiles' pitch and the other eighth at odd p keep loads and stores off each other's banks.
-            constexpr int XS = NB / 2;
-            const int w8 = warp - 8;
-            const int kg = lane >> 2, kq = lane & 3, odd = kg & 1;
-            const int tl = lane & 3, pp = (lane >> 2) & 1, hb = w8 >> 1, vg = 2 * (lane >> 3) + (pp ^ (w8 & 1));
-            const uint32_t k_off = (w8 * 16 + kg) * 128 + (((4 * odd + kq) ^ kg) * 16);   // of even blocks; odd ones: ^ 64
-            const uint32_t v_cx = ((2 * tl + pp) ^ (4 * (vg & 1))) * 16, v_row = (32 * XS * hb + 4 * vg) * 128;
-            const uint8_t *raws = smem + C::OFF_RAW;
-            const int last = (PRE ? item.pos_max : item.pos0 + (item.row0 + item.rows - 1) / G - item.tok0) - 8 * pp;
-            const int n_sink = item.n_sink, w_tile = item.w_tile, i_base = PARTS ? item.base : 0;
-            bool ok = true;
             constexpr int STEPS = C::GT / 4;
+            const int w8 = warp - 8;
+            const ApUnpack<D, QT> u(smem, raw_mask, lane, w8, item, PARTS ? item.base : 0,
+                                    PRE ? item.pos_max : item.pos0 + (item.row0 + item.rows - 1) / G - item.tok0);
+            if (PRE && wk.nrt == 1) {   // the second row tile's warps have no rows and take the values
+                unpack_keys(u);
+                continue;
+            }
+            bool ok = true;
             auto raw_wait = [&](int load) {
                 const int gb = wk.loads_before + load;
                 ok = ok && tc::mbar_wait(&raw_full[gb % C::RAWST], (uint32_t)(gb / C::RAWST) & 1u);
                 return gb % C::RAWST;
             };
-            struct Keys { uint32_t w[2][NB], d[2][NB]; bool live; };
-            struct Values { uint32_t w[4][XS], d[4][XS]; int end; };   // end: last token of the 8 that counts
-            auto load_keys = [&](int rs, int step, Keys &x) {
-                const uint8_t *raw = raws + rs * C::RAW_BYTES + (4 * step + w8) * C::PITCH;
-                x.live = (raw_mask[rs] >> (4 * step + w8)) & 1;
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-#pragma unroll
-                    for (int c = 0; c < NC; c++) {
-                        lds_words<BW>(raw + 4 * ((e * NC + c) * 32 + lane) * BW, *reinterpret_cast<uint32_t(*)[BW]>(&x.w[e][c * BW]));
-                        lds_words<BW>(raw + L::KS + 4 * ((4 * e + (kg >> 1)) * NB + c * BW), *reinterpret_cast<uint32_t(*)[BW]>(&x.d[e][c * BW]));
-                    }
-                }
-            };
-            auto put_keys = [&](uint8_t *sk, int step, const Keys &x) {
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    uint8_t *to = sk + (step * 64 + e * 8) * 128;
-#pragma unroll
-                    for (int i = 0; i < NB; i++) {   // block i ^ odd
-                        const uint32_t w = odd ? x.w[e][i ^ 1] : x.w[e][i], s = odd ? x.d[e][i ^ 1] : x.d[e][i];
-                        const __half2 d = u2h(x.live ? __byte_perm(s, 0, odd ? 0x3232 : 0x1010) : 0u);
-                        const __half2 c[4] = {signed_f16<0>(w), signed_f16<1>(w), signed_f16<2>(w), signed_f16<3>(w)};
-                        uint4 *at = reinterpret_cast<uint4 *>(to + (i >> 1) * (BT * 128) + (k_off ^ (i & 1 ? 64 : 0)));
-                        __half2 k[4];
-#pragma unroll
-                        for (int x = 0; x < 4; x++) k[x] = __hmul2(c[x], d);
-                        at[0] = make_uint4(h2u(k[0]), h2u(k[1]), h2u(k[2]), h2u(k[3]));
-                        if constexpr (C::KP == 2) {   // what the rounding left, exactly
-#pragma unroll
-                            for (int x = 0; x < 4; x++) k[x] = __hfma2(c[x], d, __hneg2(k[x]));
-                            at[C::K_PART / 16] = make_uint4(h2u(k[0]), h2u(k[1]), h2u(k[2]), h2u(k[3]));
-                        }
-                    }
-                }
-            };
-            auto load_values = [&](int rs, int j, int step, Values &x) {
-                const uint8_t *raw = raws + rs * C::RAW_BYTES + (4 * step + tl) * C::PITCH;
-                const bool live = (raw_mask[rs] >> (4 * step + tl)) & 1;
-                const int i = i_base + j * C::GT + 4 * step + tl;
-                x.end = live ? last - (i < n_sink ? i : w_tile + i - n_sink) * KV_TILE : -1;
-                const int b0 = hb * XS;
-#pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    const uint8_t *wp = raw + 4 * (((pp * NC + b0 / BW) * 32 + vg * 4 + q) * BW + b0 % BW);
-                    const uint8_t *dp = raw + (L::VS - L::VC) + 4 * ((4 * pp + q) * NB + b0);
-                    if constexpr (XS == 1) {
-                        x.w[q][0] = *reinterpret_cast<const uint32_t *>(wp);
-                        x.d[q][0] = *reinterpret_cast<const uint32_t *>(dp);
-                    } else {
-                        lds_words<XS>(wp, x.w[q]);
-                        lds_words<XS>(dp, x.d[q]);
-                    }
-                }
-            };
-            auto put_values = [&](uint8_t *sv, int step, Values &x) {
-                uint8_t *to = sv + step * (D * 128) + v_row;
-                if (x.end < 7) {   // scales of tokens past the last query's position may be anything
-                    const int end = x.end;
-#pragma unroll
-                    for (int q = 0; q < 4; q++) {
-                        const uint32_t keep = (2 * q <= end ? 0xffffu : 0u) | (2 * q + 1 <= end ? 0xffff0000u : 0u);
-#pragma unroll
-                        for (int i = 0; i < XS; i++) x.d[q][i] &= keep;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < XS; i++) {
-                    uint32_t v[4][4];
-#pragma unroll
-                    for (int q = 0; q < 4; q++) {
-                        const __half2 d = u2h(x.d[q][i]);
-                        v[0][q] = h2u(__hmul2(signed_f16<0>(x.w[q][i]), d));
-                        v[1][q] = h2u(__hmul2(signed_f16<1>(x.w[q][i]), d));
-                        v[2][q] = h2u(__hmul2(signed_f16<2>(x.w[q][i]), d));
-                        v[3][q] = h2u(__hmul2(signed_f16<3>(x.w[q][i]), d));
-                    }
-#pragma unroll
-                    for (int nib = 0; nib < 4; nib++)
-                        *reinterpret_cast<uint4 *>(to + (32 * i + nib) * 128 + (v_cx ^ (nib * 16))) =
-                            make_uint4(v[nib][0], v[nib][1], v[nib][2], v[nib][3]);
-                }
-            };
-            Keys ka, kc;
-            Values va, vc;
+            typename ApUnpack<D, QT>::Keys ka, kc;
+            typename ApUnpack<D, QT>::Values va, vc;
             int rk = 0;
             if (wk.nblk > 0) {
                 rk = raw_wait(0);
-                if (ok) load_keys(rk, 0, ka);
+                if (ok) u.load_keys(rk, 0, ka);
             }
             for (int j = 0; j < wk.nblk && ok; j++) {
                 const int kb = wk.blocks_before + j, ks = kb % C::KST, vs = kb % C::VST;
@@ -808,29 +870,29 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                 if (!ok) break;
                 const int mask = raw_mask[rk];
                 if constexpr (STEPS == 2) {
-                    load_keys(rk, 1, kc);
-                    put_keys(sk, 0, ka);
+                    u.load_keys(rk, 1, kc);
+                    u.put_keys(sk, 0, ka);
                 }
                 const int rv = raw_wait(2 * j + 1);
                 if (!ok) break;
-                load_values(rv, j, 0, va);
-                put_keys(sk, STEPS - 1, STEPS == 2 ? kc : ka);
+                u.load_values(rv, j, 0, va);
+                u.put_keys(sk, STEPS - 1, STEPS == 2 ? kc : ka);
                 arrive(&raw_empty[rk]);
                 if (w8 == 0 && lane == 0) blk_mask[kb & 7] = mask;
                 tc::fence_proxy_async_smem();
                 arrive(&k_full[ks]);
-                if constexpr (STEPS == 2) load_values(rv, j, 1, vc);
+                if constexpr (STEPS == 2) u.load_values(rv, j, 1, vc);
                 ok = tc::mbar_wait(&v_empty[vs], ((uint32_t)(kb / C::VST) & 1u) ^ 1u);
                 if (!ok) break;
-                put_values(sv, 0, va);
-                if constexpr (STEPS == 2) put_values(sv, 1, vc);
+                u.put_values(sv, 0, va);
+                if constexpr (STEPS == 2) u.put_values(sv, 1, vc);
                 arrive(&raw_empty[rv]);
                 tc::fence_proxy_async_smem();
                 arrive(&v_full[vs]);
                 if (*abort_flag) break;
                 if (j + 1 < wk.nblk) {
                     rk = raw_wait(2 * j + 2);
-                    if (ok) load_keys(rk, 0, ka);
+                    if (ok) u.load_keys(rk, 0, ka);
                 }
             }
             if (!ok && lane == 0) fail(4);
@@ -914,26 +976,33 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                 }
                 __syncwarp();
             } else if (warp == AP_LOAD) {
-                // ================= loads: the keys of a block, its values, the next one's keys, ..; lane i tile i
+                // ================= loads: the keys of a block, its values, the next one's keys, ..; lane i tile i.  The lanes
+                // hold the places of 32 tiles in the cache, and read the table for the 32 after them meanwhile (an entry at
+                // a time on the spot took 1900 cycles a load)
                 bool ok = true;
-                const int nloads = 2 * wk.nblk;
+                const int nloads = 2 * wk.nblk, i_base = PARTS ? item.base : 0, i_end = item.nt;
                 int issued = 0;
+                auto place_of = [&](int i) -> int64_t {   // of the i-th tile; -1 where it has none
+                    if (i >= i_end) return -1;
+                    const int tile = i < item.n_sink ? i : item.w_tile + i - item.n_sink;
+                    const int pi = a.tpp_shift >= 0 ? tile >> a.tpp_shift : (int)((uint32_t)tile / (uint32_t)a.tpp);
+                    const int32_t pg = pi < p.width ? p.table[item.r * p.ld + pi] : -1;
+                    if (pg >= 0 && pg < p.n_pages) return pg * a.page_bytes + (int64_t)(item.head * a.tpp + tile - pi * a.tpp) * L::BYTES;
+                    if (item.head == 0 && p.status != nullptr && (PRE ? pf_first_sight(a, item, i) : ap_first_sight(a, item, tile)))
+                        atomicAdd(p.status, 1);
+                    return -1;
+                };
+                int64_t now = place_of(i_base + lane), next = place_of(i_base + 32 + lane);
                 for (int e = 0; e < nloads && ok; e++) {
                     const int gb = wk.loads_before + e, rs = gb % C::RAWST;
                     const bool values = e & 1;
-                    const int j = e / 2;
-                    const int i = (PARTS ? item.base : 0) + j * C::GT + (lane & (C::GT - 1));
-                    int32_t pg = -1;
-                    int tok = 0;
-                    if (i < item.nt) {
-                        tok = token_of(i);
-                        const uint32_t pi = (uint32_t)tok / (uint32_t)p.page;
-                        pg = pi < p.width ? p.table[item.r * p.ld + pi] : -1;
-                        if (lane < C::GT && !values && item.head == 0 && (pg < 0 || pg >= p.n_pages) && p.status != nullptr &&
-                            (PRE ? pf_first_sight(a, item, i) : ap_first_sight(a, item, tok / KV_TILE)))
-                            atomicAdd(p.status, 1);
+                    const int i0 = e / 2 * C::GT;   // the block's first tile
+                    if (!values && i0 > 0 && i0 % 32 == 0) {
+                        now = next;
+                        next = place_of(i_base + i0 + 32 + lane);
                     }
-                    const bool live = lane < C::GT && pg >= 0 && pg < p.n_pages;
+                    const int64_t place = __shfl_sync(0xffffffffu, now, i0 % 32 + (lane & (C::GT - 1)));
+                    const bool live = lane < C::GT && place >= 0;
                     const uint32_t mask = __ballot_sync(0xffffffffu, live);
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&raw_empty[rs], ((uint32_t)(gb / C::RAWST) & 1u) ^ 1u)) && !*abort_flag;
                     if (!ok) { if (lane == 0) fail(32); break; }
@@ -942,13 +1011,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                         tc::mbar_arrive_expect_tx(&raw_full[rs], (uint32_t)__popc(mask) * (L::BYTES / 2));
                     }
                     __syncwarp();
-                    if (live) {
-                        const uint32_t off = (uint32_t)tok % (uint32_t)p.page;
-                        bulk_load(smem + C::OFF_RAW + rs * C::RAW_BYTES + lane * C::PITCH,
-                                  p.cache + pg * a.page_bytes + (values ? L::VC : 0) +
-                                      (item.head * (p.page / KV_TILE) + off / KV_TILE) * (int64_t)L::BYTES,
+                    if (live)
+                        bulk_load(smem + C::OFF_RAW + rs * C::RAW_BYTES + lane * C::PITCH, p.cache + place + (values ? L::VC : 0),
                                   L::BYTES / 2, &raw_full[rs]);
-                    }
                     issued = e + 1;
                 }
                 if (!ok)   // copies that are under way land before the CTA exits
