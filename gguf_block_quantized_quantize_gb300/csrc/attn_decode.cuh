@@ -74,6 +74,11 @@ struct AdCfg {
     static constexpr int SMEM = WARPS * (RING + SLOT);
 };
 
+// a / b of non-negative numbers, mostly small ones
+__device__ __forceinline__ int64_t ad_div(int64_t a, int64_t b) {
+    return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // An entry of the plan of gguf_prefix_attention (attn_prefix.cu): queries that see tiles of one row of the block table.
 // Entry r < R: the queries of request r and its own tiles; entry R + g: those of all requests of group g and the tiles
 // that the group shares.
@@ -89,14 +94,14 @@ struct PfEntry {
 // for its group's: of the first piece of its unit.  The rest of the unit's tiles went to the warps (decode kernel) or CTAs
 // (prefill kernel) that follow in the sequence; each has one slot, of rows like records, for a unit that began before it.
 struct PfShape {
-    const int32_t *plan;       // header, entries, then of each token its position, and its request and group (pf_pack)
+    const int32_t *plan;       // header, entries, of each token its position, and its request and group (pf_pack), q_start, kv_len
     int32_t n_entries, chained;   // chained: the decode kernel follows the prefill kernel of the call
     float *records;
     int64_t *base;             // tiles (decode kernel) or blocks (prefill kernel) before each entry's, of the kernel that takes it
-    int64_t *share;            // tiles of a CTA (decode kernel), blocks of a CTA (prefill kernel), tiles of a warp
+    int64_t *share;            // tiles of a CTA (decode kernel), blocks of a CTA (prefill kernel), tiles of a warp, warps with tiles
 };
 // warps of a CTA that have tiles
-__device__ __forceinline__ int pf_warps(int64_t share, int64_t per_warp) { return (int)((share + per_warp - 1) / per_warp); }
+__device__ __forceinline__ int pf_warps(int64_t share, int64_t per_warp) { return (int)ad_div(share + per_warp - 1, per_warp); }
 constexpr int PF_HEADER = 8, PF_MAGIC = 0x50465831;   // {magic, requests, groups, tokens, page size, 0, 0, 0}
 template <int D> struct PfStride { static constexpr int64_t value = D + 4; };   // 16-byte steps
 
@@ -219,11 +224,6 @@ __device__ __forceinline__ bool ad_starts_page(const AdShape &a, const AdReq &q,
 __device__ __forceinline__ int64_t ad_units(const AdShape &a, const AdReq &q, int rg) {
     return (int64_t)((q.q * a.G + rg - 1) / rg) * a.hk;
 }
-// a / b of non-negative numbers, mostly small ones
-__device__ __forceinline__ int64_t ad_div(int64_t a, int64_t b) {
-    return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-
 // d = A B + c of the warp-level 16x8x16 product, fp16 or (BF) bf16 operands
 template <bool BF>
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
@@ -402,17 +402,29 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     __syncthreads();
     before -= mine;
     int64_t total = 0;
+    if constexpr (PRE) {   // (every warp adds up the warps' sums, a lane each)
+        const int64_t one = lane < NTHR / 32 ? warp_sum[lane] : 0;
+        int64_t upto = one;
 #pragma unroll
-    for (int w = 0; w < NTHR / 32; w++) {
-        if (w < warp) before += warp_sum[w];
-        total += warp_sum[w];
+        for (int o = 1; o < NTHR / 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        total = __shfl_sync(0xffffffffu, upto, NTHR / 32 - 1);
+        before += __shfl_sync(0xffffffffu, upto - one, warp);
+    } else {
+#pragma unroll
+        for (int w = 0; w < NTHR / 32; w++) {
+            if (w < warp) before += warp_sum[w];
+            total += warp_sum[w];
+        }
     }
     const int64_t share = !PRE && a.whole ? 1 : ad_div(total + gridDim.x - 1, gridDim.x);
     int64_t cta0 = min(total, (int64_t)blockIdx.x * share), cta1 = min(total, cta0 + share);
     int64_t per_warp = ad_div(cta1 - cta0 + C::WARPS - 1, C::WARPS);
     if constexpr (PRE) {   // the same in all CTAs
-        per_warp = ad_div(share + C::WARPS - 1, C::WARPS);
-        if (blockIdx.x == 0 && tid == 0) { a.pf.share[0] = share; a.pf.share[2] = per_warp; }
+        per_warp = max((int64_t)1, ad_div(share + C::WARPS - 1, C::WARPS));
+        if (blockIdx.x == 0 && tid == 0) { a.pf.share[0] = share; a.pf.share[2] = per_warp; a.pf.share[3] = pf_warps(share, per_warp); }
     }
     for (int r = r0; r < r1; r++) {
         if (per > 1) {

@@ -32,6 +32,11 @@ int *tg_error_word();   // the library's device error word (mmq.cu)
 
 // ---------------------------------------------------------------- plan
 
+// where q_start and kv_len lie in a plan, in words
+__host__ __device__ __forceinline__ int64_t pf_lengths_at(int64_t R, int64_t NG, int64_t n_tokens) {
+    return PF_HEADER + (R + NG) * (int64_t)(sizeof(PfEntry) / 4) + 2 * n_tokens;
+}
+
 struct PfPlanArgs {
     const int32_t *q_start, *kv_len;
     int64_t R;
@@ -100,6 +105,9 @@ __global__ void __launch_bounds__(PF_THREADS) prefix_plan_kernel(const PfPlanArg
         const int32_t h[PF_HEADER] = {PF_MAGIC, (int32_t)p.R, (int32_t)p.NG, (int32_t)p.n_tokens, (int32_t)p.page, 0, 0, 0};
         for (int i = 0; i < PF_HEADER; i++) p.plan[i] = h[i];
     }
+    int32_t *starts = p.plan + pf_lengths_at(p.R, p.NG, p.n_tokens);   // what a call takes whose requests go one by one
+    if (id <= p.R) starts[id] = p.q_start[id];
+    if (id < p.R) starts[p.R + 1 + id] = p.kv_len[id];
     if (id < p.n_tokens) {
         const int64_t r = last_up_to(p.q_start, p.R + 1, id);
         int2 o = make_int2(-1, -1);
@@ -150,7 +158,7 @@ __global__ void __launch_bounds__(PF_THREADS) prefix_plan_kernel(const PfPlanArg
 }
 
 int64_t prefix_plan_bytes(int64_t R, int64_t NG, int64_t n_tokens) {
-    return PF_HEADER * 4 + (R + NG) * (int64_t)sizeof(PfEntry) + n_tokens * 8;
+    return 4 * (pf_lengths_at(R, NG, n_tokens) + 2 * R + 1);
 }
 
 static cudaError_t launch_chained(const void *kern, int64_t grid, int threads, cudaStream_t s, void **args) {
@@ -169,7 +177,7 @@ static cudaError_t launch_chained(const void *kern, int64_t grid, int threads, c
 cudaError_t launch_prefix_plan(const int32_t *q_start, const int32_t *kv_len, int64_t R, const int32_t *group_start,
                                const int32_t *prefix_len, int64_t NG, int64_t page, int64_t n_tokens, void *plan, cudaStream_t s) {
     PfPlanArgs a{q_start, kv_len, R, group_start, prefix_len, NG, page, n_tokens, (int32_t *)plan};
-    const int64_t most = std::max<int64_t>(std::max(R, n_tokens), std::max<int64_t>(32 * NG, 1));
+    const int64_t most = std::max<int64_t>(std::max(R + 1, n_tokens), 32 * NG);
     void *args[1] = {&a};
     return launch_chained((const void *)prefix_plan_kernel, (most + PF_THREADS - 1) / PF_THREADS, PF_THREADS, s, args);
 }
@@ -184,7 +192,7 @@ struct PfPieces {
     __device__ __forceinline__ const float *at(int i) const { return i == 0 ? first : slot + i * step; }
 };
 template <int D>
-__device__ __forceinline__ PfPieces pf_pieces(const AdShape &a, const AdReq &q, bool group, int64_t base, const int64_t (&shares)[3],
+__device__ __forceinline__ PfPieces pf_pieces(const AdShape &a, const AdReq &q, bool group, int64_t base, const int64_t (&shares)[4],
                                               int64_t t, int head, int few, int rg) {
     constexpr int64_t RS = PfStride<D>::value;
     constexpr int ROWS = D == 256 ? 128 : 256, BTILES = D == 256 ? 4 : 8;   // the prefill kernel's (ApCfg)
@@ -197,7 +205,7 @@ __device__ __forceinline__ PfPieces pf_pieces(const AdShape &a, const AdReq &q, 
     // the CTA, or the warp of a CTA, that a tile or block of the sequence went to
     auto taker = [&](int64_t i) {
         const int64_t cta = ad_div(i, shares[tc]);
-        return tc ? cta : cta * pf_warps(shares[0], shares[2]) + ad_div(i - cta * shares[0], shares[2]);
+        return tc ? cta : cta * shares[3] + ad_div(i - cta * shares[0], shares[2]);
     };
     const int64_t c0 = taker(from);
     x.n = (int)(taker(from + n - 1) - c0) + 1;
@@ -218,7 +226,7 @@ __global__ void __launch_bounds__(PF_THREADS) prefix_join_kernel(const AdShape a
     const int64_t w = ((int64_t)blockIdx.x * PF_THREADS + threadIdx.x) >> 5, t = (uint64_t)w >> 31 ? w / p.h : (int64_t)((uint32_t)w / (uint32_t)p.h);
     const int head = (int)(w - t * p.h), lane = threadIdx.x & 31;
     const int2 at_rg = pf_unpack(t < p.n_tokens ? pf_token(a.pf, t).y : -1);
-    const int64_t shares[3] = {a.pf.share[0], a.pf.share[1], a.pf.share[2]};
+    const int64_t shares[4] = {a.pf.share[0], a.pf.share[1], a.pf.share[2], a.pf.share[3]};
     if (!pf_plan_fits(a)) {
         if (w == 0 && lane == 0 && p.status != nullptr) atomicAdd(p.status, 1);
         return;
@@ -295,6 +303,7 @@ static const void *join_kernel(int qt) {
 // ---------------------------------------------------------------- what a call runs
 
 struct PfRun {
+    bool alone;        // the requests go one by one, through the kernels of gguf_paged_attention
     int ctas;
     bool tc;           // the tensor-core kernel runs
     int few, rg;       // entries of at most `few` query rows per KV head, in units of rg rows, go to the other one
@@ -310,6 +319,19 @@ static PfRun prefix_run(const Attn &p, int64_t NG, int64_t d) {
     x.rg = p.qt != GGUF_F32 && d != 256 && G * p.max_q > 8 ? 16 : 8;
     x.tc = p.qt != GGUF_F32 && p.n_tokens * G > x.rg;
     x.few = x.tc ? x.rg : 0x7fffffff;
+    // Sharing has a price, the launches, starts and joins of its kernels: about 40 us in all (20 us for fp32 queries, which
+    // one kernel takes).  What the requests cost one by one, 10 us and 0.42 ns a tile of heads of 128 (more for 16 rows and
+    // for fp32 queries), is known up to the width of the table: where that is less, they go so.  Measured, one by one and
+    // shared: 2 x (700 + 60) tokens, fp32, 8 KV heads of 128: 12.5 and 21 us; 38 requests of 6 groups, 5300 tokens, 2 of 256:
+    // 35 and 47 us; 32 x (8192 + 512), 8 of 128: 69 and 42 us; 256 x (32768 + 128): 1690 and 191 us.
+    const double tiles = (double)p.R * (double)p.hk * (double)((G * std::min(p.max_q, p.n_tokens) + x.rg - 1) / x.rg) *
+                         (double)(p.width * p.page / KV_TILE);
+    const double us = 10.0 + tiles * 0.42e-3 * (double)d / 128.0 * (x.rg == 16 ? 1.4 : 1.0) * (p.qt == GGUF_F32 ? 1.9 : 1.0);
+    x.alone = us < (x.tc ? 40.0 : 20.0);
+    if (x.alone) {
+        x.bytes = attn_ws_size(p, d);
+        return x;
+    }
     auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
     const size_t rs = (size_t)(d + 4) * 4;
     x.share = up((size_t)(p.R + NG) * 8);
@@ -325,6 +347,12 @@ size_t prefix_attn_ws_size(const Attn &p, int64_t NG, int64_t d) { return prefix
 cudaError_t launch_prefix_attn(const Attn &p, const void *plan, int64_t NG, int64_t d, void *ws, cudaStream_t s) {
     const PfRun x = prefix_run(p, NG, d);
     const int64_t es = p.qt == GGUF_F32 ? 4 : 2;
+    if (x.alone) {
+        Attn one = p;
+        one.q_start = (const int32_t *)plan + pf_lengths_at(p.R, NG, p.n_tokens);
+        one.kv_len = one.q_start + p.R + 1;
+        return launch_attn(one, d, ws, s);
+    }
     uint8_t *w = (uint8_t *)ws;
     AdShape a{};
     a.p = p;

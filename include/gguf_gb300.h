@@ -783,16 +783,17 @@ gguf_status gguf_prefix_plan(const int32_t *q_start, const int32_t *kv_len, int6
 /*
  * gguf_prefix_attention -- gguf_paged_attention for a batch whose requests share long
  * prefixes: the shared tokens of a group are read and unpacked once for the queries of all
- * its requests.  Where the rows of the block table list the same pages for the tokens that a
- * group shares, the outputs are gguf_paged_attention's (in other bits).
+ * its requests (a call whose requests can be had faster one by one, as its host arguments
+ * bound them, goes so).  Every row of the block table lists all pages of its request, the
+ * shared ones too; the outputs are gguf_paged_attention's on this table, in other bits.
  *   args : as gguf_paged_attention; q_start and kv_len are not looked at (they are in the
- *          plan).  max_q_len only chooses kernels: all queries are computed.
+ *          plan).  The table's width decides, with the other sizes, whether the shared tokens
+ *          are read together: one much wider than the requests need costs short calls time.
  *   plan : made by gguf_prefix_plan, on this stream or complete, with these n_requests,
  *          n_groups, n_tokens and page_size: plan_bytes, at least gguf_prefix_plan_bytes of
- *          them.  A plan of other sizes is not used: nothing is written, and dev_status
- *          counts 1.
+ *          them.  A plan of other sizes gives unspecified outputs.
  *   dev_status : + pages outside the cache or past the table, each once per request whose
- *          own tokens, or once per group whose shared ones, would be seen in it.
+ *          queries would see a token of it, or once for the requests of a group together.
  *   ws   : gguf_prefix_attention_ws_size(args, n_groups) bytes, 16-byte aligned: about
  *          8 (head_dim + 4) bytes per token and head, and up to 32 MB.
  * n_tokens x n_heads <= 2^30 (GGUF_ERR_SHAPE above).  Precision, windows, blocks that are not

@@ -10,10 +10,10 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda"
 
 
-def batch(groups, h, hk, d, page, typ, seed=0, peaky=2.0, own_rows=True):
+def batch(groups, h, hk, d, page, typ, seed=0, peaky=2.0, wide=True):
     """groups: (shared tokens or None for requests outside every group, [(queries, tokens of the whole request), ..]).
-    Slots that hold no token are full of NaN scales.  own_rows: every row of the table lists the shared pages; else only the
-    first request's of a group does."""
+    Slots that hold no token are full of NaN scales.  wide: a table of so many columns that the library reads the shared
+    tokens together; else one of the requests' own width, with which short requests go one by one."""
     gen = torch.Generator(device=DEV).manual_seed(seed)
     rnd = np.random.default_rng(seed)
     q_lens, kv_lens, starts, prefix, plans = [], [], [], [], []
@@ -37,7 +37,7 @@ def batch(groups, h, hk, d, page, typ, seed=0, peaky=2.0, own_rows=True):
         if m == 0 and group >= 0:
             table[r, :whole] = order[at:at + whole]
             at += whole
-        elif group >= 0 and own_rows:
+        elif group >= 0:
             table[r, :whole] = table[leader, :whole]
         n = max(0, counts[r] - (whole if group >= 0 else 0))
         first = whole if group >= 0 else 0
@@ -62,6 +62,8 @@ def batch(groups, h, hk, d, page, typ, seed=0, peaky=2.0, own_rows=True):
                             cache=cache, slots=stored, page_size=page)
     q = (torch.randn(sum(q_lens), h, d, generator=gen, device=DEV) * peaky).to(DTYPES[typ])
     ints = lambda a: torch.tensor(np.asarray(a, dtype=np.int32), device=DEV)   # noqa: E731
+    if wide:   # 200000 tiles of heads of 64 and 8 rows, as the rule counts them, take more than it gives a call one by one
+        table = np.pad(table, ((0, 0), (0, 200000 * 16 // (page * hk * len(q_lens)) + 1)), constant_values=-1)
     return dict(q=q, cache=cache, table=ints(table), start=ints(np.r_[0, np.cumsum(q_lens)]), kv_len=ints(kv_lens), gs=ints(starts),
                 prefix=ints(prefix), hk=hk, page=page, slots=slots, q_lens=q_lens, kv_lens=kv_lens, scale=d ** -0.5)
 
@@ -136,11 +138,11 @@ CASES = [
 ]
 
 
-@pytest.mark.parametrize("own_rows", [True, False])
+@pytest.mark.parametrize("wide", [True, False])
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(x).replace(" ", "")[:60] for x in c))
-def test_prefix_attention(case, own_rows):
+def test_prefix_attention(case, wide):
     groups, h, hk, d, page, typ, window, sinks = case
-    b = batch(groups, h, hk, d, page, typ, seed=h + d, own_rows=own_rows)
+    b = batch(groups, h, hk, d, page, typ, seed=h + d, wide=wide)
     refs = reference(b, window, sinks)
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
     most = max(b["q_lens"])
@@ -148,11 +150,11 @@ def test_prefix_attention(case, own_rows):
     check_attn(out, refs, typ)
     assert int(status.item()) == 0
     assert torch.equal(out, run(b, window, sinks))           # the same bits again
-    check_attn(run(b, window, sinks, max_q=1), refs, typ)    # max_q_len chooses kernels alone
-    check_attn(run(b, window, sinks, max_q=1000), refs, typ)
-    if own_rows:   # what gguf_paged_attention gives on the same table
-        check_attn(g.gguf_paged_attention(b["q"], b["cache"], b["table"], b["start"], b["kv_len"], hk, page, most, b["scale"],
-                                          window=window, sinks=sinks), refs, typ)
+    check_attn(run(b, window, sinks, max_q=1000), refs, typ)   # max_q_len chooses kernels
+    paged = g.gguf_paged_attention(b["q"], b["cache"], b["table"], b["start"], b["kv_len"], hk, page, most, b["scale"],
+                                   window=window, sinks=sinks)
+    check_attn(paged, refs, typ)
+    assert wide or torch.equal(out, paged)   # one by one they are the same kernels
 
 
 def plan_ref(start, kv, gs, prefix, page, n_tokens):
@@ -209,7 +211,9 @@ def test_plan(r, ng, seed):
                 assert a.tolist() == b.tolist()
             else:   # no queries: nothing else of it counts but the range of a request's tiles
                 assert a[1] == 0 and (a[2] == b[2] and a[7] == b[7])
-        assert np.array_equal(got[8 + 8 * (r + ng):].reshape(-1, 2), tokens)
+        at = 8 + 8 * (r + ng) + 2 * n_tokens
+        assert np.array_equal(got[8 + 8 * (r + ng):at].reshape(-1, 2), tokens)
+        assert np.array_equal(got[at:], np.r_[start, kv])
 
 
 def test_groups_out_of_range():
@@ -249,7 +253,8 @@ def test_more_queries_than_rows(typ):
         check_attn(got, [x[:held] for x in refs], typ)
 
 
-def test_another_plan_is_not_used():
+def test_another_plan():
+    """A plan of other sizes: where shared tokens are read together nothing is written, and it is counted."""
     b = batch([(64, ONE(70, 80, 90, 100, 77, 88))], 8, 2, 64, 16, "bf16")
     t = b["q"].shape[0]
     make = lambda page=16, n=t: g.gguf_prefix_plan(b["start"], b["kv_len"], b["gs"], b["prefix"], page, n)   # noqa: E731
@@ -271,7 +276,7 @@ def test_pages_outside_the_cache_are_counted_once(members, h, typ):
     """A page outside the cache hides its tokens: counted once for a group's shared page, once for a request's own."""
     b = batch([(96, [(1, 150)] * members), (None, ONE(40))], h, 1 if h == 4 else 2, 64, 32, typ)
     table = b["table"]
-    table[:members, 1] = 1 << 29                # of the group
+    table[:members, 1] = 1 << 29                # of the group, read together
     table[1, 3] = -1                            # of request 1's own tokens 96 ..
     table[members, 0] = b["cache"].shape[0]     # of the request outside
     see = [torch.ones(len(s), dtype=torch.bool) for s in b["slots"]]
@@ -293,10 +298,10 @@ def test_pages_outside_the_cache_are_counted_once(members, h, typ):
 
 def test_pages_past_the_table():
     b = batch([(96, [(1, 150)] * 9)], 8, 2, 64, 16, "bf16")
-    cut = {**b, "table": b["table"][:, :5].contiguous()}    # tokens 80 .. are not in it: one shared page, four own ones each
+    cut = {**b, "table": b["table"][:, :5].contiguous()}    # tokens 80 .. are not in it: one by one, five pages each
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
     got = run(cut, dev_status=status)
-    assert int(status.item()) == 1 + 9 * 4
+    assert int(status.item()) == 9 * 5
     short = {**b, "kv_lens": [80] * 9, "slots": [s[:80] for s in b["slots"]]}
     check_attn(got, reference(short), "bf16")
 

@@ -72,8 +72,9 @@ def test_mrope_nothing_to_do(lib):
 
 
 def test_prefix_plan_bytes(lib):
-    assert g.gguf_prefix_plan_bytes(0, 0, 0) == 32
-    assert g.gguf_prefix_plan_bytes(5, 2, 11) == 32 + 7 * 32 + 11 * 8
+    # a header, an entry per request and group, two words per token, the lengths
+    assert g.gguf_prefix_plan_bytes(0, 0, 0) == 32 + 4
+    assert g.gguf_prefix_plan_bytes(5, 2, 11) == 32 + 7 * 32 + 11 * 8 + 11 * 4
     for bad in ((-1, 0, 0), (0, -1, 0), (0, 0, -1), (16385, 0, 0), (0, 16385, 0), (0, 0, 1 << 31)):
         assert g.gguf_prefix_plan_bytes(*bad) == -1
 
@@ -89,7 +90,7 @@ def plan(lib, **kw):
     (dict(n=1 << 31), SHAPE), (dict(page=0), SHAPE), (dict(page=24), SHAPE), (dict(page=1 << 21), SHAPE), (dict(start=None), INVALID),
     (dict(kv=None), INVALID), (dict(group=None), INVALID), (dict(prefix=None), INVALID), (dict(plan=None), INVALID),
     (dict(start=258), ALIGN), (dict(kv=257), ALIGN), (dict(group=258), ALIGN), (dict(prefix=258), ALIGN), (dict(plan=264), ALIGN),
-    (dict(bytes=32 + 6 * 32 + 8 * 8 - 1), WS)])
+    (dict(bytes=32 + 6 * 32 + 8 * 8 + 9 * 4 - 1), WS)])
 def test_prefix_plan_refusals(lib, kw, want):
     assert plan(lib, **kw) == want
     assert b"prefix_plan" in lib.gguf_last_error()
@@ -109,7 +110,7 @@ def prefix(lib, plan=256, plan_bytes=1 << 20, ng=2, ws=256, ws_bytes=1 << 40, **
     (dict(page_size=20), SHAPE), (dict(n_kv_heads=3), SHAPE), (dict(n_requests=16385), SHAPE), (dict(max_q_len=0), INVALID),
     (dict(n_tokens=(1 << 27) + 1), SHAPE), (dict(ldq=1000), INVALID), (dict(ldo=1000), INVALID), (dict(ld_table=3), INVALID),
     (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID), (dict(q=None), INVALID), (dict(out=None), INVALID),
-    (dict(plan=None), INVALID), (dict(plan_bytes=32 + 6 * 32 + 4 * 8 - 1), WS), (dict(cache=None), INVALID), (dict(block_table=None), INVALID), (dict(plan=264), ALIGN),
+    (dict(plan=None), INVALID), (dict(plan_bytes=32 + 6 * 32 + 4 * 8 + 9 * 4 - 1), WS), (dict(cache=None), INVALID), (dict(block_table=None), INVALID), (dict(plan=264), ALIGN),
     (dict(q=257), ALIGN), (dict(out=257), ALIGN), (dict(cache=264), ALIGN), (dict(block_table=258), ALIGN), (dict(dev_status=258), ALIGN)])
 def test_prefix_attention_refusals(lib, kw, want):
     assert prefix(lib, **kw) == want
