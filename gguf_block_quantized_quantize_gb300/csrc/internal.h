@@ -231,7 +231,6 @@ cudaError_t launch_kv_plan(const KvPlan &p, cudaStream_t s);
 struct QkRope {   // gguf_qk_norm_rope and gguf_qk_norm_mrope
     const void *q, *k, *v;
     int64_t ldq, ldk, ldv, n_tokens, h, hk;
-    int64_t rows;   // rows of a token to norm and rotate: h queries, then the keys
     const float *qw, *kw;
     float eps;
     const int32_t *pos;

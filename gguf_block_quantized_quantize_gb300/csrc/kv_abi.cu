@@ -63,7 +63,7 @@ static gguf_status qk_norm_rope(const gguf_qk_rope_args *a, const gguf_rope_axes
     if (!at(a->q_norm, 16) || !at(a->k_norm, 16) || !at(a->cos_sin, 16) || !at(a->cache, 16))
         return refuse(GGUF_ERR_ALIGNMENT, "%s: q_norm, k_norm, cos_sin and cache must be 16-byte aligned", what);
     QkRope p{a->q, a->k, a->v, a->ldq, a->ldk, a->ldv, a->n_tokens, a->n_heads, hk,
-                   a->n_heads + hk, a->q_norm, a->k_norm, a->eps, a->positions,
+             a->q_norm, a->k_norm, a->eps, a->positions,
                    a->cos_sin, a->rot > 0 ? a->n_positions : INT64_MAX, (int)a->rot, a->rope_type == GGUF_ROPE_NEOX, a->q_out, a->k_out,
                    a->ldqo, a->ldko, (uint8_t *)a->cache, a->n_pages, a->page_size, a->slots, a->dev_status, 1, 0, {}};
     if (axes) {
