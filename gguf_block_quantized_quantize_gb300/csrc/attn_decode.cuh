@@ -90,18 +90,16 @@ struct PfEntry {
     int32_t group;             // of a request: its group's entry, -1 for none
 };
 // gguf_prefix_attention: what its kernels have beside AdShape's members.  A query row (token and head) has a record of
-// PfStride<D> floats, its output, maximum and sum, for its request's own tiles and, n_tokens x heads records later, one
-// for its group's: of the first piece of its unit.  The rest of the unit's tiles went to the warps (decode kernel) or CTAs
-// (prefill kernel) that follow in the sequence; each has one slot, of rows like records, for a unit that began before it.
+// PfStride<D> floats for its request's own tiles and, n_tokens x heads records later, one for its group's: output, maximum
+// and sum of the first piece of its unit, the slot of the next piece and how many follow (as int32).  The rest of the unit's
+// tiles went to the warps (decode kernel) or CTAs (prefill kernel) that follow in the sequence; each has one slot, of rows
+// like records, for a unit that began before it.
 struct PfShape {
     const int32_t *plan;       // header, entries, of each token its position, and its request and group (pf_pack), q_start, kv_len
     int32_t n_entries, chained;   // chained: the decode kernel follows the prefill kernel of the call
+    int32_t parts, pieces;     // slots of the decode kernel, of the prefill kernel
     float *records;
-    int64_t *base;             // tiles (decode kernel) or blocks (prefill kernel) before each entry's, of the kernel that takes it
-    int64_t *share;            // tiles of a CTA (decode kernel), blocks of a CTA (prefill kernel), tiles of a warp, warps with tiles
 };
-// warps of a CTA that have tiles
-__device__ __forceinline__ int pf_warps(int64_t share, int64_t per_warp) { return (int)ad_div(share + per_warp - 1, per_warp); }
 constexpr int PF_HEADER = 8, PF_MAGIC = 0x50465831;   // {magic, requests, groups, tokens, page size, 0, 0, 0}
 template <int D> struct PfStride { static constexpr int64_t value = D + 4; };   // 16-byte steps
 
@@ -419,20 +417,17 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             total += warp_sum[w];
         }
     }
-    const int64_t share = !PRE && a.whole ? 1 : ad_div(total + gridDim.x - 1, gridDim.x);
+    // (PRE: the same for every warp, and a step's tiles at least)
+    const int64_t even = PRE ? max((int64_t)TP, ad_div(total + gridDim.x * C::WARPS - 1, gridDim.x * C::WARPS)) : 0;
+    const int64_t share = PRE ? even * C::WARPS : a.whole ? 1 : ad_div(total + gridDim.x - 1, gridDim.x);
     int64_t cta0 = min(total, (int64_t)blockIdx.x * share), cta1 = min(total, cta0 + share);
-    int64_t per_warp = ad_div(cta1 - cta0 + C::WARPS - 1, C::WARPS);
-    if constexpr (PRE) {   // the same in all CTAs
-        per_warp = max((int64_t)1, ad_div(share + C::WARPS - 1, C::WARPS));
-        if (blockIdx.x == 0 && tid == 0) { a.pf.share[0] = share; a.pf.share[2] = per_warp; a.pf.share[3] = pf_warps(share, per_warp); }
-    }
+    int64_t per_warp = PRE ? even : ad_div(cta1 - cta0 + C::WARPS - 1, C::WARPS);
     for (int r = r0; r < r1; r++) {
         if (per > 1) {
             rq = ad_request_of<PRE>(a, r);
             if (PRE && !fits) rq.q = rq.nt = 0;
         }
         const int64_t units = ad_units(a, rq, RG), n = units * (!PRE && a.whole ? 1 : rq.nt);
-        if (PRE && blockIdx.x == 0 && rq.q > 0) a.pf.base[r] = before;
         if (before < cta1 && before + n > cta0) {
             if (!PRE && a.whole) {   // the CTA's unit: its tiles over the warps
                 const int share_w = (rq.nt + C::WARPS - 1) / C::WARPS, first = (int)(cta0 - before) * rq.nt;
@@ -882,8 +877,9 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             const bool unit_end = cur.tile == cur.q.nt;
             if constexpr (PRE) {   // rows of a unit that began here: their records; of one from the warp before: the warp's slot
                 const int64_t at = (cur.q.rows0 + (cur.r >= p.R ? p.n_tokens : 0)) * p.h + head0;
-                const int used = pf_warps(share, per_warp);
-                float *slot = a.part + (int64_t)(blockIdx.x * used + warp) * (RG * PfStride<D>::value);
+                const int mine = blockIdx.x * C::WARPS + warp;
+                float *slot = a.part + (int64_t)mine * (RG * PfStride<D>::value);
+                const int follow = (int)ad_div(cur.q.nt - seg_end + per_warp - 1, per_warp);
 #pragma unroll
                 for (int n = 0; n < NT; n++)
 #pragma unroll
@@ -896,7 +892,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                             for (int b = 0; b < NB; b++)
                                 *reinterpret_cast<float4 *>(to + 32 * b + 4 * g) =
                                     make_float4(o[b][0][n][j], o[b][0][n][2 + j], o[b][1][n][j], o[b][1][n][2 + j]);
-                            if (g == 0) *reinterpret_cast<float2 *>(to + D) = make_float2(m[n][j], lsum[n][j]);
+                            if (g == 0) *reinterpret_cast<float4 *>(to + D) = make_float4(m[n][j], lsum[n][j], __int_as_float(mine + 1), __int_as_float(follow));
                         }
                     }
             } else if (unit_end && began) {   // a whole unit

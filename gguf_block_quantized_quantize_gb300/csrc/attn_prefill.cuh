@@ -76,6 +76,7 @@ struct ApItem {
     int nt, n_sink, w_tile;       // the tiles that the rows see (see AdReq): the piece takes those from base to nt
     int base;
     int part;                     // its place among the partial results where the row block's tiles are cut, else -1
+    int follow;                   // (PRE) CTAs that take the row block's blocks after these
     int first, pos_max;           // (PRE) 1: the piece with the row block's first tiles, of a request's own tiles; 2: of a
 };                                // group's; 0: another piece.  The entry's last position
 
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     __shared__ ApItem item;
     __shared__ int32_t part[2][AP_THREADS / 32], cut_rows, cut_pieces, cut_from;
     __shared__ int32_t chunk_end[AP_THREADS];   // at most (tokens x heads / 128) items: 31 bits
-    __shared__ int64_t pre_sum[AP_THREADS / 32];   // (PRE) blocks
+    __shared__ int64_t pre_sum[AP_THREADS / 32], pre_share;   // (PRE) blocks
     __shared__ ApPlace place[1];   // thread 0's
     volatile int32_t *abort_flag = &abort_word;
     const Attn &p = a.p;
@@ -362,12 +363,11 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         // the CTA's blocks of the sequence; the thread that holds the entry of the first one writes it down
         const int64_t share = ad_div(pre_total + gridDim.x - 1, gridDim.x), own0 = min(pre_total, (int64_t)blockIdx.x * share);
         own = (int)(min(pre_total, own0 + share) - own0);
-        if (blockIdx.x == 0 && tid == 0) a.pf.share[1] = share;
+        if (tid == 0) pre_share = share;
         for (int r = tid * per; mine > 0 && r < min(R, (tid + 1) * per); r++) {
             const AdReq q = pf_request(a, r);
             const int nblk = blocks_of(q);
             const int64_t n = (int64_t)ap_items(a, q, ROWS) * nblk;
-            if (blockIdx.x == 0 && q.q > 0) a.pf.base[r] = before;   // for the join
             if (own > 0 && before <= own0 && own0 < before + n) {
                 const int unit = (int)ad_div(own0 - before, nblk);
                 place[0] = ApPlace{r, unit, (int)(own0 - before - (int64_t)unit * nblk), q};
@@ -472,6 +472,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             w.part = -1;
             w.first = at.blk > 0 ? 0 : at.entry >= p.R ? 2 : 1;
             w.pos_max = at.q.pos_max;
+            w.follow = (int)ad_div(nblk - at.blk - left + pre_share - 1, pre_share);
             item = w;
             // the next one
             at.blk = 0;
@@ -814,7 +815,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                         }
                     }
                     if constexpr (PRE) {
-                        if (there) *reinterpret_cast<float4 *>(rec + D) = make_float4(ref, lsum, 0.0f, 0.0f);
+                        if (there) *reinterpret_cast<float4 *>(rec + D) = make_float4(ref, lsum, __int_as_float(blockIdx.x + 1), __int_as_float(item.follow));
                         tc::fence_proxy_async_smem();
                         __syncwarp();
                         // the rows of a token lie side by side among the records, all rows among the slots: a copy for each run

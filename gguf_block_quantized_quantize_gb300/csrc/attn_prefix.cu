@@ -19,8 +19,7 @@
 // from the plan, and leaves (m, l, O) in fp32: a record per query row for the first
 // piece of its unit, a slot per warp or CTA for a unit that goes on from the one before.  The
 // second kernel starts as the first one's CTAs end, without waiting for its results.
-// The join takes a warp per query row, which works out from the cut where its pieces
-// lie.
+// The join takes a warp per query row; its record says where the other pieces lie.
 #include <algorithm>
 
 #include "attn_decode.cuh"
@@ -189,29 +188,24 @@ struct PfPieces {
     const float *first, *slot;
     int64_t step;
     int n;
-    __device__ __forceinline__ const float *at(int i) const { return i == 0 ? first : slot + i * step; }
+    __device__ __forceinline__ const float *at(int i) const { return i == 0 ? first : slot + (i - 1) * step; }
 };
+// next: what the record says of them; it was written if the entry has queries and tiles
 template <int D>
-__device__ __forceinline__ PfPieces pf_pieces(const AdShape &a, const AdReq &q, bool group, int64_t base, const int64_t (&shares)[4],
-                                              int64_t t, int head, int few, int rg) {
+__device__ __forceinline__ PfPieces pf_pieces(const AdShape &a, const AdReq &q, const float *record, float2 next, int64_t t, int head,
+                                              int few, int rg) {
     constexpr int64_t RS = PfStride<D>::value;
-    constexpr int ROWS = D == 256 ? 128 : 256, BTILES = D == 256 ? 4 : 8;   // the prefill kernel's (ApCfg)
     PfPieces x{};
     if (q.nt == 0 || t < q.rows0 || t >= (int64_t)q.rows0 + q.q) return x;
-    const int kh = head / a.G, row = (int)(t - q.rows0) * a.G + head - kh * a.G;
     const bool tc = (int64_t)q.q * a.G > few;
-    const int rows = tc ? ROWS : rg, n = tc ? (q.nt + BTILES - 1) / BTILES : q.nt, block = row / rows;
-    const int64_t from = base + ((int64_t)block * a.hk + kh) * n;
-    // the CTA, or the warp of a CTA, that a tile or block of the sequence went to
-    auto taker = [&](int64_t i) {
-        const int64_t cta = ad_div(i, shares[tc]);
-        return tc ? cta : cta * shares[3] + ad_div(i - cta * shares[0], shares[2]);
-    };
-    const int64_t c0 = taker(from);
-    x.n = (int)(taker(from + n - 1) - c0) + 1;
-    x.first = a.pf.records + ((t + (group ? a.p.n_tokens : 0)) * a.p.h + head) * RS;
+    const int rows = tc ? (D == 256 ? 128 : 256) : rg;   // of a unit, a power of two: the prefill kernel's (ApCfg), or rg
+    const int in = ((int)(t - q.rows0) * a.G + head % a.G) & (rows - 1);
+    // (a kernel that gave up a wait leaves records unwritten: no slot is read that is not there)
+    const int slots = tc ? a.pf.pieces : a.pf.parts, slot = min(max(__float_as_int(next.x), 0), slots);
+    x.first = record;
+    x.n = 1 + min(max(__float_as_int(next.y), 0), slots - slot);
     x.step = rows * RS;
-    x.slot = (tc ? a.pieces : a.part) + c0 * x.step + (row - block * rows) * RS;
+    x.slot = (tc ? a.pieces : a.part) + slot * x.step + in * RS;
     return x;
 }
 
@@ -225,8 +219,11 @@ __global__ void __launch_bounds__(PF_THREADS) prefix_join_kernel(const AdShape a
     const Attn &p = a.p;
     const int64_t w = ((int64_t)blockIdx.x * PF_THREADS + threadIdx.x) >> 5, t = (uint64_t)w >> 31 ? w / p.h : (int64_t)((uint32_t)w / (uint32_t)p.h);
     const int head = (int)(w - t * p.h), lane = threadIdx.x & 31;
-    const int2 at_rg = pf_unpack(t < p.n_tokens ? pf_token(a.pf, t).y : -1);
-    const int64_t shares[4] = {a.pf.share[0], a.pf.share[1], a.pf.share[2], a.pf.share[3]};
+    if (t >= p.n_tokens) return;
+    constexpr int64_t RS = PfStride<D>::value;
+    const float *own = a.pf.records + (t * p.h + head) * RS, *shared = own + p.n_tokens * p.h * RS;
+    const float2 own_next = *reinterpret_cast<const float2 *>(own + D + 2), shared_next = *reinterpret_cast<const float2 *>(shared + D + 2);
+    const int2 at_rg = pf_unpack(pf_token(a.pf, t).y);
     if (!pf_plan_fits(a)) {
         if (w == 0 && lane == 0 && p.status != nullptr) atomicAdd(p.status, 1);
         return;
@@ -234,13 +231,11 @@ __global__ void __launch_bounds__(PF_THREADS) prefix_join_kernel(const AdShape a
     const int r = at_rg.x, ge = (int)p.R + at_rg.y;
     if (r < 0 || r >= p.R) return;
     const bool grouped = ge >= p.R && ge < a.pf.n_entries;
-    const int e1 = grouped ? ge : r;
-    const int64_t base0 = a.pf.base[r], base1 = a.pf.base[e1];
-    const AdReq q0 = pf_request(a, r), q1 = pf_request(a, e1);
+    const AdReq q0 = pf_request(a, r), q1 = pf_request(a, grouped ? ge : r);
     PfPieces x[2];
-    x[0] = pf_pieces<D>(a, q0, false, base0, shares, t, head, few, rg);
+    x[0] = pf_pieces<D>(a, q0, own, own_next, t, head, few, rg);
     x[1] = PfPieces{};
-    if (grouped) x[1] = pf_pieces<D>(a, q1, true, base1, shares, t, head, few, rg);
+    if (grouped) x[1] = pf_pieces<D>(a, q1, shared, shared_next, t, head, few, rg);
     const int n = x[0].n + x[1].n;
     float mx = -INFINITY, l = 0.0f, v[PL * W];
 #pragma unroll
@@ -307,7 +302,7 @@ struct PfRun {
     int ctas;
     bool tc;           // the tensor-core kernel runs
     int few, rg;       // entries of at most `few` query rows per KV head, in units of rg rows, go to the other one
-    size_t base, share, records, part, pieces, bytes;   // offsets in the workspace
+    size_t part, pieces, bytes;   // offsets in the workspace behind the records, and its size
 };
 static PfRun prefix_run(const Attn &p, int64_t NG, int64_t d) {
     PfRun x{};
@@ -334,9 +329,7 @@ static PfRun prefix_run(const Attn &p, int64_t NG, int64_t d) {
     }
     auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
     const size_t rs = (size_t)(d + 4) * 4;
-    x.share = up((size_t)(p.R + NG) * 8);
-    x.records = x.share + 256;
-    x.part = up(x.records + 2 * (size_t)p.n_tokens * p.h * rs);
+    x.part = up(2 * (size_t)p.n_tokens * p.h * rs);
     x.pieces = up(x.part + (size_t)x.ctas * ad_warps((int)d, p.qt == GGUF_F32, x.rg / 8) * x.rg * rs);
     x.bytes = x.tc ? x.pieces + (size_t)x.ctas * (d == 256 ? 128 : 256) * rs : x.pieces;
     return x;
@@ -368,7 +361,7 @@ cudaError_t launch_prefix_attn(const Attn &p, const void *plan, int64_t NG, int6
             p.ldo * es % 16 == 0;
     a.part = (float *)(w + x.part);
     a.pieces = (float *)(w + x.pieces);
-    a.pf = PfShape{(const int32_t *)plan, (int32_t)(p.R + NG), x.tc, (float *)(w + x.records), (int64_t *)w, (int64_t *)(w + x.share)};
+    a.pf = PfShape{(const int32_t *)plan, (int32_t)(p.R + NG), x.tc, x.ctas * ad_warps((int)d, p.qt == GGUF_F32, x.rg / 8), x.ctas, (float *)ws};
     a.min_rows = x.few;
     a.max_rows = 0x7fffffff;
     if (x.tc) {
