@@ -55,7 +55,7 @@ class Layer:
         t = h.shape[0]
         start, kv_len, pos, slots, used = g.gguf_kv_plan(self.ctx, new_len, self.free, self.table, PAGE, t, dev_status=self.status)
         if positions is None:
-            positions = pos.expand(3, t).contiguous()
+            positions = pos.expand(3, t)
         _, _, xq = g.gguf_block_norm(None, h, pre_weight=self.norm, q8_1=True)
         qkv = torch.empty(t, (HEADS + 2 * KV_HEADS) * DIM, dtype=h.dtype, device=h.device)
         nq, nk = HEADS * DIM, KV_HEADS * DIM

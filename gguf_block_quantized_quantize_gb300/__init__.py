@@ -531,6 +531,12 @@ def _bound():
     return _native
 
 
+def _here(t: torch.Tensor, what: str):
+    """The launches go to the current device; its tensors are the ones that they may read."""
+    if t.is_cuda and t.device.index != _DEVICE():
+        raise ValueError(f"{what}: the tensors live on {t.device}, which is not the current device")
+
+
 def gguf_kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
                  page_size: int, n_tokens: int, out=None, dev_status: torch.Tensor | None = None):
     """Block tables, slots and positions of a step from its requests' lengths (one launch, no host sync).
@@ -575,6 +581,7 @@ def gguf_qk_norm_mrope(q: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor 
                        k_out: torch.Tensor | None = None, dev_status: torch.Tensor | None = None) -> torch.Tensor:
     """gguf_qk_norm_rope with ``positions`` [axes, t] on up to 4 axes (time, height, width): ``sections`` gives the
     rotated pairs of each axis (rot / 2 together), one section after another or, ``interleaved``, in turn."""
+    _here(q, "gguf_qk_norm_mrope")
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     st = _bound().qk_norm_mrope(q, k, v, q_norm, k_norm, eps, positions, cos_sin, rope_type, cache, slots, page_size, q_out,
@@ -603,6 +610,7 @@ def gguf_block_norm(x: torch.Tensor | None, residual: torch.Tensor | None, *, ga
     a = x if x is not None else residual
     if a is None:
         raise ValueError("gguf_block_norm: x or residual must be given")
+    _here(a, "gguf_block_norm")
     if residual_out is None and x is not None:
         residual_out = torch.empty(a.shape, dtype=a.dtype if residual is None else residual.dtype, device=a.device)
     if out is None and out_q8_1 is None and not q8_1:
@@ -658,6 +666,7 @@ def gguf_prefix_plan(q_start: torch.Tensor, kv_len: torch.Tensor, group_start: t
     """What the requests of a step share, for gguf_prefix_attention (one launch, no host sync; once for all layers):
     group g is requests group_start[g] .. group_start[g + 1] - 1, which have their first prefix_len[g] tokens in
     common.  ``n_tokens``: the rows of q.  Returns the plan (``out``: uint8, at least gguf_prefix_plan_bytes)."""
+    _here(kv_len, "gguf_prefix_plan")
     if out is None:
         out = torch.empty(max(gguf_prefix_plan_bytes(kv_len.numel(), prefix_len.numel(), n_tokens), 0), dtype=torch.uint8,
                           device=kv_len.device)
@@ -673,6 +682,7 @@ def gguf_prefix_attention(q: torch.Tensor, cache: torch.Tensor, block_table: tor
                           ws: torch.Tensor | None = None, dev_status: torch.Tensor | None = None) -> torch.Tensor:
     """gguf_paged_attention with the pages that the requests of a group share read once for all of them (see
     include/gguf_gb300.h).  ``block_table`` has a row per request of the plan."""
+    _here(q, "gguf_prefix_attention")
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     call = _bound().prefix_attention

@@ -69,6 +69,7 @@ __device__ __forceinline__ PfGroup pf_group(const PfPlanArgs &p, int64_t g) {
 }
 // the group with which a request shares tiles, or -1
 __device__ __forceinline__ int pf_group_of(const PfPlanArgs &p, int64_t r) {
+    if (p.NG == 0) return -1;   // (and there may be no arrays)
     const int64_t g = last_up_to(p.group_start, p.NG + 1, r);
     if (g < 0 || g >= p.NG) return -1;
     const PfGroup in = pf_group(p, g);

@@ -52,6 +52,7 @@ struct Bad {};   // a Python exception is set
     PyErr_Format(PyExc_ValueError, "%s: %s must be %s", what, name, want);
     throw Bad();
 }
+thread_local int device_of_call = -1;   // of the call's first tensor
 const at::Tensor &tensor(PyObject *o, const char *what, const char *name) {
     if (!THPVariable_Check(o)) refuse(what, name, "a tensor");
     const at::Tensor &t = THPVariable_Unpack(o);
@@ -59,6 +60,8 @@ const at::Tensor &tensor(PyObject *o, const char *what, const char *name) {
         PyErr_SetString(PyExc_ValueError, "gguf: tensors must live on a CUDA device");
         throw Bad();
     }
+    if (device_of_call < 0) device_of_call = t.get_device();
+    if (t.get_device() != device_of_call) refuse(what, name, "on the device of the call's other tensors");
     return t;
 }
 int64_t integer(PyObject *o) {
@@ -147,6 +150,7 @@ void count(Py_ssize_t n, Py_ssize_t want, const char *what) {
 }
 template <class F>
 PyObject *guarded(F f) {
+    device_of_call = -1;
     try {
         return f();
     } catch (const Bad &) {

@@ -47,7 +47,7 @@ static gguf_status qk_norm_rope(const gguf_qk_rope_args *a, const gguf_rope_axes
         if (pairs != a->rot / 2)
             return refuse(GGUF_ERR_SHAPE, "%s: the sections hold %lld pairs, rot=%lld has %lld", what, (long long)pairs, (long long)a->rot,
                           (long long)(a->rot / 2));
-        if (axes->n_axes > 1 && axes->ld_positions < a->n_tokens)
+        if (axes->n_axes > 1 && axes->ld_positions != 0 && axes->ld_positions < a->n_tokens)
             return refuse(GGUF_ERR_INVALID_ARG, "%s: ld_positions=%lld < n_tokens", what, (long long)axes->ld_positions);
     }
     if (a->ldq < a->n_heads * d || a->ldqo < a->n_heads * d || (keys && a->ldk < hk * d) ||
@@ -256,6 +256,10 @@ static gguf_status check_prefix_sizes(const gguf_attn_args *a, int64_t n_groups)
     gguf_status st = check_attn_sizes(a, "prefix_attention");
     if (st == GGUF_OK) st = check_plan_sizes(a->n_requests, n_groups, a->n_tokens, "prefix_attention");
     if (st != GGUF_OK) return st;
+    // the tiles of all units are shared out over SMs and warps, whose parts are counted in 31 bits
+    const double units = (double)a->n_tokens * (double)(a->n_heads / a->n_kv_heads) / 8.0 + (double)(a->n_requests + n_groups);
+    if (units * (double)a->n_kv_heads * (double)a->width * (double)(a->page_size / KV_TILE) > 0x1p40)
+        return report(GGUF_ERR_SHAPE, "prefix_attention: too many queries over too wide a table for one call; split it");
     if (a->n_tokens * a->n_heads > (1 << 30))   // records are counted in 31 bits, two a query row
         return refuse(GGUF_ERR_SHAPE, "prefix_attention: %lld tokens x %lld heads (at most 2^30)", (long long)a->n_tokens, (long long)a->n_heads);
     return GGUF_OK;

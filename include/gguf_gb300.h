@@ -669,7 +669,7 @@ gguf_status gguf_qk_norm_rope(const gguf_qk_rope_args *args, gguf_stream_t strea
  * gguf_qk_norm_mrope -- gguf_qk_norm_rope for tokens with positions on several
  * axes (text, images and video: time, height, width): each of the rot / 2 pairs
  * turns by its angle at the token's position on one of the axes.
- *   args->positions : [n_axes][ld_positions] int32.  A token that is negative on
+ *   args->positions : [n_axes][ld_positions] int32 (ld_positions = 0: one row for all axes).  A token that is negative on
  *                     any axis is left out as padding; one that is at or past
  *                     n_positions on any is left out and counted, once.
  *   sections        : pairs of each axis; together rot / 2.
@@ -796,7 +796,8 @@ gguf_status gguf_prefix_plan(const int32_t *q_start, const int32_t *kv_len, int6
  *          queries would see a token of it, or once for the requests of a group together.
  *   ws   : gguf_prefix_attention_ws_size(args, n_groups) bytes, 16-byte aligned: about
  *          8 (head_dim + 4) bytes per token and head, and up to 32 MB.
- * n_tokens x n_heads <= 2^30 (GGUF_ERR_SHAPE above).  Precision, windows, blocks that are not
+ * n_tokens x n_heads <= 2^30, and 2^40 tiles of 16 tokens under all groups of 8 query rows
+ * (GGUF_ERR_SHAPE above).  Precision, windows, blocks that are not
  * finite (which may reach the queries of their group) and timeouts are as described at
  * gguf_paged_attention; the bits of a request's outputs depend on the batch.  Made for few
  * queries per request (decoding, tokens to check): long chunks of prompts go through, but

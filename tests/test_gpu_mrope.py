@@ -124,6 +124,10 @@ def test_equal_positions_are_one_axis(d, typ, sections, interleaved, neox):
                              cache=caches[0], slots=slots.to(DEV), page_size=page)
     b = g.gguf_qk_norm_rope(q, k, v, w, w, EPS, one, table.to(DEV), kind, cache=caches[1], slots=slots.to(DEV), page_size=page)
     assert torch.equal(a, b) and torch.equal(caches[0], caches[1])
+    # one row of positions for all axes
+    c = g.gguf_qk_norm_mrope(q, k, v, w, w, EPS, one.expand(len(sections), t), table.to(DEV), sections, interleaved, kind,
+                             cache=torch.zeros_like(caches[0]), slots=slots.to(DEV), page_size=page)
+    assert torch.equal(c, b)
     # queries alone, in place
     got = q.contiguous()
     assert g.gguf_qk_norm_mrope(got, None, None, w, None, EPS, one.expand(len(sections), t).contiguous(), table.to(DEV), sections,

@@ -369,5 +369,28 @@ def test_no_groups():
     assert run(empty).shape[0] == 0
 
 
+def test_no_groups_and_no_arrays():
+    """The C call without groups needs no arrays of them."""
+    b = batch([(None, ONE(100, 200, 33, 700))], 8, 2, 64, 16, "bf16")
+    t = b["q"].shape[0]
+    plan = torch.empty(g.gguf_prefix_plan_bytes(4, 0, t), dtype=torch.uint8, device=DEV)
+    st = g.load_library().gguf_prefix_plan(b["start"].data_ptr(), b["kv_len"].data_ptr(), 4, None, None, 0, 16, t, plan.data_ptr(),
+                                           plan.numel(), torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    out = g.gguf_prefix_attention(b["q"], b["cache"], b["table"], plan, 0, 2, 16, 1, b["scale"])
+    check_attn(out, reference(b), "bf16")
+
+
+def test_another_device_is_refused(monkeypatch):
+    b = batch([(64, ONE(70, 80, 90))], 8, 2, 64, 16, "bf16")
+    monkeypatch.setattr(g, "_DEVICE", lambda: 7)
+    x = torch.randn(4, 64, device=DEV)
+    for call in (lambda: run(b), lambda: g.gguf_block_norm(x, x),
+                 lambda: g.gguf_qk_norm_mrope(x.view(4, 1, 64), None, None, None, None, 1e-6, torch.zeros(2, 4, dtype=torch.int32, device=DEV),
+                                              None, (0, 0))):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+
+
 def test_no_device_errors():
     assert g.gguf_device_errors() == 0

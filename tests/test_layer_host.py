@@ -57,7 +57,7 @@ def mrope(lib, sections=(16, 24, 24), n_axes=3, ld=4, interleaved=0, axes=True, 
 
 @pytest.mark.parametrize("kw, want", [
     (dict(axes=False), INVALID), (dict(n_axes=0), SHAPE), (dict(n_axes=5), SHAPE), (dict(n_axes=-1), SHAPE), (dict(n_axes=2), SHAPE),
-    (dict(sections=(16, 24, 25)), SHAPE), (dict(sections=(-16, 40, 40)), INVALID), (dict(rot=64), SHAPE), (dict(ld=3), INVALID),
+    (dict(sections=(16, 24, 25)), SHAPE), (dict(sections=(-16, 40, 40)), INVALID), (dict(rot=64), SHAPE), (dict(ld=3), INVALID), (dict(ld=-4), INVALID),
     (dict(sections=(0, 0, 0), rot=0, ld=-1), INVALID), (dict(xt=g.Q8_1), TYPE), (dict(head_dim=96), SHAPE), (dict(rot=24), SHAPE),
     (dict(positions=None), INVALID), (dict(cos_sin=None), INVALID), (dict(positions=258), ALIGN), (dict(cos_sin=260), ALIGN),
     (dict(rope_type=1), INVALID), (dict(ldq=1023), INVALID)])
@@ -108,7 +108,7 @@ def prefix(lib, plan=256, plan_bytes=1 << 20, ng=2, ws=256, ws_bytes=1 << 40, **
     (dict(qt=g.Q4_0), TYPE), (dict(n_tokens=-1), INVALID), (dict(n_requests=-1), INVALID), (dict(ng=-1), INVALID),
     (dict(ng=16385), SHAPE), (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(head_dim=80), SHAPE),
     (dict(page_size=20), SHAPE), (dict(n_kv_heads=3), SHAPE), (dict(n_requests=16385), SHAPE), (dict(max_q_len=0), INVALID),
-    (dict(n_tokens=(1 << 27) + 1), SHAPE), (dict(ldq=1000), INVALID), (dict(ldo=1000), INVALID), (dict(ld_table=3), INVALID),
+    (dict(n_tokens=(1 << 27) + 1), SHAPE), (dict(n_tokens=1 << 20, width=1 << 26, ld_table=1 << 26), SHAPE), (dict(ldq=1000), INVALID), (dict(ldo=1000), INVALID), (dict(ld_table=3), INVALID),
     (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID), (dict(q=None), INVALID), (dict(out=None), INVALID),
     (dict(plan=None), INVALID), (dict(plan_bytes=32 + 6 * 32 + 4 * 8 + 9 * 4 - 1), WS), (dict(cache=None), INVALID), (dict(block_table=None), INVALID), (dict(plan=264), ALIGN),
     (dict(q=257), ALIGN), (dict(out=257), ALIGN), (dict(cache=264), ALIGN), (dict(block_table=258), ALIGN), (dict(dev_status=258), ALIGN)])
