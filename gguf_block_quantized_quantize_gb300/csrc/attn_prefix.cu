@@ -53,7 +53,8 @@ __device__ __forceinline__ int64_t last_up_to(const int32_t *a, int64_t n, int64
     }
     return lo;
 }
-// the arrays that are searched, in shared memory where they fit: a search of 9 steps takes 300 cycles there, 5000 in the L2
+// the arrays of requests and groups, in shared memory where they fit: a search of 9 steps takes 300 cycles there, 5000 in the
+// L2, and what it finds is there too
 constexpr int PF_HELD = 2048;
 struct PfGroup {
     int64_t s, e;    // its requests
@@ -64,7 +65,8 @@ __device__ __forceinline__ PfGroup pf_group(const PfPlanArgs &p, int64_t g) {
     o.s = max((int64_t)p.group_start[g], (int64_t)0);
     o.e = min((int64_t)p.group_start[g + 1], p.R);
     // whole pages: the one that a prefix ends in holds tokens of a request's own, and is its own
-    o.tiles = o.e - o.s >= 2 ? (int32_t)(max(p.prefix_len[g], 0) / p.page * (p.page / KV_TILE)) : 0;
+    const uint32_t page = (uint32_t)p.page;
+    o.tiles = o.e - o.s >= 2 ? (int32_t)((uint32_t)max(p.prefix_len[g], 0) / page * (page / KV_TILE)) : 0;
     return o;
 }
 // the group with which a request shares tiles, or -1
@@ -88,15 +90,23 @@ constexpr int PF_THREADS = 256;
 __global__ void __launch_bounds__(PF_THREADS) prefix_plan_kernel(const PfPlanArgs args) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ int32_t held[2][PF_HELD];
+    __shared__ int32_t held[4][PF_HELD];
     PfPlanArgs p = args;
     if (p.R < PF_HELD) {
-        for (int i = threadIdx.x; i <= p.R; i += PF_THREADS) held[0][i] = p.q_start[i];
+        for (int i = threadIdx.x; i <= p.R; i += PF_THREADS) {
+            held[0][i] = p.q_start[i];
+            if (i < p.R) held[1][i] = p.kv_len[i];
+        }
         p.q_start = held[0];
+        p.kv_len = held[1];
     }
     if (p.NG > 0 && p.NG < PF_HELD) {
-        for (int i = threadIdx.x; i <= p.NG; i += PF_THREADS) held[1][i] = p.group_start[i];
-        p.group_start = held[1];
+        for (int i = threadIdx.x; i <= p.NG; i += PF_THREADS) {
+            held[2][i] = p.group_start[i];
+            if (i < p.NG) held[3][i] = p.prefix_len[i];
+        }
+        p.group_start = held[2];
+        p.prefix_len = held[3];
     }
     __syncthreads();
     const int64_t id = (int64_t)blockIdx.x * PF_THREADS + threadIdx.x;
@@ -210,11 +220,12 @@ __device__ __forceinline__ PfPieces pf_pieces(const AdShape &a, const AdReq &q, 
     return x;
 }
 
+constexpr int JOIN_MANY = 4;
 // Bound: the pieces' bytes, from the L2 mostly, and for few pieces the chain token, entry, pieces.  A warp per query row
 // takes AT_ONCE pieces at a time, so that their loads are under way together.
-template <int D, int QT>
+template <int D, int QT, int AT_ONCE>
 __global__ void __launch_bounds__(PF_THREADS) prefix_join_kernel(const AdShape a, const int few, const int rg) {
-    constexpr int AT_ONCE = 8, W = D == 64 ? 2 : 4, PL = D / 32 / W;   // values per load, loads per lane
+    constexpr int W = D == 64 ? 2 : 4, PL = D / 32 / W;   // values per load, loads per lane
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Attn &p = a.p;
@@ -290,11 +301,13 @@ __global__ void __launch_bounds__(PF_THREADS) prefix_join_kernel(const AdShape a
     }
 }
 
-template <int D>
+template <int D, int AT_ONCE>
 static const void *join_kernel(int qt) {
-    return qt == GGUF_F32 ? (const void *)prefix_join_kernel<D, GGUF_F32>
-         : qt == GGUF_F16 ? (const void *)prefix_join_kernel<D, GGUF_F16> : (const void *)prefix_join_kernel<D, GGUF_BF16>;
+    return qt == GGUF_F32 ? (const void *)prefix_join_kernel<D, GGUF_F32, AT_ONCE>
+         : qt == GGUF_F16 ? (const void *)prefix_join_kernel<D, GGUF_F16, AT_ONCE> : (const void *)prefix_join_kernel<D, GGUF_BF16, AT_ONCE>;
 }
+template <int D>
+static const void *join_kernel(int qt, bool many) { return many ? join_kernel<D, JOIN_MANY>(qt) : join_kernel<D, 8>(qt); }
 
 // ---------------------------------------------------------------- what a call runs
 
@@ -378,7 +391,8 @@ cudaError_t launch_prefix_attn(const Attn &p, const void *plan, int64_t NG, int6
     a.max_rows = 0x7fffffff;   // the join looks at all entries
     int few = x.few, rg = x.rg;
     void *args[3] = {&a, &few, &rg};
-    return launch_chained(d == 64 ? join_kernel<64>(p.qt) : d == 128 ? join_kernel<128>(p.qt) : join_kernel<256>(p.qt),
+    const bool many = p.n_tokens * p.h > 16 * device_info().sm_count;
+    return launch_chained(d == 64 ? join_kernel<64>(p.qt, many) : d == 128 ? join_kernel<128>(p.qt, many) : join_kernel<256>(p.qt, many),
                           (p.n_tokens * p.h + PF_THREADS / 32 - 1) / (PF_THREADS / 32), PF_THREADS, s, args);
 }
 
