@@ -526,7 +526,7 @@ def _bound():
         _bind.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "gguf_kv_plan", "gguf_qk_norm_rope", "gguf_kv_get_rows", "gguf_paged_attention_ws_size", "gguf_paged_attention",
             "gguf_kv_page_bytes", "gguf_qk_norm_mrope", "gguf_block_norm", "gguf_prefix_plan", "gguf_prefix_attention_ws_size",
-            "gguf_prefix_attention")))
+            "gguf_prefix_attention", "gguf_prefix_plan_bytes")))
         _native = _bind
     return _native
 
@@ -667,12 +667,9 @@ def gguf_prefix_plan(q_start: torch.Tensor, kv_len: torch.Tensor, group_start: t
     group g is requests group_start[g] .. group_start[g + 1] - 1, which have their first prefix_len[g] tokens in
     common.  ``n_tokens``: the rows of q.  Returns the plan (``out``: uint8, at least gguf_prefix_plan_bytes)."""
     _here(kv_len, "gguf_prefix_plan")
-    if out is None:
-        out = torch.empty(max(gguf_prefix_plan_bytes(kv_len.numel(), prefix_len.numel(), n_tokens), 0), dtype=torch.uint8,
-                          device=kv_len.device)
-    st = _bound().prefix_plan(q_start, kv_len, group_start, prefix_len, page_size, n_tokens, out, _stream())
-    if st:
-        _check(st)
+    out = _bound().prefix_plan(q_start, kv_len, group_start, prefix_len, page_size, n_tokens, out, _stream())
+    if out.__class__ is int:
+        _check(out)
     return out
 
 
@@ -683,17 +680,10 @@ def gguf_prefix_attention(q: torch.Tensor, cache: torch.Tensor, block_table: tor
     """gguf_paged_attention with the pages that the requests of a group share read once for all of them (see
     include/gguf_gb300.h).  ``block_table`` has a row per request of the plan."""
     _here(q, "gguf_prefix_attention")
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    call = _bound().prefix_attention
-    if ws is None:   # a caller's workspace is checked against the need by the library
-        need = call(q, cache, block_table, plan, n_groups, n_kv_heads, page_size, max_q_len, scale, window, sinks, out, 0,
-                    dev_status, 0)
-        ws = _workspace(need, q.device)
-    st = call(q, cache, block_table, plan, n_groups, n_kv_heads, page_size, max_q_len, scale, window, sinks, out, ws,
-              dev_status, _stream())
-    if st:
-        _check(st)
+    out = _bound().prefix_attention(q, cache, block_table, plan, n_groups, n_kv_heads, page_size, max_q_len, scale, window, sinks,
+                                    out, ws, dev_status, _stream())
+    if out.__class__ is int:
+        _check(out)
     return out
 
 

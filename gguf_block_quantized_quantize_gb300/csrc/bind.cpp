@@ -5,10 +5,14 @@
 // small call is larger than the GPU's: a call costs about 0.7 us here beside
 // the launch, and 5 to 10 us through ctypes.
 //
-// The functions take positional arguments, allocate nothing, and return the
-// status of the C function that they call (whose address bind() got), or raise
-// ValueError for a tensor that does not fit.
+// The functions take positional arguments and return the status of the C
+// function that they call (whose address bind() got), or raise ValueError for a
+// tensor that does not fit.  They allocate nothing, but prefix_plan and
+// prefix_attention: those make what they are not given (plan, output, workspace) in
+// the same call, and return the plan or the output instead of the status 0.
 #include <Python.h>
+
+#include <ATen/Functions.h>
 
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -44,6 +48,7 @@ struct {
     pplan_fn pplan;
     pattn_ws_fn pattn_ws;
     pattn_fn pattn;
+    page_fn pplan_bytes;
 } api;
 
 struct Bad {};   // a Python exception is set
@@ -422,51 +427,86 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// q_start, kv_len, group_start, prefix_len, page, n_tokens, plan, stream
+PyObject *status_or(gguf_status st, PyObject *made) {   // takes `made` over
+    if (st == GGUF_OK) return made;
+    Py_DECREF(made);
+    return PyLong_FromLong(st);
+}
+at::Tensor bytes_like(const at::Tensor &t, int64_t n) { return at::empty({n}, t.options().dtype(at::kByte)); }
+
+// q_start, kv_len, group_start, prefix_len, page, n_tokens, plan (None: it is made), stream
 PyObject *prefix_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
         const char *what = "gguf_prefix_plan";
         count(n, 8, what);
-        const int64_t r = tensor(a[1], what, "kv_len").numel(), groups = tensor(a[3], what, "prefix_len").numel();
-        const Bytes plan = bytes_or_none(a[6], what, "plan");
-        return PyLong_FromLong(api.pplan(array<int32_t>(a[0], r + 1, what, "q_start"), array<int32_t>(a[1], r, what, "kv_len"), r,
+        const at::Tensor &kv_len = tensor(a[1], what, "kv_len");
+        const int64_t r = kv_len.numel(), groups = tensor(a[3], what, "prefix_len").numel(), tokens = integer(a[5]);
+        at::Tensor made;
+        Bytes plan = bytes_or_none(a[6], what, "plan");
+        if (a[6] == Py_None) {
+            made = bytes_like(kv_len, std::max<int64_t>(api.pplan_bytes(r, groups, tokens), 0));   // (the library refuses the sizes itself)
+            plan = {made.data_ptr(), static_cast<size_t>(made.numel())};
+        }
+        const gguf_status st = api.pplan(array<int32_t>(a[0], r + 1, what, "q_start"), array<int32_t>(a[1], r, what, "kv_len"), r,
                                          array<int32_t>(a[2], groups + 1, what, "group_start"),
-                                         array<int32_t>(a[3], groups, what, "prefix_len"), groups, integer(a[4]), integer(a[5]), plan.p,
-                                         plan.n, stream(a[7])));
+                                         array<int32_t>(a[3], groups, what, "prefix_len"), groups, integer(a[4]), tokens, plan.p, plan.n,
+                                         stream(a[7]));
+        if (a[6] != Py_None) Py_INCREF(a[6]);
+        return status_or(st, a[6] != Py_None ? a[6] : THPVariable_Wrap(made));
     });
 }
 
-// q, cache, table, plan, n_groups, n_kv_heads, page, max_q_len, scale, window, sinks, out, ws, status, stream; ws as above
+// q, cache, table, plan, n_groups, n_kv_heads, page, max_q_len, scale, window, sinks, out, ws (None: they are made), status, stream
 PyObject *prefix_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
         const char *what = "gguf_prefix_attention";
         count(n, 15, what);
-        gguf_attn_args x = attn_args(a[0], a[1], a + 5, what);
+        PyObject *args[9] = {a[5], a[6], a[7], a[8], a[9], a[10], a[11], nullptr, a[13]};
+        struct Held {
+            PyObject *p;
+            ~Held() { Py_XDECREF(p); }
+        } out{a[11]};
+        if (a[11] == Py_None) {
+            const at::Tensor &q = tensor(a[0], what, "q");
+            out.p = THPVariable_Wrap(at::empty(q.sizes(), q.options()));
+        } else
+            Py_INCREF(out.p);
+        args[6] = out.p;
+        gguf_attn_args x = attn_args(a[0], a[1], args, what);
         const Table t = table(a[2], 0, what);
         x.n_requests = tensor(a[2], what, "block_table").size(0);
         x.block_table = t.p;
         x.ld_table = t.ld;
         x.width = t.width;
         const int64_t groups = integer(a[4]);
-        if (PyLong_Check(a[12])) return PyLong_FromSize_t(api.pattn_ws(&x, groups));
         const Bytes plan = bytes_or_none(a[3], what, "plan");
-        const Bytes w = bytes_or_none(a[12], what, "ws");
-        return PyLong_FromLong(api.pattn(&x, plan.p, plan.n, groups, w.p, w.n, stream(a[14])));
+        Bytes w = bytes_or_none(a[12], what, "ws");
+        at::Tensor made;
+        if (a[12] == Py_None) {
+            if (const size_t need = api.pattn_ws(&x, groups)) {
+                made = bytes_like(THPVariable_Unpack(a[0]), static_cast<int64_t>(need));
+                w = {made.data_ptr(), need};
+            }
+        }
+        const gguf_status st = api.pattn(&x, plan.p, plan.n, groups, w.p, w.n, stream(a[14]));
+        if (st != GGUF_OK) return PyLong_FromLong(st);
+        Py_INCREF(out.p);
+        return out.p;
     });
 }
 
 // the addresses of gguf_kv_plan, gguf_qk_norm_rope, gguf_kv_get_rows, gguf_paged_attention_ws_size, gguf_paged_attention,
-// gguf_kv_page_bytes, gguf_qk_norm_mrope, gguf_block_norm, gguf_prefix_plan, gguf_prefix_attention_ws_size and
-// gguf_prefix_attention
+// gguf_kv_page_bytes, gguf_qk_norm_mrope, gguf_block_norm, gguf_prefix_plan, gguf_prefix_attention_ws_size,
+// gguf_prefix_attention and gguf_prefix_plan_bytes
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
-        count(n, 11, "bind");
-        void *p[11];
-        for (int i = 0; i < 11; i++) p[i] = reinterpret_cast<void *>(static_cast<intptr_t>(integer(a[i])));
+        count(n, 12, "bind");
+        void *p[12];
+        for (int i = 0; i < 12; i++) p[i] = reinterpret_cast<void *>(static_cast<intptr_t>(integer(a[i])));
         api = {reinterpret_cast<plan_fn>(p[0]), reinterpret_cast<rope_fn>(p[1]), reinterpret_cast<rows_fn>(p[2]),
                reinterpret_cast<attn_ws_fn>(p[3]), reinterpret_cast<attn_fn>(p[4]), reinterpret_cast<page_fn>(p[5]),
                reinterpret_cast<mrope_fn>(p[6]), reinterpret_cast<norm_fn>(p[7]), reinterpret_cast<pplan_fn>(p[8]),
-               reinterpret_cast<pattn_ws_fn>(p[9]), reinterpret_cast<pattn_fn>(p[10])};
+               reinterpret_cast<pattn_ws_fn>(p[9]), reinterpret_cast<pattn_fn>(p[10]), reinterpret_cast<page_fn>(p[11])};
         Py_RETURN_NONE;
     });
 }
