@@ -17,6 +17,7 @@
 // four threads a q8_1 block.  Other rows: values a row width of threads apart,
 // single loads that lie side by side, a warp a q8_1 block.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -118,14 +119,19 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-// (every warp sums up the warps' parts in the same tree: the same bits everywhere)
-__device__ __forceinline__ float row_sum(float v, float *part, int warps) {
+// (every warp sums up the warps' parts in the same tree: the same bits everywhere.)  behind(): past the row's barrier
+struct Nothing {
+    __device__ __forceinline__ void operator()() const {}
+};
+template <class F>
+__device__ __forceinline__ float row_sum(float v, float *part, int warps, F behind) {
     v = warp_sum(v);
     if (warps == 1) return v;   // a row per warp
     constexpr int MOST = BN_THREADS / 32;   // 16: both halves of a warp sum them up
     const int lane = threadIdx.x & 31, w = lane % MOST;
     if (lane == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
+    behind();
     v = w < warps ? part[w] : 0.0f;
 #pragma unroll
     for (int o = MOST / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -133,9 +139,9 @@ __device__ __forceinline__ float row_sum(float v, float *part, int warps) {
 }
 
 // v <- N(v); part: two arrays of partial sums that nothing else uses
-template <int C, bool VEC>
+template <int C, bool VEC, class F>
 __device__ __forceinline__ void normed(const RowPart<C, VEC> &r, int kind, const float *w, const float *b, float eps, float inv_k,
-                                       float (&v)[C][8], float (*part)[BN_THREADS / 32], int warps) {
+                                       float (&v)[C][8], float (*part)[BN_THREADS / 32], int warps, F behind) {
     if (kind == GGUF_NORM_NONE) return;
     if (kind == GGUF_NORM_LAYER) {
         float s = 0.0f;
@@ -143,7 +149,7 @@ __device__ __forceinline__ void normed(const RowPart<C, VEC> &r, int kind, const
         for (int c = 0; c < C; c++)
 #pragma unroll
             for (int i = 0; i < 8; i++) s += v[c][i];   // (zeros past the row)
-        const float mean = row_sum(s, part[0], warps) * inv_k;
+        const float mean = row_sum(s, part[0], warps, behind) * inv_k;
 #pragma unroll
         for (int c = 0; c < C; c++)
 #pragma unroll
@@ -154,7 +160,8 @@ __device__ __forceinline__ void normed(const RowPart<C, VEC> &r, int kind, const
     for (int c = 0; c < C; c++)
 #pragma unroll
         for (int i = 0; i < 8; i++) s = fmaf(v[c][i], v[c][i], s);
-    const float inv = __frsqrt_rn(fmaf(row_sum(s, part[1], warps), inv_k, eps));
+    const float sum = kind == GGUF_NORM_LAYER ? row_sum(s, part[1], warps, Nothing()) : row_sum(s, part[1], warps, behind);
+    const float inv = __frsqrt_rn(fmaf(sum, inv_k, eps));
 #pragma unroll
     for (int c = 0; c < C; c++)
 #pragma unroll
@@ -196,7 +203,7 @@ __device__ __forceinline__ void q8_codes(const float (&v)[N], float d, uint32_t 
     }
 }
 
-// a row, from its x, h and gate to its outputs; release(): they are not read any more
+// a row, from its x, h and gate to its outputs; release(): behind a barrier that all threads reach when they have read them
 template <int XT, int HT, int C, bool VEC, bool EARLY, class F>
 __device__ __forceinline__ void norm_row(const BlockNorm &p, const RowPart<C, VEC> &r, int64_t t, const void *x, const void *h,
                                          const void *gate, float (*part)[BN_THREADS / 32], F release) {
@@ -206,7 +213,7 @@ __device__ __forceinline__ void norm_row(const BlockNorm &p, const RowPart<C, VE
     if (EARLY && p.h != nullptr) r.load(h, HT, 0, o);
     if (p.x != nullptr) {
         r.load(x, XT, 0, v);
-        normed(r, p.post, p.post_w, p.post_b, p.post_eps, inv_k, v, part, warps);
+        normed(r, p.post, p.post_w, p.post_b, p.post_eps, inv_k, v, part, warps, Nothing());
         if (p.gate != nullptr) {
             float g[C][8];
             r.load(gate, p.gt, 0, g);
@@ -220,10 +227,6 @@ __device__ __forceinline__ void norm_row(const BlockNorm &p, const RowPart<C, VE
                     v[c][i] *= a;
                 }
         }
-#pragma unroll
-        for (int c = 0; c < C; c++)
-#pragma unroll
-            for (int i = 0; i < 8; i++) v[c][i] *= p.branch;
     } else {
 #pragma unroll
         for (int c = 0; c < C; c++)
@@ -232,15 +235,30 @@ __device__ __forceinline__ void norm_row(const BlockNorm &p, const RowPart<C, VE
     }
     if (p.h != nullptr) {
         if (!EARLY) r.load(h, HT, 0, o);
+        if (p.resid != 1.0f) {
+#pragma unroll
+            for (int c = 0; c < C; c++)
+#pragma unroll
+                for (int i = 0; i < 8; i++) o[c][i] *= p.resid;
+        }
 #pragma unroll
         for (int c = 0; c < C; c++)
 #pragma unroll
-            for (int i = 0; i < 8; i++) v[c][i] = fmaf(o[c][i], p.resid, v[c][i]);
+            for (int i = 0; i < 8; i++) v[c][i] = fmaf(v[c][i], p.branch, o[c][i]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[c][i] *= p.branch;
     }
-    release();
+    const bool on = p.z != nullptr || p.zq != nullptr;
+    if (!std::is_same_v<F, Nothing> && (!on || p.pre == GGUF_NORM_NONE)) {   // no barrier follows
+        __syncthreads();
+        release();
+    }
     if (p.h_out != nullptr) r.store(p.h_out, HT, t * p.ldho, v);
-    if (p.z == nullptr && p.zq == nullptr) return;
-    normed(r, p.pre, p.pre_w, p.pre_b, p.pre_eps, inv_k, v, part + 2, warps);
+    if (!on) return;
+    normed(r, p.pre, p.pre_w, p.pre_b, p.pre_eps, inv_k, v, part + 2, warps, release);
     if (p.z != nullptr) r.store(p.z, p.zt, t * p.ldz, v);
     if (p.zq == nullptr) return;
     uint8_t *row = p.zq + t * (p.k / QK8 * Q8_1_BYTES);
@@ -300,7 +318,7 @@ __global__ void __launch_bounds__(BN_THREADS) block_norm_kernel(const BlockNorm 
     const RowPart<C, VEC> r{(int)threadIdx.x, (int)blockDim.x, (int)p.k};
     // h is asked for before the norm of x, where there are registers for it
     norm_row<XT, HT, C, VEC, (C < 8)>(p, r, t, row_at(p.x, XT, t * p.ldx), row_at(p.h, HT, t * p.ldh), row_at(p.gate, p.gt, t * p.ldg),
-                                      part, [] {});
+                                      part, Nothing());
 }
 
 // Many rows: a CTA takes every gridDim-th row, and bulk copies bring the rows ahead into a ring in shared memory while it
@@ -315,11 +333,15 @@ struct BnRing {
 template <int XT, int HT, int C>
 __global__ void __launch_bounds__(BN_THREADS, C <= 2 ? 2 : 1) block_norm_ring_kernel(const BlockNorm p, const BnRing ring) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float part[4][BN_THREADS / 32];
+    __shared__ float part[2][4][BN_THREADS / 32];   // of every other row: a thread may still read those of the row before
     __shared__ uint64_t full[BN_STAGES];
+    __shared__ int32_t dead_word;   // a wait was given up
+    volatile int32_t *dead = &dead_word;
     const int tid = threadIdx.x;
-    if (tid == 0)
+    if (tid == 0) {
         for (int i = 0; i < ring.stages; i++) tc::mbar_init(&full[i], 1);
+        dead_word = 0;
+    }
     tc::fence_barrier_init();
     __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -336,11 +358,16 @@ __global__ void __launch_bounds__(BN_THREADS, C <= 2 ? 2 : 1) block_norm_ring_ke
     };
     if (tid == 0)
         for (int i = 0; i < ring.stages; i++) ask(blockIdx.x + (int64_t)i * gridDim.x, i);
-    int stage = 0;
+    int stage = 0, odd = 0;
     uint32_t phase = 0;
     for (int64_t t = blockIdx.x; t < p.n_tokens; t += gridDim.x) {
-        const bool ok = tc::mbar_wait(&full[stage], phase);
-        if (!__syncthreads_and(ok)) {   // given up: what is under way lands before the CTA exits
+        if (!tc::mbar_wait(&full[stage], phase)) *dead = 1;   // (the row goes on to its barrier with what is there)
+        const uint8_t *x = smem + (size_t)stage * bytes, *h = x + ring.bytes_x;
+        const void *gate = ring.bytes_g ? h + ring.bytes_h : row_at(p.gate, p.gt, 0);
+        norm_row<XT, HT, C, true, false>(p, r, t, x, h, gate, part[odd], [&] {
+            if (tid == 0 && !*dead) ask(t + (int64_t)ring.stages * gridDim.x, stage);
+        });
+        if (*dead) {   // (written before a barrier of this row: seen by all) what is under way lands before the CTA exits
             if (tid == 0) {
                 if (ring.err != nullptr) atomicOr(ring.err, 1);
                 for (int i = 0; i < ring.stages; i++)
@@ -348,12 +375,7 @@ __global__ void __launch_bounds__(BN_THREADS, C <= 2 ? 2 : 1) block_norm_ring_ke
             }
             return;
         }
-        const uint8_t *x = smem + (size_t)stage * bytes, *h = x + ring.bytes_x;
-        const void *gate = ring.bytes_g ? h + ring.bytes_h : row_at(p.gate, p.gt, 0);
-        norm_row<XT, HT, C, true, false>(p, r, t, x, h, gate, part, [&] {
-            __syncthreads();
-            if (tid == 0) ask(t + (int64_t)ring.stages * gridDim.x, stage);
-        });
+        odd ^= 1;
         if (++stage == ring.stages) { stage = 0; phase ^= 1; }
     }
 }
