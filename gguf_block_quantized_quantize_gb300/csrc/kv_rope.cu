@@ -11,8 +11,8 @@
 // lane, so the sum of squares and a block's extreme are a few shuffles, a
 // rotation partner is in the lane itself or one shuffle away, and a lane's 8 key
 // values are exactly one word of the packed tile.  A group takes a few rows of
-// one token, loads them together, and keeps the token's cosines and sines in
-// registers.  Values: a warp takes one 32-value block of 8 tokens, so that the
+// one token, queries or keys, two of them loaded ahead (one of fp32), and keeps the
+// token's cosines and sines in registers.  Values: a warp takes one 32-value block of 8 tokens, so that the
 // 16 bits that a tile keeps together of 4 values of one token lie next to those
 // of the other tokens.  Products and sums of the rotation are rounded one by one
 // (no fused multiply-add).  Codes are exactly those of the fp32 keys that k_out
@@ -21,13 +21,14 @@
 // order of that sum gives.
 //
 // Bound: HBM for prompts (reads q, k, v; writes q and 4.5 bits per k and v
-// value), latency for single tokens.  Measured in a captured graph: 1 token, 32 +
-// 8 + 8 heads of 128, 2.8 us (bf16), 2.9 us (fp32); 2048 tokens 21.0 us (bf16; the
-// bytes take 6.7), 29.1 us (fp32); 16 + 2 + 2 heads of 256, 18.0 and 26.5 us.  Far
-// from the bytes: eight warps a scheduler at 64 registers, where four rows in flight
-// spill (16-bit heads of 128: 104 bytes of stores and 284 of loads a thread; fp32 294
-// and 528), 64-bit divisions for the place of a value block, and the chain load, sum,
-// rotate, round, store.
+// value), latency for single tokens.  Measured in a captured graph, one axis and
+// three: 1 token, 32 + 8 + 8 heads of 128, bf16 2.8 and 3.3 us; 2048 tokens 17.4 and
+// 19.9 us (the bytes take 6.7), 4096 tokens 29.1 and 31.6 us, 2048 in fp32 21.5 and
+// 24.6; 2048 tokens, 16 + 2 + 2 heads of 256, 12.3 and 14.3 us.  Between: the issue of
+// some 31 instructions a value (59 % of the slots) at eight warps a scheduler, and the
+// chain load, sum, rotate, round, store.  With queries and keys in one loop and four rows
+// loaded ahead the registers spilled (284 bytes of loads a thread) and each four rows
+// fetched their token's angles anew: 2048 tokens 20.4 and 23.3 us, 4096 38.3 and 43.9.
 #include <algorithm>
 
 #include "common.cuh"

@@ -16,6 +16,17 @@
 // Aligned rows: a thread holds 8 consecutive values of each of its C chunks,
 // four threads a q8_1 block.  Other rows: values a row width of threads apart,
 // single loads that lie side by side, a warp a q8_1 block.
+//
+// Bound: HBM for many rows (x and h in, h', z and 36 bytes per 32 values out),
+// latency for few.  Measured in a captured graph, post and pre RMS norms, bf16,
+// float and q8_1 outputs: 8192 rows of 4096 67 us (4.6 TB/s; the bytes take 45;
+// without q8_1 52 us, 5.2 TB/s), of 8192 131 us, of 16384 321 us; 2048 of 2048
+// 13.4 us; fp32, 4096 of 4096 54 us (5.3 TB/s); 1 row of 4096 2.9 us; 777 rows of
+// 1111 fp32 values (single loads, LAYER) 8.1 us.  Between the two: the issue of about
+// 49 instructions a value and 16-bit output pair (58 % of the slots), and the
+// barriers of the two sums with 32 warps an SM, which the registers of two chunks a
+// thread allow.  Sums warp by warp (16 loads each), four barriers a row and a
+// rounding at a time took 101 us.
 #include <algorithm>
 #include <type_traits>
 
