@@ -231,6 +231,8 @@ __device__ __forceinline__ PfPieces pf_pieces(const AdShape &a, const AdReq &q, 
     return x;
 }
 
+// Pieces a warp takes at a time where query rows are many (more than 16 warps an SM): 4 leave registers for twice the warps,
+// 256 requests of 32 heads 10 us, and 14 us with 8.  Where they are few nothing hides a warp's loads but its own: 8.
 constexpr int JOIN_MANY = 4;
 // Bound: the pieces' bytes, from the L2 mostly, and for few pieces the chain token, entry, pieces.  A warp per query row
 // takes AT_ONCE pieces at a time, so that their loads are under way together.

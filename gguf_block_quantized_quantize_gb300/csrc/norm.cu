@@ -23,7 +23,7 @@
 // without q8_1 52 us, 5.2 TB/s), of 8192 131 us, of 16384 321 us; 2048 of 2048
 // 13.4 us; fp32, 4096 of 4096 54 us (5.3 TB/s); 1 row of 4096 2.9 us; 777 rows of
 // 1111 fp32 values (single loads, LAYER) 8.1 us.  Between the two: the issue of about
-// 49 instructions a value and 16-bit output pair (58 % of the slots), and the
+// 48 instructions a value with its 16-bit output pair (56 % of the slots), and the
 // barriers of the two sums with 32 warps an SM, which the registers of two chunks a
 // thread allow.  Sums warp by warp (16 loads each), four barriers a row and a
 // rounding at a time took 101 us.
