@@ -98,6 +98,7 @@ struct PfShape {
     const int32_t *plan;       // header, entries, of each token its position, and its request and group (pf_pack), q_start, kv_len
     int32_t n_entries, chained;   // chained: the decode kernel follows the prefill kernel of the call
     int32_t parts, pieces;     // slots of the decode kernel, of the prefill kernel
+    int32_t tiles;             // that an entry has at most, whatever its lengths say
     float *records;
 };
 constexpr int PF_HEADER = 8, PF_MAGIC = 0x50465831;   // {magic, requests, groups, tokens, page size, 0, 0, 0}
@@ -182,7 +183,7 @@ __device__ __forceinline__ AdReq pf_request(const AdShape &a, int e) {
     const Attn &p = a.p;
     const int4 u = reinterpret_cast<const int4 *>(pf_entries(a.pf) + e)[0], v = reinterpret_cast<const int4 *>(pf_entries(a.pf) + e)[1];
     o.rows0 = u.x;
-    const int32_t tile0 = max(u.z, 0), tile1 = max(min(u.w, 1 << 27), tile0);
+    const int32_t tile0 = max(u.z, 0), tile1 = max(min(u.w, a.pf.tiles), tile0);
     const int64_t rows = (int64_t)u.y * a.G;
     const bool mine = u.x >= 0 && u.y > 0 && (int64_t)u.x + u.y <= p.n_tokens && rows > a.min_rows && rows <= a.max_rows &&
                       v.z >= 0 && v.z < p.R;

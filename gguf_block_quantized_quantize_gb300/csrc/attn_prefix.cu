@@ -388,7 +388,8 @@ cudaError_t launch_prefix_attn(const Attn &p, const void *plan, int64_t NG, int6
             p.ldo * es % 16 == 0;
     a.part = (float *)(w + x.part);
     a.pieces = (float *)(w + x.pieces);
-    a.pf = PfShape{(const int32_t *)plan, (int32_t)(p.R + NG), x.tc, x.ctas * ad_warps((int)d, p.qt == GGUF_F32, x.rg / 8), x.ctas, (float *)ws};
+    a.pf = PfShape{(const int32_t *)plan, (int32_t)(p.R + NG), x.tc, x.ctas * ad_warps((int)d, p.qt == GGUF_F32, x.rg / 8), x.ctas,
+                   (int32_t)std::min<int64_t>(p.width * p.page / KV_TILE + PF_PAST, 1 << 27), (float *)ws};
     a.min_rows = x.few;
     a.max_rows = 0x7fffffff;
     if (x.tc) {

@@ -159,6 +159,11 @@ PyObject *guarded(F f) {
     try {
         return f();
     } catch (const Bad &) {
+    } catch (const c10::OutOfMemoryError &e) {   // what torch.empty raises
+        PyObject *torch = PyImport_ImportModule("torch"), *type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+        if (type) PyErr_SetString(type, e.what());
+        Py_XDECREF(type);
+        Py_XDECREF(torch);
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
     }
@@ -465,12 +470,14 @@ PyObject *prefix_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
         struct Held {
             PyObject *p;
             ~Held() { Py_XDECREF(p); }
-        } out{a[11]};
+        } out{nullptr};
         if (a[11] == Py_None) {
             const at::Tensor &q = tensor(a[0], what, "q");
             out.p = THPVariable_Wrap(at::empty(q.sizes(), q.options()));
-        } else
+        } else {
+            out.p = a[11];
             Py_INCREF(out.p);
+        }
         args[6] = out.p;
         gguf_attn_args x = attn_args(a[0], a[1], args, what);
         const Table t = table(a[2], 0, what);

@@ -283,6 +283,7 @@ int64_t prefix_plan_bytes(int64_t R, int64_t NG, int64_t n_tokens);
 cudaError_t launch_prefix_plan(const int32_t *q_start, const int32_t *kv_len, int64_t R, const int32_t *group_start,
                                const int32_t *prefix_len, int64_t NG, int64_t page, int64_t n_tokens, void *plan, cudaStream_t s);
 size_t prefix_attn_ws_size(const Attn &p, int64_t NG, int64_t d);
+constexpr int64_t PF_PAST = 1 << 16;   // tiles past its table that a request's lengths may ask for: more are not walked over
 cudaError_t launch_prefix_attn(const Attn &p, const void *plan, int64_t NG, int64_t d, void *ws, cudaStream_t s);
 
 }  // namespace gg

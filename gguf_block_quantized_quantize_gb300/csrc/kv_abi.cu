@@ -258,7 +258,7 @@ static gguf_status check_prefix_sizes(const gguf_attn_args *a, int64_t n_groups)
     if (st != GGUF_OK) return st;
     // the tiles of all units are shared out over SMs and warps, whose parts are counted in 31 bits
     const double units = (double)a->n_tokens * (double)(a->n_heads / a->n_kv_heads) / 8.0 + (double)(a->n_requests + n_groups);
-    if (units * (double)a->n_kv_heads * (double)a->width * (double)(a->page_size / KV_TILE) > 0x1p40)
+    if (units * (double)a->n_kv_heads * ((double)a->width * (double)(a->page_size / KV_TILE) + (double)PF_PAST) > 0x1p40)
         return report(GGUF_ERR_SHAPE, "prefix_attention: too many queries over too wide a table for one call; split it");
     if (a->n_tokens * a->n_heads > (1 << 30))   // records are counted in 31 bits, two a query row
         return refuse(GGUF_ERR_SHAPE, "prefix_attention: %lld tokens x %lld heads (at most 2^30)", (long long)a->n_tokens, (long long)a->n_heads);

@@ -793,11 +793,12 @@ gguf_status gguf_prefix_plan(const int32_t *q_start, const int32_t *kv_len, int6
  *          n_groups, n_tokens and page_size: plan_bytes, at least gguf_prefix_plan_bytes of
  *          them.  A plan of other sizes gives unspecified outputs.
  *   dev_status : + pages outside the cache or past the table, each once per request whose
- *          queries would see a token of it, or once for the requests of a group together.
+ *          queries would see a token of it, or once for the requests of a group together (of
+ *          a length past its table's row, those of 2^20 tokens more where tokens are read together).
  *   ws   : gguf_prefix_attention_ws_size(args, n_groups) bytes, 16-byte aligned: about
  *          8 (head_dim + 4) bytes per token and head, and up to 32 MB.
- * n_tokens x n_heads <= 2^30, and 2^40 tiles of 16 tokens under all groups of 8 query rows
- * (GGUF_ERR_SHAPE above).  Precision, windows, blocks that are not
+ * n_tokens x n_heads <= 2^30, and 2^40 tiles of 16 tokens, 2^16 more a row than the table
+ * holds, under all groups of 8 query rows (GGUF_ERR_SHAPE above).  Precision, windows, blocks that are not
  * finite (which may reach the queries of their group) and timeouts are as described at
  * gguf_paged_attention; the bits of a request's outputs depend on the batch.  Made for few
  * queries per request (decoding, tokens to check): long chunks of prompts go through, but

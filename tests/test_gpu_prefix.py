@@ -306,6 +306,31 @@ def test_pages_past_the_table():
     check_attn(got, reference(short), "bf16")
 
 
+@pytest.mark.parametrize("members, typ", [(40, "bf16"), (9, "bf16"), (9, "f32")])
+def test_lengths_far_past_the_table(members, typ):
+    """A length that no table holds sees what the table has; 2^16 tiles past it are counted, and no more walked over."""
+    b = batch([(96, [(1, 150)] * members), (None, ONE(40))], 8, 2, 64, 16, typ)
+    lens = b["kv_len"].clone()
+    lens[members] = 1 << 30      # its 40 tokens lie in 3 pages, whose last 8 slots hold none
+    b["table"][members, 2] = -1
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = run({**b, "kv_len": lens}, dev_status=status)
+    assert int(status.item()) == int((b["table"][members] < 0).sum()) + (1 << 16)
+    short = {**b, "kv_lens": b["kv_lens"][:members] + [32], "slots": b["slots"][:members] + [b["slots"][members][:32]]}
+    check_attn(got, reference(short), typ)
+
+
+def test_no_room_for_the_output():
+    """Memory that is not there is torch's own error, as where torch makes the output."""
+    b = batch([(96, [(1, 150)] * 4)], 8, 2, 64, 16, "bf16")
+    plan = g.gguf_prefix_plan(b["start"], b["kv_len"], b["gs"], b["prefix"], 16, 4)
+    with pytest.raises(torch.OutOfMemoryError):
+        g.gguf_prefix_attention(b["q"][:1].expand(1 << 31, 8, 64), b["cache"], b["table"], plan, 1, 2, 16, 1, 0.1)
+    with pytest.raises(ValueError, match="q"):
+        g._bound().prefix_attention("q", b["cache"], b["table"], plan, 1, 2, 16, 1, 0.1, 0, 0, None, None, None, 0)
+    check_attn(run(b), reference(b), "bf16")
+
+
 def test_values_of_one_size_and_peaks():
     """A prefix that holds nearly all the weight, or nearly none of it: the join of two very different maxima."""
     for typ, gain in (("bf16", 12.0), ("f16", 12.0), ("f32", 30.0)):
