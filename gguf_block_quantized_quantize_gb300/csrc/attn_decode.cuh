@@ -134,8 +134,9 @@ struct AdReq {
     int32_t rows0;        // first query token
     int32_t q;            // query tokens
     int32_t pos0;         // position of the first
-    int32_t nt, n_sink, w_tile;   // tiles: n_sink first ones, then from w_tile on
+    int32_t nt, n_sink, w_tile;   // tiles: n_sink first ones, from s_tile on, then from w_tile on
     int32_t row, pos_max;         // (PRE) row of the block table, the last position of a query
+    int32_t s_tile;               // (PRE; else 0)
 };
 __device__ __forceinline__ AdReq ad_request(const AdShape &a, int r) {
     AdReq o;
@@ -148,7 +149,7 @@ __device__ __forceinline__ AdReq ad_request(const AdShape &a, int r) {
     const bool mine = o.rows0 >= 0 && q > 0 && q * G > a.min_rows && q * G <= a.max_rows;
     o.q = mine ? (int32_t)q : 0;
     o.row = r;
-    o.pos_max = 0;
+    o.pos_max = o.s_tile = 0;
     o.nt = o.n_sink = o.w_tile = 0;
     const int32_t kv = p.kv_len[r];
     o.pos0 = kv - (p.q_start[r + 1] - o.rows0);
@@ -192,16 +193,11 @@ __device__ __forceinline__ AdReq pf_request(const AdShape &a, int e) {
     o.pos_max = v.y;
     o.row = v.z;
     o.n_sink = 0;
-    o.w_tile = tile0;
-    if (p.window > 0) {
-        const int64_t lo = (int64_t)v.x - p.window + 1;   // what the first query sees from
-        const int32_t w = lo > 0 ? (int32_t)min(lo / KV_TILE, (int64_t)tile1) : 0;
-        if (e >= p.R) {
-            o.w_tile = w;
-            o.n_sink = (int32_t)min((p.sinks + KV_TILE - 1) / KV_TILE, (int64_t)w);
-        } else if (p.sinks <= (int64_t)tile0 * KV_TILE) {   // (else first tokens of the request's own: all its tiles)
-            o.w_tile = max(w, tile0);
-        }
+    o.s_tile = o.w_tile = tile0;
+    if (p.window > 0) {   // of the tiles from tile0 on (0 for a group): those that the sinks reach, then what the first query sees from
+        const int64_t lo = (int64_t)v.x - p.window + 1;
+        o.w_tile = max(lo > 0 ? (int32_t)min(lo / KV_TILE, (int64_t)tile1) : 0, tile0);
+        o.n_sink = (int32_t)min(max((p.sinks + KV_TILE - 1) / KV_TILE - tile0, (int64_t)0), (int64_t)(o.w_tile - tile0));
     }
     o.nt = o.q > 0 ? o.n_sink + tile1 - o.w_tile : 0;
     return o;
@@ -215,7 +211,7 @@ template <bool PRE>
 __device__ __forceinline__ int ad_requests(const AdShape &a) { return PRE ? a.pf.n_entries : (int)a.p.R; }
 
 // the tile of the request's i-th one, and whether it is the first of its page among them (a page that is not there counts once)
-__device__ __forceinline__ int ad_tile(const AdReq &q, int i) { return i < q.n_sink ? i : q.w_tile + i - q.n_sink; }
+__device__ __forceinline__ int ad_tile(const AdReq &q, int i) { return i < q.n_sink ? q.s_tile + i : q.w_tile + i - q.n_sink; }
 __device__ __forceinline__ bool ad_starts_page(const AdShape &a, const AdReq &q, int i) {
     return i == 0 || ad_tile(q, i) / a.tpp != ad_tile(q, i - 1) / a.tpp;
 }
@@ -662,6 +658,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             if (PRE && p.window <= 0) full_hi -= cur.q.w_tile;
             if (p.window > 0) {
                 full_sink = (int)min((int64_t)cur.q.n_sink, p.sinks / KV_TILE);
+                if constexpr (PRE) full_sink = (int)min((int64_t)cur.q.n_sink, max(p.sinks / KV_TILE - cur.q.s_tile, (int64_t)0));
                 const int64_t lo = (int64_t)pos_hi - p.window + 1;   // first token that the last row sees
                 const int lo_tile = lo > 0 ? (int)((lo + KV_TILE - 1) / KV_TILE) : 0, shift = cur.q.n_sink - cur.q.w_tile;
                 full_lo = max(lo_tile + shift, cur.q.n_sink);
@@ -748,7 +745,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
 #pragma unroll
                     for (int x = 0; x < TP; x++) {
                         const bool there = (use >> x) & 1;
-                        const int i = cur.tile + x, tok = (i < cur.q.n_sink ? i : cur.q.w_tile + i - cur.q.n_sink) * KV_TILE;
+                        const int tok = ad_tile(cur.q, cur.tile + x) * KV_TILE;
 #pragma unroll
                         for (int e = 0; e < 2; e++) {
                             keep[x][e] = 0;

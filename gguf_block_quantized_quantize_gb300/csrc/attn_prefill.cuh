@@ -73,7 +73,7 @@ struct ApItem {
     int r, head, row0, rows;      // request, KV head, first query row and rows (of token * G + head)
     int q0, pos0;                 // the request's first query token, position of row row0's token
     int tok0;                     // row0 / G
-    int nt, n_sink, w_tile;       // the tiles that the rows see (see AdReq): the piece takes those from base to nt
+    int nt, n_sink, w_tile, s_tile;   // the tiles that the rows see (see AdReq; s_tile: PRE): the piece takes those from base to nt
     int base;
     int part;                     // its place among the partial results where the row block's tiles are cut, else -1
     int follow;                   // (PRE) CTAs that take the row block's blocks after these
@@ -153,6 +153,7 @@ __device__ __forceinline__ bool pf_first_sight(const AdShape &a, const ApItem &w
     AdReq q{};
     q.n_sink = w.n_sink;
     q.w_tile = w.w_tile;
+    q.s_tile = w.s_tile;
     return w.row0 == 0 && ad_starts_page(a, q, i);
 }
 // whether `tile` is the first of its page that the request's queries see, and no row block before this one sees it
@@ -181,11 +182,11 @@ struct ApUnpack {
     static constexpr int NB = L::NB, BW = L::BW, NC = L::NC, BT = C::BT, XS = NB / 2, STEPS = C::GT / 4;
     const uint8_t *raws;
     const int32_t *raw_mask;
-    int lane, w8, last, n_sink, w_tile, i_base;
+    int lane, w8, last, n_sink, w_tile, s_tile, i_base;
     int kg, odd, tl, pp, hb, vg;
     uint32_t k_off, v_cx, v_row;
-    __device__ __forceinline__ ApUnpack(const uint8_t *smem, const int32_t *masks, int lane_, int w8_, const ApItem &item, int base, int last_)
-        : raws(smem + C::OFF_RAW), raw_mask(masks), lane(lane_), w8(w8_), n_sink(item.n_sink), w_tile(item.w_tile), i_base(base) {
+    __device__ __forceinline__ ApUnpack(const uint8_t *smem, const int32_t *masks, int lane_, int w8_, const ApItem &item, int sinks_from, int base, int last_)
+        : raws(smem + C::OFF_RAW), raw_mask(masks), lane(lane_), w8(w8_), n_sink(item.n_sink), w_tile(item.w_tile), s_tile(sinks_from), i_base(base) {
         const int kq = lane & 3;
         kg = lane >> 2;
         odd = kg & 1;
@@ -238,7 +239,7 @@ struct ApUnpack {
         const uint8_t *raw = raws + rs * C::RAW_BYTES + (4 * step + tl) * C::PITCH;
         const bool live = (raw_mask[rs] >> (4 * step + tl)) & 1;
         const int i = i_base + j * C::GT + 4 * step + tl;
-        x.end = live ? last - (i < n_sink ? i : w_tile + i - n_sink) * KV_TILE : -1;
+        x.end = live ? last - (i < n_sink ? s_tile + i : w_tile + i - n_sink) * KV_TILE : -1;
         const int b0 = hb * XS;
 #pragma unroll
         for (int q = 0; q < 4; q++) {
@@ -432,7 +433,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar);
     };
-    auto token_of = [&](int i) { return (i < item.n_sink ? i : item.w_tile + i - item.n_sink) * KV_TILE; };
+    auto tile_of = [&](int i) { return i < item.n_sink ? (PRE ? item.s_tile + i : i) : item.w_tile + i - item.n_sink; };
+    auto token_of = [&](int i) { return tile_of(i) * KV_TILE; };
 
     // items in stripes of one per CTA, every other stripe backwards: a request's row blocks come longest first
     using Stripe = std::conditional_t<PRE, int, int64_t>;   // (PRE) blocks of the CTA's own
@@ -467,6 +469,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             w.pos0 = 0;
             w.n_sink = at.q.n_sink;
             w.w_tile = at.q.w_tile;
+            w.s_tile = at.q.s_tile;
             w.base = at.blk * (BT / KV_TILE);
             w.nt = min(at.q.nt, (at.blk + left) * (BT / KV_TILE));
             w.part = -1;
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             w.tok0 = w.row0 / G;
             w.pos0 = q.pos0 + w.tok0;
             const int last = q.pos0 + (w.row0 + w.rows - 1) / G;
-            w.nt = w.n_sink = w.w_tile = 0;
+            w.nt = w.n_sink = w.w_tile = w.s_tile = 0;
             if (last >= 0) {
                 const int end = last / KV_TILE + 1;
                 w.nt = end;
@@ -642,7 +645,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                 arrive(&q_full);
             }
             if (PRE && wk.nrt == 1 && warp >= 4) {   // no rows of its own: the values
-                unpack_values(ApUnpack<D, QT>(smem, raw_mask, lane, warp - 4, item, item.base, item.pos_max));
+                unpack_values(ApUnpack<D, QT>(smem, raw_mask, lane, warp - 4, item, item.s_tile, item.base, item.pos_max));
                 continue;
             }
             // ================= softmax
@@ -845,7 +848,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             // bandwidth for long stretches, and a read may take many hundred cycles.
             constexpr int STEPS = C::GT / 4;
             const int w8 = warp - 8;
-            const ApUnpack<D, QT> u(smem, raw_mask, lane, w8, item, PARTS ? item.base : 0,
+            const ApUnpack<D, QT> u(smem, raw_mask, lane, w8, item, PRE ? item.s_tile : 0, PARTS ? item.base : 0,
                                     PRE ? item.pos_max : item.pos0 + (item.row0 + item.rows - 1) / G - item.tok0);
             if (PRE && wk.nrt == 1) {   // the second row tile's warps have no rows and take the values
                 unpack_keys(u);
@@ -985,7 +988,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                 int issued = 0;
                 auto place_of = [&](int i) -> int64_t {   // of the i-th tile; -1 where it has none
                     if (i >= i_end) return -1;
-                    const int tile = i < item.n_sink ? i : item.w_tile + i - item.n_sink;
+                    const int tile = tile_of(i);
                     const int pi = a.tpp_shift >= 0 ? tile >> a.tpp_shift : (int)((uint32_t)tile / (uint32_t)a.tpp);
                     const int32_t pg = pi < p.width ? p.table[item.r * p.ld + pi] : -1;
                     if (pg >= 0 && pg < p.n_pages) return pg * a.page_bytes + (int64_t)(item.head * a.tpp + tile - pi * a.tpp) * L::BYTES;

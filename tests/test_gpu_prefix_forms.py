@@ -1,0 +1,90 @@
+"""gguf_prefix_attention in calls whose answer could depend on what the host arguments choose: windows of requests that
+share nothing, groups whose first request is short, requests of more than max_q_len queries, plans of other sizes."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import gguf_block_quantized_quantize_gb300 as g
+from test_gpu_kv import check_attn
+from test_gpu_prefix import DEV, ONE, batch, poisoned, reference, run
+
+pytestmark = pytest.mark.gpu
+
+
+def reads_together(b, max_q, window=0, sinks=0):
+    """Whether the call goes through the kernels that read shared tokens together (one by one, the workspace is
+    gguf_paged_attention's)."""
+    q, t = b["q"], b["table"]
+    a = g.AttnArgs(q.data_ptr(), g._TYPE_OF[q.dtype], q.shape[0], q.stride(0), b["cache"].data_ptr(), b["cache"].shape[0], b["page"],
+                   t.data_ptr(), t.stride(0), t.shape[1], 0, 0, t.shape[0], max_q, q.shape[1], b["hk"], q.shape[2], b["scale"],
+                   window, sinks, q.data_ptr(), q.stride(0), 0)
+    lib = g.load_library()
+    return lib.gguf_prefix_attention_ws_size(ctypes.byref(a), b["prefix"].numel()) != lib.gguf_paged_attention_ws_size(ctypes.byref(a))
+
+
+def paged(b, max_q, window=0, sinks=0, **kw):
+    return g.gguf_paged_attention(b["q"], b["cache"], b["table"], b["start"], b["kv_len"], b["hk"], b["page"], max_q, b["scale"],
+                                  window=window, sinks=sinks, **kw)
+
+
+# ---------------------------------------------------------------- windows
+
+def seen_pages(b, window, sinks, max_q=1 << 30):
+    """Of each request, which pages of its row some query sees: of it, or of its group where they are shared."""
+    page, see = b["page"], []
+    for n, kv in zip(b["q_lens"], b["kv_lens"]):
+        pos, j = np.arange(kv - n, kv)[:max_q, None], np.arange(max(kv, 0))[None]
+        some = ((j <= pos) & ((j > pos - window) | (j < sinks) if window else True)).any(0)
+        mine = np.zeros(b["table"].shape[1], dtype=bool)
+        mine[np.flatnonzero(some) // page] = True
+        see.append(mine)
+    bounds = b["gs"].tolist()
+    for s, e, prefix in zip(bounds, bounds[1:], b["prefix"].tolist()):
+        if e - s >= 2:
+            whole = max(prefix, 0) // page
+            any_of = np.any([m[:whole] for m in see[s:e]], axis=0)
+            for m in see[s:e]:
+                m[:whole] = any_of
+    return np.array(see)
+
+
+def hide_pages(b, see, how):
+    """Pages that no query sees are not there any more (-1), or hold what their next owner left (NaN scales)."""
+    gone = torch.from_numpy(~see).to(DEV)
+    if how == "stale":
+        old = b["table"][gone]
+        b["cache"][old[old >= 0].long()] = 0xFF
+    else:
+        b["table"] = b["table"].masked_fill(gone, -1)
+    return int((~see).sum())
+
+
+WINDOWS = [
+    # groups, h, hk, d, page, type, window, sinks: single tokens and chunks outside every group, groups of one, groups whose
+    # prefix is shorter than the sinks or than a page
+    ([(None, ONE(*range(300, 900, 7)) + [(9, 700), (30, 1000)]), (320, ONE(*range(330, 400, 10))), (200, ONE(500))], 16, 4, 128, 16, "bf16", 100, 20),
+    ([(None, ONE(*range(200, 600, 6)) + [(12, 500)]), (100, ONE(*range(500, 520, 4)))], 8, 1, 256, 32, "f16", 64, 40),
+    ([(15, ONE(*range(200, 600, 6))), (None, [(20, 400), (3, 500)])], 6, 2, 64, 16, "f32", 77, 33),
+    ([(64, ONE(*range(300, 700, 4)) + [(40, 500)])], 8, 1, 128, 16, "bf16", 64, 200),
+    ([(400, ONE(*range(700, 900, 4)) + [(18, 800)]), (None, ONE(*range(90, 700, 10)) + [(50, 600)])], 16, 2, 64, 48, "f16", 50, 1),
+]
+
+
+@pytest.mark.parametrize("how", ["freed", "stale"])
+@pytest.mark.parametrize("case", WINDOWS, ids=lambda c: "-".join(str(x).replace(" ", "")[:60] for x in c))
+def test_windows_of_own_tokens(case, how):
+    """Between the sinks and the window of a request nothing is read, counted, or let into the outputs."""
+    groups, h, hk, d, page, typ, window, sinks = case
+    b = batch(groups, h, hk, d, page, typ, seed=h + d)
+    refs = reference(b, window, sinks)
+    table = b["table"]
+    assert hide_pages(b, seen_pages(b, window, sinks), how) > int((table < 0).sum())
+    n = b["q"].shape[0]
+    assert reads_together(b, n, window, sinks)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    check_attn(run(b, window, sinks, max_q=n, dev_status=status, ws=poisoned(b, n, window, sinks)), refs, typ)
+    assert int(status.item()) == 0
+    check_attn(paged(b, n, window, sinks, dev_status=status), refs, typ)
+    assert int(status.item()) == 0
