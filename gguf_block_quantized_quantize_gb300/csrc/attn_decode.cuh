@@ -101,7 +101,12 @@ struct PfShape {
     int32_t tiles;             // that an entry has at most, whatever its lengths say
     float *records;
 };
-constexpr int PF_HEADER = 8, PF_MAGIC = 0x50465831;   // {magic, requests, groups, tokens, page size, 0, 0, 0}
+constexpr int PF_HEADER = 8, PF_MAGIC = 0x50465831;   // {magic, requests, groups, tokens, page size, short, 0, 0}; short: 1 where the
+                                                      // first request of some group is shorter than what the group shares
+// where q_start and kv_len lie in a plan, in words
+__host__ __device__ __forceinline__ int64_t pf_lengths_at(int64_t R, int64_t NG, int64_t n_tokens) {
+    return PF_HEADER + (R + NG) * (int64_t)(sizeof(PfEntry) / 4) + 2 * n_tokens;
+}
 template <int D> struct PfStride { static constexpr int64_t value = D + 4; };   // 16-byte steps
 
 // the unit that a CTA began and did not end: the CTAs after it that hold pieces of it (0: there is none), its
@@ -214,6 +219,21 @@ __device__ __forceinline__ int ad_requests(const AdShape &a) { return PRE ? a.pf
 __device__ __forceinline__ int ad_tile(const AdReq &q, int i) { return i < q.n_sink ? q.s_tile + i : q.w_tile + i - q.n_sink; }
 __device__ __forceinline__ bool ad_starts_page(const AdShape &a, const AdReq &q, int i) {
     return i == 0 || ad_tile(q, i) / a.tpp != ad_tile(q, i - 1) / a.tpp;
+}
+// The row of the block table that a group's tiles are read through: that of its first request (q.row), which lists them if
+// the last of them begins among its tokens, else that of the request whose query stands last, of several the first.
+// By the lanes of `mask` together, of which the caller is the i-th of n.  Asked for only where the plan says that some first
+// request is short: elsewhere the lengths' load need not come before the table's.
+__device__ __forceinline__ int pf_row(const AdShape &a, const AdReq &q, int i, int n, uint32_t mask) {
+    const int32_t *lens = a.pf.plan + pf_lengths_at(a.p.R, a.pf.n_entries - a.p.R, a.p.n_tokens) + a.p.R + 1;
+    if ((int64_t)ad_tile(q, q.nt - 1) * KV_TILE < lens[q.row]) return q.row;
+    uint32_t r = 0x7fffffff;
+    for (int t = i; t < q.q; t += n) {
+        const int2 at = pf_token(a.pf, q.rows0 + t);
+        if (at.x == q.pos_max) r = min(r, (uint32_t)pf_unpack(at.y).x);
+    }
+    r = __reduce_min_sync(mask, r);
+    return r < (uint32_t)a.p.R ? (int)r : q.row;
 }
 // its units: groups of rg query rows x KV heads
 __device__ __forceinline__ int64_t ad_units(const AdShape &a, const AdReq &q, int rg) {
@@ -476,7 +496,8 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
         int tiles = mine8 ? (int)min(t1 - t0, (int64_t)0x7fffffff) : 0;   // to ask for
         int unit = 0;                 // of them, those of the unit
         int stage = 0, uses = 0;      // next stage, and how often the ring has gone round
-        int base = 0, of = -1;        // the table entries: first page, and request
+        const bool any_short = PRE && a.pf.plan[5] != 0;
+        int base = 0, of = -1, rows_of = 0;   // the table entries: first page, and request; (PRE) the table's row
         int32_t now8 = -1, next8 = -1;
         const uint32_t tpp = (uint32_t)a.tpp;
         const int shift = a.tpp_shift;
@@ -500,6 +521,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             if (go && unit == 0) {
                 if (feed.tile == feed.q.nt) ad_next_unit<RG, PRE>(a, feed);
                 unit = min(tiles, feed.q.nt - feed.tile);
+                if (PRE && of != feed.r) rows_of = !any_short || feed.r < p.R ? feed.q.row : pf_row(a, feed.q, l8, 8, 0xffu << (lane & 24));
                 head = p.cache + (int64_t)(feed.u % a.hk) * tpp * L::BYTES;
             }
             __syncwarp();
@@ -507,7 +529,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             const int at = ad_tile(feed.q, i);
             const int page_at = shift >= 0 ? at >> shift : (int)((uint32_t)at / tpp), in_page = at - page_at * (int)tpp;
             const int first = __shfl_sync(0xffffffffu, page_at, lane & 24);
-            const int32_t *row = p.table + (PRE ? feed.q.row : feed.r) * p.ld;
+            const int32_t *row = p.table + (PRE ? rows_of : feed.r) * p.ld;
             if (go && (of != feed.r || first < base || first >= base + 8)) {
                 const bool slide = of == feed.r && first >= base + 8 && first < base + 16;
                 base = slide ? base + 8 : first & ~7;

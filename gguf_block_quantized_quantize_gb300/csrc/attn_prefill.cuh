@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     __shared__ int32_t chunk_end[AP_THREADS];   // at most (tokens x heads / 128) items: 31 bits
     __shared__ int64_t pre_sum[AP_THREADS / 32], pre_share;   // (PRE) blocks
     __shared__ ApPlace place[1];   // thread 0's
+    __shared__ int32_t any_short;  // (PRE) as the plan says
     volatile int32_t *abort_flag = &abort_word;
     const Attn &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -364,7 +365,10 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         // the CTA's blocks of the sequence; the thread that holds the entry of the first one writes it down
         const int64_t share = ad_div(pre_total + gridDim.x - 1, gridDim.x), own0 = min(pre_total, (int64_t)blockIdx.x * share);
         own = (int)(min(pre_total, own0 + share) - own0);
-        if (tid == 0) pre_share = share;
+        if (tid == 0) {
+            pre_share = share;
+            any_short = a.pf.plan[5];
+        }
         for (int r = tid * per; mine > 0 && r < min(R, (tid + 1) * per); r++) {
             const AdReq q = pf_request(a, r);
             const int nblk = blocks_of(q);
@@ -459,6 +463,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         if (PRE && tid == 0) {   // piece: its first block, of the CTA's own
             ApPlace at = place[0];
             const int nblk = blocks_of(at.q), left = min(nblk - at.blk, own - (int)piece), rb = at.unit / a.hk;
+            if (any_short && at.entry >= p.R) at.q.row = pf_row(a, at.q, 0, 1, 1);
             ApItem w;
             w.r = at.q.row;
             w.head = at.unit - rb * a.hk;

@@ -12,7 +12,7 @@
 //
 // An entry of the plan is a set of consecutive queries and a range of tiles of one
 // row of the block table: one for each request (its own tiles) and one for each
-// group (the shared ones, through its first request's row).  Entries with more than
+// group (the shared ones, through one request's row).  Entries with more than
 // `few` query rows per KV head go to the tensor-core kernel of prompts
 // (attn_prefill.cuh), the others to the kernel of few rows (attn_decode.cuh), each in
 // a mode that cuts all its tiles evenly over the CTAs, takes every row's position
@@ -41,11 +41,6 @@ namespace gg {
 int *tg_error_word();   // the library's device error word (mmq.cu)
 
 // ---------------------------------------------------------------- plan
-
-// where q_start and kv_len lie in a plan, in words
-__host__ __device__ __forceinline__ int64_t pf_lengths_at(int64_t R, int64_t NG, int64_t n_tokens) {
-    return PF_HEADER + (R + NG) * (int64_t)(sizeof(PfEntry) / 4) + 2 * n_tokens;
-}
 
 struct PfPlanArgs {
     const int32_t *q_start, *kv_len;
@@ -95,8 +90,8 @@ __device__ __forceinline__ void pf_queries(const PfPlanArgs &p, int64_t s, int64
     o.q = a >= 0 && b > a ? (int32_t)(b - a) : 0;
 }
 
-// Three independent parts, over all CTAs: a thread per token, a thread per request, a warp per group.  Latency-bound: a
-// token's request is a binary search of q_start, a group's positions a loop of its requests by 32.
+// Independent parts, over all CTAs: a thread per token, a thread per request, a warp per group, and the header by a CTA of its
+// own.  Latency-bound: a token's request is a binary search of q_start, a group's positions a loop of its requests by 32.
 constexpr int PF_THREADS = 256;
 __global__ void __launch_bounds__(PF_THREADS) prefix_plan_kernel(const PfPlanArgs args) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -122,9 +117,17 @@ __global__ void __launch_bounds__(PF_THREADS) prefix_plan_kernel(const PfPlanArg
     __syncthreads();
     const int64_t id = (int64_t)blockIdx.x * PF_THREADS + threadIdx.x;
     PfEntry *entries = reinterpret_cast<PfEntry *>(p.plan + PF_HEADER);
-    if (id == 0) {
-        const int32_t h[PF_HEADER] = {PF_MAGIC, (int32_t)p.R, (int32_t)p.NG, (int32_t)p.n_tokens, (int32_t)p.page, 0, 0, 0};
-        for (int i = 0; i < PF_HEADER; i++) p.plan[i] = h[i];
+    if (blockIdx.x == gridDim.x - 1) {   // the header
+        bool is_short = false;   // some group's first request does not reach the end of what the group shares
+        for (int64_t g = threadIdx.x; g < p.NG; g += PF_THREADS) {
+            const PfGroup in = pf_group(p, g);
+            is_short |= in.tiles > 0 && p.kv_len[in.s] < (int64_t)in.tiles * KV_TILE;
+        }
+        is_short = __syncthreads_or(is_short);
+        const int32_t h[PF_HEADER] = {PF_MAGIC, (int32_t)p.R, (int32_t)p.NG, (int32_t)p.n_tokens, (int32_t)p.page, is_short, 0, 0};
+        if (threadIdx.x == 0)
+            for (int i = 0; i < PF_HEADER; i++) p.plan[i] = h[i];
+        return;
     }
     int32_t *starts = p.plan + pf_lengths_at(p.R, p.NG, p.n_tokens);   // what a call takes whose requests go one by one
     if (id <= p.R) starts[id] = p.q_start[id];
@@ -200,7 +203,7 @@ cudaError_t launch_prefix_plan(const int32_t *q_start, const int32_t *kv_len, in
     PfPlanArgs a{q_start, kv_len, R, group_start, prefix_len, NG, page, n_tokens, (int32_t *)plan};
     const int64_t most = std::max<int64_t>(std::max(R + 1, n_tokens), 32 * NG);
     void *args[1] = {&a};
-    return launch_chained((const void *)prefix_plan_kernel, (most + PF_THREADS - 1) / PF_THREADS, PF_THREADS, s, args);
+    return launch_chained((const void *)prefix_plan_kernel, (most + PF_THREADS - 1) / PF_THREADS + 1, PF_THREADS, s, args);
 }
 
 // ---------------------------------------------------------------- join

@@ -767,8 +767,10 @@ gguf_status gguf_paged_attention(const gguf_attn_args *args, void *ws, size_t ws
  *                     group share nothing, nor does a group of one.
  *   prefix_len      : [n_groups] int32: tokens that the group's requests have in common
  *                     (negative: 0).  The whole pages among them are shared: they are read
- *                     through the block table row of the group's first request.  The page
- *                     that a prefix ends in is each request's own.
+ *                     through the block table row of the group's first request or, where
+ *                     that one ends before the last page that the group's queries see, of
+ *                     the request whose query stands last.  The page that a prefix ends in
+ *                     is each request's own.
  *   n_tokens        : rows of q of the attention; the plan covers the queries that fit.
  *   plan            : gguf_prefix_plan_bytes(...) bytes of device memory, 16-byte aligned
  *                     (-1 for sizes that are not supported: up to 16384 requests and groups).

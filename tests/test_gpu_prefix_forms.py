@@ -88,3 +88,32 @@ def test_windows_of_own_tokens(case, how):
     assert int(status.item()) == 0
     check_attn(paged(b, n, window, sinks, dev_status=status), refs, typ)
     assert int(status.item()) == 0
+
+
+# ---------------------------------------------------------------- rows of the table
+
+SHORT = [
+    # groups, h, hk, d, page, type: a group's first request ends in the prefix, or has no token at all
+    ([(320, [(1, 50), *ONE(*range(330, 360))])], 8, 2, 64, 16, "bf16"),
+    ([(320, [(1, 50), (2, 400), (1, 330)])], 8, 2, 128, 16, "f16"),                        # few rows: one kernel
+    ([(320, [(0, 0), (1, 10), (3, 200), (1, 500), (1, 500), (2, 320)])], 6, 2, 64, 32, "f32"),
+    ([(640, [(2, 33), *ONE(*[700] * 20)]), (160, ONE(170, 100, 180)), (96, [(1, 95), (1, 96), (30, 130)])], 16, 2, 256, 32, "bf16"),
+    ([(4000, [(1, 2000), (1, 3999), *ONE(*range(4001, 4150, 2)), (5, 60)])], 32, 8, 128, 64, "bf16"),   # two row blocks
+    ([(320, ONE(40, 120, 90))], 16, 2, 64, 16, "f16"),                                     # all of them end in it
+]
+
+
+@pytest.mark.parametrize("wide", [True, False])
+@pytest.mark.parametrize("fill", [-1, 0])
+@pytest.mark.parametrize("case", SHORT, ids=lambda c: "-".join(str(x).replace(" ", "")[:60] for x in c))
+def test_a_short_request_comes_first(case, fill, wide):
+    """Every row lists the pages of its own tokens, and no more."""
+    groups, h, hk, d, page, typ = case
+    b = batch(groups, h, hk, d, page, typ, seed=h + d, wide=wide)
+    refs = reference(b)
+    kv = torch.tensor(b["kv_lens"], device=DEV)
+    past = torch.arange(b["table"].shape[1], device=DEV)[None] * page >= kv[:, None]
+    b["table"] = b["table"].masked_fill(past, fill)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    check_attn(run(b, dev_status=status), refs, typ)
+    assert int(status.item()) == 0
