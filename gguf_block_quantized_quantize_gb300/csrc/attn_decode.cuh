@@ -189,13 +189,20 @@ __device__ __forceinline__ AdReq pf_request(const AdShape &a, int e) {
     const Attn &p = a.p;
     const int4 u = reinterpret_cast<const int4 *>(pf_entries(a.pf) + e)[0], v = reinterpret_cast<const int4 *>(pf_entries(a.pf) + e)[1];
     o.rows0 = u.x;
-    const int32_t tile0 = max(u.z, 0), tile1 = max(min(u.w, a.pf.tiles), tile0);
-    const int64_t rows = (int64_t)u.y * a.G;
+    const int32_t tile0 = max(u.z, 0);
+    int32_t tile1 = max(min(u.w, a.pf.tiles), tile0);
+    o.q = u.y;
+    o.pos_max = v.y;
+    if (e < p.R && u.y > p.max_q) {   // the first max_q of a request's queries (the join leaves out the others of a group's)
+        o.q = (int32_t)p.max_q;
+        o.pos_max = v.x + o.q - 1;
+        tile1 = max(min(tile1, o.pos_max >= 0 ? o.pos_max / KV_TILE + 1 : 0), tile0);
+    }
+    const int64_t rows = (int64_t)o.q * a.G;
     const bool mine = u.x >= 0 && u.y > 0 && (int64_t)u.x + u.y <= p.n_tokens && rows > a.min_rows && rows <= a.max_rows &&
                       v.z >= 0 && v.z < p.R;
-    o.q = mine ? u.y : 0;
+    o.q = mine ? o.q : 0;
     o.pos0 = v.x;
-    o.pos_max = v.y;
     o.row = v.z;
     o.n_sink = 0;
     o.s_tile = o.w_tile = tile0;

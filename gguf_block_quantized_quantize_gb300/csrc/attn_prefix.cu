@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(PF_THREADS) prefix_join_kernel(const AdShape a
     if (r < 0 || r >= p.R) return;
     const bool grouped = ge >= p.R && ge < a.pf.n_entries;
     const AdReq q0 = pf_request(a, r), q1 = pf_request(a, grouped ? ge : r);
+    if (t - q0.rows0 >= q0.q) return;   // past the request's max_q first queries
     PfPieces x[2];
     x[0] = pf_pieces<D>(a, q0, own, own_next, t, head, few, rg);
     x[1] = PfPieces{};

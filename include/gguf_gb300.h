@@ -794,9 +794,12 @@ gguf_status gguf_prefix_plan(const int32_t *q_start, const int32_t *kv_len, int6
  *   plan : made by gguf_prefix_plan, on this stream or complete, with these n_requests,
  *          n_groups, n_tokens and page_size: plan_bytes, at least gguf_prefix_plan_bytes of
  *          them.  A plan of other sizes gives unspecified outputs.
+ *   max_q_len : of a request with more queries the first max_q_len are computed, as there.
  *   dev_status : + pages outside the cache or past the table, each once per request whose
  *          queries would see a token of it, or once for the requests of a group together (of
  *          a length past its table's row, those of 2^20 tokens more where tokens are read together).
+ *          Where tokens are read together, a group's pages count from the first to the last that its
+ *          queries see, queries past max_q_len among them.
  *   ws   : gguf_prefix_attention_ws_size(args, n_groups) bytes, 16-byte aligned: about
  *          8 (head_dim + 4) bytes per token and head, and up to 32 MB.
  * n_tokens x n_heads <= 2^30, and 2^40 tiles of 16 tokens, 2^16 more a row than the table

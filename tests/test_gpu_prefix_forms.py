@@ -117,3 +117,36 @@ def test_a_short_request_comes_first(case, fill, wide):
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
     check_attn(run(b, dev_status=status), refs, typ)
     assert int(status.item()) == 0
+
+
+# ---------------------------------------------------------------- max_q_len
+
+LONG = [
+    # groups, h, hk, d, page, type
+    ([(320, [(1, 400), (5, 350), (9, 330), (1, 321)]), (None, [(7, 100), (2, 50), (60, 300)])], 8, 2, 64, 16, "bf16"),
+    ([(320, [(1, 400), (5, 350), (70, 500), (2, 321)])], 24, 8, 128, 32, "f16"),
+    ([(320, [(1, 400), (5, 350), (33, 390), (2, 321)]), (None, [(7, 100), (2, 1)])], 6, 2, 64, 16, "f32"),
+    ([(160, [(40, 300)] * 12)], 8, 1, 256, 16, "bf16"),
+]
+
+
+@pytest.mark.parametrize("wide", [True, False])
+@pytest.mark.parametrize("most", [1, 3, 6])
+@pytest.mark.parametrize("case", LONG, ids=lambda c: "-".join(str(x).replace(" ", "")[:60] for x in c))
+def test_more_queries_than_max_q_len(case, most, wide):
+    """Of a request with more queries than max_q_len the first max_q_len are computed, however the call goes, and the
+    other rows of out stay as they are."""
+    groups, h, hk, d, page, typ = case
+    b = batch(groups, h, hk, d, page, typ, seed=h + d, wide=wide)
+    refs = reference(b)
+    mine = torch.cat([torch.arange(n) < most for n in b["q_lens"]])
+    b["table"] = b["table"].masked_fill(torch.from_numpy(~seen_pages(b, 0, 0, most)).to(DEV), -1)   # (for the other queries alone)
+    for call in (run, paged):
+        out = torch.full_like(b["q"], 7.0)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        call(b, max_q=most, out=out, dev_status=status)
+        check_attn(out[mine.to(DEV)], [x[mine] for x in refs], typ)
+        assert bool((out[~mine.to(DEV)] == 7).all())
+        assert int(status.item()) == 0
+    if wide:
+        assert reads_together(b, most)
