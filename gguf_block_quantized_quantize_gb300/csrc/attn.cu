@@ -66,7 +66,7 @@ static AttnPlan attn_plan(const Attn &p, int64_t d) {
 
 size_t attn_ws_size(const Attn &p, int64_t d) { return attn_plan(p, d).bytes; }
 
-cudaError_t launch_attn(const Attn &p, int64_t d, void *ws, cudaStream_t s) {
+cudaError_t launch_attn(const Attn &p, int64_t d, void *ws, cudaStream_t s, const int32_t *plan, int64_t entries) {
     const AttnPlan x = attn_plan(p, d);
     const int64_t es = p.qt == GGUF_F32 ? 4 : 2;
     AdShape a{};
@@ -75,6 +75,8 @@ cudaError_t launch_attn(const Attn &p, int64_t d, void *ws, cudaStream_t s) {
     a.part = (float *)ws;
     a.meta = (AdMeta *)((uint8_t *)ws + x.meta);
     a.err = tg_error_word();
+    a.pf.plan = plan;
+    a.pf.n_entries = (int32_t)entries;
     auto shift_of = [](int32_t v) { return (v & (v - 1)) == 0 ? __builtin_ctz(v) : -1; };
     a.G = (int32_t)(p.h / p.hk);
     a.hk = (int32_t)p.hk;
@@ -92,6 +94,7 @@ cudaError_t launch_attn(const Attn &p, int64_t d, void *ws, cudaStream_t s) {
         e = d == 64 ? launch_attn_decode_64(a, x.nt, x.ctas, s)
           : d == 128 ? launch_attn_decode_128(a, x.nt, x.ctas, s) : launch_attn_decode_256(a, x.nt, x.ctas, s);
     if (e != cudaSuccess || !x.prefill) return e;
+    a.pf.chained = x.decode;
     a.min_rows = a.max_rows;
     a.max_rows = 0x7fffffff;
     return d == 64 ? launch_attn_prefill_64(a, x.ctas, s)

@@ -96,7 +96,7 @@ struct PfEntry {
 // like records, for a unit that began before it.
 struct PfShape {
     const int32_t *plan;       // header, entries, of each token its position, and its request and group (pf_pack), q_start, kv_len
-    int32_t n_entries, chained;   // chained: the decode kernel follows the prefill kernel of the call
+    int32_t n_entries, chained;   // chained: the decode kernel follows the prefill kernel of the call; one by one, the other way round
     int32_t parts, pieces;     // slots of the decode kernel, of the prefill kernel
     int32_t tiles;             // that an entry has at most, whatever its lengths say
     float *records;
@@ -129,7 +129,7 @@ struct AdShape {
     int32_t whole;                // each CTA takes one whole unit (few short ones), and nothing is left to join
     float *part;                  // CTA-level partial results, two slots per CTA
     AdMeta *meta;                 // per CTA: the unit that goes on past it
-    PfShape pf;                   // gguf_prefix_attention alone
+    PfShape pf;                   // gguf_prefix_attention; else (and but for the plan, one by one) zeros
     int *err;                     // error word: a wait for a copy was given up
 };
 
@@ -364,8 +364,10 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
-// PRE: a launch of gguf_prefix_attention, whose units leave records and slots instead of outputs
-template <int D, int QT, int NT, bool PRE>
+// PRE: a launch of gguf_prefix_attention, whose units leave records and slots instead of outputs.  FED: a launch of its requests
+// one by one, whose q_start and kv_len lie in the plan: none is taken where that is of other sizes.  (Asked by every launch it
+// cost calls of 8 us 0.2.)
+template <int D, int QT, int NT, bool PRE, bool FED>
 __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kernel(const AdShape a) {
     using C = AdCfg<D, QT, NT>;
     using L = KvTile<D>;
@@ -402,7 +404,9 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     // takes one whole unit) and, once the sum of what comes before is known, writes down where the warps start whose
     // first tile lies in them.
     constexpr int NTHR = C::THREADS;
-    const int R = ad_requests<PRE>(a), per = (R + NTHR - 1) / NTHR, r0 = tid * per, r1 = min(R, r0 + per);
+    const bool lost = FED && !pf_plan_fits(a);
+    const int R = ad_requests<PRE>(a), per = (R + NTHR - 1) / NTHR, r0 = tid * per, r1 = lost ? r0 : min(R, r0 + per);
+    if (lost && blockIdx.x == 0 && tid == 0 && p.status != nullptr) atomicAdd(p.status, 1);
     AdReq rq{};
     int64_t mine = 0;
     bool fits = true;   // (the entries are there to be read in any case)
@@ -1125,7 +1129,7 @@ static cudaError_t attn_decode_run(const AdShape &shape, int ctas, cudaStream_t 
     a.whole = units <= ctas && span <= 2048;
     if (a.whole) ctas = (int)units;
     cudaError_t err = cudaSuccess;
-    const void *kern = (const void *)attn_decode_kernel<D, QT, NT, false>;
+    const void *kern = a.pf.plan ? (const void *)attn_decode_kernel<D, QT, NT, false, true> : (const void *)attn_decode_kernel<D, QT, NT, false, false>;
     if (kernel_occupancy(kern, C::THREADS, C::SMEM, &err) == 0) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
@@ -1137,7 +1141,8 @@ static cudaError_t attn_decode_run(const AdShape &shape, int ctas, cudaStream_t 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, QT, NT, false>, a);
+    void *args[1] = {&a};
+    cudaError_t e = cudaLaunchKernelExC(&cfg, kern, args);
     if (e != cudaSuccess || a.whole) return e;
     cfg.gridDim = dim3((unsigned)ctas, C::RG);
     cfg.blockDim = dim3(AC_THREADS);
@@ -1150,7 +1155,7 @@ template <int D, int QT, int NT>
 static cudaError_t attn_prefix_decode_run(const AdShape &a, int ctas, cudaStream_t s) {
     using C = AdCfg<D, QT, NT>;
     cudaError_t err = cudaSuccess;
-    if (kernel_occupancy((const void *)attn_decode_kernel<D, QT, NT, true>, C::THREADS, C::SMEM, &err) == 0) return err;
+    if (kernel_occupancy((const void *)attn_decode_kernel<D, QT, NT, true, false>, C::THREADS, C::SMEM, &err) == 0) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(C::THREADS);
@@ -1161,7 +1166,7 @@ static cudaError_t attn_prefix_decode_run(const AdShape &a, int ctas, cudaStream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, QT, NT, true>, a);
+    return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, QT, NT, true, false>, a);
 }
 
 }  // namespace gg

@@ -284,7 +284,7 @@ struct ApUnpack {
     }
 };
 
-template <int D, int QT, int MODE>
+template <int D, int QT, int MODE, bool FED>   // FED: as attn_decode_kernel's
 __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdShape a) {
     constexpr bool CUT = MODE == AP_CUT, PRE = MODE == AP_PRE, PARTS = MODE != AP_PLAIN;
     using C = ApCfg<D, QT>;
@@ -330,7 +330,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     // Work of all requests: thread t counts requests [t * per, (t + 1) * per), in row blocks of ROWS rows, and of 128.
     // The larger ones unpack a key for twice the rows; the smaller ones are for calls that would leave SMs idle, as are
     // row blocks whose tokens are cut into pieces (CUT; of 4 blocks at least, joined by a second launch).
-    const int R = ad_requests<PRE>(a), per = (R + AP_THREADS - 1) / AP_THREADS;
+    const bool lost = FED && !pf_plan_fits(a);
+    const int R = lost ? 0 : ad_requests<PRE>(a), per = (R + AP_THREADS - 1) / AP_THREADS;
     auto blocks_of = [](const AdReq &q) { return (q.nt + BT / KV_TILE - 1) / (BT / KV_TILE); };
     int own = 0;   // (PRE) blocks of the CTA
     int64_t pre_total = 0;
@@ -381,6 +382,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         }
         // (the first item begins behind a barrier)
     } else {
+        if (lost && !a.pf.chained && blockIdx.x == 0 && tid == 0 && p.status != nullptr) atomicAdd(p.status, 1);
         int item_rows = ROWS, splits = 1;
         int mine = 0, mine128 = 0;   // (tokens x heads / 128 is below 2^31)
         for (int r = tid * per; r < min(R, (tid + 1) * per); r++) {
@@ -1040,14 +1042,14 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
 // The pieces of row blocks whose tiles were cut: a warp per query row and head
 // joins them in order (5 requests of up to 66 tokens, 32 heads of 256 after 3032:
 // 141 us uncut, 106 us with it).
-template <int D, int QT>
+template <int D, int QT, bool FED>
 __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const AdShape a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Attn &p = a.p;
     const int64_t w = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5, t = w / p.h;
     const int head = (int)(w - t * p.h), lane = threadIdx.x & 31;
-    if (t >= p.n_tokens || t < p.q_start[0]) return;
+    if (t >= p.n_tokens || (FED && !pf_plan_fits(a)) || t < p.q_start[0]) return;
     int r = 0;   // the last request that starts at or before t
     for (int lo = 0, hi = (int)p.R; hi - lo > 1;) {
         const int mid = (lo + hi) >> 1;
@@ -1091,10 +1093,10 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const AdShape a)
     }
 }
 
-template <int D, int QT, int MODE>
+template <int D, int QT, int MODE, bool FED>
 static cudaError_t attn_prefill_launch(const AdShape &a, int ctas, cudaStream_t s) {
     cudaError_t err = cudaSuccess;
-    if (kernel_occupancy((const void *)attn_prefill_kernel<D, QT, MODE>, AP_THREADS, ApCfg<D, QT>::SMEM, &err) == 0) return err;
+    if (kernel_occupancy((const void *)attn_prefill_kernel<D, QT, MODE, FED>, AP_THREADS, ApCfg<D, QT>::SMEM, &err) == 0) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(AP_THREADS);
@@ -1105,20 +1107,21 @@ static cudaError_t attn_prefill_launch(const AdShape &a, int ctas, cudaStream_t 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D, QT, MODE>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D, QT, MODE, FED>, a);
     if constexpr (MODE == AP_CUT) {
         if (e != cudaSuccess) return e;
         cfg.gridDim = dim3((unsigned)((a.p.n_tokens * a.p.h + 7) / 8));
         cfg.blockDim = dim3(256);
         cfg.dynamicSmemBytes = 0;
-        return cudaLaunchKernelEx(&cfg, attn_prefill_join_kernel<D, QT>, a);
+        return cudaLaunchKernelEx(&cfg, attn_prefill_join_kernel<D, QT, FED>, a);
     } else return e;
 }
 
 // Two builds of the kernel: what cutting adds costs its spare registers (8192 tokens: 664 us with it, 644 without).
 template <int D, int QT>
 static cudaError_t attn_prefill_run(const AdShape &a, int ctas, cudaStream_t s) {
-    return a.max_splits > 1 ? attn_prefill_launch<D, QT, AP_CUT>(a, ctas, s) : attn_prefill_launch<D, QT, AP_PLAIN>(a, ctas, s);
+    if (a.pf.plan) return a.max_splits > 1 ? attn_prefill_launch<D, QT, AP_CUT, true>(a, ctas, s) : attn_prefill_launch<D, QT, AP_PLAIN, true>(a, ctas, s);
+    return a.max_splits > 1 ? attn_prefill_launch<D, QT, AP_CUT, false>(a, ctas, s) : attn_prefill_launch<D, QT, AP_PLAIN, false>(a, ctas, s);
 }
 
 }  // namespace gg

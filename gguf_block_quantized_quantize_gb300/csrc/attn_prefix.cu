@@ -375,7 +375,7 @@ cudaError_t launch_prefix_attn(const Attn &p, const void *plan, int64_t NG, int6
         Attn one = p;
         one.q_start = (const int32_t *)plan + pf_lengths_at(p.R, NG, p.n_tokens);
         one.kv_len = one.q_start + p.R + 1;
-        return launch_attn(one, d, ws, s);
+        return launch_attn(one, d, ws, s, (const int32_t *)plan, p.R + NG);
     }
     uint8_t *w = (uint8_t *)ws;
     AdShape a{};

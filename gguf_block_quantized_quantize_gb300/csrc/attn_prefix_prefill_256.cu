@@ -6,7 +6,7 @@ namespace gg {
 
 cudaError_t launch_prefix_prefill_256(const AdShape &a, int ctas, cudaStream_t s) {
     static_assert(ApCfg<256, GGUF_BF16>::RT * 128 == (256 == 256 ? 128 : 256) && ApCfg<256, GGUF_BF16>::GT == (256 == 256 ? 4 : 8), "as the join has them");
-    return a.p.qt == GGUF_F16 ? attn_prefill_launch<256, GGUF_F16, AP_PRE>(a, ctas, s) : attn_prefill_launch<256, GGUF_BF16, AP_PRE>(a, ctas, s);
+    return a.p.qt == GGUF_F16 ? attn_prefill_launch<256, GGUF_F16, AP_PRE, false>(a, ctas, s) : attn_prefill_launch<256, GGUF_BF16, AP_PRE, false>(a, ctas, s);
 }
 
 }  // namespace gg

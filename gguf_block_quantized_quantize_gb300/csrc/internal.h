@@ -276,7 +276,8 @@ struct Attn {   // gguf_paged_attention
     int32_t *status;
 };
 size_t attn_ws_size(const Attn &p, int64_t d);
-cudaError_t launch_attn(const Attn &p, int64_t d, void *ws, cudaStream_t s);
+// plan: of gguf_prefix_plan, in which p.q_start and p.kv_len lie, with its entries; no request is taken where it is of other sizes
+cudaError_t launch_attn(const Attn &p, int64_t d, void *ws, cudaStream_t s, const int32_t *plan = nullptr, int64_t entries = 0);
 
 // gguf_prefix_plan and gguf_prefix_attention (Attn's q_start and kv_len are in the plan; NG groups)
 int64_t prefix_plan_bytes(int64_t R, int64_t NG, int64_t n_tokens);

@@ -793,7 +793,7 @@ gguf_status gguf_prefix_plan(const int32_t *q_start, const int32_t *kv_len, int6
  *          are read together: one much wider than the requests need costs short calls time.
  *   plan : made by gguf_prefix_plan, on this stream or complete, with these n_requests,
  *          n_groups, n_tokens and page_size: plan_bytes, at least gguf_prefix_plan_bytes of
- *          them.  A plan of other sizes gives unspecified outputs.
+ *          them.  Of a plan of other sizes nothing is written, and it counts in dev_status, once.
  *   max_q_len : of a request with more queries the first max_q_len are computed, as there.
  *   dev_status : + pages outside the cache or past the table, each once per request whose
  *          queries would see a token of it, or once for the requests of a group together (of

@@ -150,3 +150,32 @@ def test_more_queries_than_max_q_len(case, most, wide):
         assert int(status.item()) == 0
     if wide:
         assert reads_together(b, most)
+
+
+# ---------------------------------------------------------------- plans of other sizes
+
+@pytest.mark.parametrize("groups, h, d, typ", [
+    ([(64, ONE(70, 80, 90, 100, 77, 88))], 8, 64, "bf16"),           # few rows, a CTA per unit
+    ([(64, ONE(70, 80, 90, 3000, 77, 88))], 8, 64, "f32"),           # units over several CTAs
+    ([(64, [(30, 120), (1, 80), (40, 90)])], 8, 128, "f16"),         # both kernels, row blocks in pieces
+    ([(64, [(2, 500)] + [(2, 70 + r) for r in range(47)])], 64, 256, "bf16"),   # the prompt kernel alone, in pieces
+])
+def test_another_plan_one_by_one(groups, h, d, typ):
+    """A plan of other sizes, where the requests go one by one: nothing is written, and it is counted once."""
+    b = batch(groups, h, 2, d, 16, typ, wide=False)
+    refs = reference(b)
+    t, most = b["q"].shape[0], max(b["q_lens"])
+    assert not reads_together(b, most)
+    make = lambda page=16, n=t, ng=1: g.gguf_prefix_plan(b["start"], b["kv_len"], b["gs"][:ng + 1], b["prefix"][:ng], page, n)   # noqa: E731
+    out = torch.full_like(b["q"], 7.0)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    call = lambda plan: g.gguf_prefix_attention(b["q"], b["cache"], b["table"], plan, 1, 2, 16, most, b["scale"], out=out,   # noqa: E731
+                                                dev_status=status)
+    fewer = torch.zeros_like(make())
+    fewer[:make(ng=0).numel()] = make(ng=0)   # of no group, in room for one
+    for i, plan in enumerate((make(page=32), make(n=t + 1), fewer, torch.zeros_like(make()))):
+        call(plan)
+        assert bool((out == 7).all()) and int(status.item()) == i + 1
+    call(make())
+    check_attn(out, refs, typ)
+    assert int(status.item()) == 4
