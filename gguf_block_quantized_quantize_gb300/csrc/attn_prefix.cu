@@ -345,15 +345,18 @@ static PfRun prefix_run(const Attn &p, int64_t NG, int64_t d) {
     x.rg = p.qt != GGUF_F32 && d != 256 && G * p.max_q > 8 ? 16 : 8;
     x.tc = p.qt != GGUF_F32 && p.n_tokens * G > x.rg;
     x.few = x.tc ? x.rg : 0x7fffffff;
-    // Sharing has a price, the launches, starts and joins of its kernels: about 40 us in all (20 us for fp32 queries, which
-    // one kernel takes).  What the requests cost one by one, 10 us and 0.42 ns a tile of heads of 128 (more for 16 rows and
-    // for fp32 queries), is known up to the width of the table: where that is less, they go so.  Measured, one by one and
-    // shared: 2 x (700 + 60) tokens, fp32, 8 KV heads of 128: 12.5 and 21 us; 38 requests of 6 groups, 5300 tokens, 2 of 256:
-    // 35 and 47 us; 32 x (8192 + 512), 8 of 128: 69 and 42 us; 256 x (32768 + 128): 1690 and 191 us.
+    // Sharing has a price, the launches, starts and joins of its kernels: about 33 us in all (45 with heads of 256; 20 us for
+    // fp32 queries, which one kernel takes).  What the requests cost one by one, 10 us and 0.42 ns a tile of heads of 128 (more
+    // for 16 rows and for fp32 queries), is known up to the width of the table and of the window: where that is less, they go
+    // so, as they do where there are no two requests of a group.  Measured without the plan, one by one and shared: 2 x (700 +
+    // 60) tokens, fp32, 8 KV heads of 128: 12.9 and 18.2 us; 38 requests of 6 groups, 5300 tokens, 2 of 256: 35 and 42 us; 8 KV
+    // heads of 128, 16 x (8192 + 200): 41 and 34 us; 32 x (8192 + 512): 69 and 39 us; 64 x (32768 + 200) with a window of 1024:
+    // 31 and 38 us; 64 x (16384 + 200) with one of 4096, 8 of 64: 47 and 36 us; 256 x (32768 + 128): 1690 and 183 us.
+    const int64_t most = p.window > 0 ? std::min(p.width * p.page, p.window + p.sinks + p.max_q + 3 * KV_TILE) : p.width * p.page;
     const double tiles = (double)p.R * (double)p.hk * (double)((G * std::min(p.max_q, p.n_tokens) + x.rg - 1) / x.rg) *
-                         (double)(p.width * p.page / KV_TILE);
+                         (double)(most / KV_TILE);
     const double us = 10.0 + tiles * 0.42e-3 * (double)d / 128.0 * (x.rg == 16 ? 1.4 : 1.0) * (p.qt == GGUF_F32 ? 1.9 : 1.0);
-    x.alone = us < (x.tc ? 40.0 : 20.0);
+    x.alone = NG == 0 || p.R < 2 || us < (!x.tc ? 20.0 : d == 256 ? 45.0 : 33.0);
     if (x.alone) {
         x.bytes = attn_ws_size(p, d);
         return x;

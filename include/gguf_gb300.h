@@ -789,8 +789,9 @@ gguf_status gguf_prefix_plan(const int32_t *q_start, const int32_t *kv_len, int6
  * bound them, goes so).  Every row of the block table lists all pages of its request, the
  * shared ones too; the outputs are gguf_paged_attention's on this table, in other bits.
  *   args : as gguf_paged_attention; q_start and kv_len are not looked at (they are in the
- *          plan).  The table's width decides, with the other sizes, whether the shared tokens
- *          are read together: one much wider than the requests need costs short calls time.
+ *          plan).  The table's width decides, with the window and the other sizes, whether the
+ *          shared tokens are read together (never without groups, or for one request): one much
+ *          wider than the requests need costs short calls time.
  *   plan : made by gguf_prefix_plan, on this stream or complete, with these n_requests,
  *          n_groups, n_tokens and page_size: plan_bytes, at least gguf_prefix_plan_bytes of
  *          them.  Of a plan of other sizes nothing is written, and it counts in dev_status, once.

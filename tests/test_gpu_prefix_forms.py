@@ -179,3 +179,23 @@ def test_another_plan_one_by_one(groups, h, d, typ):
     call(make())
     check_attn(out, refs, typ)
     assert int(status.item()) == 4
+
+
+# ---------------------------------------------------------------- what is not shared
+
+@pytest.mark.parametrize("groups, window, sinks", [
+    ([(None, ONE(100, 200, 33, 700))], 0, 0),                 # no group
+    ([(320, [(3, 400)])], 0, 0),                              # one request
+    ([(3000, ONE(*range(3010, 3050, 10)))], 64, 4),           # a window that hides nearly all of a wide table
+])
+@pytest.mark.parametrize("typ", ["bf16", "f32"])
+def test_calls_with_nothing_to_share(groups, window, sinks, typ):
+    """They go one by one, whatever the table's width: gguf_paged_attention's workspace, and its bits."""
+    b = batch(groups, 8, 2, 128, 16, typ)
+    if groups[0][0] is None:
+        b["gs"], b["prefix"] = b["gs"][:1], b["prefix"][:0]
+    most = max(b["q_lens"])
+    assert not reads_together(b, most, window, sinks)
+    out = run(b, window, sinks)
+    check_attn(out, reference(b, window, sinks), typ)
+    assert torch.equal(out, paged(b, most, window, sinks))
