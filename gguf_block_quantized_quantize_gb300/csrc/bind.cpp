@@ -57,7 +57,10 @@ struct Bad {};   // a Python exception is set
     PyErr_Format(PyExc_ValueError, "%s: %s must be %s", what, name, want);
     throw Bad();
 }
-thread_local int device_of_call = -1;   // of the call's first tensor
+// The device of the call's tensors: ANY (the calls of the cache itself: what the current device can read), or ONE, that of
+// the first
+constexpr int ANY = -2, ONE = -1;
+thread_local int device_of_call = ANY;
 const at::Tensor &tensor(PyObject *o, const char *what, const char *name) {
     if (!THPVariable_Check(o)) refuse(what, name, "a tensor");
     const at::Tensor &t = THPVariable_Unpack(o);
@@ -65,8 +68,8 @@ const at::Tensor &tensor(PyObject *o, const char *what, const char *name) {
         PyErr_SetString(PyExc_ValueError, "gguf: tensors must live on a CUDA device");
         throw Bad();
     }
-    if (device_of_call < 0) device_of_call = t.get_device();
-    if (t.get_device() != device_of_call) refuse(what, name, "on the device of the call's other tensors");
+    if (device_of_call == ONE) device_of_call = t.get_device();
+    if (device_of_call != ANY && t.get_device() != device_of_call) refuse(what, name, "on the device of the call's other tensors");
     return t;
 }
 int64_t integer(PyObject *o) {
@@ -154,8 +157,8 @@ void count(Py_ssize_t n, Py_ssize_t want, const char *what) {
     throw Bad();
 }
 template <class F>
-PyObject *guarded(F f) {
-    device_of_call = -1;
+PyObject *guarded(F f, int devices = ANY) {
+    device_of_call = devices;
     try {
         return f();
     } catch (const Bad &) {
@@ -275,7 +278,7 @@ PyObject *qk_norm_mrope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         axes.ld_positions = axes.n_axes > 1 ? pos.stride(0) : x.n_tokens;
         axes.interleaved = static_cast<int>(integer(a[17]));
         return PyLong_FromLong(api.mrope(&x, &axes, stream(a[15])));
-    });
+    }, ONE);
 }
 
 // [tokens, k] with contiguous rows, or none
@@ -353,7 +356,7 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
             x.z_q8_1 = q.data_ptr();
         }
         return PyLong_FromLong(api.norm(&x, stream(a[17])));
-    });
+    }, ONE);
 }
 
 // cache, slots, n_kv_heads, head_dim, page, k, v, stream
@@ -458,7 +461,7 @@ PyObject *prefix_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                          stream(a[7]));
         if (a[6] != Py_None) Py_INCREF(a[6]);
         return status_or(st, a[6] != Py_None ? a[6] : THPVariable_Wrap(made));
-    });
+    }, ONE);
 }
 
 // q, cache, table, plan, n_groups, n_kv_heads, page, max_q_len, scale, window, sinks, out, ws (None: they are made), status, stream
@@ -499,7 +502,7 @@ PyObject *prefix_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (st != GGUF_OK) return PyLong_FromLong(st);
         Py_INCREF(out.p);
         return out.p;
-    });
+    }, ONE);
 }
 
 // the addresses of gguf_kv_plan, gguf_qk_norm_rope, gguf_kv_get_rows, gguf_paged_attention_ws_size, gguf_paged_attention,
