@@ -199,3 +199,20 @@ def test_calls_with_nothing_to_share(groups, window, sinks, typ):
     out = run(b, window, sinks)
     check_attn(out, reference(b, window, sinks), typ)
     assert torch.equal(out, paged(b, most, window, sinks))
+
+
+# ---------------------------------------------------------------- fp32 over long prefixes
+
+@pytest.mark.parametrize("members, h, hk, d, prefix", [(40, 24, 8, 64, 30000), (60, 12, 4, 128, 16000), (30, 8, 2, 256, 12000)])
+def test_long_prefixes_in_fp32(members, h, hk, d, prefix):
+    """What the matrix unit cuts off of a sum, always towards zero, does not add up along the prefix.  A tile's products are
+    cut off three times, by 2^-23 of them at most; probabilities and values stand in two parts, each pair right to 2^-23:
+    together (5 x 2^-23) below 2^-20 of the outputs, along them."""
+    b = batch([(prefix, ONE(*range(prefix + 1, prefix + 1 + members)))], h, hk, d, 16, "f32", seed=d)
+    refs = reference(b)
+    assert reads_together(b, 1)
+    got = run(b)
+    check_attn(got, refs, "f32")
+    err = got.double().cpu() - refs[0]
+    along = float((err * refs[0]).sum() / refs[0].square().sum())
+    assert abs(along) < 2.0 ** -20
