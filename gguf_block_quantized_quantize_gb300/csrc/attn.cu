@@ -77,6 +77,7 @@ cudaError_t launch_attn(const Attn &p, int64_t d, void *ws, cudaStream_t s, cons
     a.err = tg_error_word();
     a.pf.plan = plan;
     a.pf.n_entries = (int32_t)entries;
+    a.pf.tiles = pf_most_tiles(p);
     auto shift_of = [](int32_t v) { return (v & (v - 1)) == 0 ? __builtin_ctz(v) : -1; };
     a.G = (int32_t)(p.h / p.hk);
     a.hk = (int32_t)p.hk;

@@ -143,6 +143,8 @@ struct AdReq {
     int32_t row, pos_max;         // (PRE) row of the block table, the last position of a query
     int32_t s_tile;               // (PRE; else 0)
 };
+// FED: of gguf_prefix_attention one by one, of at most a.pf.tiles tiles
+template <bool FED>
 __device__ __forceinline__ AdReq ad_request(const AdShape &a, int r) {
     AdReq o;
     const Attn &p = a.p;
@@ -160,11 +162,12 @@ __device__ __forceinline__ AdReq ad_request(const AdShape &a, int r) {
     o.pos0 = kv - (p.q_start[r + 1] - o.rows0);
     const int32_t last = o.pos0 + o.q - 1;
     if (o.q > 0 && last >= 0) {
-        const int32_t end = last / KV_TILE + 1;
+        const int32_t end = FED ? min(last / KV_TILE + 1, a.pf.tiles) : last / KV_TILE + 1;
         o.nt = end;
         if (p.window > 0) {
             const int64_t w0 = (int64_t)o.pos0 - p.window + 1;
             o.w_tile = w0 > 0 ? (int32_t)(w0 / KV_TILE) : 0;
+            if (FED) o.w_tile = min(o.w_tile, end);
             o.n_sink = (int32_t)min((p.sinks + KV_TILE - 1) / KV_TILE, (int64_t)o.w_tile);
             o.nt = o.n_sink + end - o.w_tile;
         }
@@ -214,10 +217,10 @@ __device__ __forceinline__ AdReq pf_request(const AdShape &a, int e) {
     o.nt = o.q > 0 ? o.n_sink + tile1 - o.w_tile : 0;
     return o;
 }
-template <bool PRE>
+template <bool PRE, bool FED>
 __device__ __forceinline__ AdReq ad_request_of(const AdShape &a, int r) {
     if constexpr (PRE) return pf_request(a, r);
-    else return ad_request(a, r);
+    else return ad_request<FED>(a, r);
 }
 template <bool PRE>
 __device__ __forceinline__ int ad_requests(const AdShape &a) { return PRE ? a.pf.n_entries : (int)a.p.R; }
@@ -345,14 +348,14 @@ struct AdCursor {
     AdReq q;
 };
 // the next unit with tiles
-template <int RG, bool PRE>
+template <int RG, bool PRE, bool FED>
 __device__ __forceinline__ void ad_next_unit(const AdShape &a, AdCursor &c) {
     c.tile = 0;
     if (++c.u < (c.q.q * a.G + RG - 1) / RG * a.hk) return;
     c.u = 0;
     do {
         if (++c.r >= ad_requests<PRE>(a)) return;
-        c.q = ad_request_of<PRE>(a, c.r);
+        c.q = ad_request_of<PRE, FED>(a, c.r);
     } while (c.q.nt == 0);
 }
 
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     bool fits = true;   // (the entries are there to be read in any case)
     if constexpr (PRE) fits = pf_plan_fits(a);
     for (int r = r0; r < r1; r++) {
-        rq = ad_request_of<PRE>(a, r);
+        rq = ad_request_of<PRE, FED>(a, r);
         if (PRE && !fits) rq.q = rq.nt = 0;
         mine += ad_units(a, rq, RG) * (!PRE && a.whole ? 1 : rq.nt);
         if (!PRE && rq.q > 0 && rq.nt == 0) blind = 1;   // (every writer writes the same)
@@ -452,7 +455,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     int64_t per_warp = PRE ? even : ad_div(cta1 - cta0 + C::WARPS - 1, C::WARPS);
     for (int r = r0; r < r1; r++) {
         if (per > 1) {
-            rq = ad_request_of<PRE>(a, r);
+            rq = ad_request_of<PRE, FED>(a, r);
             if (PRE && !fits) rq.q = rq.nt = 0;
         }
         const int64_t units = ad_units(a, rq, RG), n = units * (!PRE && a.whole ? 1 : rq.nt);
@@ -488,7 +491,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     auto start_of = [&](int w) {
         AdCursor c;
         c.r = start_r[w];
-        c.q = ad_request_of<PRE>(a, c.r);
+        c.q = ad_request_of<PRE, FED>(a, c.r);
         if constexpr (PRE) c.u = (int)ad_div(start_at[w], c.q.nt);
         else c.u = (int)((uint32_t)start_at[w] / (uint32_t)c.q.nt);
         c.tile = (int)(start_at[w] - (At)c.u * c.q.nt);
@@ -530,7 +533,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
             }
             idle_since = 0;
             if (go && unit == 0) {
-                if (feed.tile == feed.q.nt) ad_next_unit<RG, PRE>(a, feed);
+                if (feed.tile == feed.q.nt) ad_next_unit<RG, PRE, FED>(a, feed);
                 unit = min(tiles, feed.q.nt - feed.tile);
                 if (PRE && of != feed.r) rows_of = !any_short || feed.r < p.R ? feed.q.row : pf_row(a, feed.q, l8, 8, 0xffu << (lane & 24));
                 head = p.cache + (int64_t)(feed.u % a.hk) * tpp * L::BYTES;
@@ -977,7 +980,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
                         }
                     }
             }
-            if (left_tiles > 0) ad_next_unit<RG, PRE>(a, cur);
+            if (left_tiles > 0) ad_next_unit<RG, PRE, FED>(a, cur);
         }
     }
     if constexpr (PRE) {   // what follows this launch may count on the prefill kernel's records too
@@ -1068,7 +1071,7 @@ __global__ void __launch_bounds__(AdCfg<D, QT, NT>::THREADS, 1) attn_decode_kern
     }
     // ---- queries that see no token
     for (int r = blockIdx.x * C::WARPS + warp; blind && r < R; r += gridDim.x * C::WARPS) {
-        const AdReq q = ad_request(a, r);
+        const AdReq q = ad_request<FED>(a, r);
         if (q.nt > 0) continue;
         const int64_t n = (int64_t)q.q * p.h * (D / 4);
         for (int64_t i = lane; i < n; i += 32)

@@ -157,8 +157,9 @@ __device__ __forceinline__ bool pf_first_sight(const AdShape &a, const ApItem &w
     return w.row0 == 0 && ad_starts_page(a, q, i);
 }
 // whether `tile` is the first of its page that the request's queries see, and no row block before this one sees it
+template <bool FED>
 __device__ __forceinline__ bool ap_first_sight(const AdShape &a, const ApItem &w, int tile) {
-    const AdReq q = ad_request(a, w.r);
+    const AdReq q = ad_request<FED>(a, w.r);
     if (w.row0 > 0) {
         const int before = q.pos0 + (w.row0 - 1) / a.G;   // the position of the row before
         if (before >= 0 && tile <= before / KV_TILE) return false;
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
         int item_rows = ROWS, splits = 1;
         int mine = 0, mine128 = 0;   // (tokens x heads / 128 is below 2^31)
         for (int r = tid * per; r < min(R, (tid + 1) * per); r++) {
-            const AdReq q = ad_request(a, r);
+            const AdReq q = ad_request<FED>(a, r);
             mine += ap_items(a, q, ROWS);
             mine128 += ap_items(a, q, 128);
         }
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             int before = incl - mine;
             for (int r = tid * per; r < min(R, (tid + 1) * per); r++) {
                 a.item_base[r] = before;
-                before += ap_items(a, ad_request(a, r), item_rows);
+                before += ap_items(a, ad_request<FED>(a, r), item_rows);
             }
             if (tid == 0) { a.item_base[R] = item_rows; a.item_base[R + 1] = splits; a.item_base[R + 2] = from; }
         }
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             ApItem w;
             AdReq q;
             for (w.r = hi * per;; w.r++) {   // it is there: it < total
-                q = ad_request(a, w.r);
+                q = ad_request<FED>(a, w.r);
                 const int n = ap_items(a, q, item_rows);
                 if (before + n > it) break;
                 before += n;
@@ -522,11 +523,12 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
             const int last = q.pos0 + (w.row0 + w.rows - 1) / G;
             w.nt = w.n_sink = w.w_tile = w.s_tile = 0;
             if (last >= 0) {
-                const int end = last / KV_TILE + 1;
+                const int end = FED ? min(last / KV_TILE + 1, a.pf.tiles) : last / KV_TILE + 1;
                 w.nt = end;
                 if (p.window > 0) {
                     const int64_t w0 = (int64_t)w.pos0 - p.window + 1;
                     w.w_tile = w0 > 0 ? (int)(w0 / KV_TILE) : 0;
+                    if (FED) w.w_tile = min(w.w_tile, end);
                     w.n_sink = (int)min((p.sinks + KV_TILE - 1) / KV_TILE, (int64_t)w.w_tile);
                     w.nt = w.n_sink + end - w.w_tile;
                 }
@@ -1009,7 +1011,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
                     const int pi = a.tpp_shift >= 0 ? tile >> a.tpp_shift : (int)((uint32_t)tile / (uint32_t)a.tpp);
                     const int32_t pg = pi < p.width ? p.table[item.r * p.ld + pi] : -1;
                     if (pg >= 0 && pg < p.n_pages) return pg * a.page_bytes + (int64_t)(item.head * a.tpp + tile - pi * a.tpp) * L::BYTES;
-                    if (counts && item.head == 0 && p.status != nullptr && (PRE ? pf_first_sight(a, item, i) : ap_first_sight(a, item, tile)))
+                    if (counts && item.head == 0 && p.status != nullptr && (PRE ? pf_first_sight(a, item, i) : ap_first_sight<FED>(a, item, tile)))
                         atomicAdd(p.status, 1);
                     return -1;
                 };
@@ -1069,7 +1071,7 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const AdShape a)
         r = lo;
     }
     const int item_rows = a.item_base[p.R], splits = a.item_base[p.R + 1], first_cut = a.item_base[p.R + 2];
-    const AdReq q = ad_request(a, r);
+    const AdReq q = ad_request<FED>(a, r);
     if (splits == 1 || t - q.rows0 >= q.q) return;   // nothing was cut; not of the prefill kernel's, or past the rows that are computed
     const int kh = head / a.G, row = (int)(t - q.rows0) * a.G + head - kh * a.G;
     const int rb = row / item_rows, nrb = (q.q * a.G + item_rows - 1) / item_rows;

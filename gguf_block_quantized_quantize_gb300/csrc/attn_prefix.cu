@@ -352,11 +352,14 @@ static PfRun prefix_run(const Attn &p, int64_t NG, int64_t d) {
     // 60) tokens, fp32, 8 KV heads of 128: 12.9 and 18.2 us; 38 requests of 6 groups, 5300 tokens, 2 of 256: 35 and 42 us; 8 KV
     // heads of 128, 16 x (8192 + 200): 41 and 34 us; 32 x (8192 + 512): 69 and 39 us; 64 x (32768 + 200) with a window of 1024:
     // 31 and 38 us; 64 x (16384 + 200) with one of 4096, 8 of 64: 47 and 36 us; 256 x (32768 + 128): 1690 and 183 us.
+    const int64_t rows = G * std::min(p.max_q, p.n_tokens);
     const int64_t most = p.window > 0 ? std::min(p.width * p.page, p.window + p.sinks + p.max_q + 3 * KV_TILE) : p.width * p.page;
-    const double tiles = (double)p.R * (double)p.hk * (double)((G * std::min(p.max_q, p.n_tokens) + x.rg - 1) / x.rg) *
-                         (double)(most / KV_TILE);
+    const double tiles = (double)p.R * (double)p.hk * (double)((rows + x.rg - 1) / x.rg) * (double)(most / KV_TILE);
     const double us = 10.0 + tiles * 0.42e-3 * (double)d / 128.0 * (x.rg == 16 ? 1.4 : 1.0) * (p.qt == GGUF_F32 ? 1.9 : 1.0);
-    x.alone = NG == 0 || p.R < 2 || us < (!x.tc ? 20.0 : d == 256 ? 45.0 : 33.0);
+    // (one by one a request's units of 8 rows x tiles are counted in 32 bits; 16-bit queries have at most 64 rows in units)
+    const int64_t unit_rows = p.qt == GGUF_F32 ? rows : std::min<int64_t>(rows, 64);
+    const bool counted = (double)p.hk * (double)((unit_rows + 7) / 8) * (double)pf_most_tiles(p) <= 4.0e9;
+    x.alone = counted && (NG == 0 || p.R < 2 || us < (!x.tc ? 20.0 : d == 256 ? 45.0 : 33.0));
     if (x.alone) {
         x.bytes = attn_ws_size(p, d);
         return x;
@@ -396,7 +399,7 @@ cudaError_t launch_prefix_attn(const Attn &p, const void *plan, int64_t NG, int6
     a.part = (float *)(w + x.part);
     a.pieces = (float *)(w + x.pieces);
     a.pf = PfShape{(const int32_t *)plan, (int32_t)(p.R + NG), x.tc, x.ctas * ad_warps((int)d, p.qt == GGUF_F32, x.rg / 8), x.ctas,
-                   (int32_t)std::min<int64_t>(p.width * p.page / KV_TILE + PF_PAST, 1 << 27), (float *)ws};
+                   pf_most_tiles(p), (float *)ws};
     a.min_rows = x.few;
     a.max_rows = 0x7fffffff;
     if (x.tc) {

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/gguf_gb300.h"
 
 namespace gg {
@@ -285,6 +287,7 @@ cudaError_t launch_prefix_plan(const int32_t *q_start, const int32_t *kv_len, in
                                const int32_t *prefix_len, int64_t NG, int64_t page, int64_t n_tokens, void *plan, cudaStream_t s);
 size_t prefix_attn_ws_size(const Attn &p, int64_t NG, int64_t d);
 constexpr int64_t PF_PAST = 1 << 16;   // tiles past its table that a request's lengths may ask for: more are not walked over
+inline int32_t pf_most_tiles(const Attn &p) { return (int32_t)std::min<int64_t>(p.width * p.page / 16 + PF_PAST, 1 << 27); }
 cudaError_t launch_prefix_attn(const Attn &p, const void *plan, int64_t NG, int64_t d, void *ws, cudaStream_t s);
 
 }  // namespace gg

@@ -798,7 +798,7 @@ gguf_status gguf_prefix_plan(const int32_t *q_start, const int32_t *kv_len, int6
  *   max_q_len : of a request with more queries the first max_q_len are computed, as there.
  *   dev_status : + pages outside the cache or past the table, each once per request whose
  *          queries would see a token of it, or once for the requests of a group together (of
- *          a length past its table's row, those of 2^20 tokens more where tokens are read together).
+ *          a length past its table's row, those of 2^20 tokens more).
  *          Where tokens are read together, a group's pages count from the first to the last that its
  *          queries see, queries past max_q_len among them.
  *   ws   : gguf_prefix_attention_ws_size(args, n_groups) bytes, 16-byte aligned: about

@@ -216,3 +216,37 @@ def test_long_prefixes_in_fp32(members, h, hk, d, prefix):
     err = got.double().cpu() - refs[0]
     along = float((err * refs[0]).sum() / refs[0].square().sum())
     assert abs(along) < 2.0 ** -20
+
+
+# ---------------------------------------------------------------- one by one: lengths and counts
+
+@pytest.mark.parametrize("n, d, typ", [(1, 64, "bf16"), (1, 128, "f32"), (40, 64, "f16"), (40, 256, "bf16")])
+def test_lengths_far_past_the_table_one_by_one(n, d, typ):
+    """As where tokens are read together: 2^16 tiles past the table are counted, and no more walked over."""
+    b = batch([(96, ONE(*[150] * 9)), (None, [(n, 40)])], 8, 2, d, 16, typ, wide=False)
+    assert not reads_together(b, n)
+    lens = b["kv_len"].clone()
+    lens[9] = 1 << 30            # its 40 tokens lie in 3 pages, whose last 8 slots hold none
+    b["table"][9, 2] = -1
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for window, sinks, past in ((0, 0, 1 << 16), (100, 20, 0)):
+        status.zero_()
+        got = run({**b, "kv_len": lens}, window, sinks, dev_status=status)
+        assert int(status.item()) == (int((b["table"][9] < 0).sum()) + past if past else 0)
+        seen = 32 if not window else 20   # the window is past the table
+        short = {**b, "kv_lens": b["kv_lens"][:9] + [seen + n - 1], "slots": b["slots"][:9] + [b["slots"][9][:seen]]}
+        check_attn(got, reference(short) if not window else [torch.cat([x[:9], y[9:]]) for x, y in zip(reference(b, window, sinks), reference(short))], typ)
+
+
+def test_many_fp32_queries_are_not_counted_one_by_one():
+    """One by one a request's units x tiles have to fit in 32 bits; the other way has no such bound."""
+    lib = g.load_library()
+
+    def sizes(n, width, qt):
+        a = g.AttnArgs(256, qt, n, 4096, 256, 4, 16, 256, width, width, 256, 256, 1, n, 32, 8, 128, 0.1, 0, 0, 256, 4096, 0)
+        return lib.gguf_prefix_attention_ws_size(ctypes.byref(a), 0), lib.gguf_paged_attention_ws_size(ctypes.byref(a))
+
+    for n, width, qt, same in ((8, 64, g.F32, True), (8192, 512, g.F32, True), (60000, 512, g.F32, False), (8192, 1 << 18, g.F32, False),
+                               (60000, 512, g.BF16, True), (8192, 1 << 18, g.BF16, True)):
+        prefix, one = sizes(n, width, qt)
+        assert (prefix == one) == same and prefix > 0
