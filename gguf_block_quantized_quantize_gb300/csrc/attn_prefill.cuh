@@ -24,16 +24,16 @@
 // TMEM allocation), 13 loads.  Every wait is bounded (1 s); a timeout sets the
 // error word and the CTA drains and exits.
 //
-// Measured: a prompt of 8192 tokens, 32 query heads, 8 KV heads of 128, bf16: 648
-// us, 0.85 PFLOP/s (0.45 of the matrix rate); with heads of 256 1690 us (0.34);
-// 2 x 4093 tokens with a window of 1000, heads of 64, fp16: 154 us (0.27 PFLOP/s).
+// Measured: a prompt of 8192 tokens, 32 query heads, 8 KV heads of 128, bf16: 645
+// us, 0.85 PFLOP/s (0.45 of the matrix rate); with heads of 256 1530 us (0.38);
+// 2 x 4093 tokens with a window of 1000, heads of 64, fp16: 150 us (0.27 PFLOP/s).
 // What bounds it now: no unit (tensor pipe 37 % active, issue slots 45 % used at
 // heads of 128) but the chain scores, softmax, P, product of an S buffer, which
 // the next scores into it wait for: 4800 cycles per block and two row tiles, and
 // 4300 with heads of 64.  TMEM is full with heads of 128 only (two S buffers and O);
 // with heads of 64 and of 256 128 of its columns are unused (384 on, and 128 to 255).
 // Spills a thread: at most 76 bytes of stores and 64 of loads without CUT; with it
-// 216 / 228 with heads of 128, 108 / 128 of 64, and of 256 24 / 72 (fp16; bf16 none).
+// 216 / 228 with heads of 128, 108 / 128 of 64, none of 256.
 #pragma once
 
 #include "attn_decode.cuh"
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prefill_kernel(const AdSha
     constexpr bool CUT = MODE == AP_CUT, PRE = MODE == AP_PRE, PARTS = MODE != AP_PLAIN;
     using C = ApCfg<D, QT>;
     using L = KvTile<D>;
-    constexpr int NB = L::NB, BW = L::BW, NC = L::NC, BT = C::BT, ROWS = C::RT * 128;
+    constexpr int BT = C::BT, ROWS = C::RT * 128;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t raw_full[C::RAWST], raw_empty[C::RAWST], k_full[C::KST], k_empty[C::KST], v_full[C::VST],

@@ -6,9 +6,10 @@
 // The sums over the two ranges are taken apart, each with a maximum of its own,
 // and joined: (m, l, O) + (m', l', O') = (M, 2^(m-M) l + 2^(m'-M) l', 2^(m-M) O +
 // 2^(m'-M) O').  So the queries of all requests of a group stand together as the
-// rows of one matrix against the group's P shared tokens, which are read and
-// unpacked once for all of them; only what a request has of its own is walked over
-// per request.
+// rows of one matrix against the group's P shared tokens, which come from memory
+// once for all of them and are unpacked once for every 256 of the rows (128 with
+// heads of 256, 8 or 16 in the kernel of few rows); only what a request has of its
+// own is walked over per request.
 //
 // An entry of the plan is a set of consecutive queries and a range of tiles of one
 // row of the block table: one for each request (its own tiles) and one for each
@@ -23,14 +24,14 @@
 //
 // Measured in a captured graph, without the plan (3 to 4 us, once a step), and request
 // by request: 32 x (8192 + 512) tokens, 32 / 8 heads of 128, bf16 39 and 69 us; 256 x
-// (32768 + 128) 182 and 1690 us (0.74 PFLOP/s); 16 x 3.5 queries x (20000 + 400), heads of
-// 64, fp16 50 and 82 us.  What bounds it: with many queries the tensor-core kernel (156 of
-// the 182 us), whose matrix unit is 35 % active: its products read keys, values and Q from
+// (32768 + 128) 183 and 1690 us (0.74 PFLOP/s); 16 x 3.5 queries x (20000 + 400), heads of
+// 64, fp16 50 and 82 us.  What bounds it: with many queries the tensor-core kernel (157 of
+// the 183 us), whose matrix unit is 35 % active: its products read keys, values and Q from
 // shared memory, which unpacking fills as well (4200 cycles a block of 128 tokens and 256
-// rows; the products alone take 2600).  With few, latency: 18 + 13 + 8 us of the 39 are
-// three kernels of 4 blocks, 3 tiles a warp and 20 pieces a row.  Spills a thread (stores /
-// loads): tensor-core kernel 160 / 200 bytes with heads of 128, 76 / 84 of 64, 28 / 48 of
-// 256; few rows 24 / 72 at most, fp32 with heads of 256 142 / 160.
+// rows; the products alone take 2600).  With few, latency: three kernels (19, 13.5 and 8 us
+// by themselves) of 4 blocks, 3 tiles a warp and 20 pieces a row.  Spills a thread (stores /
+// loads): tensor-core kernel 164 / 204 bytes with heads of 128, 84 / 92 of 64, 24 / 52 of
+// 256; few rows 48 / 84 at most, fp32 with heads of 256 174 / 192.
 #include <algorithm>
 
 #include "attn_decode.cuh"

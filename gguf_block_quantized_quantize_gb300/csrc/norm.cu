@@ -22,11 +22,17 @@
 // float and q8_1 outputs: 8192 rows of 4096 67 us (4.6 TB/s; the bytes take 45;
 // without q8_1 52 us, 5.2 TB/s), of 8192 131 us, of 16384 321 us; 2048 of 2048
 // 13.4 us; fp32, 4096 of 4096 54 us (5.3 TB/s); 1 row of 4096 2.9 us; 777 rows of
-// 1111 fp32 values (single loads, LAYER) 8.1 us.  Between the two: the issue of about
+// 1111 fp32 values (single loads, LAYER, a gate row) 8.7 us.  Between the two: the issue of about
 // 48 instructions a value with its 16-bit output pair (56 % of the slots), and the
 // barriers of the two sums with 32 warps an SM, which the registers of two chunks a
 // thread allow.  Sums warp by warp (16 loads each), four barriers a row and a
 // rounding at a time took 101 us.
+//
+// Rows wider than 16384 values take eight chunks a thread, more than the registers hold:
+// 344 to 448 bytes of spill loads a thread, 1000 to 1032 with single loads.  bf16 as above,
+// 8192 rows of 24576 991 us, of 32768 1087 us (2.3 TB/s), 1 row of 32768 15 us; fp32, 4096
+// of 32768 541 us (4.3 TB/s).  Rows that start anywhere, bf16: 8192 of 16383 591 us, of
+// 32767 1472 us.
 #include <algorithm>
 #include <type_traits>
 

@@ -732,7 +732,8 @@ gguf_status gguf_kv_get_rows(const void *cache, int64_t n_pages, int64_t page_si
  * values into the matrix instructions (2e-4 of the outputs' norm, 3e-4 in prompts, beside
  * the rounding of the output), and in prompts of bf16 queries fp16 keys (4e-4); so the
  * bits of a request's outputs depend on the kernel, which depends on the call.  fp32
- * queries split operands (about 1e-6; GGUF_ERR_SHAPE where max_q_len x heads / 8 x table
+ * queries split operands (about 1e-6; the matrix unit cuts long sums off: 3e-6 at 32 requests
+ * of 4000 tokens, 2e-5 at 60 of 16000; GGUF_ERR_SHAPE where max_q_len x heads / 8 x table
  * tokens / 16 passes 4e9) and run 8 rows at a time: a prompt of 8192 tokens takes 24
  * times as long as in bf16.  Probabilities below 2^-34 of a row's largest count as zero.
  * A block that is not finite may reach the outputs of every query of its request in the
@@ -784,14 +785,17 @@ gguf_status gguf_prefix_plan(const int32_t *q_start, const int32_t *kv_len, int6
 
 /*
  * gguf_prefix_attention -- gguf_paged_attention for a batch whose requests share long
- * prefixes: the shared tokens of a group are read and unpacked once for the queries of all
- * its requests (a call whose requests can be had faster one by one, as its host arguments
- * bound them, goes so).  Every row of the block table lists all pages of its request, the
- * shared ones too; the outputs are gguf_paged_attention's on this table, in other bits.
+ * prefixes: the shared tokens of a group come from memory once for the queries of all its
+ * requests, and are unpacked once for every 256 query rows of a KV head (128 with heads of
+ * 256; 8 or 16 where there are few; 8 with fp32 queries).  A call whose requests can be had
+ * faster one by one, as its host arguments bound them, goes so.  Every row of the block table
+ * lists all pages of its request, the shared ones too; the outputs are gguf_paged_attention's
+ * on this table, in other bits.
  *   args : as gguf_paged_attention; q_start and kv_len are not looked at (they are in the
  *          plan).  The table's width decides, with the window and the other sizes, whether the
- *          shared tokens are read together (never without groups, or for one request): one much
- *          wider than the requests need costs short calls time.
+ *          shared tokens are read together (without groups, or for one request, only where
+ *          gguf_paged_attention refuses the fp32 queries): one much wider than the requests
+ *          need costs short calls time.
  *   plan : made by gguf_prefix_plan, on this stream or complete, with these n_requests,
  *          n_groups, n_tokens and page_size: plan_bytes, at least gguf_prefix_plan_bytes of
  *          them.  Of a plan of other sizes nothing is written, and it counts in dev_status, once.
@@ -806,9 +810,11 @@ gguf_status gguf_prefix_plan(const int32_t *q_start, const int32_t *kv_len, int6
  * n_tokens x n_heads <= 2^30, and 2^40 tiles of 16 tokens, 2^16 more a row than the table
  * holds, under all groups of 8 query rows (GGUF_ERR_SHAPE above).  Precision, windows, blocks that are not
  * finite (which may reach the queries of their group) and timeouts are as described at
- * gguf_paged_attention; the bits of a request's outputs depend on the batch.  Made for few
- * queries per request (decoding, tokens to check): long chunks of prompts go through, but
- * blocks that causality hides from all of a chunk's first rows are computed and dropped.
+ * gguf_paged_attention, but fp32 outputs of tokens that are read together do not shrink with
+ * the length (error 8e-7 at 40 requests of 30000); the bits of a request's outputs depend on
+ * the batch.  Made for few queries per request (decoding, tokens to check): long chunks of
+ * prompts go through, but blocks that causality hides from all of a chunk's first rows are
+ * computed and dropped.
  * Same bits on every run.
  */
 size_t gguf_prefix_attention_ws_size(const gguf_attn_args *args, int64_t n_groups);
